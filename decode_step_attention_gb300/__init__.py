@@ -32,10 +32,22 @@ The sampling side of the decode step (fusedtok README, "Operators": repetition
 penalty, temperature, top-k / top-p sampling, decode_step):
 
 * :func:`sample`                penalty -> temperature -> top-k -> top-p -> draw,
-  one launch for a batch of rows.
+  one launch for a batch of rows;
+* :func:`token_logprobs`        log probabilities of given tokens, the entropy and the
+  best alternatives of every row.
+
+One verification step of speculative decoding, for drafts of up to 64 nodes per sequence
+arranged as a tree (the decode step's operators for N queries per sequence):
+
+* :func:`qknorm_rope_tree`      QK-RMSNorm and RoPE of the nodes, K/V into the tree's own
+  buffers;
+* :func:`gqa_tree_attn`         attention of every node over the cache and its ancestors,
+  optionally with a score cap, a distance bias or a sliding window;
+* :func:`tree_commit`           the accepted path's K/V into the cache.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -50,6 +62,7 @@ _LAYOUTS = {"neox": NEOX, "interleaved": INTERLEAVED, NEOX: NEOX, INTERLEAVED: I
 DEVERR_LEN_CLAMPED = 0x1
 DEVERR_POS_SKIPPED = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
+DEVERR_TREE_CLAMPED = 0x8
 
 WORKSPACE_HEADER_BYTES = 256
 
@@ -91,6 +104,13 @@ EXPORTS = {
     "dec_attn_sublayer": (_I, [_P, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                _I, _I, _I, _I, _I, _I, _F, _I, _P, _F, _I, _I, _P, _Z, _P]),
     "dec_sample": (_I, [_P, _P, _I, _P, _P, _I, _I, _F, _F, _F, _I, _P]),
+    "dec_qknorm_rope_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                  _F, _I, _P, _F, _P, _P]),
+    "dec_tree_attn_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
+    "dec_gqa_tree_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                               _I, _I, _F, _F, _I, _I, _P, _Z, _P]),
+    "dec_tree_commit": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "dec_token_logprobs": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P]),
     "dec_diag_wait_timeout": (_I, [_P, _P]),
     "dec_status_string": (ctypes.c_char_p, [_I]),
     "dec_last_error": (ctypes.c_char_p, []),
@@ -601,6 +621,173 @@ def sample(logits, sampled_ids=None, penalty: float = 1.0, temperature: float = 
     _call("dec_sample", _ptr(logits), _ptr(sampled_ids) if L else None, L, _ptr(u), _ptr(out),
           B, V, float(penalty), float(temperature), float(top_p), int(top_k), _stream(stream))
     return out
+
+
+# -------------------------------------------------------- log probabilities ---
+def _on(stream):
+    """The stream a call's own tensors are made on: the one its kernels run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0, vocab=None,
+                   entropy: bool = True, stream=None):
+    """Scores every row of ``logits`` [B, ld] (fp32 or bf16; the first ``vocab`` columns, all
+    by default) under softmax(z / temperature). Returns (logprobs, entropy, top_ids,
+    top_logprobs): the log probabilities [B, C] of ``tokens`` [B, C] (int32; -inf for an id
+    outside the vocabulary), the entropy [B] in nats, and the ``top_k`` (at most 32) most
+    probable ids [B, K] with their log probabilities, best first, equal ones by the lower id.
+    What was not asked for is None."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, BF16):
+        raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
+    _need(logits, "logits", logits.dtype, host=True)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B, ld], got {tuple(logits.shape)}")
+    B, ld = logits.shape
+    V = ld if vocab is None else int(vocab)
+    C, K = 0, int(top_k)
+    if tokens is not None:
+        _need(tokens, "tokens", I32, host=True)
+        if tokens.dim() != 2 or tokens.shape[0] != B:
+            raise ValueError(f"tokens must be [B, C], got {tuple(tokens.shape)}")
+        C = tokens.shape[1]
+    with _on(stream):
+        lp = None if tokens is None else _empty((B, C), torch.float32, logits)
+        ent = _empty((B,), torch.float32, logits) if entropy else None
+        ids = _empty((B, K), I32, logits) if K > 0 else None
+        top = _empty((B, K), torch.float32, logits) if K > 0 else None
+    _call("dec_token_logprobs", _ptr(logits), 0 if logits.dtype == torch.float32 else 1, ld,
+          _ptr(tokens) if C else None, C, _ptr(lp) if C else None, _ptr(ent), _ptr(ids),
+          _ptr(top), K, B, V, float(temperature), _stream(stream))
+    return lp, ent, ids, top
+
+
+# -------------------------------------------------------------- draft trees ---
+def qknorm_rope_tree(q, k_new, v_new, k_tree, v_tree, pos, theta: float, layout="neox",
+                     q_norm_w=None, k_norm_w=None, eps: float = 1e-6, n_nodes=None, q_out=None,
+                     error_word=None, stream=None, inv_freq=None):
+    """:func:`qknorm_rope_kv_append` for the nodes of a draft tree: q [B, N, Hq, D] rotated
+    at pos [B, N] in place (or into ``q_out``), k_new rotated and v_new copied from
+    [B, N, Hkv, D] into the tree's buffers k_tree, v_tree [B, Hkv, N, D]. ``n_nodes`` [B]
+    (int32): the nodes each sequence has; those behind are left as they were. Returns the
+    rotated q."""
+    _need(q, "q", BF16, host=True)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq, D = q.shape
+    _need(k_tree, "k_tree", BF16)
+    if k_tree.dim() != 4:
+        raise ValueError(f"k_tree must be [B, Hkv, N, D], got {tuple(k_tree.shape)}")
+    Hkv = k_tree.shape[1]
+    _need(k_tree, "k_tree", BF16, (B, Hkv, N, D))
+    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
+    _need(k_new, "k_new", BF16, (B, N, Hkv, D), host=True)
+    _need(v_new, "v_new", BF16, (B, N, Hkv, D), host=True)
+    _need(pos, "pos", I32, (B, N), host=True)
+    if n_nodes is not None:
+        _need(n_nodes, "n_nodes", I32, (B,), host=True)
+    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
+        if w is not None:
+            _need(w, name, BF16, (D,), host=True)
+    if error_word is not None:
+        _need(error_word, "error_word", I32, host=True)
+    if q_out is None:
+        q_out = q
+    _need(q_out, "q_out", BF16, (B, N, Hq, D), host=True)
+    _call("dec_qknorm_rope_tree", _ptr(q), _ptr(q_out), _ptr(k_new), _ptr(v_new), _ptr(q_norm_w),
+          _ptr(k_norm_w), _ptr(k_tree), _ptr(v_tree), _ptr(pos), _ptr(n_nodes), B, N, Hq, Hkv, D,
+          float(theta), _LAYOUTS[layout], _freq(inv_freq, D), float(eps), _ptr(error_word),
+          _stream(stream))
+    return q_out
+
+
+def tree_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, max_len: int,
+                         num_parts: int = 0) -> int:
+    return int(lib().dec_tree_attn_workspace_bytes(B, N, Hq, Hkv, D, max_len, num_parts))
+
+
+def alloc_tree_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, max_len: int,
+                         num_parts: int = 0, device=None) -> torch.Tensor:
+    """A uint8 workspace for :func:`gqa_tree_attn`, its header zeroed."""
+    n = tree_workspace_bytes(B, N, Hq, Hkv, D, max_len, num_parts)
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:WORKSPACE_HEADER_BYTES].zero_()
+    return ws
+
+
+def gqa_tree_attn(q, k_cache, v_cache, lens, k_tree, v_tree, mask, n_nodes=None, pos=None,
+                  max_len=None, workspace=None, out=None, scale: float = 0.0,
+                  softcap: float = 0.0, slopes=None, window: int = 0, num_parts: int = 0,
+                  stream=None):
+    """Attention of the nodes of a draft tree: q [B, N, Hq, D] (rotated) over the cached
+    tokens t < lens[b] and the nodes j whose bit is set in mask[b, n] (int64 [B, N], the
+    node's ancestors and itself), whose keys and values are k_tree, v_tree [B, Hkv, N, D].
+    Returns ``out`` [B, N, Hq, D]; rows of nodes behind ``n_nodes``[b] are left as they were
+    (zeros when ``out`` is made here).
+
+    ``softcap`` > 0: scores become softcap * tanh(score / softcap). ``slopes`` (fp32 [Hq]):
+    slope * (distance to the key) is subtracted. ``window`` > 0: keys at a distance of at
+    least ``window`` are not seen. Both need the nodes' positions ``pos`` (int32 [B, N],
+    the sequence's length plus the node's depth). N = 1 is the single-token form."""
+    _need(q, "q", BF16, host=True)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq, D = q.shape
+    _need(k_cache, "k_cache", BF16)
+    if k_cache.dim() != 4 or k_cache.shape[0] != B or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache shape {tuple(k_cache.shape)} does not match q {tuple(q.shape)}")
+    Hkv, T_cap = k_cache.shape[1], k_cache.shape[2]
+    _need(v_cache, "v_cache", BF16, (B, Hkv, T_cap, D))
+    _need(k_tree, "k_tree", BF16, (B, Hkv, N, D))
+    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
+    _need(lens, "lens", I32, (B,), host=True)
+    _need(mask, "mask", torch.int64, (B, N), host=True)
+    if n_nodes is not None:
+        _need(n_nodes, "n_nodes", I32, (B,), host=True)
+    if pos is not None:
+        _need(pos, "pos", I32, (B, N), host=True)
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, (Hq,), host=True)
+    max_len = T_cap if max_len is None else int(max_len)
+    with _on(stream):
+        if workspace is None:
+            workspace = alloc_tree_workspace(B, N, Hq, Hkv, D, max_len, num_parts,
+                                             k_cache.device)
+        if out is None:
+            out = _empty(q.shape, BF16, q)
+            if n_nodes is not None:
+                out.zero_()
+    _need(workspace, "workspace", torch.uint8)
+    _need(out, "out", BF16, (B, N, Hq, D), host=True)
+    _call("dec_gqa_tree_attn", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lens), _ptr(k_tree),
+          _ptr(v_tree), _ptr(mask), _ptr(n_nodes), _ptr(pos), _ptr(slopes), _ptr(out), B, N, Hq,
+          Hkv, D, T_cap, max_len, float(scale), float(softcap), int(window), int(num_parts),
+          _ptr(workspace), workspace.numel(), _stream(stream))
+    return out
+
+
+def tree_commit(k_tree, v_tree, path, n_path, k_cache, v_cache, lens, error_word=None,
+                stream=None):
+    """The accepted path of a draft tree into the cache: for i < n_path[b], cache slot
+    lens[b] + i <- node path[b, i] (K and V, bit copies). ``lens`` itself is the caller's to
+    advance (``lens += n_path``)."""
+    _need(k_tree, "k_tree", BF16)
+    if k_tree.dim() != 4:
+        raise ValueError(f"k_tree must be [B, Hkv, N, D], got {tuple(k_tree.shape)}")
+    B, Hkv, N, D = k_tree.shape
+    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
+    _need(k_cache, "k_cache", BF16)
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [B, Hkv, T_cap, D], got {tuple(k_cache.shape)}")
+    T_cap = k_cache.shape[2]
+    _need(k_cache, "k_cache", BF16, (B, Hkv, T_cap, D))
+    _need(v_cache, "v_cache", BF16, (B, Hkv, T_cap, D))
+    _need(path, "path", I32, (B, N), host=True)
+    _need(n_path, "n_path", I32, (B,), host=True)
+    _need(lens, "lens", I32, (B,), host=True)
+    if error_word is not None:
+        _need(error_word, "error_word", I32, host=True)
+    _call("dec_tree_commit", _ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(n_path), _ptr(k_cache),
+          _ptr(v_cache), _ptr(lens), B, N, Hkv, D, T_cap, _ptr(error_word), _stream(stream))
 
 
 # ------------------------------------------------------------ CUDA graph ---

@@ -1093,3 +1093,263 @@ extern "C" dec_status dec_sample(const float *logits, const int32_t *sampled_ids
   if (e != cudaSuccess) return cuda_fail(e, "sampler launch");
   return ok();
 }
+
+// -------------------------------------------------------------- draft trees ---
+namespace {
+
+// As where_all, and device buffers must be on the current device: a kernel launched there
+// could not reach another's.
+dec_status where_all_here(std::initializer_list<Where> list) {
+  const int dev = current_device();
+  for (const Where &w : list) {
+    if (w.p == nullptr) continue;
+    cudaPointerAttributes a{};
+    const cudaError_t e = cudaPointerGetAttributes(&a, w.p);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return cuda_fail(e, w.name);
+    }
+    if (a.type == cudaMemoryTypeDevice && a.device != dev)
+      return fail(DEC_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", w.name,
+                  a.device, dev);
+    if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) continue;
+    if (w.host_ok && a.type == cudaMemoryTypeHost && a.devicePointer == w.p) continue;
+    return fail(DEC_ERR_INVALID_ARG, w.host_ok ? "%s is neither device memory nor page-locked "
+                                                 "host memory mapped at the same address"
+                                               : "%s must be device memory",
+                w.name);
+  }
+  return DEC_OK;
+}
+
+bool misaligned(std::initializer_list<const void *> list, uintptr_t bytes) {
+  for (const void *p : list)
+    if (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) return true;
+  return false;
+}
+
+dec_status check_tree_shape(int B, int N, int Hkv, int D) {
+  if (B < 0) return fail(DEC_ERR_INVALID_ARG, "B = %d < 0", B);
+  if (B > kSplitMaxB) return fail(DEC_ERR_UNSUPPORTED, "B = %d > %d", B, kSplitMaxB);
+  if (N < 1) return fail(DEC_ERR_INVALID_ARG, "N = %d < 1", N);
+  if (N > kTreeMaxNodes) return fail(DEC_ERR_UNSUPPORTED, "N = %d > %d", N, kTreeMaxNodes);
+  if (Hkv <= 0) return fail(DEC_ERR_INVALID_ARG, "head counts must be positive");
+  if (Hkv > 65535) return fail(DEC_ERR_UNSUPPORTED, "Hkv = %d > 65535", Hkv);
+  if (D != 64 && D != 128) return fail(DEC_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", D);
+  if ((long long)B * Hkv * N >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "B * Hkv * N must stay below 2^31 rows");
+  return DEC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new,
+                                const void *v_new, const void *q_norm_w, const void *k_norm_w,
+                                void *k_tree, void *v_tree, const int32_t *pos,
+                                const int32_t *n_nodes, int B, int N, int Hq, int Hkv, int D,
+                                float rope_theta, dec_rope_layout layout, const double *inv_freq,
+                                float eps, uint32_t *error_word, dec_stream_t stream) {
+  dec_status st = check_tree_shape(B, N, Hkv, D);
+  if (st != DEC_OK) return st;
+  if (Hq <= 0 || Hq % Hkv != 0)
+    return fail(DEC_ERR_INVALID_ARG, "need Hq > 0 and Hq %% Hkv == 0");
+  if ((long long)Hq + Hkv > 65535)
+    return fail(DEC_ERR_UNSUPPORTED, "Hq + Hkv > 65535 heads");
+  InvFreq inv;
+  if ((st = rope_table(D, rope_theta, inv_freq, &inv)) != DEC_OK) return st;
+  if (layout != DEC_ROPE_NEOX && layout != DEC_ROPE_INTERLEAVED)
+    return fail(DEC_ERR_INVALID_ARG, "unknown rope layout %d", (int)layout);
+  if (!(eps >= 0.f)) return fail(DEC_ERR_INVALID_ARG, "eps must be >= 0");
+  if ((q_norm_w == nullptr) != (k_norm_w == nullptr))
+    return fail(DEC_ERR_INVALID_ARG, "q_norm_w and k_norm_w must both be set or both be null");
+  if (B == 0) return ok();
+  if (!q_in || !q_out || !k_new || !v_new || !k_tree || !v_tree || !pos)
+    return fail(DEC_ERR_INVALID_ARG, "q, k_new, v_new, k_tree, v_tree and pos must be non-null");
+  if (misaligned({q_in, q_out, k_new, v_new, q_norm_w, k_norm_w, k_tree, v_tree}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({pos, n_nodes, error_word}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "pos, n_nodes and error_word must be 4-byte aligned");
+  const size_t q_bytes = (size_t)B * N * Hq * D * 2, kv_bytes = (size_t)B * N * Hkv * D * 2;
+  if (q_in != q_out && overlaps(q_in, q_bytes, q_out, q_bytes))
+    return fail(DEC_ERR_INVALID_ARG, "q_in and q_out must be the same buffer or not overlap");
+  if (overlaps(k_tree, kv_bytes, v_tree, kv_bytes) || overlaps(k_tree, kv_bytes, k_new, kv_bytes) ||
+      overlaps(k_tree, kv_bytes, v_new, kv_bytes) || overlaps(v_tree, kv_bytes, k_new, kv_bytes) ||
+      overlaps(v_tree, kv_bytes, v_new, kv_bytes))
+    return fail(DEC_ERR_INVALID_ARG, "k_tree and v_tree may not overlap each other, k_new or v_new");
+  st = where_all_here({{q_in, "q_in", true}, {q_out, "q_out", true}, {k_new, "k_new", true},
+                       {v_new, "v_new", true}, {q_norm_w, "q_norm_w", true},
+                       {k_norm_w, "k_norm_w", true}, {k_tree, "k_tree", false},
+                       {v_tree, "v_tree", false}, {pos, "pos", true}, {n_nodes, "n_nodes", true},
+                       {error_word, "error_word", true}});
+  if (st != DEC_OK) return st;
+  const cudaError_t e = launch_tree_rope(q_in, q_out, k_new, v_new, q_norm_w, k_norm_w, k_tree,
+                                         v_tree, pos, n_nodes, B, N, Hq, Hkv, D, inv,
+                                         layout == DEC_ROPE_INTERLEAVED, eps, error_word,
+                                         as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qknorm_rope_tree launch");
+  return ok();
+}
+
+size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_len,
+                                     int num_parts) {
+  if (B < 0 || N < 1 || N > kTreeMaxNodes || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
+      (D != 64 && D != 128) || max_len < 0 || num_parts < 0)
+    return 0;
+  return tree_ws_bytes(B, N, Hq, Hkv, D,
+                       tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));
+}
+
+dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *lens, const void *k_tree, const void *v_tree,
+                             const uint64_t *mask, const int32_t *n_nodes, const int32_t *pos,
+                             const float *slopes, void *out, int B, int N, int Hq, int Hkv, int D,
+                             int T_cap, int max_len, float scale, float softcap, int window,
+                             int num_parts, void *workspace, size_t ws_bytes,
+                             dec_stream_t stream) {
+  dec_status st = check_tree_shape(B, N, Hkv, D);
+  if (st != DEC_OK) return st;
+  if ((st = check_attn_shape(B, Hq, Hkv, D, T_cap, max_len)) != DEC_OK) return st;
+  if (num_parts < 0) return fail(DEC_ERR_INVALID_ARG, "num_parts = %d < 0", num_parts);
+  if (num_parts > kTreeMaxParts)
+    return fail(DEC_ERR_UNSUPPORTED, "num_parts = %d > %d", num_parts, kTreeMaxParts);
+  if (window < 0) return fail(DEC_ERR_INVALID_ARG, "window = %d < 0", window);
+  if (!std::isfinite(scale)) return fail(DEC_ERR_INVALID_ARG, "scale must be finite");
+  if (!(softcap >= 0.f) || !std::isfinite(softcap))
+    return fail(DEC_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  if (B == 0) return ok();
+  if (!q || !k_cache || !v_cache || !lens || !k_tree || !v_tree || !mask || !out)
+    return fail(DEC_ERR_INVALID_ARG,
+                "q, caches, lens, k_tree, v_tree, mask and out must be non-null");
+  if (pos == nullptr && (window > 0 || slopes != nullptr))
+    return fail(DEC_ERR_INVALID_ARG, "a window or slopes need pos");
+  if (misaligned({q, k_cache, v_cache, k_tree, v_tree, out}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({mask}, 8)) return fail(DEC_ERR_INVALID_ARG, "mask must be 8-byte aligned");
+  if (misaligned({lens, n_nodes, pos, slopes}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "lens, n_nodes, pos and slopes must be 4-byte aligned");
+  const size_t q_bytes = (size_t)B * N * Hq * D * 2;
+  if (overlaps(q, q_bytes, out, q_bytes))
+    return fail(DEC_ERR_INVALID_ARG, "out may not overlap q");
+  const int parts = tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current());
+  if (workspace == nullptr || misaligned({workspace}, 256))
+    return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+  const size_t need = tree_ws_bytes(B, N, Hq, Hkv, D, parts);
+  if (ws_bytes < need)
+    return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  st = where_all_here({{q, "q", true}, {k_cache, "k_cache", false}, {v_cache, "v_cache", false},
+                       {k_tree, "k_tree", false}, {v_tree, "v_tree", false}, {lens, "lens", true},
+                       {mask, "mask", true}, {n_nodes, "n_nodes", true}, {pos, "pos", true},
+                       {slopes, "slopes", true}, {out, "out", true},
+                       {workspace, "workspace", false}});
+  if (st != DEC_OK) return st;
+  TreeAttnArgs a{};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.k_cache = static_cast<const __nv_bfloat16 *>(k_cache);
+  a.v_cache = static_cast<const __nv_bfloat16 *>(v_cache);
+  a.k_tree = static_cast<const __nv_bfloat16 *>(k_tree);
+  a.v_tree = static_cast<const __nv_bfloat16 *>(v_tree);
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.lens = lens;
+  a.n_nodes = n_nodes;
+  a.pos = pos;
+  a.mask = mask;
+  a.slopes = slopes;
+  a.error_word = static_cast<uint32_t *>(workspace);
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.T_cap = T_cap;
+  a.window = window;
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
+  a.softcap = softcap;
+  const cudaError_t e = launch_tree_attn(a, B, D, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gqa_tree_attn launch");
+  return ok();
+}
+
+dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t *path,
+                           const int32_t *n_path, void *k_cache, void *v_cache,
+                           const int32_t *lens, int B, int N, int Hkv, int D, int T_cap,
+                           uint32_t *error_word, dec_stream_t stream) {
+  dec_status st = check_tree_shape(B, N, Hkv, D);
+  if (st != DEC_OK) return st;
+  if (T_cap <= 0) return fail(DEC_ERR_INVALID_ARG, "T_cap = %d must be positive", T_cap);
+  if (B == 0) return ok();
+  if (!k_tree || !v_tree || !path || !n_path || !k_cache || !v_cache || !lens)
+    return fail(DEC_ERR_INVALID_ARG,
+                "k_tree, v_tree, path, n_path, caches and lens must be non-null");
+  if (misaligned({k_tree, v_tree, k_cache, v_cache}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({path, n_path, lens, error_word}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "path, n_path, lens and error_word must be 4-byte aligned");
+  const size_t tree = (size_t)B * Hkv * N * D * 2, cache = (size_t)B * Hkv * T_cap * D * 2;
+  if (overlaps(k_cache, cache, v_cache, cache) || overlaps(k_cache, cache, k_tree, tree) ||
+      overlaps(k_cache, cache, v_tree, tree) || overlaps(v_cache, cache, k_tree, tree) ||
+      overlaps(v_cache, cache, v_tree, tree))
+    return fail(DEC_ERR_INVALID_ARG, "the caches may not overlap each other or the tree's buffers");
+  st = where_all_here({{k_tree, "k_tree", false}, {v_tree, "v_tree", false}, {path, "path", true},
+                       {n_path, "n_path", true}, {k_cache, "k_cache", false},
+                       {v_cache, "v_cache", false}, {lens, "lens", true},
+                       {error_word, "error_word", true}});
+  if (st != DEC_OK) return st;
+  const cudaError_t e = launch_tree_commit(k_tree, v_tree, path, n_path, k_cache, v_cache, lens, B,
+                                           N, Hkv, D, T_cap, error_word, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree_commit launch");
+  return ok();
+}
+
+// -------------------------------------------------------- log probabilities ---
+dec_status dec_token_logprobs(const void *logits, dec_dtype type, int ld, const int32_t *ids,
+                              int C, float *logprobs, float *entropy, int32_t *top_ids,
+                              float *top_logprobs, int K, int B, int V, float temperature,
+                              dec_stream_t stream) {
+  if (B < 0) return fail(DEC_ERR_INVALID_ARG, "B = %d < 0", B);
+  if (B > kLogprobMaxRows)
+    return fail(DEC_ERR_UNSUPPORTED, "B = %d rows > %d per call", B, kLogprobMaxRows);
+  if (V < 1) return fail(DEC_ERR_INVALID_ARG, "V = %d < 1", V);
+  if (V > kLogprobMaxV) return fail(DEC_ERR_UNSUPPORTED, "V = %d > %d", V, kLogprobMaxV);
+  if (ld < V) return fail(DEC_ERR_INVALID_ARG, "ld = %d < V = %d", ld, V);
+  if (type != DEC_F32 && type != DEC_BF16)
+    return fail(DEC_ERR_INVALID_ARG, "unknown logits type %d", (int)type);
+  if (C < 0 || K < 0) return fail(DEC_ERR_INVALID_ARG, "C and K must be >= 0");
+  if (C > 65536) return fail(DEC_ERR_UNSUPPORTED, "C = %d > 65536", C);
+  if (K > kLogprobMaxK) return fail(DEC_ERR_UNSUPPORTED, "K = %d > %d", K, kLogprobMaxK);
+  if (K > V) return fail(DEC_ERR_INVALID_ARG, "K = %d > V = %d", K, V);
+  if (!(temperature > 0.f) || !std::isfinite(temperature))
+    return fail(DEC_ERR_INVALID_ARG, "temperature must be finite and > 0");
+  if (B == 0 || (C == 0 && K == 0 && entropy == nullptr)) return ok();
+  if (!logits) return fail(DEC_ERR_INVALID_ARG, "logits must be non-null");
+  if (C > 0 && (!ids || !logprobs))
+    return fail(DEC_ERR_INVALID_ARG, "ids and logprobs must be non-null when C > 0");
+  if (K > 0 && (!top_ids || !top_logprobs))
+    return fail(DEC_ERR_INVALID_ARG, "top_ids and top_logprobs must be non-null when K > 0");
+  if (misaligned({logits}, type == DEC_F32 ? 4 : 2) ||
+      misaligned({ids, logprobs, entropy, top_ids, top_logprobs}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "pointers must be aligned to their elements");
+  const dec_status st = where_all_here(
+      {{logits, "logits", true}, {C > 0 ? ids : nullptr, "ids", true},
+       {C > 0 ? logprobs : nullptr, "logprobs", true}, {entropy, "entropy", true},
+       {K > 0 ? top_ids : nullptr, "top_ids", true},
+       {K > 0 ? top_logprobs : nullptr, "top_logprobs", true}});
+  if (st != DEC_OK) return st;
+  LogprobArgs a{};
+  a.logits = logits;
+  a.ids = ids;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.top_logprobs = top_logprobs;
+  a.top_ids = top_ids;
+  a.bf16 = type == DEC_BF16;
+  a.ld = ld;
+  a.V = V;
+  a.C = C;
+  a.K = K;
+  a.temperature = temperature;
+  const cudaError_t e = launch_logprobs(a, B, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "token_logprobs launch");
+  return ok();
+}
+
+}  // extern "C"

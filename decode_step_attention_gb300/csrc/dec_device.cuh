@@ -26,6 +26,7 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 constexpr uint32_t kErrLenClamped = 0x1u;
 constexpr uint32_t kErrPosSkipped = 0x2u;
 constexpr uint32_t kErrWaitTimeout = 0x4u;
+constexpr uint32_t kErrTreeClamped = 0x8u;
 
 // How the split pass cuts the stream of (sequence, KV head, token) rows into pieces.
 // The stream is split into P equal blocks of `blk` rows, one per CTA. When a block is

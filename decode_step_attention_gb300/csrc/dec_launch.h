@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -176,5 +177,47 @@ bool split_fused_fits(int num_parts, int device);
 
 cudaError_t launch_split_merge(const void *workspace, void *out, int B, int Hq, int Hkv, int D,
                                int max_len, int num_parts, cudaStream_t stream);
+
+// ---- draft trees -------------------------------------------------------------------
+constexpr int kTreeMaxNodes = 64;  // a node's ancestors are one 64-bit word
+cudaError_t launch_tree_rope(const void *q_in, void *q_out, const void *k_new, const void *v_new,
+                             const void *q_norm_w, const void *k_norm_w, void *k_tree,
+                             void *v_tree, const int32_t *pos, const int32_t *n_nodes, int B,
+                             int N, int Hq, int Hkv, int D, const InvFreq &inv, int interleaved,
+                             float eps, uint32_t *error_word, cudaStream_t stream);
+cudaError_t launch_tree_commit(const void *k_tree, const void *v_tree, const int32_t *path,
+                               const int32_t *n_path, void *k_cache, void *v_cache,
+                               const int32_t *lens, int B, int N, int Hkv, int D, int T_cap,
+                               uint32_t *error_word, cudaStream_t stream);
+
+struct TreeAttnArgs {
+  const __nv_bfloat16 *q, *k_cache, *v_cache, *k_tree, *v_tree;
+  __nv_bfloat16 *out;
+  const int32_t *lens, *n_nodes, *pos;  // n_nodes, pos: may be null
+  const uint64_t *mask;
+  const float *slopes;                  // may be null
+  uint32_t *error_word;                 // the workspace's first word
+  int N, Hq, Hkv, T_cap, window;
+  float scale, softcap;
+};
+constexpr int kTreeMaxParts = 4096;
+// CTAs the attention's work is cut over (num_parts > 0: that many) and the workspace they need.
+int tree_parts(int B, int N, int Hq, int Hkv, int max_len, int num_parts, int sms);
+size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int D, int parts);
+cudaError_t launch_tree_attn(const TreeAttnArgs &a, int B, int D, cudaStream_t stream);
+
+// ---- log probabilities -------------------------------------------------------------
+constexpr int kLogprobMaxK = 32;
+constexpr int kLogprobMaxV = 262144;
+constexpr int kLogprobMaxRows = (1 << 21) - 1;
+struct LogprobArgs {
+  const void *logits;
+  const int32_t *ids;
+  float *logprobs, *entropy, *top_logprobs;  // entropy may be null
+  int32_t *top_ids;
+  int bf16, ld, V, C, K;
+  float temperature;
+};
+cudaError_t launch_logprobs(const LogprobArgs &a, int B, cudaStream_t stream);
 
 }  // namespace decattn

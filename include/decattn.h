@@ -117,6 +117,7 @@ dec_status dec_rope_yarn_softmax_scale(int D, float factor, float *scale);
 #define DEC_DEVERR_LEN_CLAMPED   0x1u  /* a lens[b] outside [0, T_cap] was clamped */
 #define DEC_DEVERR_POS_SKIPPED   0x2u  /* a pos[b] outside [0, T_cap) was skipped */
 #define DEC_DEVERR_WAIT_TIMEOUT  0x4u  /* a pipeline wait gave up (results invalid) */
+#define DEC_DEVERR_TREE_CLAMPED  0x8u  /* a node count outside [0, N] was clamped */
 
 /* ------------------------------------------------------------------------ K1
  * RMSNorm with a fused residual add (fusedtok README, "Operators": RMSNorm
@@ -530,6 +531,114 @@ dec_status dec_attn_sublayer(const void *x, void *residual, const void *norm_w, 
 dec_status dec_sample(const float *logits, const int32_t *sampled_ids, int L, const float *u,
                       int32_t *tokens, int B, int V, float penalty, float temperature,
                       float top_p, int top_k, dec_stream_t stream);
+
+/* ------------------------------------------------------------- draft trees
+ * One verification step of speculative decoding: every sequence b has, behind its lens[b]
+ * cached tokens, a draft of up to N nodes arranged as a tree, and one pass of the model
+ * scores all of them. The drafted keys and values live in the tree's own buffers
+ * [B, Hkv, N, D], so a rejected node never touches the cache:
+ *   dec_qknorm_rope_tree   rotates the nodes' queries and keys and fills the buffers;
+ *   dec_gqa_tree_attn      attention of every node over the cache and its ancestors;
+ *   dec_token_logprobs     scores the drafted tokens under the model (below);
+ *   dec_tree_commit        copies the accepted path into the cache.
+ * The caller then adds the accepted count to lens (with work of its own on the stream).
+ * Conventions of these calls and of dec_token_logprobs, besides those above: device
+ * buffers are on the current device (refused otherwise); n_nodes[b], a device array, is the
+ * number of nodes sequence b has (NULL: N for all); nothing is read or written for the
+ * nodes behind it, their output rows are left as they were; a count outside [0, N] is
+ * clamped and raises DEC_DEVERR_TREE_CLAMPED. 1 <= N <= 64.
+ */
+
+/* dec_qknorm_rope_kv_append for a tree's nodes: node n of sequence b is rotated at
+ * position pos[b, n] (its sequence's length plus its depth), and
+ *   q_out[b, n, h]     <- bf16(RoPE(RMSNorm(q_in[b, n, h])))
+ *   k_tree[b, g, n]    <- bf16(RoPE(RMSNorm(k_new[b, n, g])))
+ *   v_tree[b, g, n]    <- v_new[b, n, g]  (bit copy)
+ * A node with pos < 0 is skipped and raises DEC_DEVERR_POS_SKIPPED.
+ * q_in, q_out    [device|host] bf16 [B, N, Hq, D], the same buffer or not overlapping.
+ * k_new, v_new   [device|host] bf16 [B, N, Hkv, D].
+ * k_tree, v_tree [device] bf16 [B, Hkv, N, D].
+ * pos            [device|host] int32 [B, N];  n_nodes [device|host] int32 [B] or NULL.
+ * The other arguments as in dec_qknorm_rope_kv_append. */
+dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new,
+                                const void *v_new, const void *q_norm_w, const void *k_norm_w,
+                                void *k_tree, void *v_tree, const int32_t *pos,
+                                const int32_t *n_nodes, int B, int N, int Hq, int Hkv, int D,
+                                float rope_theta, dec_rope_layout layout, const double *inv_freq,
+                                float eps, uint32_t *error_word, dec_stream_t stream);
+
+/* Attention of the nodes. Node n of sequence b sees the cached tokens t < lens[b] and the
+ * nodes j < n_nodes[b] whose bit j is set in mask[b, n] (its ancestors and itself; any other
+ * set works too). For query head h of KV head g = h / (Hq / Hkv):
+ *   z   = scale * q[b, n, h] . K           K: k_cache[b, g, t] or k_tree[b, g, j]
+ *   z  <- softcap * tanh(z / softcap)      softcap > 0
+ *   z  <- z - slopes[h] * (p_n - p_key)    slopes given
+ *   out[b, n, h] = sum softmax(z) V        zeros when the node sees nothing
+ * window > 0: keys with p_n - p_key >= window are not seen. The position p of a cached
+ * token is its slot, that of node n max(pos[b, n], lens[b]). N = 1 is the single-token form
+ * with a score cap or a distance bias.
+ *
+ * q              [device|host] bf16 [B, N, Hq, D] (rotated).
+ * k_cache, v_cache [device] bf16 [B, Hkv, T_cap, D]; rows t >= lens[b] may hold anything.
+ * k_tree, v_tree [device] bf16 [B, Hkv, N, D]; a node that is not seen may hold anything:
+ *                it changes nothing for the nodes that do not see it. (A cached row that
+ *                some node of its sequence sees must be finite for all of them.)
+ * lens           [device|host] int32 [B], the cached tokens without the tree.
+ * mask           [device|host] uint64 [B, N].
+ * n_nodes        [device|host] int32 [B] or NULL.
+ * pos            [device|host] int32 [B, N]; may be NULL when window = 0 and slopes = NULL.
+ * slopes         [device|host] fp32 [Hq] or NULL.
+ * out            [device|host] bf16 [B, N, Hq, D], not overlapping q.
+ * max_len        host upper bound of every lens[b], 0 <= max_len <= T_cap.
+ * scale          <= 0 selects 1/sqrt(D).  softcap >= 0.  window >= 0.
+ * num_parts      CTAs the work is cut over; 0 lets the library choose.
+ * workspace      [device] at least dec_tree_attn_workspace_bytes(...) bytes, 256-byte aligned,
+ *                its first 256 bytes zeroed before its first use (the first word is the
+ *                device error word); it serves one call at a time.
+ * D in {64, 128}; 1 <= Hq/Hkv <= 8; B * Hkv * T_cap < 2^31; B <= 8192. */
+size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_len,
+                                     int num_parts);
+dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *lens, const void *k_tree, const void *v_tree,
+                             const uint64_t *mask, const int32_t *n_nodes, const int32_t *pos,
+                             const float *slopes, void *out, int B, int N, int Hq, int Hkv, int D,
+                             int T_cap, int max_len, float scale, float softcap, int window,
+                             int num_parts, void *workspace, size_t workspace_bytes,
+                             dec_stream_t stream);
+
+/* The accepted path into the cache: for i < n_path[b],
+ *   k_cache[b, g, lens[b] + i] <- k_tree[b, g, path[b, i]],  v likewise  (bit copies).
+ * Other cache rows are untouched. A path entry outside [0, N) or a slot outside [0, T_cap)
+ * is skipped and raises DEC_DEVERR_POS_SKIPPED; n_path[b] is clamped like n_nodes.
+ * k_tree, v_tree [device] bf16 [B, Hkv, N, D];  path [device|host] int32 [B, N];
+ * n_path, lens [device|host] int32 [B];  k_cache, v_cache [device] bf16 [B, Hkv, T_cap, D],
+ * not overlapping the tree's buffers;  error_word [device|host] uint32, or NULL.
+ * D in {64, 128}. */
+dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t *path,
+                           const int32_t *n_path, void *k_cache, void *v_cache,
+                           const int32_t *lens, int B, int N, int Hkv, int D, int T_cap,
+                           uint32_t *error_word, dec_stream_t stream);
+
+/* ------------------------------------------------------- log probabilities
+ * Per row b of the logits, with z = logits[b, 0..V) / temperature and lse = ln sum e^z:
+ *   logprobs[b, c]     = z[ids[b, c]] - lse      (-inf for an id outside [0, V))
+ *   entropy[b]         = lse - sum softmax(z) z  (nats)
+ *   top_ids[b, 0..K)   = the K largest logits, largest first, equal ones by the lower id
+ *   top_logprobs[b, k] = z[top_ids[b, k]] - lse
+ * A logit of -inf has probability zero. A row with a NaN, with +inf or with nothing but
+ * -inf gives NaN for every number (its top_ids are then only certain to lie in [0, V)).
+ *   logits       [device|host] fp32 or bf16 [B, ld], the first V of each row counted
+ *   ids          [device|host] int32 [B, C], may be NULL when C = 0
+ *   logprobs     [device|host] fp32 [B, C], may be NULL when C = 0
+ *   entropy      [device|host] fp32 [B], or NULL
+ *   top_ids, top_logprobs [device|host] int32 / fp32 [B, K], may be NULL when K = 0
+ *   0 <= B < 2^21; 1 <= V <= 262144; ld >= V; 0 <= C <= 65536; 0 <= K <= min(32, V);
+ *   temperature finite, > 0. Pointers aligned to their elements. */
+typedef enum dec_dtype { DEC_F32 = 0, DEC_BF16 = 1 } dec_dtype;
+dec_status dec_token_logprobs(const void *logits, dec_dtype type, int ld, const int32_t *ids,
+                              int C, float *logprobs, float *entropy, int32_t *top_ids,
+                              float *top_logprobs, int K, int B, int V, float temperature,
+                              dec_stream_t stream);
 
 /* -------------------------------------------------------------- diagnostics
  * Runs one warp that waits on a barrier nobody arrives at, with the same bounded

@@ -1,0 +1,168 @@
+"""token_logprobs on the GPU against the float64 oracle.
+
+Tolerance, derived before the first run: log probabilities are (z - M) / T - ln S in fp32.
+The sum S of V <= 262144 exponentials is off by at most 2^-24 per addition on the longest
+chain (below 600: each thread's own terms, then the reductions) and 2^-21 from the
+exponentials, so ln S by less than 4e-5; the other terms by a few 2^-24 of their size. The
+entropy's second sum errs in the same proportion to its value, at most ln V.
+"""
+import numpy as np
+import pytest
+import torch
+
+import decode_step_attention_gb300 as dsa
+from oracle import tree as OT
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def run(z, ids, K, T=1.0, vocab=None):
+    lp, ent, top, tlp = dsa.token_logprobs(z.to(DEV), ids.to(DEV), top_k=K, temperature=T,
+                                           vocab=vocab)
+    V = vocab or z.shape[1]
+    rows = z[:, :V].double().numpy()
+    for b in range(z.shape[0]):
+        rlp, rent, rtop, rtlp = OT.logprobs(rows[b], ids[b].tolist(), K, T)
+        for got, ref in ((lp[b], rlp), (tlp[b] if K else None, rtlp)):
+            if got is None:
+                continue
+            got = got.double().cpu().numpy()
+            inf = np.isneginf(ref)
+            assert np.array_equal(np.isneginf(got), inf)
+            assert np.all(np.abs(got - ref)[~inf] <= 4e-5 + 2.0 ** -21 * np.abs(ref[~inf]))
+        assert abs(float(ent[b]) - rent) <= 4e-5 * (1 + rent)
+        if K:
+            assert top[b].tolist() == list(rtop), (b, K)
+    return lp, ent, top, tlp
+
+
+def make(seed, B, V, kind="peaked", dtype=torch.float32):
+    gen = torch.Generator().manual_seed(seed)
+    z = torch.randn(B, V, generator=gen) * 2
+    if kind == "peaked":
+        at = torch.randint(0, V, (B, 16), generator=gen)
+        z.scatter_add_(1, at, 8 + 3 * torch.randn(B, 16, generator=gen))
+    elif kind == "flat":
+        z[:] = 0.5
+    elif kind == "rising":
+        z = torch.arange(V).float().expand(B, V) * (8.0 / V)
+    elif kind == "steps":                       # many equal values
+        z = torch.randint(-3, 4, (B, V), generator=gen).float()
+    elif kind == "masked":
+        z[torch.rand(B, V, generator=gen) < 0.9] = -float("inf")
+        z[:, V // 2] = 1.0
+    elif kind == "huge":
+        z *= 1e4
+    return z.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 7, 31, 100, 1000, 4096, 4097, 16384, 32767, 50257, 65537,
+                               131072, 151936, 262143, 262144])
+def test_sizes(V, dtype):
+    z = make(V, 3, V, dtype=dtype)
+    gen = torch.Generator().manual_seed(V)
+    ids = torch.randint(0, V, (3, 5), generator=gen, dtype=torch.int32)
+    run(z, ids, min(20, V))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["flat", "rising", "steps", "masked", "huge"])
+@pytest.mark.parametrize("V", [50, 5000, 40000, 262144])
+def test_rows(kind, V, dtype):
+    z = make(1, 2, V, kind, dtype)
+    ids = torch.tensor([[0, V - 1, V // 2], [1, V // 3, 2]], dtype=torch.int32)
+    for K in (0, 1, 5, 32):
+        run(z, ids, K)
+
+
+@pytest.mark.parametrize("T", [0.1, 0.7, 1.0, 3.0])
+def test_temperature(T):
+    run(make(2, 4, 3001), torch.arange(8, dtype=torch.int32).view(4, 2), 8, T)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,ld", [(50257, 50304), (999, 1001), (5, 130), (32001, 32003)])
+def test_padded_rows(V, ld, dtype):
+    z = make(3, 5, ld, dtype=dtype)
+    z[:, V:] = float("nan")
+    run(z, torch.full((5, 1), V - 1, dtype=torch.int32), 3, vocab=V)
+
+
+@pytest.mark.parametrize("B", [1, 2, 77, 300, 2500])
+def test_many_rows(B):
+    run(make(B, B, 777), torch.randint(0, 777, (B, 3), dtype=torch.int32), 4)
+
+
+def test_ids_outside_and_repeated():
+    z = make(4, 2, 100)
+    lp, *_ = run(z, torch.tensor([[-1, 100, 3, 3], [2 ** 31 - 1, -2 ** 31, 0, 99]],
+                                 dtype=torch.int32), 2)
+    assert torch.isneginf(lp[0, :2]).all() and lp[0, 2] == lp[0, 3]
+
+
+def test_many_ids():
+    run(make(5, 2, 5000), torch.randint(0, 5000, (2, 3001), dtype=torch.int32), 1)
+
+
+def test_signed_zeros_are_equal():
+    z = torch.zeros(1, 40)
+    z[0, ::2] = -0.0
+    _, _, top, _ = dsa.token_logprobs(z.to(DEV), top_k=32)
+    assert top[0].tolist() == list(range(32))
+
+
+@pytest.mark.parametrize("V", [64, 20000])
+@pytest.mark.parametrize("bad", ["nan", "inf", "none"])
+def test_rows_without_a_distribution_are_nan_alone(bad, V):
+    z = make(6, 3, V)
+    if bad == "none":
+        z[1] = -float("inf")
+    else:
+        z[1, V // 3] = float(bad)
+    lp, ent, top, tlp = dsa.token_logprobs(z.to(DEV), torch.zeros(3, 2, dtype=torch.int32,
+                                                                  device=DEV), top_k=6)
+    for t in (lp, ent, tlp):
+        assert torch.isnan(t[1]).all() and torch.isfinite(t[0]).all() and torch.isfinite(t[2]).all()
+    assert bool(((top >= 0) & (top < V)).all())
+
+
+def test_what_is_not_asked_for_is_none():
+    z = make(7, 2, 64).to(DEV)
+    assert dsa.token_logprobs(z)[0] is None and dsa.token_logprobs(z)[2] is None
+    assert dsa.token_logprobs(z, top_k=1, entropy=False)[1] is None
+
+
+def test_guards_streams_and_graphs():
+    z = make(8, 9, 30001)
+    zd = z.to(DEV)
+    ids = torch.randint(0, 30001, (9, 3), dtype=torch.int32, device=DEV)
+    want = dsa.token_logprobs(zd, ids, top_k=7)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = dsa.token_logprobs(zd, ids, top_k=7, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = dsa.token_logprobs(zd, ids, top_k=7)
+    zd.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, dsa.token_logprobs(zd, ids, top_k=7)))
+    pinned = dsa.token_logprobs(z.pin_memory(), ids.cpu().pin_memory(), top_k=7)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b.cpu()) for a, b in zip(pinned, want))
+
+
+def test_rows_past_32_bits():
+    """More than 2^32 bytes of logits: the last row."""
+    B, V = 4200, 262144
+    z = torch.zeros(B, V, device=DEV)
+    z[-1] = make(9, 1, V)[0].to(DEV)
+    ids = torch.zeros(B, 1, dtype=torch.int32, device=DEV)
+    lp, ent, top, tlp = dsa.token_logprobs(z, ids, top_k=3)
+    _, rent, rtop, _ = OT.logprobs(z[-1].double().cpu().numpy(), [0], 3)
+    assert top[-1].tolist() == list(rtop) and abs(float(ent[-1]) - rent) <= 4e-5 * (1 + rent)
+    assert top[-2].tolist() == [0, 1, 2]
