@@ -1197,8 +1197,7 @@ size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int m
   if (B < 0 || N < 1 || N > kTreeMaxNodes || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
       (D != 64 && D != 128) || max_len < 0 || num_parts < 0)
     return 0;
-  return tree_ws_bytes(B, N, Hq, Hkv, D,
-                       tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));
+  return tree_ws_bytes(D, tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));
 }
 
 dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_cache,
@@ -1212,6 +1211,9 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   if (st != DEC_OK) return st;
   if ((st = check_attn_shape(B, Hq, Hkv, D, T_cap, max_len)) != DEC_OK) return st;
   if (num_parts < 0) return fail(DEC_ERR_INVALID_ARG, "num_parts = %d < 0", num_parts);
+  // the stream's units (pair, 128 rows, 64 keys) are counted in 32 bits
+  if ((long long)B * Hkv * ((N * (Hq / Hkv) + 127) / 128) * (T_cap / 64 + 2) >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "B * Hkv * N * T_cap too large");
   if (num_parts > kTreeMaxParts)
     return fail(DEC_ERR_UNSUPPORTED, "num_parts = %d > %d", num_parts, kTreeMaxParts);
   if (window < 0) return fail(DEC_ERR_INVALID_ARG, "window = %d < 0", window);
@@ -1235,7 +1237,7 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   const int parts = tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current());
   if (workspace == nullptr || misaligned({workspace}, 256))
     return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
-  const size_t need = tree_ws_bytes(B, N, Hq, Hkv, D, parts);
+  const size_t need = tree_ws_bytes(D, parts);
   if (ws_bytes < need)
     return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   st = where_all_here({{q, "q", true}, {k_cache, "k_cache", false}, {v_cache, "v_cache", false},
@@ -1244,6 +1246,12 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
                        {slopes, "slopes", true}, {out, "out", true},
                        {workspace, "workspace", false}});
   if (st != DEC_OK) return st;
+  CUtensorMap maps[4];
+  if ((st = encode_cache_map(&maps[0], k_cache, B, Hkv, D, T_cap, 64)) != DEC_OK ||
+      (st = encode_cache_map(&maps[1], v_cache, B, Hkv, D, T_cap, 64)) != DEC_OK ||
+      (st = encode_cache_map(&maps[2], k_tree, B, Hkv, D, N, 64)) != DEC_OK ||
+      (st = encode_cache_map(&maps[3], v_tree, B, Hkv, D, N, 64)) != DEC_OK)
+    return st;
   TreeAttnArgs a{};
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.k_cache = static_cast<const __nv_bfloat16 *>(k_cache);
@@ -1264,7 +1272,7 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   a.window = window;
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
   a.softcap = softcap;
-  const cudaError_t e = launch_tree_attn(a, B, D, as_stream(stream));
+  const cudaError_t e = launch_tree_attn(maps, a, B, D, parts, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gqa_tree_attn launch");
   return ok();
 }

@@ -93,7 +93,8 @@ def check(out, ref, size, what=""):
     bound = 2.0 ** -8 * (np.abs(ref) + size) * 1.01 + 2.0 ** -11 * size + 1e-30
     err = np.abs(got - ref)
     bad = live & (err > bound)
-    assert not bad.any(), (what, int(bad.sum()), float((err / bound)[live].max()))
+    n_bad = int(bad.sum())
+    assert n_bad == 0, (what, n_bad, float((err / bound)[live].max()))
     num = np.linalg.norm((got - ref)[live])
     assert num <= 4e-3 * max(np.linalg.norm(ref[live]), 1e-30), what  # the framework's RMS bound
 
@@ -387,7 +388,7 @@ def run_rope(c, layout, theta=1e4, in_place=False, inv_freq=None):
         assert np.all(out[~live] == 7.0)
     size = np.abs(qr).max(-1, keepdims=True)
     bad = np.abs(out - qr)[live] > (2.0 ** -8 * np.abs(qr) + 2.0 ** -18 * size)[live]
-    assert not bad.any()
+    assert int(bad.sum()) == 0
     check_ulp(f64(kt), kr, "tree keys")
     assert np.array_equal(f64(vt), vr)
     return int(err.item())
