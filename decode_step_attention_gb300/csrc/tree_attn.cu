@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   using G = Geo<D>;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_bar[2 * S + 7];
+  __shared__ uint64_t s_bar[2 * S + 8];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_sum[kThreads / 32], s_begin[2];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t q_s = smem_addr(smem), ring = q_s + G::kQ;
   const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
   const uint32_t bar_s = bar_empty + 8 * S, bar_p = bar_s + 16, bar_pv = bar_p + 16;
-  const uint32_t bar_q = bar_pv + 8, bar_end = bar_q + 8;
+  const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = gridDim.x, piece = blockIdx.x;
 
@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(bar_p, kSoftmax);
     mbar_init(bar_p + 8, kSoftmax);
     mbar_init(bar_pv, 1);
+    mbar_init(bar_pv + 8, 1);
     mbar_init(bar_q, kSoftmax);
     mbar_init(bar_end, 1);
     s_abort = 0;
@@ -382,12 +383,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
       int n = 0, seg = 0;
       bool ok = true;
-      auto issue_s = [&](int i, bool first) {
+      auto issue_s = [&](int i) {
         const int it = 2 * i, slot = it % S;
-        // the buffer's last P, that of tile i - 2, is consumed. A segment's first S follows
-        // the value product of tile i - 1, so that one's phase is the one to wait for.
-        const int last = first ? i - 1 : i - 2;
-        if (last >= 0 && !wait(bar_pv, last & 1)) return false;
+        // the buffer's last P, that of tile i - 2, is consumed
+        if (i >= 2 && !wait(bar_pv + 8 * (i & 1), ((i - 2) >> 1) & 1)) return false;
         if (!wait(bar_full + 8 * slot, (it / S) & 1)) return false;
         tc_fence_after();
         const uint32_t k_s = ring + slot * G::kTensor;
@@ -402,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       do {
         const int cnt = w.t1 - w.t0;
-        ok = wait(bar_q, seg & 1) && issue_s(n, true);
+        ok = wait(bar_q, seg & 1) && issue_s(n);
         for (int i = 0; i < cnt && ok; ++i) {
-          if (i + 1 < cnt) ok = issue_s(n + i + 1, false);
+          if (i + 1 < cnt) ok = issue_s(n + i + 1);
           const int it = 2 * (n + i) + 1, slot = it % S;
           ok = ok && wait(bar_p + 8 * ((n + i) & 1), ((n + i) >> 1) & 1) &&
                wait(bar_full + 8 * slot, (it / S) & 1);
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             umma_bf16_ts(tmem + kOCol, tmem + ((n + i) & 1) * kTile + 8 * k,
                          smem_desc_mn_sw128(v_s + k * 2048, G::kSlab), idesc_o, i > 0 || k > 0);
           umma_commit(bar_empty + 8 * slot);
-          umma_commit(bar_pv);
+          umma_commit(bar_pv + 8 * ((n + i) & 1));
         }
         n += cnt;
         ++seg;
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             m = mn;
             l *= corr;
             if (t > w.t0) {  // O holds the tiles before this one
-              if (!wait_all(bar_pv, (n - 1) & 1)) ok = false;
+              if (!wait_all(bar_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) ok = false;
               tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // every S of this segment has been read, so Q's space is free; P of the last tile must
       // stay for the values to be given back
       if (more && odd == 0) load_q(w);
-      if (!wait_all(bar_pv, (n - 1) & 1)) break;
+      if (!wait_all(bar_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
       if (active) {
         const bool whole = done.t0 == 0 && done.t1 == done.s.tiles;

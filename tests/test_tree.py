@@ -238,6 +238,61 @@ def test_many_sequences():
     run(attn_case(13, lens, 3, 2, 1, 64, nodes=nodes))
 
 
+def gpu_reference(g, slopes=None, softcap=0.0, window=0):
+    """The definition in float64 torch on the GPU, a sequence at a time: (out, sum p |v|)."""
+    B, N, Hq, D = g["q"].shape
+    G = Hq // g["k_cache"].shape[1]
+    out = torch.full(g["q"].shape, NAN, dtype=torch.float64, device=DEV)
+    size = out.clone()
+    node = torch.arange(N, device=DEV)
+    for b in range(B):
+        L, n = int(g["lens"][b]), int(g["n_nodes"][b])
+        if n == 0:
+            continue
+        cat = lambda c, t: torch.cat([c[b, :, :L], t[b, :, :n]], 1).double()  # noqa: E731
+        K = cat(g["k_cache"], g["k_tree"]).repeat_interleave(G, 0)
+        V = cat(g["v_cache"], g["v_tree"]).repeat_interleave(G, 0)
+        p = g["pos"][b, :n].long()
+        far = p[:, None] - torch.cat([torch.arange(L, device=DEV), p])[None]
+        see = torch.cat([torch.ones(n, L, dtype=torch.bool, device=DEV),
+                         ((g["mask"][b, :n, None] >> node[:n]) & 1).bool()], 1)
+        if window:
+            see &= far < window
+        z = g["q"][b, :n].double().transpose(0, 1) @ K.transpose(1, 2) / D ** 0.5
+        if softcap:
+            z = softcap * torch.tanh(z / softcap)
+        if slopes is not None:
+            z = z - slopes.double()[:, None, None] * far
+        w = torch.softmax(z.masked_fill(~see, -float("inf")), -1)
+        out[b, :n], size[b, :n] = (w @ V).transpose(0, 1), (w @ V.abs()).transpose(0, 1)
+    return f64(out), f64(size)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,lo,hi,kw", [
+    (64, 32, 4, 128, 500, 3000, {}),                  # row tiles of 128, every SM busy
+    (64, 32, 4, 128, 500, 3000, {"window": 1000}),
+    (16, 32, 8, 128, 100, 4000, {"softcap": 50.0}),
+    (5, 16, 4, 64, 1, 6000, {"alibi": True}),
+    (1, 8, 8, 128, 1, 5000, {}),
+])
+def test_full_machine(N, Hq, Hkv, D, lo, hi, kw):
+    """Ragged batches that keep every SM at work on many segments, several times over."""
+    rng = np.random.default_rng(hi)
+    B = 24
+    lens = rng.integers(lo, hi, B).tolist()
+    nodes = rng.integers(max(1, N // 2), N + 1, B).tolist()
+    c = attn_case(17, lens, N, Hq, Hkv, D, nodes=nodes)
+    g = on_gpu(c)
+    kw = dict(kw)
+    if kw.pop("alibi", False):
+        kw["slopes"] = torch.exp2(-torch.arange(1.0, Hq + 1) / 2).to(DEV)
+    ref, size = gpu_reference(g, **kw)
+    first = call(g, **kw)
+    check(first, ref, size)
+    for _ in range(10):
+        assert torch.equal(call(g, **kw), first)
+
+
 def test_no_optional_arguments():
     c = attn_case(14, [77, 5], 6, 4, 2, 128)
     g = on_gpu(c)
