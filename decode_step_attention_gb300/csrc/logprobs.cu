@@ -7,8 +7,21 @@
 //   entropy     = ln S - (sum e^(z - M) (z - M)) / S      (nats)
 //   top K       : the K largest logits, equal ones by the lower id
 //
-// One CTA per row: a pass for the maximum, one for the sums, one per alternative.
+// One read of the logits. A row is cut over a cluster of CTAs; every thread streams 16-byte
+// vectors (the next ones in flight while it works on the last), keeping a running maximum,
+// both sums relative to it (moved only when a group of vectors exceeds it) and its largest
+// logit with its id. The threads' sums meet in shared memory, the CTAs' in distributed
+// shared memory.
+//
+// Alternatives without a sort of the row: a value and its id form one 64-bit key, all
+// different. The K-th largest of the threads' own maxima bounds the K-th largest key of the
+// slice from below, and only the K threads whose maximum reaches it can hold a larger one. So
+// K threads' vectors are read again (from L2), a warp each, into a list of the 32 largest
+// keys held across its lanes; the lists are merged pairwise, then the CTAs' lists. The cost
+// does not depend on the order of the values.
 #include <math.h>
+
+#include <atomic>
 
 #include "dec_device.cuh"
 #include "dec_launch.h"
@@ -16,90 +29,429 @@
 namespace decattn {
 namespace {
 
-constexpr int kThreads = 512;
+using u64 = unsigned long long;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
-__device__ __forceinline__ float logit(const LogprobArgs &a, size_t i) {
-  return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[i])
-                : static_cast<const float *>(a.logits)[i];
-}
+constexpr int kCtasPerSm = 4;
+constexpr int kUnroll = 4;       // vectors a thread works on at a time
+constexpr int kMaxCluster = 16;
+constexpr unsigned kAll = 0xffffffffu;
 
 // Orders by value, then by the lower id: larger is better. NaN orders by its bits.
-__device__ __forceinline__ unsigned long long rank_key(float v, int id) {
-  if (v == 0.f) v = 0.f;  // -0 and 0 are equal values
-  unsigned u = __float_as_uint(v);
+__device__ __forceinline__ u64 rank_key(float v, int id) {
+  unsigned u = __float_as_uint(v + 0.f);  // -0 and 0 are equal values
   u = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-  return ((unsigned long long)u << 32) | (unsigned)~id;
+  return ((u64)u << 32) | (unsigned)~id;
+}
+__device__ __forceinline__ int key_id(u64 k) { return (int)~(unsigned)k; }
+__device__ __forceinline__ float key_value(u64 k) {
+  const unsigned u = (unsigned)(k >> 32);
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 
-template <typename T, typename F>
-__device__ T block_reduce(T v, T *s, F f) {
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T r = s[0];
-  for (int w = 1; w < kWarps; ++w) r = f(r, s[w]);
+__device__ __forceinline__ u64 umax(u64 a, u64 b) { return a > b ? a : b; }
+__device__ __forceinline__ u64 umin(u64 a, u64 b) { return a < b ? a : b; }
+
+// One key per lane, sorted downwards (bitonic).
+__device__ __forceinline__ u64 warp_sort(u64 k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int step = size >> 1; step > 0; step >>= 1) {
+      const u64 o = __shfl_xor_sync(kAll, k, step);
+      const bool first = (lane & step) == 0, down = (lane & size) == 0 || size == 32;
+      k = first == down ? umax(k, o) : umin(k, o);
+    }
+  return k;
+}
+// The 32 largest of two lists sorted downwards; `b` is lane 31 - i's of the second.
+__device__ __forceinline__ u64 warp_merge(u64 a, u64 b) {
+  const int lane = threadIdx.x & 31;
+  u64 k = umax(a, b);
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1) {
+    const u64 o = __shfl_xor_sync(kAll, k, step);
+    k = (lane & step) == 0 ? umax(k, o) : umin(k, o);
+  }
+  return k;
+}
+// A key into a list sorted downwards; the smallest falls off.
+__device__ __forceinline__ u64 warp_insert(u64 list, u64 key) {
+  const int lane = threadIdx.x & 31;
+  const int at = __popc(__ballot_sync(kAll, list > key));
+  const u64 up = __shfl_up_sync(kAll, list, 1);
+  return lane < at ? list : lane == at ? key : up;
+}
+// The 32 largest of every warp's list, in warp 0 (all warps call; the others get what
+// their part of the tree left). s: kWarps x 32.
+__device__ __forceinline__ u64 block_merge(u64 list, u64 (*s)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = kWarps / 2; half > 0; half >>= 1) {
+    if (warp >= half && warp < 2 * half) s[warp][lane] = list;
+    __syncthreads();
+    if (warp < half) list = warp_merge(list, s[warp + half][31 - lane]);
+  }
+  return list;
+}
+
+template <bool kBf16>
+struct Vec {
+  static constexpr int kN = kBf16 ? 8 : 4;
+  __device__ static void unpack(uint4 x, float (&v)[kN]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kBf16) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      } else {
+        v[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+  __device__ static float one(const void *row, int i) {
+    return kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i])
+                 : static_cast<const float *>(row)[i];
+  }
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// A running softmax state: the maximum logit m, s = sum 2^(k (v - m)) and
+// c = sum 2^(k (v - m)) k (v - m), with k = log2(e) / T. Nothing seen: m = -inf.
+struct State {
+  float m, s, c;
+  // the sums relative to a larger maximum
+  __device__ __forceinline__ void raise(float to, float k) {
+    if (m != -INFINITY) {
+      const float d = (m - to) * k, f = ex2(d);
+      c = f > 0.f ? f * fmaf(d, s, c) : 0.f * c;  // keeps a NaN
+      s *= f;
+    }
+    m = to;
+  }
+  __device__ __forceinline__ void join(State o, float k) {
+    const float to = fmaxf(m, o.m);
+    raise(to, k);
+    o.raise(to, k);
+    s += o.s;
+    c += o.c;
+  }
+};
+
+struct Slice {  // what a CTA keeps for the others of its cluster
+  State st;
+  u64 list[32];
+};
+
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a) {
-  __shared__ float s_f[kWarps];
-  __shared__ unsigned long long s_k[kWarps];
+// grid (C, B), cluster (C, 1): CTA r of row b takes vectors [v0, v1) of the row; CTA 0 also
+// the elements before the first aligned vector, the last CTA those behind the last.
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const LogprobArgs a) {
+  using V = Vec<kBf16>;
+  constexpr int E = V::kN;
+  __shared__ u64 s_list[kWarps][32];
+  __shared__ Slice s_slice;
+  __shared__ State s_state[kWarps];
+  __shared__ float s_out[2];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const size_t row = blockIdx.x, base = row * (size_t)a.ld;
-  const int tid = threadIdx.x;
-  const float inv_t = 1.f / a.temperature;
-  float m = -INFINITY;
-  bool bad = false;
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float v = logit(a, base + i);
-    bad |= isnan(v);
-    m = fmaxf(m, v);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = gridDim.x, rank = blockIdx.x;
+  const size_t row = blockIdx.y;
+  const char *base = static_cast<const char *>(a.logits) + row * (size_t)a.ld * (kBf16 ? 2 : 4);
+  const float k = 1.4426950408889634f / a.temperature;
+  // the row as [head elements][nvec vectors][tail elements]
+  const int off = (int)((16u - (unsigned)(reinterpret_cast<uintptr_t>(base) & 15u)) & 15u);
+  const int head = min(a.V, off / (kBf16 ? 2 : 4));
+  const int nvec = (a.V - head) / E, tail0 = head + nvec * E;
+  const uint4 *vec = reinterpret_cast<const uint4 *>(base + (size_t)head * (kBf16 ? 2 : 4));
+  const int v0 = (int)((long long)nvec * rank / C), v1 = (int)((long long)nvec * (rank + 1) / C);
+
+  // the given ids' logits, on their way while the row streams
+  const bool has_id = rank == 0 && tid < a.C;
+  float id_value = -INFINITY;
+  if (has_id) {
+    const int id = a.ids[row * a.C + tid];
+    if (id >= 0 && id < a.V) id_value = V::one(base, id);
   }
-  bad = __syncthreads_or(bad);
-  m = block_reduce(m, s_f, [](float x, float y) { return fmaxf(x, y); });
-  float s = 0.f, c = 0.f;
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float d = (logit(a, base + i) - m) * inv_t, e = expf(d);
-    s += e;
-    if (e > 0.f) c = fmaf(e, d, c);
-  }
-  auto add = [](float x, float y) { return x + y; };
-  s = block_reduce(s, s_f, add);
-  c = block_reduce(c, s_f, add);
-  const float ln_s = (bad || isinf(m)) ? NAN : logf(s);
-  if (tid == 0 && a.entropy != nullptr) a.entropy[row] = ln_s - c / s;
-  for (int i = tid; i < a.C; i += kThreads) {
-    const int id = a.ids[row * a.C + i];
-    const float v = id >= 0 && id < a.V ? logit(a, base + id) : -INFINITY;
-    a.logprobs[row * a.C + i] = (v - m) * inv_t - ln_s;
-  }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < a.K; ++k) {
-    unsigned long long best = 0;
-    for (int i = tid; i < a.V; i += kThreads) {
-      const unsigned long long key = rank_key(logit(a, base + i), i);
-      if (key < last && key > best) best = key;
+
+  State st{-INFINITY, 0.f, 0.f};
+  float best = -INFINITY;
+  int best_id = -1;  // none yet
+  auto group = [&](const float *v, int n, auto id_of) {
+    float mx = v[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) mx = fmaxf(mx, v[i]);
+    if (mx > st.m) st.raise(mx, k);
+    if (mx > best || best_id < 0) {  // strictly: equal values keep the lower id
+      best = mx;
+#pragma unroll
+      for (int i = n - 1; i >= 0; --i)
+        if (v[i] == mx || best_id < 0) best_id = id_of(i);
     }
-    best = block_reduce(best, s_k, [](unsigned long long x, unsigned long long y) {
-      return x > y ? x : y;
-    });
-    last = best;
-    if (tid == 0) {
-      const int id = (int)~(unsigned)best;
-      a.top_ids[row * a.K + k] = id;
-      a.top_logprobs[row * a.K + k] = (logit(a, base + id) - m) * inv_t - ln_s;
+    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+    float s = 0.f, c = 0.f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      // The difference first: k v - k m would carry the rounding of k m into every weight.
+      // Far below the maximum (or -inf): weight 0, and a finite factor beside it.
+      const float d = max_nan((v[i] - m0) * k, -400.f), e = ex2(d);
+      s += e;
+      c = fmaf(e, d, c);
+    }
+    st.s += s;
+    st.c += c;
+  };
+  if (rank == 0 && tid < head) {
+    const float v = V::one(base, tid);
+    group(&v, 1, [&](int) { return tid; });
+  }
+  {
+    uint4 next[kUnroll];
+    int at = v0 + tid;
+    auto load = [&](int from) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (from + u * kThreads < v1) next[u] = ld_stream(vec + from + u * kThreads);
+    };
+    load(at);
+    while (at < v1) {
+      uint4 cur[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+      const int here = at;
+      at += kUnroll * kThreads;
+      load(at);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (here + u * kThreads < v1) {
+          float v[E];
+          V::unpack(cur[u], v);
+          const int first = head + (here + u * kThreads) * E;
+          group(v, E, [&](int i) { return first + i; });
+        }
     }
   }
+  if (rank == C - 1 && tail0 + tid < a.V) {
+    const float v = V::one(base, tail0 + tid);
+    group(&v, 1, [&](int) { return tail0 + tid; });
+  }
+
+  // ---- the slice's sums
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    State x;
+    x.m = __shfl_xor_sync(kAll, st.m, o);
+    x.s = __shfl_xor_sync(kAll, st.s, o);
+    x.c = __shfl_xor_sync(kAll, st.c, o);
+    st.join(x, k);
+  }
+  if (lane == 0) s_state[warp] = st;
+
+  // ---- the slice's 32 best
+  if (a.K > 0) {
+    const u64 mine = best_id < 0 ? 0ull : rank_key(best, best_id);
+    u64 list = block_merge(warp_sort(mine), s_list);
+    if (a.K > 1) {
+      if (warp == 0) s_slice.list[lane] = list;
+      __syncthreads();
+      const u64 bar = s_slice.list[a.K - 1];  // 0: fewer than K threads hold anything
+      list = 0;
+      for (int i = warp; i < a.K; i += kWarps) {
+        const u64 top = s_slice.list[i];
+        if (top == 0) break;
+        const int id = key_id(top);
+        // its owner's elements: one of the head or tail, and every kThreads-th vector
+        const int owner = id < head ? id : id >= tail0 ? id - tail0 : ((id - head) / E - v0) % kThreads;
+        auto offer = [&](u64 key) {
+          unsigned todo = __ballot_sync(kAll, key >= bar && key > 0);
+          while (todo) {
+            const int from = __ffs(todo) - 1;
+            todo &= todo - 1;
+            list = warp_insert(list, __shfl_sync(kAll, key, from));
+          }
+        };
+        for (int j0 = v0 + owner; j0 < v1; j0 += 32 * kThreads) {
+          const int j = j0 + lane * kThreads;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (j < v1) x = ld_stream(vec + j);
+          float v[E];
+          V::unpack(x, v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) offer(j < v1 ? rank_key(v[e], head + j * E + e) : 0ull);
+        }
+        u64 extra = 0;
+        if (lane == 0 && rank == 0 && owner < head) extra = rank_key(V::one(base, owner), owner);
+        if (lane == 1 && rank == C - 1 && tail0 + owner < a.V)
+          extra = rank_key(V::one(base, tail0 + owner), tail0 + owner);
+        offer(extra);
+      }
+      __syncthreads();  // the bound has been read by all
+      list = block_merge(list, s_list);
+    }
+    if (warp == 0) s_slice.list[lane] = list;
+  } else {
+    __syncthreads();
+  }
+  if (tid == 0) {
+    State t = s_state[0];
+    for (int w = 1; w < kWarps; ++w) t.join(s_state[w], k);
+    s_slice.st = t;
+  }
+  // ---- the row, in CTA 0
+  cluster_sync();
+  if (rank == 0) {
+    const uint32_t here = smem_addr(&s_slice);
+    if (warp == 0) {
+      State t{-INFINITY, 0.f, 0.f};
+      if (lane < C) {
+        const uint32_t p = cluster_map(here, lane);
+        t.m = ld_cluster_f32(p);
+        t.s = ld_cluster_f32(p + 4);
+        t.c = ld_cluster_f32(p + 8);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        State x;
+        x.m = __shfl_xor_sync(kAll, t.m, o);
+        x.s = __shfl_xor_sync(kAll, t.s, o);
+        x.c = __shfl_xor_sync(kAll, t.c, o);
+        t.join(x, k);
+      }
+      if (lane == 0) {
+        const float ln_s = isinf(t.m) ? NAN : logf(t.s);
+        s_out[0] = t.m;
+        s_out[1] = ln_s;
+        if (a.entropy != nullptr) a.entropy[row] = ln_s - t.c / t.s * 0.6931471805599453f;
+      }
+    }
+    u64 list = 0;
+    if (a.K > 0) {
+      for (int r = warp; r < C; r += kWarps) {
+        const uint32_t p = cluster_map(here + (uint32_t)offsetof(Slice, list), r);
+        list = warp_merge(list, ld_cluster_u64(p + 8 * (31 - lane)));
+      }
+    }
+    __syncthreads();
+    const float m = s_out[0], ln_s = s_out[1], inv_t = 1.f / a.temperature;
+    if (has_id) a.logprobs[row * a.C + tid] = (id_value - m) * inv_t - ln_s;
+    for (int i = tid + kThreads; i < a.C; i += kThreads) {
+      const int id = a.ids[row * a.C + i];
+      const float v = id >= 0 && id < a.V ? V::one(base, id) : -INFINITY;
+      a.logprobs[row * a.C + i] = (v - m) * inv_t - ln_s;
+    }
+    if (a.K > 0) {
+      list = block_merge(list, s_list);
+      if (warp == 0 && lane < a.K) {
+        // in a row with NaN fewer than K keys may have been found: any id in range then
+        a.top_ids[row * a.K + lane] = list == 0 ? lane : key_id(list);
+        a.top_logprobs[row * a.K + lane] = (key_value(list) - m) * inv_t - ln_s;
+      }
+    }
+  }
+  if (C > 1) cluster_sync();  // no CTA leaves while another still reads its shared memory
+}
+
+// CTAs per row: the fewest that give every SM its CTAs and a few waves to even out, as long
+// as each thread keeps at least two vectors.
+int row_ctas(int B, int V, bool bf16, int sms) {
+  const long long nvec = V / (bf16 ? 8 : 4);
+  int c = 1;
+  while (c < kMaxCluster && (long long)B * c < 2ll * kCtasPerSm * sms &&
+         nvec >= 2ll * kThreads * (2 * c))
+    c *= 2;
+  return c;
+}
+
+template <bool kBf16>
+cudaError_t launch(const LogprobArgs &a, int B, cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(logprobs_kernel<kBf16>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  const int c = row_ctas(B, a.V, kBf16, sms);
+  constexpr int kMaxGridY = 65535;
+  for (int b0 = 0; b0 < B; b0 += kMaxGridY) {
+    LogprobArgs x = a;
+    x.logits = static_cast<const char *>(a.logits) + (size_t)b0 * a.ld * (kBf16 ? 2 : 4);
+    if (a.C > 0) {
+      x.ids += (size_t)b0 * a.C;
+      x.logprobs += (size_t)b0 * a.C;
+    }
+    if (a.entropy != nullptr) x.entropy += b0;
+    if (a.K > 0) {
+      x.top_ids += (size_t)b0 * a.K;
+      x.top_logprobs += (size_t)b0 * a.K;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c, B - b0 < kMaxGridY ? B - b0 : kMaxGridY);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if ((e = cudaLaunchKernelEx(&cfg, logprobs_kernel<kBf16>, x)) != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs &a, int B, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(logprobs_kernel, dim3(B), kThreads, 0, stream, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return a.bf16 ? launch<true>(a, B, stream) : launch<false>(a, B, stream);
 }
 
 }  // namespace decattn
