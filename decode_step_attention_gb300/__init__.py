@@ -157,6 +157,27 @@ def _stream(stream=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _handle(stream=None) -> int:
+    """The stream handle of a call. Without a stream argument it is asked for without
+    building a torch.cuda.Stream (3 us of a call's host time)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _at(t, name: str, dtype, shape, host: bool = False) -> int:
+    """:func:`_need`, and the tensor's address; the usual case in one line (the checks are a
+    large part of a small call's host time)."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, host)
+    return t.data_ptr()
+
+
+def _maybe_at(t, name: str, dtype, shape, host: bool = False):
+    return None if t is None else _at(t, name, dtype, shape, host)
+
+
 def _ptr(t) -> ctypes.c_void_p | None:
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -639,26 +660,39 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0
     What was not asked for is None."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, BF16):
         raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
-    _need(logits, "logits", logits.dtype, host=True)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [B, ld], got {tuple(logits.shape)}")
     B, ld = logits.shape
+    at = _at(logits, "logits", logits.dtype, (B, ld), host=True)
     V = ld if vocab is None else int(vocab)
     C, K = 0, int(top_k)
+    tokens_at = None
     if tokens is not None:
-        _need(tokens, "tokens", I32, host=True)
+        if not isinstance(tokens, torch.Tensor):
+            raise TypeError("tokens must be a torch.Tensor")
         if tokens.dim() != 2 or tokens.shape[0] != B:
             raise ValueError(f"tokens must be [B, C], got {tuple(tokens.shape)}")
         C = tokens.shape[1]
-    with _on(stream):
-        lp = None if tokens is None else _empty((B, C), torch.float32, logits)
-        ent = _empty((B,), torch.float32, logits) if entropy else None
-        ids = _empty((B, K), I32, logits) if K > 0 else None
-        top = _empty((B, K), torch.float32, logits) if K > 0 else None
-    _call("dec_token_logprobs", _ptr(logits), 0 if logits.dtype == torch.float32 else 1, ld,
-          _ptr(tokens) if C else None, C, _ptr(lp) if C else None, _ptr(ent), _ptr(ids),
-          _ptr(top), K, B, V, float(temperature), _stream(stream))
-    return lp, ent, ids, top
+        tokens_at = _at(tokens, "tokens", I32, (B, C), host=True)
+    if stream is None:
+        outs = _logprob_outputs(logits, B, C, K, tokens is not None, entropy)
+    else:
+        with torch.cuda.stream(stream):
+            outs = _logprob_outputs(logits, B, C, K, tokens is not None, entropy)
+    lp, ent, ids, top = outs
+    _call("dec_token_logprobs", at, 0 if logits.dtype is torch.float32 else 1, ld,
+          tokens_at if C else None, C, lp.data_ptr() if C else None,
+          ent.data_ptr() if entropy else None, ids.data_ptr() if K > 0 else None,
+          top.data_ptr() if K > 0 else None, K, B, V, temperature, _handle(stream))
+    return outs
+
+
+def _logprob_outputs(logits, B, C, K, given, entropy):
+    f32 = torch.float32
+    return (_empty((B, C), f32, logits) if given else None,
+            _empty((B,), f32, logits) if entropy else None,
+            _empty((B, K), I32, logits) if K > 0 else None,
+            _empty((B, K), f32, logits) if K > 0 else None)
 
 
 # -------------------------------------------------------------- draft trees ---
@@ -670,34 +704,30 @@ def qknorm_rope_tree(q, k_new, v_new, k_tree, v_tree, pos, theta: float, layout=
     [B, N, Hkv, D] into the tree's buffers k_tree, v_tree [B, Hkv, N, D]. ``n_nodes`` [B]
     (int32): the nodes each sequence has; those behind are left as they were. Returns the
     rotated q."""
-    _need(q, "q", BF16, host=True)
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
-    B, N, Hq, D = q.shape
-    _need(k_tree, "k_tree", BF16)
-    if k_tree.dim() != 4:
-        raise ValueError(f"k_tree must be [B, Hkv, N, D], got {tuple(k_tree.shape)}")
-    Hkv = k_tree.shape[1]
-    _need(k_tree, "k_tree", BF16, (B, Hkv, N, D))
-    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
-    _need(k_new, "k_new", BF16, (B, N, Hkv, D), host=True)
-    _need(v_new, "v_new", BF16, (B, N, Hkv, D), host=True)
-    _need(pos, "pos", I32, (B, N), host=True)
-    if n_nodes is not None:
-        _need(n_nodes, "n_nodes", I32, (B,), host=True)
-    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
-        if w is not None:
-            _need(w, name, BF16, (D,), host=True)
+    B, N, Hq, D = _dims4(q, "q", "[B, N, Hq, D]")
+    Hkv = _dims4(k_tree, "k_tree", "[B, Hkv, N, D]")[1]
     if error_word is not None:
         _need(error_word, "error_word", I32, host=True)
     if q_out is None:
         q_out = q
-    _need(q_out, "q_out", BF16, (B, N, Hq, D), host=True)
-    _call("dec_qknorm_rope_tree", _ptr(q), _ptr(q_out), _ptr(k_new), _ptr(v_new), _ptr(q_norm_w),
-          _ptr(k_norm_w), _ptr(k_tree), _ptr(v_tree), _ptr(pos), _ptr(n_nodes), B, N, Hq, Hkv, D,
-          float(theta), _LAYOUTS[layout], _freq(inv_freq, D), float(eps), _ptr(error_word),
-          _stream(stream))
+    nodes, heads, new = (B, N, Hq, D), (B, Hkv, N, D), (B, N, Hkv, D)
+    _call("dec_qknorm_rope_tree", _at(q, "q", BF16, nodes, True),
+          _at(q_out, "q_out", BF16, nodes, True), _at(k_new, "k_new", BF16, new, True),
+          _at(v_new, "v_new", BF16, new, True),
+          _maybe_at(q_norm_w, "q_norm_w", BF16, (D,), True),
+          _maybe_at(k_norm_w, "k_norm_w", BF16, (D,), True), _at(k_tree, "k_tree", BF16, heads),
+          _at(v_tree, "v_tree", BF16, heads), _at(pos, "pos", I32, (B, N), True),
+          _maybe_at(n_nodes, "n_nodes", I32, (B,), True), B, N, Hq, Hkv, D, theta,
+          _LAYOUTS[layout], _freq(inv_freq, D), eps, _ptr(error_word), _handle(stream))
     return q_out
+
+
+def _dims4(t, name: str, what: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be {what}, got {tuple(t.shape)}")
+    return t.shape
 
 
 def tree_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, max_len: int,
@@ -728,40 +758,29 @@ def gqa_tree_attn(q, k_cache, v_cache, lens, k_tree, v_tree, mask, n_nodes=None,
     slope * (distance to the key) is subtracted. ``window`` > 0: keys at a distance of at
     least ``window`` are not seen. Both need the nodes' positions ``pos`` (int32 [B, N],
     the sequence's length plus the node's depth). N = 1 is the single-token form."""
-    _need(q, "q", BF16, host=True)
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
-    B, N, Hq, D = q.shape
-    _need(k_cache, "k_cache", BF16)
-    if k_cache.dim() != 4 or k_cache.shape[0] != B or k_cache.shape[3] != D:
-        raise ValueError(f"k_cache shape {tuple(k_cache.shape)} does not match q {tuple(q.shape)}")
-    Hkv, T_cap = k_cache.shape[1], k_cache.shape[2]
-    _need(v_cache, "v_cache", BF16, (B, Hkv, T_cap, D))
-    _need(k_tree, "k_tree", BF16, (B, Hkv, N, D))
-    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
-    _need(lens, "lens", I32, (B,), host=True)
-    _need(mask, "mask", torch.int64, (B, N), host=True)
-    if n_nodes is not None:
-        _need(n_nodes, "n_nodes", I32, (B,), host=True)
-    if pos is not None:
-        _need(pos, "pos", I32, (B, N), host=True)
-    if slopes is not None:
-        _need(slopes, "slopes", torch.float32, (Hq,), host=True)
+    B, N, Hq, D = _dims4(q, "q", "[B, N, Hq, D]")
+    _, Hkv, T_cap, _ = _dims4(k_cache, "k_cache", "[B, Hkv, T_cap, D]")
     max_len = T_cap if max_len is None else int(max_len)
-    with _on(stream):
-        if workspace is None:
-            workspace = alloc_tree_workspace(B, N, Hq, Hkv, D, max_len, num_parts,
-                                             k_cache.device)
-        if out is None:
-            out = _empty(q.shape, BF16, q)
-            if n_nodes is not None:
-                out.zero_()
+    if workspace is None or out is None:
+        with _on(stream):
+            if workspace is None:
+                workspace = alloc_tree_workspace(B, N, Hq, Hkv, D, max_len, num_parts,
+                                                 k_cache.device)
+            if out is None:
+                out = _empty(q.shape, BF16, q)
+                if n_nodes is not None:
+                    out.zero_()
     _need(workspace, "workspace", torch.uint8)
-    _need(out, "out", BF16, (B, N, Hq, D), host=True)
-    _call("dec_gqa_tree_attn", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lens), _ptr(k_tree),
-          _ptr(v_tree), _ptr(mask), _ptr(n_nodes), _ptr(pos), _ptr(slopes), _ptr(out), B, N, Hq,
-          Hkv, D, T_cap, max_len, float(scale), float(softcap), int(window), int(num_parts),
-          _ptr(workspace), workspace.numel(), _stream(stream))
+    nodes, cache, tree = (B, N, Hq, D), (B, Hkv, T_cap, D), (B, Hkv, N, D)
+    _call("dec_gqa_tree_attn", _at(q, "q", BF16, nodes, True), _at(k_cache, "k_cache", BF16, cache),
+          _at(v_cache, "v_cache", BF16, cache), _at(lens, "lens", I32, (B,), True),
+          _at(k_tree, "k_tree", BF16, tree), _at(v_tree, "v_tree", BF16, tree),
+          _at(mask, "mask", torch.int64, (B, N), True),
+          _maybe_at(n_nodes, "n_nodes", I32, (B,), True),
+          _maybe_at(pos, "pos", I32, (B, N), True),
+          _maybe_at(slopes, "slopes", torch.float32, (Hq,), True),
+          _at(out, "out", BF16, nodes, True), B, N, Hq, Hkv, D, T_cap, max_len, scale, softcap,
+          window, num_parts, workspace.data_ptr(), workspace.numel(), _handle(stream))
     return out
 
 
@@ -770,24 +789,16 @@ def tree_commit(k_tree, v_tree, path, n_path, k_cache, v_cache, lens, error_word
     """The accepted path of a draft tree into the cache: for i < n_path[b], cache slot
     lens[b] + i <- node path[b, i] (K and V, bit copies). ``lens`` itself is the caller's to
     advance (``lens += n_path``)."""
-    _need(k_tree, "k_tree", BF16)
-    if k_tree.dim() != 4:
-        raise ValueError(f"k_tree must be [B, Hkv, N, D], got {tuple(k_tree.shape)}")
-    B, Hkv, N, D = k_tree.shape
-    _need(v_tree, "v_tree", BF16, (B, Hkv, N, D))
-    _need(k_cache, "k_cache", BF16)
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [B, Hkv, T_cap, D], got {tuple(k_cache.shape)}")
-    T_cap = k_cache.shape[2]
-    _need(k_cache, "k_cache", BF16, (B, Hkv, T_cap, D))
-    _need(v_cache, "v_cache", BF16, (B, Hkv, T_cap, D))
-    _need(path, "path", I32, (B, N), host=True)
-    _need(n_path, "n_path", I32, (B,), host=True)
-    _need(lens, "lens", I32, (B,), host=True)
+    B, Hkv, N, D = _dims4(k_tree, "k_tree", "[B, Hkv, N, D]")
+    T_cap = _dims4(k_cache, "k_cache", "[B, Hkv, T_cap, D]")[2]
     if error_word is not None:
         _need(error_word, "error_word", I32, host=True)
-    _call("dec_tree_commit", _ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(n_path), _ptr(k_cache),
-          _ptr(v_cache), _ptr(lens), B, N, Hkv, D, T_cap, _ptr(error_word), _stream(stream))
+    tree, cache = (B, Hkv, N, D), (B, Hkv, T_cap, D)
+    _call("dec_tree_commit", _at(k_tree, "k_tree", BF16, tree), _at(v_tree, "v_tree", BF16, tree),
+          _at(path, "path", I32, (B, N), True), _at(n_path, "n_path", I32, (B,), True),
+          _at(k_cache, "k_cache", BF16, cache), _at(v_cache, "v_cache", BF16, cache),
+          _at(lens, "lens", I32, (B,), True), B, N, Hkv, D, T_cap, _ptr(error_word),
+          _handle(stream))
 
 
 # ------------------------------------------------------------ CUDA graph ---

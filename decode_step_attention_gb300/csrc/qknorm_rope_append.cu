@@ -152,11 +152,18 @@ InvFreq make_inv_freq(int D, double theta) {
 }
 
 RopeTurns make_rope_turns(int D, const InvFreq &inv) {
+  // f = inv_freq / (2 pi) as the unevaluated sum p + e of two doubles (about 2^-104 of it),
+  // then its integer part in units of 2^-64 and the rest rounded: the nearest integer to
+  // within 2^-40 of a unit, on every host, without the software quadruple precision that
+  // long double is on some (5 us per table there).
   RopeTurns t{};
-  const long double two_pi = 6.283185307179586476925286766559L;
+  constexpr double kHi = 0.15915494309189535;      // 1 / (2 pi): the nearest double
+  constexpr double kLo = -9.839338337591243e-18;   // and what it lacks
   for (int i = 0; i < D / 2; ++i) {
-    const long double f = (long double)inv.v[i] / two_pi;
-    t.v[i] = (unsigned long long)llroundl(ldexpl(f, 64));  // f <= 1/(2 pi): below 2^62
+    const double f = inv.v[i], p = f * kHi, e = fma(f, kHi, -p) + f * kLo;
+    const double unit = 18446744073709551616.0;    // 2^64, exact scalings
+    const double whole = floor(p * unit);          // f <= 1: below 2^62
+    t.v[i] = (unsigned long long)((long long)whole + llround((p * unit - whole) + e * unit));
   }
   return t;
 }

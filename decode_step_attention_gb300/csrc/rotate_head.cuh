@@ -77,12 +77,13 @@ __device__ __forceinline__ void lane_freqs(const InvFreq &inv, int interleaved,
 
 // The rotation of one head held by a warp (x, and the norm weights w when has_norm):
 // optional RMSNorm over D, then RoPE at position p into y. A key (is_k) keeps the stored
-// copy within one bf16 ulp where the fp32 rotation cancels (rope_exact).
-template <int D>
+// copy within one bf16 ulp where the fp32 rotation cancels: exact(e, own, other, rstd, second)
+// forms that element again (rope_exact).
+template <int D, typename Exact>
 __device__ __forceinline__ void rotate_values(const float (&x_in)[Lanes<D>::kE],
                                               const float (&w)[Lanes<D>::kE], bool has_norm,
-                                              bool is_k, const LaneAngles<D> &ang, int p,
-                                              const double (&fr)[Lanes<D>::kE], int interleaved,
+                                              bool is_k, const LaneAngles<D> &ang,
+                                              Exact exact, int interleaved,
                                               float eps, float (&y)[Lanes<D>::kE]) {
   constexpr int E = Lanes<D>::kE;
   const int lane = threadIdx.x & 31;
@@ -114,7 +115,7 @@ __device__ __forceinline__ void rotate_values(const float (&x_in)[Lanes<D>::kE],
       const float c = ang.c[e], sn = ang.s[e];
       y[e] = first ? (x[e] * c - other * sn) : (other * sn + x[e] * c);
       if (is_k && rope_cancels(y[e], x[e], other))  // K: the stored copy within one ulp
-        y[e] = rope_exact(p, fr[e], xw[e], other_w, rstd, !first);
+        y[e] = exact(e, xw[e], other_w, rstd, !first);
     }
   } else {
     // Interleaved: element 2i pairs with 2i + 1, both in this lane.
@@ -124,9 +125,9 @@ __device__ __forceinline__ void rotate_values(const float (&x_in)[Lanes<D>::kE],
       y[e] = x[e] * c - x[e + 1] * sn;
       y[e + 1] = x[e] * sn + x[e + 1] * c;
       if (is_k && rope_cancels(y[e], x[e], x[e + 1]))
-        y[e] = rope_exact(p, fr[e], xw[e], xw[e + 1], rstd, false);
+        y[e] = exact(e, xw[e], xw[e + 1], rstd, false);
       if (is_k && rope_cancels(y[e + 1], x[e], x[e + 1]))
-        y[e + 1] = rope_exact(p, fr[e], xw[e + 1], xw[e], rstd, true);
+        y[e + 1] = exact(e, xw[e + 1], xw[e], rstd, true);
     }
   }
 }
@@ -152,7 +153,12 @@ __device__ __forceinline__ void rotate_head_loaded(
   double fr[E] = {};
   if (!is_q) lane_freqs<D>(inv, interleaved, fr);  // for the exact path of a cancelling K
   float y[E];
-  rotate_values<D>(x, w, nw != nullptr, !is_q, ang, p, fr, interleaved, eps, y);
+  rotate_values<D>(
+      x, w, nw != nullptr, !is_q, ang,
+      [&](int e, float own, float other, float rstd, bool second) {
+        return rope_exact(p, fr[e], own, other, rstd, second);
+      },
+      interleaved, eps, y);
   if (is_q) {
     L::store(q_out + ((size_t)b * Hq + task) * D + e0, y);
   } else {

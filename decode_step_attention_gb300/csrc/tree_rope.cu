@@ -11,7 +11,6 @@
 #include "dec_device.cuh"
 #include "dec_launch.h"
 #include "rope_angles.cuh"
-#include "rotate_head.cuh"
 
 namespace decattn {
 namespace {
@@ -28,57 +27,157 @@ struct TreeRopeArgs {
   float eps;
 };
 
-// One CTA per (node, block of heads): the node's D/2 angles once in shared memory, then a
-// warp per head.
-template <int D>
-__global__ void __launch_bounds__(kThreads) tree_rope_kernel(const TreeRopeArgs a,
-                                                             const InvFreq inv,
-                                                             const RopeTurns turns) {
-  using L = Lanes<D>;
-  constexpr int E = L::kE;
-  __shared__ float s_cos[D / 2];
-  __shared__ float s_sin[D / 2];
+// Elements of a rotated key whose fp32 rotation cancels (bits of this lane's 8), formed again
+// in fp64 from the stored input and written over. Rare: one lane in some 300.
+__device__ __noinline__ void exact_elements(const __nv_bfloat16 *k, const __nv_bfloat16 *w,
+                                            __nv_bfloat16 *dst,
+                                            const unsigned long long *turns, int half,
+                                            int interleaved, int e0, int p, float rstd,
+                                            unsigned bits) {
+  for (; bits != 0; bits &= bits - 1) {
+    const int j = e0 + __ffs(bits) - 1;
+    const int other = interleaved ? j ^ 1 : j ^ half;  // the head's D is 2 half, a power of 2
+    const int pair = interleaved ? j >> 1 : j & (half - 1);
+    const bool second = interleaved ? (j & 1) != 0 : j >= half;
+    const float wj = w != nullptr ? __bfloat162float(w[j]) : 1.f;
+    const float wo = w != nullptr ? __bfloat162float(w[other]) : 1.f;
+    dst[j] = __float2bfloat16(rope_exact_turns(p, turns[pair], __bfloat162float(k[j]) * wj,
+                                               __bfloat162float(k[other]) * wo, rstd, second));
+  }
+}
+
+// One CTA per (node, block of heads). A head is D / 8 lanes of 16 bytes, so a warp turns 2 (D =
+// 128) or 4 (64) heads at a time, P times over: q heads, then k heads, then v heads (copied).
+// Every load is in flight while the node's D/2 angles are formed in shared memory. The
+// arithmetic is that of rotate_head.cuh in another lane layout: the same sums in the same
+// order, so both give the same bits.
+template <int D, int P>
+__global__ void __launch_bounds__(kThreads, 5)
+    tree_rope_kernel(const TreeRopeArgs a, const __grid_constant__ RopeTurns turns) {
+  constexpr int kLanes = D / 8;           // lanes per head
+  constexpr int kHeads = 32 / kLanes;     // heads per warp and pass
+  constexpr int kStep = kWarps * kHeads;  // heads per pass of the CTA
+  constexpr int kOld = D / 32;            // elements summed in one chain
+  constexpr int kChains = 8 / kOld;
+  __shared__ __align__(16) float s_cos[D / 2];
+  __shared__ __align__(16) float s_sin[D / 2];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int row = blockIdx.x, b = row / a.N, n = row - b * a.N;
-  const int warp = threadIdx.x >> 5, e0 = (threadIdx.x & 31) * E;
-  if (a.n_nodes != nullptr) {
-    const int live = a.n_nodes[b];
-    if ((live < 0 || live > a.N) && threadIdx.x == 0 && n == 0 && blockIdx.y == 0 &&
-        a.error_word != nullptr)
-      atomicOr(a.error_word, kErrTreeClamped);
-    if (n >= live) return;
-  }
+  const int n = blockIdx.x, b = blockIdx.z;
+  const size_t row = (size_t)b * a.N + n;
+  const int live = a.n_nodes != nullptr ? a.n_nodes[b] : a.N;
   const int p = a.pos[row];
-  if (p < 0) {
-    if (threadIdx.x == 0 && blockIdx.y == 0 && a.error_word != nullptr)
-      atomicOr(a.error_word, kErrPosSkipped);
-    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hl = lane & (kLanes - 1), e0 = hl * 8;
+  const int rotated = a.Hq + a.Hkv, heads = rotated + a.Hkv;
+  const int task0 = (blockIdx.y * P * kWarps + warp) * kHeads + lane / kLanes;
+  if (threadIdx.x == 0 && blockIdx.y == 0 && a.error_word != nullptr) {
+    if (n == 0 && (live < 0 || live > a.N)) atomicOr(a.error_word, kErrTreeClamped);
+    if (n < live && p < 0) atomicOr(a.error_word, kErrPosSkipped);
+  }
+  if (n >= live || p < 0) return;
+  const __nv_bfloat16 *q_src = a.q_in + row * a.Hq * D + e0;
+  const __nv_bfloat16 *k_src = a.k_new + row * a.Hkv * D + e0 - a.Hq * D;
+  const __nv_bfloat16 *v_src = a.v_new + row * a.Hkv * D + e0 - rotated * D;
+  uint4 raw[P], wq = {}, wk = {};
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int task = task0 + i * kStep;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (task < heads)
+      raw[i] = *reinterpret_cast<const uint4 *>(
+          (task < a.Hq ? q_src : task < rotated ? k_src : v_src) + task * D);
+  }
+  const bool norm = a.q_norm_w != nullptr;
+  if (norm) {
+    wq = *reinterpret_cast<const uint4 *>(a.q_norm_w + e0);
+    wk = *reinterpret_cast<const uint4 *>(a.k_norm_w + e0);
   }
   for (int i = threadIdx.x; i < D / 2; i += kThreads)
     rope_sincos_turns(p, turns.v[i], s_sin[i], s_cos[i]);
   __syncthreads();
-  const int task = blockIdx.y * kWarps + warp;
-  if (task >= a.Hq + a.Hkv) return;
-  const bool is_q = task < a.Hq;
-  const int g = task - a.Hq;
-  const __nv_bfloat16 *nw = is_q ? a.q_norm_w : a.k_norm_w;
-  const size_t q_at = ((size_t)row * a.Hq + task) * D + e0;
-  const size_t kv_at = ((size_t)row * a.Hkv + g) * D + e0;
-  float x[E], w[E] = {}, y[E];
-  L::load(is_q ? a.q_in + q_at : a.k_new + kv_at, x);
-  if (nw != nullptr) L::load(nw + e0, w);
-  LaneAngles<D> ang;
-  ang.from_table(s_cos, s_sin, a.interleaved);
-  double fr[E] = {};
-  if (!is_q) lane_freqs<D>(inv, a.interleaved, fr);  // for the exact path of a cancelling K
-  rotate_values<D>(x, w, nw != nullptr, !is_q, ang, p, fr, a.interleaved, a.eps, y);
-  if (is_q) {
-    L::store(a.q_out + q_at, y);
-  } else {
-    const size_t slot = (((size_t)b * a.Hkv + g) * a.N + n) * D + e0;
-    L::store(a.k_tree + slot, y);
-    L::copy(a.v_tree + slot, a.v_new + kv_at);
+  const bool first = hl < kLanes / 2;
+  const size_t kv_at = ((size_t)b * a.Hkv * a.N + n) * D + e0;  // KV head 0 in the tree's buffers
+  const int kv_step = a.N * D;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int task = task0 + i * kStep;
+    if (task >= rotated && task < heads)
+      *reinterpret_cast<uint4 *>(a.v_tree + kv_at + (size_t)(task - rotated) * kv_step) = raw[i];
+    if (__all_sync(0xffffffffu, task >= rotated)) return;
+    const bool is_k = task >= a.Hq;
+    auto unpack = [](uint4 v, float (&f)[8]) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = bf16_lo(w[j]);
+        f[2 * j + 1] = bf16_hi(w[j]);
+      }
+    };
+    float x[8], y[8];
+    unpack(raw[i], x);
+    float rstd = 1.f;
+    if (norm) {
+      float ss[kChains];
+#pragma unroll
+      for (int g = 0; g < kChains; ++g) {
+        ss[g] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kOld; ++e) ss[g] = fmaf(x[g * kOld + e], x[g * kOld + e], ss[g]);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int g = 0; g < kChains; ++g) ss[g] += __shfl_xor_sync(0xffffffffu, ss[g], o);
+#pragma unroll
+      for (int o = kChains / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int g = 0; g < o; ++g) ss[g] += ss[g + o];
+      rstd = rsqrtf(ss[0] * (1.0f / (float)D) + a.eps);
+      float w[8];
+      unpack(is_k ? wk : wq, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * w[e];
+    }
+    unsigned cancels = 0;
+    if (!a.interleaved) {
+      const float4 *cp = reinterpret_cast<const float4 *>(s_cos) + (hl & (kLanes / 2 - 1)) * 2;
+      const float4 *sp = reinterpret_cast<const float4 *>(s_sin) + (hl & (kLanes / 2 - 1)) * 2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 c4 = cp[h], s4 = sp[h];
+        const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = 4 * h + k;
+          const float other = __shfl_xor_sync(0xffffffffu, x[e], kLanes / 2);
+          y[e] = first ? (x[e] * cs[k] - other * sn[k]) : (other * sn[k] + x[e] * cs[k]);
+          if (is_k && rope_cancels(y[e], x[e], other)) cancels |= 1u << e;
+        }
+      }
+    } else {
+      const float4 c4 = reinterpret_cast<const float4 *>(s_cos)[hl];
+      const float4 s4 = reinterpret_cast<const float4 *>(s_sin)[hl];
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        y[e] = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
+        y[e + 1] = x[e] * sn[e / 2] + x[e + 1] * cs[e / 2];
+        if (is_k && rope_cancels(y[e], x[e], x[e + 1])) cancels |= 1u << e;
+        if (is_k && rope_cancels(y[e + 1], x[e], x[e + 1])) cancels |= 2u << e;
+      }
+    }
+    const uint4 out = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                 pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    if (task < a.Hq) {
+      *reinterpret_cast<uint4 *>(a.q_out + (row * a.Hq + task) * D + e0) = out;
+    } else if (task < rotated) {
+      __nv_bfloat16 *dst = a.k_tree + kv_at + (size_t)(task - a.Hq) * kv_step;
+      *reinterpret_cast<uint4 *>(dst) = out;
+      if (cancels != 0)
+        exact_elements(k_src - e0 + task * D, a.k_norm_w, dst - e0, turns.v, D / 2,
+                       a.interleaved, e0, p, rstd, cancels);
+    }
   }
 }
 
@@ -129,11 +228,29 @@ cudaError_t launch_tree_rope(const void *q_in, void *q_out, const void *k_new, c
   const TreeRopeArgs a{in(q_in), in(k_new), in(v_new), in(q_norm_w), in(k_norm_w),
                        io(q_out), io(k_tree), io(v_tree), pos, n_nodes, error_word,
                        N, Hq, Hkv, interleaved, eps};
-  const dim3 grid(B * N, (Hq + Hkv + kWarps - 1) / kWarps);
+  // Passes per warp: one while that leaves SMs without two CTAs, else as many as it takes (up
+  // to 4) to hold a node's heads in one CTA.
+  int sms = 152, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int heads = Hq + 2 * Hkv, per = kWarps * (256 / D);
+  int passes = 1;
+  while (passes < 4 && per * passes < heads &&
+         (long long)B * N * ((heads + per * passes - 1) / (per * passes)) > 2ll * sms)
+    ++passes;
+  const dim3 grid(N, (heads + per * passes - 1) / (per * passes), B);
   const RopeTurns turns = make_rope_turns(D, inv);
-  const cudaError_t e =
-      D == 128 ? launch_pdl(tree_rope_kernel<128>, grid, kThreads, 0, stream, a, inv, turns)
-               : launch_pdl(tree_rope_kernel<64>, grid, kThreads, 0, stream, a, inv, turns);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, kThreads, 0, stream, a, turns);
+  };
+  const cudaError_t e = D == 128 ? (passes == 1   ? go(tree_rope_kernel<128, 1>)
+                                    : passes == 2 ? go(tree_rope_kernel<128, 2>)
+                                    : passes == 3 ? go(tree_rope_kernel<128, 3>)
+                                                  : go(tree_rope_kernel<128, 4>))
+                                 : (passes == 1   ? go(tree_rope_kernel<64, 1>)
+                                    : passes == 2 ? go(tree_rope_kernel<64, 2>)
+                                    : passes == 3 ? go(tree_rope_kernel<64, 3>)
+                                                  : go(tree_rope_kernel<64, 4>));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

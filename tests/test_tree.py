@@ -467,23 +467,26 @@ def test_rope_tree_frequency_table_and_bad_positions():
     assert run_rope(c, "neox") == dsa.DEVERR_POS_SKIPPED
 
 
-def test_rope_tree_matches_the_single_token_append():
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+def test_rope_tree_matches_the_single_token_append(D, layout):
     """One node at a sequence's length: the bits the append writes into the cache."""
-    c = rope_case(2, 5, 1, 8, 2, 128, True, far=4096)
+    B, Hq, Hkv, T = 200, 9, 3, 512
+    c = rope_case(2, B, 1, Hq, Hkv, D, True, far=T)
     c["n_nodes"][:] = 1
     g = {k: v.to(DEV) for k, v in c.items()}
-    kt = torch.zeros(5, 2, 1, 128, dtype=torch.bfloat16, device=DEV)
+    kt = torch.zeros(B, Hkv, 1, D, dtype=torch.bfloat16, device=DEV)
     vt = torch.zeros_like(kt)
-    q = dsa.qknorm_rope_tree(g["q"].clone(), g["k_new"], g["v_new"], kt, vt, g["pos"], 1e6, "neox",
+    q = dsa.qknorm_rope_tree(g["q"].clone(), g["k_new"], g["v_new"], kt, vt, g["pos"], 1e6, layout,
                              g["q_norm_w"], g["k_norm_w"])
-    kc = torch.zeros(5, 2, 4096, 128, dtype=torch.bfloat16, device=DEV)
+    kc = torch.zeros(B, Hkv, T, D, dtype=torch.bfloat16, device=DEV)
     vc = torch.zeros_like(kc)
     p = g["pos"][:, 0].contiguous()
     q1 = dsa.qknorm_rope_kv_append(g["q"][:, 0].clone(), g["k_new"][:, 0].contiguous(),
-                                   g["v_new"][:, 0].contiguous(), kc, vc, p, 1e6, "neox",
+                                   g["v_new"][:, 0].contiguous(), kc, vc, p, 1e6, layout,
                                    g["q_norm_w"], g["k_norm_w"])
     assert torch.equal(q[:, 0], q1)
-    row = torch.arange(5, device=DEV)
+    row = torch.arange(B, device=DEV)
     assert torch.equal(kt[:, :, 0], kc[row, :, p.long()])
     assert torch.equal(vt[:, :, 0], vc[row, :, p.long()])
 

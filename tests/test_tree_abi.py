@@ -105,7 +105,9 @@ def test_token_logprobs_rejects(L):
 def test_python_refusals():
     bf = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        dsa.gqa_tree_attn(bf, bf, bf, None, bf, bf, None)
+        dsa.gqa_tree_attn(bf[0], bf, bf, None, bf, bf, None)
+    with pytest.raises(TypeError):
+        dsa.gqa_tree_attn(bf, bf, bf, None, bf, bf, None, workspace=bf, out=bf)
     with pytest.raises(ValueError):
         dsa.qknorm_rope_tree(bf, bf, bf, bf, bf, None, 1e4)
     with pytest.raises(ValueError):
