@@ -1197,7 +1197,8 @@ size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int m
   if (B < 0 || N < 1 || N > kTreeMaxNodes || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
       (D != 64 && D != 128) || max_len < 0 || num_parts < 0)
     return 0;
-  return tree_ws_bytes(D, tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));
+  return tree_ws_bytes(B, N, Hq, Hkv, D,
+                       tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));
 }
 
 dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_cache,
@@ -1237,7 +1238,7 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   const int parts = tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current());
   if (workspace == nullptr || misaligned({workspace}, 256))
     return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
-  const size_t need = tree_ws_bytes(D, parts);
+  const size_t need = tree_ws_bytes(B, N, Hq, Hkv, D, parts);
   if (ws_bytes < need)
     return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   st = where_all_here({{q, "q", true}, {k_cache, "k_cache", false}, {v_cache, "v_cache", false},

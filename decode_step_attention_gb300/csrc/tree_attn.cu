@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "dec_device.cuh"
 #include "dec_launch.h"
@@ -45,6 +46,7 @@ constexpr int kRows = 128;     // query rows per tile (the MMA's M)
 constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
 constexpr int kSoftmax = 128;
 constexpr float kRescale = 8.f;  // log2 of the growth of the maximum that moves it
+constexpr int kMaxRowTiles = kTreeMaxNodes * kSplitMaxG / kRows;
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = 2 * kTile;  // S/P buffers in columns [0, 128), O behind them
 
@@ -60,17 +62,17 @@ struct Geo {
 
 // Partial slots: piece c leaves at most two, its first segment (slot 2c, when that began in
 // an earlier piece) and its last (slot 2c + 1, when it goes on in a later one). A slot holds
-// O [D / 8][128 rows][8] fp32 and (maximum, sum) [128 rows]. Records, one per piece: the
-// (pair, row tile) whose first piece boundary is this piece's start, for the merge.
-struct Record {
-  int b, g, m, first, last;  // pieces first .. last; first < 0: nothing to merge here
-  int rows, pad0, pad1;
+// O [D / 8][128 rows][8] fp32 and (maximum, sum) [128 rows]. Records, one per (pair, row
+// tile), written by the CTA that begins it: the pieces it lies in.
+struct alignas(16) Record {
+  int first, last;  // the same: nothing to merge
+  int pad[2];
 };
 
 __host__ __device__ inline size_t slot_bytes(int D) { return (size_t)kRows * (D * 4 + 8); }
 __host__ __device__ inline size_t records_offset() { return kWsHeaderBytes; }
-__host__ __device__ inline size_t slots_offset(int parts) {
-  return (records_offset() + (size_t)parts * sizeof(Record) + 255) & ~(size_t)255;
+__host__ __device__ inline size_t slots_offset(int records) {
+  return (records_offset() + (size_t)records * sizeof(Record) + 255) & ~(size_t)255;
 }
 
 // A sequence's share of the stream.
@@ -94,37 +96,39 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int b, bool report)
   return s;
 }
 
-// The segments of a piece: runs of key tiles [t0, t1) of one (sequence, KV head, row tile).
+// The segments of a piece: runs of key tiles [t0, t1) of one (sequence, KV head) and row tile
+// m. All pieces of a row tile m come one after the other, ordered by (sequence, KV head, key
+// tile): the CTAs of different row tiles then walk the same keys at the same time and share
+// them through L2.
 struct Walk {
   Seq s;
   int b, g, m, t0, t1, left;
-  __device__ __forceinline__ void begin(const TreeAttnArgs &a, int b_, int within, int units) {
+  __device__ __forceinline__ void begin(const TreeAttnArgs &a, int b_, int within, int units,
+                                        int m_) {
     b = b_;
+    m = m_;
     s = seq_of(a, b, false);
-    const int per_head = s.tiles * s.mt;
-    g = within / per_head;
-    const int r = within - g * per_head;
-    m = r / s.tiles;
-    t0 = r - m * s.tiles;
+    g = within / s.tiles;
+    t0 = within - g * s.tiles;
     left = units;
     t1 = min(s.tiles, t0 + left);
   }
   __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
     left -= t1 - t0;
     if (left <= 0) return false;
-    if (++m == s.mt) {
-      m = 0;
-      if (++g == a.Hkv) {
-        g = 0;
-        do s = seq_of(a, ++b, false);
-        while (s.live == 0);
-      }
+    if (++g == a.Hkv) {
+      g = 0;
+      do s = seq_of(a, ++b, false);
+      while (s.mt <= m);
     }
     t0 = 0;
     t1 = min(s.tiles, left);
     return true;
   }
+  // rows of this row tile, and the lanes that share a row (see the kernel)
+  __device__ __forceinline__ int rows(int G) const { return min(kRows, s.live * G - m * kRows); }
 };
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -135,6 +139,26 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations per instruction (the packed forms of this architecture).
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // ---- tensor memory ---------------------------------------------------------------------
@@ -161,6 +185,57 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_raw(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+// NC fp32 columns of this thread's lane; NC / 2 packed ones back, zeros over the other
+// slices' part of the 32 packed columns.
+template <int NC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t *r) {
+  if constexpr (NC == 64) {
+    tmem_ld32(addr, r);
+    tmem_ld32(addr + 32, r + 32);
+  } else if constexpr (NC == 32) {
+    tmem_ld32(addr, r);
+  } else {
+    tmem_ld16_raw(addr, r);
+  }
+}
+template <int NC>
+__device__ __forceinline__ void tmem_st_weights(uint32_t addr, int slice, const uint32_t *pk) {
+  if constexpr (NC == 64) {
+    tmem_st32(addr, pk);
+  } else if constexpr (NC == 32) {
+    const uint32_t z[16] = {};
+    tmem_st16(addr + (slice ^ 1) * 16, z);
+    tmem_st16(addr + slice * 16, pk);
+  } else {
+    const uint32_t z[8] = {};
+#pragma unroll
+    for (int s = 1; s < 4; ++s) tmem_st8(addr + ((slice + s) & 3) * 8, z);
+    tmem_st8(addr + slice * 8, pk);
+  }
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
@@ -208,9 +283,9 @@ __device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
 }
 
 // A store of 8 consecutive floats.
-__device__ __forceinline__ void st_v8(float *p, const uint32_t *r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void st_v8(float *p, const float *r) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(r[0]),
+               "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
                : "memory");
 }
 
@@ -236,21 +311,22 @@ struct Waiter {
 template <int D, bool kMod>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_kernel(const __grid_constant__ TreeMaps maps, const TreeAttnArgs a, int B,
-                     uint8_t *workspace) {
+                     int mts, uint8_t *workspace) {
   using G = Geo<D>;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_bar[2 * S + 8];
+  __shared__ uint64_t s_bar[2 * S + 9];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_sum[kThreads / 32], s_begin[2];
+  __shared__ int s_sum[kThreads / 32][kMaxRowTiles], s_begin[2];
+  __shared__ float2 s_ml[kSoftmax];
   __shared__ unsigned long long s_odd[2];  // tree values that are not finite, by node
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_s = smem_addr(smem), ring = q_s + G::kQ;
   const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
   const uint32_t bar_s = bar_empty + 8 * S, bar_p = bar_s + 16, bar_pv = bar_p + 16;
-  const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8;
+  const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8, bar_x = bar_end + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = gridDim.x, piece = blockIdx.x;
 
@@ -264,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(bar_pv + 8, 1);
     mbar_init(bar_q, kSoftmax);
     mbar_init(bar_end, 1);
+    mbar_init(bar_x, kSoftmax);
     s_abort = 0;
     s_odd[0] = s_odd[1] = 0;
     fence_barrier_init();
@@ -274,75 +351,94 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&maps.kt);
     tma_prefetch_desc(&maps.vt);
   }
+  if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   pdl_launch_dependents();
-  pdl_wait_prior_grid();
 
-  // ---- where this CTA's piece begins: a scan over the sequences' unit counts
+  // No kernel that may still run when this one starts writes lengths, node counts, masks or
+  // positions (only this library's kernels let a successor start early), so the piece is found
+  // before the wait for it.
+  // ---- where this CTA's piece begins: the units of every row tile m, the CTAs each m gets in
+  // proportion, and a scan over the sequences for this CTA's m
   const int per = (B + kThreads - 1) / kThreads;
-  int mine = 0;
+  int mine[kMaxRowTiles] = {};
   for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
     const Seq s = seq_of(a, b, piece == 0);
-    mine += s.tiles * s.mt * a.Hkv;
+#pragma unroll
+    for (int m = 0; m < kMaxRowTiles; ++m)
+      if (m < s.mt) mine[m] += s.tiles * a.Hkv;
   }
-  int incl = mine;
+#pragma unroll
+  for (int m = 0; m < kMaxRowTiles; ++m) {
+    const int v = __reduce_add_sync(0xffffffffu, mine[m]);
+    if (lane == 0) s_sum[warp][m] = v;
+  }
+  __syncthreads();
+  int m_total[kMaxRowTiles] = {}, m_before[kMaxRowTiles] = {};
+  long long all = 0;
+#pragma unroll
+  for (int m = 0; m < kMaxRowTiles; ++m) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) m_before[m] += s_sum[w][m];
+      m_total[m] += s_sum[w][m];
+    }
+    all += m_total[m];
+  }
+  int my_m = -1, p0 = 0, total = 0, pieces = 1, before = 0, count = 0;
+  {
+    int at = 0;
+#pragma unroll
+    for (int m = 0; m < kMaxRowTiles; ++m)
+      if (m < mts) {
+        const int n = 1 + (all > 0 ? (int)((long long)(P - mts) * m_total[m] / all) : 0);
+        if (piece >= at && piece < at + n) {
+          my_m = m;
+          p0 = at;
+          pieces = n;
+          total = m_total[m];
+          before = m_before[m];
+          count = mine[m];
+        }
+        at += n;
+      }
+  }
+  const int blk = max(1, (total + pieces - 1) / pieces);
+  const int r0 = (int)min((long long)total, (long long)(piece - p0) * blk);
+  const int units = min(blk, total - r0);
+  const bool idle = my_m < 0 || units <= 0;  // past the end of the stream
+  int incl = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  const int blk = max(1, (total + P - 1) / P);
-  const long long r0l = (long long)piece * blk;
-  const int r0 = (int)min((long long)total, r0l);
-  const int units = min(blk, total - r0);
-  Record *rec = reinterpret_cast<Record *>(workspace + records_offset()) + piece;
-  if (units <= 0) {  // past the end of the stream: nothing to do, nothing to merge
-    if (tid == 0) rec->first = -1;
-    return;
-  }
-  const int excl = before + incl - mine;
-  if (excl <= r0 && r0 < excl + mine) {
+  const int excl = before + incl - count;
+  if (!idle && excl <= r0 && r0 < excl + count) {
     int at = excl, b = tid * per;
     for (;; ++b) {
       const Seq s = seq_of(a, b, false);
-      const int u = s.tiles * s.mt * a.Hkv;
+      const int u = my_m < s.mt ? s.tiles * a.Hkv : 0;
       if (r0 < at + u) break;
       at += u;
     }
     s_begin[0] = b;
     s_begin[1] = r0 - at;
   }
-  if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  if (idle) {
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+    pdl_wait_prior_grid();  // a grid is not done before the one it follows
+    return;
+  }
   const int Gq = a.Hq / a.Hkv;
+  const int records = B * a.Hkv * mts;
   const Waiter wait{&s_abort, a.error_word};
   Walk w;
-  w.begin(a, s_begin[0], s_begin[1], units);
-  if (tid == 0) {
-    // does a (pair, row tile) meet its first piece boundary at this piece's start?
-    Record r{};
-    r.first = -1;
-    const int off = r0 - w.t0;  // its first unit
-    if (w.t0 > 0 && off / blk == piece - 1) {
-      r.b = w.b;
-      r.g = w.g;
-      r.m = w.m;
-      r.first = piece - 1;
-      r.last = (off + w.s.tiles - 1) / blk;
-      r.rows = min(kRows, w.s.live * Gq - w.m * kRows);
-    }
-    *rec = r;
-  }
+  w.begin(a, s_begin[0], s_begin[1], units, my_m);
+  pdl_wait_prior_grid();
 
   if (warp == 4) {
     // ---------------------------------------------------------------- loads
@@ -430,19 +526,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t my_tmem = tmem + ((uint32_t)(32 * warp) << 16);
     const float log2e = 1.4426950408889634f;
     const float sc = kMod ? 1.f : a.scale * log2e;
-    int n = 0, seg = 0;
+    int n = 0, seg = 0, x_phase = 0, done_units = 0;
     bool ok = true;
     // the same answer in every lane, and the warp together behind it
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wait(bar, parity) ? 1 : 0) != 0;
     };
+    auto q_row = [&](const Walk &v, int row) {
+      const int node = row / Gq;
+      return a.q + (((size_t)v.b * a.N + node) * a.Hq + (size_t)v.g * Gq + (row - node * Gq)) * D;
+    };
     // this thread's row of Q into shared memory, K-major with the 128-byte swizzle
     auto load_q = [&](const Walk &v) {
-      const int row = v.m * kRows + tid, node = row / Gq;
+      const int row = v.m * kRows + (tid & (kRows / copies_of(v.rows(Gq)) - 1)), node = row / Gq;
       const bool real = node < v.s.live;
-      const size_t at =
-          (((size_t)v.b * a.N + node) * a.Hq + (size_t)v.g * Gq + (row - node * Gq)) * D;
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at);
+      const uint4 *src = reinterpret_cast<const uint4 *>(q_row(v, row));
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint4 x[8];
@@ -461,26 +559,58 @@ __global__ void __launch_bounds__(kThreads, 2)
     load_q(w);
     bool more = true;
     while (more) {
-      const int row = w.m * kRows + tid, node = row / Gq, hi = row - node * Gq;
-      const int rows = min(kRows, w.s.live * Gq - w.m * kRows);
-      const bool real = tid < rows, active = 32 * warp < rows;
+      const int rows = w.rows(Gq), copies = copies_of(rows);
+      const int my_row = tid & (kRows / copies - 1);      // within the row tile
+      const int slice = tid / (kRows / copies);
+      const int row = w.m * kRows + my_row, node = row / Gq, hi = row - node * Gq;
+      const bool real = my_row < rows, active = copies > 1 || 32 * warp < rows;
       const size_t brow = (size_t)w.b * a.N;
+      const bool has_tree = w.t1 == w.s.tiles;
+      // what the tree's tile needs, on its way early: this row's ancestors, the nodes that any
+      // row sees, and two nodes' positions per lane
+      const uint64_t my_mask =
+          has_tree && real ? a.mask[brow + node] & bit_range(0, w.s.live) : 0;
+      uint64_t used = 0;
+      int npos[2] = {};
+      if (has_tree) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (lane + 32 * h < w.s.live) {
+            used |= a.mask[brow + lane + 32 * h];
+            if (a.pos != nullptr) npos[h] = max(a.pos[brow + lane + 32 * h], w.s.L);
+          }
+        used = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(used >> 32)) << 32 |
+               __reduce_or_sync(0xffffffffu, (uint32_t)used);
+      }
       const int qpos = real && a.pos != nullptr ? max(a.pos[brow + node], w.s.L) : 0;
       const int low = real && a.window > 0 ? qpos - a.window + 1 : 0;  // first slot in the window
       float slope = 0.f;
       if constexpr (kMod)
         if (real && a.slopes != nullptr) slope = a.slopes[w.g * Gq + hi] * log2e;
       float m = -INFINITY, l = 0.f;
+      // the segment after this one, and its Q on the way into L2
+      Walk after = w;
+      more = after.next(a);
+      if (more) {
+        const int r = after.m * kRows + (tid & (kRows / copies_of(after.rows(Gq)) - 1));
+        if (r / Gq < after.s.live) {
+          const __nv_bfloat16 *src = q_row(after, r);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+        }
+      }
       for (int t = w.t0; t < w.t1; ++t, ++n) {
         const bool tree = t == w.s.tiles - 1;
         const int t_abs = w.s.start + t * kTile;
         const uint32_t p_addr = my_tmem + (n & 1) * kTile;
         uint64_t see;
         if (tree) {
-          see = real ? a.mask[brow + node] & bit_range(0, w.s.live) : 0;
+          see = my_mask;
           if (a.window > 0)
-            for (int j = 0; j < w.s.live; ++j)
-              if (qpos - max(a.pos[brow + j], w.s.L) >= a.window) see &= ~(1ull << j);
+            for (int j = 0; j < w.s.live; ++j) {
+              const int at = __shfl_sync(0xffffffffu, j < 32 ? npos[0] : npos[1], j & 31);
+              if (qpos - at >= a.window) see &= ~(1ull << j);
+            }
         } else {
           see = real ? bit_range(low - t_abs, w.s.L - t_abs) : 0;
         }
@@ -491,48 +621,57 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         // every thread has left the segment before this one, whose marks are now free
         if (t == w.t0 && tid == 0) s_odd[(seg + 1) & 1] = 0;
-        if (active) {
-          uint32_t raw[kTile];
-          tmem_ld32(p_addr, raw);
-          tmem_ld32(p_addr + 32, raw + 32);
+        auto weights = [&](auto cols) {
+          constexpr int NC = decltype(cols)::value;
+          const int c0 = slice * NC;  // this thread's keys of the tile: [c0, c0 + NC)
+          uint32_t raw[NC];
+          tmem_ld_cols<NC>(p_addr + c0, raw);
           tmem_wait_ld();
-          float z[kTile];
+          float z[NC];
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) z[c] = __uint_as_float(raw[c]);
+          for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
           if constexpr (kMod) {
             if (a.softcap > 0.f) {
               // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
               const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
 #pragma unroll
-              for (int c = 0; c < kTile; ++c)
+              for (int c = 0; c < NC; ++c)
                 z[c] = fmaf(-2.f * cap, rcp(1.f + ex2(z[c] * in)), cap);
             } else {
 #pragma unroll
-              for (int c = 0; c < kTile; ++c) z[c] *= a.scale * log2e;
+              for (int c = 0; c < NC; ++c) z[c] *= a.scale * log2e;
             }
             if (a.slopes != nullptr) {
               if (!tree) {
+                const float far = (float)(qpos - t_abs - c0);
 #pragma unroll
-                for (int c = 0; c < kTile; ++c)
-                  z[c] = fmaf(-slope, (float)(qpos - t_abs - c), z[c]);
+                for (int c = 0; c < NC; ++c) z[c] = fmaf(-slope, far - (float)c, z[c]);
               } else {
 #pragma unroll
-                for (int c = 0; c < kTile; ++c)
-                  if (c < w.s.live)
-                    z[c] = fmaf(-slope, (float)(qpos - max(a.pos[brow + c], w.s.L)), z[c]);
+                for (int c = 0; c < NC; ++c)
+                {
+                  const int j = c0 + c;  // the same in every lane of the warp
+                  const int at = __shfl_sync(0xffffffffu, j < 32 ? npos[0] : npos[1], j & 31);
+                  if (j < w.s.live) z[c] = fmaf(-slope, (float)(qpos - at), z[c]);
+                }
               }
             }
           }
-          if (!__all_sync(0xffffffffu, see == ~0ull)) {
-            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+          const uint64_t mine = (see >> c0) & (~0ull >> (64 - NC));
+          if (!__all_sync(0xffffffffu, mine == ~0ull >> (64 - NC))) {
+            const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
+            for (int c = 0; c < NC; ++c)
               if (!(((c < 32 ? s0 : s1) >> (c & 31)) & 1u)) z[c] = -INFINITY;
           }
-          float mx = z[0];
+          float m4[4] = {z[0], z[1], z[2], z[3]};  // four chains, for the latency
 #pragma unroll
-          for (int c = 1; c < kTile; ++c) mx = fmaxf(mx, z[c]);
-          mx *= sc;
+          for (int c = 4; c < NC; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
+                                        : fmaxf(m4[i], z[c + i]);
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
           const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : m;
@@ -554,18 +693,29 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          uint32_t pk[kTile / 2];
-          float l0 = 0.f, l1 = 0.f;
+          uint32_t pk[NC / 2];
+          const uint64_t sc2 = pair_of(sc, sc), base2 = pair_of(-base, -base);
+          uint64_t l4[4] = {};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 2) {
-            const float p0 = ex2(fmaf(z[c], sc, -base)), p1 = ex2(fmaf(z[c + 1], sc, -base));
-            l0 += p0;
-            l1 += p1;
+          for (int c = 0; c < NC; c += 2) {
+            float x0, x1;
+            unpair(fma2(pair_of(z[c], z[c + 1]), sc2, base2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            l4[(c / 2) & 3] = add2(l4[(c / 2) & 3], pair_of(p0, p1));
             pk[c / 2] = pack_bf16x2(p0, p1);
           }
+          float l0, l1;
+          unpair(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), l0, l1);
           l += l0 + l1;
-          tmem_st32(p_addr, pk);
+          tmem_st_weights<NC>(p_addr, slice, pk);
           tmem_wait_st();
+        };
+        if (copies == 4) {
+          weights(std::integral_constant<int, 16>{});
+        } else if (copies == 2) {
+          weights(std::integral_constant<int, 32>{});
+        } else if (active) {
+          weights(std::integral_constant<int, 64>{});
         }
         // rows of V that nobody may read can hold anything, and 0 times NaN is NaN: they
         // are cleared in shared memory. In the tree's tile so are values that are not finite
@@ -579,11 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           const int r = tid >> 1;
           bool clear = r >= valid;
-          if (tree && !clear) {
-            uint64_t used = 0;
-            for (int j = 0; j < w.s.live; ++j) used |= a.mask[brow + j];
-            clear = !((used >> r) & 1);
-          }
+          if (tree) clear = !((used >> r) & 1);
           bool odd = false;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {  // half a row per thread
@@ -621,73 +767,170 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) break;
       // ---- the segment's end
       const Walk done = w;
+      w = after;
       uint64_t odd = 0;
       if (done.t1 == done.s.tiles) {
         // every thread's mark is visible once the tile's last arrival is
         if (!wait_all(bar_p + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
         odd = *reinterpret_cast<volatile unsigned long long *>(&s_odd[seg & 1]);
       }
-      more = w.next(a);
       // every S of this segment has been read, so Q's space is free; P of the last tile must
       // stay for the values to be given back
-      if (more && odd == 0) load_q(w);
+      const bool early_q = more && odd == 0 && copies == 1;
+      if (early_q) load_q(w);
       if (!wait_all(bar_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
-      if (active) {
-        const bool whole = done.t0 == 0 && done.t1 == done.s.tiles;
-        const float scale = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const int slot = 2 * piece + (done.t0 > 0 ? 0 : 1);
-        float *part = reinterpret_cast<float *>(workspace + slots_offset(P) +
-                                                (size_t)slot * slot_bytes(D));
-        __nv_bfloat16 *dst =
-            a.out + ((brow + node) * a.Hq + (size_t)done.g * Gq + hi) * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(my_tmem + kOCol + c, o);
-          tmem_wait_ld();
-          for (uint64_t left = odd; left != 0; left &= left - 1) {
-            const int j = __ffsll((long long)left) - 1;
-            const uint32_t pw = tmem_ld1(my_tmem + ((n - 1) & 1) * kTile + (j >> 1));
-            const float p = (j & 1) ? bf16_hi(pw) : bf16_lo(pw);
-            const bool sees = real && ((a.mask[brow + node] >> j) & 1) &&
-                              !(a.window > 0 &&
-                                qpos - max(a.pos[brow + j], done.s.L) >= a.window);
-            const __nv_bfloat16 *v =
-                a.v_tree + (((size_t)done.b * a.Hkv + done.g) * a.N + j) * D + c;
-            if (sees)
-              for (int i = 0; i < 32; ++i) {
-                const float x = __bfloat162float(v[i]);
-                if (!isfinite(x)) {
+      const bool whole = done.t0 == 0 && done.t1 == done.s.tiles;
+      const int slot = 2 * piece + (done.t0 > 0 ? 0 : 1);
+      float *part =
+          reinterpret_cast<float *>(workspace + slots_offset(records) + (size_t)slot * slot_bytes(D));
+      __nv_bfloat16 *dst = a.out + ((brow + node) * a.Hq + (size_t)done.g * Gq + hi) * D;
+      // the values of nodes that are not finite, to the rows that see them
+      auto give_back = [&](uint32_t (&o)[32], int c) {
+        for (uint64_t left = odd; left != 0; left &= left - 1) {
+          const int j = __ffsll((long long)left) - 1;
+          const uint32_t pw = tmem_ld1(my_tmem + ((n - 1) & 1) * kTile + (j >> 1));
+          const float p = (j & 1) ? bf16_hi(pw) : bf16_lo(pw);
+          const bool sees = real && j / (kTile / copies) == slice && ((my_mask >> j) & 1) &&
+                            !(a.window > 0 && qpos - max(a.pos[brow + j], done.s.L) >= a.window);
+          const __nv_bfloat16 *v =
+              a.v_tree + (((size_t)done.b * a.Hkv + done.g) * a.N + j) * D + c;
+          if (sees)
+            for (int i = 0; i < 32; ++i) {
+              const float x = __bfloat162float(v[i]);
+              if (!isfinite(x)) {
 #pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    if (k == i) o[k] = __float_as_uint(__uint_as_float(o[k]) + p * x);
-                }
+                for (int k = 0; k < 32; ++k)
+                  if (k == i) o[k] = __float_as_uint(__uint_as_float(o[k]) + p * x);
               }
-            __syncwarp();
-          }
-          if (real && whole) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[k] = pack_bf16x2(__uint_as_float(o[i + 2 * k]) * scale,
-                                   __uint_as_float(o[i + 2 * k + 1]) * scale);
-              *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(x[0], x[1], x[2], x[3]);
             }
-          } else if (real) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              st_v8(part + ((size_t)((c + i) / 8) * kRows + tid) * 8, o + i);
-          }
           __syncwarp();
         }
-        if (!whole && real)
-          reinterpret_cast<float2 *>(part + (size_t)kRows * D)[tid] = make_float2(m, l);
+      };
+      auto store8 = [&](int col, const float *v) {  // 8 columns of this thread's row
+        if (whole) {
+          *reinterpret_cast<uint4 *>(dst + col) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        } else {
+          st_v8(part + ((size_t)(col / 8) * kRows + my_row) * 8, v);
+        }
+      };
+      if (copies == 1) {
+        if (active) {
+          const float scale = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(my_tmem + kOCol + c, o);
+            tmem_wait_ld();
+            if (odd != 0) give_back(o, c);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * scale;
+            if (real) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) store8(c + i, v + i);
+            }
+            __syncwarp();
+          }
+          if (!whole && real)
+            reinterpret_cast<float2 *>(part + (size_t)kRows * D)[my_row] = make_float2(m, l);
+        }
+      } else {
+        // A row's keys were dealt to `copies` lanes, each with a maximum, sum and O of its
+        // own: joined through Q's space (every S of the segment has been read), 32 columns
+        // at a time, a lane taking 32 / copies of them.
+        auto meet = [&] {
+          mbar_arrive(bar_x);
+          const bool here = wait_all(bar_x, x_phase & 1);
+          ++x_phase;
+          return here;
+        };
+        const int span = kRows / copies;
+        constexpr int kCols = G::kQ / (kSoftmax * 4) < 64 ? G::kQ / (kSoftmax * 4) : 64;
+        float weight[4] = {}, M = -INFINITY, L = 0.f;
+        s_ml[tid] = make_float2(m, l);
+        bool joined = true;
+#pragma unroll 1
+        for (int c = 0; c < D; c += kCols) {
+          if (c > 0) joined = joined && meet();  // the space is free again
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) {
+            uint32_t o[32];
+            tmem_ld32(my_tmem + kOCol + c + h, o);
+            tmem_wait_ld();
+            if (odd != 0) give_back(o, c + h);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               q_s + (uint32_t)((h + i) / 4 * kSoftmax + tid) * 16),
+                           "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3])
+                           : "memory");
+          }
+          joined = joined && meet();
+          if (!joined) break;
+          if (c == 0) {
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = k < copies ? s_ml[my_row + k * span] : make_float2(-INFINITY, 0.f);
+            M = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+            const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              weight[k] = ex2(x[k].x - base);
+              L += x[k].y * weight[k];
+            }
+            const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) weight[k] *= inv;
+          }
+          const int cols = kCols / copies;
+          for (int i = slice * cols; i < (slice + 1) * cols; i += 8) {
+            float4 x[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < copies)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(x[k][q].x), "=f"(x[k][q].y), "=f"(x[k][q].z),
+                                 "=f"(x[k][q].w)
+                               : "r"(q_s +
+                                     (uint32_t)((i / 4 + q) * kSoftmax + my_row + k * span) * 16)
+                               : "memory");
+            float v[8] = {};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < copies)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  v[4 * q] = fmaf(x[k][q].x, weight[k], v[4 * q]);
+                  v[4 * q + 1] = fmaf(x[k][q].y, weight[k], v[4 * q + 1]);
+                  v[4 * q + 2] = fmaf(x[k][q].z, weight[k], v[4 * q + 2]);
+                  v[4 * q + 3] = fmaf(x[k][q].w, weight[k], v[4 * q + 3]);
+                }
+            if (real) store8(c + i, v);
+          }
+        }
+        joined = joined && (!more || meet());
+        if (!joined) break;
+        if (!whole && real && slice == 0)
+          reinterpret_cast<float2 *>(part + (size_t)kRows * D)[my_row] = make_float2(M, L);
       }
+      if (done.t0 == 0 && tid == 0) {
+        const int off = r0 + done_units;  // the row tile's first unit
+        Record r;
+        r.first = piece;
+        r.last = p0 + (off + done.s.tiles - 1) / blk;
+        r.pad[0] = r.pad[1] = 0;
+        reinterpret_cast<Record *>(workspace +
+                                   records_offset())[((size_t)done.b * a.Hkv + done.g) * mts + my_m] = r;
+      }
+      done_units += done.t1 - done.t0;
       tc_fence_before();
-      if (more && odd != 0) load_q(w);
+      if (more && !early_q) load_q(w);
       ++seg;
     }
   }
@@ -700,23 +943,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the partials of the (pair, row tile)s that cross pieces: out = sum_c 2^(m_c - M) O_c /
-// sum_c 2^(m_c - M) l_c. CTA (c, y) takes 8 rows of the one whose first boundary is piece
-// c's start, a thread per (row, 8 dims, every kGroups-th piece).
-template <int D>
-__global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspace, int parts,
-                                                         TreeAttnArgs a) {
-  constexpr int kD8 = D / 8, kGroups = 512 / (8 * kD8);
-  __shared__ float s_o[kGroups][8][D + 4];
-  __shared__ float s_ml[kGroups][8][2];
+// sum_c 2^(m_c - M) l_c. CTA (x, y) takes kRowsPer rows of row tile x, a thread per (row, 8
+// dims, every kGroups-th piece): 8 rows where a few long row tiles are cut into many pieces,
+// 32 where many are cut in two.
+template <int D, int kRowsPer>
+__global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspace, int mts,
+                                                         int records, int parts,
+                                                         const TreeAttnArgs a) {
+  constexpr int kD8 = D / 8, kGroups = 512 / (kRowsPer * kD8);
+  static_assert(kGroups >= 1, "threads");
+  __shared__ float s_o[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kRowsPer : 1][D + 4];
+  __shared__ float s_ml[kGroups][kRowsPer][2];
   pdl_launch_dependents();
   pdl_wait_prior_grid();
+  const int m = blockIdx.x % mts, pair = blockIdx.x / mts, b = pair / a.Hkv, g = pair - b * a.Hkv;
+  const Seq s = seq_of(a, b, false);
+  if (m >= s.mt) return;  // no such row tile in this call, its record is an earlier one's
   const Record r = reinterpret_cast<const Record *>(workspace + records_offset())[blockIdx.x];
-  const int row0 = blockIdx.y * 8;
-  if (r.first < 0 || row0 >= r.rows) return;
-  const int rr = threadIdx.x & 7, d8 = (threadIdx.x >> 3) % kD8, grp = threadIdx.x / (8 * kD8);
-  const int row = row0 + rr;
-  const uint8_t *slots = workspace + slots_offset(parts);
+  const int row0 = blockIdx.y * kRowsPer;
+  const int rows = min(kRows, s.live * (a.Hq / a.Hkv) - m * kRows);
+  // (a record left by a launch that gave up is not trusted with addresses)
+  if (r.first < 0 || r.first >= r.last || r.last >= parts || row0 >= rows) return;
+  const int rr = threadIdx.x % kRowsPer, d8 = (threadIdx.x / kRowsPer) % kD8;
+  const int grp = threadIdx.x / (kRowsPer * kD8), row = row0 + rr;
+  const uint8_t *slots = workspace + slots_offset(records);
   float M = -INFINITY, l = 0.f, o[8] = {};
+#pragma unroll 4
   for (int c = r.first + grp; c <= r.last; c += kGroups) {
     const float *p = reinterpret_cast<const float *>(
         slots + (size_t)(2 * c + (c == r.first ? 1 : 0)) * slot_bytes(D));
@@ -731,34 +983,41 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspac
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * e;
   }
+  if constexpr (kGroups > 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_o[grp][rr][d8 * 8 + i] = o[i];
-  if (d8 == 0) {
-    s_ml[grp][rr][0] = M;
-    s_ml[grp][rr][1] = l;
+    for (int i = 0; i < 8; ++i) s_o[grp][rr][d8 * 8 + i] = o[i];
+    if (d8 == 0) {
+      s_ml[grp][rr][0] = M;
+      s_ml[grp][rr][1] = l;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) M = fmaxf(M, s_ml[k][rr][0]);
+    const float base = M == -INFINITY ? 0.f : M;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float e = ex2(s_ml[k][rr][0] - base);
+      l += s_ml[k][rr][1] * e;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += s_o[k][rr][d8 * 8 + i] * e;
+    }
   }
-  __syncthreads();
-  if (grp != 0 || row >= r.rows) return;
-  float Mx = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kGroups; ++k) Mx = fmaxf(Mx, s_ml[k][rr][0]);
-  const float base = Mx == -INFINITY ? 0.f : Mx;
-  float lt = 0.f, t[8] = {};
-#pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const float e = ex2(s_ml[k][rr][0] - base);
-    lt += s_ml[k][rr][1] * e;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] += s_o[k][rr][d8 * 8 + i] * e;
-  }
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  const int Gq = a.Hq / a.Hkv, q = r.m * kRows + row, node = q / Gq;
+  if (row >= rows) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int Gq = a.Hq / a.Hkv, q = m * kRows + row, node = q / Gq;
   __nv_bfloat16 *dst =
-      a.out + (((size_t)r.b * a.N + node) * a.Hq + (size_t)r.g * Gq + (q - node * Gq)) * D + d8 * 8;
+      a.out + (((size_t)b * a.N + node) * a.Hq + (size_t)g * Gq + (q - node * Gq)) * D + d8 * 8;
   *reinterpret_cast<uint4 *>(dst) =
-      make_uint4(pack_bf16x2(t[0] * inv, t[1] * inv), pack_bf16x2(t[2] * inv, t[3] * inv),
-                 pack_bf16x2(t[4] * inv, t[5] * inv), pack_bf16x2(t[6] * inv, t[7] * inv));
+      make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                 pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
 }
+
+inline int row_tiles(int N, int G) { return (N * G + kRows - 1) / kRows; }
 
 template <int D, bool kMod>
 cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts,
@@ -774,27 +1033,32 @@ cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts
     if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
   }
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.error_word);
+  const int mts = row_tiles(a.N, a.Hq / a.Hkv), records = B * a.Hkv * mts;
   e = launch_pdl(tree_attn_kernel<D, kMod>, dim3(parts), kThreads, Geo<D>::kSmem, stream, maps, a,
-                 B, ws);
+                 B, mts, ws);
   if (e != cudaSuccess || parts == 1) return e;
   const int rows = a.N * (a.Hq / a.Hkv) < kRows ? a.N * (a.Hq / a.Hkv) : kRows;
-  return launch_pdl(tree_merge_kernel<D>, dim3(parts, (rows + 7) / 8), 512, 0, stream,
-                    (const uint8_t *)ws, parts, a);
+  if (parts >= 8 * records)
+    return launch_pdl(tree_merge_kernel<D, 8>, dim3(records, (rows + 7) / 8), 512, 0, stream,
+                      (const uint8_t *)ws, mts, records, parts, a);
+  return launch_pdl(tree_merge_kernel<D, 32>, dim3(records, (rows + 31) / 32), 512, 0, stream,
+                    (const uint8_t *)ws, mts, records, parts, a);
 }
 
 }  // namespace
 
-// Two CTAs per SM, or fewer when the stream is shorter than that many key tiles.
+// Two CTAs per SM, or fewer when the stream is shorter than that many key tiles; at least
+// one for every row tile.
 int tree_parts(int B, int N, int Hq, int Hkv, int max_len, int num_parts, int sms) {
-  if (num_parts > 0) return num_parts;
-  const long long mt = ((long long)N * (Hq / Hkv) + kRows - 1) / kRows;
+  const int mt = row_tiles(N, Hq / Hkv);
+  if (num_parts > 0) return num_parts < mt ? mt : num_parts;
   const long long units = (long long)B * Hkv * mt * ((max_len + kTile - 1) / kTile + 1);
-  const long long most = units < 1 ? 1 : units;
-  return (int)(most < 2 * sms ? most : 2 * sms);
+  const long long most = units < mt ? mt : units;
+  return (int)(most < 2 * sms ? most : 2 * sms < mt ? mt : 2 * sms);
 }
 
-size_t tree_ws_bytes(int D, int parts) {
-  return slots_offset(parts) + (size_t)2 * parts * slot_bytes(D);
+size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int D, int parts) {
+  return slots_offset(B * Hkv * row_tiles(N, Hq / Hkv)) + (size_t)2 * parts * slot_bytes(D);
 }
 
 cudaError_t launch_tree_attn(const CUtensorMap *maps, const TreeAttnArgs &a, int B, int D,
