@@ -1213,7 +1213,7 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   if ((st = check_attn_shape(B, Hq, Hkv, D, T_cap, max_len)) != DEC_OK) return st;
   if (num_parts < 0) return fail(DEC_ERR_INVALID_ARG, "num_parts = %d < 0", num_parts);
   // the stream's units (pair, 128 rows, 64 keys) are counted in 32 bits
-  if ((long long)B * Hkv * ((N * (Hq / Hkv) + 127) / 128) * (T_cap / 64 + 2) >= (1ll << 31))
+  if ((long long)B * Hkv * ((N * (Hq / Hkv) + 127) / 128) * (T_cap / 64 + 8) >= (1ll << 31))
     return fail(DEC_ERR_UNSUPPORTED, "B * Hkv * N * T_cap too large");
   if (num_parts > kTreeMaxParts)
     return fail(DEC_ERR_UNSUPPORTED, "num_parts = %d > %d", num_parts, kTreeMaxParts);

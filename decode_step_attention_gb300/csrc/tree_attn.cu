@@ -47,6 +47,9 @@ constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
 constexpr int kSoftmax = 128;
 constexpr float kRescale = 8.f;  // log2 of the growth of the maximum that moves it
 constexpr int kMaxRowTiles = kTreeMaxNodes * kSplitMaxG / kRows;
+// What beginning and ending a (pair, row tile) costs, in key tiles: the stream is cut by tiles
+// plus this, so that CTAs with many short sequences finish with the others.
+constexpr int kSegment = 6;
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = 2 * kTile;  // S/P buffers in columns [0, 128), O behind them
 
@@ -97,37 +100,45 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int b, bool report)
 }
 
 // The segments of a piece: runs of key tiles [t0, t1) of one (sequence, KV head) and row tile
-// m. All pieces of a row tile m come one after the other, ordered by (sequence, KV head, key
-// tile): the CTAs of different row tiles then walk the same keys at the same time and share
-// them through L2.
+// m. The stream of row tile m has kSegment + tiles units per (sequence, KV head), in order; the
+// first kSegment stand for work that is not a tile. All pieces of a row tile come one after
+// the other: the CTAs of different row tiles then walk the same keys at the same time and
+// share them through L2.
 struct Walk {
   Seq s;
-  int b, g, m, t0, t1, left;
+  int b, g, m, t0, t1, left, off;  // off: first unit of this (sequence, KV head)
+  __device__ __forceinline__ void take(int from) {  // from: units of this pair already behind
+    t0 = max(0, from - kSegment);
+    t1 = max(t0, min(s.tiles, from + left - kSegment));
+    left -= t1 + kSegment - from;
+  }
+  // the piece of `units` from unit r0 on, `within` units into sequence b_; empty when t0 = t1
   __device__ __forceinline__ void begin(const TreeAttnArgs &a, int b_, int within, int units,
-                                        int m_) {
+                                        int m_, int r0) {
     b = b_;
     m = m_;
     s = seq_of(a, b, false);
-    g = within / s.tiles;
-    t0 = within - g * s.tiles;
+    const int per = s.tiles + kSegment;
+    g = within / per;
+    const int from = within - g * per;
+    off = r0 - from;
     left = units;
-    t1 = min(s.tiles, t0 + left);
+    take(from);
   }
   __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
+    if (left <= kSegment) return false;
+    off += s.tiles + kSegment;
     if (++g == a.Hkv) {
       g = 0;
       do s = seq_of(a, ++b, false);
       while (s.mt <= m);
     }
-    t0 = 0;
-    t1 = min(s.tiles, left);
+    take(0);
     return true;
   }
-  // rows of this row tile, and the lanes that share a row (see the kernel)
   __device__ __forceinline__ int rows(int G) const { return min(kRows, s.live * G - m * kRows); }
 };
+// Lanes that share a row of the tile (see the kernel).
 __device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -315,18 +326,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   using G = Geo<D>;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_bar[2 * S + 9];
+  __shared__ uint64_t s_bar[2 * S + 10];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_sum[kThreads / 32][kMaxRowTiles], s_begin[2];
   __shared__ float2 s_ml[kSoftmax];
-  __shared__ unsigned long long s_odd[2];  // tree values that are not finite, by node
+  __shared__ unsigned long long s_odd;  // nodes with values that are not finite
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_s = smem_addr(smem), ring = q_s + G::kQ;
   const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
   const uint32_t bar_s = bar_empty + 8 * S, bar_p = bar_s + 16, bar_pv = bar_p + 16;
-  const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8, bar_x = bar_end + 8;
+  const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8, bar_x = bar_end + 8, bar_v = bar_x + 8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = gridDim.x, piece = blockIdx.x;
 
@@ -341,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(bar_q, kSoftmax);
     mbar_init(bar_end, 1);
     mbar_init(bar_x, kSoftmax);
+    mbar_init(bar_v, 1);
     s_abort = 0;
-    s_odd[0] = s_odd[1] = 0;
     fence_barrier_init();
   }
   if (warp == 4 && lane == 0) {
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const Seq s = seq_of(a, b, piece == 0);
 #pragma unroll
     for (int m = 0; m < kMaxRowTiles; ++m)
-      if (m < s.mt) mine[m] += s.tiles * a.Hkv;
+      if (m < s.mt) mine[m] += (s.tiles + kSegment) * a.Hkv;
   }
 #pragma unroll
   for (int m = 0; m < kMaxRowTiles; ++m) {
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int blk = max(1, (total + pieces - 1) / pieces);
   const int r0 = (int)min((long long)total, (long long)(piece - p0) * blk);
   const int units = min(blk, total - r0);
-  const bool idle = my_m < 0 || units <= 0;  // past the end of the stream
+  bool idle = my_m < 0 || units <= 0;  // past the end of the stream
   int incl = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int at = excl, b = tid * per;
     for (;; ++b) {
       const Seq s = seq_of(a, b, false);
-      const int u = my_m < s.mt ? s.tiles * a.Hkv : 0;
+      const int u = my_m < s.mt ? (s.tiles + kSegment) * a.Hkv : 0;
       if (r0 < at + u) break;
       at += u;
     }
@@ -428,6 +439,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  Walk w;
+  if (!idle) {
+    w.begin(a, s_begin[0], s_begin[1], units, my_m, r0);
+    // a piece of nothing but the units before a first tile; the next one begins it
+    if (w.t0 == w.t1) idle = true;
+  }
   if (idle) {
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
     pdl_wait_prior_grid();  // a grid is not done before the one it follows
@@ -436,8 +453,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int Gq = a.Hq / a.Hkv;
   const int records = B * a.Hkv * mts;
   const Waiter wait{&s_abort, a.error_word};
-  Walk w;
-  w.begin(a, s_begin[0], s_begin[1], units, my_m);
   pdl_wait_prior_grid();
 
   if (warp == 4) {
@@ -474,16 +489,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kTile);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
-      int n = 0, seg = 0;
-      bool ok = true;
-      auto issue_s = [&](int i) {
-        const int it = 2 * i, slot = it % S;
-        // the buffer's last P, that of tile i - 2, is consumed
-        if (i >= 2 && !wait(bar_pv + 8 * (i & 1), ((i - 2) >> 1) & 1)) return false;
-        if (!wait(bar_full + 8 * slot, (it / S) & 1)) return false;
+    // The whole warp walks along; lane 0 issues.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kTile);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
+    int n = 0, seg = 0;
+    bool ok = true;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait(bar, parity) ? 1 : 0) != 0;
+    };
+    auto issue_s = [&](int i) {
+      const int it = 2 * i, slot = it % S;
+      // the buffer's last P, that of tile i - 2, is consumed
+      if (i >= 2 && !wait_all(bar_pv + 8 * (i & 1), ((i - 2) >> 1) & 1)) return false;
+      if (!wait_all(bar_full + 8 * slot, (it / S) & 1)) return false;
+      if (lane == 0) {
         tc_fence_after();
         const uint32_t k_s = ring + slot * G::kTensor;
 #pragma unroll
@@ -493,19 +512,86 @@ __global__ void __launch_bounds__(kThreads, 2)
                     smem_desc_sw128(k_s + (k >> 2) * G::kSlab + 32 * (k & 3)), idesc_s, k > 0);
         umma_commit(bar_empty + 8 * slot);
         umma_commit(bar_s + 8 * (i & 1));
-        return true;
-      };
-      do {
-        const int cnt = w.t1 - w.t0;
-        ok = wait(bar_q, seg & 1) && issue_s(n);
-        for (int i = 0; i < cnt && ok; ++i) {
-          if (i + 1 < cnt) ok = issue_s(n + i + 1);
-          const int it = 2 * (n + i) + 1, slot = it % S;
-          ok = ok && wait(bar_p + 8 * ((n + i) & 1), ((n + i) >> 1) & 1) &&
-               wait(bar_full + 8 * slot, (it / S) & 1);
-          if (!ok) break;
+      }
+      __syncwarp();
+      return true;
+    };
+    // Rows of V that nobody may read can hold anything, and 0 times NaN is NaN: they are
+    // cleared in shared memory. 
+    auto clear_rows = [&](uint32_t v_s, int from) {
+      for (int i = lane; i < (kTile - from) * (D / 8); i += 32) {
+        const int r = from + i / (D / 8), ch = i % (D / 8);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         v_s + (ch >> 3) * G::kSlab + r * 128 + ((ch & 7) << 4)),
+                     "r"(0u)
+                     : "memory");
+      }
+    };
+    // In the tree's tile, besides, the nodes that no row sees, and single values that are not
+    // finite: the rows that do see those get them back at the end. Returns their nodes.
+    auto clear_tree = [&](uint32_t v_s, uint64_t used) {
+      uint64_t odd = 0;
+#pragma unroll 4
+      for (int i = lane; i < kTile * (D / 8); i += 32) {
+        const int r = i / (D / 8), ch = i % (D / 8);  // (any order within a row serves)
+        const uint32_t at = v_s + (ch >> 3) * G::kSlab + r * 128 + ((ch & 7) << 4);
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(at));
+        const bool clear = !((used >> r) & 1);
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u, bad = true;
+          if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0xffffu, bad = true;
+          if (clear) x[k] = 0;
+        }
+        if (bad && !clear) odd |= 1ull << r;
+        if (bad || clear)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
+                       "r"(x[1]), "r"(x[2]), "r"(x[3])
+                       : "memory");
+      }
+      return (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(odd >> 32)) << 32 |
+             __reduce_or_sync(0xffffffffu, (uint32_t)odd);
+    };
+    do {
+      const int cnt = w.t1 - w.t0;
+      uint64_t used = 0;  // nodes that some row sees
+      if (w.t1 == w.s.tiles) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (lane + 32 * h < w.s.live) used |= a.mask[(size_t)w.b * a.N + lane + 32 * h];
+        used = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(used >> 32)) << 32 |
+                __reduce_or_sync(0xffffffffu, (uint32_t)used)) &
+               bit_range(0, w.s.live);
+      }
+      ok = wait_all(bar_q, seg & 1) && issue_s(n);
+      for (int i = 0; i < cnt && ok; ++i) {
+        if (i + 1 < cnt) ok = issue_s(n + i + 1);
+        const int it = 2 * (n + i) + 1, slot = it % S;
+        const uint32_t v_s = ring + slot * G::kTensor;
+        ok = ok && wait_all(bar_full + 8 * slot, (it / S) & 1);
+        if (!ok) break;
+        const int t = w.t0 + i;
+        const bool tree = t == w.s.tiles - 1;
+        const int valid = w.s.L - w.s.start - t * kTile;
+        if (tree || valid < kTile) {
+          if (tree) {
+            const uint64_t odd = clear_tree(v_s, used);
+            if (lane == 0) s_odd = odd;
+          } else {
+            clear_rows(v_s, valid);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (tree && lane == 0) mbar_arrive(bar_v);
+        }
+        ok = wait_all(bar_p + 8 * ((n + i) & 1), ((n + i) >> 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
           tc_fence_after();
-          const uint32_t v_s = ring + slot * G::kTensor;
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             umma_bf16_ts(tmem + kOCol, tmem + ((n + i) & 1) * kTile + 8 * k,
@@ -513,20 +599,21 @@ __global__ void __launch_bounds__(kThreads, 2)
           umma_commit(bar_empty + 8 * slot);
           umma_commit(bar_pv + 8 * ((n + i) & 1));
         }
-        n += cnt;
-        ++seg;
-      } while (ok && w.next(a));
-      if (!ok) {  // let what was issued finish before tensor memory is given back
-        umma_commit(bar_end);
-        mbar_wait_bounded(bar_end, 0);
+        __syncwarp();
       }
+      n += cnt;
+      ++seg;
+    } while (ok && w.next(a));
+    if (!ok && lane == 0) {  // let what was issued finish before tensor memory is given back
+      umma_commit(bar_end);
+      mbar_wait_bounded(bar_end, 0);
     }
   } else {
     // ---------------------------------------------------------------- softmax
     const uint32_t my_tmem = tmem + ((uint32_t)(32 * warp) << 16);
     const float log2e = 1.4426950408889634f;
     const float sc = kMod ? 1.f : a.scale * log2e;
-    int n = 0, seg = 0, x_phase = 0, done_units = 0;
+    int n = 0, seg = 0, x_phase = 0, trees = 0;
     bool ok = true;
     // the same answer in every lane, and the warp together behind it
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
@@ -566,21 +653,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool real = my_row < rows, active = copies > 1 || 32 * warp < rows;
       const size_t brow = (size_t)w.b * a.N;
       const bool has_tree = w.t1 == w.s.tiles;
-      // what the tree's tile needs, on its way early: this row's ancestors, the nodes that any
-      // row sees, and two nodes' positions per lane
+      // what the tree's tile needs, on its way early: this row's ancestors, and two nodes'
+      // positions per lane
       const uint64_t my_mask =
           has_tree && real ? a.mask[brow + node] & bit_range(0, w.s.live) : 0;
-      uint64_t used = 0;
       int npos[2] = {};
-      if (has_tree) {
+      if (has_tree && a.pos != nullptr) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (lane + 32 * h < w.s.live) {
-            used |= a.mask[brow + lane + 32 * h];
-            if (a.pos != nullptr) npos[h] = max(a.pos[brow + lane + 32 * h], w.s.L);
-          }
-        used = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(used >> 32)) << 32 |
-               __reduce_or_sync(0xffffffffu, (uint32_t)used);
+          if (lane + 32 * h < w.s.live) npos[h] = max(a.pos[brow + lane + 32 * h], w.s.L);
       }
       const int qpos = real && a.pos != nullptr ? max(a.pos[brow + node], w.s.L) : 0;
       const int low = real && a.window > 0 ? qpos - a.window + 1 : 0;  // first slot in the window
@@ -619,8 +700,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         tc_fence_after();
-        // every thread has left the segment before this one, whose marks are now free
-        if (t == w.t0 && tid == 0) s_odd[(seg + 1) & 1] = 0;
         auto weights = [&](auto cols) {
           constexpr int NC = decltype(cols)::value;
           const int c0 = slice * NC;  // this thread's keys of the tile: [c0, c0 + NC)
@@ -717,50 +796,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else if (active) {
           weights(std::integral_constant<int, 64>{});
         }
-        // rows of V that nobody may read can hold anything, and 0 times NaN is NaN: they
-        // are cleared in shared memory. In the tree's tile so are values that are not finite
-        // (the nodes that do see them get them back at the end).
-        const int valid = tree ? w.s.live : w.s.L - t_abs;
-        if (tree || valid < kTile) {
-          const int it = 2 * n + 1, slot = it % S;
-          if (!wait_all(bar_full + 8 * slot, (it / S) & 1)) {
-            ok = false;
-            break;
-          }
-          const int r = tid >> 1;
-          bool clear = r >= valid;
-          if (tree) clear = !((used >> r) & 1);
-          bool odd = false;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {  // half a row per thread
-            const int ch = (tid & 1) * (D / 16) + c;
-            const uint32_t at = ring + slot * G::kTensor + (ch >> 3) * G::kSlab + r * 128 +
-                                ((ch & 7) << 4);  // any order within the row serves
-            uint32_t x[4];
-            if (!clear && tree) {
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                           : "r"(at));
-              bool bad = false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u, bad = true;
-                if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0xffffu, bad = true;
-              }
-              odd |= bad;
-              if (!bad) continue;
-            } else if (clear) {
-              x[0] = x[1] = x[2] = x[3] = 0;
-            } else {
-              continue;
-            }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
-                         "r"(x[1]), "r"(x[2]), "r"(x[3])
-                         : "memory");
-          }
-          if (odd) atomicOr(&s_odd[seg & 1], 1ull << r);
-          fence_proxy_async_smem();
-        }
         tc_fence_before();
         mbar_arrive(bar_p + 8 * (n & 1));
       }
@@ -769,10 +804,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Walk done = w;
       w = after;
       uint64_t odd = 0;
-      if (done.t1 == done.s.tiles) {
-        // every thread's mark is visible once the tile's last arrival is
-        if (!wait_all(bar_p + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
-        odd = *reinterpret_cast<volatile unsigned long long *>(&s_odd[seg & 1]);
+      if (has_tree) {
+        if (!wait_all(bar_v, trees & 1)) break;
+        ++trees;
+        odd = *reinterpret_cast<volatile unsigned long long *>(&s_odd);
       }
       // every S of this segment has been read, so Q's space is free; P of the last tile must
       // stay for the values to be given back
@@ -920,15 +955,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           reinterpret_cast<float2 *>(part + (size_t)kRows * D)[my_row] = make_float2(M, L);
       }
       if (done.t0 == 0 && tid == 0) {
-        const int off = r0 + done_units;  // the row tile's first unit
         Record r;
         r.first = piece;
-        r.last = p0 + (off + done.s.tiles - 1) / blk;
+        r.last = p0 + (done.off + kSegment + done.s.tiles - 1) / blk;
         r.pad[0] = r.pad[1] = 0;
         reinterpret_cast<Record *>(workspace +
                                    records_offset())[((size_t)done.b * a.Hkv + done.g) * mts + my_m] = r;
       }
-      done_units += done.t1 - done.t0;
       tc_fence_before();
       if (more && !early_q) load_q(w);
       ++seg;
@@ -1052,7 +1085,8 @@ cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts
 int tree_parts(int B, int N, int Hq, int Hkv, int max_len, int num_parts, int sms) {
   const int mt = row_tiles(N, Hq / Hkv);
   if (num_parts > 0) return num_parts < mt ? mt : num_parts;
-  const long long units = (long long)B * Hkv * mt * ((max_len + kTile - 1) / kTile + 1);
+  const long long units =
+      (long long)B * Hkv * mt * ((max_len + kTile - 1) / kTile + 1 + kSegment);
   const long long most = units < mt ? mt : units;
   return (int)(most < 2 * sms ? most : 2 * sms < mt ? mt : 2 * sms);
 }
