@@ -137,6 +137,10 @@ struct Walk {
     return true;
   }
   __device__ __forceinline__ int rows(int G) const { return min(kRows, s.live * G - m * kRows); }
+  // Key tile t: the cache's tiles from the newest tokens back (with a distance bias the maximum
+  // then comes first and seldom moves), the tree's nodes last.
+  __device__ __forceinline__ bool is_tree(int t) const { return t == s.tiles - 1; }
+  __device__ __forceinline__ int token(int t) const { return s.start + (s.tiles - 2 - t) * kTile; }
 };
 // Lanes that share a row of the tile (see the kernel).
 __device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
@@ -465,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint64_t policy = w.s.mt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
         const int pair = w.b * a.Hkv + w.g;
         for (int t = w.t0; t < w.t1 && ok; ++t) {
-          const bool tree = t == w.s.tiles - 1;
-          const int row = tree ? 0 : w.s.start + t * kTile;
+          const bool tree = w.is_tree(t);
+          const int row = tree ? 0 : w.token(t);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++it) {
             const int slot = it % S;
@@ -575,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         ok = ok && wait_all(bar_full + 8 * slot, (it / S) & 1);
         if (!ok) break;
         const int t = w.t0 + i;
-        const bool tree = t == w.s.tiles - 1;
-        const int valid = w.s.L - w.s.start - t * kTile;
+        const bool tree = w.is_tree(t);
+        const int valid = w.s.L - w.token(t);
         if (tree || valid < kTile) {
           if (tree) {
             const uint64_t odd = clear_tree(v_s, used);
@@ -665,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const int qpos = real && a.pos != nullptr ? max(a.pos[brow + node], w.s.L) : 0;
       const int low = real && a.window > 0 ? qpos - a.window + 1 : 0;  // first slot in the window
+      const int low_max = __reduce_max_sync(0xffffffffu, low);
       float slope = 0.f;
       if constexpr (kMod)
         if (real && a.slopes != nullptr) slope = a.slopes[w.g * Gq + hi] * log2e;
@@ -681,10 +686,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       for (int t = w.t0; t < w.t1; ++t, ++n) {
-        const bool tree = t == w.s.tiles - 1;
-        const int t_abs = w.s.start + t * kTile;
+        const bool tree = w.is_tree(t);
+        const int t_abs = w.token(t);
         const uint32_t p_addr = my_tmem + (n & 1) * kTile;
-        uint64_t see;
+        // the keys of the tile this row sees: all of them, in most tiles
+        const bool all = !tree && t_abs + kTile <= w.s.L && low_max <= t_abs;
+        uint64_t see = ~0ull;
         if (tree) {
           see = my_mask;
           if (a.window > 0)
@@ -692,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int at = __shfl_sync(0xffffffffu, j < 32 ? npos[0] : npos[1], j & 31);
               if (qpos - at >= a.window) see &= ~(1ull << j);
             }
-        } else {
-          see = real ? bit_range(low - t_abs, w.s.L - t_abs) : 0;
+        } else if (!all) {
+          see = bit_range(low - t_abs, w.s.L - t_abs);
         }
         if (!wait_all(bar_s + 8 * (n & 1), (n >> 1) & 1)) {
           ok = false;
@@ -736,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
           }
-          const uint64_t mine = (see >> c0) & (~0ull >> (64 - NC));
-          if (!__all_sync(0xffffffffu, mine == ~0ull >> (64 - NC))) {
+          if (!all) {
+            const uint64_t mine = see >> c0;
             const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
