@@ -265,28 +265,46 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[128 x N] (+)= A[128 x 16, tensor memory] B[16 x N]
-__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The MMAs with a descriptor in two halves: the low word (address and leading offset) is all
+// that changes from one to the next, by an addition.
+__device__ __forceinline__ void umma_bf16_ss(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
+                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[128 x N] (+)= A[128 x 16, tensor memory] B[16 x N]
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
+                                             uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-// Descriptor of an MN-major operand in 128-byte swizzle atoms (8 K rows of 64 MN elements):
-// the leading offset steps to the next 64 elements of MN (`slab` bytes on), the stride
-// offset to the next 8 rows of K.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t slab) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(slab >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Descriptor halves of operands in 128-byte swizzle atoms (8 rows of 128 bytes). The high word:
+// 1024 bytes from 8 rows to the next 8, the version bit, the swizzle mode. The low word: the
+// address, and for an MN-major operand (V: tokens x dims) the leading offset, the step to the
+// next 64 elements of MN (a K-major operand does not use it).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
 }
 constexpr uint32_t kBIsMnMajor = 1u << 16;  // instruction descriptor
 
@@ -342,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
   const uint32_t bar_s = bar_empty + 8 * S, bar_p = bar_s + 16, bar_pv = bar_p + 16;
   const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8, bar_x = bar_end + 8, bar_v = bar_x + 8;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int P = gridDim.x, piece = blockIdx.x;
 
   if (tid == 0) {
@@ -442,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   Walk w;
   if (!idle) {
     w.begin(a, s_begin[0], s_begin[1], units, my_m, r0);
@@ -493,9 +511,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMAs
-    // The whole warp walks along; lane 0 issues.
+    // The warp stays together and one elected lane issues: every operand is then the same across
+    // the warp as far as the compiler can tell (under `lane == 0` an MMA took 65 cycles to
+    // issue).
     constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kTile);
     constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, D) | kBIsMnMajor;
+    const uint32_t q_lo = desc_lo(q_s, 16), k_lo = desc_lo(ring, 16), v_lo = desc_lo(ring, G::kSlab);
     int n = 0, seg = 0;
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
@@ -506,14 +527,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       // the buffer's last P, that of tile i - 2, is consumed
       if (i >= 2 && !wait_all(bar_pv + 8 * (i & 1), ((i - 2) >> 1) & 1)) return false;
       if (!wait_all(bar_full + 8 * slot, (it / S) & 1)) return false;
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t k_s = ring + slot * G::kTensor;
+      tc_fence_after();
+      const uint32_t k_at = k_lo + slot * (G::kTensor >> 4), d = tmem + (i & 1) * kTile;
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          umma_bf16(tmem + (i & 1) * kTile,
-                    smem_desc_sw128(q_s + (k >> 2) * (kRows * 128) + 32 * (k & 3)),
-                    smem_desc_sw128(k_s + (k >> 2) * G::kSlab + 32 * (k & 3)), idesc_s, k > 0);
+          umma_bf16_ss(d, q_lo + (k >> 2) * (kRows * 128 >> 4) + 2 * (k & 3),
+                       k_at + (k >> 2) * (G::kSlab >> 4) + 2 * (k & 3), kDescHi, idesc_s, k > 0);
         umma_commit(bar_empty + 8 * slot);
         umma_commit(bar_s + 8 * (i & 1));
       }
@@ -571,17 +591,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __reduce_or_sync(0xffffffffu, (uint32_t)used)) &
                bit_range(0, w.s.live);
       }
-      ok = wait_all(bar_q, seg & 1) && issue_s(n);
+      ok = ok && wait_all(bar_q, seg & 1) && issue_s(n);
       for (int i = 0; i < cnt && ok; ++i) {
+        const int it = 2 * (n + i) + 1, slot = it % S, t = w.t0 + i;
         if (i + 1 < cnt) ok = issue_s(n + i + 1);
-        const int it = 2 * (n + i) + 1, slot = it % S;
-        const uint32_t v_s = ring + slot * G::kTensor;
         ok = ok && wait_all(bar_full + 8 * slot, (it / S) & 1);
         if (!ok) break;
-        const int t = w.t0 + i;
         const bool tree = w.is_tree(t);
         const int valid = w.s.L - w.token(t);
         if (tree || valid < kTile) {
+          const uint32_t v_s = ring + slot * G::kTensor;
           if (tree) {
             const uint64_t odd = clear_tree(v_s, used);
             if (lane == 0) s_odd = odd;
@@ -591,15 +610,17 @@ __global__ void __launch_bounds__(kThreads, 2)
           fence_proxy_async_smem();
           __syncwarp();
           if (tree && lane == 0) mbar_arrive(bar_v);
+          __syncwarp();
         }
         ok = wait_all(bar_p + 8 * ((n + i) & 1), ((n + i) >> 1) & 1);
         if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint32_t v_at = v_lo + slot * (G::kTensor >> 4), p = tmem + ((n + i) & 1) * kTile;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            umma_bf16_ts(tmem + kOCol, tmem + ((n + i) & 1) * kTile + 8 * k,
-                         smem_desc_mn_sw128(v_s + k * 2048, G::kSlab), idesc_o, i > 0 || k > 0);
+            umma_bf16_ts(tmem + kOCol, p + 8 * k, v_at + k * (2048 >> 4), kDescHi, idesc_o,
+                         i > 0 || k > 0);
           umma_commit(bar_empty + 8 * slot);
           umma_commit(bar_pv + 8 * ((n + i) & 1));
         }
@@ -608,8 +629,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       n += cnt;
       ++seg;
     } while (ok && w.next(a));
-    if (!ok && lane == 0) {  // let what was issued finish before tensor memory is given back
-      umma_commit(bar_end);
+    if (!ok) {  // let what was issued finish before tensor memory is given back
+      __syncwarp();
+      if (elect_one()) umma_commit(bar_end);
+      __syncwarp();
       mbar_wait_bounded(bar_end, 0);
     }
   } else {
