@@ -7,11 +7,14 @@
 //   entropy     = ln S - (sum e^(z - M) (z - M)) / S      (nats)
 //   top K       : the K largest logits, equal ones by the lower id
 //
-// One read of the logits. A row is cut over a cluster of CTAs; every thread streams 16-byte
-// vectors (the next ones in flight while it works on the last), keeping a running maximum,
-// both sums relative to it (moved only when a group of vectors exceeds it) and its largest
-// logit with its id. The threads' sums meet in shared memory, the CTAs' in distributed
-// shared memory.
+// One read of the logits. A row is cut over a cluster of CTAs; every thread streams groups of
+// four 16-byte vectors (the next group in flight while it works on the last), keeping its
+// largest logit with its id and both sums relative to it, moved only when a group exceeds
+// it. The threads' sums meet in shared memory, the CTAs' in distributed shared memory.
+//
+// The instructions per logit bound it, so the exponents' arguments and both sums run as
+// packed pairs, and a logit of -inf (0 times -inf in the entropy's sum) is not guarded against
+// but found by the group's sum being NaN, and that group done again.
 //
 // Alternatives without a sort of the row: a value and its id form one 64-bit key, all
 // different. The K-th largest of the threads' own maxima bounds the K-th largest key of the
@@ -36,6 +39,7 @@ constexpr int kCtasPerSm = 4;
 constexpr int kUnroll = 4;       // vectors a thread works on at a time
 constexpr int kMaxCluster = 16;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Orders by value, then by the lower id: larger is better. NaN orders by its bits.
 __device__ __forceinline__ u64 rank_key(float v, int id) {
@@ -99,6 +103,34 @@ __device__ __forceinline__ u64 block_merge(u64 list, u64 (*s)[32]) {
 template <bool kBf16>
 struct Vec {
   static constexpr int kN = kBf16 ? 8 : 4;
+  // the largest of n vectors' values (a NaN is passed over)
+  template <int n>
+  __device__ static float largest(const uint4 (&x)[n]) {
+    if constexpr (kBf16) {
+      __nv_bfloat162 m[4];
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+          m[i] = u == 0 ? b : __hmax2(m[i], b);
+        }
+      }
+      const __nv_bfloat162 a = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+      return fmaxf(__low2float(a), __high2float(a));
+    } else {
+      float m[4];
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m[i] = u == 0 ? __uint_as_float(w[i]) : fmaxf(m[i], __uint_as_float(w[i]));
+      }
+      return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    }
+  }
   __device__ static void unpack(uint4 x, float (&v)[kN]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -135,14 +167,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return y;
 }
 
-// A running softmax state: the maximum logit m, s = sum 2^(k (v - m)) and
-// c = sum 2^(k (v - m)) k (v - m), with k = log2(e) / T. Nothing seen: m = -inf.
+// A running softmax state: the maximum logit m and, relative to the exponent r = m k with k =
+// log2(e) / T, s = sum 2^(k v - r) and c = sum 2^(k v - r) (k v - r). (r is one rounded number
+// that every exponent is taken against, in one rounding: never contracted.) Nothing seen: m = -inf.
 struct State {
   float m, s, c;
-  // the sums relative to a larger maximum
+  // the factors that move sums from this maximum to a larger one
   __device__ __forceinline__ void raise(float to, float k) {
     if (m != -INFINITY) {
-      const float d = (m - to) * k, f = ex2(d);
+      const float d = __fmul_rn(m, k) - __fmul_rn(to, k), f = ex2(d);
       c = f > 0.f ? f * fmaf(d, s, c) : 0.f * c;  // keeps a NaN
       s *= f;
     }
@@ -156,6 +189,26 @@ struct State {
     c += o.c;
   }
 };
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ u64 pair_of(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(u64 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 struct Slice {  // what a CTA keeps for the others of its cluster
   State st;
@@ -214,68 +267,103 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
     if (id >= 0 && id < a.V) id_value = V::one(base, id);
   }
 
-  State st{-INFINITY, 0.f, 0.f};
-  float best = -INFINITY;
-  int best_id = -1;  // none yet
-  auto group = [&](const float *v, int n, auto id_of) {
-    float mx = v[0];
+  State st{-INFINITY, 0.f, 0.f};  // st.m is also this thread's largest logit
+  int best_id = -1;               // and this its id; -1: nothing seen yet
+  // n vectors' worth of logits, the first element of vector u being first + u * stride
+  auto group = [&](auto &x, int first, int stride) {
+    constexpr int n = sizeof(x) / sizeof(uint4);
+    const float mx = V::template largest<n>(x);
+    if (mx > st.m || best_id < 0) {  // strictly: of equal values the lower id stays
+      st.raise(mx, k);
+      bool found = false;
 #pragma unroll
-    for (int i = 1; i < n; ++i) mx = fmaxf(mx, v[i]);
-    if (mx > st.m) st.raise(mx, k);
-    if (mx > best || best_id < 0) {  // strictly: equal values keep the lower id
-      best = mx;
+      for (int u = n - 1; u >= 0; --u) {
+        float v[E];
+        V::unpack(x[u], v);
 #pragma unroll
-      for (int i = n - 1; i >= 0; --i)
-        if (v[i] == mx || best_id < 0) best_id = id_of(i);
+        for (int i = E - 1; i >= 0; --i)
+          if (v[i] == mx || !found) best_id = first + u * stride + i, found = true;
+      }
     }
-    const float m0 = st.m == -INFINITY ? 0.f : st.m;
-    float s = 0.f, c = 0.f;
+    const float r = st.m == -INFINITY ? 0.f : __fmul_rn(st.m, k);
+    const u64 k2 = pair_of(k, k), r2 = pair_of(-r, -r);
+    u64 s2[2] = {}, c2[2] = {};
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      // The difference first: k v - k m would carry the rounding of k m into every weight.
-      // Far below the maximum (or -inf): weight 0, and a finite factor beside it.
-      const float d = max_nan((v[i] - m0) * k, -400.f), e = ex2(d);
-      s += e;
-      c = fmaf(e, d, c);
+    for (int u = 0; u < n; ++u) {
+      float v[E];
+      V::unpack(x[u], v);
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const u64 d = fma2(pair_of(v[i], v[i + 1]), k2, r2);
+        float d0, d1;
+        unpair(d, d0, d1);
+        const u64 e = pair_of(ex2(d0), ex2(d1));
+        s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], e);
+        c2[(i / 2) & 1] = fma2(e, d, c2[(i / 2) & 1]);
+      }
     }
-    st.s += s;
+    float s0, s1, c0, c1;
+    unpair(add2(s2[0], s2[1]), s0, s1);
+    unpair(add2(c2[0], c2[1]), c0, c1);
+    float c = c0 + c1;
+    if (isnan(c)) {
+      // -inf has weight 0 and adds nothing (a real NaN comes out again)
+      c = 0.f;
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        float v[E];
+        V::unpack(x[u], v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float d = max_nan(fmaf(v[i], k, -r), -400.f);
+          c = fmaf(ex2(d), d, c);
+        }
+      }
+    }
+    st.s += s0 + s1;
     st.c += c;
   };
-  if (rank == 0 && tid < head) {
-    const float v = V::one(base, tid);
-    group(&v, 1, [&](int) { return tid; });
-  }
+  // single elements (a row's ends) as a vector of one and -infs
+  auto single = [&](int id) {
+    const float v = V::one(base, id);
+    uint4 x[1];
+    if constexpr (kBf16)
+      x[0] = make_uint4(0xff800000u | (__float_as_uint(v) >> 16), 0xff80ff80u, 0xff80ff80u,
+                        0xff80ff80u);
+    else
+      x[0] = make_uint4(__float_as_uint(v), 0xff800000u, 0xff800000u, 0xff800000u);
+    group(x, id, 0);
+  };
+  if (rank == 0 && tid < head) single(tid);
   {
-    uint4 next[kUnroll];
-    int at = v0 + tid;
-    auto load = [&](int from) {
+    constexpr int kStep = kUnroll * kThreads;
+    const int full = (v1 - v0) / kStep;  // groups that every thread has whole
+    const uint4 *p = vec + v0 + tid;
+    uint4 x[kUnroll], next[kUnroll];
+    if (full > 0) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (from + u * kThreads < v1) next[u] = ld_stream(vec + from + u * kThreads);
-    };
-    load(at);
-    while (at < v1) {
-      uint4 cur[kUnroll];
+      for (int u = 0; u < kUnroll; ++u) next[u] = ld_stream(p + u * kThreads);
+    }
+    int first = head + (v0 + tid) * E;
+    for (int i = 0; i < full; ++i) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
-      const int here = at;
-      at += kUnroll * kThreads;
-      load(at);
+      for (int u = 0; u < kUnroll; ++u) x[u] = next[u];
+      p += kStep;
+      if (i + 1 < full) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (here + u * kThreads < v1) {
-          float v[E];
-          V::unpack(cur[u], v);
-          const int first = head + (here + u * kThreads) * E;
-          group(v, E, [&](int i) { return first + i; });
-        }
+        for (int u = 0; u < kUnroll; ++u) next[u] = ld_stream(p + u * kThreads);
+      }
+      group(x, first, kThreads * E);
+      first += kStep * E;
+    }
+    for (int at = v0 + full * kStep + tid; at < v1; at += kThreads) {
+      uint4 y[1] = {ld_stream(vec + at)};
+      group(y, head + at * E, 0);
     }
   }
-  if (rank == C - 1 && tail0 + tid < a.V) {
-    const float v = V::one(base, tail0 + tid);
-    group(&v, 1, [&](int) { return tail0 + tid; });
-  }
+  if (rank == C - 1 && tail0 + tid < a.V) single(tail0 + tid);
 
+  const float st_max = st.m;
   // ---- the slice's sums
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -289,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
 
   // ---- the slice's 32 best
   if (a.K > 0) {
-    const u64 mine = best_id < 0 ? 0ull : rank_key(best, best_id);
+    const u64 mine = best_id < 0 ? 0ull : rank_key(st_max, best_id);
     u64 list = block_merge(warp_sort(mine), s_list);
     if (a.K > 1) {
       if (warp == 0) s_slice.list[lane] = list;
@@ -358,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
         t.join(x, k);
       }
       if (lane == 0) {
-        const float ln_s = isinf(t.m) ? NAN : logf(t.s);
-        s_out[0] = t.m;
-        s_out[1] = ln_s;
-        if (a.entropy != nullptr) a.entropy[row] = ln_s - t.c / t.s * 0.6931471805599453f;
+        const float log2_s = isinf(t.m) ? NAN : log2f(t.s);
+        s_out[0] = __fmul_rn(t.m, k);
+        s_out[1] = log2_s;
+        if (a.entropy != nullptr) a.entropy[row] = (log2_s - t.c / t.s) * kLn2;
       }
     }
     u64 list = 0;
@@ -372,19 +460,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) logprobs_kernel(const Lo
       }
     }
     __syncthreads();
-    const float m = s_out[0], ln_s = s_out[1], inv_t = 1.f / a.temperature;
-    if (has_id) a.logprobs[row * a.C + tid] = (id_value - m) * inv_t - ln_s;
+    const float r = s_out[0], log2_s = s_out[1];
+    auto logprob = [&](float v) { return (fmaf(v, k, -r) - log2_s) * kLn2; };
+    if (has_id) a.logprobs[row * a.C + tid] = logprob(id_value);
     for (int i = tid + kThreads; i < a.C; i += kThreads) {
       const int id = a.ids[row * a.C + i];
       const float v = id >= 0 && id < a.V ? V::one(base, id) : -INFINITY;
-      a.logprobs[row * a.C + i] = (v - m) * inv_t - ln_s;
+      a.logprobs[row * a.C + i] = logprob(v);
     }
     if (a.K > 0) {
       list = block_merge(list, s_list);
       if (warp == 0 && lane < a.K) {
         // in a row with NaN fewer than K keys may have been found: any id in range then
         a.top_ids[row * a.K + lane] = list == 0 ? lane : key_id(list);
-        a.top_logprobs[row * a.K + lane] = (key_value(list) - m) * inv_t - ln_s;
+        a.top_logprobs[row * a.K + lane] = logprob(key_value(list));
       }
     }
   }
