@@ -663,7 +663,7 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0
     if logits.dim() != 2:
         raise ValueError(f"logits must be [B, ld], got {tuple(logits.shape)}")
     B, ld = logits.shape
-    at = _at(logits, "logits", logits.dtype, (B, ld), host=True)
+    at = _at(logits, "logits", logits.dtype, (B, ld))
     V = ld if vocab is None else int(vocab)
     C, K = 0, int(top_k)
     tokens_at = None

@@ -1338,7 +1338,7 @@ dec_status dec_token_logprobs(const void *logits, dec_dtype type, int ld, const 
       misaligned({ids, logprobs, entropy, top_ids, top_logprobs}, 4))
     return fail(DEC_ERR_INVALID_ARG, "pointers must be aligned to their elements");
   const dec_status st = where_all_here(
-      {{logits, "logits", true}, {C > 0 ? ids : nullptr, "ids", true},
+      {{logits, "logits", false}, {C > 0 ? ids : nullptr, "ids", true},
        {C > 0 ? logprobs : nullptr, "logprobs", true}, {entropy, "entropy", true},
        {K > 0 ? top_ids : nullptr, "top_ids", true},
        {K > 0 ? top_logprobs : nullptr, "top_logprobs", true}});

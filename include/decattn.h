@@ -626,8 +626,10 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  *   top_ids[b, 0..K)   = the K largest logits, largest first, equal ones by the lower id
  *   top_logprobs[b, k] = z[top_ids[b, k]] - lse
  * A logit of -inf has probability zero. A row with a NaN, with +inf or with nothing but
- * -inf gives NaN for every number (its top_ids are then only certain to lie in [0, V)).
- *   logits       [device|host] fp32 or bf16 [B, ld], the first V of each row counted
+ * -inf gives NaN for every number (its top_ids are then only certain to lie in [0, V)), and so
+ * does one whose copy into the SM never came (a bounded wait gave up).
+ *   logits       [device] fp32 or bf16 [B, ld], the first V of each row counted (read with
+ *                bulk copies)
  *   ids          [device|host] int32 [B, C], may be NULL when C = 0
  *   logprobs     [device|host] fp32 [B, C], may be NULL when C = 0
  *   entropy      [device|host] fp32 [B], or NULL

@@ -151,9 +151,10 @@ def test_guards_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, dsa.token_logprobs(zd, ids, top_k=7)))
-    pinned = dsa.token_logprobs(z.pin_memory(), ids.cpu().pin_memory(), top_k=7)
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b.cpu()) for a, b in zip(pinned, want))
+    pinned = dsa.token_logprobs(z.to(DEV), ids.cpu().pin_memory(), top_k=7)
+    assert all(torch.equal(a, b) for a, b in zip(pinned, want))
+    with pytest.raises(ValueError):
+        dsa.token_logprobs(z.pin_memory())
 
 
 def test_rows_past_32_bits():
