@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ uint64_t s_bar[2 * S + 10];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_sum[kThreads / 32][kMaxRowTiles], s_begin[2];
+  __shared__ int s_sum[kThreads / 32][kMaxRowTiles], s_begin[5];
   __shared__ float2 s_ml[kSoftmax];
   __shared__ unsigned long long s_odd;  // nodes with values that are not finite
 
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int P = gridDim.x, piece = blockIdx.x;
 
-  if (tid == 0) {
+  if (tid == 5 * 32) {  // (the warps begin with different things)
     for (int i = 0; i < 2 * S; ++i) mbar_init(bar_full + 8 * i, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_s + 8, 1);
@@ -384,41 +384,53 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&maps.kt);
     tma_prefetch_desc(&maps.vt);
   }
-  if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+  if (warp == 4) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   pdl_launch_dependents();
 
   // No kernel that may still run when this one starts writes lengths, node counts, masks or
   // positions (only this library's kernels let a successor start early), so the piece is found
   // before the wait for it.
   // ---- where this CTA's piece begins: the units of every row tile m, the CTAs each m gets in
-  // proportion, and a scan over the sequences for this CTA's m
-  const int per = (B + kThreads - 1) / kThreads;
-  int mine[kMaxRowTiles] = {};
-  for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) {
-    const Seq s = seq_of(a, b, piece == 0);
+  // proportion, and a scan over the sequences for this CTA's m. Up to 32 sequences every warp
+  // scans for itself, a lane each.
+  const bool few = B <= 32;
+  const int per = few ? 1 : (B + kThreads - 1) / kThreads;
+  const int b_first = few ? lane : tid * per;
+  int mine[kMaxRowTiles] = {}, m_total[kMaxRowTiles], m_before[kMaxRowTiles] = {};
+  for (int b = b_first; b < min(B, b_first + per); ++b) {
+    const Seq s = seq_of(a, b, piece == 0 && (!few || warp == 0));
 #pragma unroll
     for (int m = 0; m < kMaxRowTiles; ++m)
       if (m < s.mt) mine[m] += (s.tiles + kSegment) * a.Hkv;
   }
 #pragma unroll
-  for (int m = 0; m < kMaxRowTiles; ++m) {
-    const int v = __reduce_add_sync(0xffffffffu, mine[m]);
-    if (lane == 0) s_sum[warp][m] = v;
-  }
-  __syncthreads();
-  int m_total[kMaxRowTiles] = {}, m_before[kMaxRowTiles] = {};
-  long long all = 0;
+  for (int m = 0; m < kMaxRowTiles; ++m)
+    m_total[m] = m < mts ? __reduce_add_sync(0xffffffffu, mine[m]) : 0;
+  if (!few) {
 #pragma unroll
-  for (int m = 0; m < kMaxRowTiles; ++m) {
+    for (int m = 0; m < kMaxRowTiles; ++m)
+      if (lane == 0) s_sum[warp][m] = m_total[m];
+    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) m_before[m] += s_sum[w][m];
-      m_total[m] += s_sum[w][m];
+    for (int m = 0; m < kMaxRowTiles; ++m) {
+      m_total[m] = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) m_before[m] += s_sum[w][m];
+        m_total[m] += s_sum[w][m];
+      }
     }
-    all += m_total[m];
   }
-  int my_m = -1, p0 = 0, total = 0, pieces = 1, before = 0, count = 0;
-  {
+  int my_m = -1, p0 = 0, total = 0, pieces = P, before = 0, count = 0;
+  if (mts == 1) {
+    my_m = 0;
+    total = m_total[0];
+    before = m_before[0];
+    count = mine[0];
+  } else {
+    long long all = 0;
+#pragma unroll
+    for (int m = 0; m < kMaxRowTiles; ++m) all += m_total[m];
     int at = 0;
 #pragma unroll
     for (int m = 0; m < kMaxRowTiles; ++m)
@@ -446,8 +458,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane >= o) incl += v;
   }
   const int excl = before + incl - count;
-  if (!idle && excl <= r0 && r0 < excl + count) {
-    int at = excl, b = tid * per;
+  const bool here = !idle && excl <= r0 && r0 < excl + count;
+  if (few) {
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    const int b = who != 0 ? __ffs(who) - 1 : 0;
+    const int at = __shfl_sync(0xffffffffu, excl, b);
+    if (tid == 0) {
+      s_begin[0] = b;
+      s_begin[1] = r0 - at;
+    }
+  } else if (here) {
+    int at = excl, b = b_first;
     for (;; ++b) {
       const Seq s = seq_of(a, b, false);
       const int u = my_m < s.mt ? (s.tiles + kSegment) * a.Hkv : 0;
@@ -457,18 +478,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     s_begin[0] = b;
     s_begin[1] = r0 - at;
   }
+  // through shared memory, so that the compiler knows them to be the same in every lane (an
+  // MMA issued with operands that might differ costs several times as much)
+  if (tid == 0) {
+    s_begin[2] = units;
+    s_begin[3] = my_m;
+    s_begin[4] = r0;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  idle = s_begin[3] < 0 || s_begin[2] <= 0;
   Walk w;
   if (!idle) {
-    w.begin(a, s_begin[0], s_begin[1], units, my_m, r0);
+    w.begin(a, s_begin[0], s_begin[1], s_begin[2], s_begin[3], s_begin[4]);
     // a piece of nothing but the units before a first tile; the next one begins it
     if (w.t0 == w.t1) idle = true;
   }
   if (idle) {
-    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 4) tmem_dealloc(tmem, kTmemCols);
     pdl_wait_prior_grid();  // a grid is not done before the one it follows
     return;
   }
@@ -551,12 +580,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                      : "memory");
       }
     };
-    // In the tree's tile, besides, the nodes that no row sees, and single values that are not
-    // finite: the rows that do see those get them back at the end. Returns their nodes.
-    auto clear_tree = [&](uint32_t v_s, uint64_t used) {
+    // In the tree's tile, besides the rows behind the last node, the nodes that no row sees, and
+    // single values that are not finite: the rows that do see those get them back at the end.
+    // Returns their nodes.
+    auto clear_tree = [&](uint32_t v_s, uint64_t used, int live) {
+      clear_rows(v_s, live);
       uint64_t odd = 0;
 #pragma unroll 4
-      for (int i = lane; i < kTile * (D / 8); i += 32) {
+      for (int i = lane; i < live * (D / 8); i += 32) {
         const int r = i / (D / 8), ch = i % (D / 8);  // (any order within a row serves)
         const uint32_t at = v_s + (ch >> 3) * G::kSlab + r * 128 + ((ch & 7) << 4);
         uint32_t x[4];
@@ -602,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (tree || valid < kTile) {
           const uint32_t v_s = ring + slot * G::kTensor;
           if (tree) {
-            const uint64_t odd = clear_tree(v_s, used);
+            const uint64_t odd = clear_tree(v_s, used, w.s.live);
             if (lane == 0) s_odd = odd;
           } else {
             clear_rows(v_s, valid);
@@ -684,13 +715,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       // positions per lane
       const uint64_t my_mask =
           has_tree && real ? a.mask[brow + node] & bit_range(0, w.s.live) : 0;
+      const bool by_distance = a.window > 0 || (kMod && a.slopes != nullptr);
       int npos[2] = {};
-      if (has_tree && a.pos != nullptr) {
+      if (has_tree && by_distance) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (lane + 32 * h < w.s.live) npos[h] = max(a.pos[brow + lane + 32 * h], w.s.L);
       }
-      const int qpos = real && a.pos != nullptr ? max(a.pos[brow + node], w.s.L) : 0;
+      const int qpos = real && by_distance ? max(a.pos[brow + node], w.s.L) : 0;
       const int low = real && a.window > 0 ? qpos - a.window + 1 : 0;  // first slot in the window
       const int low_max = __reduce_max_sync(0xffffffffu, low);
       float slope = 0.f;
@@ -999,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
