@@ -7,26 +7,29 @@
 //   entropy     = ln S - (sum e^(z - M) (z - M)) / S      (nats)
 //   top K       : the K largest logits, equal ones by the lower id
 //
-// One read of the logits. Resident clusters of CTAs take the rows in turn, each CTA a slice.
-// Three kinds of warps, each running on into the next row without the others: one copies the
-// slices into a ring of shared memory (bulk copies); twelve take groups of four 16-byte vectors
-// per thread, keeping the thread's largest logit with its id and both sums relative to it
-// (moved only when a group exceeds it), and leave these in shared memory; four put a row
-// together from them, across the cluster through distributed shared memory. (The last part is
-// a long chain of short steps, which among streaming warps took 6000 cycles a row and held
-// them all up.)
+// One read of the logits, each thread keeping its largest logit with its id and both sums
+// relative to it, moved only when a group of vectors exceeds it. Two kernels:
+//   many rows   a CTA takes whole rows in turn (two CTAs per SM). Three kinds of warps, each
+//               running on into the next row without the others: one copies rows into a ring of
+//               shared memory (bulk copies, up to 144 KB in flight per SM); twelve stream groups
+//               of four 16-byte vectors per thread and leave their results in shared memory;
+//               four put a row together from them. (That last part is a long chain of short
+//               steps; among streaming warps it took 6000 cycles a row and held them all up.)
+//               512 rows of 131072 fp32 logits: 50 us, 5.4 TB/s; 1024 rows: 95 us, 5.7 TB/s.
+//   few rows    a row over a cluster of up to 16 CTAs, the slices' results joined through
+//               distributed shared memory. One row of 151936 fp32 logits: 8 us.
 //
-// The instructions per logit bound it, so the exponents' arguments and both sums run as
-// packed pairs, and a logit of -inf (0 times -inf in the entropy's sum) is not guarded against
-// but found by the group's sum being NaN, and that group done again.
+// The instructions per logit bound the streaming, so the exponents' arguments and both sums run
+// as packed pairs, and a logit of -inf (0 times -inf in the entropy's sum) is not guarded
+// against but found by the group's sum being NaN, and that group done again.
 //
 // Alternatives without a sort of the row: a value and its id form one 64-bit key, all
-// different. The K-th largest of the maxima of 32 groups of threads bounds the K-th largest key
-// of the slice from below (for K = 8 about 9 keys of the threads' reach it), and only threads
-// whose own maximum reaches it can hold a larger one. Those threads' vectors are read again
-// (from L2), a warp each; what reaches the bound goes into a list of the warp's 32 largest, and
-// a key's place among all the lists' is the number of larger ones. No more than 32 keys per
-// warp come through whatever the order of the values.
+// different. The K-th largest of the maxima of 32 (a cluster: up to 128) groups of threads
+// bounds the K-th largest key of the row from below (K = 8: about 9 of a CTA's threads reach
+// it), and only threads whose own maximum reaches it can hold a larger one. Those threads'
+// vectors are read again (from L2), a warp each; what reaches the bound goes into a list of the
+// warp's 32 largest, and a key's place is the number of larger ones among all the lists'. No
+// more than 32 keys per warp come through whatever the order of the values.
 #include <math.h>
 
 #include <atomic>
@@ -68,10 +71,6 @@ __device__ __forceinline__ float key_value(u64 k) {
 __device__ __forceinline__ u64 umax(u64 a, u64 b) { return a > b ? a : b; }
 __device__ __forceinline__ u64 umin(u64 a, u64 b) { return a < b ? a : b; }
 
-// A barrier of the post warps.
-__device__ __forceinline__ void post_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kPost) : "memory");
-}
 // A key into a warp's list sorted downwards; the smallest falls off.
 __device__ __forceinline__ u64 warp_insert(u64 list, u64 key) {
   const int lane = threadIdx.x & 31;
@@ -225,11 +224,6 @@ __device__ __forceinline__ void warp_join(State &st, float k) {
   }
 }
 
-struct Slice {  // what a CTA keeps for the others of its cluster
-  State st;
-  u64 list[32];
-};
-
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
@@ -239,26 +233,19 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on a barrier of any CTA of the cluster; what this thread knows of is then visible to
-// who waits there.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
+// Before a CTA leaves: order is all that is needed, every remote load has returned.
+__device__ __forceinline__ void cluster_exit_sync() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
+               "barrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -286,44 +273,337 @@ struct Row {
   }
 };
 
+// A row's numbers from its sums (one thread): the exponent its logits are taken against, log2 of
+// their sum, and the entropy.
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t row, const State &q, float k,
+                                           float *out) {
+  const float log2_s = isinf(q.m) ? NAN : log2f(q.s);
+  out[0] = __fmul_rn(q.m, k);
+  out[1] = log2_s;
+  if (a.entropy != nullptr) a.entropy[row] = (log2_s - q.c / q.s) * kLn2;
+}
+__device__ __forceinline__ float logprob_of(float v, float k, const float *out) {
+  return (fmaf(v, k, -out[0]) - out[1]) * kLn2;
+}
 // One of a row's alternatives. (In a row with NaN fewer than K keys may have been found: any
 // id in range then.)
 __device__ __forceinline__ void emit(const LogprobArgs &a, size_t row, int place, u64 key, float k,
                                      const float *out) {
   a.top_ids[row * a.K + place] = key == 0 ? place : key_id(key);
   a.top_logprobs[row * a.K + place] =
-      (fmaf(key == 0 ? NAN : key_value(key), k, -out[0]) - out[1]) * kLn2;
+      logprob_of(key == 0 ? NAN : key_value(key), k, out);
 }
 
-// grid (C, clusters), cluster (C, 1): cluster y takes rows y, y + clusters, ...; its CTA r
-// takes vectors [v0, v1) of the row, CTA 0 also the elements before the first aligned vector,
-// the last CTA those behind the last. Streaming thread t has the slice's vectors t, t +
-// kThreads, ...
+// A thread's part of a row: its sums, and its largest logit (sums.m) with its id.
 template <bool kBf16>
-__global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const LogprobArgs a,
-                                                                      int rows) {
+struct Running {
+  using V = Vec<kBf16>;
+  static constexpr int E = V::kN;
+  State sums{-INFINITY, 0.f, 0.f};
+  int best_id = -1;  // nothing seen yet
+
+  __device__ __forceinline__ u64 key() const {
+    return best_id < 0 ? 0ull : rank_key(sums.m, best_id);
+  }
+  // n vectors' worth of logits, the first element of vector u being first + u * stride
+  template <int n>
+  __device__ __forceinline__ void group(const uint4 (&x)[n], int first, int stride, float k) {
+    const float mx = V::template largest<n>(x);
+    if (mx > sums.m || best_id < 0) {  // strictly: of equal values the lower id stays
+      sums.raise(mx, k);
+      bool found = false;
+#pragma unroll
+      for (int u = n - 1; u >= 0; --u) {
+        float v[E];
+        V::unpack(x[u], v);
+#pragma unroll
+        for (int i = E - 1; i >= 0; --i)
+          if (v[i] == mx || !found) best_id = first + u * stride + i, found = true;
+      }
+    }
+    const float r = sums.m == -INFINITY ? 0.f : __fmul_rn(sums.m, k);
+    const u64 k2 = pair_of(k, k), r2 = pair_of(-r, -r);
+    u64 s2[2] = {}, c2[2] = {};
+#pragma unroll
+    for (int u = 0; u < n; ++u) {
+      float v[E];
+      V::unpack(x[u], v);
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        const u64 d = fma2(pair_of(v[i], v[i + 1]), k2, r2);
+        float d0, d1;
+        unpair(d, d0, d1);
+        const u64 e = pair_of(ex2(d0), ex2(d1));
+        s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], e);
+        c2[(i / 2) & 1] = fma2(e, d, c2[(i / 2) & 1]);
+      }
+    }
+    float s0, s1, c0, c1;
+    unpair(add2(s2[0], s2[1]), s0, s1);
+    unpair(add2(c2[0], c2[1]), c0, c1);
+    float c = c0 + c1;
+    if (isnan(c)) {
+      // -inf has weight 0 and adds nothing (a real NaN comes out again)
+      c = 0.f;
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        float v[E];
+        V::unpack(x[u], v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float d = max_nan(fmaf(v[i], k, -r), -400.f);
+          c = fmaf(ex2(d), d, c);
+        }
+      }
+    }
+    sums.s += s0 + s1;
+    sums.c += c;
+  }
+  __device__ __forceinline__ void single(float v, int id, float k) {
+    if (v > sums.m || best_id < 0) {
+      sums.raise(v, k);
+      best_id = id;
+    }
+    const float r = sums.m == -INFINITY ? 0.f : __fmul_rn(sums.m, k);
+    const float d = max_nan(fmaf(v, k, -r), -400.f), e = ex2(d);
+    sums.s += e;
+    sums.c = fmaf(e, d, sums.c);
+  }
+};
+
+// A warp's 32 largest keys that reach `bound`, sorted downwards across its lanes.
+struct Best {
+  u64 list = 0, bound;
+  __device__ explicit Best(u64 bound) : bound(bound) {}
+  __device__ __forceinline__ void offer(u64 key) {  // a key per lane
+    unsigned todo = __ballot_sync(kAll, key >= bound);
+    while (todo) {
+      const int from = __ffs(todo) - 1;
+      todo &= todo - 1;
+      list = warp_insert(list, __shfl_sync(kAll, key, from));
+    }
+  }
+  // a vector per lane (those with in = true), its first element's id; most hold nothing: one
+  // comparison of the largest value tells
+  template <bool kBf16>
+  __device__ __forceinline__ void offer_vector(uint4 x, bool in, int id, float least) {
+    using V = Vec<kBf16>;
+    const uint4 one[1] = {x};
+    // (not `<`: a NaN may be the largest key)
+    if (!__any_sync(kAll, in && (!(V::template largest<1>(one) < least) || V::any_nan(x)))) return;
+    float v[V::kN];
+    V::unpack(x, v);
+#pragma unroll
+    for (int e = 0; e < V::kN; ++e) offer(in ? rank_key(v[e], id + e) : 0ull);
+  }
+};
+__device__ __forceinline__ float least_of(u64 bound) {
+  return bound > 1 ? key_value(bound) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ few rows
+// grid (C, rows), cluster (C, 1): CTA r takes vectors [v0, v1) of its row, CTA 0 also the
+// elements before the first aligned vector, the last CTA those behind the last; thread t has
+// vectors t, t + kFew, ... of the slice.
+constexpr int kFew = 256;
+constexpr int kFewWarps = kFew / 32;
+constexpr int kMaxGroups = 128;  // of a row
+
+struct Slice {  // what a CTA keeps for the others of its cluster
+  State sums[kFewWarps];
+  int n;          // keys of `list`
+  u64 group[32];  // the largest keys of its groups of threads
+  u64 list[32];   // its keys that reach the row's bound, at most K of them
+};
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs a) {
+  using V = Vec<kBf16>;
+  constexpr int E = V::kN;
+  __shared__ Slice s_slice;
+  __shared__ u64 s_all[kMaxGroups], s_bound, s_cand[kMaxCluster * 32];
+  __shared__ State s_states[kFewWarps];
+  __shared__ float s_out[2];
+  __shared__ int s_count;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = gridDim.x, rank = blockIdx.x;
+  const size_t row = blockIdx.y;
+  const float k = 1.4426950408889634f / a.temperature;
+  const Row<kBf16> r(a, row, rank, C);
+  Running<kBf16> run;
+  if (tid == 0) {
+    s_count = 0;
+    s_bound = 1;  // for fewer than K keys
+  }
+  // the given ids' logits and the row's ends, on their way while the row streams
+  const int my_id = rank == 0 && tid < a.C ? a.ids[row * a.C + tid] : -1;
+  const int end_id = rank == 0 && tid < r.head ? tid
+                     : rank == C - 1 && tid >= 32 && r.tail0 + tid - 32 < a.V ? r.tail0 + tid - 32
+                                                                              : -1;
+  const float end_value = end_id >= 0 ? V::one(r.base, end_id) : 0.f;
+  {
+    constexpr int kStep = kUnroll * kFew;
+    const int full = (r.v1 - r.v0) / kStep;  // groups that every thread has whole
+    const uint4 *p = r.vec + r.v0 + tid;
+    uint4 x[kUnroll], next[kUnroll];
+    if (full > 0) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) next[u] = ld_stream(p + u * kFew);
+    }
+    int first = r.head + (r.v0 + tid) * E;
+    for (int i = 0; i < full; ++i) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) x[u] = next[u];
+      p += kStep;
+      if (i + 1 < full) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) next[u] = ld_stream(p + u * kFew);
+      }
+      run.group(x, first, kFew * E, k);
+      first += kStep * E;
+    }
+    for (int at = r.v0 + full * kStep + tid; at < r.v1; at += kFew) {
+      const uint4 y[1] = {ld_stream(r.vec + at)};
+      run.group(y, r.head + at * E, 0, k);
+    }
+  }
+  // (an end's id need not be in order here: keys of equal values are compared by id)
+  const float given = my_id >= 0 && my_id < a.V ? V::one(r.base, my_id) : -INFINITY;
+  const u64 vec_key = run.key(), end_key = end_id >= 0 ? rank_key(end_value, end_id) : 0ull;
+  if (end_id >= 0) run.single(end_value, end_id, k);
+
+  // ---- the slice: every warp's sums, the largest keys of its groups of threads
+  const int per = min(32, kMaxGroups / C), groups = per * C;  // groups to a CTA, of the row
+  State st = run.sums;
+  warp_join(st, k);
+  if (lane == 0) s_slice.sums[warp] = st;
+  u64 g = umax(vec_key, end_key);
+  for (int o = 1; o < kFew / per; o *= 2) g = umax(g, __shfl_xor_sync(kAll, g, o));
+  if (tid % (kFew / per) == 0) s_slice.group[tid / (kFew / per)] = g;
+  cluster_sync();
+  const uint32_t here = smem_addr(&s_slice);
+  if (tid < groups)
+    s_all[tid] = ld_cluster_u64(
+        cluster_map(here + (uint32_t)offsetof(Slice, group), tid / per) + 8 * (tid % per));
+  if (rank == 0) {  // the row's sums: a state per (CTA, warp)
+    State q{-INFINITY, 0.f, 0.f};
+    if (tid < C * kFewWarps) {
+      const uint32_t at = cluster_map(here, tid / kFewWarps) +
+                          (uint32_t)sizeof(State) * (tid % kFewWarps);
+      q.m = ld_cluster_f32(at);
+      q.s = ld_cluster_f32(at + 4);
+      q.c = ld_cluster_f32(at + 8);
+    }
+    warp_join(q, k);
+    if (lane == 0) s_states[warp] = q;
+  }
+  __syncthreads();
+  if (rank == 0 && warp == kFewWarps - 1) {
+    State q{-INFINITY, 0.f, 0.f};
+    if (lane < kFewWarps) q = s_states[lane];
+    warp_join(q, k);
+    if (lane == 0) finish_row(a, row, q, k, s_out);
+  }
+  if (a.K > 0) {
+    // the K-th largest of the groups' keys
+    if (tid < groups && s_all[tid] > 0 && larger(s_all, groups, s_all[tid]) == a.K - 1)
+      s_bound = s_all[tid];
+    __syncthreads();
+    const u64 bound = s_bound;
+    Best best(bound);
+    // who can hold more than its largest: its vectors again, a warp each
+    unsigned owners = __ballot_sync(kAll, vec_key >= bound);
+    const float least = least_of(bound);
+    if (__any_sync(kAll, end_key >= bound)) best.offer(end_key);
+    for (; owners != 0; owners &= owners - 1) {
+      const int owner = warp * 32 + __ffs(owners) - 1;
+      for (int j0 = r.v0 + owner; j0 < r.v1; j0 += 32 * kFew) {
+        const int j = j0 + lane * kFew;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (j < r.v1) x = ld_stream(r.vec + j);
+        best.offer_vector<kBf16>(x, j < r.v1, r.head + j * E, least);
+      }
+    }
+    const int found = min(a.K, __popc(__ballot_sync(kAll, best.list > 0)));
+    if (found > 0) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_count, found);
+      at = __shfl_sync(kAll, at, 0);
+      if (lane < found) s_cand[at + lane] = best.list;  // at most kFewWarps x 32
+    }
+    __syncthreads();
+    const int cands = s_count;
+    if (tid < cands) {
+      const u64 key = s_cand[tid];
+      const int place = larger(s_cand, cands, key);
+      if (place < a.K) s_slice.list[place] = key;
+    }
+    if (tid == 0) s_slice.n = min(cands, a.K);
+    cluster_sync();
+    if (rank == 0) {
+      if (tid == 0) s_count = 0;
+      __syncthreads();
+      int n = 0;
+      if (lane < C) n = ld_cluster_s32(cluster_map(here + (uint32_t)offsetof(Slice, n), lane));
+      for (int i0 = 0; i0 < C * a.K; i0 += kFew) {
+        const int i = i0 + tid, c = min(i / a.K, C - 1), j = i - c * a.K;
+        const int have = __shfl_sync(kAll, n, c);
+        if (j < have && j < a.K)
+          s_cand[atomicAdd(&s_count, 1)] = ld_cluster_u64(
+              cluster_map(here + (uint32_t)offsetof(Slice, list), c) + 8 * j);
+      }
+      __syncthreads();
+      const int all = s_count;  // at most 16 x 32
+      for (int i = tid; i < max(all, a.K); i += kFew) {
+        const u64 key = i < all ? s_cand[i] : 0;
+        const int place = i < all ? larger(s_cand, all, key) : i;  // (past them: a row with NaN)
+        if (place < a.K) emit(a, row, place, key, k, s_out);
+      }
+    }
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0) {
+    if (tid < a.C) a.logprobs[row * a.C + tid] = logprob_of(given, k, s_out);
+    for (int i = tid + kFew; i < a.C; i += kFew) {
+      const int id = a.ids[row * a.C + i];
+      a.logprobs[row * a.C + i] =
+          logprob_of(id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
+    }
+  }
+  if (C > 1) cluster_exit_sync();  // no CTA leaves while another still reads its shared memory
+}
+
+// ----------------------------------------------------------------- many rows
+// A barrier of the post warps.
+__device__ __forceinline__ void post_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kPost) : "memory");
+}
+
+// CTA x takes rows x, x + grid, ... Streaming thread t has a row's vectors t, t + kThreads, ...
+template <bool kBf16>
+__global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const LogprobArgs a,
+                                                                           int rows) {
   using V = Vec<kBf16>;
   constexpr int E = V::kN;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint64_t s_bar[2 * kStages + 8];
+  __shared__ uint64_t s_bar[2 * kStages + 4];
   __shared__ float4 s_sums[2][kThreads];  // (m, s, c) of a row's streaming threads
   __shared__ u64 s_keys[2][kThreads];     // and their largest keys (0: nothing seen)
-  __shared__ Slice s_slices[2];
   __shared__ State s_states[kPostWarps];
-  __shared__ u64 s_group[32];             // the largest key of every 12 streaming threads
-  __shared__ u64 s_cand[kMaxCluster * 32];
+  __shared__ u64 s_group[32], s_bound;    // the largest key of every 12 streaming threads
+  __shared__ u64 s_cand[kPost];
   __shared__ float s_out[2];
   __shared__ int s_count[2];              // owners and candidates
   __shared__ short s_owner[kThreads];
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = gridDim.x, rank = blockIdx.x;
   const uint32_t ring = smem_addr(smem), bar_full = smem_addr(s_bar);
   const uint32_t bar_empty = bar_full + 8 * kStages;
-  // a row's sums are left; they have been taken; CTA 0's: a row's slices are there; every
-  // CTA's: its slice has been read
+  // a row's sums are left; they have been taken
   const uint32_t bar_left = bar_empty + 8 * kStages, bar_taken = bar_left + 16;
-  const uint32_t bar_ready = bar_taken + 16, bar_free = bar_ready + 16;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar_full + 8 * i, 1);
@@ -332,22 +612,20 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_left + 8 * i, kWarps);
       mbar_init(bar_taken + 8 * i, kPostWarps);
-      mbar_init(bar_ready + 8 * i, C);
-      mbar_init(bar_free + 8 * i, 1);
     }
     s_abort = 0;
     s_count[0] = s_count[1] = 0;
     fence_barrier_init();
   }
-  cluster_sync();  // (also of the CTA) every barrier is ready for the others
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const float k = 1.4426950408889634f / a.temperature;
   // A bounded wait; one that gave up makes this and the later rows NaN.
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
-    while (!try_wait_cluster(bar, parity)) {
+    while (!mbar_try_wait(bar, parity)) {
       if (s_abort) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
         s_abort = 1;
@@ -362,9 +640,9 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       int n = 0;
-      for (size_t row = blockIdx.y; row < rows && !s_abort; row += gridDim.y) {
-        const Row<kBf16> r(a, row, rank, C);
-        for (int at = r.v0; at < r.v1; at += kStageVecs, ++n) {
+      for (size_t row = blockIdx.x; row < rows && !s_abort; row += gridDim.x) {
+        const Row<kBf16> r(a, row, 0, 1);
+        for (int at = 0; at < r.v1; at += kStageVecs, ++n) {
           const int slot = n % kStages;
           if (n >= kStages && !await(bar_empty + 8 * slot, (n / kStages - 1) & 1)) break;
           const uint32_t bytes = (uint32_t)min(kStageVecs, r.v1 - at) * 16u;
@@ -376,127 +654,64 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
         for (int j = max(0, n - kStages); j < n; ++j)
           mbar_wait_bounded(bar_full + 8 * (j % kStages), (j / kStages) & 1);
     }
-    __syncwarp();
   } else if (warp < kWarps) {
     // ---------------------------------------------------------------- stream
     int n = 0;
-    for (size_t row = blockIdx.y; row < rows; row += gridDim.y, ++turn) {
-      const Row<kBf16> r_(a, row, rank, C);
-      const int head = r_.head, v0 = r_.v0, v1 = r_.v1, par = turn & 1;
-      State st{-INFINITY, 0.f, 0.f};  // st.m is also this thread's largest logit
-      int best_id = -1;               // and this its id; -1: nothing seen yet
-      // n vectors' worth of logits, the first element of vector u being first + u * stride
-      auto group = [&](auto &x, int first, int stride) {
-        constexpr int n = sizeof(x) / sizeof(uint4);
-        const float mx = V::template largest<n>(x);
-        if (mx > st.m || best_id < 0) {  // strictly: of equal values the lower id stays
-          st.raise(mx, k);
-          bool found = false;
-#pragma unroll
-          for (int u = n - 1; u >= 0; --u) {
-            float v[E];
-            V::unpack(x[u], v);
-#pragma unroll
-            for (int i = E - 1; i >= 0; --i)
-              if (v[i] == mx || !found) best_id = first + u * stride + i, found = true;
-          }
-        }
-        const float r = st.m == -INFINITY ? 0.f : __fmul_rn(st.m, k);
-        const u64 k2 = pair_of(k, k), r2 = pair_of(-r, -r);
-        u64 s2[2] = {}, c2[2] = {};
-#pragma unroll
-        for (int u = 0; u < n; ++u) {
-          float v[E];
-          V::unpack(x[u], v);
-#pragma unroll
-          for (int i = 0; i < E; i += 2) {
-            const u64 d = fma2(pair_of(v[i], v[i + 1]), k2, r2);
-            float d0, d1;
-            unpair(d, d0, d1);
-            const u64 e = pair_of(ex2(d0), ex2(d1));
-            s2[(i / 2) & 1] = add2(s2[(i / 2) & 1], e);
-            c2[(i / 2) & 1] = fma2(e, d, c2[(i / 2) & 1]);
-          }
-        }
-        float s0, s1, c0, c1;
-        unpair(add2(s2[0], s2[1]), s0, s1);
-        unpair(add2(c2[0], c2[1]), c0, c1);
-        float c = c0 + c1;
-        if (isnan(c)) {
-          // -inf has weight 0 and adds nothing (a real NaN comes out again)
-          c = 0.f;
-#pragma unroll
-          for (int u = 0; u < n; ++u) {
-            float v[E];
-            V::unpack(x[u], v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-              const float d = max_nan(fmaf(v[i], k, -r), -400.f);
-              c = fmaf(ex2(d), d, c);
-            }
-          }
-        }
-        st.s += s0 + s1;
-        st.c += c;
-      };
-      for (int at = v0; at < v1; at += kStageVecs, ++n) {
-        const int slot = n % kStages, here = min(kStageVecs, v1 - at);
+    for (size_t row = blockIdx.x; row < rows; row += gridDim.x, ++turn) {
+      const Row<kBf16> r(a, row, 0, 1);
+      const int par = turn & 1;
+      Running<kBf16> run;
+      for (int at = 0; at < r.v1; at += kStageVecs, ++n) {
+        const int slot = n % kStages, here = min(kStageVecs, r.v1 - at);
         if (!__all_sync(kAll, await(bar_full + 8 * slot, (n / kStages) & 1) ? 1 : 0)) {
-          st.s = NAN;  // a copy that never came
+          run.sums.s = NAN;  // a copy that never came
           break;
         }
         const uint32_t src = ring + slot * (kStageVecs * 16) + tid * 16;
-        const int first = head + (at + tid) * E;
+        const int first = r.head + (at + tid) * E;
         if (here == kStageVecs) {
           uint4 x[kUnroll];
 #pragma unroll
           for (int u = 0; u < kUnroll; ++u) x[u] = ld_shared(src + u * (kThreads * 16));
-          group(x, first, kThreads * E);
+          run.group(x, first, kThreads * E, k);
         } else {
           for (int u = 0; tid + u * kThreads < here; ++u) {
-            uint4 y[1] = {ld_shared(src + u * (kThreads * 16))};
-            group(y, first + u * kThreads * E, 0);
+            const uint4 y[1] = {ld_shared(src + u * (kThreads * 16))};
+            run.group(y, first + u * kThreads * E, 0, k);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
       }
       if (turn >= 2) __all_sync(kAll, await(bar_taken + 8 * par, ((turn >> 1) + 1) & 1) ? 1 : 0);
-      s_sums[par][tid] = make_float4(st.m, st.s, st.c, 0.f);
-      s_keys[par][tid] = best_id < 0 ? 0ull : rank_key(st.m, best_id);
+      s_sums[par][tid] = make_float4(run.sums.m, run.sums.s, run.sums.c, 0.f);
+      s_keys[par][tid] = run.key();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_left + 8 * par);
     }
   } else {
     // ---------------------------------------------------------------- put rows together
     const int p = tid - kThreads - 32, pw = p >> 5;
-    for (size_t row = blockIdx.y; row < rows; row += gridDim.y, ++turn) {
+    for (size_t row = blockIdx.x; row < rows; row += gridDim.x, ++turn) {
       const int par = turn & 1, phase = (turn >> 1) & 1;
-      const int leader = turn % C;  // the CTA that puts this row together
-      Slice &s_slice = s_slices[par];
-      const Row<kBf16> r(a, row, rank, C);
+      const Row<kBf16> r(a, row, 0, 1);
       // a given id's logit and one element of each of the row's ends, while the row streams
       float given = -INFINITY;
-      if (rank == leader && p < a.C) {
+      if (p < a.C) {
         const int id = a.ids[row * a.C + p];
         if (id >= 0 && id < a.V) given = V::one(r.base, id);
       }
-      State st{-INFINITY, 0.f, 0.f};
-      u64 ends[2] = {};
-      auto single = [&](int id) {
-        const float v = V::one(r.base, id);
-        if (v > st.m) st.raise(v, k);
-        const float x = st.m == -INFINITY ? 0.f : __fmul_rn(st.m, k);
-        const float d = max_nan(fmaf(v, k, -x), -400.f), e = ex2(d);
-        st.s += e;
-        st.c = fmaf(e, d, st.c);
-        return rank_key(v, id);
-      };
-      if (rank == 0 && p < r.head) ends[0] = single(p);
-      if (rank == C - 1 && r.tail0 + p < a.V) ends[1] = single(r.tail0 + p);
-
+      Running<kBf16> run;
+      u64 ends = 0;
+      const int end_id = p < r.head ? p : p >= 32 && r.tail0 + p - 32 < a.V ? r.tail0 + p - 32 : -1;
+      if (end_id >= 0) {
+        const float v = V::one(r.base, end_id);
+        run.single(v, end_id, k);
+        ends = rank_key(v, end_id);
+      }
       const bool left = await(bar_left + 8 * par, phase);
-      u64 mine[kEach], most = umax(ends[0], ends[1]);
+      State st = run.sums;
+      u64 mine[kEach], most = ends;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const float4 x = s_sums[par][p * kEach + i];
@@ -512,31 +727,22 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
       if (lane == 0) s_states[pw] = st;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_taken + 8 * par);
-      if (C > 1 && turn >= 2) await(bar_free + 8 * par, phase ^ 1);
+      if (p == 0) s_bound = 1;  // for fewer than K keys
       post_sync();
-      auto finish = [&](const State &q) {  // one thread: the row's numbers
-        const float log2_s = isinf(q.m) || s_abort ? NAN : log2f(q.s);
-        s_out[0] = __fmul_rn(q.m, k);
-        s_out[1] = log2_s;
-        if (a.entropy != nullptr) a.entropy[row] = (log2_s - q.c / q.s) * kLn2;
-      };
-      if (p < 32) {
+      if (pw == kPostWarps - 1) {
         State q{-INFINITY, 0.f, 0.f};
         if (lane < kPostWarps) q = s_states[lane];
         warp_join(q, k);
-        if (lane == 0) {
-          if (C == 1) finish(q);
-          else s_slice.st = q;
-        }
-        __syncwarp();
+        if (s_abort) q.s = NAN;
+        if (lane == 0) finish_row(a, row, q, k, s_out);
       }
-      int place = -1;  // this thread's key's place among the row's (or the slice's) best
+      int place = -1;  // this thread's key's place among the row's best
       u64 key = 0;
       if (a.K > 0) {
-        // the K-th largest of the 32, in every warp
-        const u64 g = s_group[lane];
-        const unsigned at = __ballot_sync(kAll, larger(s_group, 32, g) == a.K - 1 && g > 0);
-        const u64 bound = at != 0 ? __shfl_sync(kAll, g, __ffs(at) - 1) : 1ull;  // 1: fewer
+        if (p < 32 && s_group[p] > 0 && larger(s_group, 32, s_group[p]) == a.K - 1)
+          s_bound = s_group[p];  // the K-th largest of the groups' keys
+        post_sync();
+        const u64 bound = s_bound;
         if (a.K == 1) {
           if (p == 0) place = 0, key = bound > 1 ? bound : 0;
         } else {
@@ -544,22 +750,12 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
           for (int i = 0; i < kEach; ++i)
             if (mine[i] >= bound) s_owner[atomicAdd(&s_count[0], 1)] = (short)(p * kEach + i);
           post_sync();
+          Best best(bound);
+          best.offer(ends);
+          // Items of 32 of an owner's vectors, four at a time so that their loads overlap.
           const int owners = s_count[0];
-          u64 list = 0;
-          auto offer = [&](u64 key) {
-            unsigned todo = __ballot_sync(kAll, key >= bound);
-            while (todo) {
-              const int from = __ffs(todo) - 1;
-              todo &= todo - 1;
-              list = warp_insert(list, __shfl_sync(kAll, key, from));
-            }
-          };
-          offer(ends[0]);
-          offer(ends[1]);
-          // Items of 32 of an owner's vectors, four at a time so that their loads overlap. Most
-          // hold nothing: one comparison of the largest value tells.
-          const int chunks = (r.v1 - r.v0 + 32 * kThreads - 1) / (32 * kThreads);
-          const float least = bound > 1 ? key_value(bound) : -INFINITY;
+          const int chunks = (r.v1 + 32 * kThreads - 1) / (32 * kThreads);
+          const float least = least_of(bound);
           for (int i0 = pw; i0 < owners * chunks; i0 += 4 * kPostWarps) {
             uint4 x[4];
             int j[4];
@@ -567,176 +763,79 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_kernel(const Logp
             for (int q = 0; q < 4; ++q) {
               const int i = i0 + q * kPostWarps, o = i / chunks;
               j[q] = r.v1;
+              x[q] = make_uint4(0u, 0u, 0u, 0u);
               if (i < owners * chunks)
-                j[q] = r.v0 + s_owner[o] + ((i - o * chunks) * 32 + lane) * kThreads;
+                j[q] = s_owner[o] + ((i - o * chunks) * 32 + lane) * kThreads;
               if (j[q] < r.v1) x[q] = ld_stream(r.vec + j[q]);
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint4 one[1] = {x[q]};
-              const bool in = j[q] < r.v1;
-              // (not `<`: a NaN may be the largest key)
-              if (!__any_sync(kAll, in && (!(V::template largest<1>(one) < least) || V::any_nan(x[q]))))
-                continue;
-              float v[E];
-              V::unpack(x[q], v);
-#pragma unroll
-              for (int e = 0; e < E; ++e)
-                offer(in ? rank_key(v[e], r.head + j[q] * E + e) : 0ull);
-            }
+            for (int q = 0; q < 4; ++q)
+              best.offer_vector<kBf16>(x[q], j[q] < r.v1, r.head + j[q] * E, least);
           }
-          const int found = min(a.K, __popc(__ballot_sync(kAll, list > 0)));
-          int base_at = 0;
-          if (lane == 0 && found > 0) base_at = atomicAdd(&s_count[1], found);
-          base_at = __shfl_sync(kAll, base_at, 0);
-          if (lane < found) s_cand[base_at + lane] = list;
+          const int found = min(a.K, __popc(__ballot_sync(kAll, best.list > 0)));
+          int at = 0;
+          if (lane == 0 && found > 0) at = atomicAdd(&s_count[1], found);
+          at = __shfl_sync(kAll, at, 0);
+          if (lane < found) s_cand[at + lane] = best.list;  // at most kPostWarps x 32
           post_sync();
-          const int cands = s_count[1];  // at most kPostWarps x 32 = kPost
+          const int cands = s_count[1];
           key = p < cands ? s_cand[p] : 0;
-          place = p < cands ? larger(s_cand, cands, key) : p;  // (behind them: nothing there)
+          place = p < cands ? larger(s_cand, cands, key) : p;  // (past them: a row with NaN)
           if (place >= a.K) place = -1;
         }
       }
-      if (C > 1) {
-        // ---- the row, in CTA 0, from the CTAs' slices
-        if (place >= 0) s_slice.list[place] = key;
-        post_sync();
-        if (p == 0) {
-          s_count[0] = s_count[1] = 0;
-          arrive_cluster(cluster_map(bar_ready + 8 * par, leader));
-        }
-        if (rank != leader) continue;
-        // (C is even: a CTA always leads with the same `par`, every C-th row)
-        await(bar_ready + 8 * par, (turn / C) & 1);
-        const uint32_t here = smem_addr(&s_slice);
-        if (p < 32) {
-          State q{-INFINITY, 0.f, 0.f};
-          if (lane < C) {
-            const uint32_t at = cluster_map(here, lane);
-            q.m = ld_cluster_f32(at);
-            q.s = ld_cluster_f32(at + 4);
-            q.c = ld_cluster_f32(at + 8);
-          }
-          warp_join(q, k);
-          if (lane == 0) finish(q);
-        }
-        // Only keys that reach the largest of the slices' K-th ones can be among the K best (and
-        // K of them do): these alone are ranked.
-        u64 floor_key = 0;
-        if (a.K > 0 && lane < C)
-          floor_key = ld_cluster_u64(
-              cluster_map(here + (uint32_t)offsetof(Slice, list), lane) + 8 * (a.K - 1));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          floor_key = umax(floor_key, __shfl_xor_sync(kAll, floor_key, o));
-        for (int i = p; i < C * a.K; i += kPost) {
-          const u64 c = ld_cluster_u64(
-              cluster_map(here + (uint32_t)offsetof(Slice, list), i / a.K) + 8 * (i % a.K));
-          if (c > 0 && c >= floor_key) s_cand[atomicAdd(&s_count[1], 1)] = c;
-        }
-        post_sync();
-        if (p < C) arrive_cluster(cluster_map(bar_free + 8 * par, p));
-        place = -1;
-        const int cands = s_count[1];  // at most 16 x 32
-        for (int i = p; i < max(cands, a.K); i += kPost) {
-          const u64 c = i < cands ? s_cand[i] : 0;
-          const int at = i < cands ? larger(s_cand, cands, c) : i;  // (past them: a row with NaN)
-          if (at < a.K) emit(a, row, at, c, k, s_out);
-        }
-        post_sync();
-        if (p == 0) s_count[1] = 0;
-      } else {
-        post_sync();
-        if (p == 0) s_count[0] = s_count[1] = 0;
-      }
+      post_sync();
+      if (p == 0) s_count[0] = s_count[1] = 0;
       if (place >= 0) emit(a, row, place, key, k, s_out);
-      auto logprob = [&](float v) { return (fmaf(v, k, -s_out[0]) - s_out[1]) * kLn2; };
-      if (p < a.C) a.logprobs[row * a.C + p] = logprob(given);
+      if (p < a.C) a.logprobs[row * a.C + p] = logprob_of(given, k, s_out);
       for (int i = p + kPost; i < a.C; i += kPost) {
         const int id = a.ids[row * a.C + i];
         a.logprobs[row * a.C + i] =
-            logprob(id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY);
+            logprob_of(id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
       }
     }
   }
-  cluster_sync();  // no CTA leaves while another may still reach its shared memory
 }
 
-// Clusters of c CTAs resident at once (cached per device).
-template <bool kBf16>
-int resident(int dev, int sms, int c) {
-  static std::atomic<int> cache[64][kMaxCluster + 1];
-  if (dev < 64) {
-    const int n = cache[dev][c].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c, 1);
-  cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = kSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, logprobs_kernel<kBf16>, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    n = 0;
-  }
-  if (n <= 0) n = c == 1 ? sms * kCtasPerSm : 0;
-  if (dev < 64) cache[dev][c].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// CTAs per row: the number that gets through the rows soonest, by rounds of resident clusters
-// times a round's time. A slice costs 0.72 ns per vector (a CTA's share of HBM) and a fixed
-// part, more of it across a cluster.
-template <bool kBf16>
-int row_ctas(int B, int V, int dev, int sms) {
-  const double nvec = V / (kBf16 ? 8 : 4);
-  int best = 1;
-  double best_ns = 1e300;
-  for (int c = 1; c <= kMaxCluster; c *= 2) {
-    const int n = resident<kBf16>(dev, sms, c);
-    if (n <= 0) continue;
-    const double ns = ((B + n - 1) / n) * (nvec / c * 0.72 + (c > 1 ? 4000.0 : 2500.0));
-    if (ns < best_ns) best_ns = ns, best = c;
-  }
-  return best;
+// CTAs per row of the kernel for few rows: as many as keep at least two vectors per thread and
+// one round of CTAs, at most 16 (a cluster).
+int few_ctas(int B, int V, bool bf16, int sms) {
+  const long long nvec = V / (bf16 ? 8 : 4);
+  int c = 1;
+  while (c < kMaxCluster && (long long)B * 2 * c <= 4ll * sms && nvec >= 2ll * kFew * (2 * c)) c *= 2;
+  return c;
 }
 
 template <bool kBf16>
 cudaError_t launch(const LogprobArgs &a, int B, cudaStream_t stream) {
-  static std::atomic<bool> ready[64];
   static std::atomic<int> sm_count[64];
-  int dev = 0, sms = 0;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+  int sms = dev < 64 ? sm_count[dev].load(std::memory_order_acquire) : 0;
+  if (sms == 0) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(logprobs_kernel<kBf16>,
+        (e = cudaFuncSetAttribute(logprobs_few_kernel<kBf16>,
                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
             cudaSuccess ||
-        (e = cudaFuncSetAttribute(logprobs_kernel<kBf16>,
+        (e = cudaFuncSetAttribute(logprobs_many_kernel<kBf16>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) !=
             cudaSuccess)
       return e;
-    if (dev < 64) {
-      sm_count[dev].store(sms, std::memory_order_relaxed);
-      ready[dev].store(true, std::memory_order_release);
-    }
-  } else {
-    sms = sm_count[dev].load(std::memory_order_relaxed);
+    if (dev < 64) sm_count[dev].store(sms, std::memory_order_release);
   }
-  const int c = row_ctas<kBf16>(B, a.V, dev, sms);
-  const int n = resident<kBf16>(dev, sms, c);
+  // A row of up to 160 KB, or more rows than SMs: a CTA a row. K = 8 fp32, us of this kernel and of
+  // the one for few rows: 32000 logits 7.9 and 7.0 (1 row), 7.8 and 8.6 (32); 131072 logits 16
+  // and 7 (1), 21 and 18 (128), 24 and 25 (192), 95 and 108 (1024).
+  if ((long long)a.V * (kBf16 ? 2 : 4) <= (160 << 10) || B > sms) {
+    const int grid = B < kCtasPerSm * sms ? B : kCtasPerSm * sms;
+    e = launch_pdl(logprobs_many_kernel<kBf16>, dim3(grid), kBlock, kSmem, stream, a, B);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  const int c = few_ctas(B, a.V, kBf16, sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c, B < n ? B : n);
-  cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.gridDim = dim3(c, B);
+  cfg.blockDim = dim3(kFew);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -747,7 +846,7 @@ cudaError_t launch(const LogprobArgs &a, int B, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, logprobs_kernel<kBf16>, a, B)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, logprobs_few_kernel<kBf16>, a)) != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
