@@ -146,7 +146,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _call(name: str, *args) -> None:
-    L = lib()
+    L = _lib or lib()
     st = getattr(L, name)(*args)
     if st != 0:
         raise DecAttnError(name, st, f"{L.dec_status_string(st).decode()}: {L.dec_last_error().decode()}")
@@ -201,6 +201,7 @@ def _need(t, name: str, dtype, shape=None, host: bool = False) -> None:
 
 BF16 = torch.bfloat16
 I32 = torch.int32
+F32 = torch.float32
 
 
 def _empty(shape, dtype, like):
@@ -645,9 +646,12 @@ def sample(logits, sampled_ids=None, penalty: float = 1.0, temperature: float = 
 
 
 # -------------------------------------------------------- log probabilities ---
+_NO_STREAM = contextlib.nullcontext()
+
+
 def _on(stream):
     """The stream a call's own tensors are made on: the one its kernels run on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0, vocab=None,
@@ -658,15 +662,14 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0
     outside the vocabulary), the entropy [B] in nats, and the ``top_k`` (at most 32) most
     probable ids [B, K] with their log probabilities, best first, equal ones by the lower id.
     What was not asked for is None."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, BF16):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (F32, BF16):
         raise TypeError("logits must be a float32 or bfloat16 torch.Tensor")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [B, ld], got {tuple(logits.shape)}")
-    B, ld = logits.shape
-    at = _at(logits, "logits", logits.dtype, (B, ld))
-    V = ld if vocab is None else int(vocab)
-    C, K = 0, int(top_k)
-    tokens_at = None
+    dtype = logits.dtype
+    B, ld = shape = logits.shape
+    at = _at(logits, "logits", dtype, shape)
+    C, K, tokens_at = 0, int(top_k), None
     if tokens is not None:
         if not isinstance(tokens, torch.Tensor):
             raise TypeError("tokens must be a torch.Tensor")
@@ -674,25 +677,23 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0
             raise ValueError(f"tokens must be [B, C], got {tuple(tokens.shape)}")
         C = tokens.shape[1]
         tokens_at = _at(tokens, "tokens", I32, (B, C), host=True)
-    if stream is None:
-        outs = _logprob_outputs(logits, B, C, K, tokens is not None, entropy)
-    else:
-        with torch.cuda.stream(stream):
-            outs = _logprob_outputs(logits, B, C, K, tokens is not None, entropy)
-    lp, ent, ids, top = outs
-    _call("dec_token_logprobs", at, 0 if logits.dtype is torch.float32 else 1, ld,
-          tokens_at if C else None, C, lp.data_ptr() if C else None,
-          ent.data_ptr() if entropy else None, ids.data_ptr() if K > 0 else None,
-          top.data_ptr() if K > 0 else None, K, B, V, temperature, _handle(stream))
-    return outs
-
-
-def _logprob_outputs(logits, B, C, K, given, entropy):
-    f32 = torch.float32
-    return (_empty((B, C), f32, logits) if given else None,
-            _empty((B,), f32, logits) if entropy else None,
-            _empty((B, K), I32, logits) if K > 0 else None,
-            _empty((B, K), f32, logits) if K > 0 else None)
+    dev, empty = logits.device, torch.empty
+    lp = ent = ids = top = lp_at = ent_at = ids_at = top_at = None
+    with _on(stream):  # (what is made here belongs to the stream its kernel runs on)
+        if tokens is not None:
+            lp = empty((B, C), dtype=F32, device=dev)
+            lp_at = lp.data_ptr()
+        if entropy:
+            ent = empty((B,), dtype=F32, device=dev)
+            ent_at = ent.data_ptr()
+        if K > 0:
+            ids = empty((B, K), dtype=I32, device=dev)
+            top = empty((B, K), dtype=F32, device=dev)
+            ids_at, top_at = ids.data_ptr(), top.data_ptr()
+    _call("dec_token_logprobs", at, 0 if dtype is F32 else 1, ld, tokens_at, C, lp_at, ent_at,
+          ids_at, top_at, K, B, ld if vocab is None else int(vocab), temperature,
+          _handle(stream))
+    return lp, ent, ids, top
 
 
 # -------------------------------------------------------------- draft trees ---

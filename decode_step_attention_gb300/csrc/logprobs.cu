@@ -24,12 +24,12 @@
 // against but found by the group's sum being NaN, and that group done again.
 //
 // Alternatives without a sort of the row: a value and its id form one 64-bit key, all
-// different. The K-th largest of the maxima of 32 (a cluster: up to 128) groups of threads
-// bounds the K-th largest key of the row from below (K = 8: about 9 of a CTA's threads reach
-// it), and only threads whose own maximum reaches it can hold a larger one. Those threads'
-// vectors are read again (from L2), a warp each; what reaches the bound goes into a list of the
-// warp's 32 largest, and a key's place is the number of larger ones among all the lists'. No
-// more than 32 keys per warp come through whatever the order of the values.
+// different. The K-th largest of the maxima of 32 or 128 groups of threads bounds the K-th
+// largest key of the row from below (K = 8: about 9 of a CTA's threads reach it), and only
+// threads whose own maximum reaches it can hold a larger one. Those threads' vectors are read
+// again (from L2), a warp each; what reaches the bound goes into a list of the warp's 32
+// largest, and a key's place is the number of larger ones among all the lists'. No more than
+// 32 keys per warp come through whatever the order of the values.
 #include <math.h>
 
 #include <atomic>
@@ -69,7 +69,6 @@ __device__ __forceinline__ float key_value(u64 k) {
 }
 
 __device__ __forceinline__ u64 umax(u64 a, u64 b) { return a > b ? a : b; }
-__device__ __forceinline__ u64 umin(u64 a, u64 b) { return a < b ? a : b; }
 
 // A key into a warp's list sorted downwards; the smallest falls off.
 __device__ __forceinline__ u64 warp_insert(u64 list, u64 key) {
@@ -412,7 +411,7 @@ constexpr int kMaxGroups = 128;  // of a row
 struct Slice {  // what a CTA keeps for the others of its cluster
   State sums[kFewWarps];
   int n;          // keys of `list`
-  u64 group[32];  // the largest keys of its groups of threads
+  u64 group[kMaxGroups];  // the largest keys of its groups of threads
   u64 list[32];   // its keys that reach the row's bound, at most K of them
 };
 
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
   if (end_id >= 0) run.single(end_value, end_id, k);
 
   // ---- the slice: every warp's sums, the largest keys of its groups of threads
-  const int per = min(32, kMaxGroups / C), groups = per * C;  // groups to a CTA, of the row
+  const int per = kMaxGroups / C, groups = kMaxGroups;  // groups to a CTA, of the row
   State st = run.sums;
   warp_join(st, k);
   if (lane == 0) s_slice.sums[warp] = st;
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
   __shared__ float4 s_sums[2][kThreads];  // (m, s, c) of a row's streaming threads
   __shared__ u64 s_keys[2][kThreads];     // and their largest keys (0: nothing seen)
   __shared__ State s_states[kPostWarps];
-  __shared__ u64 s_group[32], s_bound;    // the largest key of every 12 streaming threads
+  __shared__ u64 s_group[kPost], s_bound;  // the largest key of every 3 or 12 streaming threads
   __shared__ u64 s_cand[kPost];
   __shared__ float s_out[2];
   __shared__ int s_count[2];              // owners and candidates
@@ -720,9 +719,16 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
         st.join(State{x.x, x.y, x.z}, k);
       }
       if (!left) st.s = NAN;
+      // 32 groups, or 128 where K of 32 would be too low a bound (K = 32, 64000 fp32 logits: 130
+      // threads reach it against 37, 300 rows 55 us against 20)
+      const int groups = a.K <= 8 ? 32 : kPost;
+      if (a.K <= 8) {
 #pragma unroll
-      for (int o = 2; o > 0; o >>= 1) most = umax(most, __shfl_xor_sync(kAll, most, o));
-      if ((lane & 3) == 0) s_group[p >> 2] = most;
+        for (int o = 2; o > 0; o >>= 1) most = umax(most, __shfl_xor_sync(kAll, most, o));
+        if ((lane & 3) == 0) s_group[p >> 2] = most;
+      } else {
+        s_group[p] = most;
+      }
       warp_join(st, k);
       if (lane == 0) s_states[pw] = st;
       __syncwarp();
@@ -739,7 +745,7 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
       int place = -1;  // this thread's key's place among the row's best
       u64 key = 0;
       if (a.K > 0) {
-        if (p < 32 && s_group[p] > 0 && larger(s_group, 32, s_group[p]) == a.K - 1)
+        if (p < groups && s_group[p] > 0 && larger(s_group, groups, s_group[p]) == a.K - 1)
           s_bound = s_group[p];  // the K-th largest of the groups' keys
         post_sync();
         const u64 bound = s_bound;
