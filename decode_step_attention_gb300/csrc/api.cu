@@ -1221,6 +1221,10 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   if (!std::isfinite(scale)) return fail(DEC_ERR_INVALID_ARG, "scale must be finite");
   if (!(softcap >= 0.f) || !std::isfinite(softcap))
     return fail(DEC_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  const float score_scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
+  if (softcap > 0.f && !(score_scale / softcap < 1e30f))
+    return fail(DEC_ERR_INVALID_ARG, "softcap = %g is too small for a scale of %g", softcap,
+                score_scale);
   if (B == 0) return ok();
   if (!q || !k_cache || !v_cache || !lens || !k_tree || !v_tree || !mask || !out)
     return fail(DEC_ERR_INVALID_ARG,
@@ -1271,7 +1275,7 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   a.Hkv = Hkv;
   a.T_cap = T_cap;
   a.window = window;
-  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);
+  a.scale = score_scale;
   a.softcap = softcap;
   const cudaError_t e = launch_tree_attn(maps, a, B, D, parts, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gqa_tree_attn launch");

@@ -45,6 +45,7 @@ constexpr int kTile = 64;      // keys per tile
 constexpr int kRows = 128;     // query rows per tile (the MMA's M)
 constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
 constexpr int kSoftmax = 128;
+constexpr float kLargeCap = 256.f;
 constexpr float kRescale = 8.f;  // log2 of the growth of the maximum that moves it
 constexpr int kMaxRowTiles = kTreeMaxNodes * kSplitMaxG / kRows;
 // What beginning and ending a (pair, row tile) costs, in key tiles: the stream is cut by tiles
@@ -773,11 +774,28 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
           if constexpr (kMod) {
             if (a.softcap > 0.f) {
-              // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+              // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), off by about 2^-22 cap. That
+              // serves caps of the scores' size; a far larger one, which hardly bends them,
+              // takes the series of tanh below 0.3 (next term 9e-3 x^11).
               const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
+              if (a.softcap <= kLargeCap) {
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
-                z[c] = fmaf(-2.f * cap, rcp(1.f + ex2(z[c] * in)), cap);
+                for (int c = 0; c < NC; ++c)
+                  z[c] = fmaf(-2.f * cap, rcp(1.f + ex2(z[c] * in)), cap);
+              } else {
+                const float inv = a.scale / a.softcap;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                  const float x = z[c] * inv, x2 = x * x;
+                  const float near = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f,
+                                                                         -17.f / 315.f),
+                                                                2.f / 15.f),
+                                                       -1.f / 3.f),
+                                              1.f);
+                  const float far = fmaf(-2.f, rcp(1.f + ex2(z[c] * in)), 1.f);
+                  z[c] = cap * (fabsf(x) < 0.3f ? near : far);
+                }
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < NC; ++c) z[c] *= a.scale * log2e;

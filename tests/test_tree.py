@@ -151,6 +151,29 @@ def test_score_options(softcap, alibi, N):
     run(c, "with a window", softcap=softcap, slopes=slopes, window=150, scale=0.25)
 
 
+@pytest.mark.parametrize("softcap", [1e-6, 200.0, 300.0, 3000.0, 1e6])
+def test_caps_far_from_the_scores(softcap):
+    """A cap far below the scores levels them, one far above leaves them as they are."""
+    c = attn_case(21, [500, 90], 7, 8, 2, 128, scale=3.0)  # scores up to about 400
+    run(c, f"cap={softcap}", softcap=softcap)
+    run(c, f"cap={softcap}", softcap=softcap, scale=2.0)
+
+
+def test_one_node_is_the_single_token_attention():
+    """N = 1 against the framework's decode attention with the token in the cache."""
+    c = attn_case(22, [700, 63, 0], 1, 8, 2, 128, T=701)
+    g = on_gpu(c)
+    out = call(g, max_len=700)
+    kc, vc = g["k_cache"].clone(), g["v_cache"].clone()
+    for b, n in enumerate((700, 63, 0)):
+        kc[b, :, n], vc[b, :, n] = g["k_tree"][b, :, 0], g["v_tree"][b, :, 0]
+    want = dsa.gqa_decode_attn(g["q"][:, 0].contiguous(), kc, vc, g["lens"] + 1)
+    _, size = reference(c)
+    err = (out[:, 0].float() - want.float()).abs().cpu().numpy()
+    # both within the bound of the exact result: a bf16 rounding each, and this one's weights
+    assert np.all(err <= 2.0 ** -8 * (2 * np.abs(f64(want)) + 1.1 * size[:, 0]) + 2.0 ** -10 * size[:, 0])
+
+
 def test_nodes_that_see_nothing_give_zeros():
     c = attn_case(3, [0, 0, 100], 12, 4, 2, 128, empty=True)
     assert (c["mask"] == 0).any()

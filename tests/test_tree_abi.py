@@ -58,8 +58,8 @@ def test_tree_attn_rejects(L):
                     (dict(max_len=257), 1), (dict(max_len=-1), 1), (dict(parts=-1), 1),
                     (dict(parts=1 << 20), 2), (dict(window=-1), 1),
                     (dict(scale=float("nan")), 1), (dict(cap=-1.0), 1),
-                    (dict(cap=float("inf")), 1), (dict(q=None), 1), (dict(mask=None), 1),
-                    (dict(kt=None), 1), (dict(window=8), 1), (dict(slopes=at(10)), 1),
+                    (dict(cap=float("inf")), 1), (dict(cap=1e-38), 1), (dict(q=None), 1),
+                    (dict(mask=None), 1), (dict(kt=None), 1), (dict(window=8), 1), (dict(slopes=at(10)), 1),
                     (dict(kc=at(2, 8)), 1), (dict(mask=at(7, 4)), 1), (dict(lens=at(4, 2)), 1),
                     (dict(out=at(1, 256)), 1), (dict(ws=None), 3), (dict(ws=at(9, 16)), 3),
                     (dict(ws_bytes=16), 3), (dict(B=8000, T=1 << 20, max_len=1), 2)):
