@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return true;
     };
     // Rows of V that nobody may read can hold anything, and 0 times NaN is NaN: they are
-    // cleared in shared memory. 
+    // cleared in shared memory.
     auto clear_rows = [&](uint32_t v_s, int from) {
       for (int i = lane; i < (kTile - from) * (D / 8); i += 32) {
         const int r = from + i / (D / 8), ch = i % (D / 8);

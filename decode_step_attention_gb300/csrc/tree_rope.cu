@@ -51,8 +51,18 @@ __device__ __noinline__ void exact_elements(const __nv_bfloat16 *k, const __nv_b
 // Every load is in flight while the node's D/2 angles are formed in shared memory. The
 // arithmetic is that of rotate_head.cuh in another lane layout: the same sums in the same
 // order, so both give the same bits.
+//
+// A node's chain (position, angles, barrier, rotation, stores) is hidden by the other CTAs of
+// the SM, and the instructions, some 130 per 8 elements of a head and lane, take 70% of the
+// issue slots: 6144 nodes of 32 query and 8 KV heads of 128 (interleaved, normed), 114 MB,
+// in 26.8 us, 4.3 TB/s. With 8-byte lanes 105 us. Six CTAs per SM, at 40 registers, against
+// five at 48: 26.8 and 27.6 us, 16 query heads 20.7 and 22.0; one pass (a few nodes) and
+// four lose by it: 8 nodes 3.19 and 3.05 us, 64 query heads in four passes 47.7 and 46.9 (in
+// two CTAs of three 44.2). (The
+// packed products or a branch around the check for cancelling keys cost more in registers
+// than they save: 28.3 and 29.9 us.)
 template <int D, int P>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, P == 2 || P == 3 ? 6 : 5)
     tree_rope_kernel(const TreeRopeArgs a, const __grid_constant__ RopeTurns turns) {
   constexpr int kLanes = D / 8;           // lanes per head
   constexpr int kHeads = 32 / kLanes;     // heads per warp and pass
@@ -186,10 +196,15 @@ struct TreeCommitArgs {
   uint4 *k_cache, *v_cache;
   const int32_t *path, *n_path, *lens;
   uint32_t *error_word;
-  int N, Hkv, T_cap, vec;  // vec: 16-byte words per row
+  int N, Hkv, T_cap;
 };
 
-// One CTA per (sequence, KV head): the path's rows of K and V, 16 bytes per thread.
+// One CTA per (sequence, KV head): the path's rows of K and V, 16 bytes per thread, a thread's
+// next kAtOnce rows of each loaded before the first is stored. Bound by latency: the
+// count, the path's nodes and their rows follow one another. 256 sequences x 4 heads x 8 to 64
+// rows of 128, 34 MB: 7.2 us; one row at a time 9.0, four 8.9.
+constexpr int kAtOnce = 2;
+template <int D>
 __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeCommitArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
@@ -202,17 +217,38 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const TreeCommitA
     count = count < 0 ? 0 : a.N;
   }
   const size_t pair = (size_t)b * a.Hkv + g;
-  for (int i = threadIdx.x; i < count * a.vec; i += kThreads) {
-    const int r = i / a.vec, c = i - r * a.vec;
-    const int node = a.path[(size_t)b * a.N + r];
-    const long long slot = (long long)at + r;
-    if (node < 0 || node >= a.N || slot < 0 || slot >= a.T_cap) {
-      if (g == 0 && c == 0 && a.error_word != nullptr) atomicOr(a.error_word, kErrPosSkipped);
-      continue;
+  constexpr int kVec = D / 8;  // 16-byte words per row
+  const int words = count * kVec;
+  for (int first = threadIdx.x; first < words; first += kAtOnce * kThreads) {
+    size_t dst[kAtOnce];
+    uint4 k[kAtOnce], v[kAtOnce];
+    bool good[kAtOnce];
+    int node[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = first + u * kThreads;
+      node[u] = i < words ? a.path[(size_t)b * a.N + i / kVec] : -1;
     }
-    const size_t src = (pair * a.N + node) * a.vec + c, dst = (pair * a.T_cap + slot) * a.vec + c;
-    a.k_cache[dst] = a.k_tree[src];
-    a.v_cache[dst] = a.v_tree[src];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = first + u * kThreads, r = i / kVec, c = i - r * kVec;
+      const long long slot = (long long)at + r;
+      good[u] = node[u] >= 0 && node[u] < a.N && slot >= 0 && slot < a.T_cap;
+      if (good[u]) {
+        const size_t src = (pair * a.N + node[u]) * kVec + c;
+        dst[u] = (pair * a.T_cap + slot) * kVec + c;
+        k[u] = a.k_tree[src];
+        v[u] = a.v_tree[src];
+      } else if (i < words && g == 0 && c == 0 && a.error_word != nullptr) {
+        atomicOr(a.error_word, kErrPosSkipped);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (good[u]) {
+        a.k_cache[dst[u]] = k[u];
+        a.v_cache[dst[u]] = v[u];
+      }
   }
 }
 
@@ -238,7 +274,9 @@ cudaError_t launch_tree_rope(const void *q_in, void *q_out, const void *k_new, c
   while (passes < 4 && per * passes < heads &&
          (long long)B * N * ((heads + per * passes - 1) / (per * passes)) > 2ll * sms)
     ++passes;
-  const dim3 grid(N, (heads + per * passes - 1) / (per * passes), B);
+  const int blocks = (heads + per * passes - 1) / (per * passes);
+  passes = (heads + per * blocks - 1) / (per * blocks);  // the same for each block
+  const dim3 grid(N, blocks, B);
   const RopeTurns turns = make_rope_turns(D, inv);
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, kThreads, 0, stream, a, turns);
@@ -260,9 +298,9 @@ cudaError_t launch_tree_commit(const void *k_tree, const void *v_tree, const int
                                uint32_t *error_word, cudaStream_t stream) {
   const TreeCommitArgs a{static_cast<const uint4 *>(k_tree), static_cast<const uint4 *>(v_tree),
                          static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), path,
-                         n_path, lens, error_word, N, Hkv, T_cap, D / 8};
-  const cudaError_t e =
-      launch_pdl(tree_commit_kernel, dim3(Hkv, B), kThreads, 0, stream, a);
+                         n_path, lens, error_word, N, Hkv, T_cap};
+  const cudaError_t e = launch_pdl(D == 128 ? tree_commit_kernel<128> : tree_commit_kernel<64>,
+                                   dim3(Hkv, B), kThreads, 0, stream, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
