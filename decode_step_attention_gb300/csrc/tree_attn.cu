@@ -171,6 +171,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The smaller one; NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -225,6 +236,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr));
+}
 // NC fp32 columns of this thread's lane; NC / 2 packed ones back, zeros over the other
 // slices' part of the 32 packed columns.
 template <int NC>
@@ -236,6 +254,17 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t *r) {
     tmem_ld32(addr, r);
   } else {
     tmem_ld16_raw(addr, r);
+  }
+}
+template <int NC>
+__device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t *r) {
+  if constexpr (NC == 64) {
+    tmem_st32(addr, r);
+    tmem_st32(addr + 32, r + 32);
+  } else if constexpr (NC == 32) {
+    tmem_st32(addr, r);
+  } else {
+    tmem_st16(addr, r);
   }
 }
 template <int NC>
@@ -341,13 +370,17 @@ struct Waiter {
   }
 };
 
-// kMod: a score cap or a distance bias.
-template <int D, bool kMod>
+// What the scores go through: nothing, a distance bias, or a cap (and a bias where slopes are
+// given). Kernels of their own, for the registers and for the code that a tile runs through.
+enum Scores { kPlain, kBias, kCap };
+
+template <int D, Scores kScores>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_kernel(const __grid_constant__ TreeMaps maps, const TreeAttnArgs a, int B,
                      int mts, uint8_t *workspace) {
   using G = Geo<D>;
   constexpr int S = G::kStages;
+  constexpr bool kMod = kScores != kPlain;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_bar[2 * S + 10];
   __shared__ uint32_t s_tmem;
@@ -729,6 +762,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       float slope = 0.f;
       if constexpr (kMod)
         if (real && a.slopes != nullptr) slope = a.slopes[w.g * Gq + hi] * log2e;
+      // what the common transformation adds to keys 0 to 7 of any 8: the cap, and the bias from
+      // one to the next
+      uint64_t off2[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float cap = kScores == kCap ? a.softcap * log2e : 0.f;
+        off2[k] = pair_of(fmaf(slope, 2.f * k, cap), fmaf(slope, 2.f * k + 1.f, cap));
+      }
       float m = -INFINITY, l = 0.f;
       // the segment after this one, and its Q on the way into L2
       Walk after = w;
@@ -763,74 +804,128 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         tc_fence_after();
-        auto weights = [&](auto cols) {
+        // kMod: a tile whose keys need more than the common transformation gets its scores bent
+        // in tensor memory first, 8 keys at a time. Unrolled with the rest for every key, that
+        // code would not stay in the instruction caches (it cost the common tiles half their
+        // time).
+        const bool bent = (kScores == kCap && (a.softcap > kLargeCap || !all)) ||
+                          (kMod && tree && a.slopes != nullptr);
+        auto bend = [&](int from, int count) {
+          const float inv = a.scale / a.softcap;
+#pragma unroll 1
+          for (int c = from; c < from + count; c += 8) {
+            uint32_t raw[8];
+            tmem_ld8(p_addr + c, raw);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float z = __uint_as_float(raw[i]);
+              if (kScores == kCap) {
+                // tanh by its series below 0.3 (next term 9e-3 x^11): 1 - 2 / (1 + e^(2 x)) is off
+                // by about 2^-22 of 1, too much of a small x under a large cap
+                const float x = z * inv, x2 = x * x;
+                const float near =
+                    x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f, -17.f / 315.f),
+                                               2.f / 15.f),
+                                      -1.f / 3.f),
+                             1.f);
+                const float far = fmaf(-2.f, rcp(1.f + ex2(x * (2.f * log2e))), 1.f);
+                z = a.softcap * log2e * (fabsf(x) < 0.3f ? near : far);
+              } else {
+                z *= a.scale * log2e;
+              }
+              if (a.slopes != nullptr) {
+                const int j = c + i;  // the same in every lane of the warp
+                const int at = tree ? __shfl_sync(0xffffffffu, j < 32 ? npos[0] : npos[1], j & 31)
+                                    : t_abs + j;
+                if (!tree || j < w.s.live) z = fmaf(-slope, (float)(qpos - at), z);
+              }
+              raw[i] = __float_as_uint(z);
+            }
+            tmem_st8(p_addr + c, raw);
+          }
+          tmem_wait_st();
+        };
+        // With a cap a thread's keys go NC at a time, for the registers and the code's size; the
+        // chunks before the last wait in tensor memory for the maximum.
+        auto weights = [&](auto cols, int n_chunks) {
           constexpr int NC = decltype(cols)::value;
-          const int c0 = slice * NC;  // this thread's keys of the tile: [c0, c0 + NC)
+          const int chunks = kScores == kCap ? n_chunks : 1;
+          const int first = slice * NC;  // this thread's keys of the tile: from here on
+          if (kMod && bent) bend(first, chunks * NC);
           uint32_t raw[NC];
-          tmem_ld_cols<NC>(p_addr + c0, raw);
-          tmem_wait_ld();
-          float z[NC];
+          float z[NC], mx = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0;; ++ch) {
+            const int c0 = first + ch * NC;
+            tmem_ld_cols<NC>(p_addr + c0, raw);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
-          if constexpr (kMod) {
-            if (a.softcap > 0.f) {
-              // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), off by about 2^-22 cap. That
-              // serves caps of the scores' size; a far larger one, which hardly bends them,
-              // takes the series of tanh below 0.3 (next term 9e-3 x^11).
-              const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
-              if (a.softcap <= kLargeCap) {
+            for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
+            if constexpr (kMod) {
+              if (!bent) {
+                if constexpr (kScores == kCap) {
+                  // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), off by about 2^-20 cap
+                  // Four keys share a reciprocal, 1 / a = c (b d / (a c b d)). Past 2^30 the result
+                  // is the cap, and the product of four stays finite. (The row sees every
+                  // key here: one that is NaN may reach the other three.)
+                  const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
+                  const uint64_t in2 = pair_of(in, in), one2 = pair_of(1.f, 1.f);
+                  const uint64_t minus2 = pair_of(-2.f * cap, -2.f * cap);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                  z[c] = fmaf(-2.f * cap, rcp(1.f + ex2(z[c] * in)), cap);
-              } else {
-                const float inv = a.scale / a.softcap;
+                  for (int c = 0; c < NC; c += 4) {
+                    uint64_t d[2];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                  const float x = z[c] * inv, x2 = x * x;
-                  const float near = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f,
-                                                                         -17.f / 315.f),
-                                                                2.f / 15.f),
-                                                       -1.f / 3.f),
-                                              1.f);
-                  const float far = fmaf(-2.f, rcp(1.f + ex2(z[c] * in)), 1.f);
-                  z[c] = cap * (fabsf(x) < 0.3f ? near : far);
+                    for (int i = 0; i < 2; ++i) {
+                      float x0, x1;
+                      unpair(mul2(pair_of(z[c + 2 * i], z[c + 2 * i + 1]), in2), x0, x1);
+                      d[i] = add2(pair_of(ex2(min_nan(x0, 30.f)), ex2(min_nan(x1, 30.f))), one2);
+                    }
+                    float ac, bd;
+                    unpair(mul2(d[0], d[1]), ac, bd);
+                    const float r = rcp(ac * bd);
+                    const uint64_t part = pair_of(r * bd, r * ac);
+                    unpair(fma2(minus2, mul2(part, d[1]), off2[(c / 2) & 3]), z[c], z[c + 1]);
+                    unpair(fma2(minus2, mul2(part, d[0]), off2[(c / 2 + 1) & 3]), z[c + 2], z[c + 3]);
+                  }
+                } else {
+                  const uint64_t by2 = pair_of(a.scale * log2e, a.scale * log2e);
+#pragma unroll
+                  for (int c = 0; c < NC; c += 2)
+                    unpair(fma2(pair_of(z[c], z[c + 1]), by2, off2[(c / 2) & 3]), z[c], z[c + 1]);
+                }
+                if (kScores == kBias || a.slopes != nullptr) {
+                  // (slope times the key's place among 8 is in off2)
+                  const float far = (float)(qpos - t_abs - c0);
+                  const uint64_t slope2 = pair_of(-slope, -slope);
+#pragma unroll
+                  for (int c = 0; c < NC; c += 2)
+                    unpair(fma2(slope2, pair_of(far - (float)(c & ~7), far - (float)(c & ~7)),
+                                pair_of(z[c], z[c + 1])),
+                           z[c], z[c + 1]);
                 }
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < NC; ++c) z[c] *= a.scale * log2e;
             }
-            if (a.slopes != nullptr) {
-              if (!tree) {
-                const float far = (float)(qpos - t_abs - c0);
+            if (!all) {
+              const uint64_t mine = see >> c0;
+              const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) z[c] = fmaf(-slope, far - (float)c, z[c]);
-              } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                {
-                  const int j = c0 + c;  // the same in every lane of the warp
-                  const int at = __shfl_sync(0xffffffffu, j < 32 ? npos[0] : npos[1], j & 31);
-                  if (j < w.s.live) z[c] = fmaf(-slope, (float)(qpos - at), z[c]);
-                }
-              }
+              for (int c = 0; c < NC; ++c)
+                if (!(((c < 32 ? s0 : s1) >> (c & 31)) & 1u)) z[c] = -INFINITY;
             }
+            float m4[4] = {z[0], z[1], z[2], z[3]};  // four chains, for the latency
+#pragma unroll
+            for (int c = 4; c < NC; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
+                                          : fmaxf(m4[i], z[c + i]);
+            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
+            if (ch + 1 >= chunks) break;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) raw[c] = __float_as_uint(z[c]);
+            tmem_st_cols<NC>(p_addr + c0, raw);
           }
-          if (!all) {
-            const uint64_t mine = see >> c0;
-            const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!(((c < 32 ? s0 : s1) >> (c & 31)) & 1u)) z[c] = -INFINITY;
-          }
-          float m4[4] = {z[0], z[1], z[2], z[3]};  // four chains, for the latency
-#pragma unroll
-          for (int c = 4; c < NC; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
-                                        : fmaxf(m4[i], z[c + i]);
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
           const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : m;
@@ -852,29 +947,49 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          uint32_t pk[NC / 2];
           const uint64_t sc2 = pair_of(sc, sc), base2 = pair_of(-base, -base);
-          uint64_t l4[4] = {};
+          if (chunks > 1) tmem_wait_st();
+#pragma unroll 1
+          for (int ch = chunks - 1;; --ch) {
+            uint32_t pk[NC / 2];
+            uint64_t l4[4] = {};
 #pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            float x0, x1;
-            unpair(fma2(pair_of(z[c], z[c + 1]), sc2, base2), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            l4[(c / 2) & 3] = add2(l4[(c / 2) & 3], pair_of(p0, p1));
-            pk[c / 2] = pack_bf16x2(p0, p1);
+            for (int c = 0; c < NC; c += 2) {
+              float x0, x1;
+              unpair(fma2(pair_of(z[c], z[c + 1]), sc2, base2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              l4[(c / 2) & 3] = add2(l4[(c / 2) & 3], pair_of(p0, p1));
+              pk[c / 2] = pack_bf16x2(p0, p1);
+            }
+            float l0, l1;
+            unpair(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), l0, l1);
+            l += l0 + l1;
+            if (ch > 0) {  // P lies over the first chunks' scores: those are read before
+              tmem_ld_cols<NC>(p_addr + first + (ch - 1) * NC, raw);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
+            }
+            if constexpr (NC == 32) {
+              if (chunks > 1) {
+                tmem_st16(p_addr + ch * (NC / 2), pk);
+                if (ch > 0) continue;
+                break;
+              }
+            }
+            tmem_st_weights<NC>(p_addr, slice, pk);
+            break;
           }
-          float l0, l1;
-          unpair(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), l0, l1);
-          l += l0 + l1;
-          tmem_st_weights<NC>(p_addr, slice, pk);
           tmem_wait_st();
         };
         if (copies == 4) {
-          weights(std::integral_constant<int, 16>{});
+          weights(std::integral_constant<int, 16>{}, 1);
+        } else if (kScores == kCap) {
+          if (active) weights(std::integral_constant<int, 32>{}, 2 / copies);
         } else if (copies == 2) {
-          weights(std::integral_constant<int, 32>{});
+          weights(std::integral_constant<int, 32>{}, 1);
         } else if (active) {
-          weights(std::integral_constant<int, 64>{});
+          weights(std::integral_constant<int, 64>{}, 1);
         }
         tc_fence_before();
         mbar_arrive(bar_p + 8 * (n & 1));
@@ -1132,7 +1247,7 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspac
 
 inline int row_tiles(int N, int G) { return (N * G + kRows - 1) / kRows; }
 
-template <int D, bool kMod>
+template <int D, Scores kScores>
 cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts,
                    cudaStream_t stream) {
   static std::atomic<bool> ready[64];
@@ -1140,14 +1255,14 @@ cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(tree_attn_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(tree_attn_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Geo<D>::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
   }
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.error_word);
   const int mts = row_tiles(a.N, a.Hq / a.Hkv), records = B * a.Hkv * mts;
-  e = launch_pdl(tree_attn_kernel<D, kMod>, dim3(parts), kThreads, Geo<D>::kSmem, stream, maps, a,
+  e = launch_pdl(tree_attn_kernel<D, kScores>, dim3(parts), kThreads, Geo<D>::kSmem, stream, maps, a,
                  B, mts, ws);
   if (e != cudaSuccess || parts == 1) return e;
   const int rows = a.N * (a.Hq / a.Hkv) < kRows ? a.N * (a.Hq / a.Hkv) : kRows;
@@ -1178,12 +1293,11 @@ size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int D, int parts) {
 cudaError_t launch_tree_attn(const CUtensorMap *maps, const TreeAttnArgs &a, int B, int D,
                              int parts, cudaStream_t stream) {
   const TreeMaps m{maps[0], maps[1], maps[2], maps[3]};
-  const bool mod = a.softcap > 0.f || a.slopes != nullptr;
+  auto go = [&](auto fn) { return fn(m, a, B, parts, stream); };
   const cudaError_t e =
-      D == 128 ? (mod ? launch<128, true>(m, a, B, parts, stream)
-                      : launch<128, false>(m, a, B, parts, stream))
-               : (mod ? launch<64, true>(m, a, B, parts, stream)
-                      : launch<64, false>(m, a, B, parts, stream));
+      a.softcap > 0.f ? (D == 128 ? go(launch<128, kCap>) : go(launch<64, kCap>))
+      : a.slopes != nullptr ? (D == 128 ? go(launch<128, kBias>) : go(launch<64, kBias>))
+                            : (D == 128 ? go(launch<128, kPlain>) : go(launch<64, kPlain>));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
