@@ -258,13 +258,12 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t *r) {
 }
 template <int NC>
 __device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t *r) {
-  if constexpr (NC == 64) {
+  if constexpr (NC == 32) {
     tmem_st32(addr, r);
-    tmem_st32(addr + 32, r + 32);
-  } else if constexpr (NC == 32) {
-    tmem_st32(addr, r);
-  } else {
+  } else if constexpr (NC == 16) {
     tmem_st16(addr, r);
+  } else {
+    tmem_st8(addr, r);
   }
 }
 template <int NC>
@@ -605,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     // Rows of V that nobody may read can hold anything, and 0 times NaN is NaN: they are
     // cleared in shared memory.
-    auto clear_rows = [&](uint32_t v_s, int from) {
-      for (int i = lane; i < (kTile - from) * (D / 8); i += 32) {
+    auto clear_rows = [&](uint32_t v_s, int from, int to) {
+      for (int i = lane; i < (to - from) * (D / 8); i += 32) {
         const int r = from + i / (D / 8), ch = i % (D / 8);
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
                          v_s + (ch >> 3) * G::kSlab + r * 128 + ((ch & 7) << 4)),
@@ -618,8 +617,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     // single values that are not finite: the rows that do see those get them back at the end.
     // Returns their nodes.
     auto clear_tree = [&](uint32_t v_s, uint64_t used, int live) {
-      clear_rows(v_s, live);
+      clear_rows(v_s, live, a.N);  // (behind a.N the copy left zeros)
       uint64_t odd = 0;
+      if (used == bit_range(0, live)) {  // and most often all there is to do: 0 x is 0, or NaN
+        __nv_bfloat162 sum = __float2bfloat162_rn(0.f);
+#pragma unroll 8
+        for (int i = lane; i < live * (D / 8); i += 32) {
+          const int r = i / (D / 8), ch = i % (D / 8);
+          uint32_t x[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(v_s + (ch >> 3) * G::kSlab + r * 128 + ((ch & 7) << 4)));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sum = __hfma2(reinterpret_cast<const __nv_bfloat162 &>(x[k]),
+                          __float2bfloat162_rn(0.f), sum);
+        }
+        if (!__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) return odd;
+      }
 #pragma unroll 4
       for (int i = lane; i < live * (D / 8); i += 32) {
         const int r = i / (D / 8), ch = i % (D / 8);  // (any order within a row serves)
@@ -670,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint64_t odd = clear_tree(v_s, used, w.s.live);
             if (lane == 0) s_odd = odd;
           } else {
-            clear_rows(v_s, valid);
+            clear_rows(v_s, valid, kTile);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -811,9 +826,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const bool bent = (kScores == kCap && (a.softcap > kLargeCap || !all)) ||
                           (kMod && tree && a.slopes != nullptr);
         auto bend = [&](int from, int count) {
+          const int keys = tree ? w.s.live : w.s.L - t_abs;
           const float inv = a.scale / a.softcap;
 #pragma unroll 1
-          for (int c = from; c < from + count; c += 8) {
+          for (int c = from; c < min(from + count, keys); c += 8) {  // (the others are masked)
             uint32_t raw[8];
             tmem_ld8(p_addr + c, raw);
             tmem_wait_ld();
@@ -846,86 +862,79 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           tmem_wait_st();
         };
-        // With a cap a thread's keys go NC at a time, for the registers and the code's size; the
-        // chunks before the last wait in tensor memory for the maximum.
-        auto weights = [&](auto cols, int n_chunks) {
-          constexpr int NC = decltype(cols)::value;
-          const int chunks = kScores == kCap ? n_chunks : 1;
-          const int first = slice * NC;  // this thread's keys of the tile: from here on
-          if (kMod && bent) bend(first, chunks * NC);
+        // this thread's scores of the keys from c0 on, as the softmax takes them
+        auto scores = [&](auto &z, int c0) {
+          constexpr int NC = sizeof(z) / 4;
           uint32_t raw[NC];
-          float z[NC], mx = -INFINITY;
-#pragma unroll 1
-          for (int ch = 0;; ++ch) {
-            const int c0 = first + ch * NC;
-            tmem_ld_cols<NC>(p_addr + c0, raw);
-            tmem_wait_ld();
+          tmem_ld_cols<NC>(p_addr + c0, raw);
+          tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
-            if constexpr (kMod) {
-              if (!bent) {
-                if constexpr (kScores == kCap) {
-                  // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), off by about 2^-20 cap
-                  // Four keys share a reciprocal, 1 / a = c (b d / (a c b d)). Past 2^30 the result
-                  // is the cap, and the product of four stays finite. (The row sees every
-                  // key here: one that is NaN may reach the other three.)
-                  const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
-                  const uint64_t in2 = pair_of(in, in), one2 = pair_of(1.f, 1.f);
-                  const uint64_t minus2 = pair_of(-2.f * cap, -2.f * cap);
+          for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
+          if constexpr (kMod) {
+            if (!bent) {
+              if constexpr (kScores == kCap) {
+                // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap)), off by about 2^-20 cap
+                // Four keys share a reciprocal, 1 / a = c (b d / (a c b d)). Past 2^30 the result
+                // is the cap, and the product of four stays finite. (The row sees every
+                // key here: one that is NaN may reach the other three.)
+                const float in = 2.f * log2e * a.scale / a.softcap, cap = a.softcap * log2e;
+                const uint64_t in2 = pair_of(in, in), one2 = pair_of(1.f, 1.f);
+                const uint64_t minus2 = pair_of(-2.f * cap, -2.f * cap);
 #pragma unroll
-                  for (int c = 0; c < NC; c += 4) {
-                    uint64_t d[2];
+                for (int c = 0; c < NC; c += 4) {
+                  uint64_t d[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                      float x0, x1;
-                      unpair(mul2(pair_of(z[c + 2 * i], z[c + 2 * i + 1]), in2), x0, x1);
-                      d[i] = add2(pair_of(ex2(min_nan(x0, 30.f)), ex2(min_nan(x1, 30.f))), one2);
-                    }
-                    float ac, bd;
-                    unpair(mul2(d[0], d[1]), ac, bd);
-                    const float r = rcp(ac * bd);
-                    const uint64_t part = pair_of(r * bd, r * ac);
-                    unpair(fma2(minus2, mul2(part, d[1]), off2[(c / 2) & 3]), z[c], z[c + 1]);
-                    unpair(fma2(minus2, mul2(part, d[0]), off2[(c / 2 + 1) & 3]), z[c + 2], z[c + 3]);
+                  for (int i = 0; i < 2; ++i) {
+                    float x0, x1;
+                    unpair(mul2(pair_of(z[c + 2 * i], z[c + 2 * i + 1]), in2), x0, x1);
+                    d[i] = add2(pair_of(ex2(min_nan(x0, 30.f)), ex2(min_nan(x1, 30.f))), one2);
                   }
-                } else {
-                  const uint64_t by2 = pair_of(a.scale * log2e, a.scale * log2e);
-#pragma unroll
-                  for (int c = 0; c < NC; c += 2)
-                    unpair(fma2(pair_of(z[c], z[c + 1]), by2, off2[(c / 2) & 3]), z[c], z[c + 1]);
+                  float ac, bd;
+                  unpair(mul2(d[0], d[1]), ac, bd);
+                  const float r = rcp(ac * bd);
+                  const uint64_t part = pair_of(r * bd, r * ac);
+                  unpair(fma2(minus2, mul2(part, d[1]), off2[(c / 2) & 3]), z[c], z[c + 1]);
+                  unpair(fma2(minus2, mul2(part, d[0]), off2[(c / 2 + 1) & 3]), z[c + 2], z[c + 3]);
                 }
-                if (kScores == kBias || a.slopes != nullptr) {
-                  // (slope times the key's place among 8 is in off2)
-                  const float far = (float)(qpos - t_abs - c0);
-                  const uint64_t slope2 = pair_of(-slope, -slope);
+              } else {
+                const uint64_t by2 = pair_of(a.scale * log2e, a.scale * log2e);
 #pragma unroll
-                  for (int c = 0; c < NC; c += 2)
-                    unpair(fma2(slope2, pair_of(far - (float)(c & ~7), far - (float)(c & ~7)),
-                                pair_of(z[c], z[c + 1])),
-                           z[c], z[c + 1]);
-                }
+                for (int c = 0; c < NC; c += 2)
+                  unpair(fma2(pair_of(z[c], z[c + 1]), by2, off2[(c / 2) & 3]), z[c], z[c + 1]);
+              }
+              if (kScores == kBias || a.slopes != nullptr) {
+                // (slope times the key's place among 8 is in off2)
+                const float far = (float)(qpos - t_abs - c0);
+                const uint64_t slope2 = pair_of(-slope, -slope);
+#pragma unroll
+                for (int c = 0; c < NC; c += 2)
+                  unpair(fma2(slope2, pair_of(far - (float)(c & ~7), far - (float)(c & ~7)),
+                              pair_of(z[c], z[c + 1])),
+                         z[c], z[c + 1]);
               }
             }
-            if (!all) {
-              const uint64_t mine = see >> c0;
-              const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                if (!(((c < 32 ? s0 : s1) >> (c & 31)) & 1u)) z[c] = -INFINITY;
-            }
-            float m4[4] = {z[0], z[1], z[2], z[3]};  // four chains, for the latency
-#pragma unroll
-            for (int c = 4; c < NC; c += 8)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
-                                          : fmaxf(m4[i], z[c + i]);
-            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
-            if (ch + 1 >= chunks) break;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) raw[c] = __float_as_uint(z[c]);
-            tmem_st_cols<NC>(p_addr + c0, raw);
           }
+          if (!all) {
+            const uint64_t mine = see >> c0;
+            const uint32_t s0 = (uint32_t)mine, s1 = (uint32_t)(mine >> 32);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!(((c < 32 ? s0 : s1) >> (c & 31)) & 1u)) z[c] = -INFINITY;
+          }
+        };
+        auto largest = [&](const auto &z) {
+          constexpr int NC = sizeof(z) / 4;
+          float m4[4] = {z[0], z[1], z[2], z[3]};  // four chains, for the latency
+#pragma unroll
+          for (int c = 4; c < NC; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
+                                        : fmaxf(m4[i], z[c + i]);
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+        };
+        // the running maximum for a tile whose largest score is mx
+        auto settle = [&](float mx) {
           const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : m;
@@ -946,50 +955,87 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
           }
+        };
+        // the weights as bf16, their sum to l
+        auto weights = [&](const auto &z, auto &pk) {
+          constexpr int NC = sizeof(z) / 4;
           const float base = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pair_of(sc, sc), base2 = pair_of(-base, -base);
-          if (chunks > 1) tmem_wait_st();
-#pragma unroll 1
-          for (int ch = chunks - 1;; --ch) {
-            uint32_t pk[NC / 2];
-            uint64_t l4[4] = {};
+          uint64_t l4[4] = {};
 #pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-              float x0, x1;
-              unpair(fma2(pair_of(z[c], z[c + 1]), sc2, base2), x0, x1);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              l4[(c / 2) & 3] = add2(l4[(c / 2) & 3], pair_of(p0, p1));
-              pk[c / 2] = pack_bf16x2(p0, p1);
-            }
-            float l0, l1;
-            unpair(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), l0, l1);
-            l += l0 + l1;
-            if (ch > 0) {  // P lies over the first chunks' scores: those are read before
-              tmem_ld_cols<NC>(p_addr + first + (ch - 1) * NC, raw);
+          for (int c = 0; c < NC; c += 2) {
+            float x0, x1;
+            unpair(fma2(pair_of(z[c], z[c + 1]), sc2, base2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            l4[(c / 2) & 3] = add2(l4[(c / 2) & 3], pair_of(p0, p1));
+            pk[c / 2] = pack_bf16x2(p0, p1);
+          }
+          float l0, l1;
+          unpair(add2(add2(l4[0], l4[1]), add2(l4[2], l4[3])), l0, l1);
+          l += l0 + l1;
+        };
+        auto at_once = [&](auto cols) {
+          constexpr int NC = decltype(cols)::value;
+          float z[NC];
+          uint32_t pk[NC / 2];
+          if (kMod && bent) bend(slice * NC, NC);
+          scores(z, slice * NC);
+          settle(largest(z));
+          weights(z, pk);
+          tmem_st_weights<NC>(p_addr, slice, pk);
+          tmem_wait_st();
+        };
+        // With a cap a thread's keys go NC at a time, for the registers and the code's size: all but
+        // the first chunk wait in tensor memory for the maximum, and come back in order, since
+        // P lies over the first ones. NC divides the thread's kTile / copies keys.
+        auto in_chunks = [&](auto cols) {
+          constexpr int NC = decltype(cols)::value;
+          const int span = kTile / copies, first = slice * span;
+          float z[NC], mx = -INFINITY;
+          uint32_t raw[NC];
+          if (bent) bend(first, span);
+#pragma unroll 1
+          for (int c0 = span - NC;; c0 -= NC) {
+            scores(z, first + c0);
+            mx = fmaxf(mx, largest(z));
+            if (c0 <= 0) break;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) raw[c] = __float_as_uint(z[c]);
+            tmem_st_cols<NC>(p_addr + first + c0, raw);
+          }
+          settle(mx);
+          tmem_wait_st();
+#pragma unroll 1
+          for (int c0 = 0;; c0 += NC) {
+            uint32_t pk[NC / 2];
+            weights(z, pk);
+            const bool last = c0 + NC >= span;
+            if (!last) {
+              tmem_ld_cols<NC>(p_addr + first + c0 + NC, raw);
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < NC; ++c) z[c] = __uint_as_float(raw[c]);
             }
-            if constexpr (NC == 32) {
-              if (chunks > 1) {
-                tmem_st16(p_addr + ch * (NC / 2), pk);
-                if (ch > 0) continue;
-                break;
-              }
-            }
-            tmem_st_weights<NC>(p_addr, slice, pk);
-            break;
+            tmem_st_cols<NC / 2>(p_addr + (first + c0) / 2, pk);
+            if (last) break;
           }
+          const uint32_t zero[8] = {};
+#pragma unroll 1
+          for (int c = 0; copies > 1 && c < kTile / 2; c += 8)  // the other slices' part
+            if (2 * c / span != slice) tmem_st8(p_addr + c, zero);
           tmem_wait_st();
         };
-        if (copies == 4) {
-          weights(std::integral_constant<int, 16>{}, 1);
-        } else if (kScores == kCap) {
-          if (active) weights(std::integral_constant<int, 32>{}, 2 / copies);
+        if constexpr (kScores == kCap) {
+          if (copies == 4)
+            in_chunks(std::integral_constant<int, 16>{});
+          else if (active)
+            in_chunks(std::integral_constant<int, 32>{});
+        } else if (copies == 4) {
+          at_once(std::integral_constant<int, 16>{});
         } else if (copies == 2) {
-          weights(std::integral_constant<int, 32>{}, 1);
+          at_once(std::integral_constant<int, 32>{});
         } else if (active) {
-          weights(std::integral_constant<int, 64>{}, 1);
+          at_once(std::integral_constant<int, 64>{});
         }
         tc_fence_before();
         mbar_arrive(bar_p + 8 * (n & 1));
