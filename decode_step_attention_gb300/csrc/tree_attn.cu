@@ -750,6 +750,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       fence_proxy_async_smem();
       mbar_arrive(bar_q);
     };
+    // the same in two steps, the copies in flight between them
+    auto start_q = [&](const Walk &v) {
+      const int row = v.m * kRows + (tid & (kRows / copies_of(v.rows(Gq)) - 1)), node = row / Gq;
+      const bool real = node < v.s.live;
+      const __nv_bfloat16 *src = real ? q_row(v, row) : a.q;  // (16 bytes or none are read)
+      const int bytes = real ? 16 : 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         q_s + (c >> 3) * (kRows * 128) + tid * 128 + (((c ^ tid) & 7) << 4)),
+                     "l"(src + c * 8), "r"(bytes)
+                     : "memory");
+    };
+    auto finish_q = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(bar_q);
+    };
     load_q(w);
     bool more = true;
     while (more) {
@@ -862,6 +880,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           tmem_wait_st();
         };
+        // the last S of the segment is there: Q's space is free, unless a join needs it first
+        if (__builtin_expect(t + 1 == w.t1 && more && copies == 1, 0)) start_q(after);
         // this thread's scores of the keys from c0 on, as the softmax takes them
         auto scores = [&](auto &z, int c0) {
           constexpr int NC = sizeof(z) / 4;
@@ -1050,10 +1070,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         ++trees;
         odd = *reinterpret_cast<volatile unsigned long long *>(&s_odd);
       }
-      // every S of this segment has been read, so Q's space is free; P of the last tile must
-      // stay for the values to be given back
+      // the next segment's S may follow; P of the last tile must stay for the values to be given
+      // back
       const bool early_q = more && odd == 0 && copies == 1;
-      if (early_q) load_q(w);
+      if (early_q) finish_q();
       if (!wait_all(bar_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
       const bool whole = done.t0 == 0 && done.t1 == done.s.tiles;
@@ -1092,6 +1112,21 @@ __global__ void __launch_bounds__(kThreads, 2)
           st_v8(part + ((size_t)(col / 8) * kRows + my_row) * 8, v);
         }
       };
+      const bool aligned32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+      auto store16 = [&](int col, const float *v) {
+        if (whole && aligned32) {  // a sector at a time
+          uint32_t x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + col),
+                       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]),
+                       "r"(x[7])
+                       : "memory");
+        } else {
+          store8(col, v);
+          store8(col + 8, v + 8);
+        }
+      };
       if (copies == 1) {
         if (active) {
           const float scale = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -1106,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * scale;
             if (real) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) store8(c + i, v + i);
+              for (int i = 0; i < 32; i += 16) store16(c + i, v + i);
             }
             __syncwarp();
           }
@@ -1204,9 +1239,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                                    records_offset())[((size_t)done.b * a.Hkv + done.g) * mts + my_m] = r;
       }
       tc_fence_before();
-      if (more && !early_q) load_q(w);
+      if (more && !early_q) {
+        if (copies == 1)
+          finish_q();
+        else
+          load_q(w);
+      }
       ++seg;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that gave up)
   }
   tc_fence_before();
   __syncthreads();
