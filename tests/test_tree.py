@@ -159,6 +159,68 @@ def test_caps_far_from_the_scores(softcap):
     run(c, f"cap={softcap}", softcap=softcap, scale=2.0)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 20.0, 1000.0])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("N,G", [(8, 4), (9, 4), (16, 4), (17, 4), (64, 3)])
+def test_score_options_by_rows(D, softcap, alibi, N, G):
+    """Caps and biases where 4, 2 and 1 lanes share a row, over whole and ragged tiles."""
+    c = attn_case(N * G + D, [400, 64, 1, 130], N, 2 * G, 2, D, nodes=[N, N - 3, N, 1], scale=2.0)
+    slopes = torch.exp2(-torch.arange(1.0, 2 * G + 1)) if alibi else None
+    run(c, f"cap={softcap} alibi={alibi}", softcap=softcap, slopes=slopes)
+    run(c, "split", softcap=softcap, slopes=slopes, num_parts=5, window=200)
+
+
+@pytest.mark.parametrize("softcap,alibi", [(30.0, False), (30.0, True), (0.0, True), (1e4, False)])
+@pytest.mark.parametrize("N", [4, 12, 40])
+def test_bent_scores_of_unseen_keys_change_nothing(softcap, alibi, N):
+    c = attn_case(51, [90, 64], N, 8, 2, 128)
+    c["mask"][:, :] = 1 << torch.arange(N, dtype=torch.int64)
+    c["mask"][:, 3] |= 1 << 1
+    slopes = torch.exp2(-torch.arange(1.0, 9.0)) if alibi else None
+    clean = {k: v.clone() for k, v in c.items()}
+    c["k_tree"][1, 0, 1, 5] = NAN  # keys 0, 2 and 3 are computed next to it
+    ref, size = reference(clean, softcap=softcap, slopes=slopes)
+    got = f64(call(on_gpu(c), softcap=softcap, slopes=slopes if slopes is None else slopes.to(DEV)))
+    hit = np.zeros(got.shape, bool)
+    hit[1, [1, 3], :4] = True
+    check(torch.from_numpy(np.where(hit, ref, got)), ref, size)
+    assert int(np.isfinite(got[hit]).sum()) == 0
+    # a key in the cache that every node sees
+    c = {k: v.clone() for k, v in clean.items()}
+    c["k_cache"][0, 1, 13, 0] = NAN
+    got = f64(call(on_gpu(c), softcap=softcap, slopes=slopes if slopes is None else slopes.to(DEV)))
+    hit[:] = False
+    hit[0, :, 4:] = True
+    check(torch.from_numpy(np.where(hit, ref, got)), ref, size)
+    assert int(np.isfinite(got[hit]).sum()) == 0
+
+
+@pytest.mark.parametrize("softcap", [30.0, 1e4])
+@pytest.mark.parametrize("N", [3, 24])
+def test_scores_past_the_float_range_meet_the_cap(softcap, N):
+    """Dot products that overflow fp32: their tanh is 1 or -1."""
+    c = attn_case(52, [200], N, 8, 2, 128)
+    c["q"][:] = 1.0
+    c["k_cache"][0, :, 30] = 1e37
+    c["k_cache"][0, :, 190] = 1e37
+    c["k_cache"][0, :, 31] = -1e37
+    c["k_tree"][0, :, 1] = -1e37
+    run(c, softcap=softcap, scale=1.0)
+
+
+def test_results_at_odd_16_byte_addresses():
+    for N, D in ((40, 128), (40, 64), (9, 64)):
+        c = attn_case(53, [100, 20], N, 8, 2, D)
+        ref, size = reference(c)
+        room = torch.full((c["q"].numel() + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+        out = room[8:-8].view(c["q"].shape)
+        assert out.data_ptr() % 32 == 16
+        call(on_gpu(c), out=out)
+        check(out, ref, size)
+        assert (room[:8] == 7).all() and (room[-8:] == 7).all()
+
+
 def test_one_node_is_the_single_token_attention():
     """N = 1 against the framework's decode attention with the token in the cache."""
     c = attn_case(22, [700, 63, 0], 1, 8, 2, 128, T=701)
