@@ -26,6 +26,17 @@
 //            stay below 2^8, where bf16 rounds them as well as below 1.
 // Warps whose 32 rows are all past the tile's last row only keep the barriers company.
 //
+// Measured, with the merge (floor: bytes at the measured copy bandwidth, or operations at the
+// measured bf16 rate):
+//   131072 tokens, 26 nodes, 32 / 8 heads of 128       97 us (79); HBM, 6.0 TB/s in this kernel
+//   32 sequences to 8192, 16 nodes, cap                98 us (85); HBM
+//   192 sequences to 32768, one node, 16 / 4 of 64     74 us (59); S with 16 of 128 rows in use
+//   16 sequences, window 4095, 64 nodes, 64 / 8 of 128 124 us (62); the tensor cores: an S with 64
+//       keys takes as long as one with 128, because Q is read from shared memory for each
+// Tried for the last: S for two key tiles at once. It needs both S buffers, so S, softmax and the
+// value products of a CTA take turns, and two CTAs do not fill the gaps (144 us). Eight softmax
+// warps of half a row's keys each, which agree on the maximum tile by tile: 171 us.
+//
 // The weights are rounded to bf16 (one rounding, at most 2^-8 of each, as large as the
 // output's own rounding) because the value product wants both operands alike; sums, maxima
 // and O are fp32.
@@ -49,7 +60,9 @@ constexpr float kLargeCap = 256.f;
 constexpr float kRescale = 8.f;  // log2 of the growth of the maximum that moves it
 constexpr int kMaxRowTiles = kTreeMaxNodes * kSplitMaxG / kRows;
 // What beginning and ending a (pair, row tile) costs, in key tiles: the stream is cut by tiles
-// plus this, so that CTAs with many short sequences finish with the others.
+// plus this, so that CTAs with many short sequences finish with the others. (Short single-token
+// sequences of 64 dims: 3 78.6 us, 4 74.7, 6 73.7; wide trees 128.1, 124.9, 123.9; one long
+// sequence, cut evenly by any, 94.9, 95.4, 97.1.)
 constexpr int kSegment = 6;
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCol = 2 * kTile;  // S/P buffers in columns [0, 128), O behind them
@@ -370,7 +383,9 @@ struct Waiter {
 };
 
 // What the scores go through: nothing, a distance bias, or a cap (and a bias where slopes are
-// given). Kernels of their own, for the registers and for the code that a tile runs through.
+// given). Kernels of their own, for the registers and for the code that a tile runs through: what
+// does not stay in the instruction caches costs more than it computes. (171 sequences of 56 to
+// 226 tokens, 47 nodes, cap and bias: 106 us with everything in one kernel, 80 now.)
 enum Scores { kPlain, kBias, kCap };
 
 template <int D, Scores kScores>
@@ -1260,7 +1275,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Joins the partials of the (pair, row tile)s that cross pieces: out = sum_c 2^(m_c - M) O_c /
 // sum_c 2^(m_c - M) l_c. CTA (x, y) takes kRowsPer rows of row tile x, a thread per (row, 8
 // dims, every kGroups-th piece): 8 rows where a few long row tiles are cut into many pieces,
-// 32 where many are cut in two.
+// 32 where many are cut in two. Attention and merge, us with 8 and with 32 rows, by pieces per
+// row tile: 38 97 and 120; 13 71 and 81; 7.6 59 and 64; 4.2 54 and 57, 60.0 and 60.4; 2.1
+// 109 and 108, 92 and 88; 0.6 141 and 124.
 template <int D, int kRowsPer>
 __global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspace, int mts,
                                                          int records, int parts,
@@ -1353,7 +1370,7 @@ cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts
                  B, mts, ws);
   if (e != cudaSuccess || parts == 1) return e;
   const int rows = a.N * (a.Hq / a.Hkv) < kRows ? a.N * (a.Hq / a.Hkv) : kRows;
-  if (parts >= 8 * records)
+  if (parts >= 4 * records)
     return launch_pdl(tree_merge_kernel<D, 8>, dim3(records, (rows + 7) / 8), 512, 0, stream,
                       (const uint8_t *)ws, mts, records, parts, a);
   return launch_pdl(tree_merge_kernel<D, 32>, dim3(records, (rows + 31) / 32), 512, 0, stream,
