@@ -28,10 +28,10 @@
 //
 // Measured, with the merge (floor: bytes at the measured copy bandwidth, or operations at the
 // measured bf16 rate):
-//   131072 tokens, 26 nodes, 32 / 8 heads of 128       97 us (79); HBM, 6.0 TB/s in this kernel
-//   32 sequences to 8192, 16 nodes, cap                98 us (85); HBM
-//   192 sequences to 32768, one node, 16 / 4 of 64     74 us (59); S with 16 of 128 rows in use
-//   16 sequences, window 4095, 64 nodes, 64 / 8 of 128 124 us (62); the tensor cores: an S with 64
+//   131072 tokens, 26 nodes, 32 / 8 heads of 128       98 us (79); HBM, 6.0 TB/s in this kernel
+//   32 sequences to 8192, 16 nodes, cap                100 us (85); HBM
+//   192 sequences to 32768, one node, 16 / 4 of 64     75 us (59); S with 16 of 128 rows in use
+//   16 sequences, window 4095, 64 nodes, 64 / 8 of 128 126 us (62); the tensor cores: an S with 64
 //       keys takes as long as one with 128, because Q is read from shared memory for each
 // Tried for the last: S for two key tiles at once. It needs both S buffers, so S, softmax and the
 // value products of a CTA take turns, and two CTAs do not fill the gaps (144 us). Eight softmax
@@ -433,11 +433,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&maps.vt);
   }
   if (warp == 4) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+  // the lengths and node counts, 32 to a line, on their way into L2
+  if (tid * 32 < B) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lens + tid * 32));
+    if (a.n_nodes != nullptr) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.n_nodes + tid * 32));
+  }
+  pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // No kernel that may still run when this one starts writes lengths, node counts, masks or
-  // positions (only this library's kernels let a successor start early), so the piece is found
-  // before the wait for it.
   // ---- where this CTA's piece begins: the units of every row tile m, the CTAs each m gets in
   // proportion, and a scan over the sequences for this CTA's m. Up to 32 sequences every warp
   // scans for itself, a lane each.
@@ -546,13 +549,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (idle) {
     if (warp == 4) tmem_dealloc(tmem, kTmemCols);
-    pdl_wait_prior_grid();  // a grid is not done before the one it follows
     return;
   }
   const int Gq = a.Hq / a.Hkv;
   const int records = B * a.Hkv * mts;
   const Waiter wait{&s_abort, a.error_word};
-  pdl_wait_prior_grid();
 
   if (warp == 4) {
     // ---------------------------------------------------------------- loads

@@ -42,8 +42,7 @@
  *     successor start early, and none of them writes a length array or a projection
  *     weight, so the attention kernels read `lens` (and prefetch their first cache
  *     tiles into L2), and the projections request their first weight tiles, before
- *     that wait; dec_gqa_tree_attn reads `lens` and `n_nodes` before it, which no kernel of
- *     the library writes either. Anything else a call reads or writes waits for it.
+ *     that wait. Anything else a call reads or writes waits for it.
  */
 #ifndef DECATTN_H_
 #define DECATTN_H_
@@ -591,7 +590,8 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
  * slopes         [device|host] fp32 [Hq] or NULL.
  * out            [device|host] bf16 [B, N, Hq, D], not overlapping q.
  * max_len        host upper bound of every lens[b], 0 <= max_len <= T_cap.
- * scale          <= 0 selects 1/sqrt(D).  softcap >= 0, scale / softcap < 1e30.  window >= 0.
+ * scale          <= 0 selects 1/sqrt(D).  0 <= softcap <= 1e30, scale / softcap < 1e30.
+ *                window >= 0.
  * num_parts      CTAs the work is cut over; 0 lets the library choose.
  * workspace      [device] at least dec_tree_attn_workspace_bytes(...) bytes, 256-byte aligned,
  *                its first 256 bytes zeroed before its first use (the first word is the

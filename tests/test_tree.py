@@ -159,6 +159,14 @@ def test_caps_far_from_the_scores(softcap):
     run(c, f"cap={softcap}", softcap=softcap, scale=2.0)
 
 
+@pytest.mark.parametrize("softcap", [255.0, 257.0, 1e20, 1e30])
+@pytest.mark.parametrize("N", [7, 40])
+def test_the_largest_caps_leave_the_scores(softcap, N):
+    c = attn_case(54, [200, 64], N, 8, 2, 64)
+    run(c, f"cap={softcap}", softcap=softcap)
+    run(c, "no cap", softcap=softcap, slopes=torch.full((8,), 0.125))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("softcap", [0.0, 20.0, 1000.0])
 @pytest.mark.parametrize("alibi", [False, True])

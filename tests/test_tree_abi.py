@@ -72,6 +72,18 @@ def test_tree_attn_rejects(L):
     assert L.dec_tree_attn_workspace_bytes(2, 4, 7, 2, 128, 256, 3) == 0
 
 
+def test_tree_attn_rejects_caps_beyond_the_float_range(L):
+    for cap, st in ((1.1e30, 1), (3e38, 1), (float("nan"), 1)):
+        got, msg = _st(L, "dec_gqa_tree_attn", at(1), at(2), at(3), at(4), at(5), at(6), at(7), None,
+                       None, None, at(8), 2, 4, 8, 2, 128, 256, 256, 0.0, cap, 0, 3, at(9), 1 << 40,
+                       None)
+        assert got == st and "softcap" in msg, (cap, got, msg)
+    # a cap that is allowed is refused for something else
+    got, msg = _st(L, "dec_gqa_tree_attn", at(1), at(2), at(3), at(4), at(5), at(6), at(7), None, None,
+                   None, at(8), 2, 4, 8, 2, 128, 256, 256, 0.0, 1e30, 0, 3, None, 1 << 40, None)
+    assert got == 3 and "workspace" in msg
+
+
 def test_tree_commit_rejects(L):
     def call(B=2, N=4, Hkv=2, D=128, T=256, kt=at(1), vt=at(2), path=at(3), n=at(4), kc=at(5),
              vc=at(6), lens=at(7), err=None):
