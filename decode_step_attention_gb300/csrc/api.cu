@@ -1277,7 +1277,9 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   a.window = window;
   a.scale = score_scale;
   a.softcap = softcap;
-  const cudaError_t e = launch_tree_attn(maps, a, B, D, parts, as_stream(stream));
+  const int ctas =
+      tree_join_ctas(B, N, Hq, Hkv, max_len, window, num_parts, sm_count_of_current());
+  const cudaError_t e = launch_tree_attn(maps, a, B, D, parts, ctas, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gqa_tree_attn launch");
   return ok();
 }

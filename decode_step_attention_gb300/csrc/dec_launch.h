@@ -204,10 +204,12 @@ constexpr int kTreeMaxParts = 4096;
 // CTAs the attention's work is cut over (num_parts > 0: that many) and the workspace they need.
 int tree_parts(int B, int N, int Hq, int Hkv, int max_len, int num_parts, int sms);
 size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int D, int parts);
+// CTAs per (sequence, KV head, 128 rows) of the one-launch form for short contexts; 0: not that one.
+int tree_join_ctas(int B, int N, int Hq, int Hkv, int max_len, int window, int num_parts, int sms);
 // maps: k_cache, v_cache, k_tree, v_tree as [B * Hkv, rows, D], boxes of 64 dims x 64 rows,
 // 128-byte swizzle.
 cudaError_t launch_tree_attn(const CUtensorMap *maps, const TreeAttnArgs &a, int B, int D,
-                             int parts, cudaStream_t stream);
+                             int parts, int ctas, cudaStream_t stream);
 
 // ---- log probabilities -------------------------------------------------------------
 constexpr int kLogprobMaxK = 32;

@@ -15,6 +15,9 @@
 // one per CTA (two CTAs per SM); a (pair, row tile) that crosses pieces leaves a partial
 // (unnormalised O, running maximum and sum) per piece, which tree_merge_kernel joins.
 //
+// Short contexts take one launch instead: a (pair, row tile) is a CTA's, or a cluster's, which joins
+// its partials through distributed shared memory (kJoin).
+//
 // Inside a CTA, per key tile:
 //   warp 4   loads the K and V tiles (TMA, 128-byte swizzle) into a ring of shared memory;
 //   warp 5   issues S = Q K^T (both operands in shared memory) into one of two tensor-memory
@@ -364,6 +367,33 @@ __device__ __forceinline__ void st_v8(float *p, const float *r) {
                : "memory");
 }
 
+// ---- clusters ----------------------------------------------------------------------------
+constexpr int kJoinCtas = 8;  // CTAs of a cluster at most
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void ld_cluster_f32x2(uint32_t addr, float &x, float &y) {
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ld_cluster_f32x4(uint32_t addr, float (&x)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+               : "r"(addr)
+               : "memory");
+}
+// Where 4 columns of a row of a CTA's partial lie: a row's chunks in an order of its own, so that
+// neither rows nor columns meet in a bank.
+template <int D>
+__device__ __forceinline__ uint32_t part_at(int row, int chunk) {
+  return (uint32_t)((row * (D / 4) + (chunk ^ (row & (D / 4 - 1)))) * 16);
+}
+
 struct TreeMaps {
   CUtensorMap k, v, kt, vt;
 };
@@ -388,10 +418,12 @@ struct Waiter {
 // 226 tokens, 47 nodes, cap and bias: 106 us with everything in one kernel, 80 now.)
 enum Scores { kPlain, kBias, kCap };
 
-template <int D, Scores kScores>
+// kJoin: short contexts in one launch. A cluster of CTAs has a (pair, row tile) to itself, its tiles
+// dealt out evenly, and joins its partials through distributed shared memory.
+template <int D, Scores kScores, bool kJoin>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_kernel(const __grid_constant__ TreeMaps maps, const TreeAttnArgs a, int B,
-                     int mts, uint8_t *workspace) {
+                     int mts_or_ctas, uint8_t *workspace) {
   using G = Geo<D>;
   constexpr int S = G::kStages;
   constexpr bool kMod = kScores != kPlain;
@@ -409,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t bar_s = bar_empty + 8 * S, bar_p = bar_s + 16, bar_pv = bar_p + 16;
   const uint32_t bar_q = bar_pv + 16, bar_end = bar_q + 8, bar_x = bar_end + 8, bar_v = bar_x + 8;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int P = gridDim.x, piece = blockIdx.x;
+  const int P = gridDim.x, piece = blockIdx.x, mts = kJoin ? mts_or_ctas & 255 : mts_or_ctas;
 
   if (tid == 5 * 32) {  // (the warps begin with different things)
     for (int i = 0; i < 2 * S; ++i) mbar_init(bar_full + 8 * i, 1);
@@ -441,111 +473,131 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // ---- where this CTA's piece begins: the units of every row tile m, the CTAs each m gets in
-  // proportion, and a scan over the sequences for this CTA's m. Up to 32 sequences every warp
-  // scans for itself, a lane each.
-  const bool few = B <= 32;
-  const int per = few ? 1 : (B + kThreads - 1) / kThreads;
-  const int b_first = few ? lane : tid * per;
-  int mine[kMaxRowTiles] = {}, m_total[kMaxRowTiles], m_before[kMaxRowTiles] = {};
-  for (int b = b_first; b < min(B, b_first + per); ++b) {
-    const Seq s = seq_of(a, b, piece == 0 && (!few || warp == 0));
+  int p0 = 0, blk = 1;
+  if constexpr (!kJoin) {
+    // ---- where this CTA's piece begins: the units of every row tile m, the CTAs each m gets in
+    // proportion, and a scan over the sequences for this CTA's m. Up to 32 sequences every warp
+    // scans for itself, a lane each.
+    const bool few = B <= 32;
+    const int per = few ? 1 : (B + kThreads - 1) / kThreads;
+    const int b_first = few ? lane : tid * per;
+    int mine[kMaxRowTiles] = {}, m_total[kMaxRowTiles], m_before[kMaxRowTiles] = {};
+    for (int b = b_first; b < min(B, b_first + per); ++b) {
+      const Seq s = seq_of(a, b, piece == 0 && (!few || warp == 0));
+#pragma unroll
+      for (int m = 0; m < kMaxRowTiles; ++m)
+        if (m < s.mt) mine[m] += (s.tiles + kSegment) * a.Hkv;
+    }
 #pragma unroll
     for (int m = 0; m < kMaxRowTiles; ++m)
-      if (m < s.mt) mine[m] += (s.tiles + kSegment) * a.Hkv;
-  }
+      m_total[m] = m < mts ? __reduce_add_sync(0xffffffffu, mine[m]) : 0;
+    if (!few) {
 #pragma unroll
-  for (int m = 0; m < kMaxRowTiles; ++m)
-    m_total[m] = m < mts ? __reduce_add_sync(0xffffffffu, mine[m]) : 0;
-  if (!few) {
+      for (int m = 0; m < kMaxRowTiles; ++m)
+        if (lane == 0) s_sum[warp][m] = m_total[m];
+      __syncthreads();
 #pragma unroll
-    for (int m = 0; m < kMaxRowTiles; ++m)
-      if (lane == 0) s_sum[warp][m] = m_total[m];
-    __syncthreads();
+      for (int m = 0; m < kMaxRowTiles; ++m) {
+        m_total[m] = 0;
 #pragma unroll
-    for (int m = 0; m < kMaxRowTiles; ++m) {
-      m_total[m] = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) m_before[m] += s_sum[w][m];
-        m_total[m] += s_sum[w][m];
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w < warp) m_before[m] += s_sum[w][m];
+          m_total[m] += s_sum[w][m];
+        }
       }
     }
-  }
-  int my_m = -1, p0 = 0, total = 0, pieces = P, before = 0, count = 0;
-  if (mts == 1) {
-    my_m = 0;
-    total = m_total[0];
-    before = m_before[0];
-    count = mine[0];
-  } else {
-    long long all = 0;
+    int my_m = -1, total = 0, pieces = P, before = 0, count = 0;
+    if (mts == 1) {
+      my_m = 0;
+      total = m_total[0];
+      before = m_before[0];
+      count = mine[0];
+    } else {
+      long long all = 0;
 #pragma unroll
-    for (int m = 0; m < kMaxRowTiles; ++m) all += m_total[m];
-    int at = 0;
+      for (int m = 0; m < kMaxRowTiles; ++m) all += m_total[m];
+      int at = 0;
 #pragma unroll
-    for (int m = 0; m < kMaxRowTiles; ++m)
-      if (m < mts) {
-        const int n = 1 + (all > 0 ? (int)((long long)(P - mts) * m_total[m] / all) : 0);
-        if (piece >= at && piece < at + n) {
-          my_m = m;
-          p0 = at;
-          pieces = n;
-          total = m_total[m];
-          before = m_before[m];
-          count = mine[m];
+      for (int m = 0; m < kMaxRowTiles; ++m)
+        if (m < mts) {
+          const int n = 1 + (all > 0 ? (int)((long long)(P - mts) * m_total[m] / all) : 0);
+          if (piece >= at && piece < at + n) {
+            my_m = m;
+            p0 = at;
+            pieces = n;
+            total = m_total[m];
+            before = m_before[m];
+            count = mine[m];
+          }
+          at += n;
         }
-        at += n;
-      }
-  }
-  const int blk = max(1, (total + pieces - 1) / pieces);
-  const int r0 = (int)min((long long)total, (long long)(piece - p0) * blk);
-  const int units = min(blk, total - r0);
-  bool idle = my_m < 0 || units <= 0;  // past the end of the stream
-  int incl = count;
+    }
+    blk = max(1, (total + pieces - 1) / pieces);
+    const int r0 = (int)min((long long)total, (long long)(piece - p0) * blk);
+    const int units = min(blk, total - r0);
+    const bool none = my_m < 0 || units <= 0;  // past the end of the stream
+    int incl = count;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const int excl = before + incl - count;
-  const bool here = !idle && excl <= r0 && r0 < excl + count;
-  if (few) {
-    const unsigned who = __ballot_sync(0xffffffffu, here);
-    const int b = who != 0 ? __ffs(who) - 1 : 0;
-    const int at = __shfl_sync(0xffffffffu, excl, b);
-    if (tid == 0) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int excl = before + incl - count;
+    const bool here = !none && excl <= r0 && r0 < excl + count;
+    if (few) {
+      const unsigned who = __ballot_sync(0xffffffffu, here);
+      const int b = who != 0 ? __ffs(who) - 1 : 0;
+      const int at = __shfl_sync(0xffffffffu, excl, b);
+      if (tid == 0) {
+        s_begin[0] = b;
+        s_begin[1] = r0 - at;
+      }
+    } else if (here) {
+      int at = excl, b = b_first;
+      for (;; ++b) {
+        const Seq s = seq_of(a, b, false);
+        const int u = my_m < s.mt ? (s.tiles + kSegment) * a.Hkv : 0;
+        if (r0 < at + u) break;
+        at += u;
+      }
       s_begin[0] = b;
       s_begin[1] = r0 - at;
     }
-  } else if (here) {
-    int at = excl, b = b_first;
-    for (;; ++b) {
-      const Seq s = seq_of(a, b, false);
-      const int u = my_m < s.mt ? (s.tiles + kSegment) * a.Hkv : 0;
-      if (r0 < at + u) break;
-      at += u;
+    // through shared memory, so that the compiler knows them to be the same in every lane (an
+    // MMA issued with operands that might differ costs several times as much)
+    if (tid == 0) {
+      s_begin[2] = units;
+      s_begin[3] = my_m;
+      s_begin[4] = r0;
     }
-    s_begin[0] = b;
-    s_begin[1] = r0 - at;
-  }
-  // through shared memory, so that the compiler knows them to be the same in every lane (an
-  // MMA issued with operands that might differ costs several times as much)
-  if (tid == 0) {
-    s_begin[2] = units;
-    s_begin[3] = my_m;
-    s_begin[4] = r0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-  idle = s_begin[3] < 0 || s_begin[2] <= 0;
   Walk w;
-  if (!idle) {
-    w.begin(a, s_begin[0], s_begin[1], s_begin[2], s_begin[3], s_begin[4]);
-    // a piece of nothing but the units before a first tile; the next one begins it
-    if (w.t0 == w.t1) idle = true;
+  bool idle, empty = false;  // empty: no tiles, but a cluster to join
+  int rank = 0, ctas = 1;
+  if constexpr (kJoin) {
+    ctas = mts_or_ctas >> 8;
+    rank = piece % ctas;
+    const int pair = piece / ctas / mts;
+    w.m = piece / ctas % mts;
+    w.b = pair / a.Hkv;
+    w.g = pair - w.b * a.Hkv;
+    w.s = seq_of(a, w.b, tid == 0 && rank == 0 && w.m == 0 && w.g == 0);
+    w.t0 = w.s.tiles * rank / ctas;
+    w.t1 = w.s.tiles * (rank + 1) / ctas;
+    w.left = w.off = 0;
+    idle = w.m >= w.s.mt;  // all of the cluster
+    empty = w.t0 == w.t1;
+  } else {
+    idle = s_begin[3] < 0 || s_begin[2] <= 0;
+    if (!idle) {
+      w.begin(a, s_begin[0], s_begin[1], s_begin[2], s_begin[3], s_begin[4]);
+      // a piece of nothing but the units before a first tile; the next one begins it
+      if (w.t0 == w.t1) idle = true;
+    }
   }
   if (idle) {
     if (warp == 4) tmem_dealloc(tmem, kTmemCols);
@@ -554,8 +606,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int Gq = a.Hq / a.Hkv;
   const int records = B * a.Hkv * mts;
   const Waiter wait{&s_abort, a.error_word};
+  const bool split = kJoin && ctas > 1;  // this (pair, row tile) over a cluster
 
-  if (warp == 4) {
+  if (empty) {
+    if (tid < kRows) s_ml[tid] = make_float2(-INFINITY, 0.f);
+  } else if (warp == 4) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       int it = 0;
@@ -1092,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (early_q) finish_q();
       if (!wait_all(bar_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
       tc_fence_after();
-      const bool whole = done.t0 == 0 && done.t1 == done.s.tiles;
+      const bool whole = kJoin ? !split : done.t0 == 0 && done.t1 == done.s.tiles;
       const int slot = 2 * piece + (done.t0 > 0 ? 0 : 1);
       float *part =
           reinterpret_cast<float *>(workspace + slots_offset(records) + (size_t)slot * slot_bytes(D));
@@ -1124,6 +1179,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<uint4 *>(dst + col) =
               make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                          pack_bf16x2(v[6], v[7]));
+        } else if constexpr (kJoin) {  // the ring is free
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             ring + part_at<D>(my_row, col / 4 + i)),
+                         "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                         : "memory");
         } else {
           st_v8(part + ((size_t)(col / 8) * kRows + my_row) * 8, v);
         }
@@ -1161,8 +1223,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
           }
-          if (!whole && real)
+          if (!kJoin && !whole && real)
             reinterpret_cast<float2 *>(part + (size_t)kRows * D)[my_row] = make_float2(m, l);
+          if (kJoin) s_ml[tid] = make_float2(m, l);
         }
       } else {
         // A row's keys were dealt to `copies` lanes, each with a maximum, sum and O of its
@@ -1243,16 +1306,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         joined = joined && (!more || meet());
         if (!joined) break;
-        if (!whole && real && slice == 0)
+        if (!kJoin && !whole && real && slice == 0)
           reinterpret_cast<float2 *>(part + (size_t)kRows * D)[my_row] = make_float2(M, L);
+        // (every lane has read its row's s_ml: there was a meeting since)
+        if (kJoin && slice == 0) s_ml[my_row] = make_float2(M, L);
       }
-      if (done.t0 == 0 && tid == 0) {
+      if (!kJoin && done.t0 == 0 && tid == 0) {
         Record r;
         r.first = piece;
         r.last = p0 + (done.off + kSegment + done.s.tiles - 1) / blk;
         r.pad[0] = r.pad[1] = 0;
         reinterpret_cast<Record *>(workspace +
-                                   records_offset())[((size_t)done.b * a.Hkv + done.g) * mts + my_m] = r;
+                                   records_offset())[((size_t)done.b * a.Hkv + done.g) * mts + done.m] = r;
       }
       tc_fence_before();
       if (more && !early_q) {
@@ -1270,6 +1335,47 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if constexpr (kJoin) {
+    if (!split) return;
+    // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the cluster's CTAs: a thread's items
+    // are 8 dims of a row, neighbouring threads in one row.
+    cluster_sync();
+    constexpr int kD8 = D / 8;
+    const int rows = w.rows(Gq);
+    const uint32_t ml = smem_addr(s_ml);
+    for (int i = rank * kThreads + tid; i < rows * kD8; i += ctas * kThreads) {
+      const int rr = i / kD8, d8 = i - rr * kD8, row = w.m * kRows + rr, node = row / Gq;
+      float cm[kJoinCtas], cl[kJoinCtas], M = -INFINITY, L = 0.f, o[8] = {};
+#pragma unroll
+      for (int c = 0; c < kJoinCtas; ++c) {
+        cm[c] = -INFINITY;
+        cl[c] = 0.f;
+        if (c < ctas) ld_cluster_f32x2(cluster_map(ml + rr * 8, c), cm[c], cl[c]);
+        M = fmaxf(M, cm[c]);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int c = 0; c < kJoinCtas; ++c)
+        if (c < ctas && !(cl[c] == 0.f)) {  // (nothing was seen there: no O was left)
+          const float f = ex2(cm[c] - base);
+          L = fmaf(cl[c], f, L);
+          const uint32_t at = cluster_map(ring, c);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[4];
+            ld_cluster_f32x4(at + part_at<D>(rr, 2 * d8 + h), x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[4 * h + k] = fmaf(x[k], f, o[4 * h + k]);
+          }
+        }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      *reinterpret_cast<uint4 *>(
+          a.out + (((size_t)w.b * a.N + node) * a.Hq + (size_t)w.g * Gq + (row - node * Gq)) * D +
+          d8 * 8) = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                               pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+    }
+    cluster_sync();  // no CTA leaves while another reads its partial
   }
 }
 
@@ -1352,23 +1458,49 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const uint8_t *workspac
 
 inline int row_tiles(int N, int G) { return (N * G + kRows - 1) / kRows; }
 
-template <int D, Scores kScores>
-cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts,
-                   cudaStream_t stream) {
+template <int D, Scores kScores, bool kJoin>
+cudaError_t make_ready() {
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(tree_attn_kernel<D, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Geo<D>::kSmem);
+    e = cudaFuncSetAttribute(tree_attn_kernel<D, kScores, kJoin>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<D>::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
   }
+  return cudaSuccess;
+}
+
+template <int D, Scores kScores>
+cudaError_t launch(const TreeMaps &maps, const TreeAttnArgs &a, int B, int parts, int ctas,
+                   cudaStream_t stream) {
   uint8_t *ws = reinterpret_cast<uint8_t *>(a.error_word);
   const int mts = row_tiles(a.N, a.Hq / a.Hkv), records = B * a.Hkv * mts;
-  e = launch_pdl(tree_attn_kernel<D, kScores>, dim3(parts), kThreads, Geo<D>::kSmem, stream, maps, a,
-                 B, mts, ws);
+  cudaError_t e;
+  if (ctas > 0) {
+    if ((e = make_ready<D, kScores, true>()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(records * ctas);
+    cfg.blockDim = kThreads;
+    cfg.dynamicSmemBytes = Geo<D>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, kScores, true>, maps, a, B,
+                              mts | ctas << 8, ws);
+  }
+  if ((e = make_ready<D, kScores, false>()) != cudaSuccess) return e;
+  e = launch_pdl(tree_attn_kernel<D, kScores, false>, dim3(parts), kThreads, Geo<D>::kSmem, stream,
+                 maps, a, B, mts, ws);
   if (e != cudaSuccess || parts == 1) return e;
   const int rows = a.N * (a.Hq / a.Hkv) < kRows ? a.N * (a.Hq / a.Hkv) : kRows;
   if (parts >= 4 * records)
@@ -1391,14 +1523,40 @@ int tree_parts(int B, int N, int Hq, int Hkv, int max_len, int num_parts, int sm
   return (int)(most < 2 * sms ? most : 2 * sms < mt ? mt : 2 * sms);
 }
 
+// CTAs per (pair, row tile) of the one-launch form, 0 for the stream. The form has no merge and no
+// scan, a CTA that ends makes room for the next, but it does not even out the lengths. us of the
+// stream and of this form:
+//   1 sequence, 8 nodes, 16 / 8 heads, 64 tokens 9.3 and 6.4; 512 10.9 and 9.0; 2000 15.8 and 11.3;
+//     8000 21 and 19
+//   93 sequences, 51 nodes, 32 / 8 heads, 64 tokens 51 and 45; 512 95 and 78; 1000 139 and 118
+//   32 sequences, 4 nodes, 32 / 8 heads, 1 to 1000 tokens 25 and 22; 1 to 2000 34 and 35; 1 to 4000
+//     52 and 64
+//   107 sequences, 42 nodes, 32 / 4 heads of 64, 114 to 1827 tokens 91 and 78
+// hence up to 17 tiles per CTA, or 32 where four rounds of CTAs even them out.
+// A cluster where there are few tiles to share costs its join (8 nodes, 512 tokens, 1 and 4 CTAs:
+// 11.1 and 9.0; 64 nodes: 11.8 and 12.7; 1000 tokens 17 and 14), and with more than four CTAs to three
+// SMs the CTAs of one SM share its bandwidth (64 (pair, row tile)s, 1000 tokens, 2 and 4 CTAs:
+// 15.9 and 17.5). Eight CTAs only pay for a few (8 of them, 2000 tokens, 4 and 8: 13.1 and 11.3;
+// 16: 16.7 and 21.3).
+int tree_join_ctas(int B, int N, int Hq, int Hkv, int max_len, int window, int num_parts, int sms) {
+  if (num_parts > 0) return 0;
+  const int G = Hq / Hkv;
+  const long long records = (long long)B * Hkv * row_tiles(N, G);
+  const int seen = window > 0 && window < max_len ? window : max_len;
+  const int tiles = (seen + kTile - 1) / kTile + 1;
+  int c = tiles <= (N * G <= 32 ? 5 : 9) ? 1 : tiles <= 20 || records > 8 ? 4 : kJoinCtas;
+  while (c > 1 && 3 * records * c > 4 * sms) c /= 2;
+  return (tiles + c - 1) / c <= (records >= 4 * sms ? 32 : 17) ? c : 0;
+}
+
 size_t tree_ws_bytes(int B, int N, int Hq, int Hkv, int D, int parts) {
   return slots_offset(B * Hkv * row_tiles(N, Hq / Hkv)) + (size_t)2 * parts * slot_bytes(D);
 }
 
 cudaError_t launch_tree_attn(const CUtensorMap *maps, const TreeAttnArgs &a, int B, int D,
-                             int parts, cudaStream_t stream) {
+                             int parts, int ctas, cudaStream_t stream) {
   const TreeMaps m{maps[0], maps[1], maps[2], maps[3]};
-  auto go = [&](auto fn) { return fn(m, a, B, parts, stream); };
+  auto go = [&](auto fn) { return fn(m, a, B, parts, ctas, stream); };
   const cudaError_t e =
       a.softcap > 0.f ? (D == 128 ? go(launch<128, kCap>) : go(launch<64, kCap>))
       : a.slopes != nullptr ? (D == 128 ? go(launch<128, kBias>) : go(launch<64, kBias>))

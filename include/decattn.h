@@ -592,7 +592,8 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
  * max_len        host upper bound of every lens[b], 0 <= max_len <= T_cap.
  * scale          <= 0 selects 1/sqrt(D).  0 <= softcap <= 1e30, scale / softcap < 1e30.
  *                window >= 0.
- * num_parts      CTAs the work is cut over; 0 lets the library choose.
+ * num_parts      CTAs the work is cut over; 0 lets the library choose (two launches, or one for
+ *                short contexts: about 1000 tokens per CTA of a cluster of at most 8).
  * workspace      [device] at least dec_tree_attn_workspace_bytes(...) bytes, 256-byte aligned,
  *                its first 256 bytes zeroed before its first use (the first word is the
  *                device error word); it serves one call at a time.

@@ -128,6 +128,39 @@ def test_lengths(L):
     run(attn_case(L, [L], 9, 4, 1, 128), f"L={L}")
 
 
+@pytest.mark.parametrize("L", [100, 257, 320, 513, 577, 1000, 1217, 2000, 4100, 8600])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 1, 1, 64), (8, 16, 8, 128), (33, 8, 2, 64), (64, 8, 1, 128),
+                                        (20, 8, 2, 64)])
+def test_clusters_and_the_stream_by_length(L, N, Hq, Hkv, D):
+    """Every number of CTAs that a sequence is shared by, with short sequences beside a long one
+    (CTAs without tiles, sequences without nodes), and the stream for the same."""
+    for B in (1, 4):
+        c = attn_case(L + N, [L, 0, 1, 70][:B], N, Hq, Hkv, D, nodes=[N, N, max(1, N - 1), 0][:B])
+        run(c, f"L={L} B={B}")
+    slopes = torch.exp2(-torch.arange(1.0, Hq + 1))
+    run(c, "options", softcap=25.0, slopes=slopes, window=300)
+    run(c, "options", slopes=slopes)
+    g = on_gpu(c)
+    ws = dsa.alloc_tree_workspace(*c["q"].shape[:3], Hkv, D, L, 13)
+    a = call(g, max_len=L)
+    b = call(g, max_len=L, num_parts=13, workspace=ws)
+    ref, size = reference(c)
+    err = (a.float() - b.float()).abs().cpu().numpy()
+    live = ~np.isnan(ref)
+    # both within the bound of the exact result
+    assert np.all(err[live] <= (2.0 ** -7 * (np.abs(ref) + size) * 1.02 + 2.0 ** -10 * size)[live])
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,hi", [(170, 47, 16, 4, 128, 230), (620, 3, 2, 1, 64, 1900),
+                                             (40, 64, 32, 4, 64, 500)])
+def test_more_short_sequences_than_the_machine_holds(B, N, Hq, Hkv, D, hi):
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, hi, B)]
+    nodes = [int(x) for x in rng.integers(0, N + 1, B)]
+    lens[3], nodes[4] = hi, N
+    run(attn_case(B, lens, N, Hq, Hkv, D, nodes=nodes, empty=True), f"B={B}")
+
+
 @pytest.mark.parametrize("parts", [1, 2, 3, 7, 16, 61, 304, 1000])
 def test_parts(parts):
     c = attn_case(parts, [700, 0, 5, 64, 1300, 333], 20, 8, 2, 128, nodes=[20, 20, 1, 0, 13, 7])
