@@ -15,7 +15,7 @@
 //               of four 16-byte vectors per thread and leave their results in shared memory;
 //               four put a row together from them. (That last part is a long chain of short
 //               steps; among streaming warps it took 6000 cycles a row and held them all up.)
-//               512 rows of 131072 fp32 logits: 50 us, 5.4 TB/s; 1024 rows: 95 us, 5.7 TB/s.
+//               512 rows of 131072 fp32 logits: 50 us, 5.3 TB/s; 1024 rows: 95 us, 5.7 TB/s.
 //   few rows    a row over a cluster of up to 16 CTAs, the slices' results joined through
 //               distributed shared memory. One row of 151936 fp32 logits: 8 us.
 //
@@ -758,20 +758,26 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
           post_sync();
           Best best(bound);
           best.offer(ends);
-          // Items of 32 of an owner's vectors, four at a time so that their loads overlap.
-          const int owners = s_count[0];
-          const int chunks = (r.v1 + 32 * kThreads - 1) / (32 * kThreads);
+          // Items of 32 vectors, of one owner or, in short rows, of several; four at a time so that
+          // their loads overlap. (1416 rows of 6988 fp32, K = 32: 35 us, with an item per owner 47;
+          // 512 rows of 131072, K = 8: 50.3 and 49.3.)
+          const int owners = s_count[0], each = (r.v1 + kThreads - 1) / kThreads;
+          const int wide = each > 16 ? 5 : each > 8 ? 4 : each > 4 ? 3 : 2;  // log2, lanes an owner
+          const int chunks = (each + (1 << wide) - 1) >> wide;
+          const int items = ((owners << wide) + 31) / 32 * chunks;
           const float least = least_of(bound);
-          for (int i0 = pw; i0 < owners * chunks; i0 += 4 * kPostWarps) {
+          for (int i0 = pw; i0 < items; i0 += 4 * kPostWarps) {
             uint4 x[4];
             int j[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int i = i0 + q * kPostWarps, o = i / chunks;
+              const int i = i0 + q * kPostWarps, of = i / chunks;
+              const int o = ((of << 5) + lane) >> wide;
               j[q] = r.v1;
               x[q] = make_uint4(0u, 0u, 0u, 0u);
-              if (i < owners * chunks)
-                j[q] = s_owner[o] + ((i - o * chunks) * 32 + lane) * kThreads;
+              if (i < items && o < owners)
+                j[q] = s_owner[o] +
+                       (((i - of * chunks) << wide) + (lane & ((1 << wide) - 1))) * kThreads;
               if (j[q] < r.v1) x[q] = ld_stream(r.vec + j[q]);
             }
 #pragma unroll
