@@ -617,6 +617,22 @@ def test_rope_tree_matches_the_single_token_append(D, layout):
     assert torch.equal(vt[:, :, 0], vc[row, :, p.long()])
 
 
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D", [
+    # two passes of a warp over its heads; three; four; two blocks of heads per node; as many KV
+    # heads as query heads, and more KV heads than one pass holds
+    (3, 64, 16, 8, 128), (1, 64, 32, 32, 128), (4, 64, 32, 8, 128), (8, 64, 33, 3, 128),
+    (8, 64, 24, 24, 128), (5, 62, 48, 8, 128), (8, 64, 40, 40, 128), (3, 64, 64, 32, 128),
+    (6, 64, 64, 8, 128), (320, 1, 20, 20, 128), (8, 64, 16, 16, 64), (1, 64, 64, 64, 64),
+    (8, 64, 48, 24, 64), (2, 64, 48, 48, 64), (8, 64, 64, 32, 64), (7, 50, 40, 40, 64)])
+def test_rope_tree_several_passes(B, N, Hq, Hkv, D, layout):
+    """Enough nodes and heads for a warp to turn several heads one after the other."""
+    c = rope_case(N * Hq + D, B, N, Hq, Hkv, D, Hkv % 3 != 0, far=131072)
+    c["n_nodes"][0] = N
+    assert run_rope(c, layout) == 0
+    assert run_rope(c, layout, in_place=True) == 0
+
+
 # ---------------------------------------------------------------------- commit ---
 @pytest.mark.parametrize("B,Hkv,N,D,T", [(1, 1, 1, 64, 1), (3, 2, 5, 128, 40), (40, 8, 64, 64, 200)])
 def test_commit(B, Hkv, N, D, T):
