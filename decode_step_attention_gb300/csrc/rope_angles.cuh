@@ -73,6 +73,18 @@ __device__ __noinline__ inline float rope_exact_turns(int p, unsigned long long 
   return (float)(fma((double)own, cs, o * sn) * (double)rstd);
 }
 
+// A rotated pair in fp32 with its roundings spelled out. Left to the compiler, which product of a
+// sum is fused with it differs from kernel to kernel, and with it the last bit of one result in
+// some 1e5. The rotating kernels that promise each other's bits form the pair here.
+__device__ __forceinline__ float rope_first(float a, float b, float c, float s) {  // a c - b s
+  return fmaf(a, c, -__fmul_rn(b, s));
+}
+// a s + b c. The interleaved layout at D = 64 rounds a s first, the others b c.
+template <bool kRoundsA>
+__device__ __forceinline__ float rope_second(float a, float b, float c, float s) {
+  return kRoundsA ? fmaf(b, c, __fmul_rn(a, s)) : fmaf(a, s, __fmul_rn(b, c));
+}
+
 // Whether a fp32 rotation result y of a pair whose normalised values have magnitudes
 // a and b cancels enough to be formed again by rope_exact.
 __device__ __forceinline__ bool rope_cancels(float y, float a, float b) {

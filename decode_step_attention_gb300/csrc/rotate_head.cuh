@@ -113,7 +113,7 @@ __device__ __forceinline__ void rotate_values(const float (&x_in)[Lanes<D>::kE],
       const float other = __shfl_xor_sync(0xffffffffu, x[e], 16);
       const float other_w = __shfl_xor_sync(0xffffffffu, xw[e], 16);
       const float c = ang.c[e], sn = ang.s[e];
-      y[e] = first ? (x[e] * c - other * sn) : (other * sn + x[e] * c);
+      y[e] = first ? rope_first(x[e], other, c, sn) : rope_second<false>(other, x[e], c, sn);
       if (is_k && rope_cancels(y[e], x[e], other))  // K: the stored copy within one ulp
         y[e] = exact(e, xw[e], other_w, rstd, !first);
     }
@@ -122,8 +122,8 @@ __device__ __forceinline__ void rotate_values(const float (&x_in)[Lanes<D>::kE],
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float c = ang.c[e], sn = ang.s[e];
-      y[e] = x[e] * c - x[e + 1] * sn;
-      y[e + 1] = x[e] * sn + x[e + 1] * c;
+      y[e] = rope_first(x[e], x[e + 1], c, sn);
+      y[e + 1] = rope_second<D == 64>(x[e], x[e + 1], c, sn);
       if (is_k && rope_cancels(y[e], x[e], x[e + 1]))
         y[e] = exact(e, xw[e], xw[e + 1], rstd, false);
       if (is_k && rope_cancels(y[e + 1], x[e], x[e + 1]))

@@ -52,7 +52,7 @@ __device__ __noinline__ void exact_elements(const __nv_bfloat16 *k, const __nv_b
 // 128) or 4 (64) heads at a time, P times over: q heads, then k heads, then v heads (copied).
 // Every load is in flight while the node's D/2 angles are formed in shared memory. The
 // arithmetic is that of rotate_head.cuh in another lane layout: the same sums in the same
-// order, so both give the same bits.
+// order, the rotated pair with the same roundings, so both give the same bits.
 //
 // A node's chain (position, angles, barrier, rotation, stores) is hidden by the other CTAs of
 // the SM, and the instructions, some 130 per 8 elements of a head and lane, take 70% of the
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, P == 2 || P == 3 ? 6 : 5)
         for (int k = 0; k < 4; ++k) {
           const int e = 4 * h + k;
           const float other = __shfl_xor_sync(0xffffffffu, x[e], kLanes / 2);
-          y[e] = first ? (x[e] * cs[k] - other * sn[k]) : (other * sn[k] + x[e] * cs[k]);
+          y[e] = first ? rope_first(x[e], other, cs[k], sn[k])
+                       : rope_second<false>(other, x[e], cs[k], sn[k]);
           if (is_k && rope_cancels(y[e], x[e], other)) cancels |= 1u << e;
         }
       }
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, P == 2 || P == 3 ? 6 : 5)
       const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        y[e] = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
-        y[e + 1] = x[e] * sn[e / 2] + x[e + 1] * cs[e / 2];
+        y[e] = rope_first(x[e], x[e + 1], cs[e / 2], sn[e / 2]);
+        y[e + 1] = rope_second<D == 64>(x[e], x[e + 1], cs[e / 2], sn[e / 2]);
         if (is_k && rope_cancels(y[e], x[e], x[e + 1])) cancels |= 1u << e;
         if (is_k && rope_cancels(y[e + 1], x[e], x[e + 1])) cancels |= 2u << e;
       }

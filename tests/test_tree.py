@@ -633,6 +633,30 @@ def test_rope_tree_several_passes(B, N, Hq, Hkv, D, layout):
     assert run_rope(c, layout, in_place=True) == 0
 
 
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (32, 8, 128), (32, 32, 128), (48, 8, 128),
+                                      (64, 8, 128), (32, 16, 64), (64, 64, 64), (64, 32, 64)])
+def test_rope_tree_of_many_nodes_matches_the_single_token_append(Hq, Hkv, D, layout):
+    """The same bits from the forms of several passes."""
+    B, T = 500, 16
+    c = rope_case(Hq + D, B, 1, Hq, Hkv, D, True, far=T)
+    g = {k: v.to(DEV) for k, v in c.items()}
+    kt = torch.zeros(B, Hkv, 1, D, dtype=torch.bfloat16, device=DEV)
+    vt = torch.zeros_like(kt)
+    q = dsa.qknorm_rope_tree(g["q"].clone(), g["k_new"], g["v_new"], kt, vt, g["pos"], 1e6, layout,
+                             g["q_norm_w"], g["k_norm_w"])
+    kc = torch.zeros(B, Hkv, T, D, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    p = g["pos"][:, 0].contiguous()
+    q1 = dsa.qknorm_rope_kv_append(g["q"][:, 0].clone(), g["k_new"][:, 0].contiguous(),
+                                   g["v_new"][:, 0].contiguous(), kc, vc, p, 1e6, layout,
+                                   g["q_norm_w"], g["k_norm_w"])
+    row = torch.arange(B, device=DEV)
+    assert torch.equal(q[:, 0], q1)
+    assert torch.equal(kt[:, :, 0], kc[row, :, p.long()])
+    assert torch.equal(vt[:, :, 0], vc[row, :, p.long()])
+
+
 # ---------------------------------------------------------------------- commit ---
 @pytest.mark.parametrize("B,Hkv,N,D,T", [(1, 1, 1, 64, 1), (3, 2, 5, 128, 40), (40, 8, 64, 64, 200)])
 def test_commit(B, Hkv, N, D, T):
