@@ -152,18 +152,25 @@ InvFreq make_inv_freq(int D, double theta) {
 }
 
 RopeTurns make_rope_turns(int D, const InvFreq &inv) {
-  // f = inv_freq / (2 pi) as the unevaluated sum p + e of two doubles (about 2^-104 of it),
-  // then its integer part in units of 2^-64 and the rest rounded: the nearest integer to
-  // within 2^-40 of a unit, on every host, without the software quadruple precision that
-  // long double is on some (5 us per table there).
+  // f = inv_freq / (2 pi) as the unevaluated sum p + e of two doubles (about 2^-104 of it), whole
+  // turns off each (a base below 1 has frequencies of several turns per position), then p's
+  // integer part in units of 2^-64 and the rest rounded: the nearest integer to within 2^-40 of a
+  // unit, on every host, without the software quadruple precision that long double is on some
+  // (5 us per table there).
   RopeTurns t{};
   constexpr double kHi = 0.15915494309189535;      // 1 / (2 pi): the nearest double
   constexpr double kLo = -9.839338337591243e-18;   // and what it lacks
+  constexpr double unit = 18446744073709551616.0;  // 2^64, exact scalings
   for (int i = 0; i < D / 2; ++i) {
-    const double f = inv.v[i], p = f * kHi, e = fma(f, kHi, -p) + f * kLo;
-    const double unit = 18446744073709551616.0;    // 2^64, exact scalings
-    const double whole = floor(p * unit);          // f <= 1: below 2^62
-    t.v[i] = (unsigned long long)((long long)whole + llround((p * unit - whole) + e * unit));
+    const double f = inv.v[i];
+    double p = f * kHi, e = fma(f, kHi, -p) + f * kLo;
+    p -= floor(p);                                 // in [0, 1), exact
+    e -= rint(e);                                  // in [-1/2, 1/2]
+    const double whole = floor(p * unit);          // below 2^64
+    double rest = (p * unit - whole) + e * unit;
+    if (rest >= 0.5 * unit) rest -= unit;          // (e = 1/2)
+    // the sum modulo 2^64
+    t.v[i] = (unsigned long long)whole + (unsigned long long)llround(rest);
   }
   return t;
 }

@@ -102,7 +102,7 @@ InvFreq make_inv_freq(int D, double theta);
 struct RopeTurns {
   unsigned long long v[64];
 };
-// Every inv_freq_i must lie in [0, 1], so that turns_i < 1/(2 pi) fits the fraction.
+// Any finite inv_freq_i >= 0: whole turns per position fall off like the others.
 RopeTurns make_rope_turns(int D, const InvFreq &inv);
 
 __device__ __forceinline__ void rope_sincos_turns(int p, unsigned long long turns, float &s,

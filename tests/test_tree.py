@@ -14,6 +14,7 @@ import pytest
 import torch
 
 import decode_step_attention_gb300 as dsa
+from oracle import decode_ref as O
 from oracle import tree as OT
 from tol import check_ulp
 
@@ -655,6 +656,28 @@ def test_rope_tree_of_many_nodes_matches_the_single_token_append(Hq, Hkv, D, lay
     assert torch.equal(q[:, 0], q1)
     assert torch.equal(kt[:, :, 0], kc[row, :, p.long()])
     assert torch.equal(vt[:, :, 0], vc[row, :, p.long()])
+
+
+@pytest.mark.parametrize("theta", [0.5, 0.125, 2.0 ** -10])
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rope_bases_below_one(theta, layout, D):
+    """Frequencies above one radian per position, where a position is several turns."""
+    assert run_rope(rope_case(D, 5, 7, 6, 2, D, True), layout, theta=theta) == 0
+    B, Hq, Hkv, T = 9, 6, 2, 1000  # and the single-token append
+    c = rope_case(D + 1, B, 1, Hq, Hkv, D, True, far=T)
+    g = {k: v.to(DEV) for k, v in c.items()}
+    kc = torch.zeros(B, Hkv, T, D, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    p = c["pos"][:, 0].contiguous()
+    q = dsa.qknorm_rope_kv_append(g["q"][:, 0].clone(), g["k_new"][:, 0].contiguous(),
+                                  g["v_new"][:, 0].contiguous(), kc, vc, p.to(DEV), theta, layout,
+                                  g["q_norm_w"], g["k_norm_w"])
+    turn = lambda x, w: O.qknorm_rope(f64(c[x][:, 0]), f64(c[w]), p.numpy(), theta,  # noqa: E731
+                                      layout, 1e-6)
+    ref = turn("q", "q_norm_w")
+    assert np.all(np.abs(f64(q) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * np.abs(ref).max())
+    check_ulp(f64(kc[torch.arange(B), :, p.long()]), turn("k_new", "k_norm_w"), "appended keys")
 
 
 # ---------------------------------------------------------------------- commit ---
