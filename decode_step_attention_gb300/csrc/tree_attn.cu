@@ -43,6 +43,7 @@
 // The weights are rounded to bf16 (one rounding, at most 2^-8 of each, as large as the
 // output's own rounding) because the value product wants both operands alike; sums, maxima
 // and O are fp32.
+#include <limits.h>
 #include <math.h>
 
 #include <atomic>
@@ -742,20 +743,31 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __reduce_or_sync(0xffffffffu, (uint32_t)used)) &
                bit_range(0, w.s.live);
       }
+      // With a window, the first cached row that some node sees: later than the segment's first
+      // when every node lies past the sequence's length.
+      int least = INT_MAX;
+      if (a.window > 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (lane + 32 * h < w.s.live) least = min(least, a.pos[(size_t)w.b * a.N + lane + 32 * h]);
+      }
       ok = ok && wait_all(bar_q, seg & 1) && issue_s(n);
+      const int first_seen =
+          a.window > 0 ? max(0, max(__reduce_min_sync(0xffffffffu, least), w.s.L) - a.window + 1) : 0;
       for (int i = 0; i < cnt && ok; ++i) {
         const int it = 2 * (n + i) + 1, slot = it % S, t = w.t0 + i;
         if (i + 1 < cnt) ok = issue_s(n + i + 1);
         ok = ok && wait_all(bar_full + 8 * slot, (it / S) & 1);
         if (!ok) break;
         const bool tree = w.is_tree(t);
-        const int valid = w.s.L - w.token(t);
-        if (tree || valid < kTile) {
+        const int valid = w.s.L - w.token(t), unseen = first_seen - w.token(t);
+        if (tree || valid < kTile || unseen > 0) {
           const uint32_t v_s = ring + slot * G::kTensor;
           if (tree) {
             const uint64_t odd = clear_tree(v_s, used, w.s.live);
             if (lane == 0) s_odd = odd;
           } else {
+            clear_rows(v_s, 0, min(unseen, kTile));
             clear_rows(v_s, valid, kTile);
           }
           fence_proxy_async_smem();

@@ -579,7 +579,8 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
  * with a score cap or a distance bias.
  *
  * q              [device|host] bf16 [B, N, Hq, D] (rotated).
- * k_cache, v_cache [device] bf16 [B, Hkv, T_cap, D]; rows t >= lens[b] may hold anything.
+ * k_cache, v_cache [device] bf16 [B, Hkv, T_cap, D]; rows t >= lens[b], and rows behind every
+ *                node's window, may hold anything.
  * k_tree, v_tree [device] bf16 [B, Hkv, N, D]; a node that is not seen may hold anything:
  *                it changes nothing for the nodes that do not see it. (A cached row that
  *                some node of its sequence sees must be finite for all of them.)

@@ -175,6 +175,25 @@ def test_window(window, parts):
     run(c, f"window={window}", window=window, num_parts=parts)
 
 
+@pytest.mark.parametrize("gap,window", [(3, 40), (3, 3), (1, 64), (70, 200), (130, 150), (90, 20), (1, 1)])
+@pytest.mark.parametrize("N,Hq,D,kw", [(3, 2, 64, {}), (20, 6, 128, {}), (64, 8, 64, {}),
+                                       (9, 8, 128, {"softcap": 20.0}), (40, 6, 64, {"alibi": True})])
+@pytest.mark.parametrize("parts", [0, 5])
+def test_rows_behind_every_nodes_window_may_hold_anything(gap, window, N, Hq, D, kw, parts):
+    """All nodes lie `gap` past the sequence's length (their parents are cached already): the first
+    row any of them sees is later than for a node at the length."""
+    c = attn_case(gap + window, [300, 0, 65, 20], N, Hq, 2, D, nodes=[N, N, max(1, N // 2), 1])
+    c["pos"] += gap
+    for b, L in enumerate((300, 0, 65, 20)):
+        behind = min(L, max(0, L + gap - window + 1))
+        for i, name in enumerate(("k_cache", "v_cache")):
+            c[name][b, :, :behind] = (NAN, float("inf"))[(b + i) & 1]
+    kw = dict(kw)
+    if kw.pop("alibi", False):
+        kw["slopes"] = torch.exp2(-torch.arange(1.0, Hq + 1))
+    run(c, f"gap={gap} window={window}", window=window, num_parts=parts, **kw)
+
+
 @pytest.mark.parametrize("softcap", [0.0, 0.5, 20.0, 50.0])
 @pytest.mark.parametrize("alibi", [False, True])
 @pytest.mark.parametrize("N", [1, 13])
