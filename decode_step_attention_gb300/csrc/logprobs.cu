@@ -167,24 +167,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return y;
 }
 
-// A running softmax state: the maximum logit m and, relative to the exponent r = m k with k =
-// log2(e) / T, s = sum 2^(k v - r) and c = sum 2^(k v - r) (k v - r). (r is one rounded number
-// that every exponent is taken against, in one rounding: never contracted.) Nothing seen: m = -inf.
+// The exponent that a maximum's logits are taken against: m k with k = log2(e) / T, or -2^24 where
+// that is less. A part of a row masked with -1e30 or the type's lowest value then has sums of 0 (its
+// own m k may be -inf, and the rounding of m k alone would move exponents by thousands).
+constexpr float kLowest = -0x1p24f;
+__device__ __forceinline__ float base_of(float m, float k) { return fmaxf(__fmul_rn(m, k), kLowest); }
+
+// A running softmax state: the base r of the largest logit and, relative to it, s = sum 2^(k v - r)
+// and c = sum 2^(k v - r) (k v - r). (r is one rounded number that every exponent is taken
+// against, in one rounding: never contracted.) Nothing seen: r = kLowest and no sums.
 struct State {
-  float m, s, c;
-  // the factors that move sums from this maximum to a larger one
-  __device__ __forceinline__ void raise(float to, float k) {
-    if (m != -INFINITY) {
-      const float d = __fmul_rn(m, k) - __fmul_rn(to, k), f = ex2(d);
-      c = f > 0.f ? f * fmaf(d, s, c) : 0.f * c;  // keeps a NaN
-      s *= f;
-    }
-    m = to;
+  float r = kLowest, s = 0.f, c = 0.f;
+  // moves the sums from this base to a larger one
+  __device__ __forceinline__ void raise(float to) {
+    const float d = r - to, f = ex2(d);
+    c = f > 0.f ? f * fmaf(d, s, c) : 0.f * c;  // keeps a NaN
+    s *= f;
+    r = to;
   }
-  __device__ __forceinline__ void join(State o, float k) {
-    const float to = fmaxf(m, o.m);
-    raise(to, k);
-    o.raise(to, k);
+  __device__ __forceinline__ void join(State o) {
+    const float to = fmaxf(r, o.r);
+    raise(to);
+    o.raise(to);
     s += o.s;
     c += o.c;
   }
@@ -211,11 +215,11 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
 }
 
 // The lanes' states as one, in every lane.
-__device__ __forceinline__ void warp_join(State &st, float k) {
-  float to = st.m;
+__device__ __forceinline__ void warp_join(State &st) {
+  float to = st.r;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(kAll, to, o));
-  st.raise(to, k);
+  st.raise(to);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     st.s += __shfl_xor_sync(kAll, st.s, o);
@@ -272,17 +276,61 @@ struct Row {
   }
 };
 
-// A row's numbers from its sums (one thread): the exponent its logits are taken against, log2 of
-// their sum, and the entropy.
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t row, const State &q, float k,
+// A row's numbers from its sums (one thread): out[0] the exponent its logits are taken against,
+// out[1] log2 of their sum, and the entropy. A far row, whose largest logit is beyond 2^24 / k on
+// either side (1e7; a whole row masked with -1e9 or the type's lowest value, or nothing but -inf),
+// gets an infinite out[0]: the rounding of m k moves exponents by 1 and more there.
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, size_t row, const State &q,
                                            float *out) {
-  const float log2_s = isinf(q.m) ? NAN : log2f(q.s);
-  out[0] = __fmul_rn(q.m, k);
+  const float log2_s = log2f(q.s);
+  out[0] = q.r > kLowest && q.r <= -kLowest ? q.r : INFINITY;
   out[1] = log2_s;
+  out[2] = 0.f;
   if (a.entropy != nullptr) a.entropy[row] = (log2_s - q.c / q.s) * kLn2;
 }
-__device__ __forceinline__ float logprob_of(float v, float k, const float *out) {
-  return (fmaf(v, k, -out[0]) - out[1]) * kLn2;
+// A far row again, by `warps` warps: summed with exponents (v - m) k, m = out[2] the value of the
+// largest of the groups' keys. `sync` is their barrier; one stands before the call. Rare, and slow:
+// 512 rows of 131072 equal logits (K = 8) take 110 us at 0 and 235 at -1e30, one row of 151936
+// (K = 20) 102 and 116.
+template <bool kBf16, typename Sync>
+__device__ __noinline__ void finish_far(const LogprobArgs &a, size_t row, const void *base, float k,
+                                        int t, int warps, const u64 *group, int groups,
+                                        State *states, float *out, Sync sync) {
+  u64 top = 0;
+  for (int i = 0; i < groups; ++i) top = umax(top, group[i]);
+  const float m = top == 0 ? NAN : key_value(top);
+  State q[4];
+  for (int i0 = t; i0 < a.V; i0 += 128 * warps)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 32 * warps;
+      const float v = i < a.V ? Vec<kBf16>::one(base, i) : -INFINITY;
+      const float d = max_nan((v - m) * k, -400.f), e = ex2(d);
+      q[u].s += e;
+      q[u].c = fmaf(e, d, q[u].c);
+    }
+  float s = (q[0].s + q[1].s) + (q[2].s + q[3].s), c = (q[0].c + q[1].c) + (q[2].c + q[3].c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(kAll, s, o);
+    c += __shfl_xor_sync(kAll, c, o);
+  }
+  if ((t & 31) == 0) states[t >> 5].s = s, states[t >> 5].c = c;
+  sync();
+  if (t == 0) {
+    for (int i = 1; i < warps; ++i) s += states[i].s, c += states[i].c;
+    const float log2_s = isinf(m) ? NAN : log2f(s);
+    out[1] = log2_s;
+    out[2] = m;
+    if (a.entropy != nullptr) a.entropy[row] = (log2_s - c / s) * kLn2;
+  }
+  sync();
+}
+__device__ __forceinline__ float logprob_of(const LogprobArgs &a, float v, float k, const float *out) {
+  const float d = fmaf(v, k, -out[0]);
+  if (!(fabsf(d) < INFINITY))  // a far row, or k v past the range, where z may not be (and lse is nothing)
+    return fmaf(-kLn2, out[1], (v - out[2]) / a.temperature);
+  return (d - out[1]) * kLn2;
 }
 // One of a row's alternatives. (In a row with NaN fewer than K keys may have been found: any
 // id in range then.)
@@ -290,26 +338,28 @@ __device__ __forceinline__ void emit(const LogprobArgs &a, size_t row, int place
                                      const float *out) {
   a.top_ids[row * a.K + place] = key == 0 ? place : key_id(key);
   a.top_logprobs[row * a.K + place] =
-      logprob_of(key == 0 ? NAN : key_value(key), k, out);
+      logprob_of(a, key == 0 ? NAN : key_value(key), k, out);
 }
 
-// A thread's part of a row: its sums, and its largest logit (sums.m) with its id.
+// A thread's part of a row: its sums, and its largest logit with its id.
 template <bool kBf16>
 struct Running {
   using V = Vec<kBf16>;
   static constexpr int E = V::kN;
-  State sums{-INFINITY, 0.f, 0.f};
+  State sums;
+  float m = -INFINITY;
   int best_id = -1;  // nothing seen yet
 
   __device__ __forceinline__ u64 key() const {
-    return best_id < 0 ? 0ull : rank_key(sums.m, best_id);
+    return best_id < 0 ? 0ull : rank_key(m, best_id);
   }
   // n vectors' worth of logits, the first element of vector u being first + u * stride
   template <int n>
   __device__ __forceinline__ void group(const uint4 (&x)[n], int first, int stride, float k) {
     const float mx = V::template largest<n>(x);
-    if (mx > sums.m || best_id < 0) {  // strictly: of equal values the lower id stays
-      sums.raise(mx, k);
+    if (mx > m || best_id < 0) {  // strictly: of equal values the lower id stays
+      sums.raise(base_of(mx, k));
+      m = mx;
       bool found = false;
 #pragma unroll
       for (int u = n - 1; u >= 0; --u) {
@@ -320,7 +370,7 @@ struct Running {
           if (v[i] == mx || !found) best_id = first + u * stride + i, found = true;
       }
     }
-    const float r = sums.m == -INFINITY ? 0.f : __fmul_rn(sums.m, k);
+    const float r = sums.r;
     const u64 k2 = pair_of(k, k), r2 = pair_of(-r, -r);
     u64 s2[2] = {}, c2[2] = {};
 #pragma unroll
@@ -359,12 +409,12 @@ struct Running {
     sums.c += c;
   }
   __device__ __forceinline__ void single(float v, int id, float k) {
-    if (v > sums.m || best_id < 0) {
-      sums.raise(v, k);
+    if (v > m || best_id < 0) {
+      sums.raise(base_of(v, k));
+      m = v;
       best_id = id;
     }
-    const float r = sums.m == -INFINITY ? 0.f : __fmul_rn(sums.m, k);
-    const float d = max_nan(fmaf(v, k, -r), -400.f), e = ex2(d);
+    const float d = max_nan(fmaf(v, k, -sums.r), -400.f), e = ex2(d);
     sums.s += e;
     sums.c = fmaf(e, d, sums.c);
   }
@@ -422,7 +472,7 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
   __shared__ Slice s_slice;
   __shared__ u64 s_all[kMaxGroups], s_bound, s_cand[kMaxCluster * 32];
   __shared__ State s_states[kFewWarps];
-  __shared__ float s_out[2];
+  __shared__ float s_out[3];
   __shared__ int s_count;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
@@ -476,7 +526,7 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
   // ---- the slice: every warp's sums, the largest keys of its groups of threads
   const int per = kMaxGroups / C, groups = kMaxGroups;  // groups to a CTA, of the row
   State st = run.sums;
-  warp_join(st, k);
+  warp_join(st);
   if (lane == 0) s_slice.sums[warp] = st;
   u64 g = umax(vec_key, end_key);
   for (int o = 1; o < kFew / per; o *= 2) g = umax(g, __shfl_xor_sync(kAll, g, o));
@@ -487,24 +537,29 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
     s_all[tid] = ld_cluster_u64(
         cluster_map(here + (uint32_t)offsetof(Slice, group), tid / per) + 8 * (tid % per));
   if (rank == 0) {  // the row's sums: a state per (CTA, warp)
-    State q{-INFINITY, 0.f, 0.f};
+    State q;
     if (tid < C * kFewWarps) {
       const uint32_t at = cluster_map(here, tid / kFewWarps) +
                           (uint32_t)sizeof(State) * (tid % kFewWarps);
-      q.m = ld_cluster_f32(at);
+      q.r = ld_cluster_f32(at);
       q.s = ld_cluster_f32(at + 4);
       q.c = ld_cluster_f32(at + 8);
     }
-    warp_join(q, k);
+    warp_join(q);
     if (lane == 0) s_states[warp] = q;
   }
   __syncthreads();
   if (rank == 0 && warp == kFewWarps - 1) {
-    State q{-INFINITY, 0.f, 0.f};
+    State q;
     if (lane < kFewWarps) q = s_states[lane];
-    warp_join(q, k);
-    if (lane == 0) finish_row(a, row, q, k, s_out);
+    warp_join(q);
+    if (lane == 0) finish_row(a, row, q, s_out);
   }
+  auto far_row = [&] {  // (a barrier stands between s_out's writing and this)
+    if (rank == 0 && isinf(s_out[0]))
+      finish_far<kBf16>(a, row, r.base, k, tid, kFewWarps, s_all, groups, s_states, s_out,
+                        [] { __syncthreads(); });
+  };
   if (a.K > 0) {
     // the K-th largest of the groups' keys
     if (tid < groups && s_all[tid] > 0 && larger(s_all, groups, s_all[tid]) == a.K - 1)
@@ -541,6 +596,7 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
     }
     if (tid == 0) s_slice.n = min(cands, a.K);
     cluster_sync();
+    far_row();
     if (rank == 0) {
       if (tid == 0) s_count = 0;
       __syncthreads();
@@ -563,13 +619,14 @@ __global__ void __launch_bounds__(kFew, 4) logprobs_few_kernel(const LogprobArgs
     }
   } else {
     __syncthreads();
+    far_row();
   }
   if (rank == 0) {
-    if (tid < a.C) a.logprobs[row * a.C + tid] = logprob_of(given, k, s_out);
+    if (tid < a.C) a.logprobs[row * a.C + tid] = logprob_of(a, given, k, s_out);
     for (int i = tid + kFew; i < a.C; i += kFew) {
       const int id = a.ids[row * a.C + i];
       a.logprobs[row * a.C + i] =
-          logprob_of(id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
+          logprob_of(a, id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
     }
   }
   if (C > 1) cluster_exit_sync();  // no CTA leaves while another still reads its shared memory
@@ -589,12 +646,12 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
   constexpr int E = V::kN;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t s_bar[2 * kStages + 4];
-  __shared__ float4 s_sums[2][kThreads];  // (m, s, c) of a row's streaming threads
+  __shared__ float4 s_sums[2][kThreads];  // (r, s, c) of a row's streaming threads
   __shared__ u64 s_keys[2][kThreads];     // and their largest keys (0: nothing seen)
   __shared__ State s_states[kPostWarps];
   __shared__ u64 s_group[kPost], s_bound;  // the largest key of every 3 or 12 streaming threads
   __shared__ u64 s_cand[kPost];
-  __shared__ float s_out[2];
+  __shared__ float s_out[3];
   __shared__ int s_count[2];              // owners and candidates
   __shared__ short s_owner[kThreads];
   __shared__ volatile int s_abort;
@@ -683,7 +740,7 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
         if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
       }
       if (turn >= 2) __all_sync(kAll, await(bar_taken + 8 * par, ((turn >> 1) + 1) & 1) ? 1 : 0);
-      s_sums[par][tid] = make_float4(run.sums.m, run.sums.s, run.sums.c, 0.f);
+      s_sums[par][tid] = make_float4(run.sums.r, run.sums.s, run.sums.c, 0.f);
       s_keys[par][tid] = run.key();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_left + 8 * par);
@@ -716,7 +773,7 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
         const float4 x = s_sums[par][p * kEach + i];
         mine[i] = s_keys[par][p * kEach + i];
         most = umax(most, mine[i]);
-        st.join(State{x.x, x.y, x.z}, k);
+        st.join(State{x.x, x.y, x.z});
       }
       if (!left) st.s = NAN;
       // 32 groups, or 128 where K of 32 would be too low a bound (K = 32, 64000 fp32 logits: 130
@@ -729,18 +786,18 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
       } else {
         s_group[p] = most;
       }
-      warp_join(st, k);
+      warp_join(st);
       if (lane == 0) s_states[pw] = st;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_taken + 8 * par);
       if (p == 0) s_bound = 1;  // for fewer than K keys
       post_sync();
       if (pw == kPostWarps - 1) {
-        State q{-INFINITY, 0.f, 0.f};
+        State q;
         if (lane < kPostWarps) q = s_states[lane];
-        warp_join(q, k);
-        if (s_abort) q.s = NAN;
-        if (lane == 0) finish_row(a, row, q, k, s_out);
+        warp_join(q);
+        if (s_abort) q = State{0.f, NAN, NAN};
+        if (lane == 0) finish_row(a, row, q, s_out);
       }
       int place = -1;  // this thread's key's place among the row's best
       u64 key = 0;
@@ -797,13 +854,16 @@ __global__ void __launch_bounds__(kBlock, kCtasPerSm) logprobs_many_kernel(const
         }
       }
       post_sync();
+      if (isinf(s_out[0]))
+        finish_far<kBf16>(a, row, r.base, k, p, kPostWarps, s_group, groups, s_states, s_out,
+                          [] { post_sync(); });
       if (p == 0) s_count[0] = s_count[1] = 0;
       if (place >= 0) emit(a, row, place, key, k, s_out);
-      if (p < a.C) a.logprobs[row * a.C + p] = logprob_of(given, k, s_out);
+      if (p < a.C) a.logprobs[row * a.C + p] = logprob_of(a, given, k, s_out);
       for (int i = p + kPost; i < a.C; i += kPost) {
         const int id = a.ids[row * a.C + i];
         a.logprobs[row * a.C + i] =
-            logprob_of(id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
+            logprob_of(a, id >= 0 && id < a.V ? V::one(r.base, id) : -INFINITY, k, s_out);
       }
     }
   }

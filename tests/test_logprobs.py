@@ -167,3 +167,78 @@ def test_rows_past_32_bits():
     _, rent, rtop, _ = OT.logprobs(z[-1].double().cpu().numpy(), [0], 3)
     assert top[-1].tolist() == list(rtop) and abs(float(ent[-1]) - rent) <= 4e-5 * (1 + rent)
     assert top[-2].tolist() == [0, 1, 2]
+
+
+def check_shifted(z, ids, K, T, rows):
+    """`rows` of z against the oracle, whose rows are less their largest logit. That changes nothing,
+    and beside a large one its own ln S would be lost: -3.4e38 + 1.6 is -3.4e38 in 64 bits too."""
+    lp, ent, top, tlp = dsa.token_logprobs(z.to(DEV), ids.to(DEV), top_k=K, temperature=T)
+    for b in rows:
+        row = z[b].double().numpy()
+        rlp, rent, rtop, rtlp = OT.logprobs(row - row.max(), ids[b].tolist(), K, T)
+        for got, ref in ((lp[b], rlp), (tlp[b] if K else lp[b, :0], rtlp)):
+            got = got.double().cpu().numpy()
+            far = ref < -3.4e38                # not an fp32 number
+            assert np.all(np.isneginf(got[far]) | (got[far] < -3.4e38))
+            bound = 4e-5 + 2.0 ** -21 * np.abs(ref)
+            assert np.all(np.abs(got[~far] - ref[~far]) <= bound[~far]), (b, K, T)
+        assert abs(float(ent[b]) - rent) <= 4e-5 * (1 + rent), (b, K, T)
+        if K:
+            assert top[b].tolist() == list(rtop), (b, K)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V", [(4, 5), (4, 1000), (3, 50001), (4, 151936), (200, 45001)])
+def test_logits_as_large_as_the_type(B, V, dtype):
+    """Rows masked with the type's lowest value, in part and whole, and rows up to its largest:
+    z is finite, z log2(e) is not."""
+    low = torch.finfo(dtype).min
+    z = make(V, B, V, dtype=dtype)
+    z[0] = low                                   # all alike: -ln V
+    z[1, torch.arange(V) % 7 != 3] = low         # a mask
+    z[2] = low
+    z[2, V // 2] = -low                          # one certain token, the others 2e38 and more away
+    z[2, V // 3] = 0
+    if B > 3:
+        z[3] = low * 0.75
+        z[3, 1::2] = low                         # far apart, both past the range of z log2(e)
+    ids = torch.tensor([[0, V - 1, V // 2, 3 % V]] * B, dtype=torch.int32)
+    if B > 4:
+        z[4:] = z[0]
+        z[B - 1] = z[1]
+    for K in (0, 1, min(5, V), min(32, V)):
+        for T in (1.0, 1.25):
+            check_shifted(z, ids, K, T, sorted({0, 1, 2, min(3, B - 1), B - 1}))
+
+
+@pytest.mark.parametrize("V", [5, 1000, 50001, 151936])
+@pytest.mark.parametrize("at", [-1e4, -1e6, 11629080.0, -11629080.0, 1e8, -1e9, 1e10, -1e30, 1e38])
+def test_rows_of_large_logits(at, V):
+    """All logits near one large value, at any size of it: about 1.16e7 on both sides of 2^24 in base 2."""
+    gen = torch.Generator().manual_seed(V)
+    step = float(np.spacing(np.float32(abs(at))))
+    z = at + step * torch.randint(-3, 4, (4, V), generator=gen).double()
+    z[0] = at
+    z[1, V // 2] = 0.0                           # and one far from the others
+    z[2, : V // 2] = -float("inf")
+    ids = torch.tensor([[0, V - 1, V // 2, 3 % V]] * 4, dtype=torch.int32)
+    for K in (0, min(5, V)):
+        for T in (1.0, 0.8, 3.0):
+            if abs(at) / T < 3.4e38:
+                check_shifted(z.float(), ids, K, T, range(4))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("mask", [-1e4, -1e7, -1e9, -1e10, -1e30, None, -float("inf")])
+@pytest.mark.parametrize("B,V", [(3, 40), (3, 20000), (2, 151936), (200, 50001)])
+def test_rows_masked_to_a_few_tokens(B, V, mask, dtype):
+    """All but a few logits (or one, the last) at a large negative value, some at -inf beside it."""
+    z = make(V, B, V, dtype=dtype)
+    keep = torch.zeros(V, dtype=torch.bool)
+    keep[[0, V // 3, V // 2 + 1, V - 1]] = True
+    z[:, ~keep] = torch.finfo(dtype).min if mask is None else mask
+    z[1, : V - 1] = z[1, 1]
+    z[0, 5: V // 3: 2] = -float("inf")
+    ids = torch.tensor([[0, V - 1, V // 2, 1]] * B, dtype=torch.int32)
+    for K in (0, 4):
+        check_shifted(z, ids, K, 1.0, (0, 1, B - 1))
