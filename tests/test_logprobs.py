@@ -242,3 +242,43 @@ def test_rows_masked_to_a_few_tokens(B, V, mask, dtype):
     ids = torch.tensor([[0, V - 1, V // 2, 1]] * B, dtype=torch.int32)
     for K in (0, 4):
         check_shifted(z, ids, K, 1.0, (0, 1, B - 1))
+
+
+def gpu_reference(z, ids, T):
+    """The definition in float64 torch on the GPU: (log probabilities, entropy, order of the ids)."""
+    lp = torch.log_softmax(z.double() / T, 1)
+    entropy = -(lp.exp() * lp).sum(1)
+    return lp, lp.gather(1, ids.long()), entropy, torch.sort(z.float(), dim=1, descending=True,
+                                                           stable=True).indices
+
+
+def check_rows(z, vocab, K, T):
+    """Every row of z (on the GPU), K best of the first `vocab` logits."""
+    gen = torch.Generator().manual_seed(K)
+    ids = torch.randint(0, vocab, (z.shape[0], 3), generator=gen, dtype=torch.int32).to(DEV)
+    lp, ent, top, tlp = dsa.token_logprobs(z, ids, top_k=K, temperature=T, vocab=vocab)
+    all_lp, rlp, rent, order = gpu_reference(z[:, :vocab], ids, T)
+    for got, ref in ((lp, rlp), (tlp, all_lp.gather(1, order[:, :K]))):
+        assert bool(((got.double() - ref).abs() <= 4e-5 + 2.0 ** -21 * ref.abs()).all())
+    assert bool(((ent.double() - rent).abs() <= 4e-5 * (1 + rent)).all())
+    assert torch.equal(top.long(), order[:, :K])
+
+
+@pytest.mark.parametrize("K", [1, 8, 9, 32])
+@pytest.mark.parametrize("B,V,ld,dtype", [
+    (20, 65537, 65537, torch.float32), (60, 65537, 65537, torch.float32),
+    (120, 65537, 65539, torch.float32), (60, 131072, 131072, torch.bfloat16),
+    (120, 131071, 131073, torch.bfloat16), (152, 262144, 262144, torch.bfloat16)])
+def test_every_cluster_of_few_rows(B, V, ld, dtype, K):
+    """Rows over clusters of 16, 8 and 4 CTAs."""
+    check_rows(make(B + K, B, ld, dtype=dtype).to(DEV), V, K, 0.8)
+
+
+@pytest.mark.parametrize("K", [1, 8, 9, 32])
+@pytest.mark.parametrize("B,V,ld,dtype", [
+    (430, 131072, 131072, torch.float32), (430, 131001, 131003, torch.bfloat16),
+    (650, 50257, 50304, torch.bfloat16), (700, 40003, 40003, torch.float32),
+    (310, 262144, 262144, torch.bfloat16), (900, 7000, 7001, torch.float32)])
+def test_large_batches_of_rows(B, V, ld, dtype, K):
+    """Several rows to a CTA, one after the other; long ones are read again in several pieces."""
+    check_rows(make(B + K, B, ld, dtype=dtype).to(DEV), V, K, 1.3)
