@@ -1128,6 +1128,27 @@ bool misaligned(std::initializer_list<const void *> list, uintptr_t bytes) {
   return false;
 }
 
+// What a call writes may overlap neither what it reads nor anything else it writes: other CTAs
+// still read what one has overwritten.
+struct Span {
+  const void *p;
+  size_t bytes;
+  const char *name;
+};
+dec_status check_apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto hit = [](const Span &a, const Span &b) {
+    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 &&
+           overlaps(a.p, a.bytes, b.p, b.bytes);
+  };
+  for (const Span *w = written.begin(); w != written.end(); ++w) {
+    for (const Span *o = w + 1; o != written.end(); ++o)
+      if (hit(*w, *o)) return fail(DEC_ERR_INVALID_ARG, "%s may not overlap %s", w->name, o->name);
+    for (const Span &r : read)
+      if (hit(*w, r)) return fail(DEC_ERR_INVALID_ARG, "%s may not overlap %s", w->name, r.name);
+  }
+  return DEC_OK;
+}
+
 dec_status check_tree_shape(int B, int N, int Hkv, int D) {
   if (B < 0) return fail(DEC_ERR_INVALID_ARG, "B = %d < 0", B);
   if (B > kSplitMaxB) return fail(DEC_ERR_UNSUPPORTED, "B = %d > %d", B, kSplitMaxB);
@@ -1174,10 +1195,13 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
   const size_t q_bytes = (size_t)B * N * Hq * D * 2, kv_bytes = (size_t)B * N * Hkv * D * 2;
   if (q_in != q_out && overlaps(q_in, q_bytes, q_out, q_bytes))
     return fail(DEC_ERR_INVALID_ARG, "q_in and q_out must be the same buffer or not overlap");
-  if (overlaps(k_tree, kv_bytes, v_tree, kv_bytes) || overlaps(k_tree, kv_bytes, k_new, kv_bytes) ||
-      overlaps(k_tree, kv_bytes, v_new, kv_bytes) || overlaps(v_tree, kv_bytes, k_new, kv_bytes) ||
-      overlaps(v_tree, kv_bytes, v_new, kv_bytes))
-    return fail(DEC_ERR_INVALID_ARG, "k_tree and v_tree may not overlap each other, k_new or v_new");
+  st = check_apart({{q_out, q_bytes, "q_out"}, {k_tree, kv_bytes, "k_tree"},
+                    {v_tree, kv_bytes, "v_tree"}, {error_word, 4, "error_word"}},
+                   {{q_in == q_out ? nullptr : q_in, q_bytes, "q_in"}, {k_new, kv_bytes, "k_new"},
+                    {v_new, kv_bytes, "v_new"}, {q_norm_w, (size_t)D * 2, "q_norm_w"},
+                    {k_norm_w, (size_t)D * 2, "k_norm_w"}, {pos, (size_t)B * N * 4, "pos"},
+                    {n_nodes, (size_t)B * 4, "n_nodes"}});
+  if (st != DEC_OK) return st;
   st = where_all_here({{q_in, "q_in", true}, {q_out, "q_out", true}, {k_new, "k_new", true},
                        {v_new, "v_new", true}, {q_norm_w, "q_norm_w", true},
                        {k_norm_w, "k_norm_w", true}, {k_tree, "k_tree", false},
@@ -1236,15 +1260,21 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   if (misaligned({mask}, 8)) return fail(DEC_ERR_INVALID_ARG, "mask must be 8-byte aligned");
   if (misaligned({lens, n_nodes, pos, slopes}, 4))
     return fail(DEC_ERR_INVALID_ARG, "lens, n_nodes, pos and slopes must be 4-byte aligned");
-  const size_t q_bytes = (size_t)B * N * Hq * D * 2;
-  if (overlaps(q, q_bytes, out, q_bytes))
-    return fail(DEC_ERR_INVALID_ARG, "out may not overlap q");
   const int parts = tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current());
   if (workspace == nullptr || misaligned({workspace}, 256))
     return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
   const size_t need = tree_ws_bytes(B, N, Hq, Hkv, D, parts);
   if (ws_bytes < need)
     return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  const size_t q_bytes = (size_t)B * N * Hq * D * 2, tree = (size_t)B * Hkv * N * D * 2;
+  const size_t cache = (size_t)B * Hkv * T_cap * D * 2;
+  st = check_apart({{out, q_bytes, "out"}, {workspace, need, "workspace"}},
+                   {{q, q_bytes, "q"}, {k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"},
+                    {k_tree, tree, "k_tree"}, {v_tree, tree, "v_tree"},
+                    {lens, (size_t)B * 4, "lens"}, {mask, (size_t)B * N * 8, "mask"},
+                    {n_nodes, (size_t)B * 4, "n_nodes"}, {pos, (size_t)B * N * 4, "pos"},
+                    {slopes, (size_t)Hq * 4, "slopes"}});
+  if (st != DEC_OK) return st;
   st = where_all_here({{q, "q", true}, {k_cache, "k_cache", false}, {v_cache, "v_cache", false},
                        {k_tree, "k_tree", false}, {v_tree, "v_tree", false}, {lens, "lens", true},
                        {mask, "mask", true}, {n_nodes, "n_nodes", true}, {pos, "pos", true},
@@ -1300,10 +1330,12 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
   if (misaligned({path, n_path, lens, error_word}, 4))
     return fail(DEC_ERR_INVALID_ARG, "path, n_path, lens and error_word must be 4-byte aligned");
   const size_t tree = (size_t)B * Hkv * N * D * 2, cache = (size_t)B * Hkv * T_cap * D * 2;
-  if (overlaps(k_cache, cache, v_cache, cache) || overlaps(k_cache, cache, k_tree, tree) ||
-      overlaps(k_cache, cache, v_tree, tree) || overlaps(v_cache, cache, k_tree, tree) ||
-      overlaps(v_cache, cache, v_tree, tree))
-    return fail(DEC_ERR_INVALID_ARG, "the caches may not overlap each other or the tree's buffers");
+  st = check_apart({{k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"},
+                    {error_word, 4, "error_word"}},
+                   {{k_tree, tree, "k_tree"}, {v_tree, tree, "v_tree"},
+                    {path, (size_t)B * N * 4, "path"}, {n_path, (size_t)B * 4, "n_path"},
+                    {lens, (size_t)B * 4, "lens"}});
+  if (st != DEC_OK) return st;
   st = where_all_here({{k_tree, "k_tree", false}, {v_tree, "v_tree", false}, {path, "path", true},
                        {n_path, "n_path", true}, {k_cache, "k_cache", false},
                        {v_cache, "v_cache", false}, {lens, "lens", true},
@@ -1343,7 +1375,14 @@ dec_status dec_token_logprobs(const void *logits, dec_dtype type, int ld, const 
   if (misaligned({logits}, type == DEC_F32 ? 4 : 2) ||
       misaligned({ids, logprobs, entropy, top_ids, top_logprobs}, 4))
     return fail(DEC_ERR_INVALID_ARG, "pointers must be aligned to their elements");
-  const dec_status st = where_all_here(
+  const size_t given = (size_t)B * C * 4, best = (size_t)B * K * 4;
+  dec_status st = check_apart(
+      {{logprobs, given, "logprobs"}, {entropy, (size_t)B * 4, "entropy"},
+       {top_ids, best, "top_ids"}, {top_logprobs, best, "top_logprobs"}},
+      {{logits, ((size_t)(B - 1) * ld + V) * (type == DEC_F32 ? 4 : 2), "logits"},
+       {ids, given, "ids"}});
+  if (st != DEC_OK) return st;
+  st = where_all_here(
       {{logits, "logits", false}, {C > 0 ? ids : nullptr, "ids", true},
        {C > 0 ? logprobs : nullptr, "logprobs", true}, {entropy, "entropy", true},
        {K > 0 ? top_ids : nullptr, "top_ids", true},

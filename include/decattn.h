@@ -543,10 +543,11 @@ dec_status dec_sample(const float *logits, const int32_t *sampled_ids, int L, co
  *   dec_tree_commit        copies the accepted path into the cache.
  * The caller then adds the accepted count to lens (with work of its own on the stream).
  * Conventions of these calls and of dec_token_logprobs, besides those above: device
- * buffers are on the current device (refused otherwise); n_nodes[b], a device array, is the
- * number of nodes sequence b has (NULL: N for all); nothing is read or written for the
- * nodes behind it, their output rows are left as they were; a count outside [0, N] is
- * clamped and raises DEC_DEVERR_TREE_CLAMPED. 1 <= N <= 64.
+ * buffers are on the current device (refused otherwise); what a call writes may overlap
+ * neither what it reads nor anything else it writes (refused; q_out may be q_in);
+ * n_nodes[b], a device array, is the number of nodes sequence b has (NULL: N for all);
+ * nothing is read or written for the nodes behind it, their output rows are left as they
+ * were; a count outside [0, N] is clamped and raises DEC_DEVERR_TREE_CLAMPED. 1 <= N <= 64.
  */
 
 /* dec_qknorm_rope_kv_append for a tree's nodes: node n of sequence b is rotated at

@@ -207,3 +207,64 @@ def test_oracle_rope_tree_keeps_norms_and_dead_nodes():
     assert np.allclose(qr[0, 0], q[0, 0]) and np.array_equal(qr[0, 2], q[0, 2])
     assert np.allclose(np.linalg.norm(kr[0, 0, 1]), np.linalg.norm(k[0, 1, 0]))
     assert np.all(kr[0, 0, 2] == 0) and np.array_equal(vr[0, 0, 0], v[0, 0, 0])
+
+
+def test_rope_tree_rejects_overlaps(L):
+    def call(q=at(1), qo=at(2), kn=at(3), vn=at(4), qw=None, kw=None, kt=at(5), vt=at(6), pos=at(7),
+             n=at(8), err=at(9)):
+        return _st(L, "dec_qknorm_rope_tree", q, qo, kn, vn, qw, kw, kt, vt, pos, n, 2, 4, 8, 2, 128,
+                   1e4, 0, None, 1e-6, err, None)
+    kv, q = 2 * 4 * 2 * 128 * 2, 2 * 4 * 8 * 128 * 2
+    for bad in (dict(qo=at(3, kv - 16)), dict(qo=at(4)), dict(qo=at(5, 16)), dict(qo=at(6)),
+                dict(q=at(5), qo=at(2)), dict(q=at(6, 256)), dict(kt=at(4)), dict(vt=at(3, 512)),
+                dict(kt=at(1, q - 16)), dict(vt=at(2, q - 16)), dict(qw=at(2, 256), kw=at(10)),
+                dict(qw=at(10), kw=at(5)), dict(pos=at(6, 64)), dict(n=at(2)), dict(err=at(7)),
+                dict(err=at(5, 4))):
+        got, msg = call(**bad)
+        assert got == 1 and "overlap" in msg, (bad, got, msg)
+    for fine in ({}, dict(qo=at(1)), dict(qo=at(3, kv)), dict(kt=at(1, q)), dict(vt=at(5, kv))):
+        got, msg = call(**fine)  # refused for what the addresses are, if at all
+        assert "overlap" not in msg, (fine, got, msg)
+
+
+def test_tree_attn_rejects_overlaps(L):
+    need = L.dec_tree_attn_workspace_bytes(2, 4, 8, 2, 128, 256, 3)
+
+    def call(q=at(1), kc=at(2), vc=at(3), lens=at(4), kt=at(5), vt=at(6), mask=at(7), n=at(10),
+             pos=at(11), slopes=at(12), out=at(8), ws=at(9)):
+        return _st(L, "dec_gqa_tree_attn", q, kc, vc, lens, kt, vt, mask, n, pos, slopes, out, 2, 4,
+                   8, 2, 128, 256, 256, 0.0, 0.0, 0, 3, ws, 1 << 40, None)
+    row, cache = 2 * 4 * 8 * 128 * 2, 2 * 2 * 256 * 128 * 2
+    for bad in (dict(out=at(1, row - 16)), dict(out=at(2, cache - 16)), dict(out=at(3)),
+                dict(out=at(5)), dict(out=at(6, 16)), dict(out=at(9, 256)), dict(lens=at(8, 4)),
+                dict(mask=at(8, 64)), dict(n=at(8)), dict(pos=at(8)), dict(slopes=at(8, row - 4)),
+                dict(ws=at(2)), dict(ws=at(1, 256)), dict(ws=at(8, 256)), dict(kt=at(9, need - 16)),
+                dict(pos=at(9, 128)), dict(mask=at(9))):
+        got, msg = call(**bad)
+        assert got == 1 and "overlap" in msg, (bad, got, msg)
+    for fine in ({}, dict(out=at(1, row)), dict(out=at(2, cache)), dict(kt=at(2), vt=at(2))):
+        got, msg = call(**fine)
+        assert "overlap" not in msg, (fine, got, msg)
+
+
+def test_commit_and_logprobs_reject_overlaps(L):
+    def commit(kt=at(1), vt=at(2), path=at(3), n=at(4), kc=at(5), vc=at(6), lens=at(7), err=at(8)):
+        return _st(L, "dec_tree_commit", kt, vt, path, n, kc, vc, lens, 2, 4, 2, 128, 256, err, None)
+    cache = 2 * 2 * 256 * 128 * 2
+    for bad in (dict(kt=at(6, cache - 16)), dict(vt=at(5)), dict(vc=at(5, 4096)), dict(path=at(5)),
+                dict(n=at(6, 8)), dict(lens=at(5, cache - 4)), dict(err=at(5)), dict(err=at(7, 4))):
+        got, msg = commit(**bad)
+        assert got == 1 and "overlap" in msg, (bad, got, msg)
+    assert "overlap" not in commit()[1] and "overlap" not in commit(vc=at(5, cache))[1]
+
+    def logprobs(z=at(1), ids=at(2), lp=at(3), ent=at(4), ti=at(5), tl=at(6), C=3, K=2, ty=0):
+        return _st(L, "dec_token_logprobs", z, ty, 1000, ids, C, lp, ent, ti, tl, K, 2, 900, 1.0, None)
+    for bad in (dict(lp=at(2)), dict(lp=at(2, 20)), dict(ent=at(1, 1000 * 4 + 900 * 4 - 4)),
+                dict(ti=at(6, 12)), dict(tl=at(1)), dict(ent=at(3, 8)), dict(lp=at(5)),
+                dict(ti=at(2))):
+        got, msg = logprobs(**bad)
+        assert got == 1 and "overlap" in msg, (bad, got, msg)
+    for fine in ({}, dict(ent=at(1, 7600)), dict(ty=1, ent=at(1, 3800)), dict(lp=at(2), C=0),
+                 dict(ti=at(2), K=0)):
+        got, msg = logprobs(**fine)
+        assert "overlap" not in msg, (fine, got, msg)
