@@ -61,6 +61,7 @@ constexpr int kRows = 128;     // query rows per tile (the MMA's M)
 constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
 constexpr int kSoftmax = 128;
 constexpr float kLargeCap = 256.f;
+constexpr float kFar = 0x1p24f;   // maxima past this are subtracted before the scale is applied
 constexpr float kRescale = 8.f;  // log2 of the growth of the maximum that moves it
 constexpr int kMaxRowTiles = kTreeMaxNodes * kSplitMaxG / kRows;
 // What beginning and ending a (pair, row tile) costs, in key tiles: the stream is cut by tiles
@@ -887,6 +888,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         off2[k] = pair_of(fmaf(slope, 2.f * k, cap), fmaf(slope, 2.f * k + 1.f, cap));
       }
       float m = -INFINITY, l = 0.f;
+      // Plain scores are scaled within the exponent, z sc - m. Where |m| is past 2^24 the rounding of
+      // m = z_max sc moves exponents by 1 and more (past 2^31 out of range): z_max, for those rows.
+      float far = 0.f;
+      bool any_far = false;
       // the segment after this one, and its Q on the way into L2
       Walk after = w;
       more = after.next(a);
@@ -1034,13 +1039,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int i = 0; i < 4; ++i)
               m4[i] = c + 4 + i < NC ? fmaxf(m4[i], fmaxf(z[c + i], z[c + 4 + i]))
                                         : fmaxf(m4[i], z[c + i]);
-          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         };
-        // the running maximum for a tile whose largest score is mx
-        auto settle = [&](float mx) {
+        // the running maximum for a tile whose largest score is z_max
+        auto settle = [&](float z_max) {
+          const float mx = z_max * sc;
           const bool grow = mx > m + kRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : m;
+            if constexpr (!kMod) {
+              if (grow) far = fabsf(mx) > kFar ? z_max : 0.f;
+              any_far = __any_sync(0xffffffffu, far != 0.f);
+            }
             const float corr = mn == -INFINITY ? 1.f : ex2(m - mn);
             m = mn;
             l *= corr;
@@ -1060,9 +1070,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         };
         // the weights as bf16, their sum to l
-        auto weights = [&](const auto &z, auto &pk) {
+        auto weights = [&](auto &z, auto &pk) {
           constexpr int NC = sizeof(z) / 4;
-          const float base = m == -INFINITY ? 0.f : m;
+          float base = m == -INFINITY ? 0.f : m;
+          if (!kMod && __builtin_expect(any_far, 0)) {
+            if (far != 0.f) base = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) z[c] -= far;
+          }
           const uint64_t sc2 = pair_of(sc, sc), base2 = pair_of(-base, -base);
           uint64_t l4[4] = {};
 #pragma unroll

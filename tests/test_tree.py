@@ -348,6 +348,24 @@ def test_large_scores_and_equal_keys():
     run(c, num_parts=3)
 
 
+@pytest.mark.parametrize("size", [1e3, 1e6, 1.3e8, 1e9, 1e10, 1e20, 1e35])
+@pytest.mark.parametrize("N,Hq,D", [(2, 2, 64), (7, 8, 128), (24, 4, 64), (40, 8, 128)])
+def test_scores_far_from_zero(size, N, Hq, D):
+    """Equal scores at any size of them give the mean of the values, one larger score its value."""
+    for sign in (1.0, -1.0):
+        c = attn_case(N, [700, 64, 5], N, Hq, 2, D)
+        live = c["k_cache"].isfinite()
+        c["q"][:] = 1.0
+        c["k_cache"][live] = sign * size
+        c["k_tree"][:] = sign * size
+        run(c, f"{sign * size}")
+        run(c, "split", num_parts=7)
+        c["k_cache"][0, :, 333] = 1.5 * size
+        c["k_tree"][1, :, 0] = 1.5 * size
+        run(c, "a peak")
+        run(c, "a peak, split", num_parts=7)
+
+
 def test_positions_below_the_length_count_as_the_length():
     c = attn_case(11, [100, 40], 6, 4, 2, 64)
     c["pos"][:, 2] = 3
