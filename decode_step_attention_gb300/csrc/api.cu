@@ -1218,8 +1218,10 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
 
 size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_len,
                                      int num_parts) {
-  if (B < 0 || N < 1 || N > kTreeMaxNodes || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 ||
-      (D != 64 && D != 128) || max_len < 0 || num_parts < 0)
+  // what the call refuses has no size, and the others' sizes are counted in 32 bits
+  if (B < 0 || B > kSplitMaxB || N < 1 || N > kTreeMaxNodes || Hq <= 0 || Hkv <= 0 ||
+      Hkv > 65535 || Hq % Hkv != 0 || Hq / Hkv > kSplitMaxG || (D != 64 && D != 128) ||
+      max_len < 0 || num_parts < 0 || num_parts > kTreeMaxParts)
     return 0;
   return tree_ws_bytes(B, N, Hq, Hkv, D,
                        tree_parts(B, N, Hq, Hkv, max_len, num_parts, sm_count_of_current()));

@@ -599,7 +599,8 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
  * workspace      [device] at least dec_tree_attn_workspace_bytes(...) bytes, 256-byte aligned,
  *                its first 256 bytes zeroed before its first use (the first word is the
  *                device error word); it serves one call at a time.
- * D in {64, 128}; 1 <= Hq/Hkv <= 8; B * Hkv * T_cap < 2^31; B <= 8192. */
+ * D in {64, 128}; 1 <= Hq/Hkv <= 8; B * Hkv * T_cap < 2^31; B <= 8192. The size is 0 for
+ * arguments that the call refuses. */
 size_t dec_tree_attn_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int max_len,
                                      int num_parts);
 dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_cache,

@@ -268,3 +268,12 @@ def test_commit_and_logprobs_reject_overlaps(L):
                  dict(ti=at(2), K=0)):
         got, msg = logprobs(**fine)
         assert "overlap" not in msg, (fine, got, msg)
+
+
+def test_tree_workspace_of_refused_shapes_is_nothing(L):
+    ws = L.dec_tree_attn_workspace_bytes
+    for bad in ((8193, 4, 8, 2, 128, 256, 0), (1 << 20, 64, 1 << 16, 1 << 13, 128, 256, 0),
+                (2, 4, 18, 2, 128, 256, 0), (2, 4, 65536, 65536, 128, 256, 0),
+                (2, 4, 8, 2, 128, 256, 4097), (2, 64, 1 << 30, 1, 128, 256, 3)):
+        assert ws(*bad) == 0, bad
+    assert ws(8192, 64, 64, 8, 128, 131072, 0) > ws(2, 64, 64, 8, 128, 131072, 0) > 0
