@@ -1244,7 +1244,8 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
   if (num_parts > kTreeMaxParts)
     return fail(DEC_ERR_UNSUPPORTED, "num_parts = %d > %d", num_parts, kTreeMaxParts);
   if (window < 0) return fail(DEC_ERR_INVALID_ARG, "window = %d < 0", window);
-  if (!std::isfinite(scale)) return fail(DEC_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(scale) || scale > 1e30f)  // (far above, scale * log2(e) is not a number)
+    return fail(DEC_ERR_INVALID_ARG, "scale = %g is not a number of at most 1e30", scale);
   if (!(softcap >= 0.f && softcap <= 1e30f))  // (far above, score / softcap is not a normal number)
     return fail(DEC_ERR_INVALID_ARG, "softcap = %g is not in [0, 1e30]", softcap);
   const float score_scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)D);

@@ -589,10 +589,10 @@ dec_status dec_qknorm_rope_tree(const void *q_in, void *q_out, const void *k_new
  * mask           [device|host] uint64 [B, N].
  * n_nodes        [device|host] int32 [B] or NULL.
  * pos            [device|host] int32 [B, N]; may be NULL when window = 0 and slopes = NULL.
- * slopes         [device|host] fp32 [Hq] or NULL.
+ * slopes         [device|host] fp32 [Hq] or NULL; slope * distance at most 1e37 in size.
  * out            [device|host] bf16 [B, N, Hq, D], not overlapping q.
  * max_len        host upper bound of every lens[b], 0 <= max_len <= T_cap.
- * scale          <= 0 selects 1/sqrt(D).  0 <= softcap <= 1e30, scale / softcap < 1e30.
+ * scale          <= 0 selects 1/sqrt(D); at most 1e30.  0 <= softcap <= 1e30, scale / softcap < 1e30.
  *                window >= 0.
  * num_parts      CTAs the work is cut over; 0 lets the library choose (two launches, or one for
  *                short contexts: about 1000 tokens per CTA of a cluster of at most 8).

@@ -277,3 +277,15 @@ def test_tree_workspace_of_refused_shapes_is_nothing(L):
                 (2, 4, 8, 2, 128, 256, 4097), (2, 64, 1 << 30, 1, 128, 256, 3)):
         assert ws(*bad) == 0, bad
     assert ws(8192, 64, 64, 8, 128, 131072, 0) > ws(2, 64, 64, 8, 128, 131072, 0) > 0
+
+
+def test_tree_attn_rejects_scales_beyond_the_float_range(L):
+    def call(scale, ws):
+        return _st(L, "dec_gqa_tree_attn", at(1), at(2), at(3), at(4), at(5), at(6), at(7), None, None,
+                   None, at(8), 2, 4, 8, 2, 128, 256, 256, scale, 0.0, 0, 3, ws, 1 << 40, None)
+    for scale in (1.1e30, 3e38, float("inf"), float("nan")):
+        got, msg = call(scale, at(9))
+        assert got == 1 and "scale" in msg, (scale, got, msg)
+    for scale in (1e30, 0.0, -3e38):  # allowed, and refused for something else
+        got, msg = call(scale, None)
+        assert got == 3 and "workspace" in msg
