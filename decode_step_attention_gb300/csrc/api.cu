@@ -1292,9 +1292,6 @@ dec_status dec_gqa_tree_attn(const void *q, const void *k_cache, const void *v_c
     return st;
   TreeAttnArgs a{};
   a.q = static_cast<const __nv_bfloat16 *>(q);
-  a.k_cache = static_cast<const __nv_bfloat16 *>(k_cache);
-  a.v_cache = static_cast<const __nv_bfloat16 *>(v_cache);
-  a.k_tree = static_cast<const __nv_bfloat16 *>(k_tree);
   a.v_tree = static_cast<const __nv_bfloat16 *>(v_tree);
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lens = lens;

@@ -191,7 +191,7 @@ cudaError_t launch_tree_commit(const void *k_tree, const void *v_tree, const int
                                uint32_t *error_word, cudaStream_t stream);
 
 struct TreeAttnArgs {
-  const __nv_bfloat16 *q, *k_cache, *v_cache, *k_tree, *v_tree;
+  const __nv_bfloat16 *q, *v_tree;  // (keys and values come through the tensor maps)
   __nv_bfloat16 *out;
   const int32_t *lens, *n_nodes, *pos;  // n_nodes, pos: may be null
   const uint64_t *mask;

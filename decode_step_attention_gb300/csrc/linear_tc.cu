@@ -80,27 +80,6 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last() {
 }
 
 // ---- cluster helpers ------------------------------------------------------------------
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The barrier before a CTA exits, so that no CTA leaves while another still reads its
-// shared memory. Execution order is all it needs: every remote load of the arriving thread
-// has returned (its value has been used), so the arrival is relaxed. A release here would
-// also wait for the thread's global stores to be acknowledged.
-__device__ __forceinline__ void cluster_exit_sync() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
-               "barrier.cluster.wait.aligned;" ::: "memory");
-}
-
-// The address of the same shared-memory location in CTA `rank` of this cluster.
-__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"

@@ -156,11 +156,6 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -194,26 +189,6 @@ struct State {
   }
 };
 
-// Two fp32 operations per instruction.
-__device__ __forceinline__ u64 pair_of(float a, float b) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(u64 v, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // The lanes' states as one, in every lane.
 __device__ __forceinline__ void warp_join(State &st) {
   float to = st.r;
@@ -227,20 +202,6 @@ __device__ __forceinline__ void warp_join(State &st) {
   }
 }
 
-__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Before a CTA leaves: order is all that is needed, every remote load has returned.
-__device__ __forceinline__ void cluster_exit_sync() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
-               "barrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
