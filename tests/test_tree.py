@@ -805,3 +805,124 @@ def test_speculative_step_matches_sequential_decoding():
         lens += torch.from_numpy(count).to(DEV)
         for a, s in zip(caches, seq):
             assert torch.equal(a, s)
+
+
+# ------------------------------------------------ all four calls, other ways to make them ---
+def step_inputs(seed, B, N, Hq, Hkv, D, T, V):
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=gen).bfloat16()  # noqa: E731
+    mask, depth = trees(rng, B, N)
+    lens = rng.integers(0, T - N, B)
+    count = rng.integers(0, N + 1, B)
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32))  # noqa: E731
+    return dict(q=rnd(B, N, Hq, D), k=rnd(B, N, Hkv, D), v=rnd(B, N, Hkv, D), kc=rnd(B, Hkv, T, D),
+                vc=rnd(B, Hkv, T, D), lens=i32(lens), mask=torch.from_numpy(mask.view(np.int64)),
+                pos=i32(lens[:, None] + depth), nodes=i32(rng.integers(1, N + 1, B)),
+                path=i32(rng.integers(0, N, (B, N))), count=i32(count),
+                logits=torch.randn(B * N, V, generator=gen), ids=i32(rng.integers(0, V, (B * N, 2))),
+                qw=rnd(D), kw=rnd(D))
+
+
+def step(t, kt, vt, q_out, out, ws, err, T, stream=None):
+    dsa.qknorm_rope_tree(t["q"], t["k"], t["v"], kt, vt, t["pos"], 1e4, q_norm_w=t["qw"],
+                         k_norm_w=t["kw"], n_nodes=t["nodes"], q_out=q_out, error_word=err, stream=stream)
+    dsa.gqa_tree_attn(q_out, t["kc"], t["vc"], t["lens"], kt, vt, t["mask"], n_nodes=t["nodes"],
+                      pos=t["pos"], max_len=T, workspace=ws, out=out, window=40, softcap=30.0,
+                      stream=stream)
+    lp = dsa.token_logprobs(t["logits"], t["ids"], top_k=4, stream=stream)
+    dsa.tree_commit(kt, vt, t["path"], t["count"], t["kc"], t["vc"], t["lens"], error_word=err,
+                    stream=stream)
+    return lp
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,T", [(3, 6, 8, 2, 128, 90), (40, 33, 8, 8, 64, 300)])
+def test_a_step_on_a_side_stream_and_captured(B, N, Hq, Hkv, D, T):
+    """The same step called on the current stream, on another, and replayed from a graph whose
+    buffers then hold other inputs."""
+    V = 5003
+    ws = dsa.alloc_tree_workspace(B, N, Hq, Hkv, D, T)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def buffers(t):
+        kt = torch.full((B, Hkv, N, D), 3.0, dtype=torch.bfloat16, device=DEV)
+        q = torch.full_like(t["q"], 7.0)
+        return kt, kt.clone(), q, torch.full_like(q, 9.0)
+
+    def results(t, b, lp):
+        return [x.clone() for x in (*b, t["kc"], t["vc"], *lp)]
+
+    def on_device(seed):
+        return {k: v.to(DEV) for k, v in step_inputs(seed, B, N, Hq, Hkv, D, T, V).items()}
+
+    want = []
+    for seed in (1, 2):
+        t = on_device(seed)
+        b = buffers(t)
+        want.append(results(t, b, step(t, *b, ws, err, T)))
+    side = torch.cuda.Stream()
+    t = on_device(1)
+    b = buffers(t)
+    side.wait_stream(torch.cuda.current_stream())
+    lp = step(t, *b, ws, err, T, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(results(t, b, lp), want[0]))
+    t = on_device(1)
+    b = buffers(t)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lp = step(t, *b, ws, err, T)
+    for seed in (2, 1, 2):
+        for k, v in on_device(seed).items():
+            t[k].copy_(v)
+        for x, y in zip(b, buffers(t)):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(results(t, b, lp), want[seed - 1])), seed
+    assert int(err) == 0 and dsa.device_errors(ws) == 0
+
+
+def test_a_step_with_arguments_in_pinned_host_memory():
+    B, N, Hq, Hkv, D, T, V = 3, 6, 8, 2, 128, 90, 5003
+    host = step_inputs(4, B, N, Hq, Hkv, D, T, V)
+    got = []
+    for pinned in (False, True):
+        t = {k: v.to(DEV) for k, v in host.items()}
+        err = torch.zeros(1, dtype=torch.int32)
+        kt = torch.zeros(B, Hkv, N, D, dtype=torch.bfloat16, device=DEV)
+        vt = torch.zeros_like(kt)
+        q, out = torch.zeros(B, N, Hq, D, dtype=torch.bfloat16), None
+        out = q.clone()
+        if pinned:
+            for k in t:
+                if k not in ("kc", "vc", "logits"):
+                    t[k] = host[k].pin_memory()
+            err, q, out = err.pin_memory(), q.pin_memory(), out.pin_memory()
+        else:
+            err, q, out = err.to(DEV), q.to(DEV), out.to(DEV)
+        ws = dsa.alloc_tree_workspace(B, N, Hq, Hkv, D, T)
+        t["pos"][1, 0] = -1   # reported in the error word, wherever it lies
+        lp = step(t, kt, vt, q, out, ws, err, T)
+        torch.cuda.synchronize()
+        assert int(err) == dsa.DEVERR_POS_SKIPPED
+        got.append([x.cpu() for x in (kt, vt, q, t["kc"], t["vc"], out, *lp)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_no_sequences():
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device=DEV)  # noqa: E731
+    i32, N, D = torch.int32, 4, 64
+    q = dsa.qknorm_rope_tree(z(0, N, 4, D), z(0, N, 2, D), z(0, N, 2, D), z(0, 2, N, D), z(0, 2, N, D),
+                             z(0, N, d=i32), 1e4)
+    out = dsa.gqa_tree_attn(q, z(0, 2, 8, D), z(0, 2, 8, D), z(0, d=i32), z(0, 2, N, D),
+                            z(0, 2, N, D), z(0, N, d=torch.int64))
+    dsa.tree_commit(z(0, 2, N, D), z(0, 2, N, D), z(0, N, d=i32), z(0, d=i32), z(0, 2, 8, D),
+                    z(0, 2, 8, D), z(0, d=i32))
+    lp, ent, top, tlp = dsa.token_logprobs(z(0, 100, d=torch.float32), z(0, 3, d=i32), top_k=2)
+    assert out.shape == (0, N, 4, D) and lp.shape == (0, 3) and ent.shape == (0,)
+    assert top.shape == tlp.shape == (0, 2)
+    lp, *_ = dsa.token_logprobs(z(2, 100, d=torch.float32), z(2, 0, d=i32))
+    assert lp.shape == (2, 0)
