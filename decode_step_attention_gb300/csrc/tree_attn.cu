@@ -29,20 +29,24 @@
 //            stay below 2^8, where bf16 rounds them as well as below 1.
 // Warps whose 32 rows are all past the tile's last row only keep the barriers company.
 //
-// Measured, with the merge (floor: bytes at the measured copy bandwidth, or operations at the
-// measured bf16 rate):
-//   131072 tokens, 26 nodes, 32 / 8 heads of 128       98 us (79); HBM, 6.0 TB/s in this kernel
-//   32 sequences to 8192, 16 nodes, cap                100 us (85); HBM
-//   192 sequences to 32768, one node, 16 / 4 of 64     75 us (59); S with 16 of 128 rows in use
-//   16 sequences, window 4095, 64 nodes, 64 / 8 of 128 126 us (62); the tensor cores: an S with 64
+// Measured, a call among others with the merge (floor: bytes at the measured copy bandwidth, or
+// operations at the measured bf16 rate; the sweeps below and the figures at the constants are the
+// GPU's share alone, 3 to 6 us less, both sides measured alike):
+//   131072 tokens, 26 nodes, 32 / 8 heads of 128       101 us (79); HBM, 6.0 TB/s in this kernel
+//   32 sequences to 8192, 16 nodes, cap                103 us (85); HBM
+//   192 sequences to 32768, one node, 16 / 4 of 64     74 us (59); S with 16 of 128 rows in use
+//   16 sequences, window 4095, 64 nodes, 64 / 8 of 128 131 us (62); the tensor cores: an S with 64
 //       keys takes as long as one with 128, because Q is read from shared memory for each
 // Tried for the last: S for two key tiles at once. It needs both S buffers, so S, softmax and the
 // value products of a CTA take turns, and two CTAs do not fill the gaps (144 us). Eight softmax
 // warps of half a row's keys each, which agree on the maximum tile by tile: 171 us.
 //
-// The weights are rounded to bf16 (one rounding, at most 2^-8 of each, as large as the
-// output's own rounding) because the value product wants both operands alike; sums, maxima
-// and O are fp32.
+// The weights are one bf16 each (a rounding of at most 2^-8 of each); sums, maxima and O are fp32.
+// Against 64 bits the result is off by 1.9e-3 to 2.4e-3 (relative, root mean square), of which the
+// output's own rounding is 1.7e-3. The single-token kernel of gqa_decode.cu gives the value
+// product a second bf16 per weight, what the first rounding left; here that makes the error 1.7e-3,
+// and memory does not hide it: the GPU's share of four cases like those above goes from 97.0 to
+// 100.4 us, 97.2 to 101, 76 to 88 and 125 to 147, that of 8 nodes over 512 tokens from 8.9 to 9.3.
 #include <limits.h>
 #include <math.h>
 

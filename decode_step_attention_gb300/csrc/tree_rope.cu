@@ -55,9 +55,9 @@ __device__ __noinline__ void exact_elements(const __nv_bfloat16 *k, const __nv_b
 // order, the rotated pair with the same roundings, so both give the same bits.
 //
 // A node's chain (position, angles, barrier, rotation, stores) is hidden by the other CTAs of
-// the SM, and the instructions, some 130 per 8 elements of a head and lane, take 70% of the
+// the SM, and the instructions, some 130 per 8 elements of a head and lane, take 80% of the
 // issue slots: 6144 nodes of 32 query and 8 KV heads of 128 (interleaved, normed), 114 MB,
-// in 26.8 us, 4.3 TB/s. With 8-byte lanes 105 us. Six CTAs per SM, at 40 registers, against
+// in 27.2 us, 4.2 TB/s. With 8-byte lanes 105 us. Six CTAs per SM, at 40 registers, against
 // five at 48: 26.8 and 27.6 us, 16 query heads 20.7 and 22.0; one pass (a few nodes) and
 // four lose by it: 8 nodes 3.19 and 3.05 us, 64 query heads in four passes 47.7 and 46.9 (in
 // two CTAs of three 44.2). (The
