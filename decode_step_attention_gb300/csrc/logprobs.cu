@@ -260,12 +260,14 @@ __device__ __noinline__ void finish_far(const LogprobArgs &a, size_t row, const 
   u64 top = 0;
   for (int i = 0; i < groups; ++i) top = umax(top, group[i]);
   const float m = top == 0 ? NAN : key_value(top);
+  const bool some = fabsf(m) < INFINITY;  // else the row has no distribution
+  const int V = some ? a.V : 0;
   State q[4];
-  for (int i0 = t; i0 < a.V; i0 += 128 * warps)
+  for (int i0 = t; i0 < V; i0 += 128 * warps)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u * 32 * warps;
-      const float v = i < a.V ? Vec<kBf16>::one(base, i) : -INFINITY;
+      const float v = i < V ? Vec<kBf16>::one(base, i) : -INFINITY;
       const float d = max_nan((v - m) * k, -400.f), e = ex2(d);
       q[u].s += e;
       q[u].c = fmaf(e, d, q[u].c);
@@ -280,7 +282,7 @@ __device__ __noinline__ void finish_far(const LogprobArgs &a, size_t row, const 
   sync();
   if (t == 0) {
     for (int i = 1; i < warps; ++i) s += states[i].s, c += states[i].c;
-    const float log2_s = isinf(m) ? NAN : log2f(s);
+    const float log2_s = some ? log2f(s) : NAN;
     out[1] = log2_s;
     out[2] = m;
     if (a.entropy != nullptr) a.entropy[row] = (log2_s - c / s) * kLn2;
