@@ -44,6 +44,15 @@ arranged as a tree (the decode step's operators for N queries per sequence):
 * :func:`gqa_tree_attn`         attention of every node over the cache and its ancestors,
   optionally with a score cap, a distance bias or a sliding window;
 * :func:`tree_commit`           the accepted path's K/V into the cache.
+
+A paged cache, for sequences that grow without a row held for every token they may come to
+have, in bf16 or in e4m3 codes with a scale per page and KV head (:func:`alloc_paged_cache`):
+
+* :func:`qknorm_rope_paged_append`  QK-RMSNorm, RoPE (of the whole head or a part) and the
+  append of one token per sequence or of whole prompts;
+* :func:`gqa_paged_attn`        single-query GQA attention over the pages;
+* :func:`paged_gather`          a range of tokens as contiguous bf16 caches, for the calls above;
+* :func:`paged_decode_step`     RMSNorm + residual, append and attention on one stream.
 """
 from __future__ import annotations
 
@@ -63,11 +72,13 @@ DEVERR_LEN_CLAMPED = 0x1
 DEVERR_POS_SKIPPED = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
 DEVERR_TREE_CLAMPED = 0x8
+DEVERR_PAGE_SKIPPED = 0x10
 
 WORKSPACE_HEADER_BYTES = 256
 
 # C ABI: name -> (restype, argtypes)
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 EXPORTS = {
     "dec_rmsnorm_residual": (_I, [_P, _P, _P, _P, _I, _I, _F, _P]),
     "dec_rope_inv_freq": (_I, [_I, _F, _I, _F, ctypes.POINTER(ctypes.c_double)]),
@@ -110,6 +121,17 @@ EXPORTS = {
     "dec_gqa_tree_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                _I, _I, _F, _F, _I, _I, _P, _Z, _P]),
     "dec_tree_commit": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "dec_qknorm_rope_paged_append": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _P,
+                                          _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                          _I, _P, _F, _P, _P]),
+    "dec_paged_attn_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "dec_gqa_paged_attn": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                _F, _I, _I, _P, _Z, _P]),
+    "dec_paged_gather": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                              _P, _P]),
+    "dec_paged_decode_step": (_I, [_P, _P, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P,
+                                   _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P,
+                                   _F, _I, _I, _P, _Z, _P]),
     "dec_token_logprobs": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _F, _P]),
     "dec_diag_wait_timeout": (_I, [_P, _P]),
     "dec_status_string": (ctypes.c_char_p, [_I]),
@@ -800,6 +822,191 @@ def tree_commit(k_tree, v_tree, path, n_path, k_cache, v_cache, lens, error_word
           _at(k_cache, "k_cache", BF16, cache), _at(v_cache, "v_cache", BF16, cache),
           _at(lens, "lens", I32, (B,), True), B, N, Hkv, D, T_cap, _ptr(error_word),
           _handle(stream))
+
+
+# -------------------------------------------------------------- paged cache ---
+E4M3 = torch.float8_e4m3fn
+_PAGE_TYPES = {BF16: 1, E4M3: 2}
+
+
+def alloc_paged_cache(num_pages: int, page: int, Hkv: int, D: int, dtype=E4M3, device=None):
+    """(k_pages, v_pages, k_scale, v_scale) of a paged cache: zeroed pages [num_pages, Hkv, page,
+    D] of ``dtype`` (torch.float8_e4m3fn or torch.bfloat16), scales of one [num_pages, Hkv] for
+    e4m3 pages, None for bf16. A table int32 [B, max_pages] of page numbers is the caller's."""
+    if dtype not in _PAGE_TYPES:
+        raise TypeError(f"dtype must be {E4M3} or {BF16}, got {dtype}")
+    shape, device = (num_pages, Hkv, page, D), device or "cuda"
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype is BF16:
+        return k, v, None, None
+    ks, vs = (torch.ones(shape[:2], dtype=F32, device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+def _paged(k_pages, v_pages, k_scale, v_scale, table, B: int):
+    """The cache's part of a call: (Hkv, D, num_pages, page, max_pages), addresses and type."""
+    P, Hkv, page, D = shape = _dims4(k_pages, "k_pages", "[num_pages, Hkv, page, D]")
+    dtype = k_pages.dtype
+    if dtype not in _PAGE_TYPES:
+        raise TypeError(f"k_pages must be {E4M3} or {BF16}, got {dtype}")
+    if (k_scale is None) != (dtype is BF16) or (v_scale is None) != (dtype is BF16):
+        raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages have none")
+    if not isinstance(table, torch.Tensor):
+        raise TypeError("table must be a torch.Tensor")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must be [{B}, max_pages], got {tuple(table.shape)}")
+    return ((Hkv, D, P, page, table.shape[1]),
+            (_at(k_pages, "k_pages", dtype, shape), _at(v_pages, "v_pages", dtype, shape),
+             _PAGE_TYPES[dtype], _maybe_at(k_scale, "k_scale", F32, (P, Hkv)),
+             _maybe_at(v_scale, "v_scale", F32, (P, Hkv)),
+             _at(table, "table", I32, (B, table.shape[1])), table.shape[1]))
+
+
+def _tokens(t, name: str, heads, D: int, n=None):
+    """A [n, heads, D] bf16 tensor whose tokens may lie apart: its address and token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not BF16:
+        raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
+    if not t.is_cuda and not t.is_pinned():
+        raise ValueError(f"{name} must be a CUDA tensor or a pinned host tensor (there is no CPU path)")
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or \
+            (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"({'n' if n is None else n}, {'heads' if heads is None else heads}, {D})")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and t.shape[1] != 1):
+        raise ValueError(f"{name}: a token's [heads, D] must be contiguous")
+    return t.data_ptr(), s0 if t.shape[0] > 1 else t.shape[1] * D
+
+
+def qknorm_rope_paged_append(q, k_new, v_new, k_pages, v_pages, table, start, theta: float,
+                             cu_new=None, k_scale=None, v_scale=None, layout="neox", rot_dim=None,
+                             q_norm_w=None, k_norm_w=None, eps: float = 1e-6, q_out=None,
+                             error_word=None, stream=None, inv_freq=None):
+    """QK-norm (optional) and RoPE of new tokens, K/V into pages [num_pages, Hkv, page, D] (bf16, or
+    e4m3 with ``k_scale``, ``v_scale`` fp32 [num_pages, Hkv]) through ``table`` int32 [B, max_pages].
+    ``start`` int32 [B]: the tokens each sequence holds already; its new ones, ``cu_new[b]`` <= i <
+    ``cu_new[b + 1]`` (int32 [B + 1]; None: one per sequence, in order), take the positions from there.
+    q [n, Hq, D] is rotated in place or into ``q_out``; q, k_new, v_new may be column blocks of one
+    packed projection (tokens apart, a token's heads contiguous). ``rot_dim``: the first elements
+    of a head that turn (a multiple of 16; all by default; 0: none), at theta^(-2i / rot_dim) or
+    ``inv_freq`` [rot_dim / 2]. Returns the rotated q. ``start`` itself is the caller's to advance."""
+    D = _dims4(k_pages, "k_pages", "[num_pages, Hkv, page, D]")[3]
+    if not isinstance(start, torch.Tensor):
+        raise TypeError("start must be a torch.Tensor")
+    if start.dim() != 1:
+        raise ValueError(f"start must be [B], got {tuple(start.shape)}")
+    B = start.shape[0]
+    (Hkv, _, P, page, _), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    q_at, q_ld = _tokens(q, "q", None, D)
+    n, Hq = q.shape[:2]
+    qo_at, qo_ld = (q_at, q_ld) if q_out is None else _tokens(q_out, "q_out", Hq, D, n)
+    k_at, k_ld = _tokens(k_new, "k_new", Hkv, D, n)
+    v_at, v_ld = _tokens(v_new, "v_new", Hkv, D, n)
+    if error_word is not None:
+        _need(error_word, "error_word", I32, host=True)
+    rot = D if rot_dim is None else int(rot_dim)
+    _call("dec_qknorm_rope_paged_append", q_at, q_ld, qo_at, qo_ld, k_at, k_ld, v_at, v_ld,
+          _maybe_at(q_norm_w, "q_norm_w", BF16, (D,), True),
+          _maybe_at(k_norm_w, "k_norm_w", BF16, (D,), True), *cache,
+          _at(start, "start", I32, (B,), True), _maybe_at(cu_new, "cu_new", I32, (B + 1,), True),
+          n, B, Hq, Hkv, D, P, page, rot, theta, _LAYOUTS[layout],
+          _freq(inv_freq, rot), eps, _ptr(error_word), _handle(stream))
+    return q if q_out is None else q_out
+
+
+def paged_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_len: int,
+                          num_parts: int = 0) -> int:
+    return int(lib().dec_paged_attn_workspace_bytes(B, Hq, Hkv, D, max_len, num_parts))
+
+
+def alloc_paged_workspace(B: int, Hq: int, Hkv: int, D: int, max_len: int, num_parts: int = 0,
+                          device=None) -> torch.Tensor:
+    """A zeroed uint8 workspace for :func:`gqa_paged_attn` and :func:`paged_decode_step`."""
+    n = paged_workspace_bytes(B, Hq, Hkv, D, max_len, num_parts)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _paged_q(q):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [B, Hq, D], got {tuple(q.shape)}")
+    return q.shape
+
+
+def gqa_paged_attn(q, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, max_len=None,
+                   workspace=None, out=None, scale: float = 0.0, num_parts: int = 0, stream=None,
+                   window: int = 0):
+    """Single-query GQA attention over a paged cache: q [B, Hq, D] (rotated) over the tokens t <
+    lens[b] that ``table`` int32 [B, max_pages] finds in k_pages, v_pages [num_pages, Hkv, page, D]
+    (bf16, or e4m3 with fp32 scales [num_pages, Hkv]). ``window`` > 0 restricts sequence b to its
+    last min(lens[b], window) tokens. Returns ``out`` [B, Hq, D]; a sequence without tokens
+    gives zeros."""
+    B, Hq, D = shape = _paged_q(q)
+    (Hkv, _, P, page, M), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    if k_pages.shape[3] != D:
+        raise ValueError(f"k_pages shape {tuple(k_pages.shape)} does not match q {tuple(shape)}")
+    max_len = M * page if max_len is None else int(max_len)
+    if workspace is None or out is None:
+        with _on(stream):
+            if workspace is None:
+                workspace = alloc_paged_workspace(B, Hq, Hkv, D, max_len, num_parts, k_pages.device)
+            if out is None:
+                out = _empty(shape, BF16, q)
+    _need(workspace, "workspace", torch.uint8)
+    _call("dec_gqa_paged_attn", _at(q, "q", BF16, shape, True), *cache,
+          _at(lens, "lens", I32, (B,), True), _at(out, "out", BF16, shape, True), B, Hq, Hkv, D, P,
+          page, max_len, scale, window, num_parts, workspace.data_ptr(), workspace.numel(),
+          _handle(stream))
+    return out
+
+
+def paged_gather(k_pages, v_pages, table, lens, k_out, v_out, k_scale=None, v_scale=None,
+                 start=None, error_word=None, stream=None):
+    """Tokens start[b] <= t < lens[b] (int32 [B]; from 0 without ``start``) of a paged cache into
+    contiguous bf16 caches k_out, v_out [B, Hkv, rows, D], at row t - start[b], as the calls that
+    are not paged read them. Other rows are left as they were; at most ``rows`` tokens are copied."""
+    B, Hkv, rows, D = shape = _dims4(k_out, "k_out", "[B, Hkv, rows, D]")
+    dims, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    if dims[:2] != (Hkv, D):
+        raise ValueError(f"k_out shape {tuple(shape)} does not match k_pages {tuple(k_pages.shape)}")
+    if error_word is not None:
+        _need(error_word, "error_word", I32, host=True)
+    _call("dec_paged_gather", *cache, _maybe_at(start, "start", I32, (B,), True),
+          _at(lens, "lens", I32, (B,), True), _at(k_out, "k_out", BF16, shape),
+          _at(v_out, "v_out", BF16, shape), B, Hkv, D, dims[2], dims[3], rows, _ptr(error_word),
+          _handle(stream))
+    return k_out, v_out
+
+
+def paged_decode_step(x, residual, norm_w, y, q, k_new, v_new, k_pages, v_pages, table, pos, lens,
+                      out, workspace, theta: float, k_scale=None, v_scale=None, layout="neox",
+                      rot_dim=None, q_norm_w=None, k_norm_w=None, eps: float = 1e-6, max_len=None,
+                      scale: float = 0.0, num_parts: int = 0, stream=None, window: int = 0,
+                      inv_freq=None):
+    """:func:`decode_step` over a paged cache: RMSNorm + residual, the append of one token per
+    sequence at pos[b] (q rotated in place), attention over lens[b] tokens, on one stream."""
+    B, Hq, D = shape = _paged_q(q)
+    (Hkv, _, P, page, M), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    _need(x, "x", BF16, host=True)
+    hidden = x.shape[1]
+    _need(workspace, "workspace", torch.uint8)
+    max_len = M * page if max_len is None else int(max_len)
+    rot = D if rot_dim is None else int(rot_dim)
+    _call("dec_paged_decode_step", _at(x, "x", BF16, (B, hidden), True),
+          _maybe_at(residual, "residual", BF16, (B, hidden), True),
+          _at(norm_w, "norm_w", BF16, (hidden,), True), _at(y, "y", BF16, (B, hidden), True),
+          hidden, eps, _at(q, "q", BF16, shape, True),
+          _at(k_new, "k_new", BF16, (B, Hkv, D), True), _at(v_new, "v_new", BF16, (B, Hkv, D), True),
+          _maybe_at(q_norm_w, "q_norm_w", BF16, (D,), True),
+          _maybe_at(k_norm_w, "k_norm_w", BF16, (D,), True), *cache,
+          _at(pos, "pos", I32, (B,), True), _at(lens, "lens", I32, (B,), True),
+          _at(out, "out", BF16, shape, True), B, Hq, Hkv, D, P, page, max_len, rot, theta,
+          _LAYOUTS[layout], _freq(inv_freq, rot), scale, window, num_parts, workspace.data_ptr(),
+          workspace.numel(), _handle(stream))
+    return out
 
 
 # ------------------------------------------------------------ CUDA graph ---

@@ -3,6 +3,7 @@
 // Nothing here allocates, frees or synchronises.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -1345,6 +1346,371 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
                                            N, Hkv, D, T_cap, error_word, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "tree_commit launch");
   return ok();
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------- paged cache ---
+namespace {
+
+dec_status check_paged(const PagedCache &c, dec_dtype type, int B) {
+  if (B < 0) return fail(DEC_ERR_INVALID_ARG, "B = %d < 0", B);
+  if (B > kSplitMaxB) return fail(DEC_ERR_UNSUPPORTED, "B = %d > %d", B, kSplitMaxB);
+  if (c.Hkv <= 0) return fail(DEC_ERR_INVALID_ARG, "head counts must be positive");
+  if (c.Hkv > 65535) return fail(DEC_ERR_UNSUPPORTED, "Hkv = %d > 65535", c.Hkv);
+  if (c.D != 64 && c.D != 128)
+    return fail(DEC_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", c.D);
+  if (type != DEC_BF16 && type != DEC_E4M3)
+    return fail(DEC_ERR_INVALID_ARG, "unknown page type %d", (int)type);
+  if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128)
+    return fail(DEC_ERR_UNSUPPORTED, "page = %d tokens (supported: 16, 32, 64, 128)", c.page);
+  if (c.num_pages <= 0) return fail(DEC_ERR_INVALID_ARG, "num_pages must be positive");
+  if (c.max_pages <= 0) return fail(DEC_ERR_INVALID_ARG, "max_pages must be positive");
+  if ((long long)c.num_pages * c.Hkv >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "num_pages * Hkv must stay below 2^31");
+  if ((long long)c.max_pages * c.page >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "max_pages * page must stay below 2^31 tokens");
+  return DEC_OK;
+}
+
+// The pointers of a cache that a call needs (B > 0).
+dec_status check_paged_buffers(const PagedCache &c) {
+  if (!c.k_pages || !c.v_pages || !c.table)
+    return fail(DEC_ERR_INVALID_ARG, "k_pages, v_pages and table must be non-null");
+  if (c.e4m3 && (!c.k_scale || !c.v_scale))
+    return fail(DEC_ERR_INVALID_ARG, "e4m3 pages need k_scale and v_scale");
+  if (!c.e4m3 && (c.k_scale || c.v_scale))
+    return fail(DEC_ERR_INVALID_ARG, "bf16 pages have no scales");
+  if (misaligned({c.k_pages, c.v_pages}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({c.k_scale, c.v_scale, c.table}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "scales and table must be 4-byte aligned");
+  return DEC_OK;
+}
+
+size_t pages_bytes(const PagedCache &c) {
+  return (size_t)c.num_pages * c.Hkv * c.page * c.D * (c.e4m3 ? 1 : 2);
+}
+size_t scales_bytes(const PagedCache &c) { return (size_t)c.num_pages * c.Hkv * 4; }
+size_t table_bytes(const PagedCache &c, int B) { return (size_t)B * c.max_pages * 4; }
+
+PagedCache paged_cache(void *k_pages, void *v_pages, dec_dtype type, float *k_scale,
+                       float *v_scale, const int32_t *table, int max_pages, int Hkv, int D,
+                       int num_pages, int page) {
+  return PagedCache{k_pages, v_pages, k_scale, v_scale, table,
+                    num_pages, page, max_pages, Hkv, D, type == DEC_E4M3};
+}
+
+// Rows of `width` bytes every `ld` bytes.
+struct Rows {
+  const void *p;
+  size_t ld, width;
+  const char *name;
+};
+// Whether n rows of each have a byte in common. Column blocks of one matrix do not.
+bool rows_overlap(const Rows &a, const Rows &b, size_t n) {
+  const size_t a_bytes = (n - 1) * a.ld + a.width, b_bytes = (n - 1) * b.ld + b.width;
+  if (!overlaps(a.p, a_bytes, b.p, b_bytes)) return false;
+  if (a.ld != b.ld) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t off = pb >= pa ? (pb - pa) % a.ld : (a.ld - (pa - pb) % a.ld) % a.ld;
+  return off < a.width || off + b.width > a.ld;
+}
+
+// Every host-side check of an append but where its buffers are, and its frequencies.
+dec_status check_append(const PagedCache &c, dec_dtype type, const PagedAppend &p,
+                        float rope_theta, dec_rope_layout layout, const double *inv_freq,
+                        InvFreq *inv) {
+  dec_status st = check_paged(c, type, p.B);
+  if (st != DEC_OK) return st;
+  if (p.Hq <= 0 || p.Hq % c.Hkv != 0)
+    return fail(DEC_ERR_INVALID_ARG, "need Hq > 0 and Hq %% Hkv == 0");
+  if ((long long)p.Hq + 2ll * c.Hkv > 65535)
+    return fail(DEC_ERR_UNSUPPORTED, "Hq + 2 Hkv > 65535 heads");
+  if (p.n < 0) return fail(DEC_ERR_INVALID_ARG, "n = %d < 0", p.n);
+  if (p.n >= 1 << 24) return fail(DEC_ERR_UNSUPPORTED, "n = %d tokens >= 2^24", p.n);
+  if (p.rot_dim < 0 || p.rot_dim > c.D || p.rot_dim % 16 != 0)
+    return fail(DEC_ERR_INVALID_ARG, "rot_dim = %d (need a multiple of 16 in [0, D])", p.rot_dim);
+  if (p.rot_dim > 0 && (st = rope_table(p.rot_dim, rope_theta, inv_freq, inv)) != DEC_OK)
+    return st;
+  if (layout != DEC_ROPE_NEOX && layout != DEC_ROPE_INTERLEAVED)
+    return fail(DEC_ERR_INVALID_ARG, "unknown rope layout %d", (int)layout);
+  if (!(p.eps >= 0.f)) return fail(DEC_ERR_INVALID_ARG, "eps must be >= 0");
+  if ((p.q_norm_w == nullptr) != (p.k_norm_w == nullptr))
+    return fail(DEC_ERR_INVALID_ARG, "q_norm_w and k_norm_w must both be set or both be null");
+  const long long qw = (long long)p.Hq * c.D, kw = (long long)c.Hkv * c.D;
+  if (p.q_ld < qw || p.qo_ld < qw || p.k_ld < kw || p.v_ld < kw ||
+      ((p.q_ld | p.qo_ld | p.k_ld | p.v_ld) & 7) != 0)
+    return fail(DEC_ERR_INVALID_ARG,
+                "token strides must be multiples of 8 and at least a token's elements");
+  if (std::max(std::max(p.q_ld, p.qo_ld), std::max(p.k_ld, p.v_ld)) >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "token strides must stay below 2^31 elements");
+  if (p.cu_new == nullptr && p.n != p.B)
+    return fail(DEC_ERR_INVALID_ARG, "n = %d != B = %d without cu_new", p.n, p.B);
+  if (p.n == 0 || p.B == 0) return DEC_OK;
+  if (!p.q_in || !p.q_out || !p.k_new || !p.v_new || !p.start)
+    return fail(DEC_ERR_INVALID_ARG, "q, k_new, v_new and start must be non-null");
+  if ((st = check_paged_buffers(c)) != DEC_OK) return st;
+  if (misaligned({p.q_in, p.q_out, p.k_new, p.v_new, p.q_norm_w, p.k_norm_w}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({p.start, p.cu_new, p.error_word}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "start, cu_new and error_word must be 4-byte aligned");
+  const Rows qi{p.q_in, (size_t)p.q_ld * 2, (size_t)qw * 2, "q_in"};
+  const Rows qo{p.q_out, (size_t)p.qo_ld * 2, (size_t)qw * 2, "q_out"};
+  const Rows kn{p.k_new, (size_t)p.k_ld * 2, (size_t)kw * 2, "k_new"};
+  const Rows vn{p.v_new, (size_t)p.v_ld * 2, (size_t)kw * 2, "v_new"};
+  if (!(p.q_in == p.q_out && p.q_ld == p.qo_ld) && rows_overlap(qi, qo, p.n))
+    return fail(DEC_ERR_INVALID_ARG,
+                "q_in and q_out must be the same buffer and stride, or not overlap");
+  for (const Rows &r : {kn, vn})
+    if (rows_overlap(qo, r, p.n)) return fail(DEC_ERR_INVALID_ARG, "q_out may not overlap %s", r.name);
+  auto span = [&](const Rows &r) { return Span{r.p, (p.n - 1) * r.ld + r.width, r.name}; };
+  const Span q_out = span(qo);
+  const Span small[] = {{p.q_norm_w, (size_t)c.D * 2, "q_norm_w"},
+                        {p.k_norm_w, (size_t)c.D * 2, "k_norm_w"},
+                        {c.table, table_bytes(c, p.B), "table"},
+                        {p.start, (size_t)p.B * 4, "start"},
+                        {p.cu_new, (size_t)(p.B + 1) * 4, "cu_new"}};
+  st = check_apart({{c.k_pages, pages_bytes(c), "k_pages"}, {c.v_pages, pages_bytes(c), "v_pages"},
+                    {c.k_scale, scales_bytes(c), "k_scale"},
+                    {c.v_scale, scales_bytes(c), "v_scale"}, {p.error_word, 4, "error_word"}},
+                   {q_out, span(qi), span(kn), span(vn), small[0], small[1], small[2], small[3],
+                    small[4]});
+  if (st != DEC_OK) return st;
+  return check_apart({q_out}, {small[0], small[1], small[2], small[3], small[4]});
+}
+dec_status where_append(const PagedCache &c, const PagedAppend &p) {
+  return where_all_here({{p.q_in, "q_in", true}, {p.q_out, "q_out", true},
+                         {p.k_new, "k_new", true}, {p.v_new, "v_new", true},
+                         {p.q_norm_w, "q_norm_w", true}, {p.k_norm_w, "k_norm_w", true},
+                         {c.k_pages, "k_pages", false}, {c.v_pages, "v_pages", false},
+                         {c.k_scale, "k_scale", false}, {c.v_scale, "v_scale", false},
+                         {c.table, "table", false}, {p.start, "start", true},
+                         {p.cu_new, "cu_new", true}, {p.error_word, "error_word", true}});
+}
+
+dec_status check_paged_attn(const PagedCache &c, dec_dtype type, const void *q,
+                            const int32_t *lens, void *out, int B, int Hq, int max_len, float scale,
+                            int window, int num_parts, void *workspace, size_t ws_bytes) {
+  dec_status st = check_paged(c, type, B);
+  if (st != DEC_OK) return st;
+  if (Hq <= 0 || Hq % c.Hkv != 0)
+    return fail(DEC_ERR_INVALID_ARG, "need Hq > 0 and Hq %% Hkv == 0");
+  if (Hq / c.Hkv > kSplitMaxG)
+    return fail(DEC_ERR_UNSUPPORTED, "query heads per KV head %d > %d", Hq / c.Hkv, kSplitMaxG);
+  if (max_len < 0 || max_len > c.max_pages * c.page)
+    return fail(DEC_ERR_INVALID_ARG, "max_len = %d outside [0, max_pages * page = %d]", max_len,
+                c.max_pages * c.page);
+  if ((long long)B * c.Hkv * (max_len / 128 + 8) >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "B * Hkv * max_len too large");
+  if (num_parts < 0) return fail(DEC_ERR_INVALID_ARG, "num_parts = %d < 0", num_parts);
+  if (num_parts > kPagedMaxParts)
+    return fail(DEC_ERR_UNSUPPORTED, "num_parts = %d > %d", num_parts, kPagedMaxParts);
+  if (window < 0) return fail(DEC_ERR_INVALID_ARG, "window = %d < 0", window);
+  if (!std::isfinite(scale) || scale > 1e30f)
+    return fail(DEC_ERR_INVALID_ARG, "scale = %g is not a number of at most 1e30", scale);
+  if (B == 0) return DEC_OK;
+  if (!q || !lens || !out) return fail(DEC_ERR_INVALID_ARG, "q, lens and out must be non-null");
+  if ((st = check_paged_buffers(c)) != DEC_OK) return st;
+  if (misaligned({q, out}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({lens}, 4)) return fail(DEC_ERR_INVALID_ARG, "lens must be 4-byte aligned");
+  if (workspace == nullptr || misaligned({workspace}, 256))
+    return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+  const size_t need = paged_attn_ws_bytes(
+      B, Hq, c.Hkv, c.D, paged_attn_parts(B, c.Hkv, max_len, num_parts, sm_count_of_current()));
+  if (ws_bytes < need)
+    return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  const size_t rows = (size_t)B * Hq * c.D * 2;
+  return check_apart(
+      {{out, rows, "out"}, {workspace, need, "workspace"}},
+      {{q, rows, "q"}, {c.k_pages, pages_bytes(c), "k_pages"},
+       {c.v_pages, pages_bytes(c), "v_pages"}, {c.k_scale, scales_bytes(c), "k_scale"},
+       {c.v_scale, scales_bytes(c), "v_scale"}, {c.table, table_bytes(c, B), "table"},
+       {lens, (size_t)B * 4, "lens"}});
+}
+dec_status where_attn(const PagedCache &c, const void *q, const int32_t *lens, void *out,
+                      void *workspace) {
+  return where_all_here({{q, "q", true}, {c.k_pages, "k_pages", false},
+                         {c.v_pages, "v_pages", false}, {c.k_scale, "k_scale", false},
+                         {c.v_scale, "v_scale", false}, {c.table, "table", false},
+                         {lens, "lens", true}, {out, "out", true},
+                         {workspace, "workspace", false}});
+}
+
+dec_status paged_attn_go(const PagedCache &c, const void *q, const int32_t *lens, void *out, int B,
+                         int Hq, int max_len, float scale, int window, int num_parts,
+                         void *workspace, dec_stream_t stream) {
+  PagedAttnArgs a{};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.lens = lens;
+  a.error_word = static_cast<uint32_t *>(workspace);
+  a.B = B;
+  a.Hq = Hq;
+  a.max_len = max_len;
+  a.window = window;
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)c.D);
+  a.scale_log2 = (float)((double)sc * 1.4426950408889634);
+  const int parts = paged_attn_parts(B, c.Hkv, max_len, num_parts, sm_count_of_current());
+  const cudaError_t e = launch_paged_attn(c, a, parts, workspace, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gqa_paged_attn launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+dec_status dec_qknorm_rope_paged_append(
+    const void *q_in, int64_t q_ld, void *q_out, int64_t qo_ld, const void *k_new, int64_t k_ld,
+    const void *v_new, int64_t v_ld, const void *q_norm_w, const void *k_norm_w, void *k_pages,
+    void *v_pages, dec_dtype type, float *k_scale, float *v_scale, const int32_t *table,
+    int max_pages, const int32_t *start, const int32_t *cu_new, int n, int B, int Hq, int Hkv,
+    int D, int num_pages, int page, int rot_dim, float rope_theta, dec_rope_layout layout,
+    const double *inv_freq, float eps, uint32_t *error_word, dec_stream_t stream) {
+  const PagedCache c = paged_cache(k_pages, v_pages, type, k_scale, v_scale, table, max_pages, Hkv,
+                                   D, num_pages, page);
+  const PagedAppend p{q_in, k_new, v_new, q_norm_w, k_norm_w, q_out, start, cu_new, error_word,
+                      q_ld, qo_ld, k_ld, v_ld, n, B, Hq, rot_dim, layout == DEC_ROPE_INTERLEAVED,
+                      eps};
+  InvFreq inv{};
+  dec_status st = check_append(c, type, p, rope_theta, layout, inv_freq, &inv);
+  if (st != DEC_OK) return st;
+  if (n == 0 || B == 0) return ok();
+  if ((st = where_append(c, p)) != DEC_OK) return st;
+  const cudaError_t e = launch_paged_append(c, p, inv, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qknorm_rope_paged_append launch");
+  return ok();
+}
+
+size_t dec_paged_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len, int num_parts) {
+  if (B < 0 || B > kSplitMaxB || Hq <= 0 || Hkv <= 0 || Hkv > 65535 || Hq % Hkv != 0 ||
+      Hq / Hkv > kSplitMaxG || (D != 64 && D != 128) || max_len < 0 || num_parts < 0 ||
+      num_parts > kPagedMaxParts || (long long)B * Hkv * (max_len / 128 + 8) >= (1ll << 31))
+    return 0;
+  return paged_attn_ws_bytes(
+      B, Hq, Hkv, D, paged_attn_parts(B, Hkv, max_len, num_parts, sm_count_of_current()));
+}
+
+dec_status dec_gqa_paged_attn(const void *q, const void *k_pages, const void *v_pages,
+                              dec_dtype type, const float *k_scale, const float *v_scale,
+                              const int32_t *table, int max_pages, const int32_t *lens, void *out,
+                              int B, int Hq, int Hkv, int D, int num_pages, int page, int max_len,
+                              float scale, int window, int num_parts, void *workspace,
+                              size_t ws_bytes, dec_stream_t stream) {
+  const PagedCache c = paged_cache(const_cast<void *>(k_pages), const_cast<void *>(v_pages), type,
+                                   const_cast<float *>(k_scale), const_cast<float *>(v_scale),
+                                   table, max_pages, Hkv, D, num_pages, page);
+  dec_status st = check_paged_attn(c, type, q, lens, out, B, Hq, max_len, scale, window, num_parts,
+                                   workspace, ws_bytes);
+  if (st != DEC_OK) return st;
+  if (B == 0) return ok();
+  if ((st = where_attn(c, q, lens, out, workspace)) != DEC_OK) return st;
+  return paged_attn_go(c, q, lens, out, B, Hq, max_len, scale, window, num_parts, workspace, stream);
+}
+
+dec_status dec_paged_gather(const void *k_pages, const void *v_pages, dec_dtype type,
+                            const float *k_scale, const float *v_scale, const int32_t *table,
+                            int max_pages, const int32_t *start, const int32_t *lens, void *k_out,
+                            void *v_out, int B, int Hkv, int D, int num_pages, int page, int rows,
+                            uint32_t *error_word, dec_stream_t stream) {
+  const PagedCache c = paged_cache(const_cast<void *>(k_pages), const_cast<void *>(v_pages), type,
+                                   const_cast<float *>(k_scale), const_cast<float *>(v_scale),
+                                   table, max_pages, Hkv, D, num_pages, page);
+  dec_status st = check_paged(c, type, B);
+  if (st != DEC_OK) return st;
+  if (rows < 1) return fail(DEC_ERR_INVALID_ARG, "rows = %d < 1", rows);
+  if (((long long)rows / 64 + 1) * Hkv >= (1ll << 31))
+    return fail(DEC_ERR_UNSUPPORTED, "rows * Hkv too large");
+  if (B == 0) return ok();
+  if (!lens || !k_out || !v_out)
+    return fail(DEC_ERR_INVALID_ARG, "lens, k_out and v_out must be non-null");
+  if ((st = check_paged_buffers(c)) != DEC_OK) return st;
+  if (misaligned({k_out, v_out}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (misaligned({start, lens, error_word}, 4))
+    return fail(DEC_ERR_INVALID_ARG, "start, lens and error_word must be 4-byte aligned");
+  const size_t out = (size_t)B * Hkv * rows * D * 2;
+  st = check_apart({{k_out, out, "k_out"}, {v_out, out, "v_out"}, {error_word, 4, "error_word"}},
+                   {{k_pages, pages_bytes(c), "k_pages"}, {v_pages, pages_bytes(c), "v_pages"},
+                    {k_scale, scales_bytes(c), "k_scale"}, {v_scale, scales_bytes(c), "v_scale"},
+                    {table, table_bytes(c, B), "table"}, {start, (size_t)B * 4, "start"},
+                    {lens, (size_t)B * 4, "lens"}});
+  if (st != DEC_OK) return st;
+  st = where_all_here({{k_pages, "k_pages", false}, {v_pages, "v_pages", false},
+                       {k_scale, "k_scale", false}, {v_scale, "v_scale", false},
+                       {table, "table", false}, {start, "start", true}, {lens, "lens", true},
+                       {k_out, "k_out", false}, {v_out, "v_out", false},
+                       {error_word, "error_word", true}});
+  if (st != DEC_OK) return st;
+  const cudaError_t e =
+      launch_paged_gather(c, start, lens, k_out, v_out, B, rows, error_word, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_gather launch");
+  return ok();
+}
+
+dec_status dec_paged_decode_step(
+    const void *x, void *residual, const void *norm_w, void *y, int hidden, float eps, void *q,
+    const void *k_new, const void *v_new, const void *q_norm_w, const void *k_norm_w,
+    void *k_pages, void *v_pages, dec_dtype type, float *k_scale, float *v_scale,
+    const int32_t *table, int max_pages, const int32_t *pos, const int32_t *lens, void *out, int B,
+    int Hq, int Hkv, int D, int num_pages, int page, int max_len, int rot_dim, float rope_theta,
+    dec_rope_layout layout, const double *inv_freq, float scale, int window, int num_parts,
+    void *workspace, size_t ws_bytes, dec_stream_t stream) {
+  const PagedCache c = paged_cache(k_pages, v_pages, type, k_scale, v_scale, table, max_pages, Hkv,
+                                   D, num_pages, page);
+  const long long q_ld = (long long)Hq * D, kv_ld = (long long)Hkv * D;
+  const PagedAppend p{q, k_new, v_new, q_norm_w, k_norm_w, q, pos, nullptr,
+                      static_cast<uint32_t *>(workspace), q_ld, q_ld, kv_ld, kv_ld, B, B, Hq,
+                      rot_dim, layout == DEC_ROPE_INTERLEAVED, eps};
+  InvFreq inv{};
+  // check everything before the first launch
+  dec_status st = check_paged_attn(c, type, q, lens, out, B, Hq, max_len, scale, window, num_parts,
+                                   workspace, ws_bytes);
+  if (st != DEC_OK) return st;
+  if ((st = check_append(c, type, p, rope_theta, layout, inv_freq, &inv)) != DEC_OK) return st;
+  if (hidden < 8 || hidden > 16384 || hidden % 8 != 0)
+    return fail(DEC_ERR_UNSUPPORTED, "hidden = %d (need a multiple of 8 in [8, 16384])", hidden);
+  if (B == 0) return ok();
+  if (!x || !norm_w || !y) return fail(DEC_ERR_INVALID_ARG, "x, norm_w and y must be non-null");
+  if (misaligned({x, residual, norm_w, y}, 16))
+    return fail(DEC_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  const size_t row = (size_t)B * hidden * 2, qb = (size_t)B * Hq * D * 2;
+  const size_t kb = (size_t)B * Hkv * D * 2;
+  const size_t need = paged_attn_ws_bytes(
+      B, Hq, Hkv, D, paged_attn_parts(B, Hkv, max_len, num_parts, sm_count_of_current()));
+  st = check_apart({{y, row, "y"}, {residual, row, "residual"}},
+                   {{x, row, "x"}, {norm_w, (size_t)hidden * 2, "norm_w"}, {q, qb, "q"},
+                    {k_new, kb, "k_new"}, {v_new, kb, "v_new"},
+                    {q_norm_w, (size_t)D * 2, "q_norm_w"}, {k_norm_w, (size_t)D * 2, "k_norm_w"},
+                    {k_pages, pages_bytes(c), "k_pages"}, {v_pages, pages_bytes(c), "v_pages"},
+                    {k_scale, scales_bytes(c), "k_scale"}, {v_scale, scales_bytes(c), "v_scale"},
+                    {table, table_bytes(c, B), "table"}, {pos, (size_t)B * 4, "pos"},
+                    {lens, (size_t)B * 4, "lens"}, {out, qb, "out"},
+                    {workspace, need, "workspace"}});
+  if (st == DEC_OK)
+    st = check_apart({{out, qb, "out"}, {workspace, need, "workspace"}},
+                     {{x, row, "x"}, {norm_w, (size_t)hidden * 2, "norm_w"}, {k_new, kb, "k_new"},
+                      {v_new, kb, "v_new"}, {q_norm_w, (size_t)D * 2, "q_norm_w"},
+                      {k_norm_w, (size_t)D * 2, "k_norm_w"}, {pos, (size_t)B * 4, "pos"}});
+  if (st == DEC_OK)
+    st = check_apart({{q, qb, "q"}, {k_pages, pages_bytes(c), "k_pages"},
+                      {v_pages, pages_bytes(c), "v_pages"}, {k_scale, scales_bytes(c), "k_scale"},
+                      {v_scale, scales_bytes(c), "v_scale"}},
+                     {{x, row, "x"}, {norm_w, (size_t)hidden * 2, "norm_w"},
+                      {lens, (size_t)B * 4, "lens"}});
+  if (st != DEC_OK) return st;
+  if ((st = where_attn(c, q, lens, out, workspace)) != DEC_OK ||
+      (st = where_append(c, p)) != DEC_OK ||
+      (st = where_all_here({{x, "x", true}, {residual, "residual", true}, {norm_w, "norm_w", true},
+                            {y, "y", true}})) != DEC_OK)
+    return st;
+  cudaError_t e = launch_rmsnorm_residual(x, residual, norm_w, y, B, hidden, eps, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm_residual launch");
+  e = launch_paged_append(c, p, inv, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qknorm_rope_paged_append launch");
+  return paged_attn_go(c, q, lens, out, B, Hq, max_len, scale, window, num_parts, workspace, stream);
 }
 
 // -------------------------------------------------------- log probabilities ---

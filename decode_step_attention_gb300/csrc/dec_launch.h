@@ -211,6 +211,46 @@ int tree_join_ctas(int B, int N, int Hq, int Hkv, int max_len, int window, int n
 cudaError_t launch_tree_attn(const CUtensorMap *maps, const TreeAttnArgs &a, int B, int D,
                              int parts, int ctas, cudaStream_t stream);
 
+// ---- paged cache -------------------------------------------------------------------
+// Pages [num_pages, Hkv, page, D], bf16, or e4m3 codes with scales [num_pages, Hkv]; table
+// [B, max_pages]. page: a power of two, 16 .. 128.
+struct PagedCache {
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;  // null for bf16
+  const int32_t *table;
+  int num_pages, page, max_pages, Hkv, D, e4m3;
+};
+// n new tokens, those of sequence b from cu_new[b] on (null: one each), at positions from start[b]
+// on; token strides in elements.
+struct PagedAppend {
+  const void *q_in, *k_new, *v_new, *q_norm_w, *k_norm_w;
+  void *q_out;
+  const int32_t *start, *cu_new;
+  uint32_t *error_word;
+  long long q_ld, qo_ld, k_ld, v_ld;
+  int n, B, Hq, rot_dim, interleaved;
+  float eps;
+};
+cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const InvFreq &inv,
+                                cudaStream_t stream);
+cudaError_t launch_paged_gather(const PagedCache &c, const int32_t *start, const int32_t *lens,
+                                void *k_out, void *v_out, int B, int rows, uint32_t *error_word,
+                                cudaStream_t stream);
+
+struct PagedAttnArgs {
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  const int32_t *lens;
+  uint32_t *error_word;  // the workspace's first word
+  int B, Hq, max_len, window;  // lengths are clamped to max_len
+  float scale_log2;            // softmax scale times log2(e)
+};
+constexpr int kPagedMaxParts = 4096;
+int paged_attn_parts(int B, int Hkv, int max_len, int num_parts, int sms);
+size_t paged_attn_ws_bytes(int B, int Hq, int Hkv, int D, int parts);
+cudaError_t launch_paged_attn(const PagedCache &c, const PagedAttnArgs &a, int parts,
+                              void *workspace, cudaStream_t stream);
+
 // ---- log probabilities -------------------------------------------------------------
 constexpr int kLogprobMaxK = 32;
 constexpr int kLogprobMaxV = 262144;

@@ -44,8 +44,8 @@ __device__ __noinline__ inline float rope_exact(int p, double inv_freq, float ow
 // modulo 2^64 is the angle's fractional turn, its nearest quarter turn goes off exactly in
 // integers, and the Taylor series of sine and cosine run to x^15 and x^16 at |x| <= pi / 4 (the
 // next terms are below 5e-17). About 25 fp64 operations where a general sincos takes hundreds.
-__device__ __noinline__ inline float rope_exact_turns(int p, unsigned long long turns, float own,
-                                                      float other, float rstd, bool second) {
+__device__ __forceinline__ double rope_element_turns(int p, unsigned long long turns, float own,
+                                                     float other, bool second) {
   const unsigned long long t = (unsigned long long)(unsigned)p * turns;
   const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);
   const double x = (double)(long long)(t - ((unsigned long long)quarter << 62)) *
@@ -70,7 +70,11 @@ __device__ __noinline__ inline float rope_exact_turns(int p, unsigned long long 
   double cs = quarter & 1 ? -s : c, sn = quarter & 1 ? c : s;
   if (quarter & 2) cs = -cs, sn = -sn;
   const double o = second ? (double)other : -(double)other;
-  return (float)(fma((double)own, cs, o * sn) * (double)rstd);
+  return fma((double)own, cs, o * sn);
+}
+__device__ __noinline__ inline float rope_exact_turns(int p, unsigned long long turns, float own,
+                                                      float other, float rstd, bool second) {
+  return (float)(rope_element_turns(p, turns, own, other, second) * (double)rstd);
 }
 
 // A rotated pair in fp32 with its roundings spelled out. Left to the compiler, which product of a

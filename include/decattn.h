@@ -65,6 +65,10 @@ typedef enum dec_status {
   DEC_ERR_CUDA = 4          /* the CUDA runtime or driver reported an error */
 } dec_status;
 
+/* Element types: of the logits of dec_token_logprobs (fp32, bf16) and of a paged cache
+ * (bf16, or e4m3: 8 bits, 4 of them significant, 448 the largest value, no infinity). */
+typedef enum dec_dtype { DEC_F32 = 0, DEC_BF16 = 1, DEC_E4M3 = 2 } dec_dtype;
+
 typedef enum dec_rope_layout {
   DEC_ROPE_NEOX = 0,        /* element i pairs with i + D/2 */
   DEC_ROPE_INTERLEAVED = 1  /* element 2i pairs with 2i + 1 */
@@ -118,6 +122,7 @@ dec_status dec_rope_yarn_softmax_scale(int D, float factor, float *scale);
 #define DEC_DEVERR_POS_SKIPPED   0x2u  /* a pos[b] outside [0, T_cap) was skipped */
 #define DEC_DEVERR_WAIT_TIMEOUT  0x4u  /* a pipeline wait gave up (results invalid) */
 #define DEC_DEVERR_TREE_CLAMPED  0x8u  /* a node count outside [0, N] was clamped */
+#define DEC_DEVERR_PAGE_SKIPPED  0x10u /* a page number outside [0, num_pages) was skipped */
 
 /* ------------------------------------------------------------------------ K1
  * RMSNorm with a fused residual add (fusedtok README, "Operators": RMSNorm
@@ -624,6 +629,108 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
                            const int32_t *lens, int B, int N, int Hkv, int D, int T_cap,
                            uint32_t *error_word, dec_stream_t stream);
 
+/* ------------------------------------------------------------- paged cache
+ * A key/value cache in pages, for sequences that grow without a T_cap of rows held for each,
+ * in bf16 or in 8 bits (half the bytes that a decode step reads). Token t of sequence b, KV
+ * head g, is row t % page of
+ *   k_pages, v_pages [device] [num_pages, Hkv, page, D], at page table[b, t / page]
+ *   table            [device] int32 [B, max_pages]; a sequence holds up to max_pages * page
+ *                    tokens. Pages may lie in any order and be shared by sequences that read
+ *                    them; a page that an append writes to belongs to one sequence, once.
+ *                    Entries that no token of the call needs may hold anything.
+ *   type             DEC_BF16, or DEC_E4M3 with
+ *   k_scale, v_scale [device] fp32 [num_pages, Hkv], finite and > 0 for pages that hold tokens:
+ *                    a value is code * scale. NULL for DEC_BF16.
+ * The conventions are those of the draft trees: device buffers on the current device, what a
+ * call writes overlaps neither what it reads nor anything else it writes. A token whose page
+ * number lies outside [0, num_pages) is skipped (not stored, not attended, not copied) and raises
+ * DEC_DEVERR_PAGE_SKIPPED. D in {64, 128}; page in {16, 32, 64, 128}; num_pages * Hkv < 2^31;
+ * max_pages * page < 2^31; B <= 8192. */
+
+/* dec_qknorm_rope_kv_append for any number of new tokens per sequence, into pages. Token i,
+ * cu_new[b] <= i < cu_new[b + 1], of sequence b has position p = start[b] + i - cu_new[b]:
+ *   q_out[i, h]            <- bf16(RoPE(RMSNorm(q_in[i, h])))
+ *   page row of (b, p), g  <- RoPE(RMSNorm(k_new[i, g])) for keys, v_new[i, g] for values
+ * RoPE turns the first rot_dim elements of a head, paired within them (i with i + rot_dim / 2, or
+ * 2i with 2i + 1), at frequency theta^(-2i / rot_dim) or inv_freq[i], i < rot_dim / 2; the others
+ * stay as RMSNorm (over all of D) leaves them. rot_dim = 0 turns nothing.
+ * bf16 pages: keys within one bf16 step of the exact value, values bit for bit.
+ * e4m3 pages: with s the scale of (page, g), a power of two unless the caller wrote another,
+ *   s    = the smallest power of two (2^-64 at least) with |x| <= 448 s for all finite values x
+ *          that the call stores there; if the page held tokens before (the first new row is not
+ *          row 0), the old scale if that is larger. When it grows, the page's earlier codes c
+ *          become e4m3(c * s_old / s).
+ *   code = the nearest e4m3 value to x / s (ties to even); the keys' codes are those of the
+ *          exact rotated key. Infinities become +-448 s, a NaN stays one.
+ * Rows of a page behind its last token are not touched. A token with start[b] < 0, or a position
+ * outside the table, is skipped and raises DEC_DEVERR_POS_SKIPPED (its q_out row is written when
+ * start[b] >= 0). Tokens outside every [cu_new[b], cu_new[b + 1]) are not touched.
+ * q_in, q_out   [device|host] bf16, row (i, h) at i * q_ld + h * D (qo_ld for q_out): the same
+ *               buffer and stride (in place), or not overlapping.
+ * k_new, v_new  [device|host] bf16, row (i, g) at i * k_ld + g * D (v_ld): the column blocks of a
+ *               packed projection [n, (Hq + 2 Hkv) D] serve as they are.
+ * q_ld, qo_ld >= Hq D and k_ld, v_ld >= Hkv D, in elements, multiples of 8.
+ * start [device|host] int32 [B]: the tokens that sequence b holds already.
+ * cu_new [device|host] int32 [B + 1], not decreasing; NULL: one token per sequence, n = B.
+ * n tokens, 0 <= n < 2^24.  rot_dim a multiple of 16, 0 .. D.
+ * The other arguments as in dec_qknorm_rope_kv_append. */
+dec_status dec_qknorm_rope_paged_append(
+    const void *q_in, int64_t q_ld, void *q_out, int64_t qo_ld, const void *k_new, int64_t k_ld,
+    const void *v_new, int64_t v_ld, const void *q_norm_w, const void *k_norm_w, void *k_pages,
+    void *v_pages, dec_dtype type, float *k_scale, float *v_scale, const int32_t *table,
+    int max_pages, const int32_t *start, const int32_t *cu_new, int n, int B, int Hq, int Hkv,
+    int D, int num_pages, int page, int rot_dim, float rope_theta, dec_rope_layout layout,
+    const double *inv_freq, float eps, uint32_t *error_word, dec_stream_t stream);
+
+/* dec_gqa_decode_attn over pages: sequence b attends to its tokens t < lens[b], or with window >
+ * 0 to the last min(lens[b], window) of them (pages wholly before the window are not looked up).
+ * A sequence that sees no token gives zeros. Rows behind a sequence's last token, and rows of its
+ * first page before the window, may hold anything.
+ * q          [device|host] bf16 [B, Hq, D] (rotated);  out [device|host] bf16 [B, Hq, D].
+ * lens       [device|host] int32 [B]; max_len a host upper bound, 0 <= max_len <= max_pages * page.
+ *            A length outside [0, max_len] is clamped and raises DEC_DEVERR_LEN_CLAMPED.
+ * scale      <= 0 selects 1/sqrt(D); at most 1e30.  window >= 0.
+ * num_parts  CTAs the work is cut over; 0 lets the library choose.
+ * workspace  [device] at least dec_paged_attn_workspace_bytes(...) bytes, 256-byte aligned, zeroed
+ *            before its first use (its first word is the device error word; after a
+ *            DEC_DEVERR_WAIT_TIMEOUT zero it again); it serves one call at a time.
+ * 1 <= Hq/Hkv <= 8; B * Hkv * max_len / 128 + 8 B Hkv < 2^31. The size is 0 for arguments that
+ * the call refuses. */
+size_t dec_paged_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len, int num_parts);
+dec_status dec_gqa_paged_attn(const void *q, const void *k_pages, const void *v_pages,
+                              dec_dtype type, const float *k_scale, const float *v_scale,
+                              const int32_t *table, int max_pages, const int32_t *lens, void *out,
+                              int B, int Hq, int Hkv, int D, int num_pages, int page, int max_len,
+                              float scale, int window, int num_parts, void *workspace,
+                              size_t workspace_bytes, dec_stream_t stream);
+
+/* Tokens start[b] <= t < lens[b] (start NULL: from 0) into contiguous bf16 caches, as the calls
+ * above that are not paged read them:
+ *   k_out[b, g, t - start[b]] <- bf16(code * scale), or the bf16 row itself;  v_out likewise.
+ * Other rows are untouched. At most `rows` tokens are copied (more raise DEC_DEVERR_LEN_CLAMPED, as
+ * does a length outside [0, max_pages * page]); start[b] < 0 counts as 0 and raises
+ * DEC_DEVERR_POS_SKIPPED.
+ * start, lens [device|host] int32 [B];  k_out, v_out [device] bf16 [B, Hkv, rows, D], rows >= 1;
+ * error_word [device|host] uint32, or NULL. */
+dec_status dec_paged_gather(const void *k_pages, const void *v_pages, dec_dtype type,
+                            const float *k_scale, const float *v_scale, const int32_t *table,
+                            int max_pages, const int32_t *start, const int32_t *lens, void *k_out,
+                            void *v_out, int B, int Hkv, int D, int num_pages, int page, int rows,
+                            uint32_t *error_word, dec_stream_t stream);
+
+/* dec_decode_step over a paged cache, on one stream: dec_rmsnorm_residual, then
+ * dec_qknorm_rope_paged_append of one token per sequence at pos[b] (q in place), then
+ * dec_gqa_paged_attn over lens[b] tokens. The error word is the workspace's. All arguments are
+ * checked before the first launch. q [device|host]; the others as in those calls. */
+dec_status dec_paged_decode_step(
+    const void *x, void *residual, const void *norm_w, void *y, int hidden, float eps, void *q,
+    const void *k_new, const void *v_new, const void *q_norm_w, const void *k_norm_w,
+    void *k_pages, void *v_pages, dec_dtype type, float *k_scale, float *v_scale,
+    const int32_t *table, int max_pages, const int32_t *pos, const int32_t *lens, void *out, int B,
+    int Hq, int Hkv, int D, int num_pages, int page, int max_len, int rot_dim, float rope_theta,
+    dec_rope_layout layout, const double *inv_freq, float scale, int window, int num_parts,
+    void *workspace, size_t workspace_bytes, dec_stream_t stream);
+
 /* ------------------------------------------------------- log probabilities
  * Per row b of the logits, with z = logits[b, 0..V) / temperature and lse = ln sum e^z:
  *   logprobs[b, c]     = z[ids[b, c]] - lse      (-inf for an id outside [0, V))
@@ -642,7 +749,6 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  *   z has to stay finite in fp32 (a temperature far below 1e-30 does not).
  *   0 <= B < 2^21; 1 <= V <= 262144; ld >= V; 0 <= C <= 65536; 0 <= K <= min(32, V);
  *   temperature finite, > 0. Pointers aligned to their elements. */
-typedef enum dec_dtype { DEC_F32 = 0, DEC_BF16 = 1 } dec_dtype;
 dec_status dec_token_logprobs(const void *logits, dec_dtype type, int ld, const int32_t *ids,
                               int C, float *logprobs, float *entropy, int32_t *top_ids,
                               float *top_logprobs, int K, int B, int V, float temperature,

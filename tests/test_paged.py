@@ -1,0 +1,661 @@
+"""The paged cache on the GPU against the float64 oracle: the append with its rotation, the
+single-query attention, the gather, and a run of them as a server uses them.
+
+Attention is held, element by element, to one bf16 step of the exact value (its rounding, twice over)
+plus (2^-8 + 2^-10) sum_t p_t |v_t|: a weight is held in two e4m3 terms of 4 significant bits each,
+p = hi + lo + r with |p - hi| <= 2^-4 p and |r| <= 2^-4 |p - hi|, that is 2^-8 of each; the second
+term covers the scores' fp32 arithmetic. Appended keys' and values' codes and scales have no tolerance.
+"""
+import numpy as np
+import pytest
+import torch
+
+import decode_step_attention_gb300 as dsa
+from oracle import decode_ref as O
+from oracle import paged as OP
+from tol import bf16_ulp, check_float, check_ulp
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def rnd(gen, *shape):
+    return torch.randn(shape, generator=gen).to(BF16)
+
+
+def make_cache(gen, P, Hkv, page, D, dtype, pow2=True):
+    """A pool of finite values on the GPU, and the same for the oracle."""
+    k, v = (torch.randn(P, Hkv, page, D, generator=gen) for _ in range(2))
+    if dtype is BF16:
+        k, v, ks, vs = k.to(BF16), v.to(BF16), None, None
+    else:
+        k, v = (64 * k).to(E4M3), (64 * v).to(E4M3)
+        e = torch.randint(-9, -3, (2, P, Hkv), generator=gen).float()
+        if not pow2:
+            e = e + torch.rand((2, P, Hkv), generator=gen)
+        ks, vs = torch.exp2(e)
+    gpu = [None if t is None else t.to(DEV) for t in (k, v, ks, vs)]
+    return gpu, oracle_cache(gpu)
+
+
+def oracle_cache(gpu):
+    return dict(zip(("k", "v", "ks", "vs"), (f64(t) for t in gpu)))
+
+
+def make_table(rng, lens, page, P, width=None, first=None):
+    """A table of distinct pages; entries that nothing needs are far outside the pool."""
+    need = [-(-int(n) // page) for n in lens]
+    skip = [0] * len(need) if first is None else [int(f) // page for f in first]
+    width = max([1] + need) if width is None else width
+    table = np.full((len(need), width), 0x7fffff00, dtype=np.int64)
+    free = list(rng.permutation(P))
+    for b, (n, s) in enumerate(zip(need, skip)):
+        for j in range(s, n):
+            table[b, j] = free.pop()
+    return table
+
+
+def check_attn(out, ref, size, what):
+    g, err = f64(out), np.abs(f64(out) - ref)
+    assert np.all(np.isfinite(g)), what
+    bound = bf16_ulp(ref) + (2.0 ** -8 + 2.0 ** -10) * size + 1e-30
+    assert np.all(err <= bound), (what, float((err / bound).max()))
+    norm = np.linalg.norm(ref)
+    assert np.linalg.norm(f64(out) - ref) <= 4e-3 * norm, what
+
+
+def attend(q, gpu, table, lens, **kw):
+    k, v, ks, vs = gpu
+    B, Hq, D = q.shape
+    Hkv, page = k.shape[1], k.shape[2]
+    max_len = kw.pop("max_len", max(1, int(max(lens))))
+    ws = kw.pop("workspace", None)
+    if ws is None:
+        ws = dsa.alloc_paged_workspace(B, Hq, Hkv, D, max_len, kw.get("num_parts", 0))
+    out = torch.full((B, Hq, D), float("nan"), dtype=BF16, device=DEV)
+    dsa.gqa_paged_attn(q, k, v, i32(table), i32(lens), k_scale=ks, v_scale=vs, max_len=max_len,
+                       workspace=ws, out=out, **kw)
+    torch.cuda.synchronize()
+    return out, dsa.device_errors(ws)
+
+
+# ---- attention ------------------------------------------------------------------------
+LENS = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 700]
+
+
+@pytest.mark.parametrize("window", [0, 1, 100, 129])
+@pytest.mark.parametrize("D,page,Hkv,G", [(128, 16, 2, 8), (128, 64, 1, 1), (64, 32, 3, 5),
+                                          (64, 128, 2, 7), (128, 128, 1, 3), (64, 16, 1, 8)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_attention(dtype, D, page, Hkv, G, window):
+    gen, rng = torch.Generator().manual_seed(D + page + G), np.random.default_rng(window)
+    lens = rng.permutation(LENS)
+    P = sum(-(-int(n) // page) for n in lens) + 2
+    gpu, ref = make_cache(gen, P, Hkv, page, D, dtype)
+    first = np.maximum(0, lens - window) if window else None
+    table = make_table(rng, lens, page, P, first=first)
+    # what no token of a call is: NaN in rows behind the lengths, before the windows, in other pages
+    real = np.zeros((P, page), dtype=bool)
+    for b, n in enumerate(lens):
+        for t in range(0 if first is None else first[b], n):
+            real[table[b, t // page], t % page] = True
+    dead = torch.from_numpy(~real).to(DEV)
+    for t in gpu[:2]:
+        raw = t.view(torch.uint8) if dtype is E4M3 else t.view(torch.int16)
+        raw[dead[:, None].expand(P, Hkv, page)] = 0x7f if dtype is E4M3 else 0x7fff
+    q = rnd(gen, len(lens), Hkv * G, D).to(DEV)
+    out, err = attend(q, gpu, table, lens, window=window)
+    want, size = OP.attention(f64(q), ref, table, lens, window=window)
+    check_attn(out, want, size, (dtype, D, page, G, window))
+    assert err == 0
+    assert np.all(f64(out)[np.asarray(lens) == 0] == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("parts", [0, 1, 2, 7, 152, 333])
+def test_attention_any_cut(dtype, parts):
+    """However the work is cut, and twice the same bits."""
+    gen, rng = torch.Generator().manual_seed(5), np.random.default_rng(5)
+    lens = [1500, 3, 0, 640, 129, 1, 4000]
+    gpu, ref = make_cache(gen, 400, 2, 16, 128, dtype)
+    table = make_table(rng, lens, 16, 400)
+    q = rnd(gen, len(lens), 8, 128).to(DEV)
+    ws = dsa.alloc_paged_workspace(len(lens), 8, 2, 128, 4000, parts)
+    out, err = attend(q, gpu, table, lens, num_parts=parts, workspace=ws)
+    want, size = OP.attention(f64(q), ref, table, lens)
+    check_attn(out, want, size, (dtype, parts))
+    again, err2 = attend(q, gpu, table, lens, num_parts=parts, workspace=ws)
+    assert torch.equal(out, again) and err == err2 == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_attention_many_sequences(dtype):
+    gen, rng = torch.Generator().manual_seed(6), np.random.default_rng(6)
+    lens = rng.integers(0, 300, 700)
+    page, P = 32, 700 * 10
+    gpu, ref = make_cache(gen, P, 1, page, 64, dtype, pow2=False)
+    table = make_table(rng, lens, page, P)
+    q = rnd(gen, 700, 2, 64).to(DEV)
+    out, err = attend(q, gpu, table, lens)
+    want, size = OP.attention(f64(q), ref, table, lens)
+    check_attn(out, want, size, dtype)
+    assert err == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_attention_long(dtype):
+    """131072 tokens, one page of them in use over and over behind others (a shared page may repeat)."""
+    gen, rng = torch.Generator().manual_seed(7), np.random.default_rng(7)
+    n, page, P = 131072 - 5, 128, 40
+    gpu, ref = make_cache(gen, P, 2, page, 128, dtype)
+    table = rng.integers(0, P, (1, 1024))
+    q = rnd(gen, 1, 16, 128).to(DEV)
+    out, err = attend(q, gpu, table, [n])
+    want, size = OP.attention(f64(q), ref, table, [n])
+    check_attn(out, want, size, dtype)
+    assert err == 0
+
+
+def test_attention_peaked_scores():
+    """Large scores: one token takes nearly all the weight, then the tail's share matters."""
+    gen, rng = torch.Generator().manual_seed(8), np.random.default_rng(8)
+    lens = [3000, 3000, 700]
+    for dtype in (BF16, E4M3):
+        gpu, ref = make_cache(gen, 220, 1, 32, 128, dtype)
+        table = make_table(rng, lens, 32, 220)
+        q = (rnd(gen, 3, 4, 128) * torch.tensor([1.0, 4.0, 30.0, 0.0])[None, :, None]).to(BF16).to(DEV)
+        # a sink: one row of keys along a query, its weight e^11 times the others'
+        at, row = int(table[1, 0]), 5
+        gpu[0][at, 0, row] = (q[1, 0].float() * (1 if dtype is BF16 else 64)).to(dtype)
+        if dtype is E4M3:
+            gpu[2][at, 0] = 2.0 ** -6
+        ref = oracle_cache(gpu)
+        out, _ = attend(q, gpu, table, lens)
+        want, size = OP.attention(f64(q), ref, table, lens)
+        check_attn(out, want, size, dtype)
+
+
+@pytest.mark.parametrize("spread", [4, 20, 60])
+def test_attention_scales_of_every_size(spread):
+    """Scales of values from 2^-spread to 2^spread side by side in a tile; queries far apart in size."""
+    gen, rng = torch.Generator().manual_seed(spread), np.random.default_rng(spread)
+    lens = [16, 130, 1000, 77]
+    gpu, _ = make_cache(gen, 90, 2, 16, 128, E4M3)
+    gpu[3].copy_(torch.exp2(torch.randint(-spread, spread + 1, gpu[3].shape, generator=gen).float()))
+    table = make_table(rng, lens, 16, 90)
+    ref = oracle_cache(gpu)
+    q = rnd(gen, 4, 8, 128)
+    q[:, 1] *= 2.0 ** -20
+    q[:, 2, ::2] *= 2.0 ** -9
+    q[:, 3] = 0
+    q = q.to(DEV)
+    out, _ = attend(q, gpu, table, lens)
+    want, size = OP.attention(f64(q), ref, table, lens)
+    check_attn(out, want, size, spread)
+
+
+def test_attention_scale_argument():
+    gen, rng = torch.Generator().manual_seed(9), np.random.default_rng(9)
+    for dtype in (BF16, E4M3):
+        gpu, ref = make_cache(gen, 30, 2, 32, 64, dtype)
+        lens = [300, 200]
+        table = make_table(rng, lens, 32, 30)
+        q = rnd(gen, 2, 6, 64).to(DEV)
+        for scale in (1.0, 0.01, -1.0):
+            out, _ = attend(q, gpu, table, lens, scale=scale)
+            want, size = OP.attention(f64(q), ref, table, lens, scale=max(scale, 0))
+            check_attn(out, want, size, (dtype, scale))
+
+
+def test_attention_far_pages():
+    """Pages behind 2^32 bytes of the pool."""
+    gen, rng = torch.Generator().manual_seed(10), np.random.default_rng(10)
+    for dtype in (BF16, E4M3):
+        size = 2 if dtype is BF16 else 1
+        P, Hkv, page, D = (9 << 29) // (16 * 64 * 128 * size), 16, 64, 128   # 4.5 GiB each
+        small, _ = make_cache(gen, 12, Hkv, page, D, dtype)
+        k, v = (torch.empty(P, Hkv, page, D, dtype=dtype, device=DEV) for _ in range(2))
+        at = torch.cat([torch.arange(P - 10, P), torch.tensor([0, P // 2])])
+        raw = torch.uint8 if dtype is E4M3 else torch.int16
+        for big, t in ((k, small[0]), (v, small[1])):
+            big.view(raw)[at.to(DEV)] = t.view(raw)
+        ks = vs = None
+        if dtype is E4M3:
+            ks, vs = (torch.ones(P, Hkv, device=DEV) for _ in range(2))
+            ks[at.to(DEV)], vs[at.to(DEV)] = small[2], small[3]
+        pick = rng.permutation(12)
+        table, local = at.numpy()[pick][None], pick[None]
+        q = rnd(gen, 1, 16, D).to(DEV)
+        out, err = attend(q, (k, v, ks, vs), table, [12 * 64 - 7])
+        want, sz = OP.attention(f64(q), oracle_cache(small), local, [12 * 64 - 7])
+        check_attn(out, want, sz, dtype)
+        ko, vo = (torch.zeros(1, Hkv, 40, D, dtype=BF16, device=DEV) for _ in range(2))
+        dsa.paged_gather(k, v, i32(table), i32([12 * 64]), ko, vo, ks, vs, start=i32([12 * 64 - 40]))
+        K, V, _ = OP.tokens(oracle_cache(small), local, 0, 12 * 64 - 40, 12 * 64)
+        check_ulp(f64(ko[0]), K, "far gather", 0.5)
+        check_ulp(f64(vo[0]), V, "far gather", 0.5)
+        # the append into the last page
+        new = rnd(gen, 1, Hkv, D).to(DEV)
+        dsa.qknorm_rope_paged_append(q, new, new, k, v, i32([[P - 1]]), i32([3]), 1e4, k_scale=ks,
+                                     v_scale=vs, rot_dim=0)
+        dsa.paged_gather(k, v, i32([[P - 1]]), i32([4]), ko, vo, ks, vs, start=i32([3]))
+        got = f64(vo[0, :, 0])
+        assert np.all(np.abs(got - f64(new[0])) <= np.abs(f64(new[0])) * 2.0 ** -4 + 1e-2)
+        del k, v, big
+
+
+def test_attention_flags_bad_pages_and_lengths():
+    gen, rng = torch.Generator().manual_seed(11), np.random.default_rng(11)
+    for dtype in (BF16, E4M3):
+        gpu, ref = make_cache(gen, 40, 2, 16, 128, dtype)
+        lens = [200, 90, 33]
+        table = make_table(rng, lens, 16, 40)
+        table[0, 2], table[0, 11], table[1, 5], table[2, :3] = -1, 40, -(1 << 31), (1 << 31) - 1
+        q = rnd(gen, 3, 4, 128).to(DEV)
+        out, err = attend(q, gpu, table, lens)
+        want, size = OP.attention(f64(q), ref, table, lens)
+        check_attn(out, want, size, dtype)
+        assert err == dsa.DEVERR_PAGE_SKIPPED and bool((out[2] == 0).all())
+        table = make_table(rng, lens, 16, 40)
+        out, err = attend(q, gpu, table, [300, -5, 33], max_len=200)
+        want, size = OP.attention(f64(q), ref, table, [200, 0, 33])
+        check_attn(out, want, size, dtype)
+        assert err == dsa.DEVERR_LEN_CLAMPED
+
+
+def test_attention_nan_stays_with_its_sequence_and_head():
+    gen, rng = torch.Generator().manual_seed(12), np.random.default_rng(12)
+    for dtype in (BF16, E4M3):
+        gpu, _ = make_cache(gen, 40, 2, 16, 64, dtype)
+        lens = [200, 150]
+        table = make_table(rng, lens, 16, 40)
+        raw = gpu[1].view(torch.uint8 if dtype is E4M3 else torch.int16)
+        raw[int(table[0, 3]), 1, 4, 9] = 0x7f if dtype is E4M3 else 0x7fc0
+        q = rnd(gen, 2, 8, 64).to(DEV)
+        out, _ = attend(q, gpu, table, lens)
+        bad = torch.isnan(out)
+        assert bool(bad[0, 4:, 9].all())
+        bad[0, 4:, 9] = False
+        assert not bool(bad.any())
+
+
+# ---- append -----------------------------------------------------------------------------
+def run_append(gen, rng, dtype, D, page, Hq, Hkv, layout, rot, norm, start, new, theta=1e4, big=1.0,
+               single=False, packed=False, in_place=False, pow2=True):
+    B, n = len(start), int(np.sum(new))
+    total = np.asarray(start) + np.asarray(new)
+    P = int(sum(-(-int(t) // page) for t in total)) + 3
+    gpu, ref = make_cache(gen, P, Hkv, page, D, dtype, pow2)
+    table = make_table(rng, total, page, P)
+    if packed:
+        qkv = rnd(gen, n, (Hq + 2 * Hkv) * D).to(DEV)
+        q = qkv[:, :Hq * D].view(n, Hq, D)
+        k, v = (qkv[:, (Hq + i * Hkv) * D:(Hq + (i + 1) * Hkv) * D].view(n, Hkv, D) for i in (0, 1))
+    else:
+        q, k, v = (rnd(gen, n, h, D).to(DEV) for h in (Hq, Hkv, Hkv))
+    size = torch.exp2(torch.randint(-3, 4, (n, 1, 1), generator=gen).float()).to(DEV) * big
+    k.mul_(size.to(BF16))
+    v.mul_(size.flip(0).to(BF16))
+    w = (1 + 0.1 * rnd(gen, 2, D).float()).to(BF16).to(DEV) if norm else None
+    cu = None if single else np.concatenate([[0], np.cumsum(new)])
+    args = (f64(q), f64(k), f64(v), ref, table, start, cu, theta, layout, rot)
+    q_want, c_want = OP.append(*args, *((f64(w[0]), f64(w[1])) if norm else (None, None)))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_out = None if in_place else torch.zeros(n, Hq, D, dtype=BF16, device=DEV)
+    got = dsa.qknorm_rope_paged_append(
+        q, k, v, gpu[0], gpu[1], i32(table), i32(start), theta, cu_new=None if single else i32(cu),
+        k_scale=gpu[2], v_scale=gpu[3], layout=layout, rot_dim=rot, q_norm_w=w[0] if norm else None,
+        k_norm_w=w[1] if norm else None, q_out=q_out, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    what = (dtype, D, page, layout, rot, norm)
+    check_float(f64(got), q_want, f"q {what}")
+    if dtype is BF16:
+        check_ulp(f64(gpu[0]), c_want["k"], f"keys {what}")
+    else:
+        assert np.array_equal(f64(gpu[2]), c_want["ks"]), what
+        assert np.array_equal(f64(gpu[3]), c_want["vs"]), what
+        assert np.array_equal(f64(gpu[0]), c_want["k"]), (what, int((f64(gpu[0]) != c_want["k"]).sum()))
+    assert np.array_equal(f64(gpu[1]), c_want["v"]), what
+    return gpu, table
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+@pytest.mark.parametrize("D,page,rot", [(128, 16, 128), (128, 64, 32), (64, 32, 64), (64, 128, 16),
+                                        (128, 128, 112), (64, 16, 0)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_prompts(dtype, D, page, rot, layout, norm):
+    """Ragged prompts, from a page's first row and from inside one, with sequences that get nothing."""
+    gen = torch.Generator().manual_seed(D + page + rot)
+    run_append(gen, np.random.default_rng(rot), dtype, D, page, 6, 2, layout, rot, norm,
+               [0, 5, 130, 16, 7, 127, 0, 300], [200, 1, 0, 31, page, 3, 1, 2 * page + 1])
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("layout", ["neox", "interleaved"])
+@pytest.mark.parametrize("D,page,Hq,Hkv,rot", [(128, 16, 16, 8, 128), (64, 64, 7, 7, 32),
+                                               (128, 32, 5, 1, 16), (64, 128, 40, 20, 64)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_tokens(dtype, D, page, Hq, Hkv, rot, layout, norm):
+    """One token per sequence, at every place of a page."""
+    gen, rng = torch.Generator().manual_seed(Hq), np.random.default_rng(Hq)
+    start = np.concatenate([[0, 1, page - 1, page, page + 1, 2 * page - 1], rng.integers(0, 400, 31)])
+    run_append(gen, rng, dtype, D, page, Hq, Hkv, layout, rot, norm, start, np.ones(37, dtype=int),
+               single=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [1, 2, 3, 33, 300])
+def test_append_token_batches(dtype, n):
+    gen, rng = torch.Generator().manual_seed(n), np.random.default_rng(n)
+    run_append(gen, rng, dtype, 128, 16, 4, 2, "neox", 128, True, rng.integers(0, 40, n),
+               np.ones(n, dtype=int), single=True)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** -12])
+def test_append_scales_grow_or_stay(big):
+    """New tokens far above and far below what a page holds; scales of any value in the page before."""
+    for pow2 in (True, False):
+        gen, rng = torch.Generator().manual_seed(3), np.random.default_rng(3)
+        run_append(gen, rng, E4M3, 128, 64, 2, 2, "neox", 64, False, [10, 63, 0, 40, 7],
+                   [20, 70, 3, 1, 60], big=big, pow2=pow2)
+        run_append(gen, rng, E4M3, 64, 32, 2, 2, "interleaved", 64, True, [10, 31, 0, 20, 7],
+                   np.ones(5, dtype=int), big=big, single=True, pow2=pow2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_far_positions(dtype):
+    gen, rng = torch.Generator().manual_seed(4), np.random.default_rng(4)
+    run_append(gen, rng, dtype, 128, 128, 4, 1, "neox", 128, True, [130944, 70001], [129, 1],
+               theta=1e6)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("single", [True, False])
+def test_append_from_a_packed_projection(dtype, single):
+    """q, k and v as column blocks of [n, (Hq + 2 Hkv) D], q rotated where it lies."""
+    gen, rng = torch.Generator().manual_seed(13), np.random.default_rng(13)
+    new = np.ones(9, dtype=int) if single else [40, 1, 90]
+    run_append(gen, rng, dtype, 64, 16, 6, 3, "interleaved", 32, True, rng.integers(0, 50, len(new)), new,
+               single=single, packed=True, in_place=True)
+
+
+def test_append_values_without_a_scale():
+    """Zeros, infinities and NaN: a page of zeros has the smallest scale, and neither of the others
+    sets one."""
+    k, v, ks, vs = dsa.alloc_paged_cache(4, 16, 1, 64)
+    x = torch.zeros(3, 1, 64, dtype=BF16, device=DEV)
+    table = i32([[1], [2], [3]])
+    x[1, 0, 0], x[1, 0, 1], x[1, 0, 2], x[1, 0, 3] = float("inf"), float("nan"), -1.0, float("-inf")
+    x[2, 0, 5] = 3.3e38
+    dsa.qknorm_rope_paged_append(x.clone(), x, x, k, v, table, i32([0, 0, 0]), 1e4, k_scale=ks, v_scale=vs,
+                                 rot_dim=0)
+    for s in (ks, vs):
+        assert s[1, 0] == 2.0 ** -64 and s[2, 0] == 2.0 ** -8 and s[3, 0] == 2.0 ** 120
+    for p in (k, v):
+        row = p.float()[2, 0, 0]
+        assert row[0] == 448 and torch.isnan(row[1]) and row[2] == -256 and row[3] == -448
+        assert bool((p.float()[1] == 0).all())
+
+
+def test_append_skips_what_has_no_place():
+    gen, rng = torch.Generator().manual_seed(14), np.random.default_rng(14)
+    for dtype in (BF16, E4M3):
+        for single in (True, False):
+            gpu, ref = make_cache(gen, 6, 2, 16, 64, dtype)
+            table = np.array([[0, 6], [1, -7], [2, 3], [4, 5]])
+            start = [16, 20, -1, 32]   # a bad page, a bad page, a bad start, behind the table
+            new = [1, 1, 1, 1] if single else [2, 1, 3, 5]
+            n = sum(new)
+            cu = np.concatenate([[0], np.cumsum(new)])
+            q, k, v = (rnd(gen, n, h, 64).to(DEV) for h in (4, 2, 2))
+            before = [t if t is None else t.clone() for t in gpu]
+            q_want, _ = OP.append(f64(q), f64(k), f64(v), ref, table, start, cu, 1e4, "neox", 64)
+            err = torch.zeros(1, dtype=torch.int32, device=DEV)
+            dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], i32(table), i32(start), 1e4,
+                                         cu_new=None if single else i32(cu), k_scale=gpu[2],
+                                         v_scale=gpu[3], error_word=err)
+            assert int(err) == dsa.DEVERR_PAGE_SKIPPED | dsa.DEVERR_POS_SKIPPED
+            check_float(f64(q), q_want, "q of skipped tokens")
+            for a, b in zip(gpu, before):
+                assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_append_leaves_tokens_of_no_sequence():
+    gen = torch.Generator().manual_seed(15)
+    for dtype in (BF16, E4M3):
+        gpu, _ = make_cache(gen, 6, 2, 16, 64, dtype)
+        q, k, v = (rnd(gen, 20, h, 64).to(DEV) for h in (4, 2, 2))
+        q0, before = q.clone(), [t if t is None else t.clone() for t in gpu]
+        dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], i32([[1, 2], [3, 4]]), i32([0, 9]), 1e4,
+                                     cu_new=i32([3, 8, 12]), k_scale=gpu[2], v_scale=gpu[3])
+        assert torch.equal(q[:3], q0[:3]) and torch.equal(q[12:], q0[12:])
+        assert not torch.equal(q[3:12], q0[3:12])
+        for a, b in zip(gpu[:2], before):
+            rows = (a.view(torch.uint8) != b.view(torch.uint8)).flatten(3).any(-1).any(1)
+            assert bool(rows[1, :5].all()) and bool(rows[3, 9:13].all())
+            rows[1, :5] = rows[3, 9:13] = False
+            if dtype is E4M3:
+                rows[3, :9] = False  # (what the page held, under a scale that may have grown)
+            assert not bool(rows.any())
+
+
+def test_append_frequency_table():
+    gen, rng = torch.Generator().manual_seed(16), np.random.default_rng(16)
+    gpu, ref = make_cache(gen, 9, 2, 16, 128, E4M3)
+    table = make_table(rng, [40, 30], 16, 9)
+    q, k, v = (rnd(gen, 30, h, 128).to(DEV) for h in (4, 2, 2))
+    inv = dsa.rope_inv_freq(64, 1e4, "yarn", 4.0, 4096)
+    q_want, c = OP.append(f64(q), f64(k), f64(v), ref, table, [20, 20], [0, 20, 30], 1e4, "neox", 64,
+                          inv_freq=inv.numpy())
+    dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], i32(table), i32([20, 20]), 0.0,
+                                 cu_new=i32([0, 20, 30]), k_scale=gpu[2], v_scale=gpu[3], rot_dim=64,
+                                 inv_freq=inv)
+    check_float(f64(q), q_want, "q with a table")
+    assert np.array_equal(f64(gpu[0]), c["k"]) and np.array_equal(f64(gpu[1]), c["v"])
+
+
+# ---- gather -------------------------------------------------------------------------------
+@pytest.mark.parametrize("D,page,Hkv", [(128, 16, 2), (64, 128, 3), (128, 64, 1), (64, 32, 2)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_gather(dtype, D, page, Hkv):
+    gen, rng = torch.Generator().manual_seed(D + page), np.random.default_rng(page)
+    lens = np.array([0, 1, page, page + 1, 500, 63, 64, 130])
+    start = np.array([0, 0, 3, page, 123, 62, 70, 0])
+    P = int(sum(-(-n // page) for n in lens)) + 1
+    gpu, ref = make_cache(gen, P, Hkv, page, D, dtype, pow2=False)
+    table = make_table(rng, lens, page, P)
+    for st, rows in ((None, 500), (start, 377)):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        ko, vo = (torch.full((8, Hkv, rows, D), 7.0, dtype=BF16, device=DEV) for _ in range(2))
+        dsa.paged_gather(gpu[0], gpu[1], i32(table), i32(lens), ko, vo, gpu[2], gpu[3],
+                         start=None if st is None else i32(st), error_word=err)
+        for b, n in enumerate(lens):
+            s = 0 if st is None else int(st[b])
+            K, V, _ = OP.tokens(ref, table, b, min(s, n), int(n))
+            for out, want in ((ko, K), (vo, V)):
+                check_ulp(f64(out[b, :, :max(0, n - s)]), want, "gather", 0.5)
+                assert bool((out[b, :, max(0, n - s):] == 7).all())
+        assert int(err) == 0
+
+
+def test_gather_flags():
+    gen = torch.Generator().manual_seed(1)
+    gpu, ref = make_cache(gen, 5, 1, 16, 64, BF16)
+    table = np.array([[0, 9, 2], [3, 4, -1]])
+    ko, vo = (torch.full((2, 1, 20, 64), 7.0, dtype=BF16, device=DEV) for _ in range(2))
+
+    def call(lens, start):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        dsa.paged_gather(gpu[0], gpu[1], i32(table), i32(lens), ko, vo, start=i32(start), error_word=err)
+        return int(err)
+    assert call([20, 20], [0, 0]) == dsa.DEVERR_PAGE_SKIPPED
+    assert bool((ko[0, :, 16:] == 7).all()) and np.array_equal(f64(ko[1, 0, :16]), ref["k"][3, 0])
+    assert call([16, 32], [0, 0]) == dsa.DEVERR_LEN_CLAMPED     # more than `rows` tokens
+    assert call([16, 1 << 30], [0, 30]) == dsa.DEVERR_LEN_CLAMPED | dsa.DEVERR_PAGE_SKIPPED
+    assert call([16, -3], [0, 0]) == dsa.DEVERR_LEN_CLAMPED
+    assert call([4, 0], [-2, 5]) == dsa.DEVERR_POS_SKIPPED
+
+
+# ---- together -----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,D,page", [(E4M3, 128, 16), (BF16, 64, 32), (E4M3, 64, 128)])
+def test_a_server_run(dtype, D, page):
+    """Prompts of several lengths, then tokens one by one: append and attention against the oracle
+    fed with the cache as it stands, and the contiguous calls over a gathered cache beside them."""
+    gen, rng = torch.Generator().manual_seed(21), np.random.default_rng(21)
+    B, Hq, Hkv, steps = 4, 8, 2, 20
+    new = np.array([70, 1, 33, 128])
+    P = B * -(-(128 + steps) // page)
+    k, v, ks, vs = dsa.alloc_paged_cache(P, page, Hkv, D, dtype)
+    table = rng.permutation(P).reshape(B, -1)
+    t_gpu, start = i32(table), torch.zeros(B, dtype=torch.int32, device=DEV)
+    n = int(new.sum())
+    q, kn, vn = (rnd(gen, n, h, D).to(DEV) for h in (Hq, Hkv, Hkv))
+    dsa.qknorm_rope_paged_append(q, kn, vn, k, v, t_gpu, start, 1e4, k_scale=ks, v_scale=vs,
+                                 cu_new=i32(np.concatenate([[0], np.cumsum(new)])))
+    start += i32(new)
+    ws = dsa.alloc_paged_workspace(B, Hq, Hkv, D, 128 + steps)
+    hidden = 256
+    norm_w = rnd(gen, hidden).to(DEV)
+    for step in range(steps):
+        lens = start + 1
+        x, res = (rnd(gen, B, hidden).to(DEV) for _ in range(2))
+        res0 = res.clone()
+        q, kn, vn = (rnd(gen, B, h, D).to(DEV) for h in (Hq, Hkv, Hkv))
+        q0, y, out = q.clone(), torch.empty_like(x), torch.empty_like(q)
+        before = oracle_cache((k, v, ks, vs))
+        dsa.paged_decode_step(x, res, norm_w, y, q, kn, vn, k, v, t_gpu, start, lens, out, ws, 1e4,
+                              k_scale=ks, v_scale=vs, max_len=128 + steps)
+        torch.cuda.synchronize()
+        after = oracle_cache((k, v, ks, vs))
+        q_want, want = OP.append(f64(q0), f64(kn), f64(vn), before, table, f64(start).astype(int), None, 1e4,
+                                 "neox", D)
+        check_float(f64(q), q_want, "step q")
+        if dtype is E4M3:
+            for name in want:
+                assert np.array_equal(after[name], want[name]), (step, name)
+        else:
+            check_ulp(after["k"], want["k"], "step keys")
+        ref, size = OP.attention(f64(q), after, table, f64(lens).astype(int))
+        check_attn(out, ref, size, step)
+        y_ref, s_ref = O.rmsnorm_residual(f64(x), f64(res0), f64(norm_w), 1e-6)
+        check_float(f64(y), y_ref, "step y")
+        check_ulp(f64(res), s_ref, "step residual")
+        if step % 10 == 9:  # the calls over contiguous caches
+            kc, vc = (torch.zeros(B, Hkv, 128 + steps, D, dtype=BF16, device=DEV) for _ in range(2))
+            dsa.paged_gather(k, v, t_gpu, lens, kc, vc, ks, vs)
+            flat = dsa.gqa_decode_attn(q, kc, vc, lens)
+            check_attn(flat, ref, size, ("contiguous", step))
+        start += 1
+    assert dsa.device_errors(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_captured_and_on_another_stream(dtype):
+    """A step on a side stream, captured and replayed with other tokens, lengths and tables; two
+    graphs that share a workspace, one after the other."""
+    gen, rng = torch.Generator().manual_seed(22), np.random.default_rng(22)
+    B, Hq, Hkv, D, page, P, top = 3, 8, 2, 128, 16, 150, 700
+    gpu, _ = make_cache(gen, P, Hkv, page, D, dtype)
+    k, v, ks, vs = gpu
+    table = torch.zeros(B, -(-top // page), dtype=torch.int32, device=DEV)
+    pos, lens = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(2))
+    q, kn, vn = (torch.zeros(B, h, D, dtype=BF16, device=DEV) for h in (Hq, Hkv, Hkv))
+    out = torch.zeros_like(q)
+    ws = dsa.alloc_paged_workspace(B, Hq, Hkv, D, top)
+
+    def body():
+        dsa.qknorm_rope_paged_append(q, kn, vn, k, v, table, pos, 1e4, k_scale=ks, v_scale=vs)
+        dsa.gqa_paged_attn(q, k, v, table, lens, ks, vs, max_len=top, workspace=ws, out=out)
+
+    def fill():
+        n = rng.integers(1, top, B)
+        t = make_table(rng, n, page, P, width=table.shape[1])
+        table.copy_(i32(t)), lens.copy_(i32(n)), pos.copy_(i32(n - 1))
+        for x in (q, kn, vn):
+            x.copy_(rnd(gen, *x.shape))
+        return n, t
+
+    def check(n, t, what):
+        torch.cuda.synchronize()
+        ref, size = OP.attention(f64(q), oracle_cache(gpu), t, n)
+        check_attn(out, ref, size, what)
+
+    side = torch.cuda.Stream()
+    n, t = fill()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        body()
+    check(n, t, "side stream")
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            body()
+        graphs.append(g)
+    for i in range(4):
+        n, t = fill()
+        graphs[i % 2].replay()
+        check(n, t, ("replay", i))
+    # the stream argument
+    n, t = fill()
+    side.wait_stream(torch.cuda.current_stream())
+    dsa.qknorm_rope_paged_append(q, kn, vn, k, v, table, pos, 1e4, k_scale=ks, v_scale=vs, stream=side)
+    got = dsa.gqa_paged_attn(q, k, v, table, lens, ks, vs, max_len=top, stream=side)
+    side.synchronize()
+    out.copy_(got)
+    check(n, t, "stream argument")
+    assert dsa.device_errors(ws) == 0
+
+
+def test_host_memory():
+    """Queries, lengths and outputs in pinned host memory."""
+    gen, rng = torch.Generator().manual_seed(23), np.random.default_rng(23)
+    lens = [100, 37]
+    gpu, ref = make_cache(gen, 12, 2, 16, 64, E4M3)
+    table = make_table(rng, lens, 16, 12)
+    q, k, v = (rnd(gen, 2, h, 64).pin_memory() for h in (6, 2, 2))
+    start = torch.tensor([99, 36], dtype=torch.int32).pin_memory()
+    n = torch.tensor(lens, dtype=torch.int32).pin_memory()
+    out = torch.zeros(2, 6, 64, dtype=BF16).pin_memory()
+    q_want, c = OP.append(f64(q), f64(k), f64(v), ref, table, [99, 36], None, 1e4, "neox", 64)
+    t = i32(table)
+    dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], t, start, 1e4, k_scale=gpu[2], v_scale=gpu[3])
+    dsa.gqa_paged_attn(q, gpu[0], gpu[1], t, n, gpu[2], gpu[3], out=out)
+    torch.cuda.synchronize()
+    check_float(f64(q), q_want, "host q")
+    assert np.array_equal(f64(gpu[0]), c["k"])
+    want, size = OP.attention(f64(q), oracle_cache(gpu), table, lens)
+    check_attn(out, want, size, "host out")
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    gen, rng = torch.Generator().manual_seed(24), np.random.default_rng(24)
+    lens = [5000, 3000]
+    gpu, ref = make_cache(gen, 260, 2, 32, 128, E4M3)
+    table = make_table(rng, lens, 32, 260)
+    qs = [rnd(gen, 2, 16, 128).to(DEV) for _ in range(2)]
+    t, n = i32(table), i32(lens)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [dsa.alloc_paged_workspace(2, 16, 2, 128, 5000) for _ in range(2)]
+    outs = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, s, ws, out in zip(qs, streams, spaces, outs):
+            dsa.gqa_paged_attn(q, gpu[0], gpu[1], t, n, gpu[2], gpu[3], max_len=5000, workspace=ws,
+                               out=out, stream=s)
+    torch.cuda.synchronize()
+    for q, out in zip(qs, outs):
+        want, size = OP.attention(f64(q), ref, table, lens)
+        check_attn(out, want, size, "two streams")
