@@ -1538,6 +1538,26 @@ dec_status where_attn(const PagedCache &c, const void *q, const int32_t *lens, v
                          {workspace, "workspace", false}});
 }
 
+// Pages [num_pages * Hkv, page, D] as a 3-D tensor: boxes of a page's rows, the whole row or 128 bytes of
+// it wide, with a swizzle of that width. A box outside reads as zeros.
+dec_status encode_pages_map(CUtensorMap *map, const void *pages, const PagedCache &c) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return fail(DEC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t size = c.e4m3 ? 1 : 2, row = c.D * size;
+  cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.page,
+                        (cuuint64_t)c.num_pages * (cuuint64_t)c.Hkv};
+  cuuint64_t strides[2] = {row, row * c.page};
+  cuuint32_t box[3] = {(cuuint32_t)((row < 128 ? row : 128) / size), (cuuint32_t)c.page, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void *>(pages), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DEC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return DEC_OK;
+}
+
 dec_status paged_attn_go(const PagedCache &c, const void *q, const int32_t *lens, void *out, int B,
                          int Hq, int max_len, float scale, int window, int num_parts,
                          void *workspace, dec_stream_t stream) {
@@ -1553,7 +1573,11 @@ dec_status paged_attn_go(const PagedCache &c, const void *q, const int32_t *lens
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)c.D);
   a.scale_log2 = (float)((double)sc * 1.4426950408889634);
   const int parts = paged_attn_parts(B, c.Hkv, max_len, num_parts, sm_count_of_current());
-  const cudaError_t e = launch_paged_attn(c, a, parts, workspace, as_stream(stream));
+  CUtensorMap k, v;
+  dec_status st = encode_pages_map(&k, c.k_pages, c);
+  if (st == DEC_OK) st = encode_pages_map(&v, c.v_pages, c);
+  if (st != DEC_OK) return st;
+  const cudaError_t e = launch_paged_attn(k, v, c, a, parts, workspace, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gqa_paged_attn launch");
   return ok();
 }

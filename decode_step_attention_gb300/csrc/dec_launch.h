@@ -248,8 +248,11 @@ struct PagedAttnArgs {
 constexpr int kPagedMaxParts = 4096;
 int paged_attn_parts(int B, int Hkv, int max_len, int num_parts, int sms);
 size_t paged_attn_ws_bytes(int B, int Hq, int Hkv, int D, int parts);
-cudaError_t launch_paged_attn(const PagedCache &c, const PagedAttnArgs &a, int parts,
-                              void *workspace, cudaStream_t stream);
+// k, v: the pages as [num_pages * Hkv, page, D], boxes of a page's rows, at most 128 bytes wide, with a
+// swizzle of that width.
+cudaError_t launch_paged_attn(const CUtensorMap &k, const CUtensorMap &v, const PagedCache &c,
+                              const PagedAttnArgs &a, int parts, void *workspace,
+                              cudaStream_t stream);
 
 // ---- log probabilities -------------------------------------------------------------
 constexpr int kLogprobMaxK = 32;

@@ -1,121 +1,895 @@
 // Single-query GQA attention over a paged cache of bf16 values or e4m3 codes with a scale per
-// (page, KV head): out[b, h] = sum_t softmax_t(scale q[b, h] . K_t) V_t over the last `window` tokens
-// (all of them without one).
+// (page, KV head), on the 5th-generation tensor cores:
 //
-// One block per (sequence, KV head): each of 8 warps takes every eighth token, a query group's heads
-// in registers, with a running maximum and sum; the warps' states are joined at the end.
+//   z[h, t]   = scale q[b,h] . K_t = (scale s_q s_k) (q' . c_t)      c: codes, q = s_q q'
+//   out[b,h]  = sum_t softmax_t(z) V_t over the last `window` tokens (all without one)
+//
+// Tokens are the M of the instructions, query heads the N: S^T[128 tokens, heads] = K Q^T takes a tile
+// of keys as it lies in shared memory, codes included, and O^T[D, heads] = V^T P^T the values likewise
+// (tokens x dims: the MN-major operand). No code is ever converted. N is 16, twice the 8 heads
+// of a group, which gives each query and each weight two terms:
+//   e4m3   q' = hi + lo / 16, both e4m3. bf16 has 8 significant bits and e4m3 4 (and a sign), so
+//          the sum is exact but for elements below 2^-14 of their head's largest. A weight
+//          p = hi + lo / 16 is within 2^-8 of itself.
+//   bf16   p = hi + lo, both bf16 (the second half of Q's rows is zero).
+// The weights' size is what e4m3 has little room for (2^-9 .. 448): each warp of 32 tokens takes them
+// relative to its own largest, 2^8, and has columns of its own in the product, which are joined in
+// fp32 with the running maximum. A value's scale is part of its weight: with t = z + log2(s_v), the
+// weight is 2^(t - max t) and its share of the softmax sum that over s_v.
+//
+// The tiles (128 tokens) of all (sequence, KV head) pairs form one stream, cut into equal pieces, one
+// per CTA (one per SM). A pair that lies in several pieces leaves a partial in each (O, maximum, sum,
+// fp32); the CTA that delivers a pair's last partial joins them, in the order of the pieces, so
+// that results do not depend on who that is. Counters are indexed by the piece in which a pair
+// begins (one at most goes on from a piece), not by the pair, so that they lie in the same place
+// for every shape and a workspace may serve several.
+//
+// Inside a CTA a tile goes through, each a step behind the other:
+//   warp 8       page numbers (a batch ahead), the pages' K and V boxes by TMA into a ring of shared
+//                memory, their scales beside them (cp.async), a descriptor per tile
+//   warp 9       each segment's queries as the B operand, a segment ahead
+//   warp 10      S^T into one of two buffers of tensor memory
+//   warps 0-3    a token per thread: scores, weights, their sums
+//   warp 11      the value product of the 32 tokens of each of these warps
+//   warps 4-7    a dimension per thread: the running O, and a segment's end
 #include <cuda_fp8.h>
+#include <limits.h>
+#include <math.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "dec_device.cuh"
 #include "dec_launch.h"
+#include "tcgen05.cuh"
 
 namespace decattn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 128;   // tokens per tile
 constexpr int kG = kSplitMaxG;
+constexpr int kN = 2 * kG;   // columns of the products: two terms of each head
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTma = 8, kQuery = 9, kScore = 10, kValue = 11;  // warps
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kOCol = 2 * kN;        // S buffers in columns [0, 32), O's behind them
+constexpr uint32_t kOCols = 4 * kN;       // an O buffer: 16 columns for each warp of tokens
+// What beginning and ending a segment costs, in tiles: the stream is cut by tiles plus this.
+constexpr int kSegment = 2;
+constexpr int kCounters = 4096;           // a counter per piece
+static_assert(kCounters == kPagedMaxParts, "one counter per piece");
 
 template <int D, bool kE4m3>
-__device__ __forceinline__ void load_row(const void *pages, size_t row, int lane,
-                                         float (&x)[D / 32]) {
-  constexpr int E = D / 32;
+struct Geo {
+  static constexpr int kRow = D * (kE4m3 ? 1 : 2);             // bytes of a row
+  static constexpr int kWide = kRow < 128 ? kRow : 128;        // of it in a slab: the swizzle's width
+  static constexpr int kSlabs = kRow / kWide;
+  static constexpr int kSlab = kTile * kWide;
+  static constexpr int kTensor = kSlabs * kSlab;               // a K or a V tile
+  static constexpr int kQ = kN * kRow;
+  static constexpr int kP = kTile * (kE4m3 ? 16 : 32);
+  static constexpr int kSlots = 192 * 1024 / kTensor;          // of the ring, half of them K's
+  static constexpr int kTiles = kSlots / 2;
+  static constexpr int kDescs = kTiles + 4;  // tile descriptors: none is overwritten while in use
+  static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTensor + 2 * kQ + 2 * kP;
+  // high words of the matrix descriptors: 8 rows to the next 8, the version bit, the swizzle mode
+  static constexpr uint32_t kHi =
+      (uint32_t)(8 * kWide >> 4) | (1u << 14) | ((kWide == 128 ? 2u : 4u) << 29);
+  // of the weights' operand, not swizzled: bytes from 8 heads to the next 8 (bf16)
+  static constexpr uint32_t kPHi = (uint32_t)(kTile * 16 >> 4) | (1u << 14);
+  static constexpr uint32_t kType = kE4m3 ? 0u : 1u;
+  static constexpr uint32_t idesc(int m, bool mn_major) {
+    return (1u << 4) | (kType << 7) | (kType << 10) | ((mn_major ? 3u : 0u) << 15) |
+           ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+  }
+};
+
+// Workspace: the header, a counter per piece, then two partials per piece.
+__host__ __device__ inline size_t slot_bytes(int G, int D) {
+  return ((size_t)G * (D * 4 + 8) + 15) & ~(size_t)15;
+}
+constexpr size_t kSlotsOffset = kWsHeaderBytes + kCounters * 4;
+
+struct alignas(16) Tile {
+  int lo, hi;      // rows of tokens that are seen
+  int flags;
+  int b, g;
+  int slot;        // partial of this segment, -1: it is the whole pair
+  int first, last; // the pieces the pair lies in
+};
+constexpr int kFirst = 1, kLast = 2, kEnd = 4;  // of a segment; of the piece (not a tile)
+
+struct PagedMaps {
+  CUtensorMap k, v;
+};
+
+struct Waiter {
+  volatile int *abort;
+  uint32_t *error_word;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (mbar_wait_bounded(bar, parity)) return true;
+    *abort = 1;
+    atomicOr(error_word, kErrWaitTimeout);
+    return false;
+  }
+  // the same answer in every lane, and the warp together behind it
+  __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity) ? 1 : 0) != 0;
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+template <bool kE4m3>
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                     uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kE4m3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+  return __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
+}
+// Eight values of at most 448, each as hi + lo / 16, both e4m3: the second term's own factor keeps it
+// clear of e4m3's smallest steps.
+constexpr float kLow = 1.f / 16;
+__device__ __forceinline__ void two_terms_e4m3(const float (&x)[8], uint2 &hi, uint2 &lo) {
+  uint32_t h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const size_t i = row * D + lane * E + e;
-    if (kE4m3) {
-      __nv_fp8_e4m3 c;
-      c.__x = static_cast<const uint8_t *>(pages)[i];
-      x[e] = (float)c;
-    } else {
-      x[e] = __bfloat162float(static_cast<const __nv_bfloat16 *>(pages)[i]);
+  for (int i = 0; i < 4; ++i) {
+    h[i] = e4m3x2(x[2 * i], x[2 * i + 1]);
+    const float2 f = from_e4m3x2(h[i]);
+    l[i] = e4m3x2((x[2 * i] - f.x) * 16.f, (x[2 * i + 1] - f.y) * 16.f);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+__device__ __forceinline__ void two_terms_bf16(const float (&x)[8], uint4 &hi, uint4 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    l[i] = pack_bf16x2(x[2 * i] - bf16_lo(h[i]), x[2 * i + 1] - bf16_hi(h[i]));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z),
+               "r"(x.w)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// An arrival on `bar` once this thread's copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+struct Seq {
+  int L, start, tile0, tiles;  // tokens start .. L are seen, in tiles tile0 .. tile0 + tiles
+};
+__device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
+  Seq s;
+  s.L = min(max(a.lens[b], 0), a.max_len);
+  s.start = a.window > 0 ? max(0, s.L - a.window) : 0;
+  s.tile0 = s.start / kTile;
+  s.tiles = s.L > s.start ? (s.L + kTile - 1) / kTile - s.tile0 : 0;
+  return s;
+}
+__device__ __forceinline__ int units_of(const Seq &s) { return s.tiles > 0 ? s.tiles + kSegment : 0; }
+
+// The partials of a pair of pieces first .. last into its G rows of the output, by 128 threads.
+template <int D>
+__device__ __forceinline__ void join(const uint8_t *slots, int first, int last, int G,
+                                     __nv_bfloat16 *out) {
+  const size_t slot = slot_bytes(G, D);
+  // 4 neighbouring dims of a head per thread
+  for (int i = threadIdx.x & 127; i < G * (D / 4); i += 128) {
+    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+    float M = -INFINITY, sum = 0.f, o[4] = {};
+#pragma unroll 4
+    for (int c = first; c <= last; ++c) {
+      const uint8_t *p = slots + (size_t)(2 * c + (c == first)) * slot;
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + ((size_t)h * D + d) * 4));
+      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)G * D * 4) + h);
+      const float to = fmaxf(M, ml.x), base = to == -INFINITY ? 0.f : to;
+      const float f = ex2(M - base), g = ex2(ml.x - base);
+      M = to;
+      sum = sum * f + ml.y * g;
+      o[0] = o[0] * f + x.x * g;
+      o[1] = o[1] * f + x.y * g;
+      o[2] = o[2] * f + x.z * g;
+      o[3] = o[3] * f + x.w * g;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(out + (size_t)h * D + d) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   }
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads)
-    paged_attn_kernel(const PagedCache c, const PagedAttnArgs a, int page_log2) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[kWarps][kG][D], s_m[kWarps][kG], s_l[kWarps][kG];
-  pdl_launch_dependents();
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedCache c,
+                      const PagedAttnArgs a, int page_log2, uint8_t *workspace) {
+  using Ge = Geo<D, kE4m3>;
+  constexpr int S = Ge::kSlots, ND = Ge::kDescs;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_bar[2 * S + ND + 33];
+  __shared__ Tile s_tile[ND];
+  __shared__ float s_scale[ND][2][8];          // of a tile's pages, K and V; < 0: no page
+  __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
+  __shared__ __align__(16) float s_top[2][4][kG];       // a tile's maxima, per warp of tokens
+  __shared__ __align__(16) float s_sum[4][4][2][kG];    // a segment's sums and their maxima
+  __shared__ __align__(16) float s_f[4][5 * kG];        // factors, per warp of dimensions
+  __shared__ int2 s_seg[4];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_warp_units[kWarps], s_begin[5], s_joins;
+
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t ring = smem_addr(smem), q_s = ring + S * Ge::kTensor, p_s = q_s + 2 * Ge::kQ;
+  const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
+  const uint32_t bar_desc = bar_empty + 8 * S, bar_s = bar_desc + 8 * ND, bar_p = bar_s + 16;
+  const uint32_t bar_o = bar_p + 16, bar_free = bar_o + 16, bar_q = bar_free + 16;
+  const uint32_t bar_qfree = bar_q + 32, bar_end = bar_qfree + 16, bar_sum = bar_end + 16;
+  const uint32_t bar_seg = bar_sum + 32, bar_segfree = bar_seg + 32, bar_meet = bar_segfree + 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int G = a.Hq / c.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * S; ++i) mbar_init(bar_full + 8 * i, 1);
+    for (int i = 0; i < ND; ++i) mbar_init(bar_desc + 8 * i, kE4m3 ? 33 : 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + 8 * i, 1);
+      mbar_init(bar_p + 8 * i, 128);
+      mbar_init(bar_o + 8 * i, 1);
+      mbar_init(bar_free + 8 * i, 128);
+      mbar_init(bar_qfree + 8 * i, 1);
+      mbar_init(bar_end + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar_q + 8 * i, 1);
+      mbar_init(bar_sum + 8 * i, 4);
+      mbar_init(bar_seg + 8 * i, 1);
+      mbar_init(bar_segfree + 8 * i, 1);
+    }
+    mbar_init(bar_meet, 128);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kTma) {
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.v);
+    }
+    tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+  }
+  // rows of Q that no head fills stay zero
+  for (int i = tid; i < 2 * Ge::kQ / 16; i += kThreads)
+    st_shared16(q_s + 16 * i, make_uint4(0u, 0u, 0u, 0u));
   pdl_wait_prior_grid();
-  const int b = blockIdx.y, g = blockIdx.x, G = a.Hq / c.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = a.lens[b];
-  const int L = min(max(len, 0), a.max_len);
-  if (L != len && g == 0 && threadIdx.x == 0) atomicOr(a.error_word, kErrLenClamped);
-  const int first = a.window > 0 ? max(0, L - a.window) : 0;
-  float q[kG][E], o[kG][E] = {}, m[kG], l[kG] = {};
-#pragma unroll
-  for (int h = 0; h < kG; ++h) {
-    m[h] = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      q[h][e] = h < G ? __bfloat162float(a.q[((size_t)b * a.Hq + g * G + h) * D + lane * E + e]) *
-                            a.scale_log2
-                      : 0.f;
+  pdl_launch_dependents();
+
+  // ---- where this CTA's piece begins: a scan over the sequences, a run of them per thread
+  const int P = gridDim.x, piece = blockIdx.x;
+  const int per = (a.B + kThreads - 1) / kThreads, b_first = tid * per;
+  const int b_last = min(a.B, b_first + per);
+  int mine = 0;
+  for (int b = b_first; b < b_last; ++b) {
+    const Seq s = seq_of(a, b);
+    mine += units_of(s) * c.Hkv;
+    if (piece == 0 && s.L != a.lens[b]) atomicOr(a.error_word, kErrLenClamped);
   }
-  for (int t = first + warp; t < L; t += kWarps) {
-    const int page = c.table[(size_t)b * c.max_pages + (t >> page_log2)];
-    if (page < 0 || page >= c.num_pages) {
-      if (g == 0 && lane == 0) atomicOr(a.error_word, kErrPageSkipped);
-      continue;
-    }
-    const size_t head = (size_t)page * c.Hkv + g;
-    const size_t row = (head << page_log2) + (t & ((1 << page_log2) - 1));
-    const float ks = kE4m3 ? c.k_scale[head] : 1.f, vs = kE4m3 ? c.v_scale[head] : 1.f;
-    float k[E], v[E];
-    load_row<D, kE4m3>(c.k_pages, row, lane, k);
-    load_row<D, kE4m3>(c.v_pages, row, lane, v);
-#pragma unroll
-    for (int h = 0; h < kG; ++h) {
-      if (h >= G) break;
-      float z = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) z = fmaf(q[h][e], k[e], z);
-      z = warp_sum(z) * ks;
-      const float to = fmaxf(m[h], z), base = to == -INFINITY ? 0.f : to;
-      const float alpha = exp2f(m[h] - base), p = exp2f(z - base);
-      m[h] = to;
-      l[h] = l[h] * alpha + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[h][e] = o[h][e] * alpha + p * vs * v[e];
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < kG; ++h) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][h][lane * E + e] = o[h][e];
-    if (lane == 0) s_m[warp][h] = m[h], s_l[warp][h] = l[h];
-  }
+  const int in_warp = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) s_warp_units[warp] = in_warp;
+  if (tid == 0) s_begin[0] = -1;
   __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += kThreads) {
-    const int h = i / D, d = i - h * D;
-    float M = -INFINITY, sum = 0.f, x = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
-    const float base = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(s_m[w][h] - base);
-      sum += f * s_l[w][h];
-      x += f * s_o[w][h][d];
-    }
-    a.out[((size_t)b * a.Hq + g * G + h) * D + d] = __float2bfloat16(sum == 0.f ? 0.f : x / sum);
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int u = s_warp_units[w];
+    if (w < warp) before += u;
+    total += u;
   }
+  const int blk = max(1, (int)(((long long)total + P - 1) / P));
+  const long long r0 = (long long)piece * blk;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int at = before + incl - mine;
+  if (r0 < total && at <= r0 && r0 < at + mine) {
+    int b = b_first;
+    for (;; ++b) {
+      const int u = units_of(seq_of(a, b)) * c.Hkv;
+      if (r0 < at + u) break;
+      at += u;
+    }
+    s_begin[0] = b;
+    s_begin[1] = (int)r0 - at;
+  }
+  // sequences without tokens are nobody's tiles: their zeros
+  for (int b = piece; b < a.B; b += P)
+    if (seq_of(a, b).tiles == 0)
+      for (int i = tid; i < a.Hq * D / 8; i += kThreads)
+        reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();  // (Q's zeros)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  const Waiter wait{&s_abort, a.error_word};
+
+  if (warp == kTma) {
+    // ---------------------------------------------------------------- loads
+    const int page = 1 << page_log2, ppt = kTile >> page_log2, ppt_log2 = 7 - page_log2;
+    const int batch = 32 >> ppt_log2;  // tiles whose page numbers the lanes hold
+    const uint64_t policy = l2_policy_evict_first();
+    // the walk: (b, g), its tiles t0 .. t1 of this piece (from the sequence's first seen one), and
+    // those of them that the lanes have looked up
+    int b = s_begin[0], g = 0, left = 0, t0 = 0, t1 = 0, off = 0;
+    Seq s{};
+    auto take = [&](int from) {  // from: units of this pair that lie before the piece
+      t0 = max(0, from - kSegment);
+      t1 = max(t0, min(s.tiles, from + left - kSegment));
+      left -= min(left, t1 + kSegment - from);
+    };
+    bool more = b >= 0;
+    if (more) {
+      s = seq_of(a, b);
+      const int u = units_of(s);
+      g = s_begin[1] / u;
+      const int from = s_begin[1] - g * u;
+      off = (int)r0 - from;
+      left = (int)min((long long)blk, total - r0);
+      take(from);
+    }
+    // the next pair; false: none in this piece
+    auto next_pair = [&]() {
+      if (left <= 0) return false;
+      off += units_of(s);
+      if (++g == c.Hkv) {
+        g = 0;
+        do {
+          if (++b >= a.B) return false;
+          s = seq_of(a, b);
+        } while (s.tiles == 0);
+      }
+      take(0);
+      return true;
+    };
+    struct Batch {
+      Seq s;
+      int b, g, from, to, t0, t1, off, page;
+    };
+    int at_tile = t0;
+    auto next_batch = [&](Batch &x) {
+      while (more && at_tile >= t1) {
+        more = next_pair();
+        at_tile = t0;
+      }
+      if (!more) return false;
+      x.s = s, x.b = b, x.g = g, x.t0 = t0, x.t1 = t1, x.off = off;
+      x.from = at_tile;
+      x.to = min(t1, at_tile + batch);
+      at_tile = x.to;
+      // this lane's page: tile from + lane / ppt, page lane % ppt of it; only where a token is seen
+      const int slot = ((s.tile0 + x.from) << ppt_log2) + lane;
+      x.page = -1;
+      if ((slot << page_log2) < s.L && ((slot + 1) << page_log2) > s.start &&
+          lane < (x.to - x.from) << ppt_log2)
+        x.page = c.table[(size_t)b * c.max_pages + slot];
+      return true;
+    };
+    int n = 0, seg = 0;
+    bool ok = true;
+    auto push_segment = [&](int b_, int g_) {
+      if (seg >= 4 && !wait.all(bar_segfree + 8 * (seg & 3), ((seg >> 2) - 1) & 1)) return false;
+      if (lane == 0) {
+        s_seg[seg & 3] = make_int2(b_, g_);
+        mbar_arrive(bar_seg + 8 * (seg & 3));
+      }
+      ++seg;
+      return true;
+    };
+    Batch cur, nxt;
+    bool have = next_batch(cur);
+    while (have && ok) {
+      const bool have_next = next_batch(nxt);
+      for (int i = cur.from; i < cur.to && ok; ++i, ++n) {
+        const int row0 = (cur.s.tile0 + i) * kTile;
+        const int lo = max(0, cur.s.start - row0), hi = min(kTile, cur.s.L - row0);
+        const int d = n % ND, ks = (2 * n) % S, vs = (2 * n + 1) % S;
+        // pages p0 .. p1 of the tile hold tokens that are seen; a lane each
+        const int p0 = lo >> page_log2, p1 = (hi + page - 1) >> page_log2;
+        const int number = __shfl_sync(0xffffffffu, cur.page, ((i - cur.from) << ppt_log2) + (lane & (ppt - 1)));
+        const bool here = lane >= p0 && lane < p1;
+        const bool good = number >= 0 && number < c.num_pages;
+        const int head = good ? number * c.Hkv + cur.g : -1;  // (-1: the copy leaves zeros)
+        const int bytes = (p1 - p0) * page * Ge::kRow;
+        if (2 * n >= S && !(ok = wait.all(bar_empty + 8 * ks, ((2 * n / S) - 1) & 1))) break;
+        if (i == cur.t0 && !(ok = push_segment(cur.b, cur.g))) break;
+        if (here) {
+          if (!good) {
+            s_scale[d][0][lane] = s_scale[d][1][lane] = -1.f;
+            if (cur.g == 0) atomicOr(a.error_word, kErrPageSkipped);
+          } else if (kE4m3) {
+            cp_async4(smem_addr(&s_scale[d][0][lane]), c.k_scale + head);
+            cp_async4(smem_addr(&s_scale[d][1][lane]), c.v_scale + head);
+          } else {
+            s_scale[d][0][lane] = s_scale[d][1][lane] = 1.f;
+          }
+        }
+        if (lane == 0) {
+          Tile t;
+          t.lo = lo;
+          t.hi = hi;
+          t.flags = (i == cur.t0 ? kFirst : 0) | (i == cur.t1 - 1 ? kLast : 0);
+          t.b = cur.b;
+          t.g = cur.g;
+          t.slot = cur.t0 == 0 && cur.t1 == cur.s.tiles ? -1 : 2 * piece + (cur.t0 == 0);
+          t.first = (cur.off + kSegment) / blk;
+          t.last = (cur.off + kSegment + cur.s.tiles - 1) / blk;
+          s_tile[d] = t;
+          mbar_arrive_expect_tx(bar_full + 8 * ks, bytes);
+        }
+        __syncwarp();
+        if (here)
+#pragma unroll
+          for (int sl = 0; sl < Ge::kSlabs; ++sl)
+            tma_load_3d(ring + ks * Ge::kTensor + sl * Ge::kSlab + (lane << page_log2) * Ge::kWide,
+                        &maps.k, sl * (Ge::kWide / (kE4m3 ? 1 : 2)), 0, head, bar_full + 8 * ks,
+                        policy);
+        if (kE4m3) cp_async_arrive(bar_desc + 8 * d);
+        if (lane == 0) mbar_arrive(bar_desc + 8 * d);
+        if (2 * n + 1 >= S && !(ok = wait.all(bar_empty + 8 * vs, (((2 * n + 1) / S) - 1) & 1))) {
+          ++n;  // (its keys are on their way)
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * vs, bytes);
+        __syncwarp();
+        if (here)
+#pragma unroll
+          for (int sl = 0; sl < Ge::kSlabs; ++sl)
+            tma_load_3d(ring + vs * Ge::kTensor + sl * Ge::kSlab + (lane << page_log2) * Ge::kWide,
+                        &maps.v, sl * (Ge::kWide / (kE4m3 ? 1 : 2)), 0, head, bar_full + 8 * vs,
+                        policy);
+      }
+      cur = nxt;
+      have = have_next;
+    }
+    // the end of the piece, where the next tile would be
+    const int d = n % ND;
+    if (ok && (2 * n < S || wait.all(bar_empty + 8 * ((2 * n) % S), ((2 * n / S) - 1) & 1)) &&
+        push_segment(-1, 0)) {
+      if (lane == 0) s_tile[d].flags = kEnd;
+      __syncwarp();
+      if (kE4m3) cp_async_arrive(bar_desc + 8 * d);
+      if (lane == 0) mbar_arrive(bar_desc + 8 * d);
+    }
+    // no copy into this CTA's shared memory may outlive it (all have landed unless a wait gave up)
+    for (int j = max(0, n - S / 2); j < n; ++j) {
+      mbar_wait_bounded(bar_full + 8 * ((2 * j) % S), (2 * j / S) & 1);
+      mbar_wait_bounded(bar_full + 8 * ((2 * j + 1) % S), ((2 * j + 1) / S) & 1);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kQuery) {
+    // ---------------------------------------------------------------- queries
+    // 8 elements a lane: a head is D / 8 lanes.
+    constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+    for (int seg = 0;; ++seg) {
+      const int r = seg & 3;
+      if (!wait.all(bar_seg + 8 * r, (seg >> 2) & 1)) break;
+      const int2 at_pair = s_seg[r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_segfree + 8 * r);
+      if (at_pair.x < 0) break;
+      const __nv_bfloat16 *q = a.q + ((size_t)at_pair.x * a.Hq + (size_t)at_pair.y * G) * D;
+      constexpr int kLoads = kG / kHeads;
+      uint4 w[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (i * kHeads + lane / kLanes < G)
+          w[i] = *reinterpret_cast<const uint4 *>(q + (i * 32 + lane) * 8);
+      }
+      if (seg >= 2 && !wait.all(bar_qfree + 8 * (seg & 1), ((seg >> 1) - 1) & 1)) break;
+      const uint32_t base = q_s + (seg & 1) * Ge::kQ;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int h = i * kHeads + lane / kLanes, ch = lane % kLanes;
+        float x[8] = {bf16_lo(w[i].x), bf16_hi(w[i].x), bf16_lo(w[i].y), bf16_hi(w[i].y),
+                      bf16_lo(w[i].z), bf16_hi(w[i].z), bf16_lo(w[i].w), bf16_hi(w[i].w)};
+        if (kE4m3) {
+          float m = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // 2^e with the largest of 2^8 at most times it; an infinity makes every score a NaN
+          const int e = min(max((int)(__float_as_uint(m) >> 23) - 127 - 7, -100), 100);
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= inv;
+          uint2 hi, lo;
+          two_terms_e4m3(x, hi, lo);
+          if (h < G) {
+            if (ch == 0)
+              s_qs[r][h] = m < INFINITY ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
+                                        : __uint_as_float(0x7fc00000u);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int row = h + t * kG, c16 = ch >> 1;
+              const int sw = Ge::kWide == 128 ? row & 7 : (row >> 1) & 3;
+              const uint2 v = t ? lo : hi;
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
+                               base + row * Ge::kWide + ((c16 ^ sw) << 4) + ((ch & 1) << 3)),
+                           "r"(v.x), "r"(v.y)
+                           : "memory");
+            }
+          }
+        } else if (h < G) {
+          if (ch == 0) s_qs[r][h] = a.scale_log2;
+          st_shared16(base + (ch >> 3) * (kN * 128) + h * 128 + (((ch & 7) ^ (h & 7)) << 4), w[i]);
+        }
+      }
+      if (lane < kG && lane >= G) s_qs[r][lane] = 0.f;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q + 8 * r);
+    }
+  } else if (warp == kScore) {
+    // ---------------------------------------------------------------- S^T = K Q^T
+    // (the warp stays together and an elected lane issues: the operands are then the same across
+    // the warp as far as the compiler can tell)
+    constexpr uint32_t idesc = Ge::idesc(kTile, false);
+    int seg = -1;
+    for (int n = 0;; ++n) {
+      const int d = n % ND, slot = (2 * n) % S;
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      const int flags = s_tile[d].flags;
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        ++seg;
+        if (!wait.all(bar_q + 8 * (seg & 3), (seg >> 2) & 1)) break;
+      }
+      // the buffer's last tile has been read
+      if (n >= 2 && !wait.all(bar_p + 8 * (n & 1), ((n - 2) >> 1) & 1)) break;
+      if (!wait.all(bar_full + 8 * slot, (2 * n / S) & 1)) break;
+      tc_fence_after();
+      const uint32_t k_lo = desc_lo(ring + slot * Ge::kTensor, 16);
+      const uint32_t q_lo = desc_lo(q_s + (seg & 1) * Ge::kQ, 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < Ge::kRow / 32; ++k) {
+          constexpr int kPer = Ge::kWide / 32;
+          umma<kE4m3>(tmem + (n & 1) * kN, k_lo + (k / kPer) * (Ge::kSlab >> 4) + 2 * (k % kPer),
+                      Ge::kHi, q_lo + (k / kPer) * (kN * Ge::kWide >> 4) + 2 * (k % kPer), Ge::kHi,
+                      idesc, k > 0);
+        }
+        umma_commit(bar_empty + 8 * slot);
+        umma_commit(bar_s + 8 * (n & 1));
+        if (flags & kLast) umma_commit(bar_qfree + 8 * (seg & 1));
+      }
+      __syncwarp();
+    }
+    // what was issued finishes before tensor memory is given back
+    if (elect_one()) umma_commit(bar_end);
+    __syncwarp();
+    mbar_wait_bounded(bar_end, 0);
+  } else if (warp == kValue) {
+    // ---------------------------------------------------------------- O^T = V^T P^T, 32 tokens each
+    constexpr uint32_t idesc = Ge::idesc(D, true);
+    constexpr int kStep = kE4m3 ? 32 : 16;  // tokens of an instruction
+    for (int n = 0;; ++n) {
+      const int d = n % ND, slot = (2 * n + 1) % S;
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      if (s_tile[d].flags & kEnd) break;
+      if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
+      if (n >= 2 && !wait.all(bar_free + 8 * (n & 1), ((n - 2) >> 1) & 1)) break;
+      if (!wait.all(bar_p + 8 * (n & 1), (n >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t v_lo = desc_lo(ring + slot * Ge::kTensor, Ge::kSlab);
+      const uint32_t p_lo = desc_lo(p_s + (n & 1) * Ge::kP, 128);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / kStep; ++k)
+          umma<kE4m3>(tmem + kOCol + (n & 1) * kOCols + (k * kStep / 32) * kN,
+                      v_lo + k * (kStep * Ge::kWide >> 4), Ge::kHi, p_lo + k * kStep, Ge::kPHi, idesc,
+                      (k * kStep) % 32 != 0);
+        umma_commit(bar_empty + 8 * slot);
+        umma_commit(bar_o + 8 * (n & 1));
+      }
+      __syncwarp();
+    }
+    if (elect_one()) umma_commit(bar_end + 8);
+    __syncwarp();
+    mbar_wait_bounded(bar_end + 8, 0);
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- weights
+    const uint32_t my_s = tmem + ((uint32_t)(32 * warp) << 16);
+    float qs[kG], top[kG], sum[kG];
+    int seg = -1;
+    for (int n = 0;; ++n) {
+      const int d = n % ND, buf = n & 1;
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      const Tile t = s_tile[d];
+      if (t.flags & kEnd) break;
+      const float ks = s_scale[d][0][tid >> page_log2], vs = s_scale[d][1][tid >> page_log2];
+      const bool inside = tid >= t.lo && tid < t.hi, seen = inside && ks > 0.f;
+      if (t.flags & kFirst) {
+        ++seg;
+        if (!wait.all(bar_q + 8 * (seg & 3), (seg >> 2) & 1)) break;
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+          qs[h] = s_qs[seg & 3][h];
+          top[h] = -INFINITY;
+          sum[h] = 0.f;
+        }
+      }
+      const float lvs = kE4m3 ? lg2(vs) : 0.f, ivs = kE4m3 ? 1.f / vs : 1.f;
+      if (!wait.all(bar_s + 8 * buf, (n >> 1) & 1)) break;
+      tc_fence_after();
+      float z[kN];
+      tmem_ld16(my_s + buf * kN, z);
+      float w[kG], most[kG];
+#pragma unroll
+      for (int h = 0; h < kG; ++h) {
+        w[h] = kE4m3 ? fmaf(z[kG + h], kLow, z[h]) * (qs[h] * ks) + lvs : z[h] * qs[h];
+        if (!seen) w[h] = -INFINITY;
+        most[h] = warp_max(w[h]);
+        // weights relative to 2^-8 of the warp's largest
+        w[h] = ex2(w[h] - ((most[h] == -INFINITY ? 0.f : most[h]) - 8.f));
+        const float to = fmaxf(top[h], most[h]), base = to == -INFINITY ? 0.f : to;
+        sum[h] = sum[h] * ex2(top[h] - base) + (w[h] * (seen ? ivs : 0.f)) * ex2(most[h] - base);
+        top[h] = to;
+      }
+      // the buffers of weights and maxima of tile n - 2 are consumed
+      if (n >= 2 && !wait.all(bar_o + 8 * buf, ((n - 2) >> 1) & 1)) break;
+      if (n >= 2 && !wait.all(bar_free + 8 * buf, ((n - 2) >> 1) & 1)) break;
+      if (lane == 0) {
+#pragma unroll
+        for (int h = 0; h < kG; h += 4)
+          *reinterpret_cast<float4 *>(&s_top[buf][warp][h]) =
+              make_float4(most[h], most[h + 1], most[h + 2], most[h + 3]);
+      }
+      const uint32_t my_p = p_s + buf * Ge::kP + tid * 16;
+      if (kE4m3) {
+        uint2 hi, lo;
+        two_terms_e4m3(w, hi, lo);
+        st_shared16(my_p, make_uint4(hi.x, hi.y, lo.x, lo.y));
+      } else {
+        uint4 hi, lo;
+        two_terms_bf16(w, hi, lo);
+        st_shared16(my_p, hi);
+        st_shared16(my_p + kTile * 16, lo);
+      }
+      // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
+      // page that does not exist was left zeros.)
+      if (t.lo > 0 || t.hi < kTile) {
+        const int slot = (2 * n + 1) % S;
+        if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
+        if (!inside)
+#pragma unroll
+          for (int i = 0; i < Ge::kRow / 16; ++i)
+            st_shared16(ring + slot * Ge::kTensor + (i * 16 / Ge::kWide) * Ge::kSlab +
+                            tid * Ge::kWide + (i * 16) % Ge::kWide,
+                        make_uint4(0u, 0u, 0u, 0u));
+      }
+      if (t.flags & kLast) {
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+          const float x = warp_sum(sum[h]);
+          if (lane == 0) {
+            s_sum[seg & 3][warp][0][h] = x;
+            s_sum[seg & 3][warp][1][h] = top[h];
+          }
+        }
+        if (lane == 0) mbar_arrive(bar_sum + 8 * (seg & 3));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar_p + 8 * buf);
+    }
+  } else {
+    // ---------------------------------------------------------------- the running O
+    // D = 64: an M of 64 puts row 16 w + i into lane i < 16 of warp w's quarter.
+    const int w4 = warp - 4, dim = D == 128 ? 32 * w4 + lane : 16 * w4 + lane;
+    const bool mine_too = D == 128 || lane < 16;
+    const uint32_t my_o = tmem + ((uint32_t)(32 * w4) << 16) + kOCol;
+    uint8_t *slots = workspace + kSlotsOffset;
+    int *counters = reinterpret_cast<int *>(workspace + kWsHeaderBytes);
+    const size_t slot_size = slot_bytes(G, D);
+    float acc[kG];
+    float top = -INFINITY;  // the running maximum of head lane & 7
+    int seg = -1, met = 0;
+    // the four warps together (a bounded wait: one of them may have given up)
+    auto meet = [&]() {
+      mbar_arrive(bar_meet);
+      return wait.all(bar_meet, met++ & 1);
+    };
+    for (int n = 0;; ++n) {
+      const int d = n % ND, buf = n & 1;
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      const Tile t = s_tile[d];
+      if (t.flags & kEnd) break;
+      if (t.flags & kFirst) {
+        ++seg;
+        top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kG; ++h) acc[h] = 0.f;
+      }
+      if (!wait.all(bar_p + 8 * buf, (n >> 1) & 1)) break;  // (the maxima)
+      {
+        const float x = s_top[buf][lane >> 3][lane & 7];
+        float m = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const float to = fmaxf(top, m), base = to == -INFINITY ? 0.f : to;
+        s_f[w4][lane] = ex2(x - base - 8.f);  // (0 where a warp saw nothing)
+        if (lane < kG) s_f[w4][32 + lane] = ex2(top - base);
+        top = to;
+      }
+      __syncwarp();
+      if (!wait.all(bar_o + 8 * buf, (n >> 1) & 1)) break;
+      tc_fence_after();
+      const float4 *f4 = reinterpret_cast<const float4 *>(s_f[w4]);
+      const float4 a0 = f4[8], a1 = f4[9];
+      const float al[kG] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+      for (int h = 0; h < kG; ++h) acc[h] *= al[h];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float o[kN];
+        tmem_ld16(my_o + buf * kOCols + w * kN, o);
+        const float4 f0 = f4[2 * w], f1 = f4[2 * w + 1];
+        const float f[kG] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+        for (int h = 0; h < kG; ++h) acc[h] = fmaf(fmaf(o[kG + h], kE4m3 ? kLow : 1.f, o[h]), f[h], acc[h]);
+      }
+      __syncwarp();
+      if (!(t.flags & kLast)) {
+        tc_fence_before();
+        mbar_arrive(bar_free + 8 * buf);
+        continue;
+      }
+      // a segment's end: the four warps' sums under one maximum
+      if (!wait.all(bar_sum + 8 * (seg & 3), (seg >> 2) & 1)) break;
+      float l = 0.f;
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        l += s_sum[seg & 3][w][0][lane & 7] * ex2(s_sum[seg & 3][w][1][lane & 7] - base - 8.f);
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive(bar_free + 8 * buf);  // (after the last read of what the tile and segment left)
+      if (t.slot < 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16 *out = a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D + dim;
+#pragma unroll
+        for (int h = 0; h < kG; ++h) {
+          const float x = __shfl_sync(0xffffffffu, inv, h);
+          if (h < G && mine_too) out[h * D] = __float2bfloat16(acc[h] * x);
+        }
+        continue;
+      }
+      uint8_t *part = slots + (size_t)t.slot * slot_size;
+#pragma unroll
+      for (int h = 0; h < kG; ++h)
+        if (h < G && mine_too) reinterpret_cast<float *>(part)[h * D + dim] = acc[h];
+      if (w4 == 0 && lane < G)
+        reinterpret_cast<float2 *>(part + (size_t)G * D * 4)[lane] = make_float2(top, l);
+      __threadfence();
+      if (!meet()) break;
+      if (tid == 128) {
+        const bool all = atomicAdd(counters + t.first, 1) == t.last - t.first;
+        if (all) counters[t.first] = 0;  // as the next call wants it
+        __threadfence();
+        s_joins = all;
+      }
+      if (!meet()) break;
+      if (s_joins)
+        join<D>(slots, t.first, t.last, G, a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D);
+      if (!meet()) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kE4m3>
+cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs &a, int parts,
+                   uint8_t *ws, cudaStream_t stream) {
+  // per device: the kernel's shared memory (set before its first launch there)
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, kE4m3>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Geo<D, kE4m3>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  int log2 = 4;
+  while ((1 << log2) < c.page) ++log2;
+  return launch_pdl(paged_attn_kernel<D, kE4m3>, dim3(parts), kThreads, Geo<D, kE4m3>::kSmem,
+                    stream, m, c, a, log2, ws);
 }
 
 }  // namespace
 
-int paged_attn_parts(int, int, int, int, int) { return 1; }
-size_t paged_attn_ws_bytes(int, int, int, int, int) { return 256; }
+// One CTA per SM, or fewer when there are not as many tiles.
+int paged_attn_parts(int B, int Hkv, int max_len, int num_parts, int sms) {
+  if (num_parts > 0) return num_parts;
+  const long long tiles = (long long)B * Hkv * ((max_len + kTile - 1) / kTile + 1);
+  return (int)(tiles < 1 ? 1 : tiles < sms ? tiles : sms < kPagedMaxParts ? sms : kPagedMaxParts);
+}
 
-cudaError_t launch_paged_attn(const PagedCache &c, const PagedAttnArgs &a, int, void *,
+size_t paged_attn_ws_bytes(int, int Hq, int Hkv, int D, int parts) {
+  return kSlotsOffset + (size_t)2 * parts * slot_bytes(Hq / Hkv, D);
+}
+
+cudaError_t launch_paged_attn(const CUtensorMap &k, const CUtensorMap &v, const PagedCache &c,
+                              const PagedAttnArgs &a, int parts, void *workspace,
                               cudaStream_t stream) {
-  int log2 = 4;
-  while ((1 << log2) < c.page) ++log2;
-  auto *kernel = c.D == 128 ? (c.e4m3 ? paged_attn_kernel<128, true> : paged_attn_kernel<128, false>)
-                            : (c.e4m3 ? paged_attn_kernel<64, true> : paged_attn_kernel<64, false>);
-  const cudaError_t e = launch_pdl(kernel, dim3(c.Hkv, a.B), kThreads, 0, stream, c, a, log2);
+  const PagedMaps m{k, v};
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const cudaError_t e = c.D == 128 ? (c.e4m3 ? launch<128, true>(m, c, a, parts, ws, stream)
+                                             : launch<128, false>(m, c, a, parts, ws, stream))
+                                   : (c.e4m3 ? launch<64, true>(m, c, a, parts, ws, stream)
+                                             : launch<64, false>(m, c, a, parts, ws, stream));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

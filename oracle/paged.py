@@ -117,15 +117,17 @@ def tokens(cache, table, b, lo, hi):
 
 
 def attention(q, cache, table, lens, scale=None, window=0):
-    """(out, size): single-query attention, and sum_t p_t |v_t| beside it."""
+    """(out, size, floor): single-query attention, sum_t p_t |v_t|, and with codes c_t under scales s_t
+    max_t p_t s_t sum_t |c_t| (0 without scales)."""
     B, Hq, D = q.shape
     Hkv = cache["k"].shape[1]
     G = Hq // Hkv
     scale = scale if scale else 1.0 / math.sqrt(D)
-    out, size = np.zeros(q.shape), np.zeros(q.shape)
+    out, size, floor = (np.zeros(q.shape) for _ in range(3))
     for b in range(B):
         n = int(lens[b])
-        K, V, has = tokens(cache, table, b, max(0, n - window) if window else 0, n)
+        lo = max(0, n - window) if window else 0
+        K, V, has = tokens(cache, table, b, lo, n)
         if not has.any():
             continue
         for g in range(Hkv):
@@ -133,4 +135,8 @@ def attention(q, cache, table, lens, scale=None, window=0):
             w = O.softmax(scale * (q[b, heads] @ K[g, has].T))
             out[b, heads] = w @ V[g, has]
             size[b, heads] = w @ np.abs(V[g, has])
-    return out, size
+            if cache["vs"] is not None:
+                page = cache["k"].shape[2]
+                s = np.array([cache["vs"][int(table[b, t // page]), g] for t in np.arange(lo, n)[has]])
+                floor[b, heads] = (w * s).max(1)[:, None] * np.abs(V[g, has] / s[:, None]).sum(0)
+    return out, size, floor

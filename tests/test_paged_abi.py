@@ -237,10 +237,10 @@ def test_oracle_paged_attention_is_contiguous_attention():
     K = np.stack([cache["k"][np.clip(t, 0, 6)].transpose(1, 0, 2, 3).reshape(Hkv, -1, D) for t in table])
     V = np.stack([cache["v"][np.clip(t, 0, 6)].transpose(1, 0, 2, 3).reshape(Hkv, -1, D) for t in table])
     for window in (0, 2, 17):
-        out, _ = OP.attention(q, cache, table, lens, window=window)
+        out = OP.attention(q, cache, table, lens, window=window)[0]
         assert np.allclose(out, brute.gqa_decode_attention(q, K, V, lens, window=window or None))
     cache["ks"], cache["vs"] = np.full((P, Hkv), 2.0), np.full((P, Hkv), 3.0)
-    twice, _ = OP.attention(q / 2, cache, table, lens)
+    twice = OP.attention(q / 2, cache, table, lens)[0]
     assert np.allclose(twice, 3 * OP.attention(q, dict(cache, ks=None, vs=None), table, lens)[0])
 
 
