@@ -1518,7 +1518,7 @@ dec_status check_paged_attn(const PagedCache &c, dec_dtype type, const void *q,
   if (workspace == nullptr || misaligned({workspace}, 256))
     return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
   const size_t need = paged_attn_ws_bytes(
-      B, Hq, c.Hkv, c.D, paged_attn_parts(B, c.Hkv, max_len, num_parts, sm_count_of_current()));
+      B, Hq, c.Hkv, c.D, paged_attn_parts(B, c.Hkv, c.D, c.e4m3, max_len, num_parts, sm_count_of_current()));
   if (ws_bytes < need)
     return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   const size_t rows = (size_t)B * Hq * c.D * 2;
@@ -1572,7 +1572,7 @@ dec_status paged_attn_go(const PagedCache &c, const void *q, const int32_t *lens
   a.window = window;
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)c.D);
   a.scale_log2 = (float)((double)sc * 1.4426950408889634);
-  const int parts = paged_attn_parts(B, c.Hkv, max_len, num_parts, sm_count_of_current());
+  const int parts = paged_attn_parts(B, c.Hkv, c.D, c.e4m3, max_len, num_parts, sm_count_of_current());
   CUtensorMap k, v;
   dec_status st = encode_pages_map(&k, c.k_pages, c);
   if (st == DEC_OK) st = encode_pages_map(&v, c.v_pages, c);
@@ -1613,8 +1613,10 @@ size_t dec_paged_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len
       Hq / Hkv > kSplitMaxG || (D != 64 && D != 128) || max_len < 0 || num_parts < 0 ||
       num_parts > kPagedMaxParts || (long long)B * Hkv * (max_len / 128 + 8) >= (1ll << 31))
     return 0;
-  return paged_attn_ws_bytes(
-      B, Hq, Hkv, D, paged_attn_parts(B, Hkv, max_len, num_parts, sm_count_of_current()));
+  const int sms = sm_count_of_current();  // (for pages of either type)
+  return paged_attn_ws_bytes(B, Hq, Hkv, D,
+                             std::max(paged_attn_parts(B, Hkv, D, 0, max_len, num_parts, sms),
+                                      paged_attn_parts(B, Hkv, D, 1, max_len, num_parts, sms)));
 }
 
 dec_status dec_gqa_paged_attn(const void *q, const void *k_pages, const void *v_pages,
@@ -1703,7 +1705,8 @@ dec_status dec_paged_decode_step(
   const size_t row = (size_t)B * hidden * 2, qb = (size_t)B * Hq * D * 2;
   const size_t kb = (size_t)B * Hkv * D * 2;
   const size_t need = paged_attn_ws_bytes(
-      B, Hq, Hkv, D, paged_attn_parts(B, Hkv, max_len, num_parts, sm_count_of_current()));
+      B, Hq, Hkv, D,
+      paged_attn_parts(B, Hkv, D, c.e4m3, max_len, num_parts, sm_count_of_current()));
   st = check_apart({{y, row, "y"}, {residual, row, "residual"}},
                    {{x, row, "x"}, {norm_w, (size_t)hidden * 2, "norm_w"}, {q, qb, "q"},
                     {k_new, kb, "k_new"}, {v_new, kb, "v_new"},

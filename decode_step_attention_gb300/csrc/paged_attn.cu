@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kTile = 128;   // tokens per tile
 constexpr int kG = kSplitMaxG;
-constexpr int kN = 2 * kG;   // columns of the products: two terms of each head
+constexpr int kN = 16;       // columns of the products: two terms of each of up to 8 heads
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTma = 8, kQuery = 9, kScore = 10, kValue = 11;  // warps
@@ -60,6 +60,7 @@ constexpr int kSegment = 2;
 constexpr int kCounters = 4096;           // a counter per piece
 static_assert(kCounters == kPagedMaxParts, "one counter per piece");
 
+// NH: heads of a group that the kernel computes, 4 or 8 (more than there are cost as much as others).
 template <int D, bool kE4m3>
 struct Geo {
   static constexpr int kRow = D * (kE4m3 ? 1 : 2);             // bytes of a row
@@ -69,7 +70,8 @@ struct Geo {
   static constexpr int kTensor = kSlabs * kSlab;               // a K or a V tile
   static constexpr int kQ = kN * kRow;
   static constexpr int kP = kTile * (kE4m3 ? 16 : 32);
-  static constexpr int kSlots = 192 * 1024 / kTensor;          // of the ring, half of them K's
+  static constexpr int kCtas = kTensor > 16384 ? 1 : 2;        // per SM
+  static constexpr int kSlots = (192 / kCtas) * 1024 / kTensor;  // of the ring, half of them K's
   static constexpr int kTiles = kSlots / 2;
   static constexpr int kDescs = kTiles + 4;  // tile descriptors: none is overwritten while in use
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTensor + 2 * kQ + 2 * kP;
@@ -119,6 +121,14 @@ struct Waiter {
   __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, (*this)(bar, parity) ? 1 : 0) != 0;
   }
+  // three barriers, looked at side by side: all of them have completed more often than not
+  __device__ __forceinline__ bool all(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1,
+                                      uint32_t b2, uint32_t p2) const {
+    const bool t0 = mbar_try_wait(b0, p0), t1 = mbar_try_wait(b1, p1), t2 = mbar_try_wait(b2, p2);
+    bool ok = t0 && t1 && t2;
+    if (!ok) ok = (t0 || (*this)(b0, p0)) && (t1 || (*this)(b1, p1)) && (t2 || (*this)(b2, p2));
+    return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
+  }
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -158,6 +168,11 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,29 +186,64 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return __half22float2(
       __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
 }
-// Eight values of at most 448, each as hi + lo / 16, both e4m3: the second term's own factor keeps it
-// clear of e4m3's smallest steps.
+// Values of at most 448, each as hi + lo / 16, both e4m3: the second term's own factor keeps it clear of
+// e4m3's smallest steps. Four codes to a word.
 constexpr float kLow = 1.f / 16;
-__device__ __forceinline__ void two_terms_e4m3(const float (&x)[8], uint2 &hi, uint2 &lo) {
-  uint32_t h[4], l[4];
+template <int N>
+__device__ __forceinline__ void two_terms_e4m3(const float (&x)[N], uint32_t (&hi)[N / 4],
+                                               uint32_t (&lo)[N / 4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = e4m3x2(x[2 * i], x[2 * i + 1]);
-    const float2 f = from_e4m3x2(h[i]);
-    l[i] = e4m3x2((x[2 * i] - f.x) * 16.f, (x[2 * i + 1] - f.y) * 16.f);
+  for (int i = 0; i < N / 2; ++i) {
+    // (fp16 has 11 significant bits: the rounding to it is a 2^-12 beside the 2^-8 of what follows,
+    // and none for x of 8 bits; hi, x - hi and the factor are then exact in it)
+    const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const __half2_raw vr = v;
+    const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(vr, __NV_SATFINITE, __NV_E4M3);
+    const __half2 f = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3));
+    const __half2_raw r = __hmul2(__hsub2(v, f), __float2half2_rn(16.f));
+    const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+    if (i & 1) {
+      hi[i / 2] |= h << 16;
+      lo[i / 2] |= l << 16;
+    } else {
+      hi[i / 2] = h;
+      lo[i / 2] = l;
+    }
   }
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
-__device__ __forceinline__ void two_terms_bf16(const float (&x)[8], uint4 &hi, uint4 &lo) {
-  uint32_t h[4], l[4];
+template <int N>
+__device__ __forceinline__ void two_terms_bf16(const float (&x)[N], uint32_t (&hi)[N / 2],
+                                               uint32_t (&lo)[N / 2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    l[i] = pack_bf16x2(x[2 * i] - bf16_lo(h[i]), x[2 * i + 1] - bf16_hi(h[i]));
+  for (int i = 0; i < N / 2; ++i) {
+    hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    lo[i] = pack_bf16x2(x[2 * i] - bf16_lo(hi[i]), x[2 * i + 1] - bf16_hi(hi[i]));
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// 8 or 16 fp32 columns of this thread's lane of tensor memory; wait with tmem_wait().
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15])
+        : "r"(addr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7])
+        : "r"(addr));
+}
+// The loads before it have arrived: v may be used (and its values depend on the wait).
+template <int N>
+__device__ __forceinline__ void tmem_wait(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x) {
@@ -251,8 +301,8 @@ __device__ __forceinline__ void join(const uint8_t *slots, int first, int last, 
   }
 }
 
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kE4m3, int NH>
+__global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedCache c,
                       const PagedAttnArgs a, int page_log2, uint8_t *workspace) {
   using Ge = Geo<D, kE4m3>;
@@ -262,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Tile s_tile[ND];
   __shared__ float s_scale[ND][2][8];          // of a tile's pages, K and V; < 0: no page
   __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
-  __shared__ __align__(16) float s_top[2][4][kG];       // a tile's maxima, per warp of tokens
+  __shared__ __align__(16) float s_top[2][4][kG];       // a tile's bases, per warp of tokens
+  __shared__ __align__(16) float s_base[4][3][kG];      // base, base - maximum as 2^x, maximum
   __shared__ __align__(16) float s_sum[4][4][2][kG];    // a segment's sums and their maxima
   __shared__ __align__(16) float s_f[4][5 * kG];        // factors, per warp of dimensions
   __shared__ int2 s_seg[4];
@@ -307,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   }
-  // rows of Q that no head fills stay zero
-  for (int i = tid; i < 2 * Ge::kQ / 16; i += kThreads)
+  // rows of Q that no head fills stay zero, and so do the weights' unused columns
+  for (int i = tid; i < 2 * (Ge::kQ + Ge::kP) / 16; i += kThreads)
     st_shared16(q_s + 16 * i, make_uint4(0u, 0u, 0u, 0u));
   pdl_wait_prior_grid();
   pdl_launch_dependents();
@@ -358,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (seq_of(a, b).tiles == 0)
       for (int i = tid; i < a.Hq * D / 8; i += kThreads)
         reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();  // (Q's zeros)
+  fence_proxy_async_smem();  // (the zeros)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -407,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seq s;
       int b, g, from, to, t0, t1, off, page;
     };
+    Tile t{};
     int at_tile = t0;
     auto next_batch = [&](Batch &x) {
       while (more && at_tile >= t1) {
@@ -453,7 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head = good ? number * c.Hkv + cur.g : -1;  // (-1: the copy leaves zeros)
         const int bytes = (p1 - p0) * page * Ge::kRow;
         if (2 * n >= S && !(ok = wait.all(bar_empty + 8 * ks, ((2 * n / S) - 1) & 1))) break;
-        if (i == cur.t0 && !(ok = push_segment(cur.b, cur.g))) break;
+        if (i == cur.t0) {
+          if (!(ok = push_segment(cur.b, cur.g))) break;
+          t.b = cur.b;
+          t.g = cur.g;
+          t.slot = cur.t0 == 0 && cur.t1 == cur.s.tiles ? -1 : 2 * piece + (cur.t0 == 0);
+          t.first = (cur.off + kSegment) / blk;
+          t.last = (cur.off + kSegment + cur.s.tiles - 1) / blk;
+        }
         if (here) {
           if (!good) {
             s_scale[d][0][lane] = s_scale[d][1][lane] = -1.f;
@@ -466,15 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (lane == 0) {
-          Tile t;
           t.lo = lo;
           t.hi = hi;
           t.flags = (i == cur.t0 ? kFirst : 0) | (i == cur.t1 - 1 ? kLast : 0);
-          t.b = cur.b;
-          t.g = cur.g;
-          t.slot = cur.t0 == 0 && cur.t1 == cur.s.tiles ? -1 : 2 * piece + (cur.t0 == 0);
-          t.first = (cur.off + kSegment) / blk;
-          t.last = (cur.off + kSegment + cur.s.tiles - 1) / blk;
           s_tile[d] = t;
           mbar_arrive_expect_tx(bar_full + 8 * ks, bytes);
         }
@@ -557,20 +610,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] *= inv;
-          uint2 hi, lo;
-          two_terms_e4m3(x, hi, lo);
+          uint32_t hi[2], lo[2];
+          two_terms_e4m3<8>(x, hi, lo);
           if (h < G) {
             if (ch == 0)
               s_qs[r][h] = m < INFINITY ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
                                         : __uint_as_float(0x7fc00000u);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const int row = h + t * kG, c16 = ch >> 1;
+              const int row = h + t * NH, c16 = ch >> 1;
               const int sw = Ge::kWide == 128 ? row & 7 : (row >> 1) & 3;
-              const uint2 v = t ? lo : hi;
+              const uint32_t (&v)[2] = t ? lo : hi;
               asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
                                base + row * Ge::kWide + ((c16 ^ sw) << 4) + ((ch & 1) << 3)),
-                           "r"(v.x), "r"(v.y)
+                           "r"(v[0]), "r"(v[1])
                            : "memory");
             }
           }
@@ -594,13 +647,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d = n % ND, slot = (2 * n) % S;
       if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
       const int flags = s_tile[d].flags;
-      if (flags & kEnd) break;
+      // The buffer's last tile has been read: a barrier completes its next phase only when all that wait
+      // for the one before have seen that.
+      if (n >= 2 && !wait.all(bar_p + 8 * (n & 1), ((n - 2) >> 1) & 1)) break;
+      if (flags & kEnd) {
+        if (elect_one()) umma_commit(bar_s + 8 * (n & 1));  // (the warps of weights wait for both)
+        break;
+      }
       if (flags & kFirst) {
         ++seg;
         if (!wait.all(bar_q + 8 * (seg & 3), (seg >> 2) & 1)) break;
       }
-      // the buffer's last tile has been read
-      if (n >= 2 && !wait.all(bar_p + 8 * (n & 1), ((n - 2) >> 1) & 1)) break;
       if (!wait.all(bar_full + 8 * slot, (2 * n / S) & 1)) break;
       tc_fence_after();
       const uint32_t k_lo = desc_lo(ring + slot * Ge::kTensor, 16);
@@ -620,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     // what was issued finishes before tensor memory is given back
+    __syncwarp();
     if (elect_one()) umma_commit(bar_end);
     __syncwarp();
     mbar_wait_bounded(bar_end, 0);
@@ -630,9 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0;; ++n) {
       const int d = n % ND, slot = (2 * n + 1) % S;
       if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
-      if (s_tile[d].flags & kEnd) break;
-      if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
       if (n >= 2 && !wait.all(bar_free + 8 * (n & 1), ((n - 2) >> 1) & 1)) break;
+      if (s_tile[d].flags & kEnd) {
+        if (elect_one()) umma_commit(bar_o + 8 * (n & 1));
+        break;
+      }
+      if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
       if (!wait.all(bar_p + 8 * (n & 1), (n >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t v_lo = desc_lo(ring + slot * Ge::kTensor, Ge::kSlab);
@@ -648,67 +709,116 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
+    __syncwarp();
     if (elect_one()) umma_commit(bar_end + 8);
     __syncwarp();
     mbar_wait_bounded(bar_end + 8, 0);
   } else if (warp < 4) {
     // ---------------------------------------------------------------- weights
     const uint32_t my_s = tmem + ((uint32_t)(32 * warp) << 16);
-    float qs[kG], top[kG], sum[kG];
+    // A warp's weights are 2^(8 + t - base) with a base per head that stays while the largest t of a tile
+    // lies within 2^-6 .. 2^0.5 of it: then a tile's weights, sums and part of O need no factor of their
+    // own. s_base: the base, 2^(base - maximum), and the maximum of the bases so far, which the sums
+    // are relative to.
+    float *my_base = s_base[warp][0];
+    float sum[NH];
     int seg = -1;
     for (int n = 0;; ++n) {
       const int d = n % ND, buf = n & 1;
-      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      // its descriptor, its S^T (or the end), and tile n - 2's weights and bases consumed
+      const uint32_t phase = (n >> 1) & 1;
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1, bar_s + 8 * buf, phase, bar_free + 8 * buf,
+                    phase ^ 1))
+        break;
+      if (s_tile[d].flags & kEnd) {
+        mbar_arrive(bar_p + 8 * buf);
+        break;
+      }
+      tc_fence_after();
+      constexpr int kCols = kE4m3 ? 2 * NH : 8;
+      float z[kCols];
+      tmem_ld(my_s + buf * kN, z);
       const Tile t = s_tile[d];
-      if (t.flags & kEnd) break;
       const float ks = s_scale[d][0][tid >> page_log2], vs = s_scale[d][1][tid >> page_log2];
       const bool inside = tid >= t.lo && tid < t.hi, seen = inside && ks > 0.f;
       if (t.flags & kFirst) {
         ++seg;
-        if (!wait.all(bar_q + 8 * (seg & 3), (seg >> 2) & 1)) break;
+        if (lane < kG) my_base[lane] = my_base[2 * kG + lane] = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kG; ++h) {
-          qs[h] = s_qs[seg & 3][h];
-          top[h] = -INFINITY;
-          sum[h] = 0.f;
-        }
+        for (int h = 0; h < NH; ++h) sum[h] = 0.f;
+        __syncwarp();
       }
-      const float lvs = kE4m3 ? lg2(vs) : 0.f, ivs = kE4m3 ? 1.f / vs : 1.f;
-      if (!wait.all(bar_s + 8 * buf, (n >> 1) & 1)) break;
-      tc_fence_after();
-      float z[kN];
-      tmem_ld16(my_s + buf * kN, z);
-      float w[kG], most[kG];
+      float qs[NH], base[NH], beta[NH];
+      const float4 *q4 = reinterpret_cast<const float4 *>(s_qs[seg & 3]);
+      const float4 *b4 = reinterpret_cast<const float4 *>(my_base);
 #pragma unroll
-      for (int h = 0; h < kG; ++h) {
-        w[h] = kE4m3 ? fmaf(z[kG + h], kLow, z[h]) * (qs[h] * ks) + lvs : z[h] * qs[h];
+      for (int h = 0; h < NH; h += 4) {
+        const float4 x = q4[h / 4], y = b4[h / 4], b = b4[kG / 4 + h / 4];
+        qs[h] = x.x, qs[h + 1] = x.y, qs[h + 2] = x.z, qs[h + 3] = x.w;
+        base[h] = y.x, base[h + 1] = y.y, base[h + 2] = y.z, base[h + 3] = y.w;
+        beta[h] = b.x, beta[h + 1] = b.y, beta[h + 2] = b.z, beta[h + 3] = b.w;
+      }
+      const float lvs = kE4m3 ? lg2(vs) : 0.f, ivs = seen ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
+      tmem_wait(z);
+      float w[NH], most[NH];
+      bool near = true;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if constexpr (kE4m3)
+          w[h] = fmaf(fmaf(z[NH + h], kLow, z[h]), qs[h] * ks, lvs);
+        else
+          w[h] = z[h] * qs[h];
         if (!seen) w[h] = -INFINITY;
         most[h] = warp_max(w[h]);
-        // weights relative to 2^-8 of the warp's largest
-        w[h] = ex2(w[h] - ((most[h] == -INFINITY ? 0.f : most[h]) - 8.f));
-        const float to = fmaxf(top[h], most[h]), base = to == -INFINITY ? 0.f : to;
-        sum[h] = sum[h] * ex2(top[h] - base) + (w[h] * (seen ? ivs : 0.f)) * ex2(most[h] - base);
-        top[h] = to;
+        near = near && most[h] - base[h] <= 0.5f && most[h] - base[h] >= -6.f;
       }
-      // the buffers of weights and maxima of tile n - 2 are consumed
-      if (n >= 2 && !wait.all(bar_o + 8 * buf, ((n - 2) >> 1) & 1)) break;
-      if (n >= 2 && !wait.all(bar_free + 8 * buf, ((n - 2) >> 1) & 1)) break;
+      if (!near) {  // (the same for the whole warp)
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const float x = most[h] - base[h], old = my_base[2 * kG + h];
+          if (!(x <= 0.5f && x >= -6.f) && most[h] != -INFINITY) base[h] = most[h];
+          const float to = fmaxf(old, base[h]), by = to == -INFINITY ? 0.f : to;
+          sum[h] *= ex2(old - by);
+          beta[h] = ex2(base[h] - by);
+          __syncwarp();
+          if (lane == 0) {
+            my_base[h] = base[h];
+            my_base[kG + h] = beta[h];
+            my_base[2 * kG + h] = to;
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        w[h] = ex2(w[h] - ((base[h] == -INFINITY ? 0.f : base[h]) - 8.f));
+        sum[h] = fmaf(w[h] * ivs, beta[h], sum[h]);
+      }
       if (lane == 0) {
 #pragma unroll
-        for (int h = 0; h < kG; h += 4)
+        for (int h = 0; h < NH; h += 4)
           *reinterpret_cast<float4 *>(&s_top[buf][warp][h]) =
-              make_float4(most[h], most[h + 1], most[h + 2], most[h + 3]);
+              make_float4(base[h], base[h + 1], base[h + 2], base[h + 3]);
       }
       const uint32_t my_p = p_s + buf * Ge::kP + tid * 16;
-      if (kE4m3) {
-        uint2 hi, lo;
-        two_terms_e4m3(w, hi, lo);
-        st_shared16(my_p, make_uint4(hi.x, hi.y, lo.x, lo.y));
+      if constexpr (kE4m3) {
+        uint32_t hi[NH / 4], lo[NH / 4];
+        two_terms_e4m3<NH>(w, hi, lo);
+        if constexpr (NH == 8)
+          st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+        else
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(my_p), "r"(hi[0]), "r"(lo[0])
+                       : "memory");
       } else {
-        uint4 hi, lo;
-        two_terms_bf16(w, hi, lo);
-        st_shared16(my_p, hi);
-        st_shared16(my_p + kTile * 16, lo);
+        uint32_t hi[NH / 2], lo[NH / 2];
+        two_terms_bf16<NH>(w, hi, lo);
+        if constexpr (NH == 8) {
+          st_shared16(my_p, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          st_shared16(my_p + kTile * 16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        } else {
+          st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+        }
       }
       // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
       // page that does not exist was left zeros.)
@@ -724,11 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (t.flags & kLast) {
 #pragma unroll
-        for (int h = 0; h < kG; ++h) {
+        for (int h = 0; h < NH; ++h) {
           const float x = warp_sum(sum[h]);
           if (lane == 0) {
             s_sum[seg & 3][warp][0][h] = x;
-            s_sum[seg & 3][warp][1][h] = top[h];
+            s_sum[seg & 3][warp][1][h] = my_base[2 * kG + h];
           }
         }
         if (lane == 0) mbar_arrive(bar_sum + 8 * (seg & 3));
@@ -746,8 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *slots = workspace + kSlotsOffset;
     int *counters = reinterpret_cast<int *>(workspace + kWsHeaderBytes);
     const size_t slot_size = slot_bytes(G, D);
-    float acc[kG];
-    float top = -INFINITY;  // the running maximum of head lane & 7
+    float acc[NH];
+    float top = -INFINITY;  // the running maximum of the bases of head lane & 7
     int seg = -1, met = 0;
     // the four warps together (a bounded wait: one of them may have given up)
     auto meet = [&]() {
@@ -756,16 +866,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int n = 0;; ++n) {
       const int d = n % ND, buf = n & 1;
-      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1)) break;
+      const uint32_t phase = (n >> 1) & 1;
+      // the descriptor, the bases, and the product (or the end)
+      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1, bar_p + 8 * buf, phase, bar_o + 8 * buf, phase))
+        break;
       const Tile t = s_tile[d];
       if (t.flags & kEnd) break;
+      tc_fence_after();
+      float o[2][2 * NH];
+      tmem_ld(my_o + buf * kOCols, o[0]);
+      tmem_ld(my_o + buf * kOCols + kN, o[1]);
       if (t.flags & kFirst) {
         ++seg;
         top = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kG; ++h) acc[h] = 0.f;
+        for (int h = 0; h < NH; ++h) acc[h] = 0.f;
       }
-      if (!wait.all(bar_p + 8 * buf, (n >> 1) & 1)) break;  // (the maxima)
       {
         const float x = s_top[buf][lane >> 3][lane & 7];
         float m = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -776,21 +892,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = to;
       }
       __syncwarp();
-      if (!wait.all(bar_o + 8 * buf, (n >> 1) & 1)) break;
-      tc_fence_after();
       const float4 *f4 = reinterpret_cast<const float4 *>(s_f[w4]);
-      const float4 a0 = f4[8], a1 = f4[9];
-      const float al[kG] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-      for (int h = 0; h < kG; ++h) acc[h] *= al[h];
+      for (int h = 0; h < NH; h += 4) {
+        const float4 x = f4[8 + h / 4];
+        acc[h] *= x.x, acc[h + 1] *= x.y, acc[h + 2] *= x.z, acc[h + 3] *= x.w;
+      }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float o[kN];
-        tmem_ld16(my_o + buf * kOCols + w * kN, o);
-        const float4 f0 = f4[2 * w], f1 = f4[2 * w + 1];
-        const float f[kG] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+      for (int w = 0; w < 4; w += 2) {
+        tmem_wait(o[0]);
+        tmem_wait(o[1]);
 #pragma unroll
-        for (int h = 0; h < kG; ++h) acc[h] = fmaf(fmaf(o[kG + h], kE4m3 ? kLow : 1.f, o[h]), f[h], acc[h]);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int h = 0; h < NH; h += 4) {
+            const float4 x = f4[2 * (w + u) + h / 4];
+            const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[h + j] = fmaf(fmaf(o[u][NH + h + j], kE4m3 ? kLow : 1.f, o[u][h + j]), f[j],
+                                acc[h + j]);
+          }
+        if (w == 0) {
+          tmem_ld(my_o + buf * kOCols + 2 * kN, o[0]);
+          tmem_ld(my_o + buf * kOCols + 3 * kN, o[1]);
+        }
       }
       __syncwarp();
       if (!(t.flags & kLast)) {
@@ -812,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *out = a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D + dim;
 #pragma unroll
-        for (int h = 0; h < kG; ++h) {
+        for (int h = 0; h < NH; ++h) {
           const float x = __shfl_sync(0xffffffffu, inv, h);
           if (h < G && mine_too) out[h * D] = __float2bfloat16(acc[h] * x);
         }
@@ -820,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint8_t *part = slots + (size_t)t.slot * slot_size;
 #pragma unroll
-      for (int h = 0; h < kG; ++h)
+      for (int h = 0; h < NH; ++h)
         if (h < G && mine_too) reinterpret_cast<float *>(part)[h * D + dim] = acc[h];
       if (w4 == 0 && lane < G)
         reinterpret_cast<float2 *>(part + (size_t)G * D * 4)[lane] = make_float2(top, l);
@@ -846,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int NH>
 cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs &a, int parts,
                    uint8_t *ws, cudaStream_t stream) {
   // per device: the kernel's shared memory (set before its first launch there)
@@ -856,7 +982,7 @@ cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs 
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<D, kE4m3>,
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, kE4m3, NH>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Geo<D, kE4m3>::kSmem);
     if (e != cudaSuccess) return e;
@@ -864,17 +990,20 @@ cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs 
   }
   int log2 = 4;
   while ((1 << log2) < c.page) ++log2;
-  return launch_pdl(paged_attn_kernel<D, kE4m3>, dim3(parts), kThreads, Geo<D, kE4m3>::kSmem,
+  return launch_pdl(paged_attn_kernel<D, kE4m3, NH>, dim3(parts), kThreads, Geo<D, kE4m3>::kSmem,
                     stream, m, c, a, log2, ws);
 }
 
 }  // namespace
 
-// One CTA per SM, or fewer when there are not as many tiles.
-int paged_attn_parts(int B, int Hkv, int max_len, int num_parts, int sms) {
+// As many CTAs as the SMs hold, or fewer when there are not as many tiles.
+int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts, int sms) {
   if (num_parts > 0) return num_parts;
+  const int per = D == 128 ? (e4m3 ? Geo<128, true>::kCtas : Geo<128, false>::kCtas)
+                           : (e4m3 ? Geo<64, true>::kCtas : Geo<64, false>::kCtas);
   const long long tiles = (long long)B * Hkv * ((max_len + kTile - 1) / kTile + 1);
-  return (int)(tiles < 1 ? 1 : tiles < sms ? tiles : sms < kPagedMaxParts ? sms : kPagedMaxParts);
+  const long long most = per * sms < kPagedMaxParts ? per * sms : kPagedMaxParts;
+  return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 
 size_t paged_attn_ws_bytes(int, int Hq, int Hkv, int D, int parts) {
@@ -886,10 +1015,17 @@ cudaError_t launch_paged_attn(const CUtensorMap &k, const CUtensorMap &v, const 
                               cudaStream_t stream) {
   const PagedMaps m{k, v};
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const cudaError_t e = c.D == 128 ? (c.e4m3 ? launch<128, true>(m, c, a, parts, ws, stream)
-                                             : launch<128, false>(m, c, a, parts, ws, stream))
-                                   : (c.e4m3 ? launch<64, true>(m, c, a, parts, ws, stream)
-                                             : launch<64, false>(m, c, a, parts, ws, stream));
+  auto go = [&](auto dim, auto e4m3) {
+    constexpr int kD = decltype(dim)::value;
+    constexpr bool kE = decltype(e4m3)::value;
+    return a.Hq / c.Hkv <= 4 ? launch<kD, kE, 4>(m, c, a, parts, ws, stream)
+                             : launch<kD, kE, 8>(m, c, a, parts, ws, stream);
+  };
+  using I64 = std::integral_constant<int, 64>;
+  using I128 = std::integral_constant<int, 128>;
+  const cudaError_t e =
+      c.D == 128 ? (c.e4m3 ? go(I128{}, std::true_type{}) : go(I128{}, std::false_type{}))
+                 : (c.e4m3 ? go(I64{}, std::true_type{}) : go(I64{}, std::false_type{}));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
