@@ -38,6 +38,7 @@
 
 #include <atomic>
 #include <type_traits>
+#include <utility>
 
 #include "dec_device.cuh"
 #include "dec_launch.h"
@@ -46,17 +47,16 @@
 namespace decattn {
 namespace {
 
-constexpr int kTile = 128;   // tokens per tile
 constexpr int kG = kSplitMaxG;
 constexpr int kN = 16;       // columns of the products: two terms of each of up to 8 heads
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTma = 8, kQuery = 9, kScore = 10, kValue = 11;  // warps
 constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kOCol = 2 * kN;        // S buffers in columns [0, 32), O's behind them
 constexpr uint32_t kOCols = 4 * kN;       // an O buffer: 16 columns for each warp of tokens
-// What beginning and ending a segment costs, in tiles: the stream is cut by tiles plus this.
-constexpr int kSegment = 2;
+// What beginning and ending a segment costs, in tiles: the stream is cut by tiles plus this, unless
+// there are fewer than kFew tiles per piece.
+constexpr int kSegment = 2, kFew = 4;
 constexpr int kCounters = 4096;           // a counter per piece
 static_assert(kCounters == kPagedMaxParts, "one counter per piece");
 
@@ -66,6 +66,10 @@ struct Geo {
   static constexpr int kRow = D * (kE4m3 ? 1 : 2);             // bytes of a row
   static constexpr int kWide = kRow < 128 ? kRow : 128;        // of it in a slab: the swizzle's width
   static constexpr int kSlabs = kRow / kWide;
+  // Tokens per tile: a token, or two 128 apart, for each thread of the warps of weights. Two where the
+  // products of a tile take less time than what surrounds them.
+  static constexpr int kHalves = kRow == 64 ? 2 : 1;
+  static constexpr int kTile = 128 * kHalves;
   static constexpr int kSlab = kTile * kWide;
   static constexpr int kTensor = kSlabs * kSlab;               // a K or a V tile
   static constexpr int kQ = kN * kRow;
@@ -74,6 +78,7 @@ struct Geo {
   static constexpr int kSlots = (192 / kCtas) * 1024 / kTensor;  // of the ring, half of them K's
   static constexpr int kTiles = kSlots / 2;
   static constexpr int kDescs = kTiles + 4;  // tile descriptors: none is overwritten while in use
+  static constexpr uint32_t kOCol = 2 * kHalves * kN;  // of tensor memory: O's columns behind two S's
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTensor + 2 * kQ + 2 * kP;
   // high words of the matrix descriptors: 8 rows to the next 8, the version bit, the swizzle mode
   static constexpr uint32_t kHi =
@@ -98,7 +103,7 @@ struct alignas(16) Tile {
   int flags;
   int b, g;
   int slot;        // partial of this segment, -1: it is the whole pair
-  int first, last; // the pieces the pair lies in
+  int unit, tiles; // the pair's first tile in the stream, and how many there are
 };
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;  // of a segment; of the piece (not a tile)
 
@@ -262,6 +267,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 struct Seq {
   int L, start, tile0, tiles;  // tokens start .. L are seen, in tiles tile0 .. tile0 + tiles
 };
+template <int kTile>
 __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   Seq s;
   s.L = min(max(a.lens[b], 0), a.max_len);
@@ -270,30 +276,44 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   s.tiles = s.L > s.start ? (s.L + kTile - 1) / kTile - s.tile0 : 0;
   return s;
 }
-__device__ __forceinline__ int units_of(const Seq &s) { return s.tiles > 0 ? s.tiles + kSegment : 0; }
-
-// The partials of a pair of pieces first .. last into its G rows of the output, by 128 threads.
+// The partials of a pair of pieces first .. last into its G rows of the output, by 128 threads: 4
+// neighbouring dims of a head each, the partials' loads in flight kAtOnce at a time.
 template <int D>
 __device__ __forceinline__ void join(const uint8_t *slots, int first, int last, int G,
                                      __nv_bfloat16 *out) {
+  constexpr int kAtOnce = 8;
   const size_t slot = slot_bytes(G, D);
-  // 4 neighbouring dims of a head per thread
   for (int i = threadIdx.x & 127; i < G * (D / 4); i += 128) {
     const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
     float M = -INFINITY, sum = 0.f, o[4] = {};
-#pragma unroll 4
-    for (int c = first; c <= last; ++c) {
-      const uint8_t *p = slots + (size_t)(2 * c + (c == first)) * slot;
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(p + ((size_t)h * D + d) * 4));
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)G * D * 4) + h);
-      const float to = fmaxf(M, ml.x), base = to == -INFINITY ? 0.f : to;
-      const float f = ex2(M - base), g = ex2(ml.x - base);
+    for (int c0 = first; c0 <= last; c0 += kAtOnce) {
+      float4 x[kAtOnce];
+      float2 ml[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int c = min(c0 + u, last);
+        const uint8_t *p = slots + (size_t)(2 * c + (c == first)) * slot;
+        x[u] = __ldcg(reinterpret_cast<const float4 *>(p + ((size_t)h * D + d) * 4));
+        ml[u] = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)G * D * 4) + h);
+      }
+      float to = M;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) to = fmaxf(to, ml[u].x);
+      const float base = to == -INFINITY ? 0.f : to, f = ex2(M - base);
       M = to;
-      sum = sum * f + ml.y * g;
-      o[0] = o[0] * f + x.x * g;
-      o[1] = o[1] * f + x.y * g;
-      o[2] = o[2] * f + x.z * g;
-      o[3] = o[3] * f + x.w * g;
+      sum *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] *= f;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (c0 + u > last) break;
+        const float g = ex2(ml[u].x - base);
+        sum = fmaf(ml[u].y, g, sum);
+        o[0] = fmaf(x[u].x, g, o[0]);
+        o[1] = fmaf(x[u].y, g, o[1]);
+        o[2] = fmaf(x[u].z, g, o[2]);
+        o[3] = fmaf(x[u].w, g, o[3]);
+      }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(out + (size_t)h * D + d) =
@@ -306,19 +326,20 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedCache c,
                       const PagedAttnArgs a, int page_log2, uint8_t *workspace) {
   using Ge = Geo<D, kE4m3>;
-  constexpr int S = Ge::kSlots, ND = Ge::kDescs;
+  constexpr int S = Ge::kSlots, ND = Ge::kDescs, kTile = Ge::kTile, kHalves = Ge::kHalves;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_bar[2 * S + ND + 33];
   __shared__ Tile s_tile[ND];
-  __shared__ float s_scale[ND][2][8];          // of a tile's pages, K and V; < 0: no page
+  __shared__ float s_scale[ND][2][8 * kHalves];  // of a tile's pages, K and V; < 0: no page
   __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
   __shared__ __align__(16) float s_top[2][4][kG];       // a tile's bases, per warp of tokens
-  __shared__ __align__(16) float s_base[4][3][kG];      // base, base - maximum as 2^x, maximum
+  __shared__ __align__(16) float s_base[4][4][kG];      // see the warps of weights
   __shared__ __align__(16) float s_sum[4][4][2][kG];    // a segment's sums and their maxima
   __shared__ __align__(16) float s_f[4][5 * kG];        // factors, per warp of dimensions
   __shared__ int2 s_seg[4];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_warp_units[kWarps], s_begin[5], s_joins;
+  __shared__ int s_abort, s_joins, s_begin[2];
+  __shared__ int2 s_warp_units[kWarps];
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_addr(smem), q_s = ring + S * Ge::kTensor, p_s = q_s + 2 * Ge::kQ;
@@ -330,26 +351,20 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = a.Hq / c.Hkv;
 
-  if (tid == 0) {
-    for (int i = 0; i < 2 * S; ++i) mbar_init(bar_full + 8 * i, 1);
-    for (int i = 0; i < ND; ++i) mbar_init(bar_desc + 8 * i, kE4m3 ? 33 : 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_s + 8 * i, 1);
-      mbar_init(bar_p + 8 * i, 128);
-      mbar_init(bar_o + 8 * i, 1);
-      mbar_init(bar_free + 8 * i, 128);
-      mbar_init(bar_qfree + 8 * i, 1);
-      mbar_init(bar_end + 8 * i, 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar_q + 8 * i, 1);
-      mbar_init(bar_sum + 8 * i, 4);
-      mbar_init(bar_seg + 8 * i, 1);
-      mbar_init(bar_segfree + 8 * i, 1);
-    }
-    mbar_init(bar_meet, 128);
-    s_abort = 0;
+  // A barrier per thread. (A barrier completes its next phase only when all that wait for the one
+  // before have seen that: each role's waits say so, those for the end of the piece included.)
+  if (tid < 2 * S + ND + 33) {
+    const uint32_t bar = bar_full + 8 * tid;
+    const bool many = (bar >= bar_p && bar < bar_o) || (bar >= bar_free && bar < bar_q) || bar == bar_meet;
+    mbar_init(bar, bar >= bar_desc && bar < bar_s ? (kE4m3 ? 33 : 1)
+                   : many                         ? 128
+                   : bar >= bar_sum && bar < bar_seg ? 4
+                                                     : 1);
     fence_barrier_init();
+  }
+  if (tid == 0) {
+    s_abort = 0;
+    s_begin[0] = -1;
   }
   if (warp == kTma) {
     if (lane == 0) {
@@ -366,59 +381,58 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
 
   // ---- where this CTA's piece begins: a scan over the sequences, a run of them per thread
   const int P = gridDim.x, piece = blockIdx.x;
-  const int per = (a.B + kThreads - 1) / kThreads, b_first = tid * per;
+  const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads, b_first = tid * per;
   const int b_last = min(a.B, b_first + per);
-  int mine = 0;
+  int2 mine = make_int2(0, 0);  // tiles, pairs
   for (int b = b_first; b < b_last; ++b) {
-    const Seq s = seq_of(a, b);
-    mine += units_of(s) * c.Hkv;
+    const Seq s = seq_of<kTile>(a, b);
+    mine.x += s.tiles * c.Hkv;
+    mine.y += s.tiles > 0 ? c.Hkv : 0;
     if (piece == 0 && s.L != a.lens[b]) atomicOr(a.error_word, kErrLenClamped);
   }
-  const int in_warp = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) s_warp_units[warp] = in_warp;
-  if (tid == 0) s_begin[0] = -1;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int u = s_warp_units[w];
-    if (w < warp) before += u;
-    total += u;
-  }
-  const int blk = max(1, (int)(((long long)total + P - 1) / P));
-  const long long r0 = (long long)piece * blk;
-  int incl = mine;
+  int2 incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) incl.x += x, incl.y += y;
   }
-  int at = before + incl - mine;
-  if (r0 < total && at <= r0 && r0 < at + mine) {
+  if (lane == 31) s_warp_units[warp] = incl;
+  fence_proxy_async_smem();  // (the zeros)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int2 before = make_int2(0, 0), all = before;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int2 u = s_warp_units[w];
+    if (w < warp) before.x += u.x, before.y += u.y;
+    all.x += u.x, all.y += u.y;
+  }
+  const int segment = all.x >= kFew * P ? kSegment : 0;
+  const int total = all.x + segment * all.y;
+  const int blk = max(1u, ((unsigned)total + P - 1) / (unsigned)P);
+  const long long r0 = (long long)piece * blk;
+  const int count = mine.x + segment * mine.y;
+  int at = before.x + incl.x + segment * (before.y + incl.y) - count;
+  if (at <= r0 && r0 < at + count) {
     int b = b_first;
     for (;; ++b) {
-      const int u = units_of(seq_of(a, b)) * c.Hkv;
+      const Seq s = seq_of<kTile>(a, b);
+      const int u = s.tiles > 0 ? (s.tiles + segment) * c.Hkv : 0;
       if (r0 < at + u) break;
       at += u;
     }
     s_begin[0] = b;
     s_begin[1] = (int)r0 - at;
   }
-  // sequences without tokens are nobody's tiles: their zeros
-  for (int b = piece; b < a.B; b += P)
-    if (seq_of(a, b).tiles == 0)
-      for (int i = tid; i < a.Hq * D / 8; i += kThreads)
-        reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();  // (the zeros)
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   const Waiter wait{&s_abort, a.error_word};
 
   if (warp == kTma) {
     // ---------------------------------------------------------------- loads
-    const int page = 1 << page_log2, ppt = kTile >> page_log2, ppt_log2 = 7 - page_log2;
+    const int page = 1 << page_log2, ppt = kTile >> page_log2;
+    const int ppt_log2 = (kHalves == 2 ? 8 : 7) - page_log2;
     const int batch = 32 >> ppt_log2;  // tiles whose page numbers the lanes hold
     const uint64_t policy = l2_policy_evict_first();
     // the walk: (b, g), its tiles t0 .. t1 of this piece (from the sequence's first seen one), and
@@ -426,15 +440,15 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     int b = s_begin[0], g = 0, left = 0, t0 = 0, t1 = 0, off = 0;
     Seq s{};
     auto take = [&](int from) {  // from: units of this pair that lie before the piece
-      t0 = max(0, from - kSegment);
-      t1 = max(t0, min(s.tiles, from + left - kSegment));
-      left -= min(left, t1 + kSegment - from);
+      t0 = max(0, from - segment);
+      t1 = max(t0, min(s.tiles, from + left - segment));
+      left -= min(left, t1 + segment - from);
     };
     bool more = b >= 0;
     if (more) {
-      s = seq_of(a, b);
-      const int u = units_of(s);
-      g = s_begin[1] / u;
+      s = seq_of<kTile>(a, b);
+      const int u = s.tiles + segment;
+      g = (unsigned)s_begin[1] / (unsigned)u;
       const int from = s_begin[1] - g * u;
       off = (int)r0 - from;
       left = (int)min((long long)blk, total - r0);
@@ -443,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     // the next pair; false: none in this piece
     auto next_pair = [&]() {
       if (left <= 0) return false;
-      off += units_of(s);
+      off += s.tiles + segment;
       if (++g == c.Hkv) {
         g = 0;
         do {
           if (++b >= a.B) return false;
-          s = seq_of(a, b);
+          s = seq_of<kTile>(a, b);
         } while (s.tiles == 0);
       }
       take(0);
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       // this lane's page: tile from + lane / ppt, page lane % ppt of it; only where a token is seen
       const int slot = ((s.tile0 + x.from) << ppt_log2) + lane;
       x.page = -1;
-      if ((slot << page_log2) < s.L && ((slot + 1) << page_log2) > s.start &&
+      if ((slot << page_log2) < s.L && (slot << page_log2) + page - 1 >= s.start &&
           lane < (x.to - x.from) << ppt_log2)
         x.page = c.table[(size_t)b * c.max_pages + slot];
       return true;
@@ -510,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
           t.b = cur.b;
           t.g = cur.g;
           t.slot = cur.t0 == 0 && cur.t1 == cur.s.tiles ? -1 : 2 * piece + (cur.t0 == 0);
-          t.first = (cur.off + kSegment) / blk;
-          t.last = (cur.off + kSegment + cur.s.tiles - 1) / blk;
+          t.unit = cur.off + segment;
+          t.tiles = cur.s.tiles;
         }
         if (here) {
           if (!good) {
@@ -566,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       if (lane == 0) mbar_arrive(bar_desc + 8 * d);
     }
     // no copy into this CTA's shared memory may outlive it (all have landed unless a wait gave up)
-    for (int j = max(0, n - S / 2); j < n; ++j) {
+    for (int j = max(0, n - (S + 1) / 2); j < n; ++j) {
       mbar_wait_bounded(bar_full + 8 * ((2 * j) % S), (2 * j / S) & 1);
       mbar_wait_bounded(bar_full + 8 * ((2 * j + 1) % S), ((2 * j + 1) / S) & 1);
     }
@@ -641,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     // ---------------------------------------------------------------- S^T = K Q^T
     // (the warp stays together and an elected lane issues: the operands are then the same across
     // the warp as far as the compiler can tell)
-    constexpr uint32_t idesc = Ge::idesc(kTile, false);
+    constexpr uint32_t idesc = Ge::idesc(128, false);
     int seg = -1;
     for (int n = 0;; ++n) {
       const int d = n % ND, slot = (2 * n) % S;
@@ -664,12 +678,16 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       const uint32_t q_lo = desc_lo(q_s + (seg & 1) * Ge::kQ, 16);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < Ge::kRow / 32; ++k) {
-          constexpr int kPer = Ge::kWide / 32;
-          umma<kE4m3>(tmem + (n & 1) * kN, k_lo + (k / kPer) * (Ge::kSlab >> 4) + 2 * (k % kPer),
-                      Ge::kHi, q_lo + (k / kPer) * (kN * Ge::kWide >> 4) + 2 * (k % kPer), Ge::kHi,
-                      idesc, k > 0);
-        }
+        for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+          for (int k = 0; k < Ge::kRow / 32; ++k) {
+            constexpr int kPer = Ge::kWide / 32;
+            umma<kE4m3>(tmem + ((n & 1) * kHalves + half) * kN,
+                        k_lo + (k / kPer) * (Ge::kSlab >> 4) + 2 * (k % kPer) +
+                            half * (128 * Ge::kWide >> 4),
+                        Ge::kHi, q_lo + (k / kPer) * (kN * Ge::kWide >> 4) + 2 * (k % kPer),
+                        Ge::kHi, idesc, k > 0);
+          }
         umma_commit(bar_empty + 8 * slot);
         umma_commit(bar_s + 8 * (n & 1));
         if (flags & kLast) umma_commit(bar_qfree + 8 * (seg & 1));
@@ -701,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / kStep; ++k)
-          umma<kE4m3>(tmem + kOCol + (n & 1) * kOCols + (k * kStep / 32) * kN,
+          umma<kE4m3>(tmem + Ge::kOCol + (n & 1) * kOCols + (k * kStep / 32 % 4) * kN,
                       v_lo + k * (kStep * Ge::kWide >> 4), Ge::kHi, p_lo + k * kStep, Ge::kPHi, idesc,
-                      (k * kStep) % 32 != 0);
+                      (k * kStep) % 32 != 0 || k * kStep >= 128);
         umma_commit(bar_empty + 8 * slot);
         umma_commit(bar_o + 8 * (n & 1));
       }
@@ -718,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     const uint32_t my_s = tmem + ((uint32_t)(32 * warp) << 16);
     // A warp's weights are 2^(8 + t - base) with a base per head that stays while the largest t of a tile
     // lies within 2^-6 .. 2^0.5 of it: then a tile's weights, sums and part of O need no factor of their
-    // own. s_base: the base, 2^(base - maximum), and the maximum of the bases so far, which the sums
-    // are relative to.
+    // own. s_base: the bases, 2^(base - maximum), the maximum of the bases so far, which the sums
+    // are relative to, and what the sums are to be multiplied with.
     float *my_base = s_base[warp][0];
     float sum[NH];
     int seg = -1;
@@ -736,11 +754,22 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       }
       tc_fence_after();
       constexpr int kCols = kE4m3 ? 2 * NH : 8;
-      float z[kCols];
-      tmem_ld(my_s + buf * kN, z);
+      float z[kHalves][kCols];
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half) tmem_ld(my_s + (buf * kHalves + half) * kN, z[half]);
       const Tile t = s_tile[d];
-      const float ks = s_scale[d][0][tid >> page_log2], vs = s_scale[d][1][tid >> page_log2];
-      const bool inside = tid >= t.lo && tid < t.hi, seen = inside && ks > 0.f;
+      bool inside[kHalves];
+      float ks[kHalves], lvs[kHalves], ivs[kHalves];
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half) {
+        const int row = tid + 128 * half;
+        ks[half] = s_scale[d][0][row >> page_log2];
+        const float vs = s_scale[d][1][row >> page_log2];
+        inside[half] = row >= t.lo && row < t.hi;
+        if (!inside[half]) ks[half] = -1.f;
+        lvs[half] = kE4m3 ? lg2(vs) : 0.f;
+        ivs[half] = ks[half] > 0.f ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
+      }
       if (t.flags & kFirst) {
         ++seg;
         if (lane < kG) my_base[lane] = my_base[2 * kG + lane] = -INFINITY;
@@ -749,51 +778,70 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         __syncwarp();
       }
       float qs[NH], base[NH], beta[NH];
-      const float4 *q4 = reinterpret_cast<const float4 *>(s_qs[seg & 3]);
-      const float4 *b4 = reinterpret_cast<const float4 *>(my_base);
+      auto load4 = [&](float (&to)[NH], const float *from) {
 #pragma unroll
-      for (int h = 0; h < NH; h += 4) {
-        const float4 x = q4[h / 4], y = b4[h / 4], b = b4[kG / 4 + h / 4];
-        qs[h] = x.x, qs[h + 1] = x.y, qs[h + 2] = x.z, qs[h + 3] = x.w;
-        base[h] = y.x, base[h + 1] = y.y, base[h + 2] = y.z, base[h + 3] = y.w;
-        beta[h] = b.x, beta[h + 1] = b.y, beta[h + 2] = b.z, beta[h + 3] = b.w;
-      }
-      const float lvs = kE4m3 ? lg2(vs) : 0.f, ivs = seen ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
-      tmem_wait(z);
-      float w[NH], most[NH];
+        for (int h = 0; h < NH; h += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(from + h);
+          to[h] = x.x, to[h + 1] = x.y, to[h + 2] = x.z, to[h + 3] = x.w;
+        }
+      };
+      load4(qs, s_qs[seg & 3]);
+      load4(base, my_base);
+      load4(beta, my_base + kG);
+      float w[kHalves][NH], most[NH];
       bool near = true;
 #pragma unroll
+      for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
+#pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if constexpr (kE4m3)
-          w[h] = fmaf(fmaf(z[NH + h], kLow, z[h]), qs[h] * ks, lvs);
-        else
-          w[h] = z[h] * qs[h];
-        if (!seen) w[h] = -INFINITY;
-        most[h] = warp_max(w[h]);
+        float m = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          const float *x = z[half];
+          if constexpr (kE4m3)
+            w[half][h] = fmaf(fmaf(x[NH + h], kLow, x[h]), qs[h] * ks[half], lvs[half]);
+          else
+            w[half][h] = x[h] * qs[h];
+          if (!(ks[half] > 0.f)) w[half][h] = -INFINITY;  // (not seen)
+          m = fmaxf(m, w[half][h]);
+        }
+        most[h] = warp_max(m);
         near = near && most[h] - base[h] <= 0.5f && most[h] - base[h] >= -6.f;
       }
-      if (!near) {  // (the same for the whole warp)
-        __syncwarp();
+      if (!near) {  // (the same for the whole warp) a head per lane
+        float m = most[0];
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const float x = most[h] - base[h], old = my_base[2 * kG + h];
-          if (!(x <= 0.5f && x >= -6.f) && most[h] != -INFINITY) base[h] = most[h];
-          const float to = fmaxf(old, base[h]), by = to == -INFINITY ? 0.f : to;
-          sum[h] *= ex2(old - by);
-          beta[h] = ex2(base[h] - by);
-          __syncwarp();
-          if (lane == 0) {
-            my_base[h] = base[h];
-            my_base[kG + h] = beta[h];
-            my_base[2 * kG + h] = to;
-          }
+        for (int h = 1; h < NH; ++h)
+          if ((lane & (kG - 1)) == h) m = most[h];
+        float b = my_base[lane & (kG - 1)];
+        const float old = my_base[2 * kG + (lane & (kG - 1))], x = m - b;
+        if (!(x <= 0.5f && x >= -6.f) && m != -INFINITY) b = m;
+        const float to = fmaxf(old, b), by = to == -INFINITY ? 0.f : to;
+        __syncwarp();
+        if (lane < NH) {
+          my_base[lane] = b;
+          my_base[kG + lane] = ex2(b - by);
+          my_base[2 * kG + lane] = to;
+          my_base[3 * kG + lane] = ex2(old - by);
         }
         __syncwarp();
+        load4(base, my_base);
+        load4(beta, my_base + kG);
+        float alpha[NH];
+        load4(alpha, my_base + 3 * kG);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sum[h] *= alpha[h];
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        w[h] = ex2(w[h] - ((base[h] == -INFINITY ? 0.f : base[h]) - 8.f));
-        sum[h] = fmaf(w[h] * ivs, beta[h], sum[h]);
+        const float by = (base[h] == -INFINITY ? 0.f : base[h]) - 8.f;
+        float add = 0.f;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          w[half][h] = ex2(w[half][h] - by);
+          add = fmaf(w[half][h], ivs[half], add);
+        }
+        sum[h] = fmaf(add, beta[h], sum[h]);
       }
       if (lane == 0) {
 #pragma unroll
@@ -801,23 +849,26 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
           *reinterpret_cast<float4 *>(&s_top[buf][warp][h]) =
               make_float4(base[h], base[h + 1], base[h + 2], base[h + 3]);
       }
-      const uint32_t my_p = p_s + buf * Ge::kP + tid * 16;
-      if constexpr (kE4m3) {
-        uint32_t hi[NH / 4], lo[NH / 4];
-        two_terms_e4m3<NH>(w, hi, lo);
-        if constexpr (NH == 8)
-          st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
-        else
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(my_p), "r"(hi[0]), "r"(lo[0])
-                       : "memory");
-      } else {
-        uint32_t hi[NH / 2], lo[NH / 2];
-        two_terms_bf16<NH>(w, hi, lo);
-        if constexpr (NH == 8) {
-          st_shared16(my_p, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          st_shared16(my_p + kTile * 16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half) {
+        const uint32_t my_p = p_s + buf * Ge::kP + (tid + 128 * half) * 16;
+        if constexpr (kE4m3) {
+          uint32_t hi[NH / 4], lo[NH / 4];
+          two_terms_e4m3<NH>(w[half], hi, lo);
+          if constexpr (NH == 8)
+            st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+          else
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(my_p), "r"(hi[0]), "r"(lo[0])
+                         : "memory");
         } else {
-          st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+          uint32_t hi[NH / 2], lo[NH / 2];
+          two_terms_bf16<NH>(w[half], hi, lo);
+          if constexpr (NH == 8) {
+            st_shared16(my_p, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_shared16(my_p + kTile * 16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          } else {
+            st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+          }
         }
       }
       // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
@@ -825,12 +876,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       if (t.lo > 0 || t.hi < kTile) {
         const int slot = (2 * n + 1) % S;
         if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
-        if (!inside)
 #pragma unroll
-          for (int i = 0; i < Ge::kRow / 16; ++i)
-            st_shared16(ring + slot * Ge::kTensor + (i * 16 / Ge::kWide) * Ge::kSlab +
-                            tid * Ge::kWide + (i * 16) % Ge::kWide,
-                        make_uint4(0u, 0u, 0u, 0u));
+        for (int half = 0; half < kHalves; ++half)
+          if (!inside[half])
+#pragma unroll
+            for (int i = 0; i < Ge::kRow / 16; ++i)
+              st_shared16(ring + slot * Ge::kTensor + (i * 16 / Ge::kWide) * Ge::kSlab +
+                              (tid + 128 * half) * Ge::kWide + (i * 16) % Ge::kWide,
+                          make_uint4(0u, 0u, 0u, 0u));
       }
       if (t.flags & kLast) {
 #pragma unroll
@@ -852,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     // D = 64: an M of 64 puts row 16 w + i into lane i < 16 of warp w's quarter.
     const int w4 = warp - 4, dim = D == 128 ? 32 * w4 + lane : 16 * w4 + lane;
     const bool mine_too = D == 128 || lane < 16;
-    const uint32_t my_o = tmem + ((uint32_t)(32 * w4) << 16) + kOCol;
+    const uint32_t my_o = tmem + ((uint32_t)(32 * w4) << 16) + Ge::kOCol;
     uint8_t *slots = workspace + kSlotsOffset;
     int *counters = reinterpret_cast<int *>(workspace + kWsHeaderBytes);
     const size_t slot_size = slot_bytes(G, D);
@@ -864,6 +917,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       mbar_arrive(bar_meet);
       return wait.all(bar_meet, met++ & 1);
     };
+    // sequences without tokens are nobody's tiles: their zeros
+    for (int b = piece; b < a.B; b += P)
+      if (seq_of<kTile>(a, b).tiles == 0)
+        for (int i = tid - 128; i < a.Hq * D / 8; i += 128)
+          reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int n = 0;; ++n) {
       const int d = n % ND, buf = n & 1;
       const uint32_t phase = (n >> 1) & 1;
@@ -950,17 +1008,21 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         if (h < G && mine_too) reinterpret_cast<float *>(part)[h * D + dim] = acc[h];
       if (w4 == 0 && lane < G)
         reinterpret_cast<float2 *>(part + (size_t)G * D * 4)[lane] = make_float2(top, l);
-      __threadfence();
       if (!meet()) break;
+      const int first = (unsigned)t.unit / (unsigned)blk;
+      const int last = (unsigned)(t.unit + t.tiles - 1) / (unsigned)blk;
       if (tid == 128) {
-        const bool all = atomicAdd(counters + t.first, 1) == t.last - t.first;
-        if (all) counters[t.first] = 0;  // as the next call wants it
-        __threadfence();
-        s_joins = all;
+        __threadfence();  // (the four warps' stores, which it has met)
+        const bool all_there = atomicAdd(counters + first, 1) == last - first;
+        if (all_there) {
+          counters[first] = 0;  // as the next call wants it
+          __threadfence();
+        }
+        s_joins = all_there;
       }
       if (!meet()) break;
       if (s_joins)
-        join<D>(slots, t.first, t.last, G, a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D);
+        join<D>(slots, first, last, G, a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D);
       if (!meet()) break;
     }
   }
@@ -999,9 +1061,10 @@ cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs 
 // As many CTAs as the SMs hold, or fewer when there are not as many tiles.
 int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts, int sms) {
   if (num_parts > 0) return num_parts;
-  const int per = D == 128 ? (e4m3 ? Geo<128, true>::kCtas : Geo<128, false>::kCtas)
-                           : (e4m3 ? Geo<64, true>::kCtas : Geo<64, false>::kCtas);
-  const long long tiles = (long long)B * Hkv * ((max_len + kTile - 1) / kTile + 1);
+  auto of = [](auto geo) { return std::pair<int, int>(decltype(geo)::kCtas, decltype(geo)::kTile); };
+  const auto [per, tile] = D == 128 ? (e4m3 ? of(Geo<128, true>{}) : of(Geo<128, false>{}))
+                                    : (e4m3 ? of(Geo<64, true>{}) : of(Geo<64, false>{}));
+  const long long tiles = (long long)B * Hkv * ((max_len + tile - 1) / tile + 1);
   const long long most = per * sms < kPagedMaxParts ? per * sms : kPagedMaxParts;
   return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
