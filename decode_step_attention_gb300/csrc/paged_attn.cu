@@ -19,8 +19,8 @@
 //
 // The tiles (128 tokens) of all (sequence, KV head) pairs form one stream, cut into equal pieces, one
 // per CTA (one per SM). A pair that lies in several pieces leaves a partial in each (O, maximum, sum,
-// fp32); the CTA that delivers a pair's last partial joins them, in the order of the pieces, so
-// that results do not depend on who that is. Counters are indexed by the piece in which a pair
+// fp32); the CTA that delivers a pair's last partial joins them when its own piece is done, in the
+// order of the pieces, so that results do not depend on who that is. Counters are indexed by the piece in which a pair
 // begins (one at most goes on from a piece), not by the pair, so that they lie in the same place
 // for every shape and a workspace may serve several.
 //
@@ -50,7 +50,6 @@ namespace {
 constexpr int kG = kSplitMaxG;
 constexpr int kN = 16;       // columns of the products: two terms of each of up to 8 heads
 constexpr int kThreads = 384;
-constexpr int kWarps = kThreads / 32;
 constexpr int kTma = 8, kQuery = 9, kScore = 10, kValue = 11;  // warps
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCols = 4 * kN;       // an O buffer: 16 columns for each warp of tokens
@@ -184,13 +183,6 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
-  return __half22float2(
-      __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
-}
 // Values of at most 448, each as hi + lo / 16, both e4m3: the second term's own factor keeps it clear of
 // e4m3's smallest steps. Four codes to a word.
 constexpr float kLow = 1.f / 16;
@@ -251,6 +243,9 @@ __device__ __forceinline__ void tmem_wait(float (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 __device__ __forceinline__ void st_shared16(uint32_t at, uint4 x) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z),
                "r"(x.w)
@@ -276,51 +271,6 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   s.tiles = s.L > s.start ? (s.L + kTile - 1) / kTile - s.tile0 : 0;
   return s;
 }
-// The partials of a pair of pieces first .. last into its G rows of the output, by 128 threads: 4
-// neighbouring dims of a head each, the partials' loads in flight kAtOnce at a time.
-template <int D>
-__device__ __forceinline__ void join(const uint8_t *slots, int first, int last, int G,
-                                     __nv_bfloat16 *out) {
-  constexpr int kAtOnce = 8;
-  const size_t slot = slot_bytes(G, D);
-  for (int i = threadIdx.x & 127; i < G * (D / 4); i += 128) {
-    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-    float M = -INFINITY, sum = 0.f, o[4] = {};
-    for (int c0 = first; c0 <= last; c0 += kAtOnce) {
-      float4 x[kAtOnce];
-      float2 ml[kAtOnce];
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int c = min(c0 + u, last);
-        const uint8_t *p = slots + (size_t)(2 * c + (c == first)) * slot;
-        x[u] = __ldcg(reinterpret_cast<const float4 *>(p + ((size_t)h * D + d) * 4));
-        ml[u] = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)G * D * 4) + h);
-      }
-      float to = M;
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) to = fmaxf(to, ml[u].x);
-      const float base = to == -INFINITY ? 0.f : to, f = ex2(M - base);
-      M = to;
-      sum *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] *= f;
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        if (c0 + u > last) break;
-        const float g = ex2(ml[u].x - base);
-        sum = fmaf(ml[u].y, g, sum);
-        o[0] = fmaf(x[u].x, g, o[0]);
-        o[1] = fmaf(x[u].y, g, o[1]);
-        o[2] = fmaf(x[u].z, g, o[2]);
-        o[3] = fmaf(x[u].w, g, o[3]);
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(out + (size_t)h * D + d) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  }
-}
-
 template <int D, bool kE4m3, int NH>
 __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedCache c,
@@ -338,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   __shared__ __align__(16) float s_f[4][5 * kG];        // factors, per warp of dimensions
   __shared__ int2 s_seg[4];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_joins, s_begin[2];
-  __shared__ int2 s_warp_units[kWarps];
+  __shared__ int s_abort, s_blk, s_parts, s_joins[2];
+  __shared__ int4 s_part[2];                   // pairs that the piece leaves a partial of
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_addr(smem), q_s = ring + S * Ge::kTensor, p_s = q_s + 2 * Ge::kQ;
@@ -347,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   const uint32_t bar_desc = bar_empty + 8 * S, bar_s = bar_desc + 8 * ND, bar_p = bar_s + 16;
   const uint32_t bar_o = bar_p + 16, bar_free = bar_o + 16, bar_q = bar_free + 16;
   const uint32_t bar_qfree = bar_q + 32, bar_end = bar_qfree + 16, bar_sum = bar_end + 16;
-  const uint32_t bar_seg = bar_sum + 32, bar_segfree = bar_seg + 32, bar_meet = bar_segfree + 32;
+  const uint32_t bar_seg = bar_sum + 32, bar_segfree = bar_seg + 32, bar_join = bar_segfree + 32;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = a.Hq / c.Hkv;
 
@@ -355,17 +305,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   // before have seen that: each role's waits say so, those for the end of the piece included.)
   if (tid < 2 * S + ND + 33) {
     const uint32_t bar = bar_full + 8 * tid;
-    const bool many = (bar >= bar_p && bar < bar_o) || (bar >= bar_free && bar < bar_q) || bar == bar_meet;
+    const bool many = (bar >= bar_p && bar < bar_o) || (bar >= bar_free && bar < bar_q);
     mbar_init(bar, bar >= bar_desc && bar < bar_s ? (kE4m3 ? 33 : 1)
                    : many                         ? 128
                    : bar >= bar_sum && bar < bar_seg ? 4
                                                      : 1);
     fence_barrier_init();
   }
-  if (tid == 0) {
-    s_abort = 0;
-    s_begin[0] = -1;
-  }
+  if (tid == 0) s_abort = s_parts = 0;
   if (warp == kTma) {
     if (lane == 0) {
       tma_prefetch_desc(&maps.k);
@@ -376,56 +323,13 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   // rows of Q that no head fills stay zero, and so do the weights' unused columns
   for (int i = tid; i < 2 * (Ge::kQ + Ge::kP) / 16; i += kThreads)
     st_shared16(q_s + 16 * i, make_uint4(0u, 0u, 0u, 0u));
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-
-  // ---- where this CTA's piece begins: a scan over the sequences, a run of them per thread
-  const int P = gridDim.x, piece = blockIdx.x;
-  const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads, b_first = tid * per;
-  const int b_last = min(a.B, b_first + per);
-  int2 mine = make_int2(0, 0);  // tiles, pairs
-  for (int b = b_first; b < b_last; ++b) {
-    const Seq s = seq_of<kTile>(a, b);
-    mine.x += s.tiles * c.Hkv;
-    mine.y += s.tiles > 0 ? c.Hkv : 0;
-    if (piece == 0 && s.L != a.lens[b]) atomicOr(a.error_word, kErrLenClamped);
-  }
-  int2 incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-    if (lane >= o) incl.x += x, incl.y += y;
-  }
-  if (lane == 31) s_warp_units[warp] = incl;
   fence_proxy_async_smem();  // (the zeros)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int2 before = make_int2(0, 0), all = before;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int2 u = s_warp_units[w];
-    if (w < warp) before.x += u.x, before.y += u.y;
-    all.x += u.x, all.y += u.y;
-  }
-  const int segment = all.x >= kFew * P ? kSegment : 0;
-  const int total = all.x + segment * all.y;
-  const int blk = max(1u, ((unsigned)total + P - 1) / (unsigned)P);
-  const long long r0 = (long long)piece * blk;
-  const int count = mine.x + segment * mine.y;
-  int at = before.x + incl.x + segment * (before.y + incl.y) - count;
-  if (at <= r0 && r0 < at + count) {
-    int b = b_first;
-    for (;; ++b) {
-      const Seq s = seq_of<kTile>(a, b);
-      const int u = s.tiles > 0 ? (s.tiles + segment) * c.Hkv : 0;
-      if (r0 < at + u) break;
-      at += u;
-    }
-    s_begin[0] = b;
-    s_begin[1] = (int)r0 - at;
-  }
-  __syncthreads();
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int P = gridDim.x, piece = blockIdx.x;
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   const Waiter wait{&s_abort, a.error_word};
 
@@ -435,10 +339,48 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     const int ppt_log2 = (kHalves == 2 ? 8 : 7) - page_log2;
     const int batch = 32 >> ppt_log2;  // tiles whose page numbers the lanes hold
     const uint64_t policy = l2_policy_evict_first();
+    // Where this piece begins: a scan over the sequences, a run of them per lane.
+    const int per = (a.B + 31) >> 5, b_first = min(a.B, lane * per), b_last = min(a.B, b_first + per);
+    int2 mine = make_int2(0, 0);  // tiles, pairs
+#pragma unroll 4
+    for (int i = b_first; i < b_last; ++i) {
+      const int tiles = seq_of<kTile>(a, i).tiles;
+      mine.x += tiles;
+      mine.y += tiles > 0;
+    }
+    mine.x *= c.Hkv, mine.y *= c.Hkv;
+    int2 incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) incl.x += x, incl.y += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, incl.x, 31), pairs = __shfl_sync(0xffffffffu, incl.y, 31);
+    const int segment = all >= kFew * P ? kSegment : 0, total = all + segment * pairs;
+    const int blk = max(1u, ((unsigned)total + P - 1) / (unsigned)P);
+    const long long r0 = (long long)piece * blk;
+    if (lane == 0) s_blk = blk;  // (for the end of a segment that is not a whole pair)
     // the walk: (b, g), its tiles t0 .. t1 of this piece (from the sequence's first seen one), and
     // those of them that the lanes have looked up
-    int b = s_begin[0], g = 0, left = 0, t0 = 0, t1 = 0, off = 0;
+    int b = -1, g = 0, left = 0, t0 = 0, t1 = 0, off = 0, within = 0;
     Seq s{};
+    {
+      const int count = mine.x + segment * mine.y;
+      int at = incl.x + segment * incl.y - count;
+      if (at <= r0 && r0 < at + count) {
+        for (b = b_first;; ++b) {
+          const Seq x = seq_of<kTile>(a, b);
+          const int u = x.tiles > 0 ? (x.tiles + segment) * c.Hkv : 0;
+          if (r0 < at + u) break;
+          at += u;
+        }
+        within = (int)r0 - at;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, b >= 0);
+      const int from = who != 0 ? __ffs(who) - 1 : 0;
+      b = __shfl_sync(0xffffffffu, b, from);
+      within = __shfl_sync(0xffffffffu, within, from);
+    }
     auto take = [&](int from) {  // from: units of this pair that lie before the piece
       t0 = max(0, from - segment);
       t1 = max(t0, min(s.tiles, from + left - segment));
@@ -448,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     if (more) {
       s = seq_of<kTile>(a, b);
       const int u = s.tiles + segment;
-      g = (unsigned)s_begin[1] / (unsigned)u;
-      const int from = s_begin[1] - g * u;
+      g = (unsigned)within / (unsigned)u;
+      const int from = within - g * u;
       off = (int)r0 - from;
       left = (int)min((long long)blk, total - r0);
       take(from);
@@ -906,22 +848,17 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     const int w4 = warp - 4, dim = D == 128 ? 32 * w4 + lane : 16 * w4 + lane;
     const bool mine_too = D == 128 || lane < 16;
     const uint32_t my_o = tmem + ((uint32_t)(32 * w4) << 16) + Ge::kOCol;
-    uint8_t *slots = workspace + kSlotsOffset;
-    int *counters = reinterpret_cast<int *>(workspace + kWsHeaderBytes);
-    const size_t slot_size = slot_bytes(G, D);
     float acc[NH];
     float top = -INFINITY;  // the running maximum of the bases of head lane & 7
-    int seg = -1, met = 0;
-    // the four warps together (a bounded wait: one of them may have given up)
-    auto meet = [&]() {
-      mbar_arrive(bar_meet);
-      return wait.all(bar_meet, met++ & 1);
-    };
+    int seg = -1;
     // sequences without tokens are nobody's tiles: their zeros
-    for (int b = piece; b < a.B; b += P)
-      if (seq_of<kTile>(a, b).tiles == 0)
+    for (int b = piece; b < a.B; b += P) {
+      const Seq x = seq_of<kTile>(a, b);
+      if (tid == 128 && x.L != a.lens[b]) atomicOr(a.error_word, kErrLenClamped);
+      if (x.tiles == 0)
         for (int i = tid - 128; i < a.Hq * D / 8; i += 128)
           reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
     for (int n = 0;; ++n) {
       const int d = n % ND, buf = n & 1;
       const uint32_t phase = (n >> 1) & 1;
@@ -1002,28 +939,14 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         }
         continue;
       }
-      uint8_t *part = slots + (size_t)t.slot * slot_size;
+      uint8_t *part = workspace + kSlotsOffset + (size_t)t.slot * slot_bytes(G, D);
 #pragma unroll
       for (int h = 0; h < NH; ++h)
         if (h < G && mine_too) reinterpret_cast<float *>(part)[h * D + dim] = acc[h];
       if (w4 == 0 && lane < G)
         reinterpret_cast<float2 *>(part + (size_t)G * D * 4)[lane] = make_float2(top, l);
-      if (!meet()) break;
-      const int first = (unsigned)t.unit / (unsigned)blk;
-      const int last = (unsigned)(t.unit + t.tiles - 1) / (unsigned)blk;
-      if (tid == 128) {
-        __threadfence();  // (the four warps' stores, which it has met)
-        const bool all_there = atomicAdd(counters + first, 1) == last - first;
-        if (all_there) {
-          counters[first] = 0;  // as the next call wants it
-          __threadfence();
-        }
-        s_joins = all_there;
-      }
-      if (!meet()) break;
-      if (s_joins)
-        join<D>(slots, first, last, G, a.out + ((size_t)t.b * a.Hq + (size_t)t.g * G) * D);
-      if (!meet()) break;
+      fence_proxy_async_global();  // (they are read by bulk copies)
+      if (tid == 128) s_part[s_parts++] = make_int4(t.unit, t.tiles, t.b, t.g);
     }
   }
   tc_fence_before();
@@ -1031,6 +954,69 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   if (warp == kTma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  // ---- a pair whose last partial this piece delivers is joined here
+  const int parts = s_parts;
+  if (parts == 0 || s_abort) return;
+  if (tid < parts) {
+    const int4 x = s_part[tid];
+    const int first = (unsigned)x.x / (unsigned)s_blk, last = (unsigned)(x.x + x.y - 1) / (unsigned)s_blk;
+    int *counter = reinterpret_cast<int *>(workspace + kWsHeaderBytes) + first;
+    __threadfence();  // the CTA's stores, which the barrier has gathered
+    const bool all_there = atomicAdd(counter, 1) == last - first;
+    if (all_there) *counter = 0;  // as the next call wants it
+    __threadfence();
+    fence_proxy_async_global();
+    s_joins[tid] = all_there;
+  }
+  __syncthreads();
+  // out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c in the order of the pieces: the partials come by
+  // bulk copies into the ring, as many at a time as it holds, 4 neighbouring dims of a head a thread.
+  const uint32_t slot = (uint32_t)slot_bytes(G, D);
+  const int room = min(32, (int)(S * Ge::kTensor / slot));
+  const int h = tid / (D / 4), dim4 = tid - h * (D / 4);
+  uint32_t phase = 0;
+  for (int i = 0; i < parts; ++i) {
+    if (!s_joins[i]) continue;
+    const int4 x = s_part[i];
+    const int first = (unsigned)x.x / (unsigned)s_blk, last = (unsigned)(x.x + x.y - 1) / (unsigned)s_blk;
+    float M = -INFINITY, sum = 0.f, o[4] = {};
+    for (int c0 = first; c0 <= last; c0 += room) {
+      const int n = min(room, last + 1 - c0);
+      if (warp == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(bar_join, n * slot);
+        __syncwarp();
+        if (lane < n)
+          bulk_load(ring + lane * slot,
+                    workspace + kSlotsOffset + (size_t)(2 * (c0 + lane) + (c0 + lane == first)) * slot,
+                    slot, bar_join);
+      }
+      if (!mbar_wait_bounded(bar_join, phase)) atomicOr(a.error_word, kErrWaitTimeout);
+      phase ^= 1;
+      if (h < G) {
+        const uint8_t *p = smem;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k, p += slot) {
+          const float4 y = reinterpret_cast<const float4 *>(p)[tid];
+          const float2 ml = reinterpret_cast<const float2 *>(p + (size_t)G * D * 4)[h];
+          const float to = fmaxf(M, ml.x), base = to == -INFINITY ? 0.f : to;
+          const float f = ex2(M - base), w = ex2(ml.x - base);
+          M = to;
+          sum = fmaf(sum, f, ml.y * w);
+          o[0] = fmaf(o[0], f, y.x * w);
+          o[1] = fmaf(o[1], f, y.y * w);
+          o[2] = fmaf(o[2], f, y.z * w);
+          o[3] = fmaf(o[3], f, y.w * w);
+        }
+      }
+      __syncthreads();
+    }
+    if (h < G) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      __nv_bfloat16 *out = a.out + ((size_t)x.z * a.Hq + (size_t)x.w * G + h) * D + 4 * dim4;
+      *reinterpret_cast<uint2 *>(out) =
+          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    }
   }
 }
 
