@@ -23,7 +23,7 @@ namespace decattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 4;
 constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest
 
 // A row (token, head) is D / 16 lanes; a lane has two groups of 8 elements, u and v, of which u[j]
@@ -72,6 +72,26 @@ struct Row {
     }
   }
 };
+
+// sin and cos of position p's angle: p * turns modulo 2^64 is its fraction of a turn, the nearest quarter
+// turn goes off in integers, and the Taylor series run to x^9 and x^8 at |x| <= pi / 4 (the next terms are
+// below 2e-9 and 3e-8). Half the instructions of a general sincosf, whose reduction is not needed.
+__device__ __forceinline__ void quick_sincos(int p, unsigned long long turns, float &s, float &c) {
+  const unsigned hi = (unsigned)(((unsigned long long)(unsigned)p * turns) >> 32);
+  const unsigned quarter = (hi + (1u << 29)) >> 30;
+  const float x = (float)(int)(hi - (quarter << 30)) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  const float z = x * x;
+  float a = fmaf(z, 1.f / 362880.f, -1.f / 5040.f), b = fmaf(z, 1.f / 40320.f, -1.f / 720.f);
+  a = fmaf(a, z, 1.f / 120.f);
+  b = fmaf(b, z, 1.f / 24.f);
+  a = fmaf(a, z, -1.f / 6.f);
+  b = fmaf(b, z, -0.5f);
+  a = fmaf(a * z, x, x);
+  b = fmaf(b, z, 1.f);
+  const float sn = quarter & 1 ? b : a, cs = quarter & 1 ? a : b;
+  s = quarter & 2 ? -sn : sn;
+  c = (quarter + 1) & 2 ? -cs : cs;
+}
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -126,8 +146,8 @@ struct AppendArgs {
   long long q_ld, qo_ld, k_ld, v_ld;
   int n, B, num_pages, page_log2, max_pages, Hq, Hkv, rot;
   float eps;
-  // tokens and heads of a block of rows; the blocks of them, and the tokens of a block of runs
-  int tok_par, heads_per, row_blocks, head_blocks, chunk;
+  // tokens and heads of a block of rows, and the blocks of them
+  int tok_par, heads_per, row_blocks, head_blocks;
 };
 
 // Where token i goes: its sequence, its position, and the page's number (-1: nowhere).
@@ -174,21 +194,19 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int i) {
   return p;
 }
 
-// One row of q or k in a lane's registers: normed and rotated.
-template <int D, bool kInterleaved>
+// A lane's part of a row, normed and rotated.
 struct Turned {
-  float u[8], v[8];    // the result
-  float rstd;
-  uint4 x, y;          // as loaded
+  float u[8], v[8];
 };
 
-template <int D, bool kInterleaved>
-__device__ __forceinline__ void turn(Turned<D, kInterleaved> &t, bool norm, uint4 wa, uint4 wb,
-                                     float eps, bool rotated, const float (&cs)[8],
-                                     const float (&sn)[8]) {
+// From the elements as loaded (x, y; wa, wb: the norm's weights). kBits: the elements whose rotation
+// cancels so far that fp32 leaves them more than half a bf16 step off (u, then v).
+template <int D, bool kInterleaved, bool kBits>
+__device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm, uint4 wa, uint4 wb,
+                                         float eps, bool rotated, const float (&cs)[8],
+                                         const float (&sn)[8], float &rstd) {
   using R = Row<D, kInterleaved>;
-  R::unpack(t.x, t.y, t.u, t.v);
-  t.rstd = 1.f;
+  R::unpack(x, y, t.u, t.v);
   if (norm) {
     float su = 0.f, sv = 0.f;
 #pragma unroll
@@ -199,74 +217,28 @@ __device__ __forceinline__ void turn(Turned<D, kInterleaved> &t, bool norm, uint
     su += sv;
 #pragma unroll
     for (int o = R::kLanes / 2; o > 0; o >>= 1) su += __shfl_xor_sync(0xffffffffu, su, o);
-    t.rstd = rsqrtf(su * (1.0f / (float)D) + eps);
+    rstd = rsqrtf(su * (1.0f / (float)D) + eps);
     float p[8], q[8];
     R::unpack(wa, wb, p, q);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      t.u[j] = t.u[j] * t.rstd * p[j];
-      t.v[j] = t.v[j] * t.rstd * q[j];
+      t.u[j] = t.u[j] * rstd * p[j];
+      t.v[j] = t.v[j] * rstd * q[j];
     }
   }
+  unsigned bits = 0;
   if (rotated) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float p = t.u[j], q = t.v[j];
       t.u[j] = rope_first(p, q, cs[j], sn[j]);
       t.v[j] = rope_second<false>(p, q, cs[j], sn[j]);
+      if (kBits)
+        bits |= (rope_cancels(t.u[j], p, q) ? 1u << j : 0u) |
+                (rope_cancels(t.v[j], p, q) ? 0x100u << j : 0u);
     }
   }
-}
-
-// One element of a rotated pair (or one that is not rotated), before the norm's scale, in fp64.
-__device__ __noinline__ double exact_element(int pos, unsigned long long turns, float own,
-                                             float other, bool second, bool rotated) {
-  return rotated ? rope_element_turns(pos, turns, own, other, second) : (double)own;
-}
-
-// Elements of a key whose fp32 value does not settle the stored one (bits of this lane's 16: u, then
-// v), again in fp64 from the stored inputs: u and v get convert(value). The warp comes together; rare.
-template <int D, bool kInterleaved, typename Convert>
-__device__ __forceinline__ void exact_elements(const Turned<D, kInterleaved> &t, uint4 wa, uint4 wb,
-                                               bool norm, float eps, bool rotated, int pos, int l,
-                                               const unsigned long long *turns, unsigned bits,
-                                               float (&u)[8], float (&v)[8], Convert convert) {
-  using R = Row<D, kInterleaved>;
-  if (!__any_sync(0xffffffffu, bits != 0)) return;
-  float x[8], y[8];
-  R::unpack(t.x, t.y, x, y);
-  double rstd = 1.0;
-  if (norm) {  // (the same for the whole warp)
-    double ss = 0.0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fma((double)x[j], (double)x[j], fma((double)y[j], (double)y[j], ss));
-#pragma unroll
-    for (int o = R::kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    rstd = 1.0 / sqrt(ss / D + (double)eps);
-    float p[8], q[8];
-    R::unpack(wa, wb, p, q);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= p[j], y[j] *= q[j];  // (exact products of two bf16)
-  }
-  do {
-    if (bits != 0) {
-      const int i = __ffs(bits) - 1;
-      bits &= bits - 1;
-      float first = 0.f, other = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((i & 7) == j) first = x[j], other = y[j];
-      const bool second = i >= 8;
-      const float z = convert(exact_element(pos, turns[8 * l + (i & 7)], second ? other : first,
-                                            second ? first : other, second, rotated) *
-                              rstd);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (i == j) u[j] = z;
-        if (i == 8 + j) v[j] = z;
-      }
-    }
-  } while (__any_sync(0xffffffffu, bits != 0));
+  return bits;
 }
 
 // A double as the float that e4m3's rounding takes the same way: what is cut off leaves its mark in
@@ -276,35 +248,94 @@ __device__ __forceinline__ float sticky(double x) {
   return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// How far fp32 may have moved a value of a row that was normed or rotated: a few 2^-24 of its terms.
-constexpr float kSlack = 0x1p-20f;
+// Elements of a key whose fp32 value does not settle the stored one (bits of this lane's 16: u, then
+// v), again in fp64 from the inputs, and written over. The whole warp calls it; rare. A bf16 value takes
+// the row's fp32 norm (1 without it), a code the exact one, whose sum of squares the warp forms
+// together (by one lane, 8 us of a small call).
+template <int D, bool kInterleaved, bool kE4m3>
+__device__ __noinline__ void exact_elements(const __nv_bfloat16 *src, const __nv_bfloat16 *w,
+                                            void *dst, float scale_or_rstd, float eps, int pos, int rot,
+                                            const unsigned long long *turns, unsigned bits) {
+  const int lane = threadIdx.x & 31, l = lane % Row<D, kInterleaved>::kLanes;
+  double factor;  // the norm, and the scale's inverse
+  if (kE4m3) {
+    const double s = (double)scale_or_rstd, inv = (double)(1.f / scale_or_rstd);
+    factor = inv * fma(-s, inv, 2.0);  // (a power of two's is exact before)
+    if (w != nullptr) {
+      for (unsigned who = __ballot_sync(0xffffffffu, bits != 0); who != 0; who &= who - 1) {
+        const int from = __ffs(who) - 1;
+        const __nv_bfloat16 *row = reinterpret_cast<const __nv_bfloat16 *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const double x = (double)__bfloat162float(row[lane + 32 * j]);
+          ss = fma(x, x, ss);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const double mean = fma(ss, 1.0 / D, (double)eps);
+        const double r = (double)rsqrtf((float)mean);  // (one step from 2^-22 to 2^-43)
+        if (lane == from) factor *= r * fma(-0.5 * mean * r, r, 1.5);
+      }
+    }
+  } else {
+    factor = (double)scale_or_rstd;
+  }
+  int ea, eb;
+  Row<D, kInterleaved>::places(l, rot, ea, eb);
+  const bool rotated = l < (rot >> 4);
+  for (; bits != 0; bits &= bits - 1) {
+    const int i = __ffs(bits) - 1, j = i & 7;
+    const bool second = i >= 8;
+    const int first_at = kInterleaved ? ea + 2 * j : ea + j;
+    const int second_at = kInterleaved ? ea + 2 * j + 1 : eb + j;
+    const int own_at = second ? second_at : first_at, other_at = second ? first_at : second_at;
+    float own = __bfloat162float(src[own_at]), other = __bfloat162float(src[other_at]);
+    if (w != nullptr) {  // (exact products of two bf16)
+      own *= __bfloat162float(w[own_at]);
+      other *= __bfloat162float(w[other_at]);
+    }
+    const double value =
+        (rotated ? rope_element_turns(pos, turns[8 * l + j], own, other, second) : (double)own) *
+        factor;
+    if (kE4m3)
+      static_cast<uint8_t *>(dst)[own_at] = (uint8_t)e4m3x2(sticky(value), 0.f);
+    else
+      static_cast<__nv_bfloat16 *>(dst)[own_at] = __float2bfloat16((float)value);
+  }
+}
 
-// The codes of a lane's 16 values. Where a warp has keys that were normed or rotated (inexact, norm:
-// the same for the whole warp), a value of one (key) so near a border between two codes that the fp32
-// arithmetic before it could have moved it across is formed again in fp64: the codes are the
-// exact key's.
+// How far fp32 may have moved a value of a row that was normed and rotated, of its pair's magnitudes: the
+// angle's and the series' roundings 3.5 2^-24, the rotation's 2 2^-24, the norm's 9.5 2^-24 (its sum of
+// 128 squares at most 11 halved, rsqrt 4 halved, two products).
+constexpr float kSlack = 15 * 0x1p-24f;
+
+// The codes of a lane's 16 values. check: also the values so near a border between two codes that
+// the fp32 arithmetic before could have moved them across.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ void encode(const Turned<D, kInterleaved> &t, const Unscale &un,
-                                       uint4 wa, uint4 wb, bool inexact, bool norm, float eps,
-                                       bool rotated, int pos, int l,
-                                       const unsigned long long *turns, bool key, uint2 &a,
-                                       uint2 &b) {
+__device__ __forceinline__ unsigned encode(const Turned &t, const Unscale &un, bool check, uint2 &a,
+                                           uint2 &b) {
   using R = Row<D, kInterleaved>;
   float u[8], v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) u[j] = un(t.u[j]), v[j] = un(t.v[j]);
-  if (inexact) {
-    unsigned bits = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
+  unsigned bits = 0;
+  if (check) {
+    uint32_t any = 0;
+    auto off = [&](int j) {
       const float d = kSlack * (fabsf(u[j]) + fabsf(v[j]));
-      const uint32_t off = e4m3x2(u[j] - d, v[j] - d) ^ e4m3x2(u[j] + d, v[j] + d);
-      // (-0 and +0 are no border, but counting them as one costs nothing)
-      bits |= (off & 0xffu ? 1u << j : 0u) | (off & 0xff00u ? 0x100u << j : 0u);
+      return e4m3x2(u[j] - d, v[j] - d) ^ e4m3x2(u[j] + d, v[j] + d);
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) any |= off(j);
+    if (any != 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = off(j);
+        bits |= (x & 0xffu ? 1u << j : 0u) | (x & 0xff00u ? 0x100u << j : 0u);
+      }
     }
-    exact_elements<D, kInterleaved>(
-        t, wa, wb, norm, eps, rotated, pos, l, turns, key ? bits : 0u, u, v,
-        [&](double value) { return sticky(value / (double)un.s); });
   }
   float f[16];
   R::order(u, v, f);
@@ -312,23 +343,29 @@ __device__ __forceinline__ void encode(const Turned<D, kInterleaved> &t, const U
                  e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
   b = make_uint2(e4m3x2(f[8], f[9]) | e4m3x2(f[10], f[11]) << 16,
                  e4m3x2(f[12], f[13]) | e4m3x2(f[14], f[15]) << 16);
+  return bits;
 }
 
-template <int D, bool kInterleaved>
-__device__ __forceinline__ float amax_of(const Turned<D, kInterleaved> &t) {
+// The largest magnitude of a lane's values; the finite ones', once there is one that is not.
+__device__ __forceinline__ float amax_of(const Turned &t) {
   float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(finite_abs(t.u[j]), finite_abs(t.v[j])));
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(t.u[j]), fabsf(t.v[j])));
+  if (m == INFINITY) {
+    m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(finite_abs(t.u[j]), finite_abs(t.v[j])));
+  }
   return m;
 }
 
 // ---- rows: (token, head) pairs that need nothing of each other ------------------------------
 // Heads are counted q, k, v. A block has tok_par tokens side by side, times as many heads as fit,
 // and goes through its heads_per heads with them: a lane keeps its token's angles.
-template <int D, bool kInterleaved, bool kE4m3>
-__device__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) {
+template <int D, bool kInterleaved, bool kE4m3, int kBlock>
+__device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) {
   using R = Row<D, kInterleaved>;
-  constexpr int kRows = kThreads / R::kLanes;
+  constexpr int kRows = kBlock / R::kLanes;
   const int lane = threadIdx.x & 31, l = lane % R::kLanes, row = threadIdx.x / R::kLanes;
   const int block = blockIdx.x % a.head_blocks, tile = blockIdx.x / a.head_blocks;
   const int i = tile * a.tok_par + (row & (a.tok_par - 1));
@@ -346,47 +383,56 @@ __device__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) 
   for (int j = 0; j < 8; ++j) {
     cs[j] = 1.f;
     sn[j] = 0.f;
-    if (rotated && some) rope_sincos_turns(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
-  }
-  uint4 wqa{}, wqb{}, wka{}, wkb{};
-  if (norm) {
-    wqa = *reinterpret_cast<const uint4 *>(a.q_norm_w + ea);
-    wqb = *reinterpret_cast<const uint4 *>(a.q_norm_w + eb);
-    wka = *reinterpret_cast<const uint4 *>(a.k_norm_w + ea);
-    wkb = *reinterpret_cast<const uint4 *>(a.k_norm_w + eb);
+    if (rotated && some) quick_sincos(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
   }
   const int in_page = at.pos & ((1 << a.page_log2) - 1);
+  // a head's two groups of this lane, on their way while the one before is turned
+  auto load = [&](int h, uint4 &x, uint4 &y) {
+    x = y = make_uint4(0u, 0u, 0u, 0u);
+    if (some && h < h1 && (h < a.Hq || at.page >= 0)) {
+      const __nv_bfloat16 *src = h < a.Hq ? a.q_in + i * a.q_ld + (size_t)h * D
+                                 : h < a.Hq + a.Hkv
+                                     ? a.k_new + i * a.k_ld + (size_t)(h - a.Hq) * D
+                                     : a.v_new + i * a.v_ld + (size_t)(h - a.Hq - a.Hkv) * D;
+      x = *reinterpret_cast<const uint4 *>(src + ea);
+      y = *reinterpret_cast<const uint4 *>(src + eb);
+    }
+  };
+  uint4 next_x, next_y;
+  load(h0 + row / a.tok_par, next_x, next_y);
   for (int hh = h0; hh < h1; hh += step) {  // (the same number of times in every lane)
     const int h = hh + row / a.tok_par;
     const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
     const int g = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hkv;
     const bool live = some && h < h1 && (is_q || at.page >= 0);
-    Turned<D, kInterleaved> t;
-    t.x = t.y = make_uint4(0u, 0u, 0u, 0u);
-    if (live) {
-      const __nv_bfloat16 *src = is_q   ? a.q_in + i * a.q_ld
-                                 : is_k ? a.k_new + i * a.k_ld
-                                        : a.v_new + i * a.v_ld;
-      src += (size_t)g * D;
-      t.x = *reinterpret_cast<const uint4 *>(src + ea);
-      t.y = *reinterpret_cast<const uint4 *>(src + eb);
-    }
+    Turned t;
+    const uint4 x = next_x, y = next_y;
+    if (hh + step < h1) load(h + step, next_x, next_y);
     const bool turns_here = is_q || is_k;
-    const uint4 wa = is_q ? wqa : wka, wb = is_q ? wqb : wkb;
-    if (turns_here || norm) {  // (a warp may hold values beside keys: the norm's shuffles)
-      turn(t, norm, wa, wb, a.eps, rotated, cs, sn);
+    uint4 wa{}, wb{};
+    if (norm) {
+      const __nv_bfloat16 *w = is_q ? a.q_norm_w : a.k_norm_w;
+      wa = *reinterpret_cast<const uint4 *>(w + ea);
+      wb = *reinterpret_cast<const uint4 *>(w + eb);
     }
-    if (!turns_here) R::unpack(t.x, t.y, t.u, t.v);
+    unsigned bits = 0;
+    float rstd = 1.f;
+    if (turns_here || norm)  // (a warp may hold values beside keys: the norm's shuffles)
+      bits = turn<D, kInterleaved, !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
+                                            rstd);
+    if (!turns_here) R::unpack(x, y, t.u, t.v);
     const size_t slot =
         live && !is_q
             ? ((((size_t)at.page * a.Hkv + g) << a.page_log2) + (size_t)in_page) * D
             : 0;
+    float scale = 1.f;
     if (kE4m3) {
       float m = amax_of(t);
 #pragma unroll
       for (int o = R::kLanes / 2; o > 0; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float scale = scale_for(m), old = scale;
+      scale = scale_for(m);
+      float old = scale;
       float *sp = (is_k ? a.k_scale : a.v_scale) + (live && !is_q ? (size_t)at.page * a.Hkv + g : 0);
       bool grows = false;
       if (live && !is_q && in_page > 0) {
@@ -409,33 +455,8 @@ __device__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) 
 #pragma unroll 4
         for (int k = lane; k < words; k += 32) w[k] = rescale16(w[k], ratio);
       }
-      uint2 ca, cb;
-      encode<D, kInterleaved>(t, Unscale(scale), wka, wkb, norm || a.rot > 0, norm, a.eps, rotated,
-                              at.pos, l, turns.v, live && is_k, ca, cb);
-      if (live && !is_q) {
-        uint8_t *dst = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + slot;
-        *reinterpret_cast<uint2 *>(dst + ea) = ca;
-        *reinterpret_cast<uint2 *>(dst + eb) = cb;
-      }
-    } else if (__any_sync(0xffffffffu, live && is_k)) {
-      // keys within one bf16 step where the rotation cancels
-      float u[8], v[8];
-      R::unpack(t.x, t.y, u, v);
-      unsigned bits = 0;
-      if (live && is_k && rotated) {
-        float p[8], q[8];
-        R::unpack(wka, wkb, p, q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = norm ? u[j] * t.rstd * p[j] : u[j];
-          const float y = norm ? v[j] * t.rstd * q[j] : v[j];
-          bits |= (rope_cancels(t.u[j], x, y) ? 1u << j : 0u) |
-                  (rope_cancels(t.v[j], x, y) ? 0x100u << j : 0u);
-        }
-      }
-      exact_elements<D, kInterleaved>(t, wka, wkb, norm, a.eps, rotated, at.pos, l, turns.v, bits,
-                                      t.u, t.v, [](double value) { return (float)value; });
     }
+    void *dst = nullptr;
     if (live && (is_q || !kE4m3)) {
       float f[16];
       R::order(t.u, t.v, f);
@@ -443,12 +464,26 @@ __device__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) 
                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
       uint4 ob = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
                             pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-      if (!turns_here) oa = t.x, ob = t.y;  // a copy, bit for bit
-      __nv_bfloat16 *dst = is_q ? a.q_out + i * a.qo_ld + (size_t)g * D
-                                : static_cast<__nv_bfloat16 *>(is_k ? a.k_pages : a.v_pages) + slot;
-      *reinterpret_cast<uint4 *>(dst + ea) = oa;
-      *reinterpret_cast<uint4 *>(dst + eb) = ob;
+      if (!turns_here) oa = x, ob = y;  // a copy, bit for bit
+      __nv_bfloat16 *to = is_q ? a.q_out + i * a.qo_ld + (size_t)g * D
+                               : static_cast<__nv_bfloat16 *>(is_k ? a.k_pages : a.v_pages) + slot;
+      *reinterpret_cast<uint4 *>(to + ea) = oa;
+      *reinterpret_cast<uint4 *>(to + eb) = ob;
+      dst = to;
+    } else if (live) {
+      uint2 ca, cb;
+      bits = encode<D, kInterleaved>(t, Unscale(scale), is_k && (norm || rotated), ca, cb);
+      uint8_t *to = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + slot;
+      *reinterpret_cast<uint2 *>(to + ea) = ca;
+      *reinterpret_cast<uint2 *>(to + eb) = cb;
+      dst = to;
     }
+    // bf16 keys within one step where the rotation cancels; codes of the exact key
+    if (!live || !is_k) bits = 0;
+    if (__any_sync(0xffffffffu, bits != 0))
+      exact_elements<D, kInterleaved, kE4m3>(a.k_new + i * a.k_ld + (size_t)g * D, a.k_norm_w, dst,
+                                             kE4m3 ? scale : rstd, a.eps, at.pos, a.rot, turns.v,
+                                             bits);
   }
 }
 
@@ -457,66 +492,75 @@ struct Run {
   int token, pos, page, count;
 };
 
-// One run of one KV head, by a warp (kGroup = 32, up to 4 * kRows tokens) or the block.
+// One run of one KV head, of up to 2 * kRows tokens, by kGroup threads: a warp, or as many as a page's
+// tokens take (its threads meet at the named barrier `meet`).
+constexpr int kPasses = 2;
 template <int D, bool kInterleaved, int kGroup>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
-                                       bool is_k, int g, uint4 wa, uint4 wb, float *s_max) {
+                                       bool is_k, int g, uint4 wa, uint4 wb, float *s_max, int meet) {
   using R = Row<D, kInterleaved>;
   constexpr int kRows = kGroup / R::kLanes;   // tokens side by side
-  constexpr int kPasses = kGroup == 32 ? 4 : 128 / kRows;
   const int in_group = threadIdx.x & (kGroup - 1);
   const int lane = threadIdx.x & 31, l = lane % R::kLanes, row = in_group / R::kLanes;
   const bool rotated = is_k && l < (a.rot >> 4), norm = is_k && a.k_norm_w != nullptr;
+  auto together = [&]() {
+    if (kGroup == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(meet), "n"(kGroup) : "memory");
+  };
   int ea, eb;
   R::places(l, a.rot, ea, eb);
   const __nv_bfloat16 *src = (is_k ? a.k_new : a.v_new) + (size_t)g * D;
   const long long ld = is_k ? a.k_ld : a.v_ld;
-  Turned<D, kInterleaved> t[kPasses];
-  float m = 0.f;
+  const int in_page = r.pos & ((1 << a.page_log2) - 1);
+  float *sp = (is_k ? a.k_scale : a.v_scale) + (size_t)r.page * a.Hkv + g;
+  uint8_t *base = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) +
+                  (((size_t)r.page * a.Hkv + g) << a.page_log2) * D;
+  Turned t[kPasses];
+  uint4 x[kPasses], y[kPasses];
+  float m = 0.f, old = 0.f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = p * kRows + row;
-    t[p].x = t[p].y = make_uint4(0u, 0u, 0u, 0u);
+    x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
     if (j < r.count) {
-      t[p].x = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + ea);
-      t[p].y = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + eb);
+      x[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + ea);
+      y[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + eb);
     }
   }
+  if (in_page > 0) old = *sp;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    if (p * kRows >= r.count) break;  // (the same for the whole group)
-    float cs[8], sn[8];
+    if (is_k) {
+      float cs[8], sn[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      cs[j] = 1.f;
-      sn[j] = 0.f;
-      if (rotated) rope_sincos_turns(r.pos + p * kRows + row, turns.v[8 * l + j], sn[j], cs[j]);
+      for (int j = 0; j < 8; ++j) {
+        cs[j] = 1.f;
+        sn[j] = 0.f;
+        if (rotated) quick_sincos(r.pos + p * kRows + row, turns.v[8 * l + j], sn[j], cs[j]);
+      }
+      float rstd;
+      turn<D, kInterleaved, false>(t[p], x[p], y[p], norm, wa, wb, a.eps, rotated, cs, sn, rstd);
+    } else {
+      R::unpack(x[p], y[p], t[p].u, t[p].v);
     }
-    turn(t[p], norm, wa, wb, a.eps, rotated, cs, sn);
     m = fmaxf(m, amax_of(t[p]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (kGroup > 32) {
-    __syncthreads();  // the last run's maxima have been read
     if (lane == 0) s_max[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = s_max[0];
+    together();  // (and everyone has read the scale)
+    const float *mine = s_max + (threadIdx.x / kGroup) * (kGroup / 32);
+    m = mine[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_max[w]);
+    for (int w = 1; w < kGroup / 32; ++w) m = fmaxf(m, mine[w]);
+    together();  // (before the next run's maxima)
+  } else {
+    together();
   }
-  const int in_page = r.pos & ((1 << a.page_log2) - 1);
-  float *sp = (is_k ? a.k_scale : a.v_scale) + (size_t)r.page * a.Hkv + g;
-  uint8_t *base = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) +
-                  (((size_t)r.page * a.Hkv + g) << a.page_log2) * D;
-  float scale = scale_for(m), old = scale;
-  if (in_page > 0) {
-    old = *sp;
-    scale = fmaxf(scale, old);
-  }
-  if (kGroup > 32) __syncthreads(); else __syncwarp();  // everyone has read the scale
+  const float need = scale_for(m), scale = in_page > 0 ? fmaxf(need, old) : need;
   if (in_group == 0 && (scale > old || in_page == 0)) *sp = scale;
-  if (scale > old) {
+  if (in_page > 0 && scale > old) {
     const float ratio = old / scale;
     uint4 *w = reinterpret_cast<uint4 *>(base);
 #pragma unroll 4
@@ -526,40 +570,44 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int j = p * kRows + row;
-    if (p * kRows >= r.count) break;
-    uint2 ca, cb;
-    encode<D, kInterleaved>(t[p], un, wa, wb, is_k && (norm || a.rot > 0), norm, a.eps, rotated,
-                            r.pos + j, l, turns.v, is_k && j < r.count, ca, cb);
+    if (p * kRows >= r.count) break;  // (the same for the whole group)
+    uint8_t *dst = base + (size_t)(in_page + j) * D;
+    unsigned bits = 0;
     if (j < r.count) {
-      uint8_t *dst = base + (size_t)(in_page + j) * D;
+      uint2 ca, cb;
+      bits = encode<D, kInterleaved>(t[p], un, norm || rotated, ca, cb);
       *reinterpret_cast<uint2 *>(dst + ea) = ca;
       *reinterpret_cast<uint2 *>(dst + eb) = cb;
     }
+    if (__any_sync(0xffffffffu, bits != 0))  // the codes are the exact key's
+      exact_elements<D, kInterleaved, true>(src + (r.token + j) * ld, norm ? a.k_norm_w : nullptr,
+                                            dst, scale, a.eps, r.pos + j, a.rot, turns.v, bits);
   }
 }
 
-// The runs that begin among a block's `chunk` tokens, for one KV head's keys or values.
-template <int D, bool kInterleaved>
-__device__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) {
+// The runs that begin among a block's `chunk` tokens, for one KV head's keys or values: short ones by a
+// warp each, the others by a group of as many threads as a page takes.
+template <int D, bool kInterleaved, int kBlock, int kPage>
+__device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) {
   using R = Row<D, kInterleaved>;
-  __shared__ Run s_run[128];
+  constexpr int kGroup = kPage * R::kLanes / kPasses;  // 32 (16 tokens of 64 dims) .. 512
+  constexpr int kChunk = kPage > 64 ? kPage : 64, kWarpRun = kPasses * 32 / R::kLanes;
+  __shared__ Run s_run[kChunk];
   __shared__ int s_short, s_long;
-  __shared__ float s_max[kWarps];
-  constexpr int kWarpRun = 4 * 32 / R::kLanes;  // tokens that a warp takes at once
-  const int head = block % (2 * a.Hkv), c0 = block / (2 * a.Hkv) * a.chunk;
+  __shared__ float s_max[kBlock / 32];
+  const int head = block % (2 * a.Hkv), c0 = block / (2 * a.Hkv) * kChunk;
   const bool is_k = head < a.Hkv;
   const int g = is_k ? head : head - a.Hkv;
   if (threadIdx.x == 0) s_short = s_long = 0;
   __syncthreads();
   const int i = c0 + threadIdx.x;
-  if ((int)threadIdx.x < a.chunk && i < a.n) {
+  if ((int)threadIdx.x < kChunk && i < a.n) {
     const Place p = place_of(a, i);
-    const int page = 1 << a.page_log2;
-    const bool begins = p.b >= 0 && (i == a.cu_new[p.b] || (p.pos & (page - 1)) == 0);
+    const bool begins = p.b >= 0 && (i == a.cu_new[p.b] || (p.pos & (kPage - 1)) == 0);
     if (begins && p.page >= 0) {
-      const int count = (int)min(p.end - i, (long long)(page - (p.pos & (page - 1))));
+      const int count = (int)min(p.end - i, (long long)(kPage - (p.pos & (kPage - 1))));
       // short ones from the front of the list, long ones from its back
-      const int k = count <= kWarpRun ? atomicAdd(&s_short, 1) : 127 - atomicAdd(&s_long, 1);
+      const int k = count <= kWarpRun ? atomicAdd(&s_short, 1) : kChunk - 1 - atomicAdd(&s_long, 1);
       s_run[k] = Run{i, p.pos, p.page, count};
     }
   }
@@ -572,26 +620,27 @@ __device__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) 
     wb = *reinterpret_cast<const uint4 *>(a.k_norm_w + eb);
   }
   const int shorts = s_short, longs = s_long;
-  for (int k = threadIdx.x >> 5; k < shorts; k += kWarps)
-    do_run<D, kInterleaved, 32>(a, turns, s_run[k], is_k, g, wa, wb, s_max);
-  for (int k = 0; k < longs; ++k)
-    do_run<D, kInterleaved, kThreads>(a, turns, s_run[127 - k], is_k, g, wa, wb, s_max);
+  for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
+    do_run<D, kInterleaved, 32>(a, turns, s_run[k], is_k, g, wa, wb, s_max, 0);
+  for (int k = threadIdx.x / kGroup; k < longs; k += kBlock / kGroup)
+    do_run<D, kInterleaved, kGroup>(a, turns, s_run[kChunk - 1 - k], is_k, g, wa, wb, s_max,
+                                    1 + threadIdx.x / kGroup);
 }
 
-// The first row_blocks blocks take rows: the queries, and keys and values too unless kRuns.
-template <int D, bool kInterleaved, bool kE4m3, bool kRuns>
-__global__ void __launch_bounds__(kThreads)
+// kPage = 0: every block takes rows, of queries, keys and values. Else the first row_blocks blocks take
+// the queries' rows, the others the runs of e4m3 pages of kPage tokens.
+template <int D, bool kInterleaved, bool kE4m3, int kPage, int kBlock>
+__global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  if constexpr (kRuns) {
-    if ((int)blockIdx.x >= a.row_blocks) {
-      do_runs<D, kInterleaved>(a, turns, blockIdx.x - a.row_blocks);
-      return;
-    }
-    do_rows<D, kInterleaved, false>(a, turns, a.Hq);
+  if constexpr (kPage > 0) {
+    if ((int)blockIdx.x >= a.row_blocks)
+      do_runs<D, kInterleaved, kBlock, kPage>(a, turns, blockIdx.x - a.row_blocks);
+    else
+      do_rows<D, kInterleaved, false, kBlock>(a, turns, a.Hq);
   } else {
-    do_rows<D, kInterleaved, kE4m3>(a, turns, a.Hq + 2 * a.Hkv);
+    do_rows<D, kInterleaved, kE4m3, kBlock>(a, turns, a.Hq + 2 * a.Hkv);
   }
 }
 
@@ -692,33 +741,38 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   a.num_pages = c.num_pages, a.page_log2 = log2_of(c.page), a.max_pages = c.max_pages;
   a.Hq = p.Hq, a.Hkv = c.Hkv, a.rot = p.rot_dim, a.eps = p.eps;
   const bool runs = c.e4m3 && p.cu_new != nullptr;
-  const int heads = runs ? p.Hq : p.Hq + 2 * c.Hkv, rows = kThreads / (c.D / 16);
+  // (a page of 128 tokens of 128 dims is 512 threads' work)
+  const int block = runs && c.D == 128 && c.page == 128 ? 512 : 256;
+  const int heads = runs ? p.Hq : p.Hq + 2 * c.Hkv, rows = block / (c.D / 16);
   int sms = 152, dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Tokens side by side: as many as there are, up to a block's rows. Heads one after the other: the
-  // more, the fewer angles are formed twice; as few as it takes for two blocks per SM.
+  // more, the fewer angles are formed twice; as few as it takes for kBlocksPerSm blocks per SM.
   a.tok_par = 1;
   while (a.tok_par < rows && a.tok_par < p.n) a.tok_par *= 2;
   const long long tiles = ((long long)p.n + a.tok_par - 1) / a.tok_par;
   const int side = rows / a.tok_par;
   a.heads_per = side;
-  while (a.heads_per < heads && tiles * ((heads + 2 * a.heads_per - 1) / (2 * a.heads_per)) >= 2 * sms)
+  while (a.heads_per < heads &&
+         tiles * ((heads + 2 * a.heads_per - 1) / (2 * a.heads_per)) >= kBlocksPerSm * sms)
     a.heads_per *= 2;
   a.head_blocks = (heads + a.heads_per - 1) / a.heads_per;
   a.row_blocks = (int)(tiles * a.head_blocks);
-  a.chunk = c.page > 64 ? c.page : 64;
+  const int chunk = c.page > 64 ? c.page : 64;
   const long long blocks =
-      a.row_blocks +
-      (runs ? ((long long)p.n + a.chunk - 1) / a.chunk * 2 * c.Hkv : 0);
+      a.row_blocks + (runs ? ((long long)p.n + chunk - 1) / chunk * 2 * c.Hkv : 0);
   const RopeTurns turns = make_rope_turns(p.rot_dim, inv);
   auto go = [&](auto dim, auto layout) {
     constexpr int kD = decltype(dim)::value;
     constexpr bool kI = decltype(layout)::value;
-    auto *kernel = runs     ? paged_append_kernel<kD, kI, true, true>
-                   : c.e4m3 ? paged_append_kernel<kD, kI, true, false>
-                            : paged_append_kernel<kD, kI, false, false>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, 0, stream, a, turns);
+    auto *kernel = !c.e4m3        ? paged_append_kernel<kD, kI, false, 0, 256>
+                   : !runs        ? paged_append_kernel<kD, kI, true, 0, 256>
+                   : c.page == 16 ? paged_append_kernel<kD, kI, true, 16, 256>
+                   : c.page == 32 ? paged_append_kernel<kD, kI, true, 32, 256>
+                   : c.page == 64 ? paged_append_kernel<kD, kI, true, 64, 256>
+                                  : paged_append_kernel<kD, kI, true, 128, kD == 128 ? 512 : 256>;
+    return launch_pdl(kernel, dim3((unsigned)blocks), block, 0, stream, a, turns);
   };
   using I64 = std::integral_constant<int, 64>;
   using I128 = std::integral_constant<int, 128>;
