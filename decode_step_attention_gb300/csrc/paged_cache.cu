@@ -23,7 +23,7 @@ namespace decattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 4, kMostWarps = 16;
 constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest
 
 // A row (token, head) is D / 16 lanes; a lane has two groups of 8 elements, u and v, of which u[j]
@@ -113,17 +113,28 @@ __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a < INFINITY ? a : 0.f;
 }
-// x / s, exact when s is a power of two.
-struct Unscale {
-  float s, inv;
-  bool pow2;
-  __device__ explicit Unscale(float scale) {
-    s = scale;
-    inv = 1.f / scale;
-    pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+// x / s; a product when s is a power of two, exact then too.
+__device__ __forceinline__ void unscale(const float (&u)[8], const float (&v)[8], float s,
+                                        float (&a)[8], float (&b)[8]) {
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = u[j] * inv, b[j] = v[j] * inv;
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {  // (a scale that the caller wrote: rare, and kept small)
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x = j == k ? u[k] : j == 8 + k ? v[k] : x;
+      x /= s;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a[k] = j == k ? x : a[k];
+        b[k] = j == 8 + k ? x : b[k];
+      }
+    }
   }
-  __device__ float operator()(float x) const { return pow2 ? x * inv : x / s; }
-};
+}
 
 // Sixteen codes of a page by the ratio of its old scale to its new one.
 __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
@@ -148,6 +159,7 @@ struct AppendArgs {
   float eps;
   // tokens and heads of a block of rows, and the blocks of them
   int tok_par, heads_per, row_blocks, head_blocks;
+  int run_heads, run_blocks;  // KV heads (keys, then values) of a block of runs; blocks for them all
 };
 
 // Where token i goes: its sequence, its position, and the page's number (-1: nowhere).
@@ -204,7 +216,7 @@ struct Turned {
 template <int D, bool kInterleaved, bool kBits>
 __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm, uint4 wa, uint4 wb,
                                          float eps, bool rotated, const float (&cs)[8],
-                                         const float (&sn)[8], float &rstd) {
+                                         const float (&sn)[8], bool key, float &rstd) {
   using R = Row<D, kInterleaved>;
   R::unpack(x, y, t.u, t.v);
   if (norm) {
@@ -233,10 +245,13 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
       const float p = t.u[j], q = t.v[j];
       t.u[j] = rope_first(p, q, cs[j], sn[j]);
       t.v[j] = rope_second<false>(p, q, cs[j], sn[j]);
-      if (kBits)
-        bits |= (rope_cancels(t.u[j], p, q) ? 1u << j : 0u) |
-                (rope_cancels(t.v[j], p, q) ? 0x100u << j : 0u);
     }
+    if (kBits && key)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // |p| + |q| is at most 2^0.5 of the turned pair's length
+        const float r = 0x1.7p-11f * (fabsf(t.u[j]) + fabsf(t.v[j]));
+        bits |= (fabsf(t.u[j]) < r ? 1u << j : 0u) | (fabsf(t.v[j]) < r ? 0x100u << j : 0u);
+      }
   }
   return bits;
 }
@@ -314,12 +329,11 @@ constexpr float kSlack = 15 * 0x1p-24f;
 // The codes of a lane's 16 values. check: also the values so near a border between two codes that
 // the fp32 arithmetic before could have moved them across.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ unsigned encode(const Turned &t, const Unscale &un, bool check, uint2 &a,
+__device__ __forceinline__ unsigned encode(const Turned &t, float scale, bool check, uint2 &a,
                                            uint2 &b) {
   using R = Row<D, kInterleaved>;
-  float u[8], v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = un(t.u[j]), v[j] = un(t.v[j]);
+  float u[8] = {}, v[8] = {};
+  unscale(t.u, t.v, scale, u, v);
   unsigned bits = 0;
   if (check) {
     uint32_t any = 0;
@@ -362,7 +376,8 @@ __device__ __forceinline__ float amax_of(const Turned &t) {
 // ---- rows: (token, head) pairs that need nothing of each other ------------------------------
 // Heads are counted q, k, v. A block has tok_par tokens side by side, times as many heads as fit,
 // and goes through its heads_per heads with them: a lane keeps its token's angles.
-template <int D, bool kInterleaved, bool kE4m3, int kBlock>
+// kAll: keys and values too, else queries alone.
+template <int D, bool kInterleaved, bool kE4m3, bool kAll, int kBlock>
 __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) {
   using R = Row<D, kInterleaved>;
   constexpr int kRows = kBlock / R::kLanes;
@@ -389,8 +404,8 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   // a head's two groups of this lane, on their way while the one before is turned
   auto load = [&](int h, uint4 &x, uint4 &y) {
     x = y = make_uint4(0u, 0u, 0u, 0u);
-    if (some && h < h1 && (h < a.Hq || at.page >= 0)) {
-      const __nv_bfloat16 *src = h < a.Hq ? a.q_in + i * a.q_ld + (size_t)h * D
+    if (some && h < h1 && (!kAll || h < a.Hq || at.page >= 0)) {
+      const __nv_bfloat16 *src = !kAll || h < a.Hq ? a.q_in + i * a.q_ld + (size_t)h * D
                                  : h < a.Hq + a.Hkv
                                      ? a.k_new + i * a.k_ld + (size_t)(h - a.Hq) * D
                                      : a.v_new + i * a.v_ld + (size_t)(h - a.Hq - a.Hkv) * D;
@@ -402,7 +417,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   load(h0 + row / a.tok_par, next_x, next_y);
   for (int hh = h0; hh < h1; hh += step) {  // (the same number of times in every lane)
     const int h = hh + row / a.tok_par;
-    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+    const bool is_q = !kAll || h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
     const int g = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hkv;
     const bool live = some && h < h1 && (is_q || at.page >= 0);
     Turned t;
@@ -418,8 +433,8 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     unsigned bits = 0;
     float rstd = 1.f;
     if (turns_here || norm)  // (a warp may hold values beside keys: the norm's shuffles)
-      bits = turn<D, kInterleaved, !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
-                                            rstd);
+      bits = turn<D, kInterleaved, kAll && !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
+                                            is_k, rstd);
     if (!turns_here) R::unpack(x, y, t.u, t.v);
     const size_t slot =
         live && !is_q
@@ -472,7 +487,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
       dst = to;
     } else if (live) {
       uint2 ca, cb;
-      bits = encode<D, kInterleaved>(t, Unscale(scale), is_k && (norm || rotated), ca, cb);
+      bits = encode<D, kInterleaved>(t, scale, is_k && (norm || rotated), ca, cb);
       uint8_t *to = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + slot;
       *reinterpret_cast<uint2 *>(to + ea) = ca;
       *reinterpret_cast<uint2 *>(to + eb) = cb;
@@ -480,7 +495,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     }
     // bf16 keys within one step where the rotation cancels; codes of the exact key
     if (!live || !is_k) bits = 0;
-    if (__any_sync(0xffffffffu, bits != 0))
+    if (kAll && __any_sync(0xffffffffu, bits != 0))
       exact_elements<D, kInterleaved, kE4m3>(a.k_new + i * a.k_ld + (size_t)g * D, a.k_norm_w, dst,
                                              kE4m3 ? scale : rstd, a.eps, at.pos, a.rot, turns.v,
                                              bits);
@@ -492,112 +507,153 @@ struct Run {
   int token, pos, page, count;
 };
 
-// One run of one KV head, of up to 2 * kRows tokens, by kGroup threads: a warp, or as many as a page's
-// tokens take (its threads meet at the named barrier `meet`).
+// One run of up to 2 * kRows tokens, for the KV heads h0 .. h1 (keys first, then values) one after the
+// other, by kGroup threads: a warp, or as many as a page's tokens take. These meet at the named barrier
+// `meet` and have the run's angles in `table`: [token][4 pairs of each lane, then the others] cosines,
+// then the sines.
 constexpr int kPasses = 2;
 template <int D, bool kInterleaved, int kGroup>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
-                                       bool is_k, int g, uint4 wa, uint4 wb, float *s_max, int meet) {
+                                       int h0, int h1, float *s_max, float *table, int meet) {
   using R = Row<D, kInterleaved>;
+  constexpr bool kWarp = kGroup == 32;
   constexpr int kRows = kGroup / R::kLanes;   // tokens side by side
+  constexpr int kToken = D / 2;               // floats of a token's cosines
+  constexpr int kSines = kPasses * kRows * kToken;
   const int in_group = threadIdx.x & (kGroup - 1);
   const int lane = threadIdx.x & 31, l = lane % R::kLanes, row = in_group / R::kLanes;
-  const bool rotated = is_k && l < (a.rot >> 4), norm = is_k && a.k_norm_w != nullptr;
+  const bool turned = l < (a.rot >> 4), norm = a.k_norm_w != nullptr;
   auto together = [&]() {
-    if (kGroup == 32) __syncwarp();
+    if (kWarp) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(meet), "n"(kGroup) : "memory");
   };
   int ea, eb;
   R::places(l, a.rot, ea, eb);
-  const __nv_bfloat16 *src = (is_k ? a.k_new : a.v_new) + (size_t)g * D;
-  const long long ld = is_k ? a.k_ld : a.v_ld;
   const int in_page = r.pos & ((1 << a.page_log2) - 1);
-  float *sp = (is_k ? a.k_scale : a.v_scale) + (size_t)r.page * a.Hkv + g;
-  uint8_t *base = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) +
-                  (((size_t)r.page * a.Hkv + g) << a.page_log2) * D;
-  Turned t[kPasses];
-  uint4 x[kPasses], y[kPasses];
-  float m = 0.f, old = 0.f;
+  if (!kWarp && h0 < a.Hkv) {
+    for (int i = in_group; i < r.count * R::kLanes; i += kGroup) {
+      const int j = i / R::kLanes, of = i % R::kLanes;
+      if (of < (a.rot >> 4)) {
+        float c[8], s[8];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kRows + row;
-    x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (j < r.count) {
-      x[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + ea);
-      y[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + eb);
-    }
-  }
-  if (in_page > 0) old = *sp;
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    if (is_k) {
-      float cs[8], sn[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cs[j] = 1.f;
-        sn[j] = 0.f;
-        if (rotated) quick_sincos(r.pos + p * kRows + row, turns.v[8 * l + j], sn[j], cs[j]);
+        for (int k = 0; k < 8; ++k) quick_sincos(r.pos + j, turns.v[8 * of + k], s[k], c[k]);
+        float4 *to = reinterpret_cast<float4 *>(table + j * kToken) + of;
+        to[0] = make_float4(c[0], c[1], c[2], c[3]);
+        to[R::kLanes] = make_float4(c[4], c[5], c[6], c[7]);
+        to += kSines / 4;
+        to[0] = make_float4(s[0], s[1], s[2], s[3]);
+        to[R::kLanes] = make_float4(s[4], s[5], s[6], s[7]);
       }
-      float rstd;
-      turn<D, kInterleaved, false>(t[p], x[p], y[p], norm, wa, wb, a.eps, rotated, cs, sn, rstd);
-    } else {
-      R::unpack(x[p], y[p], t[p].u, t[p].v);
     }
-    m = fmaxf(m, amax_of(t[p]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (kGroup > 32) {
-    if (lane == 0) s_max[threadIdx.x >> 5] = m;
-    together();  // (and everyone has read the scale)
-    const float *mine = s_max + (threadIdx.x / kGroup) * (kGroup / 32);
-    m = mine[0];
-#pragma unroll
-    for (int w = 1; w < kGroup / 32; ++w) m = fmaxf(m, mine[w]);
-    together();  // (before the next run's maxima)
-  } else {
     together();
   }
-  const float need = scale_for(m), scale = in_page > 0 ? fmaxf(need, old) : need;
-  if (in_group == 0 && (scale > old || in_page == 0)) *sp = scale;
-  if (in_page > 0 && scale > old) {
-    const float ratio = old / scale;
-    uint4 *w = reinterpret_cast<uint4 *>(base);
-#pragma unroll 4
-    for (int k = in_group; k < in_page * (D / 16); k += kGroup) w[k] = rescale16(w[k], ratio);
-  }
-  const Unscale un(scale);
+  for (int head = h0; head < h1; ++head) {
+    const bool is_k = head < a.Hkv;
+    const int g = is_k ? head : head - a.Hkv;
+    const __nv_bfloat16 *src = (is_k ? a.k_new : a.v_new) + (size_t)g * D;
+    const long long ld = is_k ? a.k_ld : a.v_ld;
+    float *sp = (is_k ? a.k_scale : a.v_scale) + (size_t)r.page * a.Hkv + g;
+    uint8_t *base = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) +
+                    (((size_t)r.page * a.Hkv + g) << a.page_log2) * D;
+    uint4 x[kPasses], y[kPasses], wa{}, wb{};
+    float m = 0.f, old = 0.f;
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int j = p * kRows + row;
-    if (p * kRows >= r.count) break;  // (the same for the whole group)
-    uint8_t *dst = base + (size_t)(in_page + j) * D;
-    unsigned bits = 0;
-    if (j < r.count) {
-      uint2 ca, cb;
-      bits = encode<D, kInterleaved>(t[p], un, norm || rotated, ca, cb);
-      *reinterpret_cast<uint2 *>(dst + ea) = ca;
-      *reinterpret_cast<uint2 *>(dst + eb) = cb;
+    for (int p = 0; p < kPasses; ++p) {
+      const int j = p * kRows + row;
+      x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < r.count) {
+        x[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + ea);
+        y[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + eb);
+      }
     }
-    if (__any_sync(0xffffffffu, bits != 0))  // the codes are the exact key's
-      exact_elements<D, kInterleaved, true>(src + (r.token + j) * ld, norm ? a.k_norm_w : nullptr,
-                                            dst, scale, a.eps, r.pos + j, a.rot, turns.v, bits);
+    if (in_page > 0) old = *sp;
+    if (is_k && norm) {
+      wa = *reinterpret_cast<const uint4 *>(a.k_norm_w + ea);
+      wb = *reinterpret_cast<const uint4 *>(a.k_norm_w + eb);
+    }
+    Turned t[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      if (is_k) {
+        const int j = p * kRows + row;
+        float cs[8], sn[8], rstd;
+        if (kWarp) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            cs[k] = 1.f;
+            sn[k] = 0.f;
+            if (turned) quick_sincos(r.pos + j, turns.v[8 * l + k], sn[k], cs[k]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 *at = reinterpret_cast<const float4 *>(table + j * kToken) + l + h * R::kLanes;
+            const float4 c = at[0], s = at[kSines / 4];
+            cs[4 * h] = c.x, cs[4 * h + 1] = c.y, cs[4 * h + 2] = c.z, cs[4 * h + 3] = c.w;
+            sn[4 * h] = s.x, sn[4 * h + 1] = s.y, sn[4 * h + 2] = s.z, sn[4 * h + 3] = s.w;
+          }
+        }
+        // (rows behind the run's last token turn zeros by what the table holds: they are masked)
+        turn<D, kInterleaved, false>(t[p], x[p], y[p], norm, wa, wb, a.eps, turned, cs, sn, true, rstd);
+        if (j < r.count) m = fmaxf(m, amax_of(t[p]));
+      } else {
+        R::unpack(x[p], y[p], t[p].u, t[p].v);
+        m = fmaxf(m, amax_of(t[p]));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!kWarp) {
+      // (two sets of maxima in turn: a warp may be a head ahead of the group's others)
+      float *mine = s_max + ((head & 1) ? kMostWarps : 0) + (threadIdx.x / kGroup) * (kGroup / 32);
+      if (lane == 0) mine[in_group >> 5] = m;
+      together();  // (and everyone has read the scale)
+      m = mine[0];
+#pragma unroll
+      for (int w = 1; w < kGroup / 32; ++w) m = fmaxf(m, mine[w]);
+    } else {
+      together();
+    }
+    const float need = scale_for(m), scale = in_page > 0 ? fmaxf(need, old) : need;
+    if (in_group == 0 && (scale > old || in_page == 0)) *sp = scale;
+    if (in_page > 0 && scale > old) {
+      const float ratio = old / scale;
+      uint4 *w = reinterpret_cast<uint4 *>(base);
+#pragma unroll 4
+      for (int k = in_group; k < in_page * (D / 16); k += kGroup) w[k] = rescale16(w[k], ratio);
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int j = p * kRows + row;
+      if (p * kRows >= r.count) break;  // (the same for the whole group)
+      uint8_t *dst = base + (size_t)(in_page + j) * D;
+      unsigned bits = 0;
+      if (j < r.count) {
+        uint2 ca, cb;
+        bits = encode<D, kInterleaved>(t[p], scale, is_k && (norm || turned), ca, cb);
+        *reinterpret_cast<uint2 *>(dst + ea) = ca;
+        *reinterpret_cast<uint2 *>(dst + eb) = cb;
+      }
+      if (__any_sync(0xffffffffu, bits != 0))  // the codes are the exact key's
+        exact_elements<D, kInterleaved, true>(src + (r.token + j) * ld, a.k_norm_w, dst, scale, a.eps,
+                                              r.pos + j, a.rot, turns.v, bits);
+    }
   }
 }
 
-// The runs that begin among a block's `chunk` tokens, for one KV head's keys or values: short ones by a
-// warp each, the others by a group of as many threads as a page takes.
+// The runs that begin among a block's `chunk` tokens, for some of the KV heads' keys and values: short
+// ones by a warp each, the others by a group of as many threads as a page takes.
 template <int D, bool kInterleaved, int kBlock, int kPage>
 __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) {
   using R = Row<D, kInterleaved>;
   constexpr int kGroup = kPage * R::kLanes / kPasses;  // 32 (16 tokens of 64 dims) .. 512
   constexpr int kChunk = kPage > 64 ? kPage : 64, kWarpRun = kPasses * 32 / R::kLanes;
+  extern __shared__ __align__(16) float s_table[];  // of each group: kPage * D
   __shared__ Run s_run[kChunk];
   __shared__ int s_short, s_long;
-  __shared__ float s_max[kBlock / 32];
-  const int head = block % (2 * a.Hkv), c0 = block / (2 * a.Hkv) * kChunk;
-  const bool is_k = head < a.Hkv;
-  const int g = is_k ? head : head - a.Hkv;
+  __shared__ float s_max[2 * kMostWarps];
+  const int c0 = block / a.run_blocks * kChunk, h0 = block % a.run_blocks * a.run_heads;
+  const int h1 = min(2 * a.Hkv, h0 + a.run_heads);
   if (threadIdx.x == 0) s_short = s_long = 0;
   __syncthreads();
   const int i = c0 + threadIdx.x;
@@ -612,19 +668,17 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
     }
   }
   __syncthreads();
-  uint4 wa{}, wb{};
-  if (is_k && a.k_norm_w != nullptr) {
-    int ea, eb;
-    R::places((threadIdx.x & 31) % R::kLanes, a.rot, ea, eb);
-    wa = *reinterpret_cast<const uint4 *>(a.k_norm_w + ea);
-    wb = *reinterpret_cast<const uint4 *>(a.k_norm_w + eb);
-  }
   const int shorts = s_short, longs = s_long;
   for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
-    do_run<D, kInterleaved, 32>(a, turns, s_run[k], is_k, g, wa, wb, s_max, 0);
-  for (int k = threadIdx.x / kGroup; k < longs; k += kBlock / kGroup)
-    do_run<D, kInterleaved, kGroup>(a, turns, s_run[kChunk - 1 - k], is_k, g, wa, wb, s_max,
-                                    1 + threadIdx.x / kGroup);
+    do_run<D, kInterleaved, 32>(a, turns, s_run[k], h0, h1, nullptr, nullptr, 0);
+  if constexpr (kGroup > 32)
+    for (int k = threadIdx.x / kGroup; k < longs; k += kBlock / kGroup) {
+      const int group = threadIdx.x / kGroup;
+      do_run<D, kInterleaved, kGroup>(a, turns, s_run[kChunk - 1 - k], h0, h1, s_max,
+                                      s_table + group * kPage * D, 1 + group);
+      // (the next run's angles and maxima take this one's place)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory");
+    }
 }
 
 // kPage = 0: every block takes rows, of queries, keys and values. Else the first row_blocks blocks take
@@ -638,9 +692,9 @@ __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     if ((int)blockIdx.x >= a.row_blocks)
       do_runs<D, kInterleaved, kBlock, kPage>(a, turns, blockIdx.x - a.row_blocks);
     else
-      do_rows<D, kInterleaved, false, kBlock>(a, turns, a.Hq);
+      do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq);
   } else {
-    do_rows<D, kInterleaved, kE4m3, kBlock>(a, turns, a.Hq + 2 * a.Hkv);
+    do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv);
   }
 }
 
@@ -760,8 +814,15 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   a.head_blocks = (heads + a.heads_per - 1) / a.heads_per;
   a.row_blocks = (int)(tiles * a.head_blocks);
   const int chunk = c.page > 64 ? c.page : 64;
-  const long long blocks =
-      a.row_blocks + (runs ? ((long long)p.n + chunk - 1) / chunk * 2 * c.Hkv : 0);
+  const long long chunks = ((long long)p.n + chunk - 1) / chunk;
+  a.run_heads = 1;
+  while (a.run_heads < c.Hkv && chunks * ((2 * c.Hkv + 2 * a.run_heads - 1) / (2 * a.run_heads)) >=
+                                    kBlocksPerSm * sms)
+    a.run_heads *= 2;
+  a.run_blocks = (2 * c.Hkv + a.run_heads - 1) / a.run_heads;
+  const long long blocks = a.row_blocks + (runs ? chunks * a.run_blocks : 0);
+  // (the angles of the pages that a block has under way at a time)
+  const size_t smem = runs ? (size_t)block * kPasses / (c.D / 16) * c.D * 4 : 0;
   const RopeTurns turns = make_rope_turns(p.rot_dim, inv);
   auto go = [&](auto dim, auto layout) {
     constexpr int kD = decltype(dim)::value;
@@ -772,7 +833,12 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
                    : c.page == 32 ? paged_append_kernel<kD, kI, true, 32, 256>
                    : c.page == 64 ? paged_append_kernel<kD, kI, true, 64, 256>
                                   : paged_append_kernel<kD, kI, true, 128, kD == 128 ? 512 : 256>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), block, 0, stream, a, turns);
+    if (smem > 48 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, dim3((unsigned)blocks), block, smem, stream, a, turns);
   };
   using I64 = std::integral_constant<int, 64>;
   using I128 = std::integral_constant<int, 128>;
