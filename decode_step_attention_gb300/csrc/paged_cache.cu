@@ -162,7 +162,8 @@ struct AppendArgs {
   int run_heads, run_blocks;  // KV heads (keys, then values) of a block of runs; blocks for them all
 };
 
-// Where token i goes: its sequence, its position, and the page's number (-1: nowhere).
+// Where token i goes: its sequence, its position, and the page's number (-1: nowhere). The whole warp
+// calls it, with any i.
 struct Place {
   int b, pos, page;
   long long end;  // the first token behind the sequence's
@@ -172,17 +173,25 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int i) {
   long long first = i;
   p.end = i + 1;
   if (a.cu_new == nullptr) {
-    p.b = i;
+    p.b = i < a.n ? i : -1;
   } else {
-    int lo = 0, hi = a.B;  // cu_new[lo] <= i < cu_new[hi] where cu_new is in order
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu_new[mid] <= i) lo = mid; else hi = mid;
+    // the last sequence that begins at or before i: up to 32 at once, a lane each, more by halving
+    int lo = 0, hi = a.B;
+    if (a.B <= 32) {
+      const int lane = threadIdx.x & 31, mine = a.cu_new[min(lane, a.B - 1)];
+      for (int b = 1; b < a.B; ++b)
+        if (__shfl_sync(0xffffffffu, mine, b) <= i) lo = b;
+      first = __shfl_sync(0xffffffffu, mine, lo);
+    } else {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_new[mid] <= i) lo = mid; else hi = mid;
+      }
+      first = a.cu_new[lo];
     }
     p.b = lo;
-    first = a.cu_new[lo];
     p.end = min(a.cu_new[lo + 1], a.n);
-    if (first > i || p.end <= i) p.b = -1;  // a token of no sequence
+    if (first > i || p.end <= i) p.b = -1;  // a token of no sequence, or none
   }
   p.pos = p.page = -1;
   if (p.b < 0) return p;
@@ -264,14 +273,14 @@ __device__ __forceinline__ float sticky(double x) {
 }
 
 // Elements of a key whose fp32 value does not settle the stored one (bits of this lane's 16: u, then
-// v), again in fp64 from the inputs, and written over. The whole warp calls it; rare. A bf16 value takes
+// v; l: its place in the row), again in fp64 from the inputs, and written over. The whole warp calls it; rare. A bf16 value takes
 // the row's fp32 norm (1 without it), a code the exact one, whose sum of squares the warp forms
 // together (by one lane, 8 us of a small call).
 template <int D, bool kInterleaved, bool kE4m3>
 __device__ __noinline__ void exact_elements(const __nv_bfloat16 *src, const __nv_bfloat16 *w,
                                             void *dst, float scale_or_rstd, float eps, int pos, int rot,
-                                            const unsigned long long *turns, unsigned bits) {
-  const int lane = threadIdx.x & 31, l = lane % Row<D, kInterleaved>::kLanes;
+                                            int l, const unsigned long long *turns, unsigned bits) {
+  const int lane = threadIdx.x & 31;
   double factor;  // the norm, and the scale's inverse
   if (kE4m3) {
     const double s = (double)scale_or_rstd, inv = (double)(1.f / scale_or_rstd);
@@ -321,24 +330,24 @@ __device__ __noinline__ void exact_elements(const __nv_bfloat16 *src, const __nv
   }
 }
 
-// How far fp32 may have moved a value of a row that was normed and rotated, of its pair's magnitudes: the
-// angle's and the series' roundings 3.5 2^-24, the rotation's 2 2^-24, the norm's 9.5 2^-24 (its sum of
-// 128 squares at most 11 halved, rsqrt 4 halved, two products).
-constexpr float kSlack = 15 * 0x1p-24f;
+// How far fp32 may have moved a value, of its pair's magnitudes: the angle's and the series' roundings 3.5
+// 2^-24 and the rotation's 2 2^-24; with the norm 9.5 2^-24 more (its sum of 128 squares at most 11
+// halved, rsqrt 4 halved, two products).
+__device__ __forceinline__ float slack(bool norm) { return norm ? 15 * 0x1p-24f : 5.5f * 0x1p-24f; }
 
-// The codes of a lane's 16 values. check: also the values so near a border between two codes that
+// The codes of a lane's 16 values, and with slack > 0 the values so near a border between two codes that
 // the fp32 arithmetic before could have moved them across.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ unsigned encode(const Turned &t, float scale, bool check, uint2 &a,
+__device__ __forceinline__ unsigned encode(const Turned &t, float scale, float slack, uint2 &a,
                                            uint2 &b) {
   using R = Row<D, kInterleaved>;
   float u[8] = {}, v[8] = {};
   unscale(t.u, t.v, scale, u, v);
   unsigned bits = 0;
-  if (check) {
+  if (slack > 0.f) {
     uint32_t any = 0;
     auto off = [&](int j) {
-      const float d = kSlack * (fabsf(u[j]) + fabsf(v[j]));
+      const float d = slack * (fabsf(u[j]) + fabsf(v[j]));
       return e4m3x2(u[j] - d, v[j] - d) ^ e4m3x2(u[j] + d, v[j] + d);
     };
 #pragma unroll
@@ -378,33 +387,23 @@ __device__ __forceinline__ float amax_of(const Turned &t) {
 // and goes through its heads_per heads with them: a lane keeps its token's angles.
 // kAll: keys and values too, else queries alone.
 template <int D, bool kInterleaved, bool kE4m3, bool kAll, int kBlock>
-__device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads) {
+__device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
+                                        int which) {
   using R = Row<D, kInterleaved>;
   constexpr int kRows = kBlock / R::kLanes;
   const int lane = threadIdx.x & 31, l = lane % R::kLanes, row = threadIdx.x / R::kLanes;
-  const int block = blockIdx.x % a.head_blocks, tile = blockIdx.x / a.head_blocks;
+  const int block = which % a.head_blocks, tile = which / a.head_blocks;
   const int i = tile * a.tok_par + (row & (a.tok_par - 1));
   const int step = kRows / a.tok_par;
   const int h0 = block * a.heads_per, h1 = min(heads, h0 + a.heads_per);
-  Place at{};
-  at.b = at.pos = at.page = -1;
-  if (i < a.n) at = place_of(a, i);
-  const bool some = at.pos >= 0;
   const bool rotated = l < (a.rot >> 4), norm = a.q_norm_w != nullptr;
   int ea, eb;
   R::places(l, a.rot, ea, eb);
-  float cs[8], sn[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-    if (rotated && some) quick_sincos(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
-  }
-  const int in_page = at.pos & ((1 << a.page_log2) - 1);
-  // a head's two groups of this lane, on their way while the one before is turned
+  // a head's two groups of this lane, on their way while the one before is turned (the first while the
+  // token's place is looked up)
   auto load = [&](int h, uint4 &x, uint4 &y) {
     x = y = make_uint4(0u, 0u, 0u, 0u);
-    if (some && h < h1 && (!kAll || h < a.Hq || at.page >= 0)) {
+    if (i < a.n && h < h1) {
       const __nv_bfloat16 *src = !kAll || h < a.Hq ? a.q_in + i * a.q_ld + (size_t)h * D
                                  : h < a.Hq + a.Hkv
                                      ? a.k_new + i * a.k_ld + (size_t)(h - a.Hq) * D
@@ -415,6 +414,16 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   };
   uint4 next_x, next_y;
   load(h0 + row / a.tok_par, next_x, next_y);
+  const Place at = place_of(a, i);
+  const bool some = at.pos >= 0;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = 1.f;
+    sn[j] = 0.f;
+    if (rotated && some) quick_sincos(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
+  }
+  const int in_page = at.pos & ((1 << a.page_log2) - 1);
   for (int hh = h0; hh < h1; hh += step) {  // (the same number of times in every lane)
     const int h = hh + row / a.tok_par;
     const bool is_q = !kAll || h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
@@ -487,7 +496,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
       dst = to;
     } else if (live) {
       uint2 ca, cb;
-      bits = encode<D, kInterleaved>(t, scale, is_k && (norm || rotated), ca, cb);
+      bits = encode<D, kInterleaved>(t, scale, is_k && (norm || rotated) ? slack(norm) : 0.f, ca, cb);
       uint8_t *to = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) + slot;
       *reinterpret_cast<uint2 *>(to + ea) = ca;
       *reinterpret_cast<uint2 *>(to + eb) = cb;
@@ -497,7 +506,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     if (!live || !is_k) bits = 0;
     if (kAll && __any_sync(0xffffffffu, bits != 0))
       exact_elements<D, kInterleaved, kE4m3>(a.k_new + i * a.k_ld + (size_t)g * D, a.k_norm_w, dst,
-                                             kE4m3 ? scale : rstd, a.eps, at.pos, a.rot, turns.v,
+                                             kE4m3 ? scale : rstd, a.eps, at.pos, a.rot, l, turns.v,
                                              bits);
   }
 }
@@ -507,6 +516,13 @@ struct Run {
   int token, pos, page, count;
 };
 
+// An element of a key to be formed again.
+struct Fix {
+  int token, head, place;  // of the run; lane and bit
+  float scale;
+};
+constexpr int kFixes = 64;
+
 // One run of up to 2 * kRows tokens, for the KV heads h0 .. h1 (keys first, then values) one after the
 // other, by kGroup threads: a warp, or as many as a page's tokens take. These meet at the named barrier
 // `meet` and have the run's angles in `table`: [token][4 pairs of each lane, then the others] cosines,
@@ -514,7 +530,8 @@ struct Run {
 constexpr int kPasses = 2;
 template <int D, bool kInterleaved, int kGroup>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
-                                       int h0, int h1, float *s_max, float *table, int meet) {
+                                       int h0, int h1, float *s_max, float *table, Fix *fixes,
+                                       int *fix_count, int meet) {
   using R = Row<D, kInterleaved>;
   constexpr bool kWarp = kGroup == 32;
   constexpr int kRows = kGroup / R::kLanes;   // tokens side by side
@@ -630,14 +647,39 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
       unsigned bits = 0;
       if (j < r.count) {
         uint2 ca, cb;
-        bits = encode<D, kInterleaved>(t[p], scale, is_k && (norm || turned), ca, cb);
+        bits = encode<D, kInterleaved>(t[p], scale, is_k && (norm || turned) ? slack(norm) : 0.f, ca,
+                                       cb);
         *reinterpret_cast<uint2 *>(dst + ea) = ca;
         *reinterpret_cast<uint2 *>(dst + eb) = cb;
       }
-      if (__any_sync(0xffffffffu, bits != 0))  // the codes are the exact key's
-        exact_elements<D, kInterleaved, true>(src + (r.token + j) * ld, a.k_norm_w, dst, scale, a.eps,
-                                              r.pos + j, a.rot, turns.v, bits);
+      // The codes are the exact key's: a group's elements go into a list, which its threads work off when
+      // the heads are done (on the way each would hold up the whole group).
+      if (!kWarp)
+        for (; bits != 0; bits &= bits - 1) {
+          const int k = atomicAdd(fix_count, 1);
+          if (k >= kFixes) break;  // (the rest here)
+          fixes[k] = Fix{j, g, l * 16 + __ffs(bits) - 1, scale};
+        }
+      if (__any_sync(0xffffffffu, bits != 0))
+        exact_elements<D, kInterleaved, true>(a.k_new + (size_t)g * D + (r.token + j) * a.k_ld,
+                                              a.k_norm_w, dst, scale, a.eps, r.pos + j, a.rot, l,
+                                              turns.v, bits);
     }
+  }
+  if (!kWarp) {
+    together();
+    const int count = min(*fix_count, kFixes);
+    for (int k = in_group; (k & ~31) < count; k += kGroup) {  // (whole warps)
+      const Fix f = k < count ? fixes[k] : Fix{};
+      exact_elements<D, kInterleaved, true>(
+          a.k_new + (size_t)f.head * D + (r.token + f.token) * a.k_ld, a.k_norm_w,
+          static_cast<uint8_t *>(a.k_pages) +
+              ((((size_t)r.page * a.Hkv + f.head) << a.page_log2) + in_page + f.token) * D,
+          f.scale, a.eps, r.pos + f.token, a.rot, f.place >> 4, turns.v,
+          k < count ? 1u << (f.place & 15) : 0u);
+    }
+    together();
+    if (in_group == 0) *fix_count = 0;
   }
 }
 
@@ -650,14 +692,16 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   constexpr int kChunk = kPage > 64 ? kPage : 64, kWarpRun = kPasses * 32 / R::kLanes;
   extern __shared__ __align__(16) float s_table[];  // of each group: kPage * D
   __shared__ Run s_run[kChunk];
-  __shared__ int s_short, s_long;
+  __shared__ int s_short, s_long, s_fix_count[kBlock / kGroup];
   __shared__ float s_max[2 * kMostWarps];
+  __shared__ Fix s_fix[kBlock / kGroup][kFixes];
   const int c0 = block / a.run_blocks * kChunk, h0 = block % a.run_blocks * a.run_heads;
   const int h1 = min(2 * a.Hkv, h0 + a.run_heads);
   if (threadIdx.x == 0) s_short = s_long = 0;
+  if (threadIdx.x < kBlock / kGroup) s_fix_count[threadIdx.x] = 0;
   __syncthreads();
   const int i = c0 + threadIdx.x;
-  if ((int)threadIdx.x < kChunk && i < a.n) {
+  if ((int)threadIdx.x < kChunk) {  // (whole warps)
     const Place p = place_of(a, i);
     const bool begins = p.b >= 0 && (i == a.cu_new[p.b] || (p.pos & (kPage - 1)) == 0);
     if (begins && p.page >= 0) {
@@ -670,12 +714,13 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   __syncthreads();
   const int shorts = s_short, longs = s_long;
   for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
-    do_run<D, kInterleaved, 32>(a, turns, s_run[k], h0, h1, nullptr, nullptr, 0);
+    do_run<D, kInterleaved, 32>(a, turns, s_run[k], h0, h1, nullptr, nullptr, nullptr, nullptr, 0);
   if constexpr (kGroup > 32)
     for (int k = threadIdx.x / kGroup; k < longs; k += kBlock / kGroup) {
       const int group = threadIdx.x / kGroup;
       do_run<D, kInterleaved, kGroup>(a, turns, s_run[kChunk - 1 - k], h0, h1, s_max,
-                                      s_table + group * kPage * D, 1 + group);
+                                      s_table + group * kPage * D, s_fix[group], &s_fix_count[group],
+                                      1 + group);
       // (the next run's angles and maxima take this one's place)
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory");
     }
@@ -688,13 +733,19 @@ __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
+  int block = blockIdx.x;
   if constexpr (kPage > 0) {
-    if ((int)blockIdx.x >= a.row_blocks)
-      do_runs<D, kInterleaved, kBlock, kPage>(a, turns, blockIdx.x - a.row_blocks);
+    // blocks of rows, which memory bounds, and of runs, which instructions do, side by side
+    const unsigned all = gridDim.x, rows = a.row_blocks, i = blockIdx.x;
+    const unsigned before = (unsigned)((unsigned long long)i * rows / all);
+    const bool is_row = (unsigned)((unsigned long long)(i + 1) * rows / all) != before;
+    block = is_row ? before : i - before;
+    if (!is_row)
+      do_runs<D, kInterleaved, kBlock, kPage>(a, turns, block);
     else
-      do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq);
+      do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq, block);
   } else {
-    do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv);
+    do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   }
 }
 
