@@ -228,37 +228,57 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
                                          const float (&sn)[8], bool key, float &rstd) {
   using R = Row<D, kInterleaved>;
   R::unpack(x, y, t.u, t.v);
+  uint64_t u[4], v[4];  // two elements at a time
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u[j] = pair_of(t.u[2 * j], t.u[2 * j + 1]);
+    v[j] = pair_of(t.v[2 * j], t.v[2 * j + 1]);
+  }
   if (norm) {
-    float su = 0.f, sv = 0.f;
+    uint64_t su = mul2(u[0], u[0]), sv = mul2(v[0], v[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      su = fmaf(t.u[j], t.u[j], su);
-      sv = fmaf(t.v[j], t.v[j], sv);
+    for (int j = 1; j < 4; ++j) {
+      su = fma2(u[j], u[j], su);
+      sv = fma2(v[j], v[j], sv);
     }
-    su += sv;
+    float s0, s1;
+    unpair(add2(su, sv), s0, s1);
+    s0 += s1;
 #pragma unroll
-    for (int o = R::kLanes / 2; o > 0; o >>= 1) su += __shfl_xor_sync(0xffffffffu, su, o);
-    rstd = rsqrtf(su * (1.0f / (float)D) + eps);
+    for (int o = R::kLanes / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    rstd = rsqrtf(s0 * (1.0f / (float)D) + eps);
+    const uint64_t r = pair_of(rstd, rstd);
     float p[8], q[8];
     R::unpack(wa, wb, p, q);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      t.u[j] = t.u[j] * rstd * p[j];
-      t.v[j] = t.v[j] * rstd * q[j];
+    for (int j = 0; j < 4; ++j) {
+      u[j] = mul2(mul2(u[j], r), pair_of(p[2 * j], p[2 * j + 1]));
+      v[j] = mul2(mul2(v[j], r), pair_of(q[2 * j], q[2 * j + 1]));
     }
   }
   unsigned bits = 0;
   if (rotated) {
+    // (the roundings are those of rope_first and rope_second: a product, then a fused sum)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float p = t.u[j], q = t.v[j];
-      t.u[j] = rope_first(p, q, cs[j], sn[j]);
-      t.v[j] = rope_second<false>(p, q, cs[j], sn[j]);
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t c = pair_of(cs[2 * j], cs[2 * j + 1]), n = pair_of(sn[2 * j], sn[2 * j + 1]);
+      const uint64_t a = fma2(u[j], c, mul2(v[j], pair_of(-sn[2 * j], -sn[2 * j + 1])));
+      v[j] = fma2(u[j], n, mul2(v[j], c));
+      u[j] = a;
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    unpair(u[j], t.u[2 * j], t.u[2 * j + 1]);
+    unpair(v[j], t.v[2 * j], t.v[2 * j + 1]);
+  }
+  if (rotated) {
     if (kBits && key)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // |p| + |q| is at most 2^0.5 of the turned pair's length
-        const float r = 0x1.7p-11f * (fabsf(t.u[j]) + fabsf(t.v[j]));
+      for (int j = 0; j < 8; ++j) {
+        // fp32 is off by 7.5 2^-24 of |p| + |q| at most, half a bf16 step is 2^-9 of the value, and |p| + |q|
+        // at most 2^0.5 of the turned pair's length
+        const float r = 0x1.7p-12f * (fabsf(t.u[j]) + fabsf(t.v[j]));
         bits |= (fabsf(t.u[j]) < r ? 1u << j : 0u) | (fabsf(t.v[j]) < r ? 0x100u << j : 0u);
       }
   }
@@ -382,6 +402,36 @@ __device__ __forceinline__ float amax_of(const Turned &t) {
   return m;
 }
 
+// An element of a key to be formed again when a block or a group of threads is done with the others.
+struct Fix {
+  const __nv_bfloat16 *src;
+  void *dst;
+  int pos, place;  // place: the row's lane, and the element's bit
+  float scale_or_rstd;
+};
+constexpr int kFixes = 64;
+// This lane's elements into a list; what it has no room for is left in `bits`.
+__device__ __forceinline__ void put_off(Fix *fixes, int *count, const __nv_bfloat16 *src, void *dst,
+                                        int pos, int l, float scale_or_rstd, unsigned &bits) {
+  for (; bits != 0; bits &= bits - 1) {
+    const int k = atomicAdd(count, 1);
+    if (k >= kFixes) break;
+    fixes[k] = Fix{src, dst, pos, l * 16 + __ffs(bits) - 1, scale_or_rstd};
+  }
+}
+// The list, a lane each, by threads `of` them (whole warps).
+template <int D, bool kInterleaved, bool kE4m3>
+__device__ __forceinline__ void work_off(const AppendArgs &a, const RopeTurns &turns, const Fix *fixes,
+                                         int count, int thread, int of) {
+  count = min(count, kFixes);
+  for (int k = thread; (k & ~31) < count; k += of) {
+    const Fix f = fixes[k < count ? k : 0];
+    exact_elements<D, kInterleaved, kE4m3>(f.src, a.k_norm_w, f.dst, f.scale_or_rstd, a.eps, f.pos,
+                                           a.rot, f.place >> 4, turns.v,
+                                           k < count ? 1u << (f.place & 15) : 0u);
+  }
+}
+
 // ---- rows: (token, head) pairs that need nothing of each other ------------------------------
 // Heads are counted q, k, v. A block has tok_par tokens side by side, times as many heads as fit,
 // and goes through its heads_per heads with them: a lane keeps its token's angles.
@@ -401,13 +451,14 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   R::places(l, a.rot, ea, eb);
   // a head's two groups of this lane, on their way while the one before is turned (the first while the
   // token's place is looked up)
+  const __nv_bfloat16 *q_src = a.q_in + i * a.q_ld;
+  const __nv_bfloat16 *k_src = a.k_new + i * a.k_ld - (ptrdiff_t)a.Hq * D;
+  const __nv_bfloat16 *v_src = a.v_new + i * a.v_ld - (ptrdiff_t)(a.Hq + a.Hkv) * D;
+  __nv_bfloat16 *q_dst = a.q_out + i * a.qo_ld;
   auto load = [&](int h, uint4 &x, uint4 &y) {
     x = y = make_uint4(0u, 0u, 0u, 0u);
     if (i < a.n && h < h1) {
-      const __nv_bfloat16 *src = !kAll || h < a.Hq ? a.q_in + i * a.q_ld + (size_t)h * D
-                                 : h < a.Hq + a.Hkv
-                                     ? a.k_new + i * a.k_ld + (size_t)(h - a.Hq) * D
-                                     : a.v_new + i * a.v_ld + (size_t)(h - a.Hq - a.Hkv) * D;
+      const __nv_bfloat16 *src = (!kAll || h < a.Hq ? q_src : h < a.Hq + a.Hkv ? k_src : v_src) + h * D;
       x = *reinterpret_cast<const uint4 *>(src + ea);
       y = *reinterpret_cast<const uint4 *>(src + eb);
     }
@@ -424,6 +475,14 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     if (rotated && some) quick_sincos(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
   }
   const int in_page = at.pos & ((1 << a.page_log2) - 1);
+  // keys of bf16 pages: within one step where the rotation cancels, worked off at the end
+  constexpr bool kList = kAll && !kE4m3;
+  __shared__ Fix s_fixes[kList ? kFixes : 1];
+  __shared__ int s_fix_total;
+  if (kList) {
+    if (threadIdx.x == 0) s_fix_total = 0;
+    __syncthreads();
+  }
   for (int hh = h0; hh < h1; hh += step) {  // (the same number of times in every lane)
     const int h = hh + row / a.tok_par;
     const bool is_q = !kAll || h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
@@ -441,7 +500,8 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     }
     unsigned bits = 0;
     float rstd = 1.f;
-    if (turns_here || norm)  // (a warp may hold values beside keys: the norm's shuffles)
+    // (a warp may hold values beside keys: the norm's shuffles)
+    if (!kAll || (norm ? __any_sync(0xffffffffu, turns_here) : turns_here))
       bits = turn<D, kInterleaved, kAll && !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
                                             is_k, rstd);
     if (!turns_here) R::unpack(x, y, t.u, t.v);
@@ -489,7 +549,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
       uint4 ob = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
                             pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
       if (!turns_here) oa = x, ob = y;  // a copy, bit for bit
-      __nv_bfloat16 *to = is_q ? a.q_out + i * a.qo_ld + (size_t)g * D
+      __nv_bfloat16 *to = is_q ? q_dst + h * D
                                : static_cast<__nv_bfloat16 *>(is_k ? a.k_pages : a.v_pages) + slot;
       *reinterpret_cast<uint4 *>(to + ea) = oa;
       *reinterpret_cast<uint4 *>(to + eb) = ob;
@@ -502,12 +562,126 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
       *reinterpret_cast<uint2 *>(to + eb) = cb;
       dst = to;
     }
-    // bf16 keys within one step where the rotation cancels; codes of the exact key
+    if (!kAll) continue;
+    const __nv_bfloat16 *key = k_src + h * D;
     if (!live || !is_k) bits = 0;
-    if (kAll && __any_sync(0xffffffffu, bits != 0))
-      exact_elements<D, kInterleaved, kE4m3>(a.k_new + i * a.k_ld + (size_t)g * D, a.k_norm_w, dst,
-                                             kE4m3 ? scale : rstd, a.eps, at.pos, a.rot, l, turns.v,
-                                             bits);
+    if (kList) put_off(s_fixes, &s_fix_total, key, dst, at.pos, l, rstd, bits);
+    if (__any_sync(0xffffffffu, bits != 0))  // (e4m3: the codes are the exact key's)
+      exact_elements<D, kInterleaved, kE4m3>(key, a.k_norm_w, dst, kE4m3 ? scale : rstd, a.eps, at.pos,
+                                             a.rot, l, turns.v, bits);
+  }
+  if (kList) {
+    __syncthreads();
+    work_off<D, kInterleaved, false>(a, turns, s_fixes, s_fix_total, threadIdx.x, kThreads);
+  }
+}
+
+// The same for batches that fill a block with tokens: a token per row, so that every row of the block is
+// at the same head, and the heads go by in loops of their own. kAll: keys and values (bf16 pages) too.
+template <int D, bool kInterleaved, bool kAll, int kBlock>
+__device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
+                                              int which) {
+  using R = Row<D, kInterleaved>;
+  constexpr int kRows = kBlock / R::kLanes;
+  __shared__ Fix s_fixes[kAll ? kFixes : 1];
+  __shared__ int s_fix_total;
+  const int l = threadIdx.x % R::kLanes, row = threadIdx.x / R::kLanes;
+  const int block = which % a.head_blocks, tile = which / a.head_blocks;
+  const int i = tile * kRows + row, from = min(i, a.n - 1);  // (rows behind the last token read its)
+  const int h0 = block * a.heads_per, h1 = min(heads, h0 + a.heads_per);
+  const bool rotated = l < (a.rot >> 4), norm = a.q_norm_w != nullptr;
+  int ea, eb;
+  R::places(l, a.rot, ea, eb);
+  const __nv_bfloat16 *src = a.q_in + from * a.q_ld + (ptrdiff_t)h0 * D;
+  uint4 nx{}, ny{};
+  auto load = [&](const __nv_bfloat16 *at) {
+    nx = *reinterpret_cast<const uint4 *>(at + ea);
+    ny = *reinterpret_cast<const uint4 *>(at + eb);
+  };
+  if (h0 < a.Hq) load(src);  // (under way while the token's place is looked up)
+  if (kAll) {
+    if (threadIdx.x == 0) s_fix_total = 0;
+    __syncthreads();
+  }
+  const Place at = place_of(a, i);
+  const bool some = at.pos >= 0;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = 1.f;
+    sn[j] = 0.f;
+    if (rotated && some) quick_sincos(at.pos, turns.v[8 * l + j], sn[j], cs[j]);
+  }
+  auto pack = [&](const Turned &t, __nv_bfloat16 *to) {
+    float f[16];
+    R::order(t.u, t.v, f);
+    *reinterpret_cast<uint4 *>(to + ea) =
+        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7]));
+    *reinterpret_cast<uint4 *>(to + eb) =
+        make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]),
+                   pack_bf16x2(f[14], f[15]));
+  };
+  uint4 wa{}, wb{};
+  auto weights = [&](const __nv_bfloat16 *w) {
+    if (norm) {
+      wa = *reinterpret_cast<const uint4 *>(w + ea);
+      wb = *reinterpret_cast<const uint4 *>(w + eb);
+    }
+  };
+  weights(a.q_norm_w);
+  __nv_bfloat16 *q_dst = a.q_out + from * a.qo_ld + (ptrdiff_t)h0 * D;
+  const int q1 = min(h1, a.Hq);
+  for (int h = h0; h < q1; ++h, q_dst += D) {
+    const uint4 x = nx, y = ny;
+    if (h + 1 < q1) load(src += D);
+    Turned t;
+    float rstd;
+    turn<D, kInterleaved, false>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, false, rstd);
+    if (some) pack(t, q_dst);
+  }
+  if constexpr (kAll) {
+    const bool kept = some && at.page >= 0;
+    const int in_page = at.pos & ((1 << a.page_log2) - 1);
+    const size_t head = (size_t)D << a.page_log2;  // elements of a page's head
+    const size_t slot = kept ? (size_t)at.page * a.Hkv * head + (size_t)in_page * D : 0;
+    const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, a.Hkv);
+    src = a.k_new + from * a.k_ld + (ptrdiff_t)k0 * D;
+    if (k0 < k1) {
+      load(src);
+      weights(a.k_norm_w);
+    }
+    for (int g = k0; g < k1; ++g) {
+      const uint4 x = nx, y = ny;
+      const __nv_bfloat16 *key = src;
+      if (g + 1 < k1) load(src += D);
+      Turned t;
+      float rstd = 1.f;
+      unsigned bits = turn<D, kInterleaved, true>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, true,
+                                                  rstd);
+      __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.k_pages) + slot + g * head;
+      if (kept) pack(t, to);
+      else bits = 0;
+      // within one step where the rotation cancels: worked off at the end
+      put_off(s_fixes, &s_fix_total, key, to, at.pos, l, rstd, bits);
+      if (__any_sync(0xffffffffu, bits != 0))
+        exact_elements<D, kInterleaved, false>(key, a.k_norm_w, to, rstd, a.eps, at.pos, a.rot, l,
+                                               turns.v, bits);
+    }
+    const int v0 = max(h0 - a.Hq - a.Hkv, 0), v1 = min(h1 - a.Hq - a.Hkv, a.Hkv);
+    src = a.v_new + from * a.v_ld + (ptrdiff_t)v0 * D;
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.v_pages) + slot + v0 * head;
+#pragma unroll 2
+    for (int g = v0; g < v1; ++g, src += D, to += head) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(src + ea);
+      const uint4 y = *reinterpret_cast<const uint4 *>(src + eb);
+      if (kept) {
+        *reinterpret_cast<uint4 *>(to + ea) = x;
+        *reinterpret_cast<uint4 *>(to + eb) = y;
+      }
+    }
+    __syncthreads();
+    work_off<D, kInterleaved, false>(a, turns, s_fixes, s_fix_total, threadIdx.x, kBlock);
   }
 }
 
@@ -515,13 +689,6 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
 struct Run {
   int token, pos, page, count;
 };
-
-// An element of a key to be formed again.
-struct Fix {
-  int token, head, place;  // of the run; lane and bit
-  float scale;
-};
-constexpr int kFixes = 64;
 
 // One run of up to 2 * kRows tokens, for the KV heads h0 .. h1 (keys first, then values) one after the
 // other, by kGroup threads: a warp, or as many as a page's tokens take. These meet at the named barrier
@@ -654,30 +821,16 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
       }
       // The codes are the exact key's: a group's elements go into a list, which its threads work off when
       // the heads are done (on the way each would hold up the whole group).
-      if (!kWarp)
-        for (; bits != 0; bits &= bits - 1) {
-          const int k = atomicAdd(fix_count, 1);
-          if (k >= kFixes) break;  // (the rest here)
-          fixes[k] = Fix{j, g, l * 16 + __ffs(bits) - 1, scale};
-        }
+      const __nv_bfloat16 *key = a.k_new + (size_t)g * D + (r.token + j) * a.k_ld;
+      if (!kWarp) put_off(fixes, fix_count, key, dst, r.pos + j, l, scale, bits);
       if (__any_sync(0xffffffffu, bits != 0))
-        exact_elements<D, kInterleaved, true>(a.k_new + (size_t)g * D + (r.token + j) * a.k_ld,
-                                              a.k_norm_w, dst, scale, a.eps, r.pos + j, a.rot, l,
+        exact_elements<D, kInterleaved, true>(key, a.k_norm_w, dst, scale, a.eps, r.pos + j, a.rot, l,
                                               turns.v, bits);
     }
   }
   if (!kWarp) {
     together();
-    const int count = min(*fix_count, kFixes);
-    for (int k = in_group; (k & ~31) < count; k += kGroup) {  // (whole warps)
-      const Fix f = k < count ? fixes[k] : Fix{};
-      exact_elements<D, kInterleaved, true>(
-          a.k_new + (size_t)f.head * D + (r.token + f.token) * a.k_ld, a.k_norm_w,
-          static_cast<uint8_t *>(a.k_pages) +
-              ((((size_t)r.page * a.Hkv + f.head) << a.page_log2) + in_page + f.token) * D,
-          f.scale, a.eps, r.pos + f.token, a.rot, f.place >> 4, turns.v,
-          k < count ? 1u << (f.place & 15) : 0u);
-    }
+    work_off<D, kInterleaved, true>(a, turns, fixes, *fix_count, in_group, kGroup);
     together();
     if (in_group == 0) *fix_count = 0;
   }
@@ -728,8 +881,8 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
 
 // kPage = 0: every block takes rows, of queries, keys and values. Else the first row_blocks blocks take
 // the queries' rows, the others the runs of e4m3 pages of kPage tokens.
-template <int D, bool kInterleaved, bool kE4m3, int kPage, int kBlock>
-__global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
+template <int D, bool kInterleaved, bool kE4m3, bool kTokens, int kPage, int kBlock>
+__global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 2)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
@@ -742,8 +895,12 @@ __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     block = is_row ? before : i - before;
     if (!is_row)
       do_runs<D, kInterleaved, kBlock, kPage>(a, turns, block);
+    else if constexpr (kTokens)
+      do_token_rows<D, kInterleaved, false, kBlock>(a, turns, a.Hq, block);
     else
       do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq, block);
+  } else if constexpr (kTokens) {
+    do_token_rows<D, kInterleaved, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   } else {
     do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   }
@@ -855,7 +1012,7 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   // Tokens side by side: as many as there are, up to a block's rows. Heads one after the other: the
   // more, the fewer angles are formed twice; as few as it takes for kBlocksPerSm blocks per SM.
   a.tok_par = 1;
-  while (a.tok_par < rows && a.tok_par < p.n) a.tok_par *= 2;
+  while (a.tok_par < rows && (runs || a.tok_par < p.n)) a.tok_par *= 2;
   const long long tiles = ((long long)p.n + a.tok_par - 1) / a.tok_par;
   const int side = rows / a.tok_par;
   a.heads_per = side;
@@ -878,12 +1035,14 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   auto go = [&](auto dim, auto layout) {
     constexpr int kD = decltype(dim)::value;
     constexpr bool kI = decltype(layout)::value;
-    auto *kernel = !c.e4m3        ? paged_append_kernel<kD, kI, false, 0, 256>
-                   : !runs        ? paged_append_kernel<kD, kI, true, 0, 256>
-                   : c.page == 16 ? paged_append_kernel<kD, kI, true, 16, 256>
-                   : c.page == 32 ? paged_append_kernel<kD, kI, true, 32, 256>
-                   : c.page == 64 ? paged_append_kernel<kD, kI, true, 64, 256>
-                                  : paged_append_kernel<kD, kI, true, 128, kD == 128 ? 512 : 256>;
+    constexpr int kLarge = kD == 128 ? 512 : 256;
+    auto *kernel = runs ? (c.page == 16   ? paged_append_kernel<kD, kI, true, true, 16, 256>
+                           : c.page == 32 ? paged_append_kernel<kD, kI, true, true, 32, 256>
+                           : c.page == 64 ? paged_append_kernel<kD, kI, true, true, 64, 256>
+                                          : paged_append_kernel<kD, kI, true, true, 128, kLarge>)
+                   : c.e4m3 ? paged_append_kernel<kD, kI, true, false, 0, 256>
+                   : side == 1 ? paged_append_kernel<kD, kI, false, true, 0, 256>
+                               : paged_append_kernel<kD, kI, false, false, 0, 256>;
     if (smem > 48 * 1024) {
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
