@@ -844,40 +844,47 @@ def alloc_paged_cache(num_pages: int, page: int, Hkv: int, D: int, dtype=E4M3, d
 
 
 def _paged(k_pages, v_pages, k_scale, v_scale, table, B: int):
-    """The cache's part of a call: (Hkv, D, num_pages, page, max_pages), addresses and type."""
+    """The cache's part of a call: Hkv, D, num_pages, page, max_pages, and the C call's arguments."""
     P, Hkv, page, D = shape = _dims4(k_pages, "k_pages", "[num_pages, Hkv, page, D]")
     dtype = k_pages.dtype
-    if dtype not in _PAGE_TYPES:
+    kind = _PAGE_TYPES.get(dtype)
+    if kind is None:
         raise TypeError(f"k_pages must be {E4M3} or {BF16}, got {dtype}")
-    if (k_scale is None) != (dtype is BF16) or (v_scale is None) != (dtype is BF16):
+    if (k_scale is None) != (kind == 1) or (v_scale is None) != (kind == 1):
         raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages have none")
+    ks = vs = None
+    if kind == 2:
+        heads = (P, Hkv)
+        ks, vs = _at(k_scale, "k_scale", F32, heads), _at(v_scale, "v_scale", F32, heads)
     if not isinstance(table, torch.Tensor):
         raise TypeError("table must be a torch.Tensor")
-    if table.dim() != 2 or table.shape[0] != B:
-        raise ValueError(f"table must be [{B}, max_pages], got {tuple(table.shape)}")
-    return ((Hkv, D, P, page, table.shape[1]),
-            (_at(k_pages, "k_pages", dtype, shape), _at(v_pages, "v_pages", dtype, shape),
-             _PAGE_TYPES[dtype], _maybe_at(k_scale, "k_scale", F32, (P, Hkv)),
-             _maybe_at(v_scale, "v_scale", F32, (P, Hkv)),
-             _at(table, "table", I32, (B, table.shape[1])), table.shape[1]))
+    entries = table.shape
+    if len(entries) != 2 or entries[0] != B:
+        raise ValueError(f"table must be [{B}, max_pages], got {tuple(entries)}")
+    M = entries[1]
+    return Hkv, D, P, page, M, (_at(k_pages, "k_pages", dtype, shape),
+                                _at(v_pages, "v_pages", dtype, shape), kind, ks, vs,
+                                _at(table, "table", I32, entries), M)
 
 
-def _tokens(t, name: str, heads, D: int, n=None):
-    """A [n, heads, D] bf16 tensor whose tokens may lie apart: its address and token stride."""
+def _tokens(t, name: str, shape):
+    """A bf16 tensor [n, heads, D] whose tokens may lie apart: its address and token stride."""
+    if type(t) is torch.Tensor and t.dtype is BF16 and t.is_cuda and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not BF16:
         raise TypeError(f"{name} must be {BF16}, got {t.dtype}")
     if not t.is_cuda and not t.is_pinned():
         raise ValueError(f"{name} must be a CUDA tensor or a pinned host tensor (there is no CPU path)")
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads) or \
-            (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"({'n' if n is None else n}, {'heads' if heads is None else heads}, {D})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, heads, D = shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and t.shape[1] != 1):
+    if s2 != 1 or (s1 != D and heads != 1):
         raise ValueError(f"{name}: a token's [heads, D] must be contiguous")
-    return t.data_ptr(), s0 if t.shape[0] > 1 else t.shape[1] * D
+    return t.data_ptr(), s0 if n > 1 else heads * D
 
 
 def qknorm_rope_paged_append(q, k_new, v_new, k_pages, v_pages, table, start, theta: float,
@@ -892,18 +899,18 @@ def qknorm_rope_paged_append(q, k_new, v_new, k_pages, v_pages, table, start, th
     packed projection (tokens apart, a token's heads contiguous). ``rot_dim``: the first elements
     of a head that turn (a multiple of 16; all by default; 0: none), at theta^(-2i / rot_dim) or
     ``inv_freq`` [rot_dim / 2]. Returns the rotated q. ``start`` itself is the caller's to advance."""
-    D = _dims4(k_pages, "k_pages", "[num_pages, Hkv, page, D]")[3]
     if not isinstance(start, torch.Tensor):
         raise TypeError("start must be a torch.Tensor")
     if start.dim() != 1:
         raise ValueError(f"start must be [B], got {tuple(start.shape)}")
     B = start.shape[0]
-    (Hkv, _, P, page, _), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
-    q_at, q_ld = _tokens(q, "q", None, D)
-    n, Hq = q.shape[:2]
-    qo_at, qo_ld = (q_at, q_ld) if q_out is None else _tokens(q_out, "q_out", Hq, D, n)
-    k_at, k_ld = _tokens(k_new, "k_new", Hkv, D, n)
-    v_at, v_ld = _tokens(v_new, "v_new", Hkv, D, n)
+    Hkv, D, P, page, _, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    n, Hq, _ = _paged_q(q, "[n, Hq, D]")
+    heads, new = (n, Hq, D), (n, Hkv, D)
+    q_at, q_ld = _tokens(q, "q", heads)
+    qo_at, qo_ld = (q_at, q_ld) if q_out is None else _tokens(q_out, "q_out", heads)
+    k_at, k_ld = _tokens(k_new, "k_new", new)
+    v_at, v_ld = _tokens(v_new, "v_new", new)
     if error_word is not None:
         _need(error_word, "error_word", I32, host=True)
     rot = D if rot_dim is None else int(rot_dim)
@@ -928,11 +935,11 @@ def alloc_paged_workspace(B: int, Hq: int, Hkv: int, D: int, max_len: int, num_p
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _paged_q(q):
+def _paged_q(q, what: str = "[B, Hq, D]"):
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.dim() != 3:
-        raise ValueError(f"q must be [B, Hq, D], got {tuple(q.shape)}")
+        raise ValueError(f"q must be {what}, got {tuple(q.shape)}")
     return q.shape
 
 
@@ -945,8 +952,8 @@ def gqa_paged_attn(q, k_pages, v_pages, table, lens, k_scale=None, v_scale=None,
     last min(lens[b], window) tokens. Returns ``out`` [B, Hq, D]; a sequence without tokens
     gives zeros."""
     B, Hq, D = shape = _paged_q(q)
-    (Hkv, _, P, page, M), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
-    if k_pages.shape[3] != D:
+    Hkv, dim, P, page, M, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    if dim != D:
         raise ValueError(f"k_pages shape {tuple(k_pages.shape)} does not match q {tuple(shape)}")
     max_len = M * page if max_len is None else int(max_len)
     if workspace is None or out is None:
@@ -969,14 +976,14 @@ def paged_gather(k_pages, v_pages, table, lens, k_out, v_out, k_scale=None, v_sc
     contiguous bf16 caches k_out, v_out [B, Hkv, rows, D], at row t - start[b], as the calls that
     are not paged read them. Other rows are left as they were; at most ``rows`` tokens are copied."""
     B, Hkv, rows, D = shape = _dims4(k_out, "k_out", "[B, Hkv, rows, D]")
-    dims, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
-    if dims[:2] != (Hkv, D):
+    heads, dim, P, page, _, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    if heads != Hkv or dim != D:
         raise ValueError(f"k_out shape {tuple(shape)} does not match k_pages {tuple(k_pages.shape)}")
     if error_word is not None:
         _need(error_word, "error_word", I32, host=True)
     _call("dec_paged_gather", *cache, _maybe_at(start, "start", I32, (B,), True),
           _at(lens, "lens", I32, (B,), True), _at(k_out, "k_out", BF16, shape),
-          _at(v_out, "v_out", BF16, shape), B, Hkv, D, dims[2], dims[3], rows, _ptr(error_word),
+          _at(v_out, "v_out", BF16, shape), B, Hkv, D, P, page, rows, _ptr(error_word),
           _handle(stream))
     return k_out, v_out
 
@@ -989,7 +996,9 @@ def paged_decode_step(x, residual, norm_w, y, q, k_new, v_new, k_pages, v_pages,
     """:func:`decode_step` over a paged cache: RMSNorm + residual, the append of one token per
     sequence at pos[b] (q rotated in place), attention over lens[b] tokens, on one stream."""
     B, Hq, D = shape = _paged_q(q)
-    (Hkv, _, P, page, M), cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    Hkv, dim, P, page, M, cache = _paged(k_pages, v_pages, k_scale, v_scale, table, B)
+    if dim != D:
+        raise ValueError(f"k_pages shape {tuple(k_pages.shape)} does not match q {tuple(shape)}")
     _need(x, "x", BF16, host=True)
     hidden = x.shape[1]
     _need(workspace, "workspace", torch.uint8)

@@ -1603,7 +1603,7 @@ dec_status dec_qknorm_rope_paged_append(
   if (st != DEC_OK) return st;
   if (n == 0 || B == 0) return ok();
   if ((st = where_append(c, p)) != DEC_OK) return st;
-  const cudaError_t e = launch_paged_append(c, p, inv, as_stream(stream));
+  const cudaError_t e = launch_paged_append(c, p, inv, sm_count_of_current(), as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qknorm_rope_paged_append launch");
   return ok();
 }
@@ -1735,7 +1735,7 @@ dec_status dec_paged_decode_step(
     return st;
   cudaError_t e = launch_rmsnorm_residual(x, residual, norm_w, y, B, hidden, eps, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm_residual launch");
-  e = launch_paged_append(c, p, inv, as_stream(stream));
+  e = launch_paged_append(c, p, inv, sm_count_of_current(), as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qknorm_rope_paged_append launch");
   return paged_attn_go(c, q, lens, out, B, Hq, max_len, scale, window, num_parts, workspace, stream);
 }

@@ -986,7 +986,7 @@ int log2_of(int x) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const InvFreq &inv,
-                                cudaStream_t stream) {
+                                int sms, cudaStream_t stream) {
   AppendArgs a{};
   a.q_in = static_cast<const __nv_bfloat16 *>(p.q_in);
   a.q_out = static_cast<__nv_bfloat16 *>(p.q_out);
@@ -1006,9 +1006,6 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   // (a page of 128 tokens of 128 dims is 512 threads' work)
   const int block = runs && c.D == 128 && c.page == 128 ? 512 : 256;
   const int heads = runs ? p.Hq : p.Hq + 2 * c.Hkv, rows = block / (c.D / 16);
-  int sms = 152, dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Tokens side by side: as many as there are, up to a block's rows. Heads one after the other: the
   // more, the fewer angles are formed twice; as few as it takes for kBlocksPerSm blocks per SM.
   a.tok_par = 1;
