@@ -11,6 +11,8 @@ of that over 16, 2^-14, where it is more than 2^-8 p: with the largest weight (t
 ones are, has nothing else to be measured by). Appended keys' and values' codes and scales have no
 tolerance.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -210,6 +212,41 @@ def test_attention_scales_of_every_size(spread):
     check_attn(out, want, spread)
 
 
+def test_attention_of_8192_sequences():
+    """The most sequences of a call, none or one token each: a value or zeros."""
+    gen, rng = torch.Generator().manual_seed(32), np.random.default_rng(32)
+    for dtype in (BF16, E4M3):
+        lens = rng.integers(0, 2, 8192)
+        gpu, ref = make_cache(gen, 64, 1, 16, 64, dtype)
+        table = rng.integers(0, 64, (8192, 1))
+        q = rnd(gen, 8192, 2, 64).to(DEV)
+        out, err = attend(q, gpu, table, lens)
+        v = ref["v"][table[:, 0], 0, 0] * (1 if dtype is BF16 else ref["vs"][table[:, 0], 0][:, None])
+        want = np.where(lens[:, None, None] > 0, v[:, None, :], 0.0)
+        check_ulp(f64(out), np.broadcast_to(want, (8192, 2, 64)), "one token", 0.5)
+        assert err == 0
+
+
+def test_one_workspace_for_calls_of_every_shape():
+    """One workspace, of the largest call's size, for calls of other shapes and types in between."""
+    rng = np.random.default_rng(33)
+    shapes = [(1, 8, 8, 128, 16, [5000]), (7, 8, 1, 64, 32, [900, 3, 70, 0, 128, 1500, 2]),
+              (2, 14, 2, 64, 128, [4000, 129]), (40, 4, 4, 128, 64, list(range(1, 400, 10)))]
+    ws = torch.zeros(max(dsa.paged_workspace_bytes(B, Hq, Hkv, D, max(n))
+                         for B, Hq, Hkv, D, _, n in shapes), dtype=torch.uint8, device=DEV)
+    for turn in range(2):
+        for dtype in (E4M3, BF16):
+            for B, Hq, Hkv, D, page, lens in shapes:
+                gen = torch.Generator().manual_seed(turn + Hq)
+                P = sum(-(-n // page) for n in lens)
+                gpu, ref = make_cache(gen, P, Hkv, page, D, dtype)
+                table = make_table(rng, lens, page, P)
+                q = rnd(gen, B, Hq, D).to(DEV)
+                out, err = attend(q, gpu, table, lens, workspace=ws)
+                check_attn(out, OP.attention(f64(q), ref, table, lens), (turn, dtype, B, Hq))
+                assert err == 0
+
+
 def test_attention_scale_argument():
     gen, rng = torch.Generator().manual_seed(9), np.random.default_rng(9)
     for dtype in (BF16, E4M3):
@@ -395,6 +432,67 @@ def test_append_from_a_packed_projection(dtype, single):
     new = np.ones(9, dtype=int) if single else [40, 1, 90]
     run_append(gen, rng, dtype, 64, 16, 6, 3, "interleaved", 32, True, rng.integers(0, 50, len(new)), new,
                single=single, packed=True, in_place=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_mixed_batch(dtype, page):
+    """Prompts among many sequences that get one token each, or none: more than 32 sequences."""
+    gen, rng = torch.Generator().manual_seed(34), np.random.default_rng(34)
+    new = rng.choice([0, 1, 1, 1, 2, 9], 90)
+    new[[7, 50]] = 150, 33
+    run_append(gen, rng, dtype, 64, page, 4, 2, "neox", 64, True, rng.integers(0, 200, 90), new)
+
+
+def test_append_where_every_element_is_on_a_border():
+    """Keys that lie halfway between two codes, which only their exact value settles (ties to even),
+    in more places than the kernel's lists hold: nothing turns (frequencies of zero), as prompts and as
+    single tokens, with scales that stay and scales that grow."""
+    gen, rng = torch.Generator().manual_seed(35), np.random.default_rng(35)
+    for layout in ("neox", "interleaved"):
+        for D, page, single in ((128, 64, False), (64, 128, False), (128, 16, True), (128, 128, False)):
+            start = [0, 5, 70] if not single else [0, 3, 17, 40]
+            new = [page + 9, 40, 3] if not single else [1, 1, 1, 1]
+            B, n = len(start), sum(new)
+            P = 3 * B * (2 + 160 // page)
+            gpu, ref = make_cache(gen, P, 2, page, D, E4M3)
+            table = make_table(rng, np.add(start, new), page, P)
+            steps = torch.randint(8, 16, (n, 2, D), generator=gen).float() + 0.5
+            k = (steps * torch.exp2(torch.randint(-5, 3, (n, 2, D), generator=gen).float())).to(BF16).to(DEV)
+            q, v = rnd(gen, n, 4, D).to(DEV), rnd(gen, n, 2, D).to(DEV)
+            cu = None if single else np.concatenate([[0], np.cumsum(new)])
+            inv = torch.zeros(D // 2, dtype=torch.float64)
+            _, c = OP.append(f64(q), f64(k), f64(v), ref, table, start, cu, 1e4, layout, D,
+                             inv_freq=inv.numpy())
+            dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], i32(table), i32(start), 1e4,
+                                         cu_new=None if single else i32(cu), k_scale=gpu[2],
+                                         v_scale=gpu[3], layout=layout, inv_freq=inv)
+            assert np.array_equal(f64(gpu[2]), c["ks"])
+            assert np.array_equal(f64(gpu[0]), c["k"]), (layout, D, page, single)
+            assert np.array_equal(f64(gpu[1]), c["v"])
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_append_where_every_rotation_cancels(n):
+    """bf16 keys of equal pairs turned by an eighth of a turn: the first of each pair nearly vanishes, and
+    is within one step of what it is."""
+    gen, rng = torch.Generator().manual_seed(36), np.random.default_rng(36)
+    for layout in ("neox", "interleaved"):
+        gpu, ref = make_cache(gen, 100, 3, 16, 128, BF16)
+        start = np.full(n, 999)
+        table = rng.permutation(100)[:n][:, None].repeat(63, 1)
+        q = rnd(gen, n, 6, 128).to(DEV)
+        half = rnd(gen, n, 3, 64)
+        k = (torch.cat([half, half], -1) if layout == "neox" else half.repeat_interleave(2, -1)).to(DEV)
+        inv = torch.full((64,), math.pi / 4 / 999, dtype=torch.float64)
+        _, c = OP.append(f64(q), f64(k), f64(k), ref, table, start, None, 1e4, layout, 128,
+                         inv_freq=inv.numpy())
+        dsa.qknorm_rope_paged_append(q, k, k.clone(), gpu[0], gpu[1], i32(table), i32(start), 1e4,
+                                     layout=layout, inv_freq=inv)
+        # (what nearly vanishes goes by the angle's own rounding, 2^-64 of a turn a position)
+        small = 2.0 ** -64 * 2 * math.pi * 999 * 8
+        g, want = f64(gpu[0]), c["k"]
+        assert np.all(np.abs(g - want) <= bf16_ulp(want) + small), np.abs(g - want).max()
 
 
 def test_append_values_without_a_scale():
