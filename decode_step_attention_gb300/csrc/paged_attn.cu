@@ -17,12 +17,13 @@
 // fp32 with the running maximum. A value's scale is part of its weight: with t = z + log2(s_v), the
 // weight is 2^(t - max t) and its share of the softmax sum that over s_v.
 //
-// The tiles (128 tokens) of all (sequence, KV head) pairs form one stream, cut into equal pieces, one
-// per CTA (one per SM). A pair that lies in several pieces leaves a partial in each (O, maximum, sum,
+// The tiles (128 tokens; 256 of 64 dims in e4m3) of all (sequence, KV head) pairs form one stream, cut
+// into equal pieces, one per CTA (two CTAs per SM; one for bf16 rows of 128 dims, whose ring takes
+// the shared memory). A pair that lies in several pieces leaves a partial in each (O, maximum, sum,
 // fp32); the CTA that delivers a pair's last partial joins them when its own piece is done, in the
-// order of the pieces, so that results do not depend on who that is. Counters are indexed by the piece in which a pair
-// begins (one at most goes on from a piece), not by the pair, so that they lie in the same place
-// for every shape and a workspace may serve several.
+// order of the pieces, so that results do not depend on who that is. Counters are indexed by the piece
+// in which a pair begins (one at most goes on from a piece), not by the pair, so that they lie in the
+// same place for every shape and a workspace may serve several.
 //
 // Inside a CTA a tile goes through, each a step behind the other:
 //   warp 8       page numbers (a batch ahead), the pages' K and V boxes by TMA into a ring of shared
@@ -32,6 +33,22 @@
 //   warps 0-3    a token per thread: scores, weights, their sums
 //   warp 11      the value product of the 32 tokens of each of these warps
 //   warps 4-7    a dimension per thread: the running O, and a segment's end
+//
+// Pages that end inside a tile, windows and lengths cost nothing but the rows they leave unused: only
+// pages with a token that is seen are copied, and rows of V that are not seen are cleared.
+//
+// What bounds it, and what it measured (us as a user's call with a workspace of its own; GB/s of K and V
+// read; a plain copy moves 6687 GB/s):
+//   256 ragged sequences (539 MB), 4 KV heads of 128, e4m3         86   6.2 TB/s   memory, and that
+//                                                    equal pieces take the SMs 10-15% unequal times
+//   32 sequences of 512 .. 8192 tokens, 8 KV heads of 128, bf16    90   6.4 TB/s   the same
+//   131072 tokens of one sequence, 8 KV heads of 128, e4m3         47   5.7 TB/s   start and joining
+//   192 windows of 4095 tokens, 2 KV heads of 64, e4m3             37   4.7 TB/s   start (a third),
+//                                                    then the instructions of the weights
+//   512 tokens, 8 KV heads of 128, e4m3                            12              the call (8 on the GPU)
+// The steps that led here (the serving mix): one CTA per SM 168, two 124, weights relative to a base
+// that stays while it is near 92, partials joined from bulk copies 90, a segment as one tile 86. A
+// kernel of plain loads and fp32 sums took 2126.
 #include <cuda_fp8.h>
 #include <limits.h>
 #include <math.h>
@@ -457,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         const int d = n % ND, ks = (2 * n) % S, vs = (2 * n + 1) % S;
         // pages p0 .. p1 of the tile hold tokens that are seen; a lane each
         const int p0 = lo >> page_log2, p1 = (hi + page - 1) >> page_log2;
-        const int number = __shfl_sync(0xffffffffu, cur.page, ((i - cur.from) << ppt_log2) + (lane & (ppt - 1)));
+        const int number =
+            __shfl_sync(0xffffffffu, cur.page, ((i - cur.from) << ppt_log2) + (lane & (ppt - 1)));
         const bool here = lane >= p0 && lane < p1;
         const bool good = number >= 0 && number < c.num_pages;
         const int head = good ? number * c.Hkv + cur.g : -1;  // (-1: the copy leaves zeros)

@@ -10,9 +10,27 @@
 // Append: per token i of sequence b at position p = start[b] + i the step of
 // qknorm_rope_append.cu (fusedtok README, "Operators": RoPE with a kv-cache position offset;
 // cutileGPT README, "The current runtime includes": fused QK-Norm + RoPE + KV-cache writes), the
-// first rot_dim elements of a head rotated.
+// first rot_dim elements of a head rotated. Two kinds of work:
+//   rows   a (token, head) by D / 16 lanes, 16 elements each: queries, and keys and values wherever a
+//          page's scale needs no other token (bf16 pages; one token per sequence)
+//   runs   the tokens of a call that share an e4m3 page, which one scale has to hold: read once, the
+//          largest magnitude over all of them, then coded from registers
+// A key's code is the nearest to the exact rotated key. The fp32 value settles it but where it lies
+// within fp32's error of the border between two codes: those elements (one in some thousands) are formed
+// again in fp64. The same for bf16 keys whose rotation cancels.
+//
+// What bounds it, and what it measured (us on the GPU; TB/s of what is read and written):
+//   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  59  4.7  the rows alone 35 (memory),
+//       the runs alone 38: the keys' instructions, a quarter of them for the borders of codes
+//   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  42  5.4  memory
+//   256 single tokens, 16 + 4 heads, e4m3  8.3  the chain of look-up, scale, rotation, exact elements
+//   one token  3.7  the launch
+// One warp per run and general sines measured 218 and 84 for the first two; short series 124, the
+// exact elements off the common path 95, a run's angles once for several heads 81, rows and runs side
+// by side 71, tokens that fill a block 66 and 47, heads on their way in shared memory 59 and 42.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "dec_device.cuh"
@@ -22,8 +40,11 @@
 namespace decattn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 4, kMostWarps = 16;
+constexpr int kThreads = 256;  // of a block; 512 where a page takes as many
+// Heads are spread over more blocks until there are so many per SM. (The prompts and chunks above, us with
+// 2, 4, 6, 8 and 12: 64.6 and 50.6, 59.9 and 41.9, 64.0 and 43.5, 63.9 and 43.5, 81.3 and 49.6.)
+constexpr int kBlocksPerSm = 4;
+constexpr int kMostWarps = 16;
 constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest
 
 // A row (token, head) is D / 16 lanes; a lane has two groups of 8 elements, u and v, of which u[j]
@@ -276,7 +297,7 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
     if (kBits && key)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // fp32 is off by 7.5 2^-24 of |p| + |q| at most, half a bf16 step is 2^-9 of the value, and |p| + |q|
+        // fp32 is off by 7.5 2^-24 of |p| + |q| at most, half a bf16 step is 2^-9 of the value, |p| + |q|
         // at most 2^0.5 of the turned pair's length
         const float r = 0x1.7p-12f * (fabsf(t.u[j]) + fabsf(t.v[j]));
         bits |= (fabsf(t.u[j]) < r ? 1u << j : 0u) | (fabsf(t.v[j]) < r ? 0x100u << j : 0u);
@@ -293,9 +314,9 @@ __device__ __forceinline__ float sticky(double x) {
 }
 
 // Elements of a key whose fp32 value does not settle the stored one (bits of this lane's 16: u, then
-// v; l: its place in the row), again in fp64 from the inputs, and written over. The whole warp calls it; rare. A bf16 value takes
-// the row's fp32 norm (1 without it), a code the exact one, whose sum of squares the warp forms
-// together (by one lane, 8 us of a small call).
+// v; l: its place in the row), again in fp64 from the inputs, and written over. The whole warp calls it;
+// rare. A bf16 value takes the row's fp32 norm (1 without it), a code the exact one, whose sum of squares
+// the warp forms together (by one lane, 8 us of a small call).
 template <int D, bool kInterleaved, bool kE4m3>
 __device__ __noinline__ void exact_elements(const __nv_bfloat16 *src, const __nv_bfloat16 *w,
                                             void *dst, float scale_or_rstd, float eps, int pos, int rot,
@@ -576,13 +597,67 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   }
 }
 
+// Copies of 16 bytes into shared memory, to be read by the warp: loads on their way without registers.
+// `bytes` of 0 leaves zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups of copies have arrived.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+
+// Where the rows of a block's lanes lie in shared memory while they are on their way: row after row in
+// chunks of 16 bytes, every second 128 bytes with neighbours swapped, so that eight lanes that read
+// every second chunk meet 32 banks. A lane copies chunks l and l + kLanes of its row, whole sectors side
+// by side, and reads those that it turns, after the warp has met.
+template <int D, bool kInterleaved, int kBlock>
+struct RowsAhead {
+  using R = Row<D, kInterleaved>;
+  static constexpr int kBytes = 32 * kBlock;
+  uint32_t to_a, to_b, from_a, from_b;
+  int l;
+  __device__ __forceinline__ RowsAhead(uint32_t base, int l_, int ea, int eb) : l(l_) {
+    const int row = (int)threadIdx.x / R::kLanes * (D / 8);
+    auto at = [&](int chunk) {
+      const int i = row + chunk;
+      return base + ((i ^ ((i >> 3) & 1)) << 4);
+    };
+    to_a = at(l);
+    to_b = at(l + R::kLanes);
+    from_a = at(ea >> 3);
+    from_b = at(eb >> 3);
+  }
+  // (at: 0, kBytes, 2 kBytes ..; row: of the lane's own element 8 l)
+  __device__ __forceinline__ void copy(int at, const __nv_bfloat16 *row, int bytes = 16) const {
+    copy16(to_a + at, row, bytes);
+    copy16(to_b + at, row + 8 * R::kLanes, bytes);
+  }
+};
+
 // The same for batches that fill a block with tokens: a token per row, so that every row of the block is
 // at the same head, and the heads go by in loops of their own. kAll: keys and values (bf16 pages) too.
+// kHeadsAhead heads are on their way while one is turned, in dynamic shared memory (the prompts and chunks
+// above, us with 1, 2, 3, 5 and 7: 62.1 and 42.7, 60.4 and 41.3, 59.9 and 41.9, 59.5 and 42.6, 67.8 and
+// 41.5; one in registers 65.7 and 47.2).
+constexpr int kHeadsAhead = 3;
 template <int D, bool kInterleaved, bool kAll, int kBlock>
 __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
                                               int which) {
   using R = Row<D, kInterleaved>;
   constexpr int kRows = kBlock / R::kLanes;
+  extern __shared__ __align__(128) float s_table[];
   __shared__ Fix s_fixes[kAll ? kFixes : 1];
   __shared__ int s_fix_total;
   const int l = threadIdx.x % R::kLanes, row = threadIdx.x / R::kLanes;
@@ -592,13 +667,38 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
   const bool rotated = l < (a.rot >> 4), norm = a.q_norm_w != nullptr;
   int ea, eb;
   R::places(l, a.rot, ea, eb);
-  const __nv_bfloat16 *src = a.q_in + from * a.q_ld + (ptrdiff_t)h0 * D;
-  uint4 nx{}, ny{};
-  auto load = [&](const __nv_bfloat16 *at) {
-    nx = *reinterpret_cast<const uint4 *>(at + ea);
-    ny = *reinterpret_cast<const uint4 *>(at + eb);
+  const RowsAhead<D, kInterleaved, kBlock> ahead(smem_addr(s_table), l, ea, eb);
+  // the next head's row, and its place
+  const __nv_bfloat16 *const k_row = a.k_new + from * a.k_ld + 8 * l, *const v_row =
+      a.v_new + from * a.v_ld + 8 * l;
+  const __nv_bfloat16 *next = !kAll || h0 < a.Hq ? a.q_in + from * a.q_ld + (ptrdiff_t)h0 * D + 8 * l
+                              : h0 < a.Hq + a.Hkv ? k_row + (ptrdiff_t)(h0 - a.Hq) * D
+                                                  : v_row + (ptrdiff_t)(h0 - a.Hq - a.Hkv) * D;
+  int next_h = h0, next_at = 0, head_at = 0;
+  auto after = [&](int at) { return at == kHeadsAhead * ahead.kBytes ? 0 : at + ahead.kBytes; };
+  auto fetch = [&]() {
+    if (next_h < h1) {
+      ahead.copy(next_at, next);
+      next += D;
+      ++next_h;
+      if (kAll && next_h == a.Hq) next = k_row;
+      if (kAll && next_h == a.Hq + a.Hkv) next = v_row;
+    }
+    next_at = after(next_at);
+    copies_end();
   };
-  if (h0 < a.Hq) load(src);  // (under way while the token's place is looked up)
+  uint4 x, y;
+  auto take = [&](uint32_t at_a, uint32_t at_b) {  // this lane's part of the next head
+    __syncwarp();  // (the head before has been read, its place is the next one's)
+    fetch();
+    copies_wait<kHeadsAhead>();
+    __syncwarp();
+    x = shared16(at_a + head_at);
+    y = shared16(at_b + head_at);
+    head_at = after(head_at);
+  };
+#pragma unroll
+  for (int k = 0; k < kHeadsAhead; ++k) fetch();  // (under way while the place is looked up)
   if (kAll) {
     if (threadIdx.x == 0) s_fix_total = 0;
     __syncthreads();
@@ -630,11 +730,10 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
     }
   };
   weights(a.q_norm_w);
+  int h = h0;
   __nv_bfloat16 *q_dst = a.q_out + from * a.qo_ld + (ptrdiff_t)h0 * D;
-  const int q1 = min(h1, a.Hq);
-  for (int h = h0; h < q1; ++h, q_dst += D) {
-    const uint4 x = nx, y = ny;
-    if (h + 1 < q1) load(src += D);
+  for (const int q1 = min(h1, a.Hq); h < q1; ++h, q_dst += D) {
+    take(ahead.from_a, ahead.from_b);
     Turned t;
     float rstd;
     turn<D, kInterleaved, false>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, false, rstd);
@@ -645,16 +744,10 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
     const int in_page = at.pos & ((1 << a.page_log2) - 1);
     const size_t head = (size_t)D << a.page_log2;  // elements of a page's head
     const size_t slot = kept ? (size_t)at.page * a.Hkv * head + (size_t)in_page * D : 0;
-    const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, a.Hkv);
-    src = a.k_new + from * a.k_ld + (ptrdiff_t)k0 * D;
-    if (k0 < k1) {
-      load(src);
-      weights(a.k_norm_w);
-    }
-    for (int g = k0; g < k1; ++g) {
-      const uint4 x = nx, y = ny;
-      const __nv_bfloat16 *key = src;
-      if (g + 1 < k1) load(src += D);
+    if (h < h1) weights(a.k_norm_w);
+    for (const int k1 = min(h1, a.Hq + a.Hkv); h < k1; ++h) {
+      take(ahead.from_a, ahead.from_b);
+      const int g = h - a.Hq;
       Turned t;
       float rstd = 1.f;
       unsigned bits = turn<D, kInterleaved, true>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, true,
@@ -663,21 +756,19 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
       if (kept) pack(t, to);
       else bits = 0;
       // within one step where the rotation cancels: worked off at the end
+      const __nv_bfloat16 *key = a.k_new + from * a.k_ld + (ptrdiff_t)g * D;
       put_off(s_fixes, &s_fix_total, key, to, at.pos, l, rstd, bits);
       if (__any_sync(0xffffffffu, bits != 0))
         exact_elements<D, kInterleaved, false>(key, a.k_norm_w, to, rstd, a.eps, at.pos, a.rot, l,
                                                turns.v, bits);
     }
-    const int v0 = max(h0 - a.Hq - a.Hkv, 0), v1 = min(h1 - a.Hq - a.Hkv, a.Hkv);
-    src = a.v_new + from * a.v_ld + (ptrdiff_t)v0 * D;
-    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.v_pages) + slot + v0 * head;
-#pragma unroll 2
-    for (int g = v0; g < v1; ++g, src += D, to += head) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(src + ea);
-      const uint4 y = *reinterpret_cast<const uint4 *>(src + eb);
+    for (; h < h1; ++h) {
+      take(ahead.to_a, ahead.to_b);
+      __nv_bfloat16 *to =
+          static_cast<__nv_bfloat16 *>(a.v_pages) + slot + (h - a.Hq - a.Hkv) * head + 8 * l;
       if (kept) {
-        *reinterpret_cast<uint4 *>(to + ea) = x;
-        *reinterpret_cast<uint4 *>(to + eb) = y;
+        *reinterpret_cast<uint4 *>(to) = x;
+        *reinterpret_cast<uint4 *>(to + 8 * R::kLanes) = y;
       }
     }
     __syncthreads();
@@ -690,15 +781,18 @@ struct Run {
   int token, pos, page, count;
 };
 
-// One run of up to 2 * kRows tokens, for the KV heads h0 .. h1 (keys first, then values) one after the
-// other, by kGroup threads: a warp, or as many as a page's tokens take. These meet at the named barrier
-// `meet` and have the run's angles in `table`: [token][4 pairs of each lane, then the others] cosines,
-// then the sines.
-constexpr int kPasses = 2;
-template <int D, bool kInterleaved, int kGroup>
+// One run of up to kPasses * kRows tokens, for the KV heads h0 .. h1 (keys first, then values) one after
+// the other, by kGroup threads: a warp, or as many as a page's tokens take. These meet at the named
+// barrier `meet` and have the run's angles in `table`: [token][4 pairs of each lane, then the others]
+// cosines, then the sines.
+// Rows of 128 dims, and pages of 128 tokens, go two tokens to a row's lanes: half the threads to meet.
+// (12.6 k tokens of prompts, us with one token and with two; 128 dims, pages of 16 and 32: 62.2, 59.6 and
+// 64.1, 59.4; 64 dims, pages of 16, 32, 64 and 128: 35.8, 53.2; 37.2, 42.1; 37.6, 43.0 and 48.7, 42.8.)
+__host__ __device__ constexpr int passes_of(int D, int page) { return D == 128 || page == 128 ? 2 : 1; }
+template <int D, bool kInterleaved, int kGroup, int kBlock, int kPasses>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
-                                       int h0, int h1, float *s_max, float *table, Fix *fixes,
-                                       int *fix_count, int meet) {
+                                       int h0, int h1, uint32_t slots, float *s_max, float *table,
+                                       Fix *fixes, int *fix_count, int meet) {
   using R = Row<D, kInterleaved>;
   constexpr bool kWarp = kGroup == 32;
   constexpr int kRows = kGroup / R::kLanes;   // tokens side by side
@@ -731,29 +825,42 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
     }
     together();
   }
+  // a head's rows, on their way while the one before is coded
+  const RowsAhead<D, kInterleaved, kBlock> ahead(slots, l, ea, eb);
+  auto fetch = [&](int head) {
+    if (head < h1) {
+      const bool is_k = head < a.Hkv;
+      const __nv_bfloat16 *src =
+          (is_k ? a.k_new : a.v_new) + (size_t)(is_k ? head : head - a.Hkv) * D + 8 * l;
+      const long long ld = is_k ? a.k_ld : a.v_ld;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int j = p * kRows + row;  // (rows behind the run's last token: zeros)
+        ahead.copy(p * ahead.kBytes, src + (r.token + min(j, r.count - 1)) * ld, j < r.count ? 16 : 0);
+      }
+    }
+    copies_end();
+  };
+  fetch(h0);
   for (int head = h0; head < h1; ++head) {
     const bool is_k = head < a.Hkv;
     const int g = is_k ? head : head - a.Hkv;
-    const __nv_bfloat16 *src = (is_k ? a.k_new : a.v_new) + (size_t)g * D;
-    const long long ld = is_k ? a.k_ld : a.v_ld;
     float *sp = (is_k ? a.k_scale : a.v_scale) + (size_t)r.page * a.Hkv + g;
     uint8_t *base = static_cast<uint8_t *>(is_k ? a.k_pages : a.v_pages) +
                     (((size_t)r.page * a.Hkv + g) << a.page_log2) * D;
     uint4 x[kPasses], y[kPasses], wa{}, wb{};
     float m = 0.f, old = 0.f;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int j = p * kRows + row;
-      x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < r.count) {
-        x[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + ea);
-        y[p] = *reinterpret_cast<const uint4 *>(src + (r.token + j) * ld + eb);
-      }
-    }
     if (in_page > 0) old = *sp;
     if (is_k && norm) {
       wa = *reinterpret_cast<const uint4 *>(a.k_norm_w + ea);
       wb = *reinterpret_cast<const uint4 *>(a.k_norm_w + eb);
+    }
+    copies_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      x[p] = shared16(ahead.from_a + p * ahead.kBytes);
+      y[p] = shared16(ahead.from_b + p * ahead.kBytes);
     }
     Turned t[kPasses];
 #pragma unroll
@@ -787,6 +894,7 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    fetch(head + 1);  // (its place has been read by the whole warp)
     if (!kWarp) {
       // (two sets of maxima in turn: a warp may be a head ahead of the group's others)
       float *mine = s_max + ((head & 1) ? kMostWarps : 0) + (threadIdx.x / kGroup) * (kGroup / 32);
@@ -816,8 +924,12 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
         uint2 ca, cb;
         bits = encode<D, kInterleaved>(t[p], scale, is_k && (norm || turned) ? slack(norm) : 0.f, ca,
                                        cb);
-        *reinterpret_cast<uint2 *>(dst + ea) = ca;
-        *reinterpret_cast<uint2 *>(dst + eb) = cb;
+        if (kInterleaved) {  // (16 neighbours)
+          *reinterpret_cast<uint4 *>(dst + ea) = make_uint4(ca.x, ca.y, cb.x, cb.y);
+        } else {
+          *reinterpret_cast<uint2 *>(dst + ea) = ca;
+          *reinterpret_cast<uint2 *>(dst + eb) = cb;
+        }
       }
       // The codes are the exact key's: a group's elements go into a list, which its threads work off when
       // the heads are done (on the way each would hold up the whole group).
@@ -841,9 +953,10 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
 template <int D, bool kInterleaved, int kBlock, int kPage>
 __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) {
   using R = Row<D, kInterleaved>;
-  constexpr int kGroup = kPage * R::kLanes / kPasses;  // 32 (16 tokens of 64 dims) .. 512
+  constexpr int kPasses = passes_of(D, kPage);
+  constexpr int kGroup = kPage * R::kLanes / kPasses;  // 64 (16 tokens of 64 dims) .. 512
   constexpr int kChunk = kPage > 64 ? kPage : 64, kWarpRun = kPasses * 32 / R::kLanes;
-  extern __shared__ __align__(16) float s_table[];  // of each group: kPage * D
+  extern __shared__ __align__(128) float s_table[];  // of each group: kPage * D
   __shared__ Run s_run[kChunk];
   __shared__ int s_short, s_long, s_fix_count[kBlock / kGroup];
   __shared__ float s_max[2 * kMostWarps];
@@ -866,23 +979,26 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   }
   __syncthreads();
   const int shorts = s_short, longs = s_long;
+  const uint32_t slots = smem_addr(s_table) + kBlock / kGroup * kPage * D * 4;  // (behind the tables)
   for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
-    do_run<D, kInterleaved, 32>(a, turns, s_run[k], h0, h1, nullptr, nullptr, nullptr, nullptr, 0);
-  if constexpr (kGroup > 32)
-    for (int k = threadIdx.x / kGroup; k < longs; k += kBlock / kGroup) {
-      const int group = threadIdx.x / kGroup;
-      do_run<D, kInterleaved, kGroup>(a, turns, s_run[kChunk - 1 - k], h0, h1, s_max,
-                                      s_table + group * kPage * D, s_fix[group], &s_fix_count[group],
-                                      1 + group);
-      // (the next run's angles and maxima take this one's place)
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory");
-    }
+    do_run<D, kInterleaved, 32, kBlock, kPasses>(a, turns, s_run[k], h0, h1, slots, nullptr, nullptr,
+                                                 nullptr, nullptr, 0);
+  const int group = threadIdx.x / kGroup;
+  for (int k = group; k < longs; k += kBlock / kGroup) {
+    do_run<D, kInterleaved, kGroup, kBlock, kPasses>(
+        a, turns, s_run[kChunk - 1 - k], h0, h1, slots, s_max, s_table + group * kPage * D, s_fix[group],
+        &s_fix_count[group], 1 + group);
+    // (the next run's angles and maxima take this one's place)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory");
+  }
 }
 
 // kPage = 0: every block takes rows, of queries, keys and values. Else the first row_blocks blocks take
 // the queries' rows, the others the runs of e4m3 pages of kPage tokens.
+// (Blocks of 256 threads three to an SM, 80 registers a thread; four, with 64, spill: the prompts above 59
+// and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM 82 us, two 94.)
 template <int D, bool kInterleaved, bool kE4m3, bool kTokens, int kPage, int kBlock>
-__global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 2)
+__global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
@@ -918,7 +1034,9 @@ struct GatherArgs {
 
 constexpr int kGatherRows = 64;
 
-// One block per (64 rows, KV head, sequence): 16 elements a thread at a time, K and V.
+// One block per (64 rows, KV head, sequence): 16 elements a thread at a time, K and V. A copy that memory
+// bounds: 139 us for 32 sequences of 512 .. 8192 tokens in e4m3 (856 MB, 6.2 TB/s), 2.9 on the GPU for 512
+// tokens.
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherArgs a) {
   pdl_launch_dependents();
@@ -1004,7 +1122,7 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   a.Hq = p.Hq, a.Hkv = c.Hkv, a.rot = p.rot_dim, a.eps = p.eps;
   const bool runs = c.e4m3 && p.cu_new != nullptr;
   // (a page of 128 tokens of 128 dims is 512 threads' work)
-  const int block = runs && c.D == 128 && c.page == 128 ? 512 : 256;
+  const int block = runs && c.page * (c.D / 16) > 512 ? 512 : 256;
   const int heads = runs ? p.Hq : p.Hq + 2 * c.Hkv, rows = block / (c.D / 16);
   // Tokens side by side: as many as there are, up to a block's rows. Heads one after the other: the
   // more, the fewer angles are formed twice; as few as it takes for kBlocksPerSm blocks per SM.
@@ -1026,8 +1144,12 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
     a.run_heads *= 2;
   a.run_blocks = (2 * c.Hkv + a.run_heads - 1) / a.run_heads;
   const long long blocks = a.row_blocks + (runs ? chunks * a.run_blocks : 0);
-  // (the angles of the pages that a block has under way at a time)
-  const size_t smem = runs ? (size_t)block * kPasses / (c.D / 16) * c.D * 4 : 0;
+  // the rows on their way; of runs also the angles of the pages that a block has under way at a time
+  const size_t ahead = (size_t)block * 32;
+  const int passes = passes_of(c.D, c.page);
+  const size_t tables = (size_t)block * passes / (c.D / 16) * c.D * 4;
+  const size_t smem = runs ? std::max(tables + passes * ahead, (kHeadsAhead + 1) * ahead)
+                      : !c.e4m3 && side == 1 ? (kHeadsAhead + 1) * ahead : 0;
   const RopeTurns turns = make_rope_turns(p.rot_dim, inv);
   auto go = [&](auto dim, auto layout) {
     constexpr int kD = decltype(dim)::value;
@@ -1040,7 +1162,7 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
                    : c.e4m3 ? paged_append_kernel<kD, kI, true, false, 0, 256>
                    : side == 1 ? paged_append_kernel<kD, kI, false, true, 0, 256>
                                : paged_append_kernel<kD, kI, false, false, 0, 256>;
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // (48 KB with what the kernels declare needs no leave)
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
@@ -1062,7 +1184,7 @@ cudaError_t launch_paged_gather(const PagedCache &c, const int32_t *start, const
   const GatherArgs a{c.k_pages, c.v_pages, c.k_scale, c.v_scale, c.table, start, lens,
                      static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out),
                      error_word, c.num_pages, log2_of(c.page), c.max_pages, c.Hkv, rows};
-  const dim3 grid((unsigned)((rows + kGatherRows - 1) / kGatherRows * c.Hkv), B);
+  const dim3 grid((unsigned)(((rows - 1) / kGatherRows + 1) * c.Hkv), B);
   auto *kernel = c.D == 128 ? (c.e4m3 ? paged_gather_kernel<128, true> : paged_gather_kernel<128, false>)
                             : (c.e4m3 ? paged_gather_kernel<64, true> : paged_gather_kernel<64, false>);
   const cudaError_t e = launch_pdl(kernel, grid, kThreads, 0, stream, a);

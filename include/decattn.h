@@ -639,8 +639,9 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  *                    them; a page that an append writes to belongs to one sequence, once.
  *                    Entries that no token of the call needs may hold anything.
  *   type             DEC_BF16, or DEC_E4M3 with
- *   k_scale, v_scale [device] fp32 [num_pages, Hkv], finite and > 0 for pages that hold tokens:
- *                    a value is code * scale. NULL for DEC_BF16.
+ *   k_scale, v_scale [device] fp32 [num_pages, Hkv], finite, > 0 and not subnormal for pages that
+ *                    hold tokens: a value is code * scale. NULL for DEC_BF16. Attention wants a
+ *                    sequence's v_scales of one head within a factor of 2^100 of one another.
  * The conventions are those of the draft trees: device buffers on the current device, what a
  * call writes overlaps neither what it reads nor anything else it writes. A token whose page
  * number lies outside [0, num_pages) is skipped (not stored, not attended, not copied) and raises
@@ -657,14 +658,16 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  * bf16 pages: keys within one bf16 step of the exact value, values bit for bit.
  * e4m3 pages: with s the scale of (page, g), a power of two unless the caller wrote another,
  *   s    = the smallest power of two (2^-64 at least) with |x| <= 448 s for all finite values x
- *          that the call stores there; if the page held tokens before (the first new row is not
+ *          that the call stores there (keys as fp32 leaves them, 2^-19 of their size off at
+ *          most); if the page held tokens before (the first new row is not
  *          row 0), the old scale if that is larger. When it grows, the page's earlier codes c
  *          become e4m3(c * s_old / s).
  *   code = the nearest e4m3 value to x / s (ties to even); the keys' codes are those of the
  *          exact rotated key. Infinities become +-448 s, a NaN stays one.
  * Rows of a page behind its last token are not touched. A token with start[b] < 0, or a position
  * outside the table, is skipped and raises DEC_DEVERR_POS_SKIPPED (its q_out row is written when
- * start[b] >= 0). Tokens outside every [cu_new[b], cu_new[b + 1]) are not touched.
+ * start[b] >= 0 and the position is below 2^31). The sum of a head's squares has to stay finite in
+ * fp32 where there is a norm. Tokens outside every [cu_new[b], cu_new[b + 1]) are not touched.
  * q_in, q_out   [device|host] bf16, row (i, h) at i * q_ld + h * D (qo_ld for q_out): the same
  *               buffer and stride (in place), or not overlapping.
  * k_new, v_new  [device|host] bf16, row (i, g) at i * k_ld + g * D (v_ld): the column blocks of a
