@@ -1671,7 +1671,8 @@ dec_status dec_paged_gather(const void *k_pages, const void *v_pages, dec_dtype 
                        {error_word, "error_word", true}});
   if (st != DEC_OK) return st;
   const cudaError_t e =
-      launch_paged_gather(c, start, lens, k_out, v_out, B, rows, error_word, as_stream(stream));
+      launch_paged_gather(c, start, lens, k_out, v_out, B, rows, error_word, sm_count_of_current(),
+                          as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_gather launch");
   return ok();
 }

@@ -235,7 +235,7 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
                                 int sms, cudaStream_t stream);
 cudaError_t launch_paged_gather(const PagedCache &c, const int32_t *start, const int32_t *lens,
                                 void *k_out, void *v_out, int B, int rows, uint32_t *error_word,
-                                cudaStream_t stream);
+                                int sms, cudaStream_t stream);
 
 struct PagedAttnArgs {
   const __nv_bfloat16 *q;

@@ -1029,19 +1029,20 @@ struct GatherArgs {
   const int32_t *table, *start, *lens;  // start: may be null (0)
   __nv_bfloat16 *k_out, *v_out;
   uint32_t *error_word;
-  int num_pages, page_log2, max_pages, Hkv, rows;
+  int num_pages, page_log2, max_pages, Hkv, rows, rows_per;
 };
 
-constexpr int kGatherRows = 64;
-
-// One block per (64 rows, KV head, sequence): 16 elements a thread at a time, K and V. A copy that memory
-// bounds: 139 us for 32 sequences of 512 .. 8192 tokens in e4m3 (856 MB, 6.2 TB/s), 2.9 on the GPU for 512
-// tokens.
+// One block per (rows_per rows, KV head, sequence): 8 elements a thread at a time, K and V, so that each
+// store fills whole sectors (16 elements, two stores of half sectors: 137 us below). A copy that memory
+// bounds: 130 us for 32 sequences of 512 .. 8192 tokens in e4m3 (856 MB, 6.6 TB/s), 14.4 for 12.3 k tokens
+// of prompts, 2.1 for 512 tokens. Rows of a block, us of the three with 16, 32 and 64: 172, 136, 130; 14.8,
+// 14.4, 15.1; 2.1, 2.3, 2.8. Hence as few as kGatherBlocks blocks per SM allow.
+constexpr int kGatherBlocks = 32;
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherArgs a) {
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int g = blockIdx.x % a.Hkv, r0 = blockIdx.x / a.Hkv * kGatherRows, b = blockIdx.y;
+  const int g = blockIdx.x % a.Hkv, r0 = blockIdx.x / a.Hkv * a.rows_per, b = blockIdx.y;
   const long long cap = (long long)a.max_pages << a.page_log2;
   const int len = a.lens[b], from = a.start != nullptr ? a.start[b] : 0;
   const int L = (int)min((long long)max(len, 0), cap), S = max(from, 0);
@@ -1049,11 +1050,11 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherArgs
     if (L != len || (long long)L - S > a.rows) atomicOr(a.error_word, kErrLenClamped);
     if (S != from) atomicOr(a.error_word, kErrPosSkipped);
   }
-  const int rows = min(min(L - min(S, L), a.rows) - r0, kGatherRows);
-  constexpr int kWords = D / 16;
+  const int rows = min(min(L - min(S, L), a.rows) - r0, a.rows_per);
+  constexpr int kWords = D / 8;
   const size_t out0 = (((size_t)b * a.Hkv + g) * a.rows + r0) * D;
   for (int k = threadIdx.x; k < rows * kWords; k += kThreads) {
-    const int r = k / kWords, c = (k - r * kWords) * 16, t = S + r0 + r;
+    const int r = k / kWords, c = (k - r * kWords) * 8, t = S + r0 + r;
     const int page = a.table[(size_t)b * a.max_pages + (t >> a.page_log2)];
     if (page < 0 || page >= a.num_pages) {
       if (g == 0 && c == 0 && a.error_word != nullptr) atomicOr(a.error_word, kErrPageSkipped);
@@ -1061,37 +1062,29 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherArgs
     }
     const size_t head = (size_t)page * a.Hkv + g;
     const size_t src = ((head << a.page_log2) + (t & ((1 << a.page_log2) - 1))) * D + c;
-    uint4 out[2][2];
+    uint4 out[2];
     if (kE4m3) {
-      const uint4 w[2] = {
-          *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.k_pages) + src),
-          *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.v_pages) + src)};
+      const uint2 w[2] = {
+          *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.k_pages) + src),
+          *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.v_pages) + src)};
       const float s[2] = {a.k_scale[head], a.v_scale[head]};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t y[8];
+        const uint32_t x[2] = {w[i].x, w[i].y};
+        uint32_t y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float2 f = from_e4m3x2(j & 1 ? x[j >> 1] >> 16 : x[j >> 1] & 0xffffu);
           y[j] = pack_bf16x2(f.x * s[i], f.y * s[i]);
         }
-        out[i][0] = make_uint4(y[0], y[1], y[2], y[3]);
-        out[i][1] = make_uint4(y[4], y[5], y[6], y[7]);
+        out[i] = make_uint4(y[0], y[1], y[2], y[3]);
       }
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        out[0][h] =
-            reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k_pages) + src)[h];
-        out[1][h] =
-            reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v_pages) + src)[h];
-      }
+      out[0] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.k_pages) + src);
+      out[1] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v_pages) + src);
     }
-    uint4 *ko = reinterpret_cast<uint4 *>(a.k_out + out0 + (size_t)r * D + c);
-    uint4 *vo = reinterpret_cast<uint4 *>(a.v_out + out0 + (size_t)r * D + c);
-    ko[0] = out[0][0], ko[1] = out[0][1];
-    vo[0] = out[1][0], vo[1] = out[1][1];
+    *reinterpret_cast<uint4 *>(a.k_out + out0 + (size_t)k * 8) = out[0];
+    *reinterpret_cast<uint4 *>(a.v_out + out0 + (size_t)k * 8) = out[1];
   }
 }
 
@@ -1180,11 +1173,14 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
 
 cudaError_t launch_paged_gather(const PagedCache &c, const int32_t *start, const int32_t *lens,
                                 void *k_out, void *v_out, int B, int rows, uint32_t *error_word,
-                                cudaStream_t stream) {
+                                int sms, cudaStream_t stream) {
+  int per = 16;
+  auto blocks = [&]() { return ((long long)(rows - 1) / per + 1) * c.Hkv; };
+  while (per < 64 && blocks() * B > (long long)kGatherBlocks * sms) per *= 2;
   const GatherArgs a{c.k_pages, c.v_pages, c.k_scale, c.v_scale, c.table, start, lens,
                      static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out),
-                     error_word, c.num_pages, log2_of(c.page), c.max_pages, c.Hkv, rows};
-  const dim3 grid((unsigned)(((rows - 1) / kGatherRows + 1) * c.Hkv), B);
+                     error_word, c.num_pages, log2_of(c.page), c.max_pages, c.Hkv, rows, per};
+  const dim3 grid((unsigned)blocks(), B);
   auto *kernel = c.D == 128 ? (c.e4m3 ? paged_gather_kernel<128, true> : paged_gather_kernel<128, false>)
                             : (c.e4m3 ? paged_gather_kernel<64, true> : paged_gather_kernel<64, false>);
   const cudaError_t e = launch_pdl(kernel, grid, kThreads, 0, stream, a);

@@ -594,6 +594,24 @@ def test_gather(dtype, D, page, Hkv):
         assert int(err) == 0
 
 
+@pytest.mark.parametrize("B,rows", [(20, 600), (64, 1000)])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_gather_into_long_caches(dtype, B, rows):
+    """Room for many more rows than there are tokens, in more blocks than the SMs hold."""
+    gen, rng = torch.Generator().manual_seed(B), np.random.default_rng(B)
+    lens = rng.integers(0, 330, B)
+    P = int(sum(-(-n // 32) for n in lens))
+    gpu, ref = make_cache(gen, P, 8, 32, 64, dtype, pow2=False)
+    table = make_table(rng, lens, 32, P)
+    ko, vo = (torch.full((B, 8, rows, 64), 7.0, dtype=BF16, device=DEV) for _ in range(2))
+    dsa.paged_gather(gpu[0], gpu[1], i32(table), i32(lens), ko, vo, gpu[2], gpu[3])
+    for b, n in enumerate(lens):
+        K, V, _ = OP.tokens(ref, table, b, 0, int(n))
+        for out, want in ((ko, K), (vo, V)):
+            check_ulp(f64(out[b, :, :n]), want, "gather", 0.5)
+            assert bool((out[b, :, n:] == 7).all())
+
+
 def test_gather_flags():
     gen = torch.Generator().manual_seed(1)
     gpu, ref = make_cache(gen, 5, 1, 16, 64, BF16)
