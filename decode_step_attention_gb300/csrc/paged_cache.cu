@@ -20,14 +20,15 @@
 // again in fp64. The same for bf16 keys whose rotation cancels.
 //
 // What bounds it, and what it measured (us on the GPU; TB/s of what is read and written):
-//   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  59  4.7  the rows alone 35 (memory),
+//   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  55  5.1  the rows alone 35 (memory),
 //       the runs alone 38: the keys' instructions, a quarter of them for the borders of codes
-//   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  42  5.4  memory
-//   256 single tokens, 16 + 4 heads, e4m3  8.3  the chain of look-up, scale, rotation, exact elements
+//   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  40  5.7  memory
+//   256 single tokens, 16 + 4 heads, e4m3  8.2  the chain of look-up, scale, rotation, exact elements
 //   one token  3.7  the launch
 // One warp per run and general sines measured 218 and 84 for the first two; short series 124, the
 // exact elements off the common path 95, a run's angles once for several heads 81, rows and runs side
-// by side 71, tokens that fill a block 66 and 47, heads on their way in shared memory 59 and 42.
+// by side 71, tokens that fill a block 66 and 47, heads on their way in shared memory 57 and 40, no
+// branches where nothing is normed and all is turned 55.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -241,9 +242,10 @@ struct Turned {
   float u[8], v[8];
 };
 
-// From the elements as loaded (x, y; wa, wb: the norm's weights). kBits: the elements whose rotation
-// cancels so far that fp32 leaves them more than half a bf16 step off (u, then v).
-template <int D, bool kInterleaved, bool kBits>
+// From the elements as loaded (x, y; wa, wb: the norm's weights). kPlain: no norm, and all are turned.
+// kBits: the elements whose rotation cancels so far that fp32 leaves them more than half a bf16 step off
+// (u, then v).
+template <int D, bool kInterleaved, bool kPlain, bool kBits>
 __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm, uint4 wa, uint4 wb,
                                          float eps, bool rotated, const float (&cs)[8],
                                          const float (&sn)[8], bool key, float &rstd) {
@@ -255,7 +257,7 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
     u[j] = pair_of(t.u[2 * j], t.u[2 * j + 1]);
     v[j] = pair_of(t.v[2 * j], t.v[2 * j + 1]);
   }
-  if (norm) {
+  if (!kPlain && norm) {
     uint64_t su = mul2(u[0], u[0]), sv = mul2(v[0], v[0]);
 #pragma unroll
     for (int j = 1; j < 4; ++j) {
@@ -278,7 +280,7 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
     }
   }
   unsigned bits = 0;
-  if (rotated) {
+  if (kPlain || rotated) {
     // (the roundings are those of rope_first and rope_second: a product, then a fused sum)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -293,7 +295,7 @@ __device__ __forceinline__ unsigned turn(Turned &t, uint4 x, uint4 y, bool norm,
     unpair(u[j], t.u[2 * j], t.u[2 * j + 1]);
     unpair(v[j], t.v[2 * j], t.v[2 * j + 1]);
   }
-  if (rotated) {
+  if (kPlain || rotated) {
     if (kBits && key)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -523,7 +525,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     float rstd = 1.f;
     // (a warp may hold values beside keys: the norm's shuffles)
     if (!kAll || (norm ? __any_sync(0xffffffffu, turns_here) : turns_here))
-      bits = turn<D, kInterleaved, kAll && !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
+      bits = turn<D, kInterleaved, false, kAll && !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
                                             is_k, rstd);
     if (!turns_here) R::unpack(x, y, t.u, t.v);
     const size_t slot =
@@ -652,7 +654,7 @@ struct RowsAhead {
 // above, us with 1, 2, 3, 5 and 7: 62.1 and 42.7, 60.4 and 41.3, 59.9 and 41.9, 59.5 and 42.6, 67.8 and
 // 41.5; one in registers 65.7 and 47.2).
 constexpr int kHeadsAhead = 3;
-template <int D, bool kInterleaved, bool kAll, int kBlock>
+template <int D, bool kInterleaved, bool kPlain, bool kAll, int kBlock>
 __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
                                               int which) {
   using R = Row<D, kInterleaved>;
@@ -736,7 +738,7 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
     take(ahead.from_a, ahead.from_b);
     Turned t;
     float rstd;
-    turn<D, kInterleaved, false>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, false, rstd);
+    turn<D, kInterleaved, kPlain, false>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, false, rstd);
     if (some) pack(t, q_dst);
   }
   if constexpr (kAll) {
@@ -750,8 +752,8 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
       const int g = h - a.Hq;
       Turned t;
       float rstd = 1.f;
-      unsigned bits = turn<D, kInterleaved, true>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, true,
-                                                  rstd);
+      unsigned bits = turn<D, kInterleaved, kPlain, true>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
+                                                          true, rstd);
       __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.k_pages) + slot + g * head;
       if (kept) pack(t, to);
       else bits = 0;
@@ -789,7 +791,7 @@ struct Run {
 // (12.6 k tokens of prompts, us with one token and with two; 128 dims, pages of 16 and 32: 62.2, 59.6 and
 // 64.1, 59.4; 64 dims, pages of 16, 32, 64 and 128: 35.8, 53.2; 37.2, 42.1; 37.6, 43.0 and 48.7, 42.8.)
 __host__ __device__ constexpr int passes_of(int D, int page) { return D == 128 || page == 128 ? 2 : 1; }
-template <int D, bool kInterleaved, int kGroup, int kBlock, int kPasses>
+template <int D, bool kInterleaved, bool kPlain, int kGroup, int kBlock, int kPasses>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
                                        int h0, int h1, uint32_t slots, float *s_max, float *table,
                                        Fix *fixes, int *fix_count, int meet) {
@@ -885,7 +887,8 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
           }
         }
         // (rows behind the run's last token turn zeros by what the table holds: they are masked)
-        turn<D, kInterleaved, false>(t[p], x[p], y[p], norm, wa, wb, a.eps, turned, cs, sn, true, rstd);
+        turn<D, kInterleaved, kPlain, false>(t[p], x[p], y[p], norm, wa, wb, a.eps, turned, cs, sn, true,
+                                             rstd);
         if (j < r.count) m = fmaxf(m, amax_of(t[p]));
       } else {
         R::unpack(x[p], y[p], t[p].u, t[p].v);
@@ -950,7 +953,7 @@ __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &tur
 
 // The runs that begin among a block's `chunk` tokens, for some of the KV heads' keys and values: short
 // ones by a warp each, the others by a group of as many threads as a page takes.
-template <int D, bool kInterleaved, int kBlock, int kPage>
+template <int D, bool kInterleaved, bool kPlain, int kBlock, int kPage>
 __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &turns, int block) {
   using R = Row<D, kInterleaved>;
   constexpr int kPasses = passes_of(D, kPage);
@@ -981,23 +984,24 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   const int shorts = s_short, longs = s_long;
   const uint32_t slots = smem_addr(s_table) + kBlock / kGroup * kPage * D * 4;  // (behind the tables)
   for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
-    do_run<D, kInterleaved, 32, kBlock, kPasses>(a, turns, s_run[k], h0, h1, slots, nullptr, nullptr,
+    do_run<D, kInterleaved, kPlain, 32, kBlock, kPasses>(a, turns, s_run[k], h0, h1, slots, nullptr, nullptr,
                                                  nullptr, nullptr, 0);
   const int group = threadIdx.x / kGroup;
   for (int k = group; k < longs; k += kBlock / kGroup) {
-    do_run<D, kInterleaved, kGroup, kBlock, kPasses>(
-        a, turns, s_run[kChunk - 1 - k], h0, h1, slots, s_max, s_table + group * kPage * D, s_fix[group],
-        &s_fix_count[group], 1 + group);
+    do_run<D, kInterleaved, kPlain, kGroup, kBlock, kPasses>(
+        a, turns, s_run[kChunk - 1 - k], h0, h1, slots, s_max, s_table + group * kPage * D,
+        s_fix[group], &s_fix_count[group], 1 + group);
     // (the next run's angles and maxima take this one's place)
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory");
   }
 }
 
-// kPage = 0: every block takes rows, of queries, keys and values. Else the first row_blocks blocks take
-// the queries' rows, the others the runs of e4m3 pages of kPage tokens.
-// (Blocks of 256 threads three to an SM, 80 registers a thread; four, with 64, spill: the prompts above 59
-// and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM 82 us, two 94.)
-template <int D, bool kInterleaved, bool kE4m3, bool kTokens, int kPage, int kBlock>
+// kPage = 0: every block takes rows, of queries, keys and values. Else row_blocks of the blocks take the
+// queries' rows, the others the runs of e4m3 pages of kPage tokens. kPlain: no norm, all elements turned
+// (the two branches cost a tenth of the instructions, most of them moves: the prompts above 57 and 55 us).
+// Blocks of 256 threads go three to an SM, 80 registers a thread; four, with 64, spill: the prompts above
+// 59 and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM 82 us, two 94.
+template <int D, bool kInterleaved, bool kE4m3, bool kPlain, bool kTokens, int kPage, int kBlock>
 __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
   pdl_launch_dependents();
@@ -1010,13 +1014,13 @@ __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     const bool is_row = (unsigned)((unsigned long long)(i + 1) * rows / all) != before;
     block = is_row ? before : i - before;
     if (!is_row)
-      do_runs<D, kInterleaved, kBlock, kPage>(a, turns, block);
+      do_runs<D, kInterleaved, kPlain, kBlock, kPage>(a, turns, block);
     else if constexpr (kTokens)
-      do_token_rows<D, kInterleaved, false, kBlock>(a, turns, a.Hq, block);
+      do_token_rows<D, kInterleaved, kPlain, false, kBlock>(a, turns, a.Hq, block);
     else
       do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq, block);
   } else if constexpr (kTokens) {
-    do_token_rows<D, kInterleaved, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
+    do_token_rows<D, kInterleaved, kPlain, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   } else {
     do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   }
@@ -1144,17 +1148,17 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   const size_t smem = runs ? std::max(tables + passes * ahead, (kHeadsAhead + 1) * ahead)
                       : !c.e4m3 && side == 1 ? (kHeadsAhead + 1) * ahead : 0;
   const RopeTurns turns = make_rope_turns(p.rot_dim, inv);
-  auto go = [&](auto dim, auto layout) {
+  auto go = [&](auto dim, auto layout, auto all_turned) {
     constexpr int kD = decltype(dim)::value;
-    constexpr bool kI = decltype(layout)::value;
+    constexpr bool kI = decltype(layout)::value, kP = decltype(all_turned)::value;
     constexpr int kLarge = kD == 128 ? 512 : 256;
-    auto *kernel = runs ? (c.page == 16   ? paged_append_kernel<kD, kI, true, true, 16, 256>
-                           : c.page == 32 ? paged_append_kernel<kD, kI, true, true, 32, 256>
-                           : c.page == 64 ? paged_append_kernel<kD, kI, true, true, 64, 256>
-                                          : paged_append_kernel<kD, kI, true, true, 128, kLarge>)
-                   : c.e4m3 ? paged_append_kernel<kD, kI, true, false, 0, 256>
-                   : side == 1 ? paged_append_kernel<kD, kI, false, true, 0, 256>
-                               : paged_append_kernel<kD, kI, false, false, 0, 256>;
+    auto *kernel = runs ? (c.page == 16   ? paged_append_kernel<kD, kI, true, kP, true, 16, 256>
+                           : c.page == 32 ? paged_append_kernel<kD, kI, true, kP, true, 32, 256>
+                           : c.page == 64 ? paged_append_kernel<kD, kI, true, kP, true, 64, 256>
+                                          : paged_append_kernel<kD, kI, true, kP, true, 128, kLarge>)
+                   : c.e4m3 ? paged_append_kernel<kD, kI, true, false, false, 0, 256>
+                   : side == 1 ? paged_append_kernel<kD, kI, false, kP, true, 0, 256>
+                               : paged_append_kernel<kD, kI, false, false, false, 0, 256>;
     if (smem > 32 * 1024) {  // (48 KB with what the kernels declare needs no leave)
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1164,10 +1168,14 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   };
   using I64 = std::integral_constant<int, 64>;
   using I128 = std::integral_constant<int, 128>;
-  const cudaError_t e = c.D == 128 ? (p.interleaved ? go(I128{}, std::true_type{})
-                                                    : go(I128{}, std::false_type{}))
-                                   : (p.interleaved ? go(I64{}, std::true_type{})
-                                                    : go(I64{}, std::false_type{}));
+  const bool plain = p.k_norm_w == nullptr && p.rot_dim == c.D;
+  auto with = [&](auto dim, auto layout) {
+    return plain ? go(dim, layout, std::true_type{}) : go(dim, layout, std::false_type{});
+  };
+  const cudaError_t e = c.D == 128 ? (p.interleaved ? with(I128{}, std::true_type{})
+                                                    : with(I128{}, std::false_type{}))
+                                   : (p.interleaved ? with(I64{}, std::true_type{})
+                                                    : with(I64{}, std::false_type{}));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
