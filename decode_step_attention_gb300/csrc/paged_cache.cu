@@ -16,8 +16,8 @@
 //   runs   the tokens of a call that share an e4m3 page, which one scale has to hold: read once, the
 //          largest magnitude over all of them, then coded from registers
 // A key's code is the nearest to the exact rotated key. The fp32 value settles it but where it lies
-// within fp32's error of the border between two codes: those elements (one in some thousands) are formed
-// again in fp64. The same for bf16 keys whose rotation cancels.
+// within fp32's error of the border between two codes: those elements (one in some 50,000; 20,000
+// with a norm) are formed again in fp64. The same for bf16 keys whose rotation cancels.
 //
 // What bounds it, and what it measured (us on the GPU; TB/s of what is read and written):
 //   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  55  5.1  the rows alone 35 (memory),
