@@ -984,8 +984,8 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   const int shorts = s_short, longs = s_long;
   const uint32_t slots = smem_addr(s_table) + kBlock / kGroup * kPage * D * 4;  // (behind the tables)
   for (int k = threadIdx.x >> 5; k < shorts; k += kBlock / 32)
-    do_run<D, kInterleaved, kPlain, 32, kBlock, kPasses>(a, turns, s_run[k], h0, h1, slots, nullptr, nullptr,
-                                                 nullptr, nullptr, 0);
+    do_run<D, kInterleaved, kPlain, 32, kBlock, kPasses>(a, turns, s_run[k], h0, h1, slots, nullptr,
+                                                         nullptr, nullptr, nullptr, 0);
   const int group = threadIdx.x / kGroup;
   for (int k = group; k < longs; k += kBlock / kGroup) {
     do_run<D, kInterleaved, kPlain, kGroup, kBlock, kPasses>(

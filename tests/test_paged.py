@@ -495,6 +495,122 @@ def test_append_where_every_rotation_cancels(n):
         assert np.all(np.abs(g - want) <= bf16_ulp(want) + small), np.abs(g - want).max()
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 65, 129])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_at_the_edges_of_a_block(D, n):
+    """As many tokens as a block has rows, and one less and one more."""
+    for norm, rot in ((False, D), (True, D // 2)):
+        for layout in ("neox", "interleaved"):
+            gen, rng = torch.Generator().manual_seed(n), np.random.default_rng(n)
+            run_append(gen, rng, BF16, D, 32, 9, 3, layout, rot, norm, rng.integers(0, 90, n),
+                       np.ones(n, dtype=int), single=True, in_place=norm)
+            for dtype in (BF16, E4M3):
+                run_append(gen, rng, dtype, D, 64, 9, 3, layout, rot, norm, [7], [n], in_place=norm)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_many_heads(dtype):
+    gen, rng = torch.Generator().manual_seed(41), np.random.default_rng(41)
+    run_append(gen, rng, dtype, 64, 128, 66, 33, "neox", 64, False, [100, 0], [180, 90])
+    run_append(gen, rng, dtype, 128, 128, 33, 33, "interleaved", 128, True, [100, 0], [180, 90])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_prompts_from_host_memory(dtype):
+    gen, rng = torch.Generator().manual_seed(42), np.random.default_rng(42)
+    start, new = [3, 0], [100, 61]
+    gpu, ref = make_cache(gen, 12, 2, 16, 64, dtype)
+    table = make_table(rng, np.add(start, new), 16, 12)
+    q, k, v = (rnd(gen, 161, h, 64).pin_memory() for h in (6, 2, 2))
+    cu = torch.tensor([0, 100, 161], dtype=torch.int32).pin_memory()
+    at = torch.tensor(start, dtype=torch.int32).pin_memory()
+    q_want, c = OP.append(f64(q), f64(k), f64(v), ref, table, start, [0, 100, 161], 1e4, "neox", 64)
+    dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], i32(table), at, 1e4, cu_new=cu,
+                                 k_scale=gpu[2], v_scale=gpu[3])
+    torch.cuda.synchronize()
+    check_float(f64(q), q_want, "host q")
+    check_ulp(f64(gpu[0]), c["k"], "keys")
+    assert np.array_equal(f64(gpu[1]), c["v"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_append_prompts_captured(dtype):
+    """A captured append, replayed with other sequences, starts and tables of the same number of tokens."""
+    gen, rng = torch.Generator().manual_seed(43), np.random.default_rng(43)
+    n, B, P, page = 150, 4, 80, 32
+    gpu, _ = make_cache(gen, P, 2, page, 128, dtype)
+    q, k, v = (torch.zeros(n, h, 128, dtype=BF16, device=DEV) for h in (4, 2, 2))
+    q_out = torch.zeros_like(q)
+    table = torch.zeros(B, 16, dtype=torch.int32, device=DEV)
+    start, cu = (torch.zeros(m, dtype=torch.int32, device=DEV) for m in (B, B + 1))
+
+    def body():
+        dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], table, start, 1e4, cu_new=cu,
+                                     k_scale=gpu[2], v_scale=gpu[3], q_out=q_out)
+
+    body()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for _ in range(3):
+        s, ends = rng.integers(0, 200, B), np.sort(rng.integers(0, n + 1, B - 1))
+        c = np.concatenate([[0], ends, [n]])
+        t = make_table(rng, s + np.diff(c), page, P, width=16)
+        table.copy_(i32(t)), start.copy_(i32(s)), cu.copy_(i32(c))
+        for x in (q, k, v):
+            x.copy_(rnd(gen, *x.shape))
+        q_want, want = OP.append(f64(q), f64(k), f64(v), oracle_cache(gpu), t, s, c, 1e4, "neox", 128)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_float(f64(q_out), q_want, "captured q")
+        check_ulp(f64(gpu[0]), want["k"], "captured keys")
+        assert np.array_equal(f64(gpu[1]), want["v"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_nothing_beside_the_buffers_is_written(dtype):
+    """Guard bytes around all that append, attention and gather write."""
+    gen, rng = torch.Generator().manual_seed(44), np.random.default_rng(44)
+    B, Hq, Hkv, D, page, rows = 3, 6, 2, 64, 16, 90
+    start, new = np.array([40, 0, 15]), np.array([33, 70, 1])
+    lens, n = start + new, int(new.sum())
+    P = int(sum(-(-m // page) for m in lens))
+    gpu, ref = make_cache(gen, P, Hkv, page, D, dtype)
+    table = make_table(rng, lens, page, P)
+    pad, spaces = 4096, []
+
+    def guarded(like):
+        raw = torch.full((2 * pad + like.numel() * like.element_size(),), 0x5a, dtype=torch.uint8,
+                         device=DEV)
+        t = raw[pad:-pad].view(like.dtype).view(like.shape)
+        t.copy_(like)
+        spaces.append(raw)
+        return t
+
+    k, v, ks, vs = (None if t is None else guarded(t) for t in gpu)
+    q_out = guarded(torch.zeros(n, Hq, D, dtype=BF16, device=DEV))
+    out = guarded(torch.zeros(B, Hq, D, dtype=BF16, device=DEV))
+    ko, vo = (guarded(torch.zeros(B, Hkv, rows, D, dtype=BF16, device=DEV)) for _ in range(2))
+    ws = guarded(dsa.alloc_paged_workspace(B, Hq, Hkv, D, int(lens.max())))
+    err = guarded(torch.zeros(1, dtype=torch.int32, device=DEV))
+    q, kn, vn = (rnd(gen, n, h, D).to(DEV) for h in (Hq, Hkv, Hkv))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    dsa.qknorm_rope_paged_append(q, kn, vn, k, v, i32(table), i32(start), 1e4, cu_new=i32(cu), k_scale=ks,
+                                 v_scale=vs, q_out=q_out, error_word=err)
+    last = q_out[torch.from_numpy(cu[1:] - 1).to(DEV)].contiguous()
+    dsa.gqa_paged_attn(last, k, v, i32(table), i32(lens), ks, vs, max_len=int(lens.max()), workspace=ws,
+                       out=out)
+    dsa.paged_gather(k, v, i32(table), i32(lens), ko, vo, ks, vs, error_word=err)
+    torch.cuda.synchronize()
+    for raw in spaces:
+        assert bool((raw[:pad] == 0x5a).all()) and bool((raw[-pad:] == 0x5a).all())
+    _, want = OP.append(f64(q), f64(kn), f64(vn), ref, table, start, cu, 1e4, "neox", D)
+    check_ulp(f64(k), want["k"], "keys")
+    assert np.array_equal(f64(v), want["v"]) and int(err) == 0
+    check_attn(out, OP.attention(f64(last), oracle_cache((k, v, ks, vs)), table, lens), "out")
+
+
 def test_append_values_without_a_scale():
     """Zeros, infinities and NaN: a page of zeros has the smallest scale, and neither of the others
     sets one."""
@@ -739,6 +855,56 @@ def test_captured_and_on_another_stream(dtype):
     out.copy_(got)
     check(n, t, "stream argument")
     assert dsa.device_errors(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_pages_beyond_32_bits(dtype):
+    """A pool of more than 2^32 bytes per tensor, whose last pages are in use."""
+    gen, rng = torch.Generator().manual_seed(45), np.random.default_rng(45)
+    Hkv, page, D, used = 8, 128, 128, 20
+    P = 2 ** 32 // (Hkv * page * D * (2 if dtype is BF16 else 1)) + used
+    if torch.cuda.mem_get_info()[0] < 16 * 2 ** 30:
+        pytest.skip("needs 10 GB of device memory")
+    k, v, ks, vs = dsa.alloc_paged_cache(P, page, Hkv, D, dtype)
+    start, new = np.array([200, 0, 126]), np.array([70, 300, 1])
+    lens, n = start + new, int(new.sum())
+    near = make_table(rng, lens, page, used)
+    far = np.where(near < used, near + P - used, near)
+    gpu, ref = make_cache(gen, used, Hkv, page, D, dtype)
+    for t, x in zip((k, v, ks, vs), gpu):
+        if t is not None:
+            t[P - used:].copy_(x)
+    q, kn, vn = (rnd(gen, n, h, D).to(DEV) for h in (16, Hkv, Hkv))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q_want, want = OP.append(f64(q), f64(kn), f64(vn), ref, near, start, cu, 1e4, "neox", D)
+    dsa.qknorm_rope_paged_append(q, kn, vn, k, v, i32(far), i32(start), 1e4, cu_new=i32(cu), k_scale=ks,
+                                 v_scale=vs)
+    check_float(f64(q), q_want, "q")
+    check_ulp(f64(k[P - used:]), want["k"], "far keys")
+    assert np.array_equal(f64(v[P - used:]), want["v"])
+    last = q[torch.from_numpy(cu[1:] - 1).to(DEV)].contiguous()
+    out, err = attend(last, (k, v, ks, vs), far, lens)
+    now = oracle_cache([None if t is None else t[P - used:] for t in (k, v, ks, vs)])
+    check_attn(out, OP.attention(f64(last), now, near, lens), "far pages")
+    rows = int(lens.max())
+    ko, vo = (torch.zeros(3, Hkv, rows, D, dtype=BF16, device=DEV) for _ in range(2))
+    dsa.paged_gather(k, v, i32(far), i32(lens), ko, vo, ks, vs)
+    for b, m in enumerate(lens):
+        K, V, _ = OP.tokens(now, near, b, 0, int(m))
+        check_ulp(f64(ko[b, :, :m]), K, "gather", 0.5)
+        check_ulp(f64(vo[b, :, :m]), V, "gather", 0.5)
+    assert err == 0
+    for t in (k, v):  # (page 0, where a wrapped offset would land)
+        assert not bool(t[:used].view(torch.uint8 if dtype is E4M3 else torch.int16).any())
+
+
+def test_attention_of_no_tokens_at_all():
+    gen = torch.Generator().manual_seed(46)
+    gpu, _ = make_cache(gen, 2, 2, 16, 64, E4M3)
+    q = rnd(gen, 3, 4, 64).to(DEV)
+    for max_len in (0, 16):
+        out, err = attend(q, gpu, np.full((3, 1), -1), [0, 0, 0], max_len=max_len)
+        assert not bool(out.any()) and err == 0
 
 
 def test_host_memory():
