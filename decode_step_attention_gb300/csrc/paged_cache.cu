@@ -20,15 +20,15 @@
 // with a norm) are formed again in fp64. The same for bf16 keys whose rotation cancels.
 //
 // What bounds it, and what it measured (us on the GPU; TB/s of what is read and written):
-//   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  55  5.1  the rows alone 35 (memory),
+//   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  51  5.4  the rows alone 35 (memory),
 //       the runs alone 38: the keys' instructions, a quarter of them for the borders of codes
 //   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  40  5.7  memory
-//   256 single tokens, 16 + 4 heads, e4m3  8.2  the chain of look-up, scale, rotation, exact elements
+//   256 single tokens, 16 + 4 heads, e4m3  8.3  the chain of look-up, scale, rotation, exact elements
 //   one token  3.7  the launch
 // One warp per run and general sines measured 218 and 84 for the first two; short series 124, the
 // exact elements off the common path 95, a run's angles once for several heads 81, rows and runs side
 // by side 71, tokens that fill a block 66 and 47, heads on their way in shared memory 57 and 40, no
-// branches where nothing is normed and all is turned 55.
+// branches where nothing is normed and all is turned 55, blocks of keys before those of values 51.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -42,8 +42,9 @@ namespace decattn {
 namespace {
 
 constexpr int kThreads = 256;  // of a block; 512 where a page takes as many
-// Heads are spread over more blocks until there are so many per SM. (The prompts and chunks above, us with
-// 2, 4, 6, 8 and 12: 64.6 and 50.6, 59.9 and 41.9, 64.0 and 43.5, 63.9 and 43.5, 81.3 and 49.6.)
+// Heads are spread over more blocks until there are so many (of 256 threads) per SM. (The prompts and
+// chunks above, us with 4, 6 and 8: 51.5 and 39.9, 56.5 and 41.1, 56.4 and 41.2; two steps before, with 2, 4
+// and 12, 64.6 and 50.6, 59.9 and 41.9, 81.3 and 49.6.)
 constexpr int kBlocksPerSm = 4;
 constexpr int kMostWarps = 16;
 constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest
@@ -964,7 +965,9 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
   __shared__ int s_short, s_long, s_fix_count[kBlock / kGroup];
   __shared__ float s_max[2 * kMostWarps];
   __shared__ Fix s_fix[kBlock / kGroup][kFixes];
-  const int c0 = block / a.run_blocks * kChunk, h0 = block % a.run_blocks * a.run_heads;
+  // (the heavier blocks, those of keys, first: what is left for the end is short)
+  const int chunks = (a.n + kChunk - 1) / kChunk;
+  const int c0 = block % chunks * kChunk, h0 = block / chunks * a.run_heads;
   const int h1 = min(2 * a.Hkv, h0 + a.run_heads);
   if (threadIdx.x == 0) s_short = s_long = 0;
   if (threadIdx.x < kBlock / kGroup) s_fix_count[threadIdx.x] = 0;
@@ -1000,7 +1003,8 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
 // queries' rows, the others the runs of e4m3 pages of kPage tokens. kPlain: no norm, all elements turned
 // (the two branches cost a tenth of the instructions, most of them moves: the prompts above 57 and 55 us).
 // Blocks of 256 threads go three to an SM, 80 registers a thread; four, with 64, spill: the prompts above
-// 59 and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM 82 us, two 94.
+// then 59 and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM then 82 us (now 64),
+// two 94.
 template <int D, bool kInterleaved, bool kE4m3, bool kPlain, bool kTokens, int kPage, int kBlock>
 __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
@@ -1121,23 +1125,24 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedAppend &p, const
   // (a page of 128 tokens of 128 dims is 512 threads' work)
   const int block = runs && c.page * (c.D / 16) > 512 ? 512 : 256;
   const int heads = runs ? p.Hq : p.Hq + 2 * c.Hkv, rows = block / (c.D / 16);
+  const int enough = kBlocksPerSm * sms * 256 / block;
   // Tokens side by side: as many as there are, up to a block's rows. Heads one after the other: the
-  // more, the fewer angles are formed twice; as few as it takes for kBlocksPerSm blocks per SM.
+  // more, the fewer angles are formed twice; as few as it takes for enough blocks.
   a.tok_par = 1;
   while (a.tok_par < rows && (runs || a.tok_par < p.n)) a.tok_par *= 2;
   const long long tiles = ((long long)p.n + a.tok_par - 1) / a.tok_par;
   const int side = rows / a.tok_par;
   a.heads_per = side;
   while (a.heads_per < heads &&
-         tiles * ((heads + 2 * a.heads_per - 1) / (2 * a.heads_per)) >= kBlocksPerSm * sms)
+         tiles * ((heads + 2 * a.heads_per - 1) / (2 * a.heads_per)) >= enough)
     a.heads_per *= 2;
   a.head_blocks = (heads + a.heads_per - 1) / a.heads_per;
   a.row_blocks = (int)(tiles * a.head_blocks);
   const int chunk = c.page > 64 ? c.page : 64;
   const long long chunks = ((long long)p.n + chunk - 1) / chunk;
   a.run_heads = 1;
-  while (a.run_heads < c.Hkv && chunks * ((2 * c.Hkv + 2 * a.run_heads - 1) / (2 * a.run_heads)) >=
-                                    kBlocksPerSm * sms)
+  while (a.run_heads < c.Hkv &&
+         chunks * ((2 * c.Hkv + 2 * a.run_heads - 1) / (2 * a.run_heads)) >= enough)
     a.run_heads *= 2;
   a.run_blocks = (2 * c.Hkv + a.run_heads - 1) / a.run_heads;
   const long long blocks = a.row_blocks + (runs ? chunks * a.run_blocks : 0);
