@@ -844,27 +844,41 @@ def alloc_paged_cache(num_pages: int, page: int, Hkv: int, D: int, dtype=E4M3, d
 
 
 def _paged(k_pages, v_pages, k_scale, v_scale, table, B: int):
-    """The cache's part of a call: Hkv, D, num_pages, page, max_pages, and the C call's arguments."""
+    """The cache's part of a call: Hkv, D, num_pages, page, max_pages, and the C call's arguments.
+    (The usual cases of :func:`_at`, written out: a sixth of a small call's host time.)"""
+    Tensor = torch.Tensor
     P, Hkv, page, D = shape = _dims4(k_pages, "k_pages", "[num_pages, Hkv, page, D]")
     dtype = k_pages.dtype
     kind = _PAGE_TYPES.get(dtype)
     if kind is None:
         raise TypeError(f"k_pages must be {E4M3} or {BF16}, got {dtype}")
+    if not (k_pages.is_cuda and k_pages.is_contiguous()):
+        _need(k_pages, "k_pages", dtype, shape)
+    if not (type(v_pages) is Tensor and v_pages.dtype is dtype and v_pages.is_cuda
+            and v_pages.shape == shape and v_pages.is_contiguous()):
+        _need(v_pages, "v_pages", dtype, shape)
     if (k_scale is None) != (kind == 1) or (v_scale is None) != (kind == 1):
         raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages have none")
     ks = vs = None
     if kind == 2:
-        heads = (P, Hkv)
-        ks, vs = _at(k_scale, "k_scale", F32, heads), _at(v_scale, "v_scale", F32, heads)
-    if not isinstance(table, torch.Tensor):
+        heads = shape[:2]
+        if not (type(k_scale) is Tensor and k_scale.dtype is F32 and k_scale.is_cuda
+                and k_scale.shape == heads and k_scale.is_contiguous()):
+            _need(k_scale, "k_scale", F32, heads)
+        if not (type(v_scale) is Tensor and v_scale.dtype is F32 and v_scale.is_cuda
+                and v_scale.shape == heads and v_scale.is_contiguous()):
+            _need(v_scale, "v_scale", F32, heads)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    if not isinstance(table, Tensor):
         raise TypeError("table must be a torch.Tensor")
     entries = table.shape
     if len(entries) != 2 or entries[0] != B:
         raise ValueError(f"table must be [{B}, max_pages], got {tuple(entries)}")
+    if not (table.dtype is I32 and table.is_cuda and table.is_contiguous()):
+        _need(table, "table", I32, entries)
     M = entries[1]
-    return Hkv, D, P, page, M, (_at(k_pages, "k_pages", dtype, shape),
-                                _at(v_pages, "v_pages", dtype, shape), kind, ks, vs,
-                                _at(table, "table", I32, entries), M)
+    return Hkv, D, P, page, M, (k_pages.data_ptr(), v_pages.data_ptr(), kind, ks, vs,
+                                table.data_ptr(), M)
 
 
 def _tokens(t, name: str, shape):
