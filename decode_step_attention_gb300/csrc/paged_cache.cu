@@ -664,10 +664,7 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
   __shared__ Fix s_fixes[kAll ? kFixes : 1];
   __shared__ int s_fix_total;
   const int l = threadIdx.x % R::kLanes, row = threadIdx.x / R::kLanes;
-  // (kAll: the last heads first, values and keys, whose blocks take longer)
-  const int tiles = a.row_blocks / a.head_blocks;
-  const int block = kAll ? a.head_blocks - 1 - which / tiles : which % a.head_blocks;
-  const int tile = kAll ? which % tiles : which / a.head_blocks;
+  const int block = which % a.head_blocks, tile = which / a.head_blocks;
   const int i = tile * kRows + row, from = min(i, a.n - 1);  // (rows behind the last token read its)
   const int h0 = block * a.heads_per, h1 = min(heads, h0 + a.heads_per);
   const bool rotated = l < (a.rot >> 4), norm = a.q_norm_w != nullptr;
