@@ -45,7 +45,7 @@
 //   131072 tokens of one sequence, 8 KV heads of 128, e4m3         47   5.7 TB/s   start and joining
 //   192 windows of 4095 tokens, 2 KV heads of 64, e4m3             37   4.7 TB/s   start (a third),
 //                                                    then the instructions of the weights
-//   512 tokens, 8 KV heads of 128, e4m3                            12              the call (8 on the GPU)
+//   512 tokens, 8 KV heads of 128, e4m3                            11              the call (8 on the GPU)
 // The steps that led here (the serving mix): one CTA per SM 168, two 124, weights relative to a base
 // that stays while it is near 92, partials joined from bulk copies 90, a segment as one tile 86. A
 // kernel of plain loads and fp32 sums took 2126.

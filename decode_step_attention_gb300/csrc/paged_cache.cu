@@ -22,7 +22,7 @@
 // What bounds it, and what it measured (us on the GPU; TB/s of what is read and written):
 //   12.3 k tokens of 8 prompts, 32 + 8 heads of 128, e4m3 pages of 64  51  5.4  the rows alone 35 (memory),
 //       the runs alone 38: the keys' instructions, a quarter of them for the borders of codes
-//   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  40  5.7  memory
+//   9.2 k tokens in 3 chunks, bf16 pages, norm, 32 of 128 elements turned  39  5.8  memory
 //   256 single tokens, 16 + 4 heads, e4m3  8.3  the chain of look-up, scale, rotation, exact elements
 //   one token  3.7  the launch
 // One warp per run and general sines measured 218 and 84 for the first two; short series 124, the
@@ -664,7 +664,13 @@ __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTur
   __shared__ Fix s_fixes[kAll ? kFixes : 1];
   __shared__ int s_fix_total;
   const int l = threadIdx.x % R::kLanes, row = threadIdx.x / R::kLanes;
-  const int block = which % a.head_blocks, tile = which / a.head_blocks;
+  // kAll: one block of heads after the other for all tokens, keys and values last, the likelier in L2 when
+  // they are read (the chunks above, appended and read back, 51.4 and 49.2 us; with a norm and all turned
+  // the append alone 55.4 and 51.3). Queries alone: a token's heads side by side (51.4 us of the prompts, else
+  // 52.2).
+  const int tiles = a.row_blocks / a.head_blocks;
+  const int block = kAll ? which / tiles : which % a.head_blocks;
+  const int tile = kAll ? which % tiles : which / a.head_blocks;
   const int i = tile * kRows + row, from = min(i, a.n - 1);  // (rows behind the last token read its)
   const int h0 = block * a.heads_per, h1 = min(heads, h0 + a.heads_per);
   const bool rotated = l < (a.rot >> 4), norm = a.q_norm_w != nullptr;
