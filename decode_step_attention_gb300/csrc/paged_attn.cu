@@ -15,7 +15,8 @@
 // The weights' size is what e4m3 has little room for (2^-9 .. 448): each warp of 32 tokens takes them
 // relative to its own largest, 2^8, and has columns of its own in the product, which are joined in
 // fp32 with the running maximum. A value's scale is part of its weight: with t = z + log2(s_v), the
-// weight is 2^(t - max t) and its share of the softmax sum that over s_v.
+// weight is 2^(t - max t) and its share of the softmax sum that over s_v. (Scores beyond 2^10, where
+// fp32 no longer holds such sums closely, are taken apart from log2(s_v): far_tile.)
 //
 // The tiles (128 tokens; 256 of 64 dims in e4m3) of all (sequence, KV head) pairs form one stream, cut
 // into equal pieces, one per CTA (two CTAs per SM; one for bf16 rows of 128 dims, whose ring takes
@@ -75,6 +76,9 @@ constexpr uint32_t kOCols = 4 * kN;       // an O buffer: 16 columns for each wa
 // 90.6, 93.0, 97.5; 192 windows of 64 dims 38.1, 37.9, 38.6, 38.6, 39.2; 32 sequences in bf16 92.1, 91.2,
 // 91.6, 92.6, 93.3.)
 constexpr int kSegment = 1, kFew = 4;
+// Weights are taken relative to a base. Up to this size of it (in powers of two) fp32 holds the base, the
+// scores and log2 of a value's scale to 2^-14; beyond it, see the warps of weights.
+constexpr float kFar = 1024.f;
 constexpr int kCounters = 4096;           // a counter per piece
 static_assert(kCounters == kPagedMaxParts, "one counter per piece");
 
@@ -112,7 +116,7 @@ struct Geo {
 
 // Workspace: the header, a counter per piece, then two partials per piece.
 __host__ __device__ inline size_t slot_bytes(int G, int D) {
-  return ((size_t)G * (D * 4 + 8) + 15) & ~(size_t)15;
+  return (size_t)G * (D * 4 + 16);  // O, then the maximum (two terms) and the sum
 }
 constexpr size_t kSlotsOffset = kWsHeaderBytes + kCounters * 4;
 
@@ -124,6 +128,20 @@ struct alignas(16) Tile {
   int unit, tiles; // the pair's first tile in the stream, and how many there are
 };
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;  // of a segment; of the piece (not a tile)
+
+// A base, or a maximum of bases: hi + lo. lo is 0 but where scores are far from zero (is_far): there hi is
+// the largest score, and lo what log2 of the values' scales add to it, which hi's steps would swallow.
+__device__ __forceinline__ bool is_far(float hi) { return !(fabsf(hi) <= kFar) && hi != -INFINITY; }
+struct Base {
+  float hi, lo;
+  // (hi first: equal ones cancel exactly; NaN for two that are -inf)
+  __device__ __forceinline__ float above(const Base &o) const { return (hi - o.hi) + (lo - o.lo); }
+  __device__ __forceinline__ Base max(const Base &o) const {
+    return above(o) > 0.f || o.hi == -INFINITY ? *this : o;
+  }
+  // what is subtracted: 0 while there is none
+  __device__ __forceinline__ Base or_zero() const { return Base{hi == -INFINITY ? 0.f : hi, lo}; }
+};
 
 struct PagedMaps {
   CUtensorMap k, v;
@@ -290,6 +308,111 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   s.tiles = s.L > s.start ? (s.L + kTile - 1) / kTile - s.tile0 : 0;
   return s;
 }
+
+// A token's weights into the operand of the value product.
+template <int kTile, bool kE4m3, int NH>
+__device__ __forceinline__ void put_weights(const float (&w)[NH], uint32_t at) {
+  if constexpr (kE4m3) {
+    uint32_t hi[NH / 4], lo[NH / 4];
+    two_terms_e4m3<NH>(w, hi, lo);
+    if constexpr (NH == 8)
+      st_shared16(at, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+    else
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(lo[0]) : "memory");
+  } else {
+    uint32_t hi[NH / 2], lo[NH / 2];
+    two_terms_bf16<NH>(w, hi, lo);
+    if constexpr (NH == 8) {
+      st_shared16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      st_shared16(at + kTile * 16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    } else {
+      st_shared16(at, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+    }
+  }
+}
+
+// A tile's weights where a base lies beyond kFar, by the warp of its tokens. The steps of fp32 are no longer
+// small beside a weight's exponent there: the largest score is subtracted from the scores before
+// anything is added, which is exact for equal ones, and the base has two terms. Nothing stays for the
+// next tile, and its sticky base is none. (A function of its own, called in the place of the common tiles'
+// code: in line, or in a loop of its own behind theirs, it cost the windows above 10 to 20%; so 4%.)
+struct FarTile {
+  const float *scale, *qs;  // [2][8 kHalves] K's and V's of the tile's pages; the queries'
+  float *base, *top;        // the warp's s_base, and its two rows of s_top, 4 kG apart
+  uint32_t s, p;            // S^T in tensor memory, this thread's weights in shared memory
+  int page_log2, lo, hi;
+};
+template <int D, bool kE4m3, int NH>
+__device__ __noinline__ void far_tile(const FarTile f, float (&sum)[NH]) {
+  using Ge = Geo<D, kE4m3>;
+  constexpr int kHalves = Ge::kHalves, kCols = kE4m3 ? 2 * NH : 8;
+  const int lane = threadIdx.x & 31, mine = lane & (kG - 1);
+  float z[kHalves][kCols], w[kHalves][NH], ks[kHalves], lvs[kHalves], ivs[kHalves];
+  bool seen[kHalves];
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+    tmem_ld(f.s + half * kN, z[half]);
+    const int row = threadIdx.x + 128 * half;
+    ks[half] = f.scale[row >> f.page_log2];
+    const float vs = f.scale[8 * kHalves + (row >> f.page_log2)];
+    seen[half] = row >= f.lo && row < f.hi && ks[half] > 0.f;
+    lvs[half] = kE4m3 ? lg2(vs) : 0.f;
+    ivs[half] = seen[half] ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
+  }
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
+  Base b{-INFINITY, 0.f};  // of this lane's head
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    float m = -INFINITY, r = -INFINITY;
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      const float *x = z[half];
+      if constexpr (kE4m3)
+        w[half][h] = fmaf(x[NH + h], kLow, x[h]) * (f.qs[h] * ks[half]);
+      else
+        w[half][h] = x[h] * f.qs[h];
+      if (!seen[half]) w[half][h] = -INFINITY;
+      m = fmaxf(m, w[half][h]);
+    }
+    m = warp_max(m);
+    const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      w[half][h] -= from;
+      if (seen[half]) w[half][h] += lvs[half];
+      r = fmaxf(r, w[half][h]);
+    }
+    r = m == -INFINITY ? 0.f : warp_max(r);
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) w[half][h] = ex2((w[half][h] - r) + 8.f);
+    if (mine == h) b = is_far(m) ? Base{m, r} : Base{m + r, 0.f};
+  }
+  const Base old{f.base[2 * kG + mine], f.base[4 * kG + mine]};
+  const Base to = b.max(old), by = to.or_zero();
+  __syncwarp();
+  if (lane < NH) {
+    f.base[lane] = -INFINITY;
+    f.base[kG + lane] = ex2(b.above(by));
+    f.base[2 * kG + lane] = to.hi;
+    f.base[3 * kG + lane] = ex2(old.above(by));
+    f.base[4 * kG + lane] = to.lo;
+    f.top[lane] = b.hi;
+    f.top[4 * kG + lane] = b.lo;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    float add = 0.f;
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) add = fmaf(w[half][h], ivs[half], add);
+    sum[h] = fmaf(add, f.base[kG + h], sum[h] * f.base[3 * kG + h]);
+  }
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half)
+    put_weights<Ge::kTile, kE4m3, NH>(w[half], f.p + 128 * half * 16);
+}
+
 template <int D, bool kE4m3, int NH>
 __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const PagedCache c,
@@ -301,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   __shared__ Tile s_tile[ND];
   __shared__ float s_scale[ND][2][8 * kHalves];  // of a tile's pages, K and V; < 0: no page
   __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
-  __shared__ __align__(16) float s_top[2][4][kG];       // a tile's bases, per warp of tokens
-  __shared__ __align__(16) float s_base[4][4][kG];      // see the warps of weights
-  __shared__ __align__(16) float s_sum[4][4][2][kG];    // a segment's sums and their maxima
+  __shared__ __align__(16) float s_top[2][2][4][kG];    // a tile's bases (hi, lo), per warp of tokens
+  __shared__ __align__(16) float s_base[4][5][kG];      // see the warps of weights
+  __shared__ __align__(16) float s_sum[4][4][3][kG];    // a segment's sums and their maxima (hi, lo)
   __shared__ __align__(16) float s_f[4][5 * kG];        // factors, per warp of dimensions
   __shared__ int2 s_seg[4];
   __shared__ uint32_t s_tmem;
@@ -698,8 +821,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     const uint32_t my_s = tmem + ((uint32_t)(32 * warp) << 16);
     // A warp's weights are 2^(8 + t - base) with a base per head that stays while the largest t of a tile
     // lies within 2^-6 .. 2^0.5 of it: then a tile's weights, sums and part of O need no factor of their
-    // own. s_base: the bases, 2^(base - maximum), the maximum of the bases so far, which the sums
-    // are relative to, and what the sums are to be multiplied with.
+    // own. s_base: the bases, 2^(base - maximum), the maximum of the bases so far (hi; its lo last), which
+    // the sums are relative to, and what the sums are to be multiplied with.
     float *my_base = s_base[warp][0];
     float sum[NH];
     int seg = -1;
@@ -734,7 +857,10 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       }
       if (t.flags & kFirst) {
         ++seg;
-        if (lane < kG) my_base[lane] = my_base[2 * kG + lane] = -INFINITY;
+        if (lane < kG) {
+          my_base[lane] = my_base[2 * kG + lane] = -INFINITY;
+          my_base[4 * kG + lane] = 0.f;
+        }
 #pragma unroll
         for (int h = 0; h < NH; ++h) sum[h] = 0.f;
         __syncwarp();
@@ -770,6 +896,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         most[h] = warp_max(m);
         near = near && most[h] - base[h] <= 0.5f && most[h] - base[h] >= -6.f;
       }
+      bool far = false;
       if (!near) {  // (the same for the whole warp) a head per lane
         float m = most[0];
 #pragma unroll
@@ -777,61 +904,57 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
           if ((lane & (kG - 1)) == h) m = most[h];
         float b = my_base[lane & (kG - 1)];
         const float old = my_base[2 * kG + (lane & (kG - 1))], x = m - b;
-        if (!(x <= 0.5f && x >= -6.f) && m != -INFINITY) b = m;
-        const float to = fmaxf(old, b), by = to == -INFINITY ? 0.f : to;
-        __syncwarp();
-        if (lane < NH) {
-          my_base[lane] = b;
-          my_base[kG + lane] = ex2(b - by);
-          my_base[2 * kG + lane] = to;
-          my_base[3 * kG + lane] = ex2(old - by);
-        }
-        __syncwarp();
-        load4(base, my_base);
-        load4(beta, my_base + kG);
-        float alpha[NH];
-        load4(alpha, my_base + 3 * kG);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) sum[h] *= alpha[h];
-      }
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const float by = (base[h] == -INFINITY ? 0.f : base[h]) - 8.f;
-        float add = 0.f;
-#pragma unroll
-        for (int half = 0; half < kHalves; ++half) {
-          w[half][h] = ex2(w[half][h] - by);
-          add = fmaf(w[half][h], ivs[half], add);
-        }
-        sum[h] = fmaf(add, beta[h], sum[h]);
-      }
-      if (lane == 0) {
-#pragma unroll
-        for (int h = 0; h < NH; h += 4)
-          *reinterpret_cast<float4 *>(&s_top[buf][warp][h]) =
-              make_float4(base[h], base[h + 1], base[h + 2], base[h + 3]);
-      }
-#pragma unroll
-      for (int half = 0; half < kHalves; ++half) {
-        const uint32_t my_p = p_s + buf * Ge::kP + (tid + 128 * half) * 16;
-        if constexpr (kE4m3) {
-          uint32_t hi[NH / 4], lo[NH / 4];
-          two_terms_e4m3<NH>(w[half], hi, lo);
-          if constexpr (NH == 8)
-            st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
-          else
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(my_p), "r"(hi[0]), "r"(lo[0])
-                         : "memory");
-        } else {
-          uint32_t hi[NH / 2], lo[NH / 2];
-          two_terms_bf16<NH>(w[half], hi, lo);
-          if constexpr (NH == 8) {
-            st_shared16(my_p, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            st_shared16(my_p + kTile * 16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          } else {
-            st_shared16(my_p, make_uint4(hi[0], hi[1], lo[0], lo[1]));
+        far = __any_sync(0xffffffffu, is_far(m) || is_far(old));
+        if (!far) {
+          if (!(x <= 0.5f && x >= -6.f) && m != -INFINITY) b = m;
+          const float to = fmaxf(old, b), by = to == -INFINITY ? 0.f : to;
+          __syncwarp();
+          if (lane < NH) {
+            my_base[lane] = b;
+            my_base[kG + lane] = ex2(b - by);
+            my_base[2 * kG + lane] = to;
+            my_base[3 * kG + lane] = ex2(old - by);
           }
+          __syncwarp();
+          load4(base, my_base);
+          load4(beta, my_base + kG);
+          float alpha[NH];
+          load4(alpha, my_base + 3 * kG);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) sum[h] *= alpha[h];
         }
+      }
+      if (__builtin_expect(far, 0)) {
+        float sums[NH];  // (whose address goes out)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sums[h] = sum[h];
+        far_tile<D, kE4m3, NH>(
+            FarTile{s_scale[d][0], s_qs[seg & 3], my_base, s_top[buf][0][warp],
+                    my_s + buf * kHalves * kN, p_s + buf * Ge::kP + tid * 16, page_log2, t.lo, t.hi},
+            sums);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sum[h] = sums[h];
+      } else {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const float by = (base[h] == -INFINITY ? 0.f : base[h]) - 8.f;
+          float add = 0.f;
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            w[half][h] = ex2(w[half][h] - by);
+            add = fmaf(w[half][h], ivs[half], add);
+          }
+          sum[h] = fmaf(add, beta[h], sum[h]);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < NH; h += 4)
+            *reinterpret_cast<float4 *>(&s_top[buf][0][warp][h]) =
+                make_float4(base[h], base[h + 1], base[h + 2], base[h + 3]);
+        }
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half)
+          put_weights<kTile, kE4m3, NH>(w[half], p_s + buf * Ge::kP + (tid + 128 * half) * 16);
       }
       // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
       // page that does not exist was left zeros.)
@@ -854,6 +977,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
           if (lane == 0) {
             s_sum[seg & 3][warp][0][h] = x;
             s_sum[seg & 3][warp][1][h] = my_base[2 * kG + h];
+            s_sum[seg & 3][warp][2][h] = my_base[4 * kG + h];
           }
         }
         if (lane == 0) mbar_arrive(bar_sum + 8 * (seg & 3));
@@ -869,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     const bool mine_too = D == 128 || lane < 16;
     const uint32_t my_o = tmem + ((uint32_t)(32 * w4) << 16) + Ge::kOCol;
     float acc[NH];
-    float top = -INFINITY;  // the running maximum of the bases of head lane & 7
+    Base top{-INFINITY, 0.f};  // the running maximum of the bases of head lane & 7
     int seg = -1;
     // sequences without tokens are nobody's tiles: their zeros
     for (int b = piece; b < a.B; b += P) {
@@ -893,17 +1017,31 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       tmem_ld(my_o + buf * kOCols + kN, o[1]);
       if (t.flags & kFirst) {
         ++seg;
-        top = -INFINITY;
+        top = Base{-INFINITY, 0.f};
 #pragma unroll
         for (int h = 0; h < NH; ++h) acc[h] = 0.f;
       }
       {
-        const float x = s_top[buf][lane >> 3][lane & 7];
-        float m = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const float to = fmaxf(top, m), base = to == -INFINITY ? 0.f : to;
-        s_f[w4][lane] = ex2(x - base - 8.f);  // (0 where a warp saw nothing)
-        if (lane < kG) s_f[w4][32 + lane] = ex2(top - base);
+        Base x{s_top[buf][0][lane >> 3][lane & 7], 0.f}, to;
+        if (__any_sync(0xffffffffu, (lane & 7) < NH && (is_far(x.hi) || is_far(top.hi)))) {
+          if (is_far(x.hi)) x.lo = s_top[buf][1][lane >> 3][lane & 7];
+          to = x;
+#pragma unroll
+          for (int o = 8; o < 32; o *= 2)
+            to = to.max(Base{__shfl_xor_sync(0xffffffffu, to.hi, o),
+                             __shfl_xor_sync(0xffffffffu, to.lo, o)});
+          to = to.max(top);
+          const Base base = to.or_zero();
+          s_f[w4][lane] = ex2(x.above(base) - 8.f);
+          if (lane < kG) s_f[w4][32 + lane] = ex2(top.above(base));
+        } else {
+          float m = fmaxf(x.hi, __shfl_xor_sync(0xffffffffu, x.hi, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          to = Base{fmaxf(top.hi, m), 0.f};
+          const float base = to.hi == -INFINITY ? 0.f : to.hi;
+          s_f[w4][lane] = ex2(x.hi - base - 8.f);  // (0 where a warp saw nothing)
+          if (lane < kG) s_f[w4][32 + lane] = ex2(top.hi - base);
+        }
         top = to;
       }
       __syncwarp();
@@ -942,10 +1080,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       // a segment's end: the four warps' sums under one maximum
       if (!wait.all(bar_sum + 8 * (seg & 3), (seg >> 2) & 1)) break;
       float l = 0.f;
-      const float base = top == -INFINITY ? 0.f : top;
+      const Base base = top.or_zero();
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        l += s_sum[seg & 3][w][0][lane & 7] * ex2(s_sum[seg & 3][w][1][lane & 7] - base - 8.f);
+      for (int w = 0; w < 4; ++w) {
+        const Base of{s_sum[seg & 3][w][1][lane & 7], s_sum[seg & 3][w][2][lane & 7]};
+        l += s_sum[seg & 3][w][0][lane & 7] * ex2(of.above(base) - 8.f);
+      }
       __syncwarp();
       tc_fence_before();
       mbar_arrive(bar_free + 8 * buf);  // (after the last read of what the tile and segment left)
@@ -964,7 +1104,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       for (int h = 0; h < NH; ++h)
         if (h < G && mine_too) reinterpret_cast<float *>(part)[h * D + dim] = acc[h];
       if (w4 == 0 && lane < G)
-        reinterpret_cast<float2 *>(part + (size_t)G * D * 4)[lane] = make_float2(top, l);
+        reinterpret_cast<float4 *>(part + (size_t)G * D * 4)[lane] =
+            make_float4(top.hi, top.lo, l, 0.f);
       fence_proxy_async_global();  // (they are read by bulk copies)
       if (tid == 128) s_part[s_parts++] = make_int4(t.unit, t.tiles, t.b, t.g);
     }
@@ -1000,7 +1141,8 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     if (!s_joins[i]) continue;
     const int4 x = s_part[i];
     const int first = (unsigned)x.x / (unsigned)s_blk, last = (unsigned)(x.x + x.y - 1) / (unsigned)s_blk;
-    float M = -INFINITY, sum = 0.f, o[4] = {};
+    Base M{-INFINITY, 0.f};
+    float sum = 0.f, o[4] = {};
     for (int c0 = first; c0 <= last; c0 += room) {
       const int n = min(room, last + 1 - c0);
       if (warp == 0) {
@@ -1018,11 +1160,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
 #pragma unroll 4
         for (int k = 0; k < n; ++k, p += slot) {
           const float4 y = reinterpret_cast<const float4 *>(p)[tid];
-          const float2 ml = reinterpret_cast<const float2 *>(p + (size_t)G * D * 4)[h];
-          const float to = fmaxf(M, ml.x), base = to == -INFINITY ? 0.f : to;
-          const float f = ex2(M - base), w = ex2(ml.x - base);
+          const float4 ml = reinterpret_cast<const float4 *>(p + (size_t)G * D * 4)[h];
+          const Base of{ml.x, ml.y}, to = of.max(M), base = to.or_zero();
+          const float f = ex2(M.above(base)), w = ex2(of.above(base));
           M = to;
-          sum = fmaf(sum, f, ml.y * w);
+          sum = fmaf(sum, f, ml.z * w);
           o[0] = fmaf(o[0], f, y.x * w);
           o[1] = fmaf(o[1], f, y.y * w);
           o[2] = fmaf(o[2], f, y.z * w);

@@ -947,3 +947,98 @@ def test_two_streams_with_workspaces_of_their_own():
     for q, out in zip(qs, outs):
         want = OP.attention(f64(q), ref, table, lens)
         check_attn(out, want, "two streams")
+
+
+def equal_keys(gen, value, P, Hkv, page, D, dtype, pow2=True):
+    """A pool whose keys are all `value` (at most four significant bits), in e4m3 under scales that
+    differ from page to page, and values under scales of any size."""
+    gpu, _ = make_cache(gen, P, Hkv, page, D, dtype, pow2)
+    if dtype is BF16:
+        gpu[0].fill_(value)
+    else:
+        e = math.frexp(value)[1]
+        up = torch.randint(0, 6, (P, Hkv), generator=gen).to(DEV)
+        code = torch.exp2(up.float()) * (value * 2.0 ** -e)
+        gpu[0].copy_(code[:, :, None, None].expand(gpu[0].shape).to(E4M3))
+        gpu[2].copy_(torch.exp2((e - up).float()))
+    return gpu
+
+
+@pytest.mark.parametrize("e", [9, 12, 16, 20, 24, 25, 27, 28, 30, 66, 116])
+@pytest.mark.parametrize("dtype,D,page,G", [(E4M3, 128, 16, 4), (E4M3, 128, 64, 7), (E4M3, 64, 32, 8),
+                                            (E4M3, 64, 128, 2), (BF16, 128, 32, 3), (BF16, 64, 16, 8)])
+def test_attention_scores_far_from_zero(dtype, D, page, G, e):
+    """Equal scores of some 2^e give the mean of the values, one larger score its value, one smaller
+    score nothing, whatever the scales of keys and values and however the tokens are cut."""
+    gen, rng = torch.Generator().manual_seed(e + D + G), np.random.default_rng(e)
+    lens = [700, 64, 5, 1300]
+    P = sum(-(-n // page) for n in lens)
+    for sign in (1.0, -1.0):
+        for pow2 in (True, False):
+            size = sign * 1.25 * 2.0 ** e
+            gpu = equal_keys(gen, size, P, 2, page, D, dtype, pow2)
+            table = make_table(rng, lens, page, P)
+            q = torch.ones(4, 2 * G, D, dtype=BF16, device=DEV)
+            q[:, 1::3] = 0.5
+            for peak in (False, True):
+                if peak:  # 1.5 times as far: a page's row
+                    at, row = int(table[0, 333 // page]), 333 % page
+                    gpu[0][at, :, row] = (1.5 * gpu[0][at, :, row].float()).to(dtype)
+                want = OP.attention(f64(q), oracle_cache(gpu), table, lens)
+                for parts in (0, 7):
+                    out, err = attend(q, gpu, table, lens, num_parts=parts)
+                    check_attn(out, want, (dtype, D, page, G, size, pow2, peak, parts))
+                    assert err == 0
+
+
+@pytest.mark.parametrize("dtype,D,page,G", [(E4M3, 128, 16, 4), (E4M3, 64, 32, 8), (BF16, 128, 32, 3),
+                                            (BF16, 64, 16, 8)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("falls", [False, True])
+def test_attention_scores_that_grow(falls, sign, dtype, D, page, G):
+    """Scores that double from page to page, from small to far ones and back: a call's partials and sums
+    lie at bases far apart."""
+    gen, rng = torch.Generator().manual_seed(D + G), np.random.default_rng(D)
+    lens = [70 * page - 3, 9 * page, 1, 40 * page]
+    P = sum(-(-n // page) for n in lens)
+    gpu, _ = make_cache(gen, P, 2, page, D, dtype)
+    table = make_table(rng, lens, page, P)
+    for b, n in enumerate(lens):
+        pages = [int(at) for at in table[b, :-(-n // page)]]
+        for j, at in enumerate(pages[::-1] if falls else pages):
+            if dtype is BF16:
+                gpu[0][at] = sign * 1.5 * 2.0 ** (j - 8)
+            else:
+                gpu[0][at] = torch.full((2, page, D), sign * 1.5 * 2.0 ** (j % 5), device=DEV).to(E4M3)
+                gpu[2][at] = 2.0 ** (j - 8 - j % 5)
+    q = torch.ones(4, 2 * G, D, dtype=BF16, device=DEV)
+    q[:, ::2] = -0.75
+    want = OP.attention(f64(q), oracle_cache(gpu), table, lens)
+    for parts in (0, 1, 40):
+        out, err = attend(q, gpu, table, lens, num_parts=parts)
+        check_attn(out, want, (dtype, D, page, G, sign, falls, parts))
+        assert err == 0
+
+
+@pytest.mark.parametrize("falls", [False, True])
+def test_attention_far_scores_a_step_apart(falls):
+    """Scores of 2^27.3 (in powers of two) that rise or fall by 16, one step of fp32 there, every 32
+    tokens: a weight of 2^-16 stays one. The softmax scale is ln 2, so that a score is its q . k."""
+    gen, rng = torch.Generator().manual_seed(3), np.random.default_rng(3)
+    lens = [640, 130, 40]
+    gpu, _ = make_cache(gen, 60, 1, 16, 128, BF16)
+    table = make_table(rng, lens, 16, 60)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            j = t // 32 % 5
+            row = gpu[0][int(table[b, t // 16]), 0, t % 16]
+            row[:127] = 1.25 * 2.0 ** 20
+            row[127] = 256.0 * (4 - j if falls else j)
+    q = torch.ones(3, 4, 128, dtype=BF16, device=DEV)
+    q[..., 127] = 2.0 ** -4
+    ln2 = float(np.float32(math.log(2.0)))
+    want = OP.attention(f64(q), oracle_cache(gpu), table, lens, scale=ln2)
+    for parts in (0, 1, 7):
+        out, err = attend(q, gpu, table, lens, num_parts=parts, scale=ln2)
+        check_attn(out, want, (falls, parts))
+        assert err == 0
