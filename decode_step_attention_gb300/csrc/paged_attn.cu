@@ -305,7 +305,7 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   s.L = min(max(a.lens[b], 0), a.max_len);
   s.start = a.window > 0 ? max(0, s.L - a.window) : 0;
   s.tile0 = s.start / kTile;
-  s.tiles = s.L > s.start ? (s.L + kTile - 1) / kTile - s.tile0 : 0;
+  s.tiles = s.L > s.start ? (s.L - 1) / kTile + 1 - s.tile0 : 0;  // (L: up to 2^31 - 1)
   return s;
 }
 
@@ -570,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
       at_tile = x.to;
       // this lane's page: tile from + lane / ppt, page lane % ppt of it; only where a token is seen
       const int slot = ((s.tile0 + x.from) << ppt_log2) + lane;
+      const long long row = (long long)slot << page_log2;
       x.page = -1;
-      if ((slot << page_log2) < s.L && (slot << page_log2) + page - 1 >= s.start &&
-          lane < (x.to - x.from) << ppt_log2)
+      if (row < s.L && row + page - 1 >= s.start && lane < (x.to - x.from) << ppt_log2)
         x.page = c.table[(size_t)b * c.max_pages + slot];
       return true;
     };
@@ -1212,7 +1212,7 @@ int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts
   auto of = [](auto geo) { return std::pair<int, int>(decltype(geo)::kCtas, decltype(geo)::kTile); };
   const auto [per, tile] = D == 128 ? (e4m3 ? of(Geo<128, true>{}) : of(Geo<128, false>{}))
                                     : (e4m3 ? of(Geo<64, true>{}) : of(Geo<64, false>{}));
-  const long long tiles = (long long)B * Hkv * ((max_len + tile - 1) / tile + 1);
+  const long long tiles = (long long)B * Hkv * (((long long)max_len + tile - 1) / tile + 1);
   const long long most = per * sms < kPagedMaxParts ? per * sms : kPagedMaxParts;
   return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }

@@ -1042,3 +1042,40 @@ def test_attention_far_scores_a_step_apart(falls):
         out, err = attend(q, gpu, table, lens, num_parts=parts, scale=ln2)
         check_attn(out, want, (falls, parts))
         assert err == 0
+
+
+@pytest.mark.parametrize("dtype,D", [(E4M3, 64), (E4M3, 128), (BF16, 64)])
+def test_the_longest_contexts(dtype, D):
+    """Sequences of nearly 2^31 tokens (a table may name a page over and over): a token appended, a window
+    and the last rows of them, beside a short sequence."""
+    gen, rng = torch.Generator().manual_seed(D), np.random.default_rng(D)
+    page, M, P, window = 64, 2 ** 25 - 1, 40, 300
+    lens = np.array([M * page, 90, M * page - 1, 1])
+    gpu, ref = make_cache(gen, P, 2, page, D, dtype)
+    table = np.full((4, M), 39, dtype=np.int32)
+    table[:, -8:] = np.arange(32).reshape(4, 8)
+    table[1, :2], table[3, 0] = [32, 33], 34
+    t, start, n = i32(table), i32(lens - 1), i32(lens)
+    q, k, v = (rnd(gen, 4, h, D).to(DEV) for h in (8, 2, 2))
+    q_want, want = OP.append(f64(q), f64(k), f64(v), ref, table, lens - 1, None, 1e4, "neox", D)
+    dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], t, start, 1e4, k_scale=gpu[2], v_scale=gpu[3])
+    check_float(f64(q), q_want, "q")
+    check_ulp(f64(gpu[0]), want["k"], "keys")
+    now = oracle_cache(gpu)
+    for parts in (0, 5):
+        ws = dsa.alloc_paged_workspace(4, 8, 2, D, M * page, parts)
+        out = torch.full_like(q, float("nan"))
+        dsa.gqa_paged_attn(q, gpu[0], gpu[1], t, n, gpu[2], gpu[3], workspace=ws, out=out, window=window,
+                           num_parts=parts)
+        torch.cuda.synchronize()
+        assert dsa.device_errors(ws) == 0
+        check_attn(out, OP.attention(f64(q), now, table, lens, window=window), (dtype, D, parts))
+    first = np.maximum(lens - 200, 0)
+    ko, vo = (torch.zeros(4, 2, 200, D, dtype=BF16, device=DEV) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dsa.paged_gather(gpu[0], gpu[1], t, n, ko, vo, gpu[2], gpu[3], start=i32(first), error_word=err)
+    assert int(err) == 0
+    for b, (lo, m) in enumerate(zip(first, lens)):
+        K, V, _ = OP.tokens(now, table, b, int(lo), int(m))
+        check_ulp(f64(ko[b, :, :m - lo]), K, "gather", 0.5)
+        check_ulp(f64(vo[b, :, :m - lo]), V, "gather", 0.5)

@@ -168,6 +168,14 @@ def test_workspace_of_refused_shapes_is_nothing(L):
     assert ws(1, 1, 1, 64, 0, 0) > 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_of_the_longest_contexts(L, D):
+    """Lengths up to 2^31 - 1 are as many tiles as they are: no less workspace than half of them."""
+    ws = L.dec_paged_attn_workspace_bytes
+    for max_len in (2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 128, 2 ** 31 - 256):
+        assert ws(1, 1, 1, D, max_len, 0) == ws(1, 1, 1, D, 2 ** 30, 0) > ws(1, 1, 1, D, 0, 0), max_len
+
+
 def test_binding_checks():
     bf = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     q, i = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
