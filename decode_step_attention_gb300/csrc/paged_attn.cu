@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // 2^e with the largest of 2^8 at most times it; an infinity makes every score a NaN
-          const int e = min(max((int)(__float_as_uint(m) >> 23) - 127 - 7, -100), 100);
+          // 2^e with the largest below 2^8 times it (any finite one, down to 2^-119); an infinity makes
+          // every score a NaN
+          const int e = min(max((int)(__float_as_uint(m) >> 23) - 127 - 7, -126), 120);
           const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] *= inv;

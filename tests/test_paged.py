@@ -1020,6 +1020,25 @@ def test_attention_scores_that_grow(falls, sign, dtype, D, page, G):
         assert err == 0
 
 
+@pytest.mark.parametrize("e", [-120, -100, -60, 60, 100, 110, 117, 120])
+@pytest.mark.parametrize("dtype,D", [(E4M3, 128), (E4M3, 64), (BF16, 128)])
+def test_attention_queries_of_every_size(dtype, D, e):
+    """Queries of some 2^e over keys of some 2^-e."""
+    gen, rng = torch.Generator().manual_seed(D), np.random.default_rng(0)
+    lens = [300, 40]
+    gpu, _ = make_cache(gen, 30, 2, 16, D, dtype)
+    table = make_table(rng, lens, 16, 30)
+    if dtype is BF16:
+        gpu[0].copy_((gpu[0].float() * 2.0 ** -e).to(BF16))
+    else:
+        gpu[2].copy_(torch.full((30, 2), 2.0 ** (-e - 6)))
+    q = (rnd(gen, 2, 8, D).double() * 2.0 ** e).to(BF16).to(DEV)
+    assert bool(q.isfinite().all())
+    out, err = attend(q, gpu, table, lens)
+    check_attn(out, OP.attention(f64(q), oracle_cache(gpu), table, lens), (dtype, D, e))
+    assert err == 0
+
+
 @pytest.mark.parametrize("falls", [False, True])
 def test_attention_far_scores_a_step_apart(falls):
     """Scores of 2^27.3 (in powers of two) that rise or fall by 16, one step of fp32 there, every 32
