@@ -640,8 +640,9 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  *                    Entries that no token of the call needs may hold anything.
  *   type             DEC_BF16, or DEC_E4M3 with
  *   k_scale, v_scale [device] fp32 [num_pages, Hkv], finite, > 0 and not subnormal for pages that
- *                    hold tokens: a value is code * scale. NULL for DEC_BF16. Attention wants a
- *                    sequence's v_scales of one head within a factor of 2^100 of one another.
+ *                    hold tokens: a value is code * scale. NULL for DEC_BF16. Attention wants
+ *                    v_scales between 2^-64 and 2^120 (the append's own are), a sequence's of one head
+ *                    within a factor of 2^100 of one another; other sizes may give zeros.
  * The conventions are those of the draft trees: device buffers on the current device, what a
  * call writes overlaps neither what it reads nor anything else it writes. A token whose page
  * number lies outside [0, num_pages) is skipped (not stored, not attended, not copied) and raises
@@ -689,6 +690,11 @@ dec_status dec_qknorm_rope_paged_append(
  * 0 to the last min(lens[b], window) of them (pages wholly before the window are not looked up).
  * A sequence that sees no token gives zeros. Rows behind a sequence's last token, and rows of its
  * first page before the window, may hold anything.
+ * Products are summed in fp32; scores, and the products q k, scale q and scale q k of single elements,
+ * have to stay finite there. Over e4m3 pages q is exact but for elements below 2^-14 of their head's
+ * largest, and a softmax weight, times its value's scale, within 2^-8 of itself or 2^-22 of the
+ * sequence's largest; over bf16 pages q is exact and a weight within 2^-16 of itself. An infinity among
+ * the values that a sequence sees gives NaN.
  * q          [device|host] bf16 [B, Hq, D] (rotated);  out [device|host] bf16 [B, Hq, D].
  * lens       [device|host] int32 [B]; max_len a host upper bound, 0 <= max_len <= max_pages * page.
  *            A length outside [0, max_len] is clamped and raises DEC_DEVERR_LEN_CLAMPED.

@@ -1039,6 +1039,21 @@ def test_attention_queries_of_every_size(dtype, D, e):
     assert err == 0
 
 
+@pytest.mark.parametrize("lo,hi", [(-64, -64), (-64, 36), (19, 119), (119, 119)])
+def test_attention_values_at_the_ends_of_their_scales(lo, hi):
+    """Values' scales from one end of their range to the other, short and long contexts."""
+    gen, rng = torch.Generator().manual_seed(hi), np.random.default_rng(0)
+    for D, G, n in ((128, 2, 131072), (64, 8, 3000), (128, 5, 17)):
+        gpu, _ = make_cache(gen, 40, 1, 32, D, E4M3)
+        gpu[3].copy_(torch.exp2(torch.randint(lo, hi + 1, gpu[3].shape, generator=gen).float()))
+        gpu[3][0], gpu[3][1] = 2.0 ** lo, 2.0 ** hi
+        table = rng.integers(0, 40, (1, -(-n // 32)))
+        q = rnd(gen, 1, G, D).to(DEV)
+        out, err = attend(q, gpu, table, [n])
+        check_attn(out, OP.attention(f64(q), oracle_cache(gpu), table, [n]), (lo, hi, D, n))
+        assert err == 0
+
+
 @pytest.mark.parametrize("falls", [False, True])
 def test_attention_far_scores_a_step_apart(falls):
     """Scores of 2^27.3 (in powers of two) that rise or fall by 16, one step of fp32 there, every 32
