@@ -898,6 +898,73 @@ def test_pages_beyond_32_bits(dtype):
         assert not bool(t[:used].view(torch.uint8 if dtype is E4M3 else torch.int16).any())
 
 
+@pytest.mark.parametrize("single", [True, False])
+def test_captured_appends_leave_their_scales(single):
+    """Scales and codes of a captured append in e4m3, replayed on other tokens, starts and tables; scales of
+    other pages stay."""
+    gen, rng = torch.Generator().manual_seed(47), np.random.default_rng(47)
+    B, P, page = 5, 80, 16
+    n = B if single else 130
+    gpu, _ = make_cache(gen, P, 2, page, 128, E4M3)
+    q, k, v = (torch.zeros(n, h, 128, dtype=BF16, device=DEV) for h in (4, 2, 2))
+    q_out = torch.zeros_like(q)
+    table = torch.zeros(B, 16, dtype=torch.int32, device=DEV)
+    start, cu = (torch.zeros(m, dtype=torch.int32, device=DEV) for m in (B, B + 1))
+
+    def body():
+        dsa.qknorm_rope_paged_append(q, k, v, gpu[0], gpu[1], table, start, 1e4,
+                                     cu_new=None if single else cu, k_scale=gpu[2], v_scale=gpu[3],
+                                     q_out=q_out)
+
+    body()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for turn in range(4):
+        s = rng.integers(0, 100, B)
+        c = np.arange(B + 1) if single else np.concatenate([[0], np.sort(rng.integers(0, n + 1, B - 1)), [n]])
+        t = make_table(rng, s + np.diff(c), page, P, width=16)
+        table.copy_(i32(t)), start.copy_(i32(s)), cu.copy_(i32(c))
+        for x in (q, k, v):  # (larger from turn to turn: scales grow)
+            x.copy_((rnd(gen, *x.shape).float() * 4.0 ** (turn - 1)).to(BF16))
+        _, want = OP.append(f64(q), f64(k), f64(v), oracle_cache(gpu), t, s, c, 1e4, "neox", 128)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, name in zip(gpu, ("k", "v", "ks", "vs")):
+            assert np.array_equal(f64(got), want[name]), (turn, name)
+
+
+@pytest.mark.parametrize("single", [True, False])
+def test_scales_of_pages_beyond_32_bits(single):
+    """A pool of more than 2^32 bytes per tensor: the scales and codes of its last pages after an append, and
+    nothing of the others'."""
+    gen, rng = torch.Generator().manual_seed(48), np.random.default_rng(48)
+    Hkv, page, D, used = 8, 64, 128, 20
+    P = 2 ** 32 // (Hkv * page * D) + used
+    if torch.cuda.mem_get_info()[0] < 16 * 2 ** 30:
+        pytest.skip("needs 10 GB of device memory")
+    k, v, ks, vs = dsa.alloc_paged_cache(P, page, Hkv, D, E4M3)
+    start = np.array([200, 0, 127, 63])
+    new = np.ones(4, dtype=int) if single else np.array([70, 300, 1, 2])
+    lens, n = start + new, int(new.sum())
+    near = make_table(rng, lens, page, used)
+    far = np.where(near < used, near + P - used, near)
+    gpu, ref = make_cache(gen, used, Hkv, page, D, E4M3)
+    for t, x in zip((k, v, ks, vs), gpu):
+        t[P - used:].copy_(x)
+    q, kn, vn = (rnd(gen, n, h, D).to(DEV) for h in (16, Hkv, Hkv))
+    cu = None if single else np.concatenate([[0], np.cumsum(new)])
+    _, want = OP.append(f64(q), f64(kn), f64(vn), ref, near, start, cu, 1e4, "neox", D)
+    dsa.qknorm_rope_paged_append(q, kn, vn, k, v, i32(far), i32(start), 1e4,
+                                 cu_new=None if single else i32(cu), k_scale=ks, v_scale=vs)
+    for got, name in zip((k, v, ks, vs), ("k", "v", "ks", "vs")):
+        assert np.array_equal(f64(got[P - used:]), want[name]), name
+    assert bool((ks[:P - used] == 1).all()) and bool((vs[:P - used] == 1).all())
+    for t in (k, v):
+        assert not bool(t[:used].view(torch.uint8).any())
+
+
 def test_attention_of_no_tokens_at_all():
     gen = torch.Generator().manual_seed(46)
     gpu, _ = make_cache(gen, 2, 2, 16, 64, E4M3)
