@@ -1518,7 +1518,7 @@ dec_status check_paged_attn(const PagedCache &c, dec_dtype type, const void *q,
   if (workspace == nullptr || misaligned({workspace}, 256))
     return fail(DEC_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
   const size_t need = paged_attn_ws_bytes(
-      B, Hq, c.Hkv, c.D, paged_attn_parts(B, c.Hkv, c.D, c.e4m3, max_len, num_parts, sm_count_of_current()));
+      Hq, c.Hkv, c.D, paged_attn_parts(B, c.Hkv, c.D, c.e4m3, max_len, num_parts, sm_count_of_current()));
   if (ws_bytes < need)
     return fail(DEC_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   const size_t rows = (size_t)B * Hq * c.D * 2;
@@ -1614,7 +1614,7 @@ size_t dec_paged_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len
       num_parts > kPagedMaxParts || (long long)B * Hkv * (max_len / 128 + 8) >= (1ll << 31))
     return 0;
   const int sms = sm_count_of_current();  // (for pages of either type)
-  return paged_attn_ws_bytes(B, Hq, Hkv, D,
+  return paged_attn_ws_bytes(Hq, Hkv, D,
                              std::max(paged_attn_parts(B, Hkv, D, 0, max_len, num_parts, sms),
                                       paged_attn_parts(B, Hkv, D, 1, max_len, num_parts, sms)));
 }
@@ -1706,7 +1706,7 @@ dec_status dec_paged_decode_step(
   const size_t row = (size_t)B * hidden * 2, qb = (size_t)B * Hq * D * 2;
   const size_t kb = (size_t)B * Hkv * D * 2;
   const size_t need = paged_attn_ws_bytes(
-      B, Hq, Hkv, D,
+      Hq, Hkv, D,
       paged_attn_parts(B, Hkv, D, c.e4m3, max_len, num_parts, sm_count_of_current()));
   st = check_apart({{y, row, "y"}, {residual, row, "residual"}},
                    {{x, row, "x"}, {norm_w, (size_t)hidden * 2, "norm_w"}, {q, qb, "q"},

@@ -247,7 +247,7 @@ struct PagedAttnArgs {
 };
 constexpr int kPagedMaxParts = 4096;
 int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts, int sms);
-size_t paged_attn_ws_bytes(int B, int Hq, int Hkv, int D, int parts);
+size_t paged_attn_ws_bytes(int Hq, int Hkv, int D, int parts);
 // k, v: the pages as [num_pages * Hkv, page, D], boxes of a page's rows, at most 128 bytes wide, with a
 // swizzle of that width.
 cudaError_t launch_paged_attn(const CUtensorMap &k, const CUtensorMap &v, const PagedCache &c,

@@ -1218,7 +1218,7 @@ int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts
   return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 
-size_t paged_attn_ws_bytes(int, int Hq, int Hkv, int D, int parts) {
+size_t paged_attn_ws_bytes(int Hq, int Hkv, int D, int parts) {
   return kSlotsOffset + (size_t)2 * parts * slot_bytes(Hq / Hkv, D);
 }
 

@@ -459,8 +459,7 @@ __device__ __forceinline__ void work_off(const AppendArgs &a, const RopeTurns &t
 // ---- rows: (token, head) pairs that need nothing of each other ------------------------------
 // Heads are counted q, k, v. A block has tok_par tokens side by side, times as many heads as fit,
 // and goes through its heads_per heads with them: a lane keeps its token's angles.
-// kAll: keys and values too, else queries alone.
-template <int D, bool kInterleaved, bool kE4m3, bool kAll, int kBlock>
+template <int D, bool kInterleaved, bool kE4m3, int kBlock>
 __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
                                         int which) {
   using R = Row<D, kInterleaved>;
@@ -482,7 +481,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   auto load = [&](int h, uint4 &x, uint4 &y) {
     x = y = make_uint4(0u, 0u, 0u, 0u);
     if (i < a.n && h < h1) {
-      const __nv_bfloat16 *src = (!kAll || h < a.Hq ? q_src : h < a.Hq + a.Hkv ? k_src : v_src) + h * D;
+      const __nv_bfloat16 *src = (h < a.Hq ? q_src : h < a.Hq + a.Hkv ? k_src : v_src) + h * D;
       x = *reinterpret_cast<const uint4 *>(src + ea);
       y = *reinterpret_cast<const uint4 *>(src + eb);
     }
@@ -500,7 +499,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   }
   const int in_page = at.pos & ((1 << a.page_log2) - 1);
   // keys of bf16 pages: within one step where the rotation cancels, worked off at the end
-  constexpr bool kList = kAll && !kE4m3;
+  constexpr bool kList = !kE4m3;
   __shared__ Fix s_fixes[kList ? kFixes : 1];
   __shared__ int s_fix_total;
   if (kList) {
@@ -509,7 +508,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   }
   for (int hh = h0; hh < h1; hh += step) {  // (the same number of times in every lane)
     const int h = hh + row / a.tok_par;
-    const bool is_q = !kAll || h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
     const int g = is_q ? h : is_k ? h - a.Hq : h - a.Hq - a.Hkv;
     const bool live = some && h < h1 && (is_q || at.page >= 0);
     Turned t;
@@ -525,9 +524,9 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
     unsigned bits = 0;
     float rstd = 1.f;
     // (a warp may hold values beside keys: the norm's shuffles)
-    if (!kAll || (norm ? __any_sync(0xffffffffu, turns_here) : turns_here))
-      bits = turn<D, kInterleaved, false, kAll && !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn,
-                                            is_k, rstd);
+    if (norm ? __any_sync(0xffffffffu, turns_here) : turns_here)
+      bits = turn<D, kInterleaved, false, !kE4m3>(t, x, y, norm, wa, wb, a.eps, rotated, cs, sn, is_k,
+                                                  rstd);
     if (!turns_here) R::unpack(x, y, t.u, t.v);
     const size_t slot =
         live && !is_q
@@ -586,7 +585,6 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
       *reinterpret_cast<uint2 *>(to + eb) = cb;
       dst = to;
     }
-    if (!kAll) continue;
     const __nv_bfloat16 *key = k_src + h * D;
     if (!live || !is_k) bits = 0;
     if (kList) put_off(s_fixes, &s_fix_total, key, dst, at.pos, l, rstd, bits);
@@ -596,7 +594,7 @@ __device__ __forceinline__ void do_rows(const AppendArgs &a, const RopeTurns &tu
   }
   if (kList) {
     __syncthreads();
-    work_off<D, kInterleaved, false>(a, turns, s_fixes, s_fix_total, threadIdx.x, kThreads);
+    work_off<D, kInterleaved, false>(a, turns, s_fixes, s_fix_total, threadIdx.x, kBlock);
   }
 }
 
@@ -1006,8 +1004,9 @@ __device__ __forceinline__ void do_runs(const AppendArgs &a, const RopeTurns &tu
 }
 
 // kPage = 0: every block takes rows, of queries, keys and values. Else row_blocks of the blocks take the
-// queries' rows, the others the runs of e4m3 pages of kPage tokens. kPlain: no norm, all elements turned
-// (the two branches cost a tenth of the instructions, most of them moves: the prompts above 57 and 55 us).
+// queries' rows, the others the runs of e4m3 pages of kPage tokens. kTokens: rows go a token to each, heads
+// in loops (with kPage > 0 always). kPlain: no norm, all elements turned (the two branches cost a tenth of
+// the instructions, most of them moves: the prompts above 57 and 55 us).
 // Blocks of 256 threads go three to an SM, 80 registers a thread; four, with 64, spill: the prompts above
 // then 59 and 86 us. Pages of 128 tokens of 128 dims in blocks of 512, one to an SM then 82 us (now 64),
 // two 94.
@@ -1025,14 +1024,12 @@ __global__ void __launch_bounds__(kBlock, kBlock == 256 ? 3 : 1)
     block = is_row ? before : i - before;
     if (!is_row)
       do_runs<D, kInterleaved, kPlain, kBlock, kPage>(a, turns, block);
-    else if constexpr (kTokens)
-      do_token_rows<D, kInterleaved, kPlain, false, kBlock>(a, turns, a.Hq, block);
     else
-      do_rows<D, kInterleaved, false, false, kBlock>(a, turns, a.Hq, block);
+      do_token_rows<D, kInterleaved, kPlain, false, kBlock>(a, turns, a.Hq, block);
   } else if constexpr (kTokens) {
     do_token_rows<D, kInterleaved, kPlain, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   } else {
-    do_rows<D, kInterleaved, kE4m3, true, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
+    do_rows<D, kInterleaved, kE4m3, kBlock>(a, turns, a.Hq + 2 * a.Hkv, block);
   }
 }
 
