@@ -420,7 +420,13 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   using Ge = Geo<D, kE4m3>;
   constexpr int S = Ge::kSlots, ND = Ge::kDescs, kTile = Ge::kTile, kHalves = Ge::kHalves;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_bar[2 * S + ND + 33];
+  // barriers: where each kind begins, in this order
+  constexpr int kFullAt = 0, kEmptyAt = kFullAt + S, kDescAt = kEmptyAt + S, kSAt = kDescAt + ND,
+                kPAt = kSAt + 2, kOAt = kPAt + 2, kFreeAt = kOAt + 2, kQAt = kFreeAt + 2,
+                kQFreeAt = kQAt + 4, kEndAt = kQFreeAt + 2, kSumAt = kEndAt + 2, kSegAt = kSumAt + 4,
+                kSegFreeAt = kSegAt + 4, kJoinAt = kSegFreeAt + 4, kBars = kJoinAt + 1;
+  static_assert(kBars <= kThreads, "a barrier per thread");
+  __shared__ uint64_t s_bar[kBars];
   __shared__ Tile s_tile[ND];
   __shared__ float s_scale[ND][2][8 * kHalves];  // of a tile's pages, K and V; < 0: no page
   __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
@@ -435,23 +441,23 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_addr(smem), q_s = ring + S * Ge::kTensor, p_s = q_s + 2 * Ge::kQ;
-  const uint32_t bar_full = smem_addr(s_bar), bar_empty = bar_full + 8 * S;
-  const uint32_t bar_desc = bar_empty + 8 * S, bar_s = bar_desc + 8 * ND, bar_p = bar_s + 16;
-  const uint32_t bar_o = bar_p + 16, bar_free = bar_o + 16, bar_q = bar_free + 16;
-  const uint32_t bar_qfree = bar_q + 32, bar_end = bar_qfree + 16, bar_sum = bar_end + 16;
-  const uint32_t bar_seg = bar_sum + 32, bar_segfree = bar_seg + 32, bar_join = bar_segfree + 32;
+  const uint32_t bars = smem_addr(s_bar), bar_full = bars + 8 * kFullAt, bar_empty = bars + 8 * kEmptyAt;
+  const uint32_t bar_desc = bars + 8 * kDescAt, bar_s = bars + 8 * kSAt, bar_p = bars + 8 * kPAt;
+  const uint32_t bar_o = bars + 8 * kOAt, bar_free = bars + 8 * kFreeAt, bar_q = bars + 8 * kQAt;
+  const uint32_t bar_qfree = bars + 8 * kQFreeAt, bar_end = bars + 8 * kEndAt;
+  const uint32_t bar_sum = bars + 8 * kSumAt, bar_seg = bars + 8 * kSegAt;
+  const uint32_t bar_segfree = bars + 8 * kSegFreeAt, bar_join = bars + 8 * kJoinAt;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = a.Hq / c.Hkv;
 
   // A barrier per thread. (A barrier completes its next phase only when all that wait for the one
   // before have seen that: each role's waits say so, those for the end of the piece included.)
-  if (tid < 2 * S + ND + 33) {
-    const uint32_t bar = bar_full + 8 * tid;
-    const bool many = (bar >= bar_p && bar < bar_o) || (bar >= bar_free && bar < bar_q);
-    mbar_init(bar, bar >= bar_desc && bar < bar_s ? (kE4m3 ? 33 : 1)
-                   : many                         ? 128
-                   : bar >= bar_sum && bar < bar_seg ? 4
-                                                     : 1);
+  if (tid < kBars) {
+    const bool many = (tid >= kPAt && tid < kOAt) || (tid >= kFreeAt && tid < kQAt);
+    mbar_init(bars + 8 * tid, tid >= kDescAt && tid < kSAt ? (kE4m3 ? 33 : 1)
+                              : many                       ? 128
+                              : tid >= kSumAt && tid < kSegAt ? 4
+                                                              : 1);
     fence_barrier_init();
   }
   if (tid == 0) s_abort = s_parts = 0;
