@@ -342,8 +342,12 @@ struct FarTile {
   uint32_t s, p;            // S^T in tensor memory, this thread's weights in shared memory
   int page_log2, lo, hi;
 };
+template <int NH>
+struct Sums {
+  float v[NH];
+};
 template <int D, bool kE4m3, int NH>
-__device__ __noinline__ void far_tile(const FarTile f, float (&sum)[NH]) {
+__device__ __noinline__ Sums<NH> far_tile(const FarTile f, Sums<NH> sum) {
   using Ge = Geo<D, kE4m3>;
   constexpr int kHalves = Ge::kHalves, kCols = kE4m3 ? 2 * NH : 8;
   const int lane = threadIdx.x & 31, mine = lane & (kG - 1);
@@ -406,11 +410,12 @@ __device__ __noinline__ void far_tile(const FarTile f, float (&sum)[NH]) {
     float add = 0.f;
 #pragma unroll
     for (int half = 0; half < kHalves; ++half) add = fmaf(w[half][h], ivs[half], add);
-    sum[h] = fmaf(add, f.base[kG + h], sum[h] * f.base[3 * kG + h]);
+    sum.v[h] = fmaf(add, f.base[kG + h], sum.v[h] * f.base[3 * kG + h]);
   }
 #pragma unroll
   for (int half = 0; half < kHalves; ++half)
     put_weights<Ge::kTile, kE4m3, NH>(w[half], f.p + 128 * half * 16);
+  return sum;
 }
 
 template <int D, bool kE4m3, int NH>
@@ -932,15 +937,15 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
         }
       }
       if (__builtin_expect(far, 0)) {
-        float sums[NH];  // (whose address goes out)
+        Sums<NH> sums;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) sums[h] = sum[h];
-        far_tile<D, kE4m3, NH>(
+        for (int h = 0; h < NH; ++h) sums.v[h] = sum[h];
+        sums = far_tile<D, kE4m3, NH>(
             FarTile{s_scale[d][0], s_qs[seg & 3], my_base, s_top[buf][0][warp],
                     my_s + buf * kHalves * kN, p_s + buf * Ge::kP + tid * 16, page_log2, t.lo, t.hi},
             sums);
 #pragma unroll
-        for (int h = 0; h < NH; ++h) sum[h] = sums[h];
+        for (int h = 0; h < NH; ++h) sum[h] = sums.v[h];
       } else {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {

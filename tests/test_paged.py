@@ -1121,6 +1121,40 @@ def test_attention_values_at_the_ends_of_their_scales(lo, hi):
         assert err == 0
 
 
+@pytest.mark.parametrize("dtype,D,page,G", [(E4M3, 128, 16, 3), (E4M3, 64, 32, 7), (BF16, 128, 64, 8)])
+def test_attention_far_and_common_scores_side_by_side(dtype, D, page, G):
+    """Heads of far, equal scores beside heads of common ones in the same tiles, with a window, a page that
+    does not exist, sequences of common scores before and after, and what no token is not a number."""
+    gen, rng = torch.Generator().manual_seed(G), np.random.default_rng(G)
+    lens, window, e = [300, 700, 0, 200, 33], 450, 40
+    P = sum(-(-n // page) for n in lens)
+    gpu, _ = make_cache(gen, P, 2, page, D, dtype)
+    table = make_table(rng, lens, page, P)
+    for at in table[1, :-(-lens[1] // page)]:  # the second sequence: half of a key's elements the same
+        if dtype is BF16:
+            gpu[0][int(at)] = (gpu[0][int(at)].float() * 2.0 ** e).to(BF16)
+            gpu[0][int(at), ..., :D // 2] = 1.25 * 2.0 ** e
+        else:
+            j = int(rng.integers(0, 5))
+            gpu[0][int(at), ..., :D // 2] = torch.full((2, page, D // 2), 1.25 * 2.0 ** j, device=DEV).to(E4M3)
+            gpu[2][int(at)] = 2.0 ** (e - j)
+    table[1, 9] = -7
+    if lens[1] % page:
+        raw = gpu[1].view(torch.uint8 if dtype is E4M3 else torch.int16)
+        raw[int(table[1, -(-lens[1] // page) - 1]), :, lens[1] % page:] = 0x7f if dtype is E4M3 else 0x7fff
+    q = rnd(gen, 5, 2 * G, D).double()
+    q[1, ::2, D // 2:] = 0                      # far scores, alike over the tokens
+    q[1, 1::2, :D // 2] = 0
+    q[1, 1::2] *= 2.0 ** -(e + (0 if dtype is BF16 else 6))
+    q = q.to(BF16).to(DEV)
+    for parts in (0, 3):
+        out, err = attend(q, gpu, table, lens, window=window, num_parts=parts)
+        want = OP.attention(f64(q), oracle_cache(gpu), table, lens, window=window)
+        check_attn(out, want, (dtype, D, page, G, parts))
+        # (a page wholly before the window is not looked up)
+        assert err == (dsa.DEVERR_PAGE_SKIPPED if 10 * page > lens[1] - window else 0)
+
+
 @pytest.mark.parametrize("falls", [False, True])
 def test_attention_far_scores_a_step_apart(falls):
     """Scores of 2^27.3 (in powers of two) that rise or fall by 16, one step of fp32 there, every 32
