@@ -12,11 +12,13 @@
 //          the sum is exact but for elements below 2^-14 of their head's largest. A weight
 //          p = hi + lo / 16 is within 2^-8 of itself.
 //   bf16   p = hi + lo, both bf16 (the second half of Q's rows is zero).
-// The weights' size is what e4m3 has little room for (2^-9 .. 448): each warp of 32 tokens takes them
-// relative to its own largest, 2^8, and has columns of its own in the product, which are joined in
-// fp32 with the running maximum. A value's scale is part of its weight: with t = z + log2(s_v), the
-// weight is 2^(t - max t) and its share of the softmax sum that over s_v. (Scores beyond 2^10, where
-// fp32 no longer holds such sums closely, are taken apart from log2(s_v): far_tile.)
+// The weights' size is what e4m3 has little room for (2^-9 .. 448): each of four warps takes those of its
+// tokens (32 of a tile of 128, 64 of one of 256) relative to a base of its own, which is 2^8 and stays
+// from tile to tile while the largest weight lies within 2^2 .. 2^8.5, and has columns of its own in the
+// product, which are joined in fp32 with the running maximum. A value's scale is part of its weight: with
+// t = z + log2(s_v), the weight is 2^(8 + t - base) and its share of the softmax sum that over s_v.
+// (Scores beyond 2^10, where fp32 no longer holds such sums closely, are taken apart from log2(s_v):
+// far_tile.)
 //
 // The tiles (128 tokens; 256 of 64 dims in e4m3) of all (sequence, KV head) pairs form one stream, cut
 // into equal pieces, one per CTA (two CTAs per SM; one for bf16 rows of 128 dims, whose ring takes
@@ -40,16 +42,16 @@
 //
 // What bounds it, and what it measured (us as a user's call with a workspace of its own; GB/s of K and V
 // read; a plain copy moves 6687 GB/s):
-//   256 ragged sequences (539 MB), 4 KV heads of 128, e4m3         86   6.2 TB/s   memory, and that
+//   256 ragged sequences (539 MB), 4 KV heads of 128, e4m3         88   6.1 TB/s   memory, and that
 //                                                    equal pieces take the SMs 10-15% unequal times
-//   32 sequences of 512 .. 8192 tokens, 8 KV heads of 128, bf16    90   6.4 TB/s   the same
-//   131072 tokens of one sequence, 8 KV heads of 128, e4m3         47   5.7 TB/s   start and joining
-//   192 windows of 4095 tokens, 2 KV heads of 64, e4m3             37   4.7 TB/s   start (a third),
+//   32 sequences of 512 .. 8192 tokens, 8 KV heads of 128, bf16    91   6.3 TB/s   the same
+//   131072 tokens of one sequence, 8 KV heads of 128, e4m3         48   5.5 TB/s   start and joining
+//   192 windows of 4095 tokens, 2 KV heads of 64, e4m3             38   4.5 TB/s   start (a third),
 //                                                    then the instructions of the weights
 //   512 tokens, 8 KV heads of 128, e4m3                            11              the call (8 on the GPU)
 // The steps that led here (the serving mix): one CTA per SM 168, two 124, weights relative to a base
-// that stays while it is near 92, partials joined from bulk copies 90, a segment as one tile 86. A
-// kernel of plain loads and fp32 sums took 2126.
+// that stays while it is near 92, partials joined from bulk copies 90, a segment as one tile 87, bases
+// of two terms for far scores 88. A kernel of plain loads and fp32 sums took 2126.
 #include <cuda_fp8.h>
 #include <limits.h>
 #include <math.h>
@@ -72,9 +74,10 @@ constexpr int kTma = 8, kQuery = 9, kScore = 10, kValue = 11;  // warps
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kOCols = 4 * kN;       // an O buffer: 16 columns for each warp of tokens
 // What beginning and ending a segment costs, in tiles: the stream is cut by tiles plus this, unless
-// there are fewer than kFew tiles per piece. (256 ragged sequences, us with 0, 1, 2, 3 and 5: 89.0, 89.4,
-// 90.6, 93.0, 97.5; 192 windows of 64 dims 38.1, 37.9, 38.6, 38.6, 39.2; 32 sequences in bf16 92.1, 91.2,
-// 91.6, 92.6, 93.3.)
+// there are fewer than kFew tiles per piece. (256 ragged sequences, us on the GPU with 0, 1, 2, 3 and 5:
+// 88.4, 88.0, 90.6, 92.7, 97.8; 192 windows of 64 dims 38.8, 38.3, 38.5, 39.2, 40.1; 32 sequences in bf16
+// 90.8, 91.1, 90.3, 90.1, 91.2. kFew of 0, 1, 2, 4, 8 and 16: 8 sequences of 2048 tokens, 8 KV heads, 12.8,
+// 12.9, 12.9, 12.6, 12.6, 12.6; 8 of 8192 27.0, 27.0, 27.0, 27.0, 27.1, 27.6.)
 constexpr int kSegment = 1, kFew = 4;
 // Weights are taken relative to a base. Up to this size of it (in powers of two) fp32 holds the base, the
 // scores and log2 of a value's scale to 2^-14; beyond it, see the warps of weights.
@@ -335,7 +338,8 @@ __device__ __forceinline__ void put_weights(const float (&w)[NH], uint32_t at) {
 // small beside a weight's exponent there: the largest score is subtracted from the scores before
 // anything is added, which is exact for equal ones, and the base has two terms. Nothing stays for the
 // next tile, and its sticky base is none. (A function of its own, called in the place of the common tiles'
-// code: in line, or in a loop of its own behind theirs, it cost the windows above 10 to 20%; so 4%.)
+// code: in line, or in a loop of its own behind theirs, it cost the windows above 10 to 20%; so 4%, 36.8
+// to 38.2 us.)
 struct FarTile {
   const float *scale, *qs;  // [2][8 kHalves] K's and V's of the tile's pages; the queries'
   float *base, *top;        // the warp's s_base, and its two rows of s_top, 4 kG apart

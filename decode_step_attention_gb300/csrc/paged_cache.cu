@@ -43,8 +43,7 @@ namespace {
 
 constexpr int kThreads = 256;  // of a block; 512 where a page takes as many
 // Heads are spread over more blocks until there are so many (of 256 threads) per SM. (The prompts and
-// chunks above, us with 4, 6 and 8: 51.5 and 39.9, 56.5 and 41.1, 56.4 and 41.2; two steps before, with 2, 4
-// and 12, 64.6 and 50.6, 59.9 and 41.9, 81.3 and 49.6.)
+// chunks above, us with 2, 4, 6 and 8: 52.7 and 41.8, 51.3 and 38.8, 56.4 and 38.9, 56.4 and 38.8.)
 constexpr int kBlocksPerSm = 4;
 constexpr int kMostWarps = 16;
 constexpr int kMinScaleExp = -64;  // the scale of a page of zeros, and the smallest
@@ -649,9 +648,9 @@ struct RowsAhead {
 
 // The same for batches that fill a block with tokens: a token per row, so that every row of the block is
 // at the same head, and the heads go by in loops of their own. kAll: keys and values (bf16 pages) too.
-// kHeadsAhead heads are on their way while one is turned, in dynamic shared memory (the prompts and chunks
-// above, us with 1, 2, 3, 5 and 7: 62.1 and 42.7, 60.4 and 41.3, 59.9 and 41.9, 59.5 and 42.6, 67.8 and
-// 41.5; one in registers 65.7 and 47.2).
+// kHeadsAhead heads are on their way while one is turned, in dynamic shared memory, 8 KB a block for each
+// (the prompts and chunks above, us with 1, 2, 3, 4, 5 and 7: 54.8 and 41.5, 52.0 and 39.7, 51.3 and 38.8,
+// 50.7 and 38.2, 50.2 and 37.8, 51.6 and 37.9; one in registers, some steps before, 6 and 5 more than 3).
 constexpr int kHeadsAhead = 3;
 template <int D, bool kInterleaved, bool kPlain, bool kAll, int kBlock>
 __device__ __forceinline__ void do_token_rows(const AppendArgs &a, const RopeTurns &turns, int heads,
@@ -793,8 +792,9 @@ struct Run {
 // barrier `meet` and have the run's angles in `table`: [token][4 pairs of each lane, then the others]
 // cosines, then the sines.
 // Rows of 128 dims, and pages of 128 tokens, go two tokens to a row's lanes: half the threads to meet.
-// (12.6 k tokens of prompts, us with one token and with two; 128 dims, pages of 16 and 32: 62.2, 59.6 and
-// 64.1, 59.4; 64 dims, pages of 16, 32, 64 and 128: 35.8, 53.2; 37.2, 42.1; 37.6, 43.0 and 48.7, 42.8.)
+// (The prompts above, us with one token and with two; 128 dims, pages of 16 and 32: 55.3, 51.4 and 56.1,
+// 50.9; 64 dims, pages of 16, 32 and 64: 32.1, 40.7; 32.3, 35.8 and 32.3, 35.5. Larger pages with one would
+// need blocks of 512 threads.)
 __host__ __device__ constexpr int passes_of(int D, int page) { return D == 128 || page == 128 ? 2 : 1; }
 template <int D, bool kInterleaved, bool kPlain, int kGroup, int kBlock, int kPasses>
 __device__ __forceinline__ void do_run(const AppendArgs &a, const RopeTurns &turns, const Run &r,
