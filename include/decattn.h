@@ -667,8 +667,9 @@ dec_status dec_tree_commit(const void *k_tree, const void *v_tree, const int32_t
  *          exact rotated key. Infinities become +-448 s, a NaN stays one.
  * Rows of a page behind its last token are not touched. A token with start[b] < 0, or a position
  * outside the table, is skipped and raises DEC_DEVERR_POS_SKIPPED (its q_out row is written when
- * start[b] >= 0 and the position is below 2^31). The sum of a head's squares has to stay finite in
- * fp32 where there is a norm. Tokens outside every [cu_new[b], cu_new[b + 1]) are not touched.
+ * start[b] >= 0 and the position is below 2^31). Where there is a norm, the sum of a head's squares
+ * has to stay finite in fp32, and their mean plus eps at least 2^-110. Tokens outside every
+ * [cu_new[b], cu_new[b + 1]) are not touched.
  * q_in, q_out   [device|host] bf16, row (i, h) at i * q_ld + h * D (qo_ld for q_out): the same
  *               buffer and stride (in place), or not overlapping.
  * k_new, v_new  [device|host] bf16, row (i, g) at i * k_ld + g * D (v_ld): the column blocks of a
