@@ -17,8 +17,8 @@
 // from tile to tile while the largest weight lies within 2^2 .. 2^8.5, and has columns of its own in the
 // product, which are joined in fp32 with the running maximum. A value's scale is part of its weight: with
 // t = z + log2(s_v), the weight is 2^(8 + t - base) and its share of the softmax sum that over s_v.
-// (Scores beyond 2^10, where fp32 no longer holds such sums closely, are taken apart from log2(s_v):
-// far_tile.)
+// (Scores beyond 2^10, where fp32 no longer holds such sums closely, are taken apart from log2(s_v): see
+// the warps of weights.)
 //
 // The tiles (128 tokens; 256 of 64 dims in e4m3) of all (sequence, KV head) pairs form one stream, cut
 // into equal pieces, one per CTA (two CTAs per SM; one for bf16 rows of 128 dims, whose ring takes
@@ -103,6 +103,13 @@ struct Geo {
   static constexpr int kSlots = (192 / kCtas) * 1024 / kTensor;  // of the ring, half of them K's
   static constexpr int kTiles = kSlots / 2;
   static constexpr int kDescs = kTiles + 4;  // tile descriptors: none is overwritten while in use
+  // barriers: where each kind begins, in this order
+  static constexpr int kFullAt = 0, kEmptyAt = kFullAt + kSlots, kDescAt = kEmptyAt + kSlots,
+                       kSAt = kDescAt + kDescs, kPAt = kSAt + 2, kOAt = kPAt + 2, kFreeAt = kOAt + 2,
+                       kQAt = kFreeAt + 2, kQFreeAt = kQAt + 4, kEndAt = kQFreeAt + 2,
+                       kSumAt = kEndAt + 2, kSegAt = kSumAt + 4, kSegFreeAt = kSegAt + 4,
+                       kJoinAt = kSegFreeAt + 4, kBars = kJoinAt + 1;
+  static_assert(kBars <= kThreads, "a barrier per thread");
   static constexpr uint32_t kOCol = 2 * kHalves * kN;  // of tensor memory: O's columns behind two S's
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * kTensor + 2 * kQ + 2 * kP;
   // high words of the matrix descriptors: 8 rows to the next 8, the version bit, the swizzle mode
@@ -334,92 +341,241 @@ __device__ __forceinline__ void put_weights(const float (&w)[NH], uint32_t at) {
   }
 }
 
-// A tile's weights where a base lies beyond kFar, by the warp of its tokens. The steps of fp32 are no longer
-// small beside a weight's exponent there: the largest score is subtracted from the scores before
-// anything is added, which is exact for equal ones, and the base has two terms. Nothing stays for the
-// next tile, and its sticky base is none. (A function of its own, called in the place of the common tiles'
-// code: in line, or in a loop of its own behind theirs, it cost the windows above 10 to 20%; so 4%, 36.8
-// to 38.2 us.)
-struct FarTile {
-  const float *scale, *qs;  // [2][8 kHalves] K's and V's of the tile's pages; the queries'
-  float *base, *top;        // the warp's s_base, and its two rows of s_top, 4 kG apart
-  uint32_t s, p;            // S^T in tensor memory, this thread's weights in shared memory
-  int page_log2, lo, hi;
-};
-template <int NH>
-struct Sums {
-  float v[NH];
+// A warp of weights: a token per thread (two of 256). A warp's weights are 2^(8 + t - base) with a base per
+// head that stays while the largest t of a tile lies within 2^-6 .. 2^0.5 of it: then a tile's weights,
+// sums and part of O need no factor of their own.
+// Where a base lies beyond kFar, the steps of fp32 are no longer small beside a weight's exponent: the
+// largest score is then subtracted from the scores before anything is added, which is exact for equal ones,
+// every tile has bases of its own, and they have two terms (kAnyBase). From the first such tile on, a warp
+// goes through what is left of the piece in any_base_tiles, a function so that its code lies apart from the
+// common tiles': in line behind them it cost the windows above 9%, called tile by tile 4%, so 2% (37.0 to
+// 37.7 us).
+enum Step { kGo, kStop, kTooFar };
+template <int D, bool kE4m3, int NH>
+struct Weights {
+  using Ge = Geo<D, kE4m3>;
+  static constexpr int kHalves = Ge::kHalves, kTile = Ge::kTile;
+  Waiter wait;
+  const Tile *tile;
+  const float (*scale)[2][8 * kHalves];
+  const float (*qs)[kG];
+  float (*top)[2][4][kG];
+  float *base;  // the warp's: bases, 2^(base - maximum), the maximum of the bases so far (hi; its lo last),
+                // which the sums are relative to, and what the sums are to be multiplied with
+  float (*sums)[4][3][kG];
+  uint32_t bars, s, p, ring;  // (s: S^T in this warp's lanes of tensor memory)
+  int page_log2;
+  int seg;
+  float sum[NH];
+
+  __device__ __forceinline__ uint32_t bar(int at, int i) const { return bars + 8 * (at + i); }
+  __device__ __forceinline__ static void load4(float (&to)[NH], const float *from) {
+#pragma unroll
+    for (int h = 0; h < NH; h += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(from + h);
+      to[h] = x.x, to[h + 1] = x.y, to[h + 2] = x.z, to[h + 3] = x.w;
+    }
+  }
+  template <bool kAnyBase>
+  __device__ __forceinline__ Step step(int n) {
+    constexpr int S = Ge::kSlots, ND = Ge::kDescs;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int d = n % ND, buf = n & 1;
+    // its descriptor, its S^T (or the end), and tile n - 2's weights and bases consumed
+    const uint32_t phase = (n >> 1) & 1;
+    if (!wait.all(bar(Ge::kDescAt, d), (n / ND) & 1, bar(Ge::kSAt, buf), phase, bar(Ge::kFreeAt, buf),
+                  phase ^ 1))
+      return kStop;
+    if (tile[d].flags & kEnd) {
+      mbar_arrive(bar(Ge::kPAt, buf));
+      return kStop;
+    }
+    tc_fence_after();
+    constexpr int kCols = kE4m3 ? 2 * NH : 8;
+    float z[kHalves][kCols];
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) tmem_ld(s + (buf * kHalves + half) * kN, z[half]);
+    const Tile t = tile[d];
+    bool inside[kHalves];
+    float ks[kHalves], lvs[kHalves], ivs[kHalves];
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      const int row = tid + 128 * half;
+      ks[half] = scale[d][0][row >> page_log2];
+      const float vs = scale[d][1][row >> page_log2];
+      inside[half] = row >= t.lo && row < t.hi;
+      if (!inside[half]) ks[half] = -1.f;
+      lvs[half] = kE4m3 ? lg2(vs) : 0.f;
+      ivs[half] = ks[half] > 0.f ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
+    }
+    if (t.flags & kFirst) {
+      ++seg;
+      if (lane < kG) {
+        base[lane] = base[2 * kG + lane] = -INFINITY;
+        base[4 * kG + lane] = 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) sum[h] = 0.f;
+      __syncwarp();
+    }
+    float q[NH], w[kHalves][NH];
+    load4(q, qs[seg & 3]);
+    if constexpr (kAnyBase) {
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
+      Base b{-INFINITY, 0.f};  // of the head lane & 7
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float m = -INFINITY, r = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          const float *x = z[half];
+          if constexpr (kE4m3)
+            w[half][h] = fmaf(x[NH + h], kLow, x[h]) * (q[h] * ks[half]);
+          else
+            w[half][h] = x[h] * q[h];
+          if (!(ks[half] > 0.f)) w[half][h] = -INFINITY;  // (not seen)
+          m = fmaxf(m, w[half][h]);
+        }
+        m = warp_max(m);
+        const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          w[half][h] -= from;
+          if (ks[half] > 0.f) w[half][h] += lvs[half];
+          r = fmaxf(r, w[half][h]);
+        }
+        r = m == -INFINITY ? 0.f : warp_max(r);
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) w[half][h] = ex2((w[half][h] - r) + 8.f);
+        if ((lane & (kG - 1)) == h) b = is_far(m) ? Base{m, r} : Base{m + r, 0.f};
+      }
+      const Base old{base[2 * kG + (lane & (kG - 1))], base[4 * kG + (lane & (kG - 1))]};
+      const Base to = b.max(old), by = to.or_zero();
+      __syncwarp();
+      if (lane < NH) {
+        base[kG + lane] = ex2(b.above(by));
+        base[2 * kG + lane] = to.hi;
+        base[3 * kG + lane] = ex2(old.above(by));
+        base[4 * kG + lane] = to.lo;
+        top[buf][0][warp][lane] = b.hi;
+        top[buf][1][warp][lane] = b.lo;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float add = 0.f;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) add = fmaf(w[half][h], ivs[half], add);
+        sum[h] = fmaf(add, base[kG + h], sum[h] * base[3 * kG + h]);
+      }
+    } else {
+      float at[NH], beta[NH], most[NH];  // (at: the bases)
+      load4(at, base);
+      load4(beta, base + kG);
+      bool near = true;
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          const float *x = z[half];
+          if constexpr (kE4m3)
+            w[half][h] = fmaf(fmaf(x[NH + h], kLow, x[h]), q[h] * ks[half], lvs[half]);
+          else
+            w[half][h] = x[h] * q[h];
+          if (!(ks[half] > 0.f)) w[half][h] = -INFINITY;  // (not seen)
+          m = fmaxf(m, w[half][h]);
+        }
+        most[h] = warp_max(m);
+        near = near && most[h] - at[h] <= 0.5f && most[h] - at[h] >= -6.f;
+      }
+      if (!near) {  // (the same for the whole warp) a head per lane
+        float m = most[0];
+#pragma unroll
+        for (int h = 1; h < NH; ++h)
+          if ((lane & (kG - 1)) == h) m = most[h];
+        if (__any_sync(0xffffffffu, is_far(m))) {
+          if (t.flags & kFirst) --seg;  // (the tile is gone through again)
+          return kTooFar;
+        }
+        float b = base[lane & (kG - 1)];
+        const float old = base[2 * kG + (lane & (kG - 1))], x = m - b;
+        if (!(x <= 0.5f && x >= -6.f) && m != -INFINITY) b = m;
+        const float to = fmaxf(old, b), by = to == -INFINITY ? 0.f : to;
+        __syncwarp();
+        if (lane < NH) {
+          base[lane] = b;
+          base[kG + lane] = ex2(b - by);
+          base[2 * kG + lane] = to;
+          base[3 * kG + lane] = ex2(old - by);
+        }
+        __syncwarp();
+        load4(at, base);
+        load4(beta, base + kG);
+        float alpha[NH];
+        load4(alpha, base + 3 * kG);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) sum[h] *= alpha[h];
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const float by = (at[h] == -INFINITY ? 0.f : at[h]) - 8.f;
+        float add = 0.f;
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half) {
+          w[half][h] = ex2(w[half][h] - by);
+          add = fmaf(w[half][h], ivs[half], add);
+        }
+        sum[h] = fmaf(add, beta[h], sum[h]);
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int h = 0; h < NH; h += 4)
+          *reinterpret_cast<float4 *>(&top[buf][0][warp][h]) =
+              make_float4(at[h], at[h + 1], at[h + 2], at[h + 3]);
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half)
+      put_weights<kTile, kE4m3, NH>(w[half], p + buf * Ge::kP + (tid + 128 * half) * 16);
+    // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
+    // page that does not exist was left zeros.)
+    if (t.lo > 0 || t.hi < kTile) {
+      const int slot = (2 * n + 1) % S;
+      if (!wait.all(bar(Ge::kFullAt, slot), ((2 * n + 1) / S) & 1)) return kStop;
+#pragma unroll
+      for (int half = 0; half < kHalves; ++half)
+        if (!inside[half])
+#pragma unroll
+          for (int i = 0; i < Ge::kRow / 16; ++i)
+            st_shared16(ring + slot * Ge::kTensor + (i * 16 / Ge::kWide) * Ge::kSlab +
+                            (tid + 128 * half) * Ge::kWide + (i * 16) % Ge::kWide,
+                        make_uint4(0u, 0u, 0u, 0u));
+    }
+    if (t.flags & kLast) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const float x = warp_sum(sum[h]);
+        if (lane == 0) {
+          sums[seg & 3][warp][0][h] = x;
+          sums[seg & 3][warp][1][h] = base[2 * kG + h];
+          sums[seg & 3][warp][2][h] = base[4 * kG + h];
+        }
+      }
+      if (lane == 0) mbar_arrive(bar(Ge::kSumAt, seg & 3));
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    mbar_arrive(bar(Ge::kPAt, buf));
+    return kGo;
+  }
 };
 template <int D, bool kE4m3, int NH>
-__device__ __noinline__ Sums<NH> far_tile(const FarTile f, Sums<NH> sum) {
-  using Ge = Geo<D, kE4m3>;
-  constexpr int kHalves = Ge::kHalves, kCols = kE4m3 ? 2 * NH : 8;
-  const int lane = threadIdx.x & 31, mine = lane & (kG - 1);
-  float z[kHalves][kCols], w[kHalves][NH], ks[kHalves], lvs[kHalves], ivs[kHalves];
-  bool seen[kHalves];
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half) {
-    tmem_ld(f.s + half * kN, z[half]);
-    const int row = threadIdx.x + 128 * half;
-    ks[half] = f.scale[row >> f.page_log2];
-    const float vs = f.scale[8 * kHalves + (row >> f.page_log2)];
-    seen[half] = row >= f.lo && row < f.hi && ks[half] > 0.f;
-    lvs[half] = kE4m3 ? lg2(vs) : 0.f;
-    ivs[half] = seen[half] ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
-  }
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
-  Base b{-INFINITY, 0.f};  // of this lane's head
-#pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    float m = -INFINITY, r = -INFINITY;
-#pragma unroll
-    for (int half = 0; half < kHalves; ++half) {
-      const float *x = z[half];
-      if constexpr (kE4m3)
-        w[half][h] = fmaf(x[NH + h], kLow, x[h]) * (f.qs[h] * ks[half]);
-      else
-        w[half][h] = x[h] * f.qs[h];
-      if (!seen[half]) w[half][h] = -INFINITY;
-      m = fmaxf(m, w[half][h]);
-    }
-    m = warp_max(m);
-    const float from = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int half = 0; half < kHalves; ++half) {
-      w[half][h] -= from;
-      if (seen[half]) w[half][h] += lvs[half];
-      r = fmaxf(r, w[half][h]);
-    }
-    r = m == -INFINITY ? 0.f : warp_max(r);
-#pragma unroll
-    for (int half = 0; half < kHalves; ++half) w[half][h] = ex2((w[half][h] - r) + 8.f);
-    if (mine == h) b = is_far(m) ? Base{m, r} : Base{m + r, 0.f};
-  }
-  const Base old{f.base[2 * kG + mine], f.base[4 * kG + mine]};
-  const Base to = b.max(old), by = to.or_zero();
-  __syncwarp();
-  if (lane < NH) {
-    f.base[lane] = -INFINITY;
-    f.base[kG + lane] = ex2(b.above(by));
-    f.base[2 * kG + lane] = to.hi;
-    f.base[3 * kG + lane] = ex2(old.above(by));
-    f.base[4 * kG + lane] = to.lo;
-    f.top[lane] = b.hi;
-    f.top[4 * kG + lane] = b.lo;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    float add = 0.f;
-#pragma unroll
-    for (int half = 0; half < kHalves; ++half) add = fmaf(w[half][h], ivs[half], add);
-    sum.v[h] = fmaf(add, f.base[kG + h], sum.v[h] * f.base[3 * kG + h]);
-  }
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half)
-    put_weights<Ge::kTile, kE4m3, NH>(w[half], f.p + 128 * half * 16);
-  return sum;
+__device__ __noinline__ void any_base_tiles(Weights<D, kE4m3, NH> role, int n) {
+  while (role.template step<true>(n) == kGo) ++n;
 }
 
 template <int D, bool kE4m3, int NH>
@@ -429,13 +585,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
   using Ge = Geo<D, kE4m3>;
   constexpr int S = Ge::kSlots, ND = Ge::kDescs, kTile = Ge::kTile, kHalves = Ge::kHalves;
   extern __shared__ uint8_t smem_raw[];
-  // barriers: where each kind begins, in this order
-  constexpr int kFullAt = 0, kEmptyAt = kFullAt + S, kDescAt = kEmptyAt + S, kSAt = kDescAt + ND,
-                kPAt = kSAt + 2, kOAt = kPAt + 2, kFreeAt = kOAt + 2, kQAt = kFreeAt + 2,
-                kQFreeAt = kQAt + 4, kEndAt = kQFreeAt + 2, kSumAt = kEndAt + 2, kSegAt = kSumAt + 4,
-                kSegFreeAt = kSegAt + 4, kJoinAt = kSegFreeAt + 4, kBars = kJoinAt + 1;
-  static_assert(kBars <= kThreads, "a barrier per thread");
-  __shared__ uint64_t s_bar[kBars];
+  __shared__ uint64_t s_bar[Ge::kBars];
   __shared__ Tile s_tile[ND];
   __shared__ float s_scale[ND][2][8 * kHalves];  // of a tile's pages, K and V; < 0: no page
   __shared__ __align__(16) float s_qs[4][kG];  // a segment's score scales
@@ -450,22 +600,23 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
 
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_addr(smem), q_s = ring + S * Ge::kTensor, p_s = q_s + 2 * Ge::kQ;
-  const uint32_t bars = smem_addr(s_bar), bar_full = bars + 8 * kFullAt, bar_empty = bars + 8 * kEmptyAt;
-  const uint32_t bar_desc = bars + 8 * kDescAt, bar_s = bars + 8 * kSAt, bar_p = bars + 8 * kPAt;
-  const uint32_t bar_o = bars + 8 * kOAt, bar_free = bars + 8 * kFreeAt, bar_q = bars + 8 * kQAt;
-  const uint32_t bar_qfree = bars + 8 * kQFreeAt, bar_end = bars + 8 * kEndAt;
-  const uint32_t bar_sum = bars + 8 * kSumAt, bar_seg = bars + 8 * kSegAt;
-  const uint32_t bar_segfree = bars + 8 * kSegFreeAt, bar_join = bars + 8 * kJoinAt;
+  const uint32_t bars = smem_addr(s_bar), bar_full = bars + 8 * Ge::kFullAt;
+  const uint32_t bar_empty = bars + 8 * Ge::kEmptyAt;
+  const uint32_t bar_desc = bars + 8 * Ge::kDescAt, bar_s = bars + 8 * Ge::kSAt, bar_p = bars + 8 * Ge::kPAt;
+  const uint32_t bar_o = bars + 8 * Ge::kOAt, bar_free = bars + 8 * Ge::kFreeAt, bar_q = bars + 8 * Ge::kQAt;
+  const uint32_t bar_qfree = bars + 8 * Ge::kQFreeAt, bar_end = bars + 8 * Ge::kEndAt;
+  const uint32_t bar_sum = bars + 8 * Ge::kSumAt, bar_seg = bars + 8 * Ge::kSegAt;
+  const uint32_t bar_segfree = bars + 8 * Ge::kSegFreeAt, bar_join = bars + 8 * Ge::kJoinAt;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int G = a.Hq / c.Hkv;
 
   // A barrier per thread. (A barrier completes its next phase only when all that wait for the one
   // before have seen that: each role's waits say so, those for the end of the piece included.)
-  if (tid < kBars) {
-    const bool many = (tid >= kPAt && tid < kOAt) || (tid >= kFreeAt && tid < kQAt);
-    mbar_init(bars + 8 * tid, tid >= kDescAt && tid < kSAt ? (kE4m3 ? 33 : 1)
+  if (tid < Ge::kBars) {
+    const bool many = (tid >= Ge::kPAt && tid < Ge::kOAt) || (tid >= Ge::kFreeAt && tid < Ge::kQAt);
+    mbar_init(bars + 8 * tid, tid >= Ge::kDescAt && tid < Ge::kSAt ? (kE4m3 ? 33 : 1)
                               : many                       ? 128
-                              : tid >= kSumAt && tid < kSegAt ? 4
+                              : tid >= Ge::kSumAt && tid < Ge::kSegAt ? 4
                                                               : 1);
     fence_barrier_init();
   }
@@ -834,174 +985,12 @@ __global__ void __launch_bounds__(kThreads, Geo<D, kE4m3>::kCtas)
     mbar_wait_bounded(bar_end + 8, 0);
   } else if (warp < 4) {
     // ---------------------------------------------------------------- weights
-    const uint32_t my_s = tmem + ((uint32_t)(32 * warp) << 16);
-    // A warp's weights are 2^(8 + t - base) with a base per head that stays while the largest t of a tile
-    // lies within 2^-6 .. 2^0.5 of it: then a tile's weights, sums and part of O need no factor of their
-    // own. s_base: the bases, 2^(base - maximum), the maximum of the bases so far (hi; its lo last), which
-    // the sums are relative to, and what the sums are to be multiplied with.
-    float *my_base = s_base[warp][0];
-    float sum[NH];
-    int seg = -1;
-    for (int n = 0;; ++n) {
-      const int d = n % ND, buf = n & 1;
-      // its descriptor, its S^T (or the end), and tile n - 2's weights and bases consumed
-      const uint32_t phase = (n >> 1) & 1;
-      if (!wait.all(bar_desc + 8 * d, (n / ND) & 1, bar_s + 8 * buf, phase, bar_free + 8 * buf,
-                    phase ^ 1))
-        break;
-      if (s_tile[d].flags & kEnd) {
-        mbar_arrive(bar_p + 8 * buf);
-        break;
-      }
-      tc_fence_after();
-      constexpr int kCols = kE4m3 ? 2 * NH : 8;
-      float z[kHalves][kCols];
-#pragma unroll
-      for (int half = 0; half < kHalves; ++half) tmem_ld(my_s + (buf * kHalves + half) * kN, z[half]);
-      const Tile t = s_tile[d];
-      bool inside[kHalves];
-      float ks[kHalves], lvs[kHalves], ivs[kHalves];
-#pragma unroll
-      for (int half = 0; half < kHalves; ++half) {
-        const int row = tid + 128 * half;
-        ks[half] = s_scale[d][0][row >> page_log2];
-        const float vs = s_scale[d][1][row >> page_log2];
-        inside[half] = row >= t.lo && row < t.hi;
-        if (!inside[half]) ks[half] = -1.f;
-        lvs[half] = kE4m3 ? lg2(vs) : 0.f;
-        ivs[half] = ks[half] > 0.f ? (kE4m3 ? rcp(vs) : 1.f) : 0.f;
-      }
-      if (t.flags & kFirst) {
-        ++seg;
-        if (lane < kG) {
-          my_base[lane] = my_base[2 * kG + lane] = -INFINITY;
-          my_base[4 * kG + lane] = 0.f;
-        }
-#pragma unroll
-        for (int h = 0; h < NH; ++h) sum[h] = 0.f;
-        __syncwarp();
-      }
-      float qs[NH], base[NH], beta[NH];
-      auto load4 = [&](float (&to)[NH], const float *from) {
-#pragma unroll
-        for (int h = 0; h < NH; h += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(from + h);
-          to[h] = x.x, to[h + 1] = x.y, to[h + 2] = x.z, to[h + 3] = x.w;
-        }
-      };
-      load4(qs, s_qs[seg & 3]);
-      load4(base, my_base);
-      load4(beta, my_base + kG);
-      float w[kHalves][NH], most[NH];
-      bool near = true;
-#pragma unroll
-      for (int half = 0; half < kHalves; ++half) tmem_wait(z[half]);
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < kHalves; ++half) {
-          const float *x = z[half];
-          if constexpr (kE4m3)
-            w[half][h] = fmaf(fmaf(x[NH + h], kLow, x[h]), qs[h] * ks[half], lvs[half]);
-          else
-            w[half][h] = x[h] * qs[h];
-          if (!(ks[half] > 0.f)) w[half][h] = -INFINITY;  // (not seen)
-          m = fmaxf(m, w[half][h]);
-        }
-        most[h] = warp_max(m);
-        near = near && most[h] - base[h] <= 0.5f && most[h] - base[h] >= -6.f;
-      }
-      bool far = false;
-      if (!near) {  // (the same for the whole warp) a head per lane
-        float m = most[0];
-#pragma unroll
-        for (int h = 1; h < NH; ++h)
-          if ((lane & (kG - 1)) == h) m = most[h];
-        float b = my_base[lane & (kG - 1)];
-        const float old = my_base[2 * kG + (lane & (kG - 1))], x = m - b;
-        far = __any_sync(0xffffffffu, is_far(m) || is_far(old));
-        if (!far) {
-          if (!(x <= 0.5f && x >= -6.f) && m != -INFINITY) b = m;
-          const float to = fmaxf(old, b), by = to == -INFINITY ? 0.f : to;
-          __syncwarp();
-          if (lane < NH) {
-            my_base[lane] = b;
-            my_base[kG + lane] = ex2(b - by);
-            my_base[2 * kG + lane] = to;
-            my_base[3 * kG + lane] = ex2(old - by);
-          }
-          __syncwarp();
-          load4(base, my_base);
-          load4(beta, my_base + kG);
-          float alpha[NH];
-          load4(alpha, my_base + 3 * kG);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) sum[h] *= alpha[h];
-        }
-      }
-      if (__builtin_expect(far, 0)) {
-        Sums<NH> sums;
-#pragma unroll
-        for (int h = 0; h < NH; ++h) sums.v[h] = sum[h];
-        sums = far_tile<D, kE4m3, NH>(
-            FarTile{s_scale[d][0], s_qs[seg & 3], my_base, s_top[buf][0][warp],
-                    my_s + buf * kHalves * kN, p_s + buf * Ge::kP + tid * 16, page_log2, t.lo, t.hi},
-            sums);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) sum[h] = sums.v[h];
-      } else {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const float by = (base[h] == -INFINITY ? 0.f : base[h]) - 8.f;
-          float add = 0.f;
-#pragma unroll
-          for (int half = 0; half < kHalves; ++half) {
-            w[half][h] = ex2(w[half][h] - by);
-            add = fmaf(w[half][h], ivs[half], add);
-          }
-          sum[h] = fmaf(add, beta[h], sum[h]);
-        }
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < NH; h += 4)
-            *reinterpret_cast<float4 *>(&s_top[buf][0][warp][h]) =
-                make_float4(base[h], base[h + 1], base[h + 2], base[h + 3]);
-        }
-#pragma unroll
-        for (int half = 0; half < kHalves; ++half)
-          put_weights<kTile, kE4m3, NH>(w[half], p_s + buf * Ge::kP + (tid + 128 * half) * 16);
-      }
-      // Rows of V that are not seen can hold anything, and 0 times NaN is NaN: they are cleared. (A
-      // page that does not exist was left zeros.)
-      if (t.lo > 0 || t.hi < kTile) {
-        const int slot = (2 * n + 1) % S;
-        if (!wait.all(bar_full + 8 * slot, ((2 * n + 1) / S) & 1)) break;
-#pragma unroll
-        for (int half = 0; half < kHalves; ++half)
-          if (!inside[half])
-#pragma unroll
-            for (int i = 0; i < Ge::kRow / 16; ++i)
-              st_shared16(ring + slot * Ge::kTensor + (i * 16 / Ge::kWide) * Ge::kSlab +
-                              (tid + 128 * half) * Ge::kWide + (i * 16) % Ge::kWide,
-                          make_uint4(0u, 0u, 0u, 0u));
-      }
-      if (t.flags & kLast) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const float x = warp_sum(sum[h]);
-          if (lane == 0) {
-            s_sum[seg & 3][warp][0][h] = x;
-            s_sum[seg & 3][warp][1][h] = my_base[2 * kG + h];
-            s_sum[seg & 3][warp][2][h] = my_base[4 * kG + h];
-          }
-        }
-        if (lane == 0) mbar_arrive(bar_sum + 8 * (seg & 3));
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(bar_p + 8 * buf);
-    }
+    Weights<D, kE4m3, NH> role{wait, s_tile, s_scale, s_qs, s_top, s_base[warp][0], s_sum, bars,
+                               tmem + ((uint32_t)(32 * warp) << 16), p_s, ring, page_log2, -1, {}};
+    int n = 0;
+    Step last;
+    while ((last = role.template step<false>(n)) == kGo) ++n;
+    if (last == kTooFar) any_base_tiles(role, n);
   } else {
     // ---------------------------------------------------------------- the running O
     // D = 64: an M of 64 puts row 16 w + i into lane i < 16 of warp w's quarter.

@@ -1155,6 +1155,34 @@ def test_attention_far_and_common_scores_side_by_side(dtype, D, page, G):
         assert err == (dsa.DEVERR_PAGE_SKIPPED if 10 * page > lens[1] - window else 0)
 
 
+@pytest.mark.parametrize("dtype,D,page,G", [(E4M3, 128, 32, 3), (E4M3, 64, 64, 7), (BF16, 128, 16, 8),
+                                            (BF16, 64, 128, 4)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attention_far_scores_amid_common_ones(sign, dtype, D, page, G):
+    """Two pages of far, equal scores amid a sequence of common ones, in every third head 0 instead, and
+    common sequences on either side: all of it in one piece, in few, and in many."""
+    gen, rng = torch.Generator().manual_seed(D + G), np.random.default_rng(D + G)
+    lens = [333, 1500, 40, 900]
+    P = sum(-(-n // page) for n in lens)
+    gpu, _ = make_cache(gen, P, 2, page, D, dtype)
+    gpu[0][..., 0] = 0
+    table = make_table(rng, lens, page, P)
+    for at in table[1, 640 // page:640 // page + 2]:
+        gpu[0][int(at)] = 0
+        gpu[0][int(at), ..., 0] = sign * 1.5 * (1.0 if dtype is E4M3 else 2.0 ** 40)
+        if dtype is E4M3:
+            gpu[2][int(at)] = 2.0 ** 40
+    q = rnd(gen, 4, 2 * G, D)
+    q[..., 0] = 1
+    q[:, ::3, 0] = 0
+    q = q.to(BF16).to(DEV)
+    want = OP.attention(f64(q), oracle_cache(gpu), table, lens)
+    for parts in (0, 1, 3, 40):
+        out, err = attend(q, gpu, table, lens, num_parts=parts)
+        check_attn(out, want, (dtype, D, page, G, sign, parts))
+        assert err == 0
+
+
 @pytest.mark.parametrize("falls", [False, True])
 def test_attention_far_scores_a_step_apart(falls):
     """Scores of 2^27.3 (in powers of two) that rise or fall by 16, one step of fp32 there, every 32
