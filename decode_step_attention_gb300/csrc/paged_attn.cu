@@ -56,6 +56,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -1213,11 +1214,12 @@ cudaError_t launch(const PagedMaps &m, const PagedCache &c, const PagedAttnArgs 
 
 // As many CTAs as the SMs hold, or fewer when there are not as many tiles.
 int paged_attn_parts(int B, int Hkv, int D, int e4m3, int max_len, int num_parts, int sms) {
-  if (num_parts > 0) return num_parts;
   auto of = [](auto geo) { return std::pair<int, int>(decltype(geo)::kCtas, decltype(geo)::kTile); };
   const auto [per, tile] = D == 128 ? (e4m3 ? of(Geo<128, true>{}) : of(Geo<128, false>{}))
                                     : (e4m3 ? of(Geo<64, true>{}) : of(Geo<64, false>{}));
   const long long tiles = (long long)B * Hkv * (((long long)max_len + tile - 1) / tile + 1);
+  // (a piece's ring goes by 32-bit numbers, two to a tile)
+  if (num_parts > 0) return std::max(num_parts, (int)((tiles + (1 << 28) - 1) >> 28));
   const long long most = per * sms < kPagedMaxParts ? per * sms : kPagedMaxParts;
   return (int)(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }

@@ -700,7 +700,8 @@ dec_status dec_qknorm_rope_paged_append(
  * lens       [device|host] int32 [B]; max_len a host upper bound, 0 <= max_len <= max_pages * page.
  *            A length outside [0, max_len] is clamped and raises DEC_DEVERR_LEN_CLAMPED.
  * scale      <= 0 selects 1/sqrt(D); at most 1e30.  window >= 0.
- * num_parts  CTAs the work is cut over; 0 lets the library choose.
+ * num_parts  CTAs the work is cut over, raised (to 8 at most) where one would take more than 2^28 tiles of
+ *            128 tokens; 0 lets the library choose.
  * workspace  [device] at least dec_paged_attn_workspace_bytes(...) bytes, 256-byte aligned, zeroed
  *            before its first use (its first word is the device error word; after a
  *            DEC_DEVERR_WAIT_TIMEOUT zero it again); it serves one call at a time.

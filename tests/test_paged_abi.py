@@ -176,6 +176,17 @@ def test_workspace_of_the_longest_contexts(L, D):
         assert ws(1, 1, 1, D, max_len, 0) == ws(1, 1, 1, D, 2 ** 30, 0) > ws(1, 1, 1, D, 0, 0), max_len
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_of_few_parts_for_very_many_tiles(L, D):
+    """A piece's ring goes by 32-bit numbers, two to a tile: parts asked for are raised until a piece has some
+    2^28 tiles at most, and left alone where it has fewer."""
+    ws = L.dec_paged_attn_workspace_bytes
+    for max_len, least in ((2 ** 31 - 1, 8), (2 ** 30, 4), (2 ** 28, 1), (4096, 1)):
+        for parts in (1, 2, 3, 5, 8, 300):
+            # (bf16's tiles of 128 tokens, more than e4m3's; 15 of the largest: B Hkv max_len / 128 < 2^31)
+            assert ws(15, 8, 8, D, max_len, parts) == ws(1, 8, 8, D, 0, max(parts, least)), (max_len, parts)
+
+
 def test_binding_checks():
     bf = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     q, i = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
